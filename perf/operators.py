@@ -120,13 +120,18 @@ def work(case):
 
 # ------------------------------------------------------------------------------------ inputs
 
+def _two(e):
+    """2^e exactly, as 32-bit floats, for whole e of the normal range."""
+    return ((e + 127).to(torch.int32) << 23).view(torch.float32)
+
+
 def _quantise(x):
     """8-bit codes of rows x and the exponent byte of each row's power of two."""
     a = x.float().abs().amax(-1)
     m, e = torch.frexp(a)
     e = torch.where(m <= 0.875, e - 9, e - 8)
     e = torch.where(a > 0, e, -117).clamp(min=-117)
-    codes = torch.ldexp(x.float(), -e[..., None]).to(torch.float8_e4m3fn)
+    codes = (x.float() * _two(-e)[..., None]).to(torch.float8_e4m3fn)
     return codes, (e + 127).to(torch.uint8)
 
 
@@ -261,7 +266,7 @@ def _prepare(s):
 
 
 def _value(codes, scale):
-    return codes.float() if scale is None else torch.ldexp(codes.float(), scale.int()[..., None] - 127)
+    return codes.float() if scale is None else codes.float() * _two(scale.int() - 127)[..., None]
 
 
 def _read(s):
@@ -302,6 +307,11 @@ def _attention(s):
 
 # ------------------------------------------------------------------------------------ the definition, in 64 bits
 
+def _power(e):
+    """2^e exactly, as 64-bit floats."""
+    return ((e + 1023) << 52).view(torch.float64)
+
+
 def exact(case, seed):
     s = prepare(case, seed)
     hq, hkv, D, page = s["dims"]
@@ -314,7 +324,7 @@ def exact(case, seed):
         ids = s["table"][n, first:-(-hi // page)].long()
         y = x.view(torch.uint8)[ids].view(x.dtype).double() if scale is not None else x[ids].double()
         if scale is not None:
-            y = y * torch.pow(2.0, scale[ids].double() - 127.0)[..., None]
+            y = y * _power(scale[ids].long() - 127)[..., None]
         return y.transpose(0, 1).reshape(hkv, -1, D)[:, lo - first * page:hi - first * page]
 
     if case["op"] == "read":
@@ -344,7 +354,7 @@ def exact(case, seed):
             if s["bits8"]:
                 top = x.abs().amax(-1, keepdim=True)
                 top = top.bfloat16().double()
-                two = torch.exp2(torch.ceil(torch.log2(top / 448.0) - 1e-6))  # top has 8 bits: no ratio above a power of two is as near to it
+                two = _power(torch.ceil(torch.log2(top / 448.0) - 1e-6).long())  # top has 8 bits: no ratio above a power of two is as near to it
                 x = x / two
             for n, (st, kv) in enumerate(zip(starts, kv_lens)):
                 at = torch.arange(st, kv, device="cuda")
