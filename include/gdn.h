@@ -506,9 +506,154 @@ GDN_API gdn_status gdn_chunk_prefill_noalloc(const gdn_geometry* geo, const gdn_
                                              const gdn_bf16* norm_w, float rms_eps, gdn_bf16* out,
                                              void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * Softmax attention over a paged key/value cache: the attention layers that stand between the GDN
+ * layers of a hybrid model (Qwen3.8 kernel architecture and TDD ledger, "Current dense-27B kernel
+ * map": d256 grouped-query attention, KV cache, 8-bit KV, batched KV writes).
+ *
+ *   q, k, v --gdn_attn_prepare--> q' and the sequence's pages    (norm, rotation, quantisation)
+ *   q', pages --gdn_attn_prefill / gdn_attn_decode_step--> out    (optionally gated by sigmoid(z))
+ *   pages --gdn_attn_cache_read--> k, v                           (dense rows)
+ *
+ * Positions.  Sequence n has kv_lens[n] positions in its cache, its new tokens (the rows
+ * cu_seqlens[n] .. cu_seqlens[n+1]-1 of the call) among them as the last ones: new token i of q_len
+ * has position p = kv_lens[n] - q_len + i.  cu_seqlens NULL means one token for every sequence
+ * (total_tokens = num_seqs, token n is sequence n's).  A token with p < 0 has no place in the cache:
+ * gdn_attn_prepare writes none of it there, and no key is visible to it.  A sequence with
+ * kv_lens[n] = 0 (an unused slot of a fixed-size batch) is thus allowed, whatever its table row
+ * holds.  Rows from cu_seqlens[num_seqs] on are left as they were.
+ *
+ * Pages.  Position p of sequence n lies in page block_table[n * max_pages + p / page_size], row
+ * p % page_size.  Pages may be shared by sequences that only read them; two tokens of one call must
+ * not write the same row.  Device-side faults -- a page that is needed and lies outside
+ * [0, num_pages), kv_lens[n] outside [0, max_pages * page_size], bad cu_seqlens -- set
+ * GDN_ERR_DEVICE_ARGUMENT in the device error word; nothing is written for those tokens by
+ * gdn_attn_prepare, and the rows of such a sequence are unspecified in the other calls.
+ *
+ * This build supports head_dim 128 and 256, num_q_heads a multiple of num_kv_heads with at most 64
+ * query heads to a key head, at most 256 query heads, and pages of 16, 32, 64 or 128 rows. */
+typedef struct {
+  int32_t num_q_heads;  /* Hq: query head h reads key head h / (Hq / Hkv) */
+  int32_t num_kv_heads; /* Hkv */
+  int32_t head_dim;     /* D: 128 or 256 */
+} gdn_attn_geometry;
+
+#define GDN_CACHE_BF16 0 /* bf16 rows                                                          */
+#define GDN_CACHE_E4M3 1 /* e4m3 codes with one power of two for each row of a key head         */
+
+/* The page pool of one layer.  An e4m3 row x of D values is held as codes c and a byte b with
+ * x ~ c * 2^(b - 127): with a the row's largest finite magnitude, 2^(b - 127) is the least power of
+ * two (2^-117 or more) with a <= 448 * 2^(b - 127), and c is x * 2^(127 - b) rounded to the nearest
+ * e4m3 (ties to even).  Values that are not finite become NaN.  The value of a code is exact in
+ * bf16 (one that was rounded up to 2^128, from a magnitude above 1.9375 * 2^127, reads as an infinity). */
+typedef struct {
+  int32_t type;      /* GDN_CACHE_BF16 or GDN_CACHE_E4M3 */
+  int32_t page_size; /* rows of a page: 16, 32, 64 or 128 */
+  int32_t num_pages;
+  void* k;           /* [num_pages, Hkv, page_size, D] bf16 or e4m3 (16-byte aligned) */
+  void* v;           /* the same */
+  uint8_t* k_scale;  /* [num_pages, Hkv, page_size] exponent bytes (E4M3; NULL for BF16) */
+  uint8_t* v_scale;  /* the same */
+} gdn_kv_cache;
+
+/* Position rotation of the first rot_dim values of a head (0: none): with theta_j = p * freqs[j],
+ * j < rot_dim / 2, and the pair (a, b) = (x_j, x_{j + rot_dim/2}), or (x_{2j}, x_{2j+1}) when
+ * interleaved, becomes (a c - b s, b c + a s) with c = magnitude * cos theta, s = magnitude * sin theta. */
+typedef struct {
+  int32_t rot_dim;     /* a multiple of 16, at most D */
+  int32_t interleaved; /* 0: halves, 1: neighbours */
+  float magnitude;
+  const double* freqs; /* [rot_dim / 2] radians for each position (device, 8-byte aligned, finite, |f| <= 2 pi) */
+} gdn_rope;
+
+#define GDN_ROPE_PLAIN 0  /* f_j = base^(-2j / rot_dim)                                                       */
+#define GDN_ROPE_LINEAR 1 /* f_j / factor: positions interpolated                                             */
+#define GDN_ROPE_BASE 2   /* the plain f_j of base * factor^(rot_dim / (rot_dim - 2)): the lowest is f / factor */
+#define GDN_ROPE_RAMP 3   /* by the turns r_j = original_positions * f_j / (2 pi): f_j where r_j >= high,
+                             f_j / factor where r_j <= low, between them in proportion to r_j; the
+                             magnitude is 0.1 ln(factor) + 1 (1 for factor <= 1) */
+typedef struct {
+  int32_t kind;
+  double base, factor;
+  double original_positions, low, high; /* GDN_ROPE_RAMP */
+} gdn_rope_scaling;
+
+/* Host function: fills freqs[rot_dim / 2] and *magnitude (host memory) for gdn_rope.  rot_dim is
+ * positive and even (at least 4 for GDN_ROPE_BASE), base > 0, factor > 0, low < high. */
+GDN_API gdn_status gdn_attn_rope_frequencies(int32_t rot_dim, const gdn_rope_scaling* scaling, double* freqs,
+                                             double* magnitude);
+
+/*
+ * What the attention reads, from the projections, in one pass: every query and key head normalised
+ * and rotated, the queries written to q_out and the keys and values to the sequences' pages.
+ *   y = x * (mean_d x^2 + rms_eps)^(-1/2) * w   (y = x when w is NULL), then the rotation of gdn_rope,
+ * computed in fp32 and rounded once to bf16; an e4m3 cache quantises the rounded keys and the values.
+ *   q          Hq heads of D bf16 for each token, head h of token t at q + t * q_token_stride +
+ *              h * q_head_stride (elements, multiples of 8); NULL: keys and values alone
+ *   k, v       Hkv heads each, the same way
+ *   q_norm_w, k_norm_w  [D] bf16, or NULL for no norm
+ *   rope       NULL or rot_dim 0: no rotation.  Angles are formed to about 2^-23 turns at positions below
+ *              2^24 (2^-18 at any) without fp64 arithmetic in the token loop
+ *   q_out      [total_tokens, Hq, D] bf16; may be q itself where q has that layout
+ */
+GDN_API gdn_status gdn_attn_prepare(const gdn_attn_geometry* geo, const gdn_bf16* q, int64_t q_token_stride,
+                                    int64_t q_head_stride, const gdn_bf16* k, int64_t k_token_stride,
+                                    int64_t k_head_stride, const gdn_bf16* v, int64_t v_token_stride,
+                                    int64_t v_head_stride, const gdn_bf16* q_norm_w,
+                                    const gdn_bf16* k_norm_w, float rms_eps, const gdn_rope* rope,
+                                    const gdn_kv_cache* cache, const int32_t* block_table,
+                                    int32_t max_pages, const int32_t* kv_lens, const int32_t* cu_seqlens,
+                                    int32_t num_seqs, int32_t total_tokens, gdn_bf16* q_out, void* stream);
+
+/*
+ * Rows of the cache as dense bf16 (exact for both cache types): output rows cu_seqlens[n] ..
+ * cu_seqlens[n+1]-1 receive positions starts[n], starts[n] + 1, ... of sequence n (starts NULL: 0).
+ *   k_out, v_out  [total_tokens, Hkv, D] bf16
+ * Positions outside [0, max_pages * page_size) or on a bad page set GDN_ERR_DEVICE_ARGUMENT; their
+ * rows are left as they were.
+ */
+GDN_API gdn_status gdn_attn_cache_read(const gdn_attn_geometry* geo, const gdn_kv_cache* cache,
+                                       const int32_t* block_table, int32_t max_pages,
+                                       const int32_t* starts, const int32_t* cu_seqlens, int32_t num_seqs,
+                                       int32_t total_tokens, gdn_bf16* k_out, gdn_bf16* v_out, void* stream);
+
+/* Bytes of device workspace of the two attention calls (0 for an unsupported geometry); it needs no
+ * initialisation and is dead when the call's kernels finish. */
+GDN_API size_t gdn_attn_workspace_size(const gdn_attn_geometry* geo);
+
+/*
+ * Causal attention of the new tokens of packed sequences over their caches (which hold the new tokens
+ * too: gdn_attn_prepare first).  With p the token's position and j = 0 .. p:
+ *   s_j = softmax_scale * q . k_j,   o = sum_j e^(s_j) v_j / sum_j e^(s_j)   (0 when p < 0),
+ *   out = o, or o * sigmoid(z) where z is given.
+ * Scores and sums are fp32 with a running maximum; the weights e^(s_j - max) are rounded to bf16
+ * (binary16 for an e4m3 cache) for the product with v.
+ *   q          [total_tokens, Hq, D] bf16
+ *   z          Hq heads of D bf16 for each token, head h of token t at z + t * z_token_stride +
+ *              h * z_head_stride (elements, multiples of 8), or NULL
+ *   out        [total_tokens, Hq, D] bf16; must not overlap q or z
+ *   workspace  256-byte aligned device memory of gdn_attn_workspace_size() bytes; calls that may
+ *              overlap on the GPU (other streams, graphs replayed together) need one each
+ */
+GDN_API gdn_status gdn_attn_prefill(const gdn_attn_geometry* geo, const gdn_bf16* q, const gdn_kv_cache* cache,
+                                    const int32_t* block_table, int32_t max_pages, const int32_t* kv_lens,
+                                    const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                                    float softmax_scale, const gdn_bf16* z, int64_t z_token_stride,
+                                    int64_t z_head_stride, gdn_bf16* out, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* The same for one new token of each of `batch` sequences: q, out [batch, Hq, D], row n is sequence n's. */
+GDN_API gdn_status gdn_attn_decode_step(const gdn_attn_geometry* geo, const gdn_bf16* q,
+                                        const gdn_kv_cache* cache, const int32_t* block_table,
+                                        int32_t max_pages, const int32_t* kv_lens, int32_t batch,
+                                        float softmax_scale, const gdn_bf16* z, int64_t z_token_stride,
+                                        int64_t z_head_stride, gdn_bf16* out, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
 /*
  * Waits for `stream`, then reads and clears the library's device error word.  Returns GDN_OK,
- * GDN_ERR_DEVICE_ARGUMENT (a kernel skipped a sequence with bad cu_seqlens entries),
+ * GDN_ERR_DEVICE_ARGUMENT (a kernel skipped a sequence with bad cu_seqlens entries, or a bad page or
+ * length of a paged cache),
  * GDN_ERR_TIMEOUT (a bounded in-kernel wait ran out) or GDN_ERR_CUDA.  The word is per device
  * and shared by all streams; the kernels only ever set bits in it.
  */

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from dataclasses import dataclass
 
 import torch
 
@@ -44,9 +45,30 @@ class _Geo(ctypes.Structure):
                 ("conv_width", ctypes.c_int32)]
 
 
+class _AttnGeo(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("freqs", ctypes.c_void_p)]
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_positions", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
+
+
 def _configure(lib, debug: bool):
     P, I, F, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
-    G = ctypes.POINTER(_Geo)
+    L = ctypes.c_int64
+    G, A, C = ctypes.POINTER(_Geo), ctypes.POINTER(_AttnGeo), ctypes.POINTER(_Cache)
     sig = {
         "gdn_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "gdn_last_error_message": ([], ctypes.c_char_p),
@@ -73,6 +95,13 @@ def _configure(lib, debug: bool):
         "gdn_verify_commit": ([G, P, P, S, P, P, I, I, P], ctypes.c_int),
         "gdn_verify_fp16_state": ([G, P, P, P, P, P, P, P, P, F, F, F, P, I, I, P, S, P], ctypes.c_int),
         "gdn_verify_commit_fp16_state": ([G, P, P, S, P, P, I, I, P], ctypes.c_int),
+        "gdn_attn_rope_frequencies": ([I, ctypes.POINTER(_RopeScaling), P, P], ctypes.c_int),
+        "gdn_attn_prepare": ([A, P, L, L, P, L, L, P, L, L, P, P, F, ctypes.POINTER(_Rope), C, P, I, P, P, I, I, P, P],
+                             ctypes.c_int),
+        "gdn_attn_cache_read": ([A, C, P, I, P, P, I, I, P, P, P], ctypes.c_int),
+        "gdn_attn_workspace_size": ([A], S),
+        "gdn_attn_prefill": ([A, P, C, P, I, P, P, I, I, F, P, L, L, P, P, S, P], ctypes.c_int),
+        "gdn_attn_decode_step": ([A, P, C, P, I, P, I, F, P, L, L, P, P, S, P], ctypes.c_int),
         "gdn_check_device_errors": ([P], ctypes.c_int),
     }
     if debug:
@@ -713,3 +742,215 @@ def gdn_kda_prefill(x, conv_w, cu_seqlens, g, beta, z, norm_w, q_scale, g_min=fl
                                float(l2_eps), _p(state_in), _p(state_out), _p(z), _p(norm_w), float(rms_eps),
                                _p(out), _p(workspace), wbytes, _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------ softmax attention over a paged cache
+
+_ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3}
+
+
+@dataclass
+class KVCache:
+    """The page pool of one attention layer: k, v [num_pages, Hkv, page_size, D] bf16, or
+    float8_e4m3fn with k_scale, v_scale [num_pages, Hkv, page_size] uint8 exponent bytes."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+    @classmethod
+    def allocate(cls, num_pages, num_kv_heads, page_size, head_dim, dtype=torch.bfloat16, device="cuda"):
+        """A pool of empty pages (zeros; scale bytes of 1.0)."""
+        shape = (num_pages, num_kv_heads, page_size, head_dim)
+        k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+        if dtype == torch.bfloat16:
+            return cls(k, v)
+        ks, vs = (torch.full(shape[:3], 127, dtype=torch.uint8, device=device) for _ in range(2))
+        return cls(k, v, ks, vs)
+
+
+class _on_device:
+    """Makes a tensor's device current for a call (nothing to do when it already is)."""
+
+    def __init__(self, device):
+        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+        return False
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call is on {device}")
+
+
+def _cache_arg(cache: KVCache):
+    """Checks a cache and returns (its C struct, Hkv, D)."""
+    e4m3 = isinstance(cache.k, torch.Tensor) and cache.k.dtype == torch.float8_e4m3fn
+    kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    _dev(cache.k, kind, "cache.k")
+    if cache.k.dim() != 4:
+        raise ValueError("cache.k must be [num_pages, num_kv_heads, page_size, head_dim]")
+    pages, hkv, page, dim = cache.k.shape
+    _dev(cache.v, kind, "cache.v", (pages, hkv, page, dim))
+    ks = vs = None
+    if e4m3:
+        if cache.k_scale is None or cache.v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        ks = _dev(cache.k_scale, torch.uint8, "cache.k_scale", (pages, hkv, page)).data_ptr()
+        vs = _dev(cache.v_scale, torch.uint8, "cache.v_scale", (pages, hkv, page)).data_ptr()
+    _same_device(cache.k.device, cache_v=cache.v, cache_k_scale=cache.k_scale if e4m3 else None,
+                 cache_v_scale=cache.v_scale if e4m3 else None)
+    return _Cache(int(e4m3), page, pages, cache.k.data_ptr(), cache.v.data_ptr(), ks, vs), hkv, dim
+
+
+def _heads(t, name, T, H, D):
+    """A bf16 [T, H, D] tensor whose D values are contiguous: (pointer, token stride, head stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if tuple(t.shape) != (T, H, D):
+        raise ValueError(f"{name} must have shape {(T, H, D)}, got {tuple(t.shape)}")
+    st, sh, sd = t.stride()
+    if sd != 1:
+        raise ValueError(f"the values of a head of {name} must be contiguous")
+    return t.data_ptr(), (st if T > 1 else H * D), (sh if H > 1 else D)
+
+
+def _attn_table(block_table, per_seq, name, cu_seqlens, T):
+    """Number of sequences of a call, its per-sequence arrays checked."""
+    N = T if cu_seqlens is None else cu_seqlens.numel() - 1
+    _dev(cu_seqlens, torch.int32, "cu_seqlens", (N + 1,))
+    _dev(per_seq, torch.int32, name, (N,))
+    _dev(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != N:
+        raise ValueError(f"block_table must have shape ({N}, max_pages), got {tuple(block_table.shape)}")
+    return N
+
+
+def gdn_attn_rope_frequencies(rot_dim: int, base: float, scaling: str = "plain", factor: float = 1.0,
+                              original_positions: float = 0.0, low: float = 1.0, high: float = 32.0):
+    """Frequencies [rot_dim / 2] (float64, on the host) and magnitude of the position rotation;
+    scaling is "plain", "linear", "base" or "ramp" (GDN_ROPE_* of gdn.h)."""
+    if scaling not in _ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_KINDS)}, got {scaling!r}")
+    sc = _RopeScaling(_ROPE_KINDS[scaling], float(base), float(factor), float(original_positions), float(low),
+                      float(high))
+    freqs = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.float64)
+    mag = ctypes.c_double()
+    _check(_L().gdn_attn_rope_frequencies(int(rot_dim), ctypes.byref(sc), _p(freqs), ctypes.byref(mag)))
+    return freqs, mag.value
+
+
+def gdn_attn_prepare(q, k, v, cache: KVCache, block_table, kv_lens, cu_seqlens=None, q_norm_w=None, k_norm_w=None,
+                     rope_freqs=None, rope_interleaved=False, rope_scale=1.0, rms_eps=1e-6, q_out=None, stream=None):
+    """Norms and rotates every head of q and k, writes k and v to their pages; returns q_out
+    [T, Hq, D] (None when q is None).
+
+    q [T, Hq, D], k, v [T, Hkv, D] bf16 with contiguous heads (views of one projection's output
+    will do); rope_freqs [rot_dim / 2] float64 on the GPU, scaled cos and sin by rope_scale.
+    """
+    lib = _L()
+    c, hkv, D = _cache_arg(cache)
+    T = k.shape[0]
+    kp, vp = _heads(k, "k", T, hkv, D), _heads(v, "v", T, hkv, D)
+    hq, qp = hkv, (None, 0, 0)
+    if q is not None:
+        hq = q.shape[1]
+        qp = _heads(q, "q", T, hq, D)
+        if q_out is None:
+            q_out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device)
+        _dev(q_out, torch.bfloat16, "q_out", (T, hq, D))
+    else:
+        q_out = None
+    N = _attn_table(block_table, kv_lens, "kv_lens", cu_seqlens, T)
+    _dev(q_norm_w, torch.bfloat16, "q_norm_w", (D,))
+    _dev(k_norm_w, torch.bfloat16, "k_norm_w", (D,))
+    rope = None
+    if rope_freqs is not None:
+        _dev(rope_freqs, torch.float64, "rope_freqs")
+        rope = ctypes.byref(_Rope(2 * rope_freqs.numel(), int(bool(rope_interleaved)), float(rope_scale),
+                                  rope_freqs.data_ptr()))
+    dev = cache.k.device
+    _same_device(dev, q=q, k=k, v=v, q_out=q_out, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens,
+                 q_norm_w=q_norm_w, k_norm_w=k_norm_w, rope_freqs=rope_freqs)
+    with _on_device(dev):
+        _check(lib.gdn_attn_prepare(ctypes.byref(_AttnGeo(hq, hkv, D)), *qp, *kp, *vp, _p(q_norm_w), _p(k_norm_w),
+                                    float(rms_eps), rope, ctypes.byref(c), _p(block_table), block_table.shape[1],
+                                    _p(kv_lens), _p(cu_seqlens), N, T, _p(q_out), _stream(stream)))
+    return q_out
+
+
+def gdn_attn_cache_read(cache: KVCache, block_table, cu_seqlens, k_out, v_out, starts=None, stream=None):
+    """Rows of the cache as dense bf16: k_out, v_out [T, Hkv, D] receive, for every sequence, the
+    positions from starts[n] (0 when None) on; returns (k_out, v_out)."""
+    lib = _L()
+    c, hkv, D = _cache_arg(cache)
+    T = k_out.shape[0]
+    _dev(k_out, torch.bfloat16, "k_out", (T, hkv, D))
+    _dev(v_out, torch.bfloat16, "v_out", (T, hkv, D))
+    N = _attn_table(block_table, starts, "starts", cu_seqlens, T)
+    dev = cache.k.device
+    _same_device(dev, k_out=k_out, v_out=v_out, block_table=block_table, starts=starts, cu_seqlens=cu_seqlens)
+    with _on_device(dev):
+        _check(lib.gdn_attn_cache_read(ctypes.byref(_AttnGeo(hkv, hkv, D)), ctypes.byref(c), _p(block_table),
+                                       block_table.shape[1], _p(starts), _p(cu_seqlens), N, T, _p(k_out), _p(v_out),
+                                       _stream(stream)))
+    return k_out, v_out
+
+
+def gdn_attn_workspace_size(num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    return int(_L().gdn_attn_workspace_size(ctypes.byref(_AttnGeo(num_q_heads, num_kv_heads, head_dim))))
+
+
+def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out, workspace, stream):
+    lib = _L()
+    c, hkv, D = _cache_arg(cache)
+    _dev(q, torch.bfloat16, "q")
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q must have shape (T, Hq, {D}), got {tuple(q.shape)}")
+    T, hq, _ = q.shape
+    N = _attn_table(block_table, kv_lens, "kv_lens", cu_seqlens, T)
+    zp = (None, 0, 0) if z is None else _heads(z, "z", T, hq, D)
+    if out is None:
+        out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device)
+    _dev(out, torch.bfloat16, "out", (T, hq, D))
+    geo = ctypes.byref(_AttnGeo(hq, hkv, D))
+    if workspace is None:
+        workspace = torch.empty(lib.gdn_attn_workspace_size(geo), dtype=torch.uint8, device=q.device)
+    dev = cache.k.device
+    _same_device(dev, q=q, z=z, out=out, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens,
+                 workspace=workspace)
+    with _on_device(dev):
+        args = (float(softmax_scale), *zp, _p(out), _p(workspace), workspace.numel() * workspace.element_size(),
+                _stream(stream))
+        if cu_seqlens is None:
+            _check(lib.gdn_attn_decode_step(geo, _p(q), ctypes.byref(c), _p(block_table), block_table.shape[1],
+                                            _p(kv_lens), T, *args))
+        else:
+            _check(lib.gdn_attn_prefill(geo, _p(q), ctypes.byref(c), _p(block_table), block_table.shape[1],
+                                        _p(kv_lens), _p(cu_seqlens), N, T, *args))
+    return out
+
+
+def gdn_attn_prefill(q, cache: KVCache, block_table, kv_lens, cu_seqlens, softmax_scale, z=None, out=None,
+                     workspace=None, stream=None):
+    """Causal attention of packed new tokens over their caches (which hold them too), optionally
+    gated by sigmoid(z); q, z, out [T, Hq, D] bf16.  Returns out."""
+    if cu_seqlens is None:
+        raise TypeError("cu_seqlens must be a CUDA tensor")
+    return _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out, workspace, stream)
+
+
+def gdn_attn_decode_step(q, cache: KVCache, block_table, kv_lens, softmax_scale, z=None, out=None, workspace=None,
+                         stream=None):
+    """gdn_attn_prefill for one new token of every sequence: row n of q [B, Hq, D] is sequence n's."""
+    return _attention(q, cache, block_table, kv_lens, None, softmax_scale, z, out, workspace, stream)

@@ -4,6 +4,7 @@
 // returns an error has launched nothing.  Device-side faults (bad cu_seqlens contents, a bounded
 // wait that ran out) set bits in a per-device error word that gdn_check_device_errors() reads.
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -708,6 +709,242 @@ gdn_status gdn_chunk_prefill_noalloc(const gdn_geometry* geo, const gdn_bf16* qk
                            state_out, z, norm_w, rms_eps, out, scratch, GDN_NOALLOC_SCRATCH_BYTES, stream);
 }
 
+}  // extern "C"
+
+namespace {
+
+gdn_status check_attn_geometry(const gdn_attn_geometry* geo) {
+  if (!geo) return fail(GDN_ERR_INVALID_ARGUMENT, "geometry is NULL");
+  if (geo->num_kv_heads <= 0 || geo->num_q_heads <= 0 || geo->num_q_heads % geo->num_kv_heads != 0)
+    return fail(GDN_ERR_UNSUPPORTED_GEOMETRY, "num_q_heads (%d) must be a positive multiple of num_kv_heads (%d)",
+                geo->num_q_heads, geo->num_kv_heads);
+  if (geo->head_dim != 128 && geo->head_dim != 256)
+    return fail(GDN_ERR_UNSUPPORTED_GEOMETRY, "head_dim must be 128 or 256 (got %d)", geo->head_dim);
+  if (geo->num_q_heads > 256 || geo->num_q_heads / geo->num_kv_heads > 64)
+    return fail(GDN_ERR_UNSUPPORTED_GEOMETRY, "at most 256 query heads and 64 to a key head (got %d, %d key heads)",
+                geo->num_q_heads, geo->num_kv_heads);
+  return GDN_OK;
+}
+
+gdn_status check_paged_cache(const gdn_kv_cache* c, const int32_t* block_table, int32_t max_pages,
+                             gdn::PagedCache* out) {
+  if (!c) return fail(GDN_ERR_INVALID_ARGUMENT, "cache is NULL");
+  if (c->type != GDN_CACHE_BF16 && c->type != GDN_CACHE_E4M3)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "unknown cache type %d", c->type);
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return fail(GDN_ERR_UNSUPPORTED_GEOMETRY, "page_size must be 16, 32, 64 or 128 (got %d)", c->page_size);
+  if (c->num_pages < 1 || max_pages < 1)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "num_pages (%d) and max_pages (%d) must be positive", c->num_pages,
+                max_pages);
+  GDN_REQUIRE(c->k, "cache k");
+  GDN_REQUIRE(c->v, "cache v");
+  if (c->type == GDN_CACHE_E4M3 && (!c->k_scale || !c->v_scale))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "k_scale or v_scale is NULL");
+  if (!block_table) return fail(GDN_ERR_INVALID_ARGUMENT, "block_table is NULL");
+  if (reinterpret_cast<uintptr_t>(block_table) & 3u)
+    return fail(GDN_ERR_MISALIGNED, "block_table is not 4-byte aligned");
+  out->k = c->k;
+  out->v = c->v;
+  out->k_scale = c->k_scale;
+  out->v_scale = c->v_scale;
+  out->table = block_table;
+  out->max_pages = max_pages;
+  out->num_pages = c->num_pages;
+  out->page_shift = c->page_size == 16 ? 4 : c->page_size == 32 ? 5 : c->page_size == 64 ? 6 : 7;
+  out->e4m3 = c->type == GDN_CACHE_E4M3;
+  return GDN_OK;
+}
+
+// num_seqs, total_tokens and the arrays that go by sequence; *nothing: the call has no rows.
+gdn_status check_attn_batch(const int32_t* per_seq, const char* name, bool required, const int32_t* cu_seqlens,
+                            int32_t num_seqs, int32_t total_tokens, bool* nothing) {
+  if (num_seqs < 0 || total_tokens < 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "negative size (num_seqs=%d, total_tokens=%d)", num_seqs, total_tokens);
+  if (num_seqs == 0 && total_tokens > 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "total_tokens=%d with no sequence", total_tokens);
+  *nothing = total_tokens == 0;
+  if (*nothing) return GDN_OK;
+  if (!cu_seqlens && num_seqs != total_tokens)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "without cu_seqlens num_seqs (%d) must be total_tokens (%d)", num_seqs,
+                total_tokens);
+  if (required && !per_seq) return fail(GDN_ERR_INVALID_ARGUMENT, "%s is NULL", name);
+  if ((reinterpret_cast<uintptr_t>(cu_seqlens) | reinterpret_cast<uintptr_t>(per_seq)) & 3u)
+    return fail(GDN_ERR_MISALIGNED, "cu_seqlens or %s is not 4-byte aligned", name);
+  return GDN_OK;
+}
+
+gdn_status check_head_rows(const gdn_bf16* p, int64_t token, int64_t head, const char* name) {
+  GDN_REQUIRE(p, name);
+  if ((token | head) & 7)
+    return fail(GDN_ERR_MISALIGNED, "the strides of %s (%lld, %lld) must be multiples of 8 elements", name,
+                (long long)token, (long long)head);
+  return GDN_OK;
+}
+
+gdn_status attention(const gdn_attn_geometry* geo, const gdn_bf16* q, const gdn_kv_cache* cache,
+                     const int32_t* block_table, int32_t max_pages, const int32_t* kv_lens,
+                     const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens, float softmax_scale,
+                     const gdn_bf16* z, int64_t z_token_stride, int64_t z_head_stride, gdn_bf16* out,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_status s = check_attn_geometry(geo);
+  if (s != GDN_OK) return s;
+  bool nothing;
+  if ((s = check_attn_batch(kv_lens, "kv_lens", true, cu_seqlens, num_seqs, total_tokens, &nothing)) != GDN_OK)
+    return s;
+  if (nothing) return ok();
+  gdn::PagedCache c;
+  if ((s = check_paged_cache(cache, block_table, max_pages, &c)) != GDN_OK) return s;
+  GDN_REQUIRE(q, "q");
+  GDN_REQUIRE(out, "out");
+  if (z && (s = check_head_rows(z, z_token_stride, z_head_stride, "z")) != GDN_OK) return s;
+  if (!(softmax_scale > 0.f) || softmax_scale > 3.4e38f)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "softmax_scale must be positive and finite");
+  const size_t bytes = (size_t)total_tokens * geo->num_q_heads * geo->head_dim * 2;
+  if (overlaps(q, bytes, out, bytes)) return fail(GDN_ERR_INVALID_ARGUMENT, "out overlaps q");
+  const size_t need = gdn::attn_workspace_bytes(geo->head_dim);
+  if (!workspace || workspace_bytes < need)
+    return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, workspace ? workspace_bytes : 0);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(GDN_ERR_MISALIGNED, "workspace is not 256-byte aligned");
+  gdn::LaunchEnv env;
+  if ((s = make_env(stream, &env)) != GDN_OK) return s;
+  return launched(gdn::launch_attn(env, geo->num_q_heads, geo->num_kv_heads, geo->head_dim, q, c, kv_lens, cu_seqlens,
+                                   num_seqs, total_tokens, softmax_scale, {z, z_token_stride, z_head_stride}, out,
+                                   workspace),
+                  "attention launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_attn_rope_frequencies(int32_t rot_dim, const gdn_rope_scaling* sc, double* freqs, double* magnitude) {
+  if (!sc || !freqs || !magnitude) return fail(GDN_ERR_INVALID_ARGUMENT, "scaling, freqs or magnitude is NULL");
+  if (rot_dim <= 0 || rot_dim % 2) return fail(GDN_ERR_INVALID_ARGUMENT, "rot_dim (%d) must be positive and even", rot_dim);
+  if (sc->kind < GDN_ROPE_PLAIN || sc->kind > GDN_ROPE_RAMP)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "unknown scaling kind %d", sc->kind);
+  if (!(sc->base > 0.) || !std::isfinite(sc->base)) return fail(GDN_ERR_INVALID_ARGUMENT, "base must be positive");
+  const bool scaled = sc->kind != GDN_ROPE_PLAIN;
+  if (scaled && (!(sc->factor > 0.) || !std::isfinite(sc->factor)))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "factor must be positive");
+  if (sc->kind == GDN_ROPE_BASE && rot_dim < 4)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "GDN_ROPE_BASE needs rot_dim >= 4");
+  if (sc->kind == GDN_ROPE_RAMP && (!(sc->low < sc->high) || !(sc->original_positions > 0.)))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "low < high and original_positions > 0 are required");
+  *magnitude = 1.;
+  double base = sc->base;
+  if (sc->kind == GDN_ROPE_BASE) base *= std::pow(sc->factor, rot_dim / (rot_dim - 2.));
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    double f = std::pow(base, -2. * j / rot_dim);
+    if (sc->kind == GDN_ROPE_LINEAR) f /= sc->factor;
+    if (sc->kind == GDN_ROPE_RAMP) {
+      const double turns = sc->original_positions * f / 6.283185307179586477;
+      const double kept = std::fmin(std::fmax((turns - sc->low) / (sc->high - sc->low), 0.), 1.);
+      f = f * kept + f / sc->factor * (1. - kept);
+    }
+    freqs[j] = f;
+  }
+  if (sc->kind == GDN_ROPE_RAMP && sc->factor > 1.) *magnitude = 0.1 * std::log(sc->factor) + 1.;
+  return ok();
+}
+
+gdn_status gdn_attn_prepare(const gdn_attn_geometry* geo, const gdn_bf16* q, int64_t q_token_stride,
+                            int64_t q_head_stride, const gdn_bf16* k, int64_t k_token_stride, int64_t k_head_stride,
+                            const gdn_bf16* v, int64_t v_token_stride, int64_t v_head_stride, const gdn_bf16* q_norm_w,
+                            const gdn_bf16* k_norm_w, float rms_eps, const gdn_rope* rope, const gdn_kv_cache* cache,
+                            const int32_t* block_table, int32_t max_pages, const int32_t* kv_lens,
+                            const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens, gdn_bf16* q_out,
+                            void* stream) {
+  gdn_status s = check_attn_geometry(geo);
+  if (s != GDN_OK) return s;
+  bool nothing;
+  if ((s = check_attn_batch(kv_lens, "kv_lens", true, cu_seqlens, num_seqs, total_tokens, &nothing)) != GDN_OK)
+    return s;
+  if (nothing) return ok();
+  gdn::PagedCache c;
+  if ((s = check_paged_cache(cache, block_table, max_pages, &c)) != GDN_OK) return s;
+  const int D = geo->head_dim;
+  if (q) {
+    if ((s = check_head_rows(q, q_token_stride, q_head_stride, "q")) != GDN_OK) return s;
+    GDN_REQUIRE(q_out, "q_out");
+    // Each row is read whole before it is written, by the same lanes: q_out may be q itself, but rows
+    // at other places would be overwritten before they are read.
+    const bool same = q == q_out && q_head_stride == D && q_token_stride == (int64_t)D * geo->num_q_heads;
+    if (!same && q_token_stride >= 0 && q_head_stride >= 0) {
+      const size_t span = ((size_t)(total_tokens - 1) * q_token_stride + (size_t)(geo->num_q_heads - 1) * q_head_stride + D) * 2;
+      if (overlaps(q, span, q_out, (size_t)total_tokens * geo->num_q_heads * D * 2))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "q_out overlaps q without being it");
+    }
+  }
+  if ((s = check_head_rows(k, k_token_stride, k_head_stride, "k")) != GDN_OK) return s;
+  if ((s = check_head_rows(v, v_token_stride, v_head_stride, "v")) != GDN_OK) return s;
+  GDN_OPTIONAL(q_norm_w, "q_norm_w");
+  GDN_OPTIONAL(k_norm_w, "k_norm_w");
+  if (!(rms_eps >= 0.f)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be >= 0");
+  gdn::Rope r = {nullptr, 0, 0, 1.f};
+  if (rope && rope->rot_dim != 0) {
+    if (rope->rot_dim < 0 || rope->rot_dim % 16 || rope->rot_dim > D)
+      return fail(GDN_ERR_UNSUPPORTED_GEOMETRY, "rot_dim must be a multiple of 16 and at most %d (got %d)", D,
+                  rope->rot_dim);
+    if (!rope->freqs) return fail(GDN_ERR_INVALID_ARGUMENT, "freqs is NULL");
+    if (reinterpret_cast<uintptr_t>(rope->freqs) & 7u) return fail(GDN_ERR_MISALIGNED, "freqs is not 8-byte aligned");
+    r = {rope->freqs, rope->rot_dim, rope->interleaved, rope->magnitude};
+  }
+  gdn::LaunchEnv env;
+  if ((s = make_env(stream, &env)) != GDN_OK) return s;
+  return launched(gdn::launch_attn_prepare(env, geo->num_q_heads, geo->num_kv_heads, D,
+                                           {q, q_token_stride, q_head_stride}, {k, k_token_stride, k_head_stride},
+                                           {v, v_token_stride, v_head_stride}, q_norm_w, k_norm_w, rms_eps, r, c,
+                                           kv_lens, cu_seqlens, num_seqs, total_tokens, q_out),
+                  "attention prepare launch");
+}
+
+gdn_status gdn_attn_cache_read(const gdn_attn_geometry* geo, const gdn_kv_cache* cache, const int32_t* block_table,
+                               int32_t max_pages, const int32_t* starts, const int32_t* cu_seqlens, int32_t num_seqs,
+                               int32_t total_tokens, gdn_bf16* k_out, gdn_bf16* v_out, void* stream) {
+  gdn_status s = check_attn_geometry(geo);
+  if (s != GDN_OK) return s;
+  bool nothing;
+  if ((s = check_attn_batch(starts, "starts", false, cu_seqlens, num_seqs, total_tokens, &nothing)) != GDN_OK)
+    return s;
+  if (nothing) return ok();
+  gdn::PagedCache c;
+  if ((s = check_paged_cache(cache, block_table, max_pages, &c)) != GDN_OK) return s;
+  GDN_REQUIRE(k_out, "k_out");
+  GDN_REQUIRE(v_out, "v_out");
+  gdn::LaunchEnv env;
+  if ((s = make_env(stream, &env)) != GDN_OK) return s;
+  return launched(gdn::launch_attn_cache_read(env, geo->num_kv_heads, geo->head_dim, c, starts, cu_seqlens, num_seqs,
+                                              total_tokens, k_out, v_out),
+                  "cache read launch");
+}
+
+size_t gdn_attn_workspace_size(const gdn_attn_geometry* geo) {
+  return check_attn_geometry(geo) == GDN_OK ? gdn::attn_workspace_bytes(geo->head_dim) : 0;
+}
+
+gdn_status gdn_attn_prefill(const gdn_attn_geometry* geo, const gdn_bf16* q, const gdn_kv_cache* cache,
+                            const int32_t* block_table, int32_t max_pages, const int32_t* kv_lens,
+                            const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens, float softmax_scale,
+                            const gdn_bf16* z, int64_t z_token_stride, int64_t z_head_stride, gdn_bf16* out,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  if (total_tokens > 0 && num_seqs > 0 && !cu_seqlens) return fail(GDN_ERR_INVALID_ARGUMENT, "cu_seqlens is NULL");
+  return attention(geo, q, cache, block_table, max_pages, kv_lens, cu_seqlens, num_seqs, total_tokens, softmax_scale, z,
+                   z_token_stride, z_head_stride, out, workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_attn_decode_step(const gdn_attn_geometry* geo, const gdn_bf16* q, const gdn_kv_cache* cache,
+                                const int32_t* block_table, int32_t max_pages, const int32_t* kv_lens, int32_t batch,
+                                float softmax_scale, const gdn_bf16* z, int64_t z_token_stride, int64_t z_head_stride,
+                                gdn_bf16* out, void* workspace, size_t workspace_bytes, void* stream) {
+  return attention(geo, q, cache, block_table, max_pages, kv_lens, nullptr, batch, batch, softmax_scale, z,
+                   z_token_stride, z_head_stride, out, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+extern "C" {
+
 gdn_status gdn_check_device_errors(void* stream) {
   gdn::LaunchEnv env;
   gdn_status s = make_env(stream, &env);
@@ -724,7 +961,7 @@ gdn_status gdn_check_device_errors(void* stream) {
   }
   if (word & gdn::kErrTimeout) return fail(GDN_ERR_TIMEOUT, "an in-kernel wait ran out (word 0x%x)", word);
   if (word & gdn::kErrDeviceArgument)
-    return fail(GDN_ERR_DEVICE_ARGUMENT, "a kernel rejected cu_seqlens contents (word 0x%x)", word);
+    return fail(GDN_ERR_DEVICE_ARGUMENT, "a kernel rejected cu_seqlens, page or length contents (word 0x%x)", word);
   return ok();
 }
 

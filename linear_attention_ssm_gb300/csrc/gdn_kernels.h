@@ -115,4 +115,38 @@ cudaError_t test_set_dropped_copy_decode(unsigned on);  // the binary16 decode s
 cudaError_t test_set_dropped_copy_chunk(unsigned on);   // the chunk state kernel's first vector-block copy
 #endif
 
+// Softmax attention over a paged key/value cache (attn_cache.cu, attn.cu).
+struct PagedCache {
+  void* k;               // [pages, Hkv, page, D] bf16 or e4m3
+  void* v;
+  uint8_t* k_scale;      // [pages, Hkv, page] exponent bytes (e4m3), else NULL
+  uint8_t* v_scale;
+  const int32_t* table;  // [N, max_pages]
+  int32_t max_pages, num_pages;
+  int page_shift;        // log2 of the rows of a page
+  bool e4m3;
+};
+// A strided tensor of heads: head h of token t at p + t * token + h * head (elements).
+struct HeadRows {
+  const uint16_t* p;
+  long token, head;
+};
+struct Rope {
+  const double* freqs;
+  int rot;  // rotated values of a head, 0: none
+  int interleaved;
+  float magnitude;
+};
+cudaError_t launch_attn_prepare(const LaunchEnv& env, int Hq, int Hkv, int D, const HeadRows& q, const HeadRows& k,
+                                const HeadRows& v, const uint16_t* qw, const uint16_t* kw, float eps,
+                                const Rope& rope, const PagedCache& cache, const int32_t* kv_lens,
+                                const int32_t* cu, int N, int T, uint16_t* q_out);
+cudaError_t launch_attn_cache_read(const LaunchEnv& env, int Hkv, int D, const PagedCache& cache,
+                                   const int32_t* starts, const int32_t* cu, int N, int T, uint16_t* k_out,
+                                   uint16_t* v_out);
+size_t attn_workspace_bytes(int D);
+cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint16_t* q, const PagedCache& cache,
+                        const int32_t* kv_lens, const int32_t* cu, int N, int T, float scale, const HeadRows& z,
+                        uint16_t* out, void* workspace);
+
 }  // namespace gdn
