@@ -1,10 +1,39 @@
-// attn.cu -- softmax attention of new tokens over a paged key/value cache.
+// attn.cu -- softmax attention of new tokens over a paged key/value cache, on the tcgen05 tensor cores.
+//
+// A tile is 128 rows of one key head of one sequence: the group's query heads of consecutive tokens,
+// row = token * group + head.  Per block of 128 keys
+//   S = Q K^T (fp32, tensor memory)  ->  p = 2^(S - m)  ->  P (16 bits, tensor memory, over S)  ->  O += P V
+// with the running maximum m and sum l of every row in the registers of the thread that owns the row, O
+// in tensor memory.  m is raised (and O, l scaled down) only when a block exceeds it by more than 2^8:
+// the weights stay below 2^8 and the common block leaves O alone.
+//
+// Two S slots let one block's softmax run beside the other's products.  Long chunks at D = 128 take two
+// tiles a CTA, a slot each (kTiles = 2: K and V are read once for 256 rows); otherwise the blocks of
+// one tile alternate between the slots (kTiles = 1; at D = 256 O alone fills half the tensor memory).
+//
+// Warps: four a tile for the softmax, one that issues the products, one that loads K and V by TMA
+// into a ring of 32 KB stages, one that zeroes the value rows behind the last key (a page's unused rows
+// may hold anything, and 0 * NaN is not 0).
+//
+// Work: the (tile, block) pairs of all sequences in one line, cut into one equal piece for each SM.  A
+// tile that a cut falls into leaves its parts (O, m, l) in the workspace for a second kernel to join,
+// so a few long sequences spread over the whole GPU as a large batch does.
+#include <cstring>
+
 #include "attn_common.cuh"
+#include "chunk_common.cuh"
 
 namespace gdn {
 namespace {
 
+constexpr int kMaxCtas = 160;   // SMs of the largest part of this architecture
+constexpr int kBlock = 128;     // keys of a block
+constexpr uint32_t kStage = 32768;
+constexpr float kLazy = 8.f;    // the maximum is raised when a block exceeds it by this power of two
+
 struct AttnParams {
+  CUtensorMap tmap_k;  // pages as [pages * Hkv * page][D] bf16, box 64 x min(page, 64), 128-byte swizzle
+  CUtensorMap tmap_v;
   const uint16_t* q;
   PagedCache cache;
   const int32_t* kv_lens;
@@ -13,8 +42,774 @@ struct AttnParams {
   uint16_t* out;
   unsigned* err;
   float scale_log2;
-  int Hq, Hkv, N, T;
+  int Hq, Hkv, G, N, T;
+  int sub;       // tokens of one 128-row tile: 128 / G
+  int4* desc;    // [2 * grid] what each part of a cut tile holds
+  float2* ml;    // [2 * grid][rows] maximum (log2 units) and sum
+  float4* part;  // [2 * grid][tiles][D / 4][128] unnormalised O
 };
+
+// ---------------------------------------------------------------- the line of work
+
+// sum_{i < n} floor((a i + b) / m), all arguments >= 0
+__device__ __forceinline__ long floor_sum(long n, long m, long a, long b) {
+  long s = 0;
+  while (n > 0) {
+    if (a >= m) {
+      s += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      s += n * (b / m);
+      b %= m;
+    }
+    const long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// One sequence's new tokens and cache.
+struct SeqInfo {
+  int first, len, kv;
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, bool report) {
+  SeqInfo s = {n, 1, 0};
+  bool bad = false;
+  if (p.cu) {
+    const int a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1);
+    bad = a < 0 || b < a || b > p.T;
+    s.first = a;
+    s.len = bad ? 0 : b - a;
+  }
+  s.kv = __ldg(p.kv_lens + n);
+  if (s.kv < 0 || s.kv > ((long)p.cache.max_pages << p.cache.page_shift)) {
+    bad = true;
+    s.kv = 0;
+  }
+  if (bad && report) raise_error(p.err, kErrDeviceArgument);
+  return s;
+}
+
+// Keys that the last token of tile i sees; blocks of that tile (one at least, so that rows without a
+// key are visited too); blocks of the tiles before tile i.
+struct Tiles {
+  int p0, len, step;  // position of the first new token, new tokens, tokens of a tile
+  __device__ __forceinline__ int count() const { return (len + step - 1) / step; }
+  __device__ __forceinline__ int keys(int i) const { return p0 + (int)min((long)(i + 1) * step, (long)len); }
+  __device__ __forceinline__ int blocks(int i) const {
+    const int k = keys(i);
+    return k <= kBlock ? 1 : (int)(((long)k + kBlock - 1) / kBlock);
+  }
+  __device__ __forceinline__ long before(int i) const {
+    const int last = count() - 1, full = min(i, last);
+    if (full <= 0) return i > last && last >= 0 ? blocks(last) : 0;
+    const long lead = (long)kBlock - p0;  // tiles with at most one block: (t + 1) step <= lead
+    const int t0 = lead < step ? 0 : (int)min((long)full, lead / step);
+    long s = t0;
+    if (full > t0) s += floor_sum(full - t0, kBlock, step, (long)(t0 + 1) * step + p0 + kBlock - 1);
+    return s + (i > last ? blocks(last) : 0);
+  }
+};
+
+// A run of blocks [j0, j1) of one tile.
+struct Segment {
+  int n, hk;
+  int row0, ntok, pos0;  // packed row and position of the tile's first token, tokens
+  int keys;              // that the tile's last token sees (<= 0: no row sees any)
+  int j0, j1, nb;        // nb: the tile's blocks
+};
+
+// A CTA's piece of the line, segment by segment.  Every warp walks it by itself.
+struct Walk {
+  long left;  // blocks not yet taken
+  int n, hk, tile, j;
+  SeqInfo s;
+  Tiles t;
+
+  __device__ __forceinline__ void load(const AttnParams& p, int step) {
+    s = seq_info(p, n, false);
+    t = {s.kv - s.len, s.len, step};
+  }
+  __device__ __forceinline__ bool next(const AttnParams& p, int step, Segment& g) {
+    if (left <= 0) return false;
+    g.n = n;
+    g.hk = hk;
+    g.nb = t.blocks(tile);
+    g.row0 = s.first + tile * step;
+    g.ntok = min(step, s.len - tile * step);
+    g.pos0 = t.p0 + tile * step;
+    g.keys = t.keys(tile);
+    g.j0 = j;
+    g.j1 = (int)min((long)g.nb, j + left);
+    left -= g.j1 - g.j0;
+    j = g.j1;
+    if (left > 0) {  // the next tile, key head, sequence
+      j = 0;
+      if (++tile == t.count()) {
+        tile = 0;
+        if (++hk == p.Hkv) {
+          hk = 0;
+          do {
+            if (++n >= p.N) {
+              left = 0;
+              break;
+            }
+            load(p, step);
+          } while (s.len == 0);
+        }
+      }
+    }
+    return true;
+  }
+};
+
+struct WalkStart {
+  long left, rem;
+  int n, hk, tile, j;
+};
+
+// ---------------------------------------------------------------- layout of a CTA
+
+template <int D, int kTiles>
+struct Cfg {
+  static constexpr int kSoftWarps = 4 * kTiles;
+  static constexpr int kThreads = 32 * (kSoftWarps + 4);
+  static constexpr uint32_t kQ = kTiles * 128 * D * 2;
+  static constexpr int kStages = (int)((224 * 1024 - kQ) / kStage);
+  static constexpr int kParts = D / 128;  // stages of a block's keys, and of its values
+  static constexpr uint32_t kOffStage = kQ;
+  static constexpr uint32_t kOffBar = kQ + kStages * kStage;
+  static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;  // barriers; alignment of the base
+  static constexpr uint32_t kColO = 256;                    // tensor memory: two S slots of 128 columns, then O
+};
+
+struct Bars {
+  uint32_t full, empty, tail, s_full, p_full, o_full, q_full, done;  // shared addresses of the first of each kind
+};
+
+// 128 columns of this warp's 32 lanes, behind one wait.
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
+  uint32_t r[128];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,"
+      "%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,"
+      "%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,"
+      "%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
+        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
+        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]),
+        "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]),
+        "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]),
+        "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]),
+        "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]),
+        "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]),
+        "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
+        "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]),
+        "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]),
+        "=r"(r[126]), "=r"(r[127])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* q) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(q) + 1023) & ~(uintptr_t)1023);
+}
+
+// A position in the ring of stages: which stage, and which pass over the ring.
+template <int kStages>
+struct Ring {
+  int i = 0;
+  uint32_t pass = 0;
+  __device__ __forceinline__ void step() {
+    if (++i == kStages) {
+      i = 0;
+      pass ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void skip(long n) {
+    const long at = i + n;
+    pass ^= (uint32_t)(at / kStages) & 1u;
+    i = (int)(at % kStages);
+  }
+};
+
+template <int D, int kTiles>
+__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
+  using C = Cfg<D, kTiles>;
+  constexpr int kStages = C::kStages, kParts = C::kParts;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int step = kTiles * p.sub;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
+  WalkStart* start = reinterpret_cast<WalkStart*>(bars + 34);
+  long* scan = reinterpret_cast<long*>(bars + 40);
+  const uint32_t b0 = smem_u32(bars);
+  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26};
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar.full + 8 * i, 1);
+      mbar_init(bar.empty + 8 * i, 1);
+      mbar_init(bar.tail + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar.s_full + 8 * i, 1);
+      mbar_init(bar.p_full + 8 * i, 4);
+      mbar_init(bar.o_full + 8 * i, 1);
+      mbar_init(bar.q_full + 8 * i, 4);
+    }
+    mbar_init(bar.done, 1);
+    fence_mbar_init();
+    prefetch_tensormap(&p.tmap_k);
+    prefetch_tensormap(&p.tmap_v);
+    start->left = 0;
+    p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    p.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+  }
+  if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
+
+  // ---- this CTA's piece of the line
+  {
+    long mine = 0;
+    for (int n = tid; n < p.N; n += C::kThreads) {
+      const SeqInfo s = seq_info(p, n, blockIdx.x == 0);
+      const Tiles t = {s.kv - s.len, s.len, step};
+      if (s.len > 0) mine += t.before(t.count());
+    }
+    mine *= p.Hkv;
+    long sum = mine;
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) scan[warp] = sum;
+    __syncthreads();
+    long total = 0;
+    for (int w = 0; w < C::kThreads / 32; ++w) total += scan[w];
+    __syncthreads();
+    const long u0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
+    const long u1 = total / gridDim.x * (blockIdx.x + 1) + total % gridDim.x * (blockIdx.x + 1) / gridDim.x;
+    if (u1 > u0) {
+      long base = 0;  // blocks of the sequences before this round's
+      for (int n0 = 0; n0 < p.N; n0 += C::kThreads) {
+        const int n = n0 + tid;
+        long u = 0;
+        if (n < p.N) {
+          const SeqInfo s = seq_info(p, n, false);
+          const Tiles t = {s.kv - s.len, s.len, step};
+          if (s.len > 0) u = t.before(t.count()) * p.Hkv;
+        }
+        long inc = u;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+          if (lane >= o) inc += x;
+        }
+        if (lane == 31) scan[warp] = inc;
+        __syncthreads();
+        long before = base, round = 0;
+        for (int w = 0; w < C::kThreads / 32; ++w) {
+          if (w < warp) before += scan[w];
+          round += scan[w];
+        }
+        const long lo = before + inc - u;
+        if (u > 0 && u0 >= lo && u0 < lo + u) {
+          start->left = u1 - u0;
+          start->rem = u0 - lo;
+          start->n = n;
+        }
+        base += round;
+        __syncthreads();
+        if (u0 < base) break;
+      }
+      // the key head, then the tile: every thread looks at one stretch of tiles
+      const SeqInfo s = seq_info(p, start->n, false);
+      const Tiles t = {s.kv - s.len, s.len, step};
+      const int count = t.count(), stretch = (count + C::kThreads - 1) / C::kThreads;
+      const long per = t.before(count), rem = start->rem % per;
+      const int lo = min(tid * stretch, count), hi = min(lo + stretch, count);
+      if (lo < hi) {
+        long at = t.before(lo);
+        if (rem >= at) {
+          for (int i = lo; i < hi; ++i) {
+            const int nb = t.blocks(i);
+            if (rem < at + nb) {
+              start->hk = (int)(start->rem / per);
+              start->tile = i;
+              start->j = (int)(rem - at);
+              break;
+            }
+            at += nb;
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Walk walk;
+  walk.left = start->left;
+  if (walk.left > 0) {
+    walk.n = start->n;
+    walk.hk = start->hk;
+    walk.tile = start->tile;
+    walk.j = start->j;
+    walk.load(p, step);
+  }
+  Segment seg;
+  bool ok = true;
+  // A bounded wait of the whole warp, or (the products) of one thread.  After one that ran out the warp
+  // takes no more work; the others' waits run out in turn.
+  auto await_one = [&](uint32_t b, uint32_t parity) {
+    if (!mbar_wait(b, parity, kWaitLimit)) {
+      raise_error(p.err, kErrTimeout);
+      ok = false;
+    }
+    return ok;
+  };
+  auto await = [&](uint32_t b, uint32_t parity) {
+    await_one(b, parity);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    return ok;
+  };
+
+  if (warp < C::kSoftWarps) {
+    // ------------------------------------------------------------------ softmax: one thread for a row
+    const int sub = kTiles == 2 ? warp >> 2 : 0, w4 = warp & 3, row = w4 * 32 + lane;
+    const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
+    const uint32_t t_o = tmem + lanes + C::kColO + sub * D;
+    const int g = row % p.G, tok_in = row / p.G;
+    uint8_t* sq = sm + sub * 128 * D * 2;
+    uint32_t n_blk = 0, n_pv = 0;  // blocks this warp has met (slot and parity go by it), PV products issued
+    // The product of block b.  With one tile the next block's scores may be here before the product of
+    // the block before them has ended: one barrier for even and one for odd blocks, so that no wait is
+    // for a phase that could lie two behind.
+    auto await_pv = [&](uint32_t b) {
+      return kTiles == 2 ? await(bar.o_full + 8 * sub, b & 1u) : await(bar.o_full + 8 * (b & 1u), (b >> 1) & 1u);
+    };
+    while (ok && walk.next(p, step, seg)) {
+      const int hk = seg.hk, ntok = min(p.sub, seg.ntok - sub * p.sub);  // tokens of this tile
+      const int row0 = seg.row0 + sub * p.sub, rows = max(ntok, 0) * p.G;
+      const bool mine = tok_in < ntok;
+      uint16_t* out = p.out + ((long)(row0 + tok_in) * p.Hq + hk * p.G + g) * D;
+      if (seg.keys <= 0) {
+        if (mine)
+          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
+        continue;
+      }
+      // Q into shared memory; zeros in the other rows of a warp that has some (what the rest of the tile
+      // holds stays in rows that nobody reads)
+      {
+        const int filled = (rows + 31) & ~31;
+        constexpr int kPer = D / 8, kRowsAt = 32 / kPer;  // 16-byte pieces of a row, rows of a warp at a time
+        const int piece = lane % kPer;
+        const uint16_t* src = p.q + (long)hk * p.G * D + piece * 8;
+#pragma unroll 4
+        for (int r = w4 * kRowsAt + lane / kPer; r < filled; r += 4 * kRowsAt) {
+          const int t = r / p.G;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (r < rows)
+            x = __ldg(reinterpret_cast<const uint4*>(src + ((long)(row0 + t) * p.Hq + (r - t * p.G)) * D));
+          *reinterpret_cast<uint4*>(sq + sw128_offset(r, piece * 8, 16384)) = x;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && rows > 0) mbar_arrive(bar.q_full + 8 * sub);
+      float m = -INFINITY, l = 0.f;
+      const int last = seg.pos0 + sub * p.sub + tok_in;  // the row's position: its last visible key
+      const bool busy = w4 * 32 < rows;                   // this warp has rows at all
+      if (rows > 0) {
+        for (int j = seg.j0; j < seg.j1; ++j, ++n_blk) {
+          const uint32_t slot = kTiles == 2 ? sub : n_blk & 1u, par = kTiles == 2 ? n_blk & 1u : (n_blk >> 1) & 1u;
+          if (!await(bar.s_full + 8 * slot, par)) break;
+          tc_fence_after();
+          if (busy) {
+            const uint32_t t_s = tmem + lanes + slot * 128;
+            float s[128];
+            tmem_ld128(t_s, s);
+            const int lim = last + 1 - j * kBlock;  // columns from here on are not visible
+            if (__any_sync(0xFFFFFFFFu, lim < kBlock)) {
+#pragma unroll
+              for (int i = 0; i < 128; ++i)
+                if (i >= lim) s[i] = -INFINITY;
+            }
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+            const bool raise = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+            if (__any_sync(0xFFFFFFFFu, raise)) {
+              const float m2 = raise ? top : m;
+              const float a = raise ? ex2_approx(m - m2) : 1.f;
+              l *= a;
+              m = m2;
+              if (j > seg.j0) {  // O holds the blocks before this one: wait for their product, then scale
+                if (!await_pv(n_pv - 1)) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  float o[32];
+                  tmem_ld32(t_o + c, o);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) o[i] *= a;
+                  tmem_st32(t_o + c, o);
+                }
+              }
+            }
+            const float off = m == -INFINITY ? 0.f : -m;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float w[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float a = ex2_approx(fmaf(s[64 * h + 2 * i], p.scale_log2, off));
+                const float b = ex2_approx(fmaf(s[64 * h + 2 * i + 1], p.scale_log2, off));
+                sum[(2 * i) & 3] += a;
+                sum[(2 * i + 1) & 3] += b;
+                w[i] = __uint_as_float(pack_bf2(a, b));
+              }
+              tmem_st32(t_s + 32 * h, w);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.p_full + 8 * slot);
+          ++n_pv;
+        }
+        if (!ok) break;
+        if (!await_pv(n_pv - 1)) break;
+        tc_fence_after();
+        const bool whole = seg.j0 == 0 && seg.j1 == seg.nb;
+        if (whole && busy) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const uint16_t* z = p.z.p + (long)(row0 + tok_in) * p.z.token + (long)(hk * p.G + g) * p.z.head;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(t_o + c, o);
+            if (mine) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8) {
+                float y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0.f : o[i + k] * inv;  // no visible key: zero
+                if (p.z.p) {
+                  const uint4 zz = __ldg(reinterpret_cast<const uint4*>(z + c + i));
+                  const uint32_t zr[4] = {zz.x, zz.y, zz.z, zz.w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    y[2 * k] *= sigmoid_fast(__uint_as_float(zr[k] << 16));
+                    y[2 * k + 1] *= sigmoid_fast(__uint_as_float(zr[k] & 0xFFFF0000u));
+                  }
+                }
+                *reinterpret_cast<uint4*>(out + c + i) =
+                    make_uint4(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7]));
+              }
+            }
+          }
+        } else if (busy) {
+          const int slot = 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0);
+          p.ml[(long)slot * 128 * kTiles + sub * 128 + row] = make_float2(m, l);
+          float4* dst = p.part + ((long)slot * kTiles + sub) * (D / 4) * 128 + row;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(t_o + c, o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[(c / 4 + i) * 128] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        if (!whole && warp == 0 && lane == 0)
+          p.desc[2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0)] =
+              make_int4(seg.row0, seg.ntok, hk, 1 | (seg.j1 == seg.nb ? 2 : 0));
+        tc_fence_before();
+      }
+    }
+  } else if (warp == C::kSoftWarps) {
+    // ------------------------------------------------------------------ the products
+    if (lane == 0) {
+      constexpr uint32_t kIdQK = idesc_bf16_f32(128, 128), kIdPV = idesc_bf16_f32_bmn(128, D);
+      constexpr uint32_t kVBlock = D == 256 ? 8192 : 16384;  // bytes between 64-value blocks of a value stage
+      Ring<kStages> ring;
+      uint32_t q_par[2] = {0, 0}, n_blk[2] = {0, 0};
+      while (ok && walk.next(p, step, seg)) {
+        const int two = kTiles == 2 && seg.ntok > p.sub ? 2 : 1;
+        if (seg.keys > 0) {
+          for (int t = 0; t < two; ++t) {
+            await_one(bar.q_full + 8 * t, q_par[t]);
+            q_par[t] ^= 1u;
+          }
+          if (!ok) break;
+          tc_fence_after();
+          auto qk = [&](int sub, uint32_t slot, const Ring<kStages>& r, int part) {
+            const uint32_t q = sb + sub * 128 * D * 2, k = sb + C::kOffStage + r.i * kStage;
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+              mma_bf16_k4<2, 2>(tmem + slot * 128, sw128_desc(q + (2 * part + d) * 16384), sw128_desc(k + d * 16384),
+                                kIdQK, part + d > 0);
+          };
+          auto pv = [&](int sub, uint32_t slot, const Ring<kStages>& r, int part, bool acc) {
+            const uint32_t v = sb + C::kOffStage + r.i * kStage;
+            constexpr int kSteps = 2 / kParts;  // 64 keys each
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d)
+              mma_bf16_k4_ta<128>(tmem + C::kColO + sub * D, tmem + slot * 128 + (part * kSteps + d) * 32,
+                                  sw128_mn_desc(v + d * 8192, kVBlock), kIdPV, acc || d > 0);
+          };
+          if constexpr (kTiles == 2) {
+            Ring<kStages> r = ring;
+            if (!await_one(bar.full + 8 * r.i, r.pass)) break;
+            tc_fence_after();
+            for (int t = 0; t < two; ++t) {
+              qk(t, t, r, 0);
+              mma_commit(bar.s_full + 8 * t);
+            }
+            mma_commit(bar.empty + 8 * r.i);
+            ring.step();
+            for (int j = seg.j0; j < seg.j1 && ok; ++j) {
+              const Ring<kStages> rv = ring;
+              Ring<kStages> rk = ring;
+              rk.step();
+              const bool more = j + 1 < seg.j1;
+              if (!await_one(bar.full + 8 * rv.i, rv.pass)) break;
+              for (int t = 0; t < two; ++t) {
+                if (!await_one(bar.p_full + 8 * t, n_blk[t] & 1u)) break;
+                ++n_blk[t];
+                tc_fence_after();
+                pv(t, t, rv, 0, j > seg.j0);
+                mma_commit(bar.o_full + 8 * t);
+                if (t == two - 1) mma_commit(bar.empty + 8 * rv.i);
+                if (more) {
+                  if (t == 0) {
+                    if (!await_one(bar.full + 8 * rk.i, rk.pass)) break;
+                    tc_fence_after();
+                  }
+                  qk(t, t, rk, 0);
+                  mma_commit(bar.s_full + 8 * t);
+                  if (t == two - 1) mma_commit(bar.empty + 8 * rk.i);
+                }
+              }
+              ring.step();
+              if (more) ring.step();
+            }
+          } else {
+            uint32_t b_qk = n_blk[0];  // blocks whose scores have been issued: the slot goes by it
+            auto scores = [&]() {
+              for (int part = 0; part < kParts; ++part) {
+                if (!await_one(bar.full + 8 * ring.i, ring.pass)) return;
+                tc_fence_after();
+                qk(0, b_qk & 1u, ring, part);
+                mma_commit(bar.empty + 8 * ring.i);
+                ring.step();
+              }
+              mma_commit(bar.s_full + 8 * (b_qk & 1u));
+              ++b_qk;
+            };
+            scores();
+            if (ok && seg.j0 + 1 < seg.j1) scores();
+            for (int j = seg.j0; j < seg.j1 && ok; ++j) {
+              const uint32_t slot = n_blk[0] & 1u;
+              if (!await_one(bar.p_full + 8 * slot, (n_blk[0] >> 1) & 1u)) break;
+              ++n_blk[0];
+              tc_fence_after();
+              for (int part = 0; part < kParts; ++part) {
+                if (!await_one(bar.full + 8 * ring.i, ring.pass)) break;
+                tc_fence_after();
+                pv(0, slot, ring, part, j > seg.j0 || part > 0);
+                mma_commit(bar.empty + 8 * ring.i);
+                ring.step();
+              }
+              if (!ok) break;
+              mma_commit(bar.o_full + 8 * slot);
+              if (j + 2 < seg.j1) scores();
+            }
+          }
+        }
+      }
+      // every product has ended, and every arrival it owes, before the CTA does
+      mma_commit(bar.done);
+      mbar_wait(bar.done, 0, kWaitLimit);
+    }
+  } else if (warp == C::kSoftWarps + 1) {
+    // ------------------------------------------------------------------ K and V by TMA
+    const int page = 1 << p.cache.page_shift, box = min(page, 64), box_shift = min(p.cache.page_shift, 6);
+    Ring<kStages> ring;
+    uint32_t tails = 0, tail_par = 0, used = 0;  // stages whose last copy went to the tail barrier, its parity; stages in use
+    while (ok && walk.next(p, step, seg)) {
+      if (seg.keys > 0) {
+        const int hk = seg.hk, keys = seg.keys;
+        const int32_t* table = p.cache.table + (long)seg.n * p.cache.max_pages;
+        // One stage: `rows` keys from key0 on (those below `keys`, by whole boxes), kD 64-value blocks from
+        // d0 on, `pitch` bytes apart.
+        auto load = [&](const CUtensorMap* map, int key0, int rows, int d0, int nd, uint32_t pitch, bool value) {
+          if (!await(bar.empty + 8 * ring.i, ring.pass ^ 1u)) return;
+          const int boxes = rows >> box_shift, have = min(max((keys - key0 + box - 1) >> box_shift, 0), boxes);
+          const bool tail = value && key0 + rows > keys;  // the warp that zeroes the rest passes it on
+          const uint32_t to = (tail ? bar.tail : bar.full) + 8 * ring.i, bit = 1u << ring.i;
+          used |= bit;
+          tails = tail ? tails | bit : tails & ~bit;
+          if (tail) tail_par ^= bit;
+          int y = 0;
+          if (lane < have) {
+            const int key = key0 + (lane << box_shift);
+            int id = __ldg(table + (key >> p.cache.page_shift));
+            if ((unsigned)id >= (unsigned)p.cache.num_pages) {
+              raise_error(p.err, kErrDeviceArgument);
+              id = 0;
+            }
+            y = ((id * p.Hkv + hk) << p.cache.page_shift) + (key & (page - 1));
+          }
+          if (lane == 0) mbar_arrive_expect_tx(to, (uint32_t)(have * box * nd * 128));
+          __syncwarp();
+          if (lane < have) {
+            const uint32_t dst = sb + C::kOffStage + ring.i * kStage + (uint32_t)(lane << box_shift) * 128;
+            for (int d = 0; d < nd; ++d) tma_load_2d(dst + d * pitch, map, (d0 + d) * 64, y, to);
+          }
+          ring.step();
+        };
+        auto keys_of = [&](int j) {
+          for (int part = 0; part < kParts && ok; ++part)
+            load(&p.tmap_k, j * kBlock, 128, 2 * part, 2, 16384, false);
+        };
+        auto values_of = [&](int j) {
+          for (int part = 0; part < kParts && ok; ++part)
+            load(&p.tmap_v, j * kBlock + part * 64, 128 / kParts, 0, D / 64, D == 256 ? 8192 : 16384, true);
+        };
+        keys_of(seg.j0);
+        for (int j = seg.j0; j < seg.j1 && ok; ++j) {
+          if (kTiles == 1) {
+            if (j + 1 < seg.j1) keys_of(j + 1);
+            if (ok) values_of(j);
+          } else {
+            values_of(j);
+            if (ok && j + 1 < seg.j1) keys_of(j + 1);
+          }
+        }
+      }
+    }
+    // After a wait that ran out, the copies in flight land before the CTA ends: the last copy into stage
+    // i went out on this pass over the ring for the stages before ring.i, on the last one for the rest.
+    if (!ok) {
+      for (int i = 0; i < kStages; ++i) {
+        if (!(used >> i & 1u)) continue;
+        if (tails >> i & 1u) mbar_wait(bar.tail + 8 * i, (tail_par >> i & 1u) ^ 1u, kWaitLimit);
+        else mbar_wait(bar.full + 8 * i, i < ring.i ? ring.pass : ring.pass ^ 1u, kWaitLimit);
+      }
+    }
+  } else if (warp == C::kSoftWarps + 2) {
+    // ------------------------------------------------------------------ value rows behind the last key
+    Ring<kStages> ring;
+    uint32_t used[kStages] = {};  // parity of each stage's tail barrier
+    while (ok && walk.next(p, step, seg)) {
+      if (seg.keys > 0) {
+        const long stages = (long)(seg.j1 - seg.j0) * 2 * kParts;
+        ring.skip(stages - kParts);
+        for (int part = 0; part < kParts; ++part, ring.step()) {
+          constexpr int kRows = 128 / kParts;
+          const int key0 = (seg.j1 - 1) * kBlock + part * kRows;
+          const int have = max(seg.keys - key0, 0);
+          if (have >= kRows) continue;
+          uint32_t par = 0;
+#pragma unroll
+          for (int i = 0; i < kStages; ++i)
+            if (i == ring.i) {
+              par = used[i];
+              used[i] ^= 1u;
+            }
+          if (!await(bar.tail + 8 * ring.i, par)) break;
+          uint8_t* st = sm + C::kOffStage + ring.i * kStage;
+          for (int d = 0; d < D / 64; ++d)
+            for (int i = have * 8 + lane; i < kRows * 8; i += 32)
+              *reinterpret_cast<uint4*>(st + d * (D == 256 ? 8192 : 16384) + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.full + 8 * ring.i);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of cut tiles: out = sum_c O_c 2^(m_c - m) / sum_c l_c 2^(m_c - m), c over the tile's
+// parts in the order of the line.  The CTA of the tile's first part does it; blockIdx.y takes a share
+// of the columns.  A few rows (one token's heads) or 256: lanes are rows either way, as they were written.
+template <int D, int kTiles>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p, int ctas) {
+  const int4 d = p.desc[2 * blockIdx.x + 1];
+  if (!(d.w & 1)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int subs = d.y > p.sub ? 2 : 1;
+  for (int i = blockIdx.y * 8 + warp; i < subs * 4 * (D / 4); i += gridDim.y * 8) {
+    const int col = i % (D / 4), rw = i / (D / 4), sub = rw >> 2, row = (rw & 3) * 32 + lane;
+    const int rows = min(p.sub, d.y - sub * p.sub) * p.G;
+    if ((rw & 3) * 32 >= rows) continue;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    int flags = d.w;
+    for (int c = blockIdx.x, slot = 2 * c + 1;;) {
+      const float2 ml = p.ml[(long)slot * 128 * kTiles + sub * 128 + row];
+      const float4 x = p.part[(((long)slot * kTiles + sub) * (D / 4) + col) * 128 + row];
+      const float m2 = fmaxf(m, ml.x);
+      const float off = m2 == -INFINITY ? 0.f : m2;
+      const float a = ex2_approx(m - off), b = ex2_approx(ml.x - off);
+      l = l * a + ml.y * b;
+      o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
+      m = m2;
+      if (flags & 2) break;
+      do {  // the next CTA that has a piece
+        if (++c >= ctas) break;
+        slot = 2 * c;
+        flags = p.desc[slot].w;
+      } while (!(flags & 1));
+      if (c >= ctas) break;
+    }
+    if (row < rows) {
+      const int t = row / p.G, h = d.z * p.G + row - t * p.G;
+      const long r = d.x + sub * p.sub + t;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
+      if (l == 0.f) y[0] = y[1] = y[2] = y[3] = 0.f;
+      if (p.z.p) {
+        const uint2 zz = __ldg(reinterpret_cast<const uint2*>(p.z.p + r * p.z.token + h * p.z.head + col * 4));
+        y[0] *= sigmoid_fast(__uint_as_float(zz.x << 16));
+        y[1] *= sigmoid_fast(__uint_as_float(zz.x & 0xFFFF0000u));
+        y[2] *= sigmoid_fast(__uint_as_float(zz.y << 16));
+        y[3] *= sigmoid_fast(__uint_as_float(zz.y & 0xFFFF0000u));
+      }
+      *reinterpret_cast<uint2*>(p.out + (r * p.Hq + h) * D + col * 4) = make_uint2(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]));
+    }
+  }
+}
 
 // One warp for one query head of one token: D / 32 values a lane, the keys one after the other.
 template <int D, bool kE4M3>
@@ -75,23 +870,79 @@ __global__ void __launch_bounds__(256) attn_simple_kernel(const __grid_constant_
   }
 }
 
+
+// Rows of K or V as the TMA sees them.
+cudaError_t encode_pages(CUtensorMap* map, const void* base, const PagedCache& c, int Hkv, int D) {
+  return encode_bf16_2d_sw128(map, base, D, ((uint64_t)c.num_pages * Hkv) << c.page_shift, (uint64_t)D * 2, 64,
+                              c.page_shift > 6 ? 64 : 1u << c.page_shift);
+}
+
+template <int D, int kTiles>
+cudaError_t launch_tiles(const LaunchEnv& env, AttnParams& p, int ctas) {
+  using C = Cfg<D, kTiles>;
+  static int done[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(attn_kernel<D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = 1;
+  }
+  attn_kernel<D, kTiles><<<ctas, C::kThreads, C::kSmem, env.stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  attn_join_kernel<D, kTiles><<<dim3(ctas, 8), 256, 0, env.stream>>>(p, ctas);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
+// Descriptors, maxima and sums, and 128 KB of O for each of two parts a CTA.
 size_t attn_workspace_bytes(int D) {
   (void)D;
-  return 256;
+  return 2 * kMaxCtas * (sizeof(int4) + 256 * sizeof(float2) + 131072) ;
 }
 
 cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint16_t* q, const PagedCache& cache,
                         const int32_t* kv_lens, const int32_t* cu, int N, int T, float scale, const HeadRows& z,
                         uint16_t* out, void* workspace) {
-  (void)workspace;
-  const AttnParams p = {q, cache, kv_lens, cu, z, out, env.err, scale * kLog2e, Hq, Hkv, N, T};
-  const long grid = ((long)T * Hq + 7) / 8;
-  auto kern = D == 128 ? (cache.e4m3 ? attn_simple_kernel<128, true> : attn_simple_kernel<128, false>)
-                       : (cache.e4m3 ? attn_simple_kernel<256, true> : attn_simple_kernel<256, false>);
-  kern<<<(unsigned)grid, 256, 0, env.stream>>>(p);
-  return cudaGetLastError();
+  AttnParams p;
+  memset(&p, 0, sizeof p);
+  p.q = q;
+  p.cache = cache;
+  p.kv_lens = kv_lens;
+  p.cu = cu;
+  p.z = z;
+  p.out = out;
+  p.err = env.err;
+  p.scale_log2 = scale * kLog2e;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.N = N;
+  p.T = T;
+  p.sub = 128 / p.G;
+  if (cache.e4m3) {
+    const long grid = ((long)T * Hq + 7) / 8;
+    auto kern = D == 128 ? attn_simple_kernel<128, true> : attn_simple_kernel<256, true>;
+    kern<<<(unsigned)grid, 256, 0, env.stream>>>(p);
+    return cudaGetLastError();
+  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.desc = reinterpret_cast<int4*>(ws);
+  p.ml = reinterpret_cast<float2*>(ws + 2 * kMaxCtas * sizeof(int4));
+  p.part = reinterpret_cast<float4*>(ws + 2 * kMaxCtas * (sizeof(int4) + 256 * sizeof(float2)));
+  cudaError_t e = encode_pages(&p.tmap_k, cache.k, cache, Hkv, D);
+  if (e == cudaSuccess) e = encode_pages(&p.tmap_v, cache.v, cache, Hkv, D);
+  int sms = 0;
+  if (e == cudaSuccess) e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  if (D == 256) return launch_tiles<256, 1>(env, p, ctas);
+  // two tiles a CTA where a sequence has more rows than one holds, on average
+  if ((long)T * p.G > 128L * N) return launch_tiles<128, 2>(env, p, ctas);
+  return launch_tiles<128, 1>(env, p, ctas);
 }
 
 }  // namespace gdn

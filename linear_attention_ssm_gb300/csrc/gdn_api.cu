@@ -801,6 +801,8 @@ gdn_status attention(const gdn_attn_geometry* geo, const gdn_bf16* q, const gdn_
     return fail(GDN_ERR_INVALID_ARGUMENT, "softmax_scale must be positive and finite");
   const size_t bytes = (size_t)total_tokens * geo->num_q_heads * geo->head_dim * 2;
   if (overlaps(q, bytes, out, bytes)) return fail(GDN_ERR_INVALID_ARGUMENT, "out overlaps q");
+  if ((int64_t)c.num_pages * geo->num_kv_heads * cache->page_size > 0x7FFFFFFFL)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "the pool has more than 2^31 rows");
   const size_t need = gdn::attn_workspace_bytes(geo->head_dim);
   if (!workspace || workspace_bytes < need)
     return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, workspace ? workspace_bytes : 0);
