@@ -177,55 +177,67 @@ struct WalkStart {
 
 // ---------------------------------------------------------------- layout of a CTA
 
-template <int D, int kTiles>
+template <int D, int kTiles, bool kE4M3>
 struct Cfg {
   static constexpr int kSoftWarps = 4 * kTiles;
-  static constexpr int kThreads = 32 * (kSoftWarps + 4);
+  static constexpr int kConvWarps = kE4M3 ? (kTiles == 2 ? 4 : 8) : 0;
+  static constexpr int kThreads = 32 * (kSoftWarps + 4 + kConvWarps);
   static constexpr uint32_t kQ = kTiles * 128 * D * 2;
-  static constexpr int kStages = (int)((224 * 1024 - kQ) / kStage);
+  // An e4m3 cache's loads wait in registers, so one stage less will do, and its place holds the scales.
+  static constexpr int kStages = (int)((224 * 1024 - kQ) / kStage) - (kE4M3 ? 1 : 0);
   static constexpr int kParts = D / 128;  // stages of a block's keys, and of its values
   static constexpr uint32_t kOffStage = kQ;
-  static constexpr uint32_t kOffBar = kQ + kStages * kStage;
+  static constexpr uint32_t kOffScale = kOffStage + kStages * kStage;  // 4 blocks' scales
+  static constexpr uint32_t kOffBar = kOffScale + (kE4M3 ? 4 * 1024 : 0);
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;  // barriers; alignment of the base
   static constexpr uint32_t kColO = 256;                    // tensor memory: two S slots of 128 columns, then O
+  // Registers: the softmax warps hold a row of 128 scores each, the others need few.  The shares of the
+  // warpgroups come to no more than the launch's: 512 threads of 128, 384 of 168; 256 threads have
+  // enough as they are.
+  static constexpr int kRegLaunch = 65536 / kThreads / 8 * 8;
+  static constexpr bool kSplit = kThreads > 256;
+  static constexpr int kRegSoft = kTiles == 2 ? (kE4M3 ? 184 : 208) : 216;
+  static constexpr int kRegAux = kE4M3 ? 40 : 80;
+  static constexpr int kRegConv = kTiles == 2 ? 96 : 120;
+  static_assert(!kSplit || kSoftWarps * kRegSoft + 4 * kRegAux + kConvWarps * kRegConv <= kThreads / 32 * kRegLaunch,
+                "the shares exceed the launch's registers");
 };
 
 struct Bars {
-  uint32_t full, empty, tail, s_full, p_full, o_full, q_full, done;  // shared addresses of the first of each kind
+  uint32_t full, empty, tail, s_full, p_full, o_full, q_full, done, sc_full;  // shared addresses of the first of each kind
 };
 
-// 128 columns of this warp's 32 lanes, behind one wait.
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
-  uint32_t r[128];
+// 64 columns of this warp's 32 lanes.  The wait for the load is a statement of its own (two loads, one
+// wait): tmem_ld64_wait hands the values on, so that no use of them is moved ahead of it.
+__device__ __forceinline__ void tmem_ld64_begin(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
-      "%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,"
-      "%58,%59,%60,%61,%62,%63,%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,"
-      "%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,"
-      "%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n"
-      "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]),
-        "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]),
-        "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
-        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
-        "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63]), "=r"(r[64]),
-        "=r"(r[65]), "=r"(r[66]), "=r"(r[67]), "=r"(r[68]), "=r"(r[69]), "=r"(r[70]), "=r"(r[71]), "=r"(r[72]),
-        "=r"(r[73]), "=r"(r[74]), "=r"(r[75]), "=r"(r[76]), "=r"(r[77]), "=r"(r[78]), "=r"(r[79]), "=r"(r[80]),
-        "=r"(r[81]), "=r"(r[82]), "=r"(r[83]), "=r"(r[84]), "=r"(r[85]), "=r"(r[86]), "=r"(r[87]), "=r"(r[88]),
-        "=r"(r[89]), "=r"(r[90]), "=r"(r[91]), "=r"(r[92]), "=r"(r[93]), "=r"(r[94]), "=r"(r[95]), "=r"(r[96]),
-        "=r"(r[97]), "=r"(r[98]), "=r"(r[99]), "=r"(r[100]), "=r"(r[101]), "=r"(r[102]), "=r"(r[103]), "=r"(r[104]),
-        "=r"(r[105]), "=r"(r[106]), "=r"(r[107]), "=r"(r[108]), "=r"(r[109]), "=r"(r[110]), "=r"(r[111]),
-        "=r"(r[112]), "=r"(r[113]), "=r"(r[114]), "=r"(r[115]), "=r"(r[116]), "=r"(r[117]), "=r"(r[118]),
-        "=r"(r[119]), "=r"(r[120]), "=r"(r[121]), "=r"(r[122]), "=r"(r[123]), "=r"(r[124]), "=r"(r[125]),
-        "=r"(r[126]), "=r"(r[127])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
+      "%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,"
+      "%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
-#pragma unroll
-  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_ld64_wait(uint32_t (&r)[64]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+        "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+        "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+        "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+        "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+               :
+               : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t addr) {
@@ -254,9 +266,18 @@ struct Ring {
   }
 };
 
-template <int D, int kTiles>
-__global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
-  using C = Cfg<D, kTiles>;
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <int D, int kTiles, bool kE4M3>
+__global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
+  using C = Cfg<D, kTiles, kE4M3>;
   constexpr int kStages = C::kStages, kParts = C::kParts;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
@@ -269,10 +290,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
   WalkStart* start = reinterpret_cast<WalkStart*>(bars + 34);
   long* scan = reinterpret_cast<long*>(bars + 40);
   const uint32_t b0 = smem_u32(bars);
-  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26};
+  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26, b0 + 8 * 27};
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar.full + 8 * i, 1);
+      mbar_init(bar.full + 8 * i, kE4M3 ? C::kConvWarps : 1);
       mbar_init(bar.empty + 8 * i, 1);
       mbar_init(bar.tail + 8 * i, 1);
     }
@@ -283,9 +304,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
       mbar_init(bar.q_full + 8 * i, 4);
     }
     mbar_init(bar.done, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bar.sc_full + 8 * i, 1);
     fence_mbar_init();
-    prefetch_tensormap(&p.tmap_k);
-    prefetch_tensormap(&p.tmap_v);
+    if constexpr (!kE4M3) {
+      prefetch_tensormap(&p.tmap_k);
+      prefetch_tensormap(&p.tmap_v);
+    }
     start->left = 0;
     p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     p.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
@@ -395,14 +419,23 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
     return ok;
   };
 
+  auto finish = [&]() {
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+  };
+
   if (warp < C::kSoftWarps) {
+    if constexpr (C::kSplit) regs_inc<C::kRegSoft>();
     // ------------------------------------------------------------------ softmax: one thread for a row
     const int sub = kTiles == 2 ? warp >> 2 : 0, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t t_o = tmem + lanes + C::kColO + sub * D;
     const int g = row % p.G, tok_in = row / p.G;
     uint8_t* sq = sm + sub * 128 * D * 2;
-    uint32_t n_blk = 0, n_pv = 0;  // blocks this warp has met (slot and parity go by it), PV products issued
+    // blocks of this tile so far (slot and parity go by it), its products with V, blocks of the CTA
+    uint32_t n_blk = 0, n_pv = 0, all_blk = 0;
     // The product of block b.  With one tile the next block's scores may be here before the product of
     // the block before them has ended: one barrier for even and one for odd blocks, so that no wait is
     // for a phase that could lie two behind.
@@ -438,19 +471,48 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && rows > 0) mbar_arrive(bar.q_full + 8 * sub);
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, r = -INFINITY;
       const int last = seg.pos0 + sub * p.sub + tok_in;  // the row's position: its last visible key
       const bool busy = w4 * 32 < rows;                   // this warp has rows at all
+      const uint32_t seg_blk = all_blk;
+      all_blk += seg.j1 - seg.j0;
       if (rows > 0) {
-        for (int j = seg.j0; j < seg.j1; ++j, ++n_blk) {
+        uint32_t blk = seg_blk;
+        for (int j = seg.j0; j < seg.j1; ++j, ++n_blk, ++blk) {
           const uint32_t slot = kTiles == 2 ? sub : n_blk & 1u, par = kTiles == 2 ? n_blk & 1u : (n_blk >> 1) & 1u;
           if (!await(bar.s_full + 8 * slot, par)) break;
           tc_fence_after();
           if (busy) {
             const uint32_t t_s = tmem + lanes + slot * 128;
             float s[128];
-            tmem_ld128(t_s, s);
+            {
+              uint32_t lo[64], hi[64];
+              tmem_ld64_begin(t_s, lo);
+              tmem_ld64_begin(t_s + 64, hi);
+              tmem_ld64_wait(lo);
+              tmem_ld64_wait(hi);
+#pragma unroll
+              for (int i = 0; i < 64; ++i) {
+                s[i] = __uint_as_float(lo[i]);
+                s[64 + i] = __uint_as_float(hi[i]);
+              }
+            }
             const int lim = last + 1 - j * kBlock;  // columns from here on are not visible
+            // e4m3: the codes' products become scores by the keys' powers of two
+            float ev = 0.f;
+            const uint8_t* sc = sm + C::kOffScale + (blk & 3u) * 1024;
+            if constexpr (kE4M3) {
+              if (!await(bar.sc_full + 8 * (blk & 3u), (blk >> 2) & 1u)) break;
+              ev = *reinterpret_cast<const float*>(bars + 56 + (blk & 3u));
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float4 k = *reinterpret_cast<const float4*>(sc + 16 * i);
+                s[4 * i] *= k.x;
+                s[4 * i + 1] *= k.y;
+                s[4 * i + 2] *= k.z;
+                s[4 * i + 3] *= k.w;
+              }
+            }
             if (__any_sync(0xFFFFFFFFu, lim < kBlock)) {
 #pragma unroll
               for (int i = 0; i < 128; ++i)
@@ -459,42 +521,71 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
             for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-            const bool raise = top > m + kLazy || (m == -INFINITY && top > -INFINITY);
+            const float unit = kE4M3 ? 1.f : p.scale_log2;  // of s in log2 units (e4m3: already in the scales)
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * unit;
+            if (top > m + kLazy) {
+              l *= ex2_approx(m - top);
+              m = top;
+            }
+            // O is held in units of 2^r: the row's maximum times the block's largest value scale
+            const float e = m + ev;
+            const bool raise = e > r + kLazy;
             if (__any_sync(0xFFFFFFFFu, raise)) {
-              const float m2 = raise ? top : m;
-              const float a = raise ? ex2_approx(m - m2) : 1.f;
-              l *= a;
-              m = m2;
+              const float a = raise ? ex2_approx(r - e) : 1.f;
+              if (raise) r = e;
               if (j > seg.j0) {  // O holds the blocks before this one: wait for their product, then scale
                 if (!await_pv(n_pv - 1)) break;
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                  float o[32];
-                  tmem_ld32(t_o + c, o);
+                for (int c = 0; c < D; c += 16) {
+                  float o[16];
+                  tmem_ld16(t_o + c, o);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] *= a;
-                  tmem_st32(t_o + c, o);
+                  for (int i = 0; i < 16; ++i) o[i] *= a;
+                  tmem_st16(t_o + c, o);
                 }
               }
             }
-            const float off = m == -INFINITY ? 0.f : -m;
+            // weights 2^(s - m + d), d = e - r the distance of this block's unit from O's; d is cut off at
+            // -40 for them, lest a block of tiny values vanish from l, and the rest goes to P alone
+            float d = 0.f, rest = 1.f;
+            if constexpr (kE4M3) {
+              d = m == -INFINITY ? 0.f : fmaxf(e - r, -40.f);
+              rest = m == -INFINITY ? 1.f : ex2_approx(e - r - d);
+            }
+            const bool cut = kE4M3 && __any_sync(0xFFFFFFFFu, rest != 1.f);
+            const float off = m == -INFINITY ? 0.f : d - m;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float w[32];
+            for (int h = 0; h < 4; ++h) {
+              float w[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float a = ex2_approx(fmaf(s[64 * h + 2 * i], p.scale_log2, off));
-                const float b = ex2_approx(fmaf(s[64 * h + 2 * i + 1], p.scale_log2, off));
-                sum[(2 * i) & 3] += a;
-                sum[(2 * i + 1) & 3] += b;
-                w[i] = __uint_as_float(pack_bf2(a, b));
+              for (int i = 0; i < 16; i += 2) {
+                float x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float y = s[32 * h + 2 * i + k];
+                  x[k] = ex2_approx(kE4M3 ? y + off : fmaf(y, unit, off));
+                  sum[k] += x[k];
+                }
+                if constexpr (kE4M3) {  // the values' powers of two, relative to the block's largest
+                  const float4 v = *reinterpret_cast<const float4*>(sc + 512 + 128 * h + 8 * i);
+                  x[0] *= v.x;
+                  x[1] *= v.y;
+                  x[2] *= v.z;
+                  x[3] *= v.w;
+                  if (cut) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] *= rest;
+                  }
+                }
+                w[i] = __uint_as_float(pack_bf2(x[0], x[1]));
+                w[i + 1] = __uint_as_float(pack_bf2(x[2], x[3]));
               }
-              tmem_st32(t_s + 32 * h, w);
+              tmem_st16(t_s + 16 * h, w);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            l += kE4M3 ? all * ex2_approx(-d) : all;
           }
           tc_fence_before();
           __syncwarp();
@@ -505,6 +596,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
         if (!await_pv(n_pv - 1)) break;
         tc_fence_after();
         const bool whole = seg.j0 == 0 && seg.j1 == seg.nb;
+        // O in units of 2^m (half the exponent at a time where both ends of the range meet)
+        const float unit_o = kE4M3 && m > -INFINITY ? ex2_approx(0.5f * (r - m)) : 1.f;
         if (whole && busy) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const uint16_t* z = p.z.p + (long)(row0 + tok_in) * p.z.token + (long)(hk * p.G + g) * p.z.head;
@@ -517,7 +610,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
               for (int i = 0; i < 32; i += 8) {
                 float y[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0.f : o[i + k] * inv;  // no visible key: zero
+                for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0.f : kE4M3 ? o[i + k] * unit_o * inv * unit_o : o[i + k] * inv;  // no visible key: zero
                 if (p.z.p) {
                   const uint4 zz = __ldg(reinterpret_cast<const uint4*>(z + c + i));
                   const uint32_t zr[4] = {zz.x, zz.y, zz.z, zz.w};
@@ -540,6 +633,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
           for (int c = 0; c < D; c += 32) {
             float o[32];
             tmem_ld32(t_o + c, o);
+            if constexpr (kE4M3) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = o[i] * unit_o * unit_o;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               dst[(c / 4 + i) * 128] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -551,7 +648,159 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
         tc_fence_before();
       }
     }
-  } else if (warp == C::kSoftWarps) {
+    finish();
+    return;
+  }
+  if (kE4M3 && warp >= C::kSoftWarps + 4) {
+    if constexpr (C::kSplit) regs_dec<C::kRegConv>();
+    // ------------------------------------------------------------------ e4m3: codes -> bf16 stages
+    // 16 codes a load; the loads of the next kAhead stages wait in registers while this one's codes are
+    // widened (exactly) and written in the layout that the TMA gives a bf16 cache.
+    constexpr int kConv = C::kConvWarps > 0 ? C::kConvWarps : 4, kUnits = 1024 / (32 * kConv), kAhead = kConv == 8 ? 3 : 2;
+    const int ct = tid - 32 * (C::kSoftWarps + 4), cw = ct >> 5;
+    const int shift = p.cache.page_shift;
+    Ring<kStages> ring;
+    int op = 0, ops = 0, part = 0;           // of the segment: each op is a block's keys or values, in kParts stages
+    int id_k = 0, id_v = 0, id_next = 0;     // lane i: page of the i-th stretch of the block being fetched
+    uint32_t blk = 0;
+    uint4 raw[kAhead][kUnits];
+    int meta[kAhead];                        // -1: no more; bit 0: values, bits 1..: part
+    uint32_t kb[kAhead], vb[kAhead];         // warp 0, first stage of a block's keys: scale bytes of four keys a lane
+    int have[kAhead];                        // ... and the block's visible keys
+    auto page_of = [&](int j) {
+      const int key = j * kBlock + (lane << shift);
+      int id = 0;
+      if ((lane << shift) < kBlock && key < seg.keys) {
+        id = __ldg(p.cache.table + (long)seg.n * p.cache.max_pages + (key >> shift));
+        if ((unsigned)id >= (unsigned)p.cache.num_pages) {
+          raise_error(p.err, kErrDeviceArgument);
+          id = 0;
+        }
+      }
+      return id;
+    };
+    auto fetch = [&](uint4 (&x)[kUnits], int& mt, uint32_t& k4, uint32_t& v4, int& hv) {
+      while (op == ops) {
+        if (!walk.next(p, step, seg)) {
+          mt = -1;
+          return;
+        }
+        op = 0;
+        ops = seg.keys > 0 ? 2 * (seg.j1 - seg.j0) : 0;
+        if (ops) id_next = page_of(seg.j0);
+      }
+      // the order of the stages: K0 V0 K1 V1 .. with two tiles, K0 K1 V0 K2 V1 .. with one
+      const bool value = kTiles == 2 ? op & 1 : op == ops - 1 || (op > 0 && !(op & 1));
+      const int j = seg.j0 + (kTiles == 2 ? op >> 1 : op == ops - 1 ? (ops >> 1) - 1 : value ? (op >> 1) - 1 : (op + 1) >> 1);
+      if (!value && part == 0) {
+        id_v = id_k;
+        id_k = id_next;
+        if (j + 1 < seg.j1) id_next = page_of(j + 1);
+      }
+      // with one tile the values fetched are those of the block before the latest keys, but for the last
+      const int ids = value && kTiles == 1 && op != ops - 1 ? id_v : id_k;
+      const bool wide = value && D == 256;  // 64 rows of 256 codes, else 128 rows of 128
+      const uint8_t* src = static_cast<const uint8_t*>(value ? p.cache.v : p.cache.k);
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int unit = u * 32 * kConv + ct;
+        const int row = wide ? (unit >> 4) + part * 64 : unit >> 3;  // key of the block
+        const int d = wide ? (unit & 15) * 16 : (unit & 7) * 16 + (value ? 0 : part * 128);
+        const int page = __shfl_sync(0xFFFFFFFFu, ids, row >> shift);
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (j * kBlock + row < seg.keys) {
+          const long at = (((long)page * p.Hkv + seg.hk) << shift) + (row & ((1 << shift) - 1));
+          x[u] = __ldg(reinterpret_cast<const uint4*>(src + at * D + d));
+        }
+      }
+      mt = (value ? 1 : 0) | part << 1;
+      if (cw == 0 && !value && part == 0) {
+        const int page = __shfl_sync(0xFFFFFFFFu, ids, (lane * 4) >> shift);
+        hv = seg.keys - j * kBlock;
+        k4 = v4 = 0;
+        if (lane * 4 < hv) {
+          const long at = (((long)page * p.Hkv + seg.hk) << shift) + ((lane * 4) & ((1 << shift) - 1));
+          k4 = __ldg(reinterpret_cast<const uint32_t*>(p.cache.k_scale + at));
+          v4 = __ldg(reinterpret_cast<const uint32_t*>(p.cache.v_scale + at));
+        }
+      }
+      if (++part == kParts) {
+        part = 0;
+        ++op;
+      }
+    };
+    auto process = [&](const uint4 (&x)[kUnits], int mt, uint32_t k4, uint32_t v4, int hv) {
+      if (!await(bar.empty + 8 * ring.i, ring.pass ^ 1u)) return false;
+      const bool value = mt & 1;
+      if (mt == 0) {  // a block's first stage: its scales
+        if (cw == 0) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = max(top, lane * 4 + i < hv ? (v4 >> (8 * i)) & 255u : 0u);
+          top = __reduce_max_sync(0xFFFFFFFFu, top);
+          float kf[4], vf[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool in = lane * 4 + i < hv;
+            const int diff = (int)((v4 >> (8 * i)) & 255u) - (int)top;
+            kf[i] = in ? e8m0_value((k4 >> (8 * i)) & 255u) * p.scale_log2 : 0.f;
+            vf[i] = in && diff >= -126 ? __uint_as_float((uint32_t)(127 + diff) << 23) : 0.f;
+          }
+          uint8_t* sc = sm + C::kOffScale + (blk & 3u) * 1024;
+          reinterpret_cast<float4*>(sc)[lane] = make_float4(kf[0], kf[1], kf[2], kf[3]);
+          reinterpret_cast<float4*>(sc + 512)[lane] = make_float4(vf[0], vf[1], vf[2], vf[3]);
+          if (lane == 0) *reinterpret_cast<float*>(bars + 56 + (blk & 3u)) = (float)((int)top - 127);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar.sc_full + 8 * (blk & 3u));
+        }
+        ++blk;
+      }
+      const bool wide = value && D == 256;
+      uint8_t* st = sm + C::kOffStage + ring.i * kStage;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        const int unit = u * 32 * kConv + ct;
+        const int row = wide ? unit >> 4 : unit >> 3, d = wide ? (unit & 15) * 16 : (unit & 7) * 16;
+        const uint32_t c[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 a = e4m3x2_to_float2((uint16_t)(c[i] & 0xFFFFu)), b = e4m3x2_to_float2((uint16_t)(c[i] >> 16));
+          o[2 * i] = pack_bf2(a.x, a.y);
+          o[2 * i + 1] = pack_bf2(b.x, b.y);
+        }
+        uint8_t* to = st + (d >> 6) * (wide ? 8192 : 16384) + row * 128;
+        const int c0 = ((d & 63) >> 3) ^ (row & 7);
+        const uint4 first = make_uint4(o[0], o[1], o[2], o[3]), second = make_uint4(o[4], o[5], o[6], o[7]);
+        // lanes of neighbouring 64-value blocks share banks: they write their halves in opposite order
+        const bool odd = (d >> 6) & 1;
+        *reinterpret_cast<uint4*>(to + ((odd ? c0 ^ 1 : c0) << 4)) = odd ? second : first;
+        *reinterpret_cast<uint4*>(to + ((odd ? c0 : c0 ^ 1) << 4)) = odd ? first : second;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.full + 8 * ring.i);
+      ring.step();
+      return true;
+    };
+    if (walk.left > 0) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch(raw[i], meta[i], kb[i], vb[i], have[i]);
+      for (bool on = true; on;) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (on) {
+            on = meta[i] >= 0 && process(raw[i], meta[i], kb[i], vb[i], have[i]);
+            if (on) fetch(raw[i], meta[i], kb[i], vb[i], have[i]);
+          }
+        }
+      }
+    }
+    finish();
+    return;
+  }
+  if constexpr (C::kSplit) regs_dec<C::kRegAux>();
+  if (warp == C::kSoftWarps) {
     // ------------------------------------------------------------------ the products
     if (lane == 0) {
       constexpr uint32_t kIdQK = idesc_bf16_f32(128, 128), kIdPV = idesc_bf16_f32_bmn(128, D);
@@ -656,7 +905,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
       mma_commit(bar.done);
       mbar_wait(bar.done, 0, kWaitLimit);
     }
-  } else if (warp == C::kSoftWarps + 1) {
+  } else if (!kE4M3 && warp == C::kSoftWarps + 1) {
     // ------------------------------------------------------------------ K and V by TMA
     const int page = 1 << p.cache.page_shift, box = min(page, 64), box_shift = min(p.cache.page_shift, 6);
     Ring<kStages> ring;
@@ -722,7 +971,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
         else mbar_wait(bar.full + 8 * i, i < ring.i ? ring.pass : ring.pass ^ 1u, kWaitLimit);
       }
     }
-  } else if (warp == C::kSoftWarps + 2) {
+  } else if (!kE4M3 && warp == C::kSoftWarps + 2) {
     // ------------------------------------------------------------------ value rows behind the last key
     Ring<kStages> ring;
     uint32_t used[kStages] = {};  // parity of each stage's tail barrier
@@ -754,10 +1003,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles>::kThreads, 1) attn_kernel(const
       }
     }
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  finish();
 }
 
 // Joins the parts of cut tiles: out = sum_c O_c 2^(m_c - m) / sum_c l_c 2^(m_c - m), c over the tile's
@@ -811,85 +1057,30 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
 }
 
-// One warp for one query head of one token: D / 32 values a lane, the keys one after the other.
-template <int D, bool kE4M3>
-__global__ void __launch_bounds__(256) attn_simple_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int kV = D / 32;
-  const long w = (long)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (w >= (long)p.T * p.Hq) return;
-  const int t = (int)(w / p.Hq), h = (int)(w % p.Hq), hk = h / (p.Hq / p.Hkv);
-  int first, len;
-  const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
-  if (seq < 0) {
-    if (seq == -2) raise_error(p.err, kErrDeviceArgument);
-    return;
-  }
-  int kv = __ldg(p.kv_lens + seq);
-  if (kv < 0 || kv > (long)p.cache.max_pages << p.cache.page_shift) {
-    raise_error(p.err, kErrDeviceArgument);
-    kv = 0;
-  }
-  const int pos = kv - len + (t - first), mask = (1 << p.cache.page_shift) - 1;
-  float q[kV], o[kV] = {}, m = -INFINITY, l = 0.f;
-  for (int i = 0; i < kV; ++i) q[i] = bf2f(p.q[((long)t * p.Hq + h) * D + lane * kV + i]) * p.scale_log2;
-  for (int j = 0; j <= pos; ++j) {
-    const int page = __ldg(p.cache.table + (long)seq * p.cache.max_pages + (j >> p.cache.page_shift));
-    if ((unsigned)page >= (unsigned)p.cache.num_pages) {
-      raise_error(p.err, kErrDeviceArgument);
-      continue;
-    }
-    const long row = (((long)page * p.Hkv + hk) << p.cache.page_shift) + (j & mask);
-    float k[kV], v[kV];
-    for (int i = 0; i < kV; ++i) {
-      const long at = row * D + lane * kV + i;
-      if (kE4M3) {
-        __nv_fp8_e4m3 a, b;
-        a.__x = static_cast<const uint8_t*>(p.cache.k)[at];
-        b.__x = static_cast<const uint8_t*>(p.cache.v)[at];
-        k[i] = (float)a * e8m0_value(p.cache.k_scale[row]);
-        v[i] = (float)b * e8m0_value(p.cache.v_scale[row]);
-      } else {
-        k[i] = bf2f(static_cast<const uint16_t*>(p.cache.k)[at]);
-        v[i] = bf2f(static_cast<const uint16_t*>(p.cache.v)[at]);
-      }
-    }
-    float s = 0.f;
-    for (int i = 0; i < kV; ++i) s = fmaf(q[i], k[i], s);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-    const float m2 = fmaxf(m, s), a = exp2f(m - m2), e = exp2f(s - m2);
-    l = l * a + e;
-    for (int i = 0; i < kV; ++i) o[i] = fmaf(e, v[i], o[i] * a);
-    m = m2;
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  for (int i = 0; i < kV; ++i) {
-    float y = o[i] * inv;
-    if (p.z.p) y *= sigmoidf_(bf2f(p.z.p[t * p.z.token + h * p.z.head + lane * kV + i]));
-    p.out[((long)t * p.Hq + h) * D + lane * kV + i] = f2bf(y);
-  }
-}
-
-
 // Rows of K or V as the TMA sees them.
 cudaError_t encode_pages(CUtensorMap* map, const void* base, const PagedCache& c, int Hkv, int D) {
   return encode_bf16_2d_sw128(map, base, D, ((uint64_t)c.num_pages * Hkv) << c.page_shift, (uint64_t)D * 2, 64,
                               c.page_shift > 6 ? 64 : 1u << c.page_shift);
 }
 
-template <int D, int kTiles>
-cudaError_t launch_tiles(const LaunchEnv& env, AttnParams& p, int ctas) {
-  using C = Cfg<D, kTiles>;
+template <int D, int kTiles, bool kE4M3>
+cudaError_t launch_tiles(const LaunchEnv& env, const AttnParams& p, int ctas) {
+  using C = Cfg<D, kTiles, kE4M3>;
   static int done[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !done[dev]) {
-    e = cudaFuncSetAttribute(attn_kernel<D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    e = cudaFuncSetAttribute(attn_kernel<D, kTiles, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
+    // the warpgroups redistribute the registers of the launch: with fewer they would wait for ever
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, attn_kernel<D, kTiles, kE4M3>);
+    if (e != cudaSuccess) return e;
+    if (C::kSplit && a.numRegs != C::kRegLaunch) return cudaErrorInvalidKernelImage;
     if (dev < 64) done[dev] = 1;
   }
-  attn_kernel<D, kTiles><<<ctas, C::kThreads, C::kSmem, env.stream>>>(p);
+  attn_kernel<D, kTiles, kE4M3><<<ctas, C::kThreads, C::kSmem, env.stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   attn_join_kernel<D, kTiles><<<dim3(ctas, 8), 256, 0, env.stream>>>(p, ctas);
@@ -923,26 +1114,27 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   p.N = N;
   p.T = T;
   p.sub = 128 / p.G;
-  if (cache.e4m3) {
-    const long grid = ((long)T * Hq + 7) / 8;
-    auto kern = D == 128 ? attn_simple_kernel<128, true> : attn_simple_kernel<256, true>;
-    kern<<<(unsigned)grid, 256, 0, env.stream>>>(p);
-    return cudaGetLastError();
-  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.desc = reinterpret_cast<int4*>(ws);
   p.ml = reinterpret_cast<float2*>(ws + 2 * kMaxCtas * sizeof(int4));
   p.part = reinterpret_cast<float4*>(ws + 2 * kMaxCtas * (sizeof(int4) + 256 * sizeof(float2)));
-  cudaError_t e = encode_pages(&p.tmap_k, cache.k, cache, Hkv, D);
-  if (e == cudaSuccess) e = encode_pages(&p.tmap_v, cache.v, cache, Hkv, D);
+  cudaError_t e = cudaSuccess;
+  if (!cache.e4m3) {
+    e = encode_pages(&p.tmap_k, cache.k, cache, Hkv, D);
+    if (e == cudaSuccess) e = encode_pages(&p.tmap_v, cache.v, cache, Hkv, D);
+  }
   int sms = 0;
   if (e == cudaSuccess) e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  if (D == 256) return launch_tiles<256, 1>(env, p, ctas);
   // two tiles a CTA where a sequence has more rows than one holds, on average
-  if ((long)T * p.G > 128L * N) return launch_tiles<128, 2>(env, p, ctas);
-  return launch_tiles<128, 1>(env, p, ctas);
+  const bool two = (long)T * p.G > 128L * N;
+  if (cache.e4m3) {
+    if (D == 256) return launch_tiles<256, 1, true>(env, p, ctas);
+    return two ? launch_tiles<128, 2, true>(env, p, ctas) : launch_tiles<128, 1, true>(env, p, ctas);
+  }
+  if (D == 256) return launch_tiles<256, 1, false>(env, p, ctas);
+  return two ? launch_tiles<128, 2, false>(env, p, ctas) : launch_tiles<128, 1, false>(env, p, ctas);
 }
 
 }  // namespace gdn
