@@ -552,7 +552,7 @@ typedef struct {
   int32_t num_pages;
   void* k;           /* [num_pages, Hkv, page_size, D] bf16 or e4m3 (16-byte aligned) */
   void* v;           /* the same */
-  uint8_t* k_scale;  /* [num_pages, Hkv, page_size] exponent bytes (E4M3; NULL for BF16) */
+  uint8_t* k_scale;  /* [num_pages, Hkv, page_size] exponent bytes (E4M3, 16-byte aligned; NULL for BF16) */
   uint8_t* v_scale;  /* the same */
 } gdn_kv_cache;
 

@@ -26,154 +26,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kMaxCtas = 160;   // SMs of the largest part of this architecture
-constexpr int kBlock = 128;     // keys of a block
 constexpr uint32_t kStage = 32768;
-constexpr float kLazy = 8.f;    // the maximum is raised when a block exceeds it by this power of two
-
-struct AttnParams {
-  CUtensorMap tmap_k;  // pages as [pages * Hkv * page][D] bf16, box 64 x min(page, 64), 128-byte swizzle
-  CUtensorMap tmap_v;
-  const uint16_t* q;
-  PagedCache cache;
-  const int32_t* kv_lens;
-  const int32_t* cu;
-  HeadRows z;
-  uint16_t* out;
-  unsigned* err;
-  float scale_log2;
-  int Hq, Hkv, G, N, T;
-  int sub;       // tokens of one 128-row tile: 128 / G
-  int4* desc;    // [2 * grid] what each part of a cut tile holds
-  float2* ml;    // [2 * grid][rows] maximum (log2 units) and sum
-  float4* part;  // [2 * grid][tiles][D / 4][128] unnormalised O
-};
-
-// ---------------------------------------------------------------- the line of work
-
-// sum_{i < n} floor((a i + b) / m), all arguments >= 0
-__device__ __forceinline__ long floor_sum(long n, long m, long a, long b) {
-  long s = 0;
-  while (n > 0) {
-    if (a >= m) {
-      s += n * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      s += n * (b / m);
-      b %= m;
-    }
-    const long y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const long t = m;
-    m = a;
-    a = t;
-  }
-  return s;
-}
-
-// One sequence's new tokens and cache.
-struct SeqInfo {
-  int first, len, kv;
-};
-
-__device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, bool report) {
-  SeqInfo s = {n, 1, 0};
-  bool bad = false;
-  if (p.cu) {
-    const int a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1);
-    bad = a < 0 || b < a || b > p.T;
-    s.first = a;
-    s.len = bad ? 0 : b - a;
-  }
-  s.kv = __ldg(p.kv_lens + n);
-  if (s.kv < 0 || s.kv > ((long)p.cache.max_pages << p.cache.page_shift)) {
-    bad = true;
-    s.kv = 0;
-  }
-  if (bad && report) raise_error(p.err, kErrDeviceArgument);
-  return s;
-}
-
-// Keys that the last token of tile i sees; blocks of that tile (one at least, so that rows without a
-// key are visited too); blocks of the tiles before tile i.
-struct Tiles {
-  int p0, len, step;  // position of the first new token, new tokens, tokens of a tile
-  __device__ __forceinline__ int count() const { return (len + step - 1) / step; }
-  __device__ __forceinline__ int keys(int i) const { return p0 + (int)min((long)(i + 1) * step, (long)len); }
-  __device__ __forceinline__ int blocks(int i) const {
-    const int k = keys(i);
-    return k <= kBlock ? 1 : (int)(((long)k + kBlock - 1) / kBlock);
-  }
-  __device__ __forceinline__ long before(int i) const {
-    const int last = count() - 1, full = min(i, last);
-    if (full <= 0) return i > last && last >= 0 ? blocks(last) : 0;
-    const long lead = (long)kBlock - p0;  // tiles with at most one block: (t + 1) step <= lead
-    const int t0 = lead < step ? 0 : (int)min((long)full, lead / step);
-    long s = t0;
-    if (full > t0) s += floor_sum(full - t0, kBlock, step, (long)(t0 + 1) * step + p0 + kBlock - 1);
-    return s + (i > last ? blocks(last) : 0);
-  }
-};
-
-// A run of blocks [j0, j1) of one tile.
-struct Segment {
-  int n, hk;
-  int row0, ntok, pos0;  // packed row and position of the tile's first token, tokens
-  int keys;              // that the tile's last token sees (<= 0: no row sees any)
-  int j0, j1, nb;        // nb: the tile's blocks
-};
-
-// A CTA's piece of the line, segment by segment.  Every warp walks it by itself.
-struct Walk {
-  long left;  // blocks not yet taken
-  int n, hk, tile, j;
-  SeqInfo s;
-  Tiles t;
-
-  __device__ __forceinline__ void load(const AttnParams& p, int step) {
-    s = seq_info(p, n, false);
-    t = {s.kv - s.len, s.len, step};
-  }
-  __device__ __forceinline__ bool next(const AttnParams& p, int step, Segment& g) {
-    if (left <= 0) return false;
-    g.n = n;
-    g.hk = hk;
-    g.nb = t.blocks(tile);
-    g.row0 = s.first + tile * step;
-    g.ntok = min(step, s.len - tile * step);
-    g.pos0 = t.p0 + tile * step;
-    g.keys = t.keys(tile);
-    g.j0 = j;
-    g.j1 = (int)min((long)g.nb, j + left);
-    left -= g.j1 - g.j0;
-    j = g.j1;
-    if (left > 0) {  // the next tile, key head, sequence
-      j = 0;
-      if (++tile == t.count()) {
-        tile = 0;
-        if (++hk == p.Hkv) {
-          hk = 0;
-          do {
-            if (++n >= p.N) {
-              left = 0;
-              break;
-            }
-            load(p, step);
-          } while (s.len == 0);
-        }
-      }
-    }
-    return true;
-  }
-};
-
-struct WalkStart {
-  long left, rem;
-  int n, hk, tile, j;
-};
 
 // ---------------------------------------------------------------- layout of a CTA
 
@@ -240,14 +93,6 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t (&r)[64]) {
                : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-__device__ __forceinline__ uint8_t* align1024(uint8_t* q) {
-  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(q) + 1023) & ~(uintptr_t)1023);
-}
-
 // A position in the ring of stages: which stage, and which pass over the ring.
 template <int kStages>
 struct Ring {
@@ -265,6 +110,21 @@ struct Ring {
     i = (int)(at % kStages);
   }
 };
+
+// Loads that stay where they are written: the compiler may otherwise sink a read-only load to its use,
+// three stages later.
+__device__ __forceinline__ uint4 ld_ahead16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_ahead4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
@@ -316,79 +176,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   }
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
 
-  // ---- this CTA's piece of the line
-  {
-    long mine = 0;
-    for (int n = tid; n < p.N; n += C::kThreads) {
-      const SeqInfo s = seq_info(p, n, blockIdx.x == 0);
-      const Tiles t = {s.kv - s.len, s.len, step};
-      if (s.len > 0) mine += t.before(t.count());
-    }
-    mine *= p.Hkv;
-    long sum = mine;
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) scan[warp] = sum;
-    __syncthreads();
-    long total = 0;
-    for (int w = 0; w < C::kThreads / 32; ++w) total += scan[w];
-    __syncthreads();
-    const long u0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
-    const long u1 = total / gridDim.x * (blockIdx.x + 1) + total % gridDim.x * (blockIdx.x + 1) / gridDim.x;
-    if (u1 > u0) {
-      long base = 0;  // blocks of the sequences before this round's
-      for (int n0 = 0; n0 < p.N; n0 += C::kThreads) {
-        const int n = n0 + tid;
-        long u = 0;
-        if (n < p.N) {
-          const SeqInfo s = seq_info(p, n, false);
-          const Tiles t = {s.kv - s.len, s.len, step};
-          if (s.len > 0) u = t.before(t.count()) * p.Hkv;
-        }
-        long inc = u;
-        for (int o = 1; o < 32; o <<= 1) {
-          const long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-          if (lane >= o) inc += x;
-        }
-        if (lane == 31) scan[warp] = inc;
-        __syncthreads();
-        long before = base, round = 0;
-        for (int w = 0; w < C::kThreads / 32; ++w) {
-          if (w < warp) before += scan[w];
-          round += scan[w];
-        }
-        const long lo = before + inc - u;
-        if (u > 0 && u0 >= lo && u0 < lo + u) {
-          start->left = u1 - u0;
-          start->rem = u0 - lo;
-          start->n = n;
-        }
-        base += round;
-        __syncthreads();
-        if (u0 < base) break;
-      }
-      // the key head, then the tile: every thread looks at one stretch of tiles
-      const SeqInfo s = seq_info(p, start->n, false);
-      const Tiles t = {s.kv - s.len, s.len, step};
-      const int count = t.count(), stretch = (count + C::kThreads - 1) / C::kThreads;
-      const long per = t.before(count), rem = start->rem % per;
-      const int lo = min(tid * stretch, count), hi = min(lo + stretch, count);
-      if (lo < hi) {
-        long at = t.before(lo);
-        if (rem >= at) {
-          for (int i = lo; i < hi; ++i) {
-            const int nb = t.blocks(i);
-            if (rem < at + nb) {
-              start->hk = (int)(start->rem / per);
-              start->tile = i;
-              start->j = (int)(rem - at);
-              break;
-            }
-            at += nb;
-          }
-        }
-      }
-    }
-  }
+  find_start<C::kThreads>(p, step, scan, start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -627,8 +415,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           }
         } else if (busy) {
           const int slot = 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0);
-          p.ml[(long)slot * 128 * kTiles + sub * 128 + row] = make_float2(m, l);
-          float4* dst = p.part + ((long)slot * kTiles + sub) * (D / 4) * 128 + row;
+          p.ml[(long)slot * 256 + sub * 128 + row] = make_float2(m, l);
+          float4* dst = p.part + (long)slot * (kPartBytes / sizeof(float4)) + sub * (D / 4) * 128 + row;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float o[32];
@@ -644,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         }
         if (!whole && warp == 0 && lane == 0)
           p.desc[2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0)] =
-              make_int4(seg.row0, seg.ntok, hk, 1 | (seg.j1 == seg.nb ? 2 : 0));
+              make_int4(seg.row0, seg.ntok, hk, kPart | (seg.j1 == seg.nb ? kPartLast : 0));
         tc_fence_before();
       }
     }
@@ -671,7 +459,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       const int key = j * kBlock + (lane << shift);
       int id = 0;
       if ((lane << shift) < kBlock && key < seg.keys) {
-        id = __ldg(p.cache.table + (long)seg.n * p.cache.max_pages + (key >> shift));
+        id = (int)ld_ahead4(p.cache.table + (long)seg.n * p.cache.max_pages + (key >> shift));
         if ((unsigned)id >= (unsigned)p.cache.num_pages) {
           raise_error(p.err, kErrDeviceArgument);
           id = 0;
@@ -710,7 +498,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         x[u] = make_uint4(0, 0, 0, 0);
         if (j * kBlock + row < seg.keys) {
           const long at = (((long)page * p.Hkv + seg.hk) << shift) + (row & ((1 << shift) - 1));
-          x[u] = __ldg(reinterpret_cast<const uint4*>(src + at * D + d));
+          x[u] = ld_ahead16(src + at * D + d);
         }
       }
       mt = (value ? 1 : 0) | part << 1;
@@ -720,8 +508,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         k4 = v4 = 0;
         if (lane * 4 < hv) {
           const long at = (((long)page * p.Hkv + seg.hk) << shift) + ((lane * 4) & ((1 << shift) - 1));
-          k4 = __ldg(reinterpret_cast<const uint32_t*>(p.cache.k_scale + at));
-          v4 = __ldg(reinterpret_cast<const uint32_t*>(p.cache.v_scale + at));
+          k4 = ld_ahead4(p.cache.k_scale + at);
+          v4 = ld_ahead4(p.cache.v_scale + at);
         }
       }
       if (++part == kParts) {
@@ -1007,37 +795,64 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
 }
 
 // Joins the parts of cut tiles: out = sum_c O_c 2^(m_c - m) / sum_c l_c 2^(m_c - m), c over the tile's
-// parts in the order of the line.  The CTA of the tile's first part does it; blockIdx.y takes a share
-// of the columns.  A few rows (one token's heads) or 256: lanes are rows either way, as they were written.
+// parts in the order of the line (so the result does not depend on who is first).  The CTAs of the
+// tile's first part do it, blockIdx.y takes a share of rows and columns.  The parts are listed first, so
+// that their loads do not wait for one another.
+//   kTiles 1, 2: parts [tile][D / 4][128 rows], lanes are rows;  kTiles 0: parts [row][D], lanes are columns
 template <int D, int kTiles>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p, int ctas) {
+  __shared__ int s_slot[kMaxCtas + 1];
+  __shared__ int s_n;
   const int4 d = p.desc[2 * blockIdx.x + 1];
-  if (!(d.w & 1)) return;
+  if (!(d.w & kPart)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int subs = d.y > p.sub ? 2 : 1;
-  for (int i = blockIdx.y * 8 + warp; i < subs * 4 * (D / 4); i += gridDim.y * 8) {
-    const int col = i % (D / 4), rw = i / (D / 4), sub = rw >> 2, row = (rw & 3) * 32 + lane;
-    const int rows = min(p.sub, d.y - sub * p.sub) * p.G;
-    if ((rw & 3) * 32 >= rows) continue;
+  if (warp == 0) {
+    int n = 1;
+    if (lane == 0) s_slot[0] = 2 * blockIdx.x + 1;
+    for (int c = blockIdx.x + 1; c < ctas; c += 32) {  // CTAs without work lie between the parts of a short line
+      const int w = c + lane < ctas ? p.desc[2 * (c + lane)].w : 0;
+      const unsigned last = __ballot_sync(0xFFFFFFFFu, w & kPartLast);
+      unsigned have = __ballot_sync(0xFFFFFFFFu, w & kPart);
+      if (last) have &= (last & -last) * 2u - 1u;  // up to the first that ends a tile
+      if (have >> lane & 1u) s_slot[n + __popc(have & ((1u << lane) - 1u))] = 2 * (c + lane);
+      n += __popc(have);
+      if (last) break;
+    }
+    if (lane == 0) s_n = n;
+  }
+  __syncthreads();
+  const int parts = s_n;
+  const int subs = kTiles == 2 && d.y > p.sub ? 2 : 1;
+  const int items = kTiles ? subs * 4 * (D / 4) : (p.G * (D / 4) + 31) / 32;  // of a warp each
+  for (int i = blockIdx.y * 8 + warp; i < items; i += gridDim.y * 8) {
+    int col, row, sub = 0, rows = p.G;
+    if constexpr (kTiles > 0) {
+      const int rw = i / (D / 4);
+      col = i % (D / 4);
+      sub = rw >> 2;
+      row = (rw & 3) * 32 + lane;
+      rows = min(p.sub, d.y - sub * p.sub) * p.G;
+      if ((rw & 3) * 32 >= rows) continue;
+    } else {
+      col = (i * 32 + lane) % (D / 4);
+      row = (i * 32 + lane) / (D / 4);
+    }
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    int flags = d.w;
-    for (int c = blockIdx.x, slot = 2 * c + 1;;) {
-      const float2 ml = p.ml[(long)slot * 128 * kTiles + sub * 128 + row];
-      const float4 x = p.part[(((long)slot * kTiles + sub) * (D / 4) + col) * 128 + row];
-      const float m2 = fmaxf(m, ml.x);
-      const float off = m2 == -INFINITY ? 0.f : m2;
-      const float a = ex2_approx(m - off), b = ex2_approx(ml.x - off);
-      l = l * a + ml.y * b;
-      o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
-      m = m2;
-      if (flags & 2) break;
-      do {  // the next CTA that has a piece
-        if (++c >= ctas) break;
-        slot = 2 * c;
-        flags = p.desc[slot].w;
-      } while (!(flags & 1));
-      if (c >= ctas) break;
+    if (kTiles > 0 || row < rows) {
+#pragma unroll 4
+      for (int k = 0; k < parts; ++k) {
+        const long slot = s_slot[k];
+        const float2 ml = p.ml[slot * 256 + sub * 128 + row];
+        const float4* part = p.part + slot * (long)(kPartBytes / sizeof(float4));
+        const float4 x = kTiles > 0 ? part[(sub * (D / 4) + col) * 128 + row] : part[row * (D / 4) + col];
+        const float m2 = fmaxf(m, ml.x);
+        const float off = m2 == -INFINITY ? 0.f : m2;
+        const float a = ex2_approx(m - off), b = ex2_approx(ml.x - off);
+        l = l * a + ml.y * b;
+        o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
+        m = m2;
+      }
     }
     if (row < rows) {
       const int t = row / p.G, h = d.z * p.G + row - t * p.G;
@@ -1063,6 +878,13 @@ cudaError_t encode_pages(CUtensorMap* map, const void* base, const PagedCache& c
                               c.page_shift > 6 ? 64 : 1u << c.page_shift);
 }
 
+template <int D, int kTiles>
+cudaError_t launch_join(const LaunchEnv& env, const AttnParams& p, int ctas) {
+  const int items = kTiles ? 4 * kTiles * (D / 4) : (p.G * (D / 4) + 31) / 32;
+  attn_join_kernel<D, kTiles><<<dim3(ctas, items < 64 ? (items + 7) / 8 : 8), 256, 0, env.stream>>>(p, ctas);
+  return cudaGetLastError();
+}
+
 template <int D, int kTiles, bool kE4M3>
 cudaError_t launch_tiles(const LaunchEnv& env, const AttnParams& p, int ctas) {
   using C = Cfg<D, kTiles, kE4M3>;
@@ -1083,8 +905,7 @@ cudaError_t launch_tiles(const LaunchEnv& env, const AttnParams& p, int ctas) {
   attn_kernel<D, kTiles, kE4M3><<<ctas, C::kThreads, C::kSmem, env.stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_join_kernel<D, kTiles><<<dim3(ctas, 8), 256, 0, env.stream>>>(p, ctas);
-  return cudaGetLastError();
+  return launch_join<D, kTiles>(env, p, ctas);
 }
 
 }  // namespace
@@ -1092,7 +913,7 @@ cudaError_t launch_tiles(const LaunchEnv& env, const AttnParams& p, int ctas) {
 // Descriptors, maxima and sums, and 128 KB of O for each of two parts a CTA.
 size_t attn_workspace_bytes(int D) {
   (void)D;
-  return 2 * kMaxCtas * (sizeof(int4) + 256 * sizeof(float2) + 131072) ;
+  return 2 * kMaxCtas * (sizeof(int4) + 256 * sizeof(float2) + kPartBytes);
 }
 
 cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint16_t* q, const PagedCache& cache,
@@ -1118,15 +939,23 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   p.desc = reinterpret_cast<int4*>(ws);
   p.ml = reinterpret_cast<float2*>(ws + 2 * kMaxCtas * sizeof(int4));
   p.part = reinterpret_cast<float4*>(ws + 2 * kMaxCtas * (sizeof(int4) + 256 * sizeof(float2)));
-  cudaError_t e = cudaSuccess;
+  int sms = 0;
+  cudaError_t e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  // One token of each sequence and at most 16 query heads to a key head: too few rows to fill a
+  // 128-row tile, and HBM bounds the call.
+  if (!cu && p.G <= 16) {
+    p.sub = 1;
+    e = launch_attn_decode(env, p, D, ctas);
+    if (e != cudaSuccess) return e;
+    return D == 128 ? launch_join<128, 0>(env, p, ctas) : launch_join<256, 0>(env, p, ctas);
+  }
   if (!cache.e4m3) {
     e = encode_pages(&p.tmap_k, cache.k, cache, Hkv, D);
     if (e == cudaSuccess) e = encode_pages(&p.tmap_v, cache.v, cache, Hkv, D);
+    if (e != cudaSuccess) return e;
   }
-  int sms = 0;
-  if (e == cudaSuccess) e = device_sm_count(&sms);
-  if (e != cudaSuccess) return e;
-  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   // two tiles a CTA where a sequence has more rows than one holds, on average
   const bool two = (long)T * p.G > 128L * N;
   if (cache.e4m3) {

@@ -39,4 +39,245 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+constexpr int kBlock = 128;     // keys of a block, the unit of work
+
+struct AttnParams {
+  CUtensorMap tmap_k;  // pages as [pages * Hkv * page][D] bf16, box 64 x min(page, 64), 128-byte swizzle
+  CUtensorMap tmap_v;
+  const uint16_t* q;
+  PagedCache cache;
+  const int32_t* kv_lens;
+  const int32_t* cu;
+  HeadRows z;
+  uint16_t* out;
+  unsigned* err;
+  float scale_log2;
+  int Hq, Hkv, G, N, T;
+  int sub;       // tokens of one tile: 128 / G on the tcgen05 cores, 1 in the one-token kernel
+  int4* desc;    // [2 * grid] what each part of a cut tile holds: packed row, tokens, key head, flags
+  float2* ml;    // [2 * grid][256] maximum (log2 units) and sum of a row
+  float4* part;  // [2 * grid][128 KB] unnormalised O
+};
+
+// ---------------------------------------------------------------- the line of work
+
+// sum_{i < n} floor((a i + b) / m), all arguments >= 0
+__device__ __forceinline__ long floor_sum(long n, long m, long a, long b) {
+  long s = 0;
+  while (n > 0) {
+    if (a >= m) {
+      s += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      s += n * (b / m);
+      b %= m;
+    }
+    const long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
+
+// One sequence's new tokens and cache.
+struct SeqInfo {
+  int first, len, kv;
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, bool report) {
+  SeqInfo s = {n, 1, 0};
+  bool bad = false;
+  if (p.cu) {
+    const int a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1);
+    bad = a < 0 || b < a || b > p.T;
+    s.first = a;
+    s.len = bad ? 0 : b - a;
+  }
+  s.kv = __ldg(p.kv_lens + n);
+  if (s.kv < 0 || s.kv > ((long)p.cache.max_pages << p.cache.page_shift)) {
+    bad = true;
+    s.kv = 0;
+  }
+  if (bad && report) raise_error(p.err, kErrDeviceArgument);
+  return s;
+}
+
+// Keys that the last token of tile i sees; blocks of that tile (one at least, so that rows without a
+// key are visited too); blocks of the tiles before tile i.
+struct Tiles {
+  int p0, len, step;  // position of the first new token, new tokens, tokens of a tile
+  __device__ __forceinline__ int count() const { return (len + step - 1) / step; }
+  __device__ __forceinline__ int keys(int i) const { return p0 + (int)min((long)(i + 1) * step, (long)len); }
+  __device__ __forceinline__ int blocks(int i) const {
+    const int k = keys(i);
+    return k <= kBlock ? 1 : (int)(((long)k + kBlock - 1) / kBlock);
+  }
+  __device__ __forceinline__ long before(int i) const {
+    const int last = count() - 1, full = min(i, last);
+    if (full <= 0) return i > last && last >= 0 ? blocks(last) : 0;
+    const long lead = (long)kBlock - p0;  // tiles with at most one block: (t + 1) step <= lead
+    const int t0 = lead < step ? 0 : (int)min((long)full, lead / step);
+    long s = t0;
+    if (full > t0) s += floor_sum(full - t0, kBlock, step, (long)(t0 + 1) * step + p0 + kBlock - 1);
+    return s + (i > last ? blocks(last) : 0);
+  }
+};
+
+// A run of blocks [j0, j1) of one tile.
+struct Segment {
+  int n, hk;
+  int row0, ntok, pos0;  // packed row and position of the tile's first token, tokens
+  int keys;              // that the tile's last token sees (<= 0: no row sees any)
+  int j0, j1, nb;        // nb: the tile's blocks
+};
+
+// A CTA's piece of the line, segment by segment.  Every warp walks it by itself.
+struct Walk {
+  long left;  // blocks not yet taken
+  int n, hk, tile, j;
+  SeqInfo s;
+  Tiles t;
+
+  __device__ __forceinline__ void load(const AttnParams& p, int step) {
+    s = seq_info(p, n, false);
+    t = {s.kv - s.len, s.len, step};
+  }
+  __device__ __forceinline__ bool next(const AttnParams& p, int step, Segment& g) {
+    if (left <= 0) return false;
+    g.n = n;
+    g.hk = hk;
+    g.nb = t.blocks(tile);
+    g.row0 = s.first + tile * step;
+    g.ntok = min(step, s.len - tile * step);
+    g.pos0 = t.p0 + tile * step;
+    g.keys = t.keys(tile);
+    g.j0 = j;
+    g.j1 = (int)min((long)g.nb, j + left);
+    left -= g.j1 - g.j0;
+    j = g.j1;
+    if (left > 0) {  // the next tile, key head, sequence
+      j = 0;
+      if (++tile == t.count()) {
+        tile = 0;
+        if (++hk == p.Hkv) {
+          hk = 0;
+          do {
+            if (++n >= p.N) {
+              left = 0;
+              break;
+            }
+            load(p, step);
+          } while (s.len == 0);
+        }
+      }
+    }
+    return true;
+  }
+};
+
+struct WalkStart {
+  long left, rem;
+  int n, hk, tile, j;
+};
+
+// This CTA's piece of the line: an equal share of all blocks, found by the whole CTA.  `scan`: one long
+// for each warp; start->left is 0 before the call and stays 0 for a CTA without work.  The caller
+// synchronises before it reads *start.
+template <int kThreads>
+__device__ __forceinline__ void find_start(const AttnParams& p, int step, long* scan, WalkStart* start) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  long mine = 0;
+  for (int n = tid; n < p.N; n += kThreads) {
+    const SeqInfo s = seq_info(p, n, blockIdx.x == 0);
+    const Tiles t = {s.kv - s.len, s.len, step};
+    if (s.len > 0) mine += t.before(t.count());
+  }
+  mine *= p.Hkv;
+  long sum = mine;
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if (lane == 0) scan[warp] = sum;
+  __syncthreads();
+  long total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) total += scan[w];
+  __syncthreads();
+  const long u0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
+  const long u1 = total / gridDim.x * (blockIdx.x + 1) + total % gridDim.x * (blockIdx.x + 1) / gridDim.x;
+  if (u1 > u0) {
+    long base = 0;  // blocks of the sequences before this round's
+    for (int n0 = 0; n0 < p.N; n0 += kThreads) {
+      const int n = n0 + tid;
+      long u = 0;
+      if (n < p.N) {
+        const SeqInfo s = seq_info(p, n, false);
+        const Tiles t = {s.kv - s.len, s.len, step};
+        if (s.len > 0) u = t.before(t.count()) * p.Hkv;
+      }
+      long inc = u;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      if (lane == 31) scan[warp] = inc;
+      __syncthreads();
+      long before = base, round = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += scan[w];
+        round += scan[w];
+      }
+      const long lo = before + inc - u;
+      if (u > 0 && u0 >= lo && u0 < lo + u) {
+        start->left = u1 - u0;
+        start->rem = u0 - lo;
+        start->n = n;
+      }
+      base += round;
+      __syncthreads();
+      if (u0 < base) break;
+    }
+    // the key head, then the tile: every thread looks at one stretch of tiles
+    const SeqInfo s = seq_info(p, start->n, false);
+    const Tiles t = {s.kv - s.len, s.len, step};
+    const int count = t.count(), stretch = (count + kThreads - 1) / kThreads;
+    const long per = t.before(count), rem = start->rem % per;
+    const int lo = min(tid * stretch, count), hi = min(lo + stretch, count);
+    if (lo < hi) {
+      long at = t.before(lo);
+      if (rem >= at) {
+        for (int i = lo; i < hi; ++i) {
+          const int nb = t.blocks(i);
+          if (rem < at + nb) {
+            start->hk = (int)(start->rem / per);
+            start->tile = i;
+            start->j = (int)(rem - at);
+            break;
+          }
+          at += nb;
+        }
+      }
+    }
+  }
+}
+
+// Flags of a part in AttnParams::desc.
+enum : int { kPart = 1, kPartLast = 2 };
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* q) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(q) + 1023) & ~(uintptr_t)1023);
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+constexpr float kLazy = 8.f;  // a row's maximum is raised when a score exceeds it by this power of two
+constexpr int kMaxCtas = 160;  // SMs of the largest part of this architecture
+constexpr size_t kPartBytes = 131072;
+
+cudaError_t launch_attn_decode(const LaunchEnv& env, AttnParams& p, int D, int ctas);
+
 }  // namespace gdn

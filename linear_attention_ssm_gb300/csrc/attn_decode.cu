@@ -1,0 +1,586 @@
+// attn_decode.cu -- softmax attention of one new token of each sequence over its paged cache.
+//
+// A key head's at most 16 query rows do not fill a tcgen05 tile, and every cached byte is used once: HBM
+// bounds the kernel, so it is built to keep copies in flight and to finish a key quickly.  The keys of a
+// segment go round the CTA's warps 16 at a time.  A warp's groups arrive by TMA in a ring of its own, and
+// it takes them through both products with mma.sync (m16n8k16), transposed so that keys and values fill
+// the 16 rows and the query rows the 8 columns:
+//   S^T [16 keys x q] = K Q^T,   p = 2^(S - m),   O^T [D x q] += V^T P^T
+// with its own running m, l and O in registers: no barrier between the warps until the segment ends,
+// where they are joined pairwise.  (Work is cut into one piece for each SM as in the tile kernel.)
+//
+// An e4m3 cache is widened between shared memory and the registers, two codes an instruction, to
+// binary16, which holds every code exactly.  The queries become binary16 too, each row divided by the
+// power of two of its largest value: what that loses is below 2^-25 of that value.  Scores get the keys'
+// powers of two, weights the values' (relative to the group's largest; O is held in units of 2^r, raised
+// with it).  Weights are at most 2^8: times 2^7 they still fit binary16, and only weights below 2^-21 of
+// a row's largest leave its normal range.
+#include <cstring>
+
+#include "attn_common.cuh"
+#include "chunk_common.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kGroup = 16;       // keys of a group: the rows of one mma
+constexpr float kWeight = 7.f;   // log2 of the factor on binary16 weights
+
+template <int D, bool kE4M3, int kQ8>  // kQ8: columns of 8 query rows
+struct DCfg {
+  // A warp's ring needs three groups to cover HBM's latency; at D = 256 in bf16 (16 KB a group) shared
+  // memory holds that for four warps, which is enough for the bandwidth.
+  static constexpr int kWarps = !kE4M3 && D == 256 ? 4 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kRow = D * (kE4M3 ? 1 : 2);  // bytes of a key
+  static constexpr int kBoxes = kRow / 128;         // 128-byte columns of a group, [16 rows][128 bytes] swizzled
+  static constexpr int kHalf = kGroup * kRow;       // a group's keys, then its values
+  static constexpr int kTiles = D / 16;             // of O^T
+  static constexpr int kMergeO = kWarps / 2 * kQ8 * 8 * D * 4, kMergeMl = kWarps / 2 * 32 * kQ8 * 16;
+  static constexpr int kFixed = kMergeO + kMergeMl + 1024 + 1024;  // and scan, start; alignment of the base
+  static constexpr int kPerSlot = 2 * kHalf + 32 + 32 + 8;         // ring, meta, scales, barrier
+  static constexpr int kFit = (232448 - kFixed) / (kWarps * kPerSlot);
+  static constexpr int kSlots = kFit < 8 ? kFit : 8;
+  static_assert(kSlots >= 2, "a ring of two groups at least");
+  static constexpr int kOffMerge = kWarps * kSlots * 2 * kHalf;
+  static constexpr int kOffMl = kOffMerge + kMergeO;
+  static constexpr int kOffMeta = kOffMl + kMergeMl;
+  static constexpr int kOffScale = kOffMeta + kWarps * kSlots * 32;
+  static constexpr int kOffBar = kOffScale + kWarps * kSlots * 32;
+  static constexpr int kOffScan = kOffBar + kWarps * kSlots * 8;
+  static constexpr int kSmem = kOffScan + 512 + 1024;
+  static_assert(kSmem <= 232448, "shared memory");
+};
+
+// What a slot of the ring holds.
+struct Group {
+  int key0, n;    // first key; keys, 0: none (a segment with fewer groups than warps)
+  int flags;
+  int row0, hk;   // packed row, key head
+  int part;       // slot of the segment's part in the workspace
+  int pad[2];
+};
+enum : int { kFirst = 1, kLastOfSegment = 2, kEnd = 4, kWhole = 8, kEndsTile = 16 };
+
+template <bool kF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (kF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+// two e4m3 codes -> two binary16 values
+__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t v) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((uint16_t)v, __NV_E4M3);
+  return (uint32_t)h.x | (uint32_t)h.y << 16;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int D, bool kE4M3, int kQ8>
+__global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_kernel(const __grid_constant__ AttnParams p) {
+  using C = DCfg<D, kE4M3, kQ8>;
+  constexpr int kWarps = C::kWarps, kSlots = C::kSlots, kTiles = C::kTiles;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = align1024(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  uint8_t* ring = sm + warp * kSlots * 2 * C::kHalf;
+  Group* groups = reinterpret_cast<Group*>(sm + C::kOffMeta) + warp * kSlots;
+  uint8_t* scales = sm + C::kOffScale + warp * kSlots * 32;
+  const uint32_t ring_s = smem_u32(ring), scale_s = smem_u32(scales);
+  const uint32_t bar = smem_u32(sm + C::kOffBar) + warp * kSlots * 8;
+  long* scan = reinterpret_cast<long*>(sm + C::kOffScan);
+  WalkStart* start = reinterpret_cast<WalkStart*>(scan + 16);
+  if (lane == 0) {
+    for (int i = 0; i < kSlots; ++i) mbar_init(bar + 8 * i, 1);
+    fence_mbar_init();
+    if (warp == 0) {
+      prefetch_tensormap(&p.tmap_k);
+      prefetch_tensormap(&p.tmap_v);
+      start->left = 0;
+      p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+      p.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+    }
+  }
+  find_start<C::kThreads>(p, 1, scan, start);
+  __syncthreads();
+  Walk walk;
+  walk.left = start->left;
+  if (walk.left == 0) return;
+  walk.n = start->n;
+  walk.hk = start->hk;
+  walk.tile = start->tile;
+  walk.j = start->j;
+  walk.load(p, 1);
+
+  // ---- the loading side: the warp's next group into a slot
+  Segment seg = {};
+  bool dead = false;                      // a wait ran out
+  bool open = false;                      // a segment has groups left for this warp
+  int gi = 0, ng = 0, base = 0, lim = 0;  // next group, groups, first key, end of the segment
+  int id = 0;                             // page of group gi
+  auto page_id = [&](int key) {
+    return (int)__ldg(p.cache.table + (long)seg.n * p.cache.max_pages + (key >> p.cache.page_shift));
+  };
+  auto issue = [&](int slot) {
+    Group* m = groups + slot;
+    int flags = 0;
+    if (!open) {
+      if (!walk.next(p, 1, seg)) {
+        if (lane == 0) m->flags = kEnd;
+        return;
+      }
+      open = true;
+      flags = kFirst;
+      base = seg.j0 * kBlock;
+      lim = min(seg.keys, seg.j1 * kBlock);
+      ng = lim > base ? (lim - base + kGroup - 1) / kGroup : 0;
+      gi = warp;
+      if (gi < ng) id = page_id(base + gi * kGroup);
+    }
+    const int key0 = base + gi * kGroup, n = gi < ng && !dead ? min(kGroup, lim - key0) : 0;
+    if (gi + kWarps >= ng) {
+      flags |= kLastOfSegment;
+      open = false;
+    }
+    if (seg.j0 == 0 && seg.j1 == seg.nb) flags |= kWhole;
+    if (seg.j1 == seg.nb) flags |= kEndsTile;
+    if (n > 0 && (unsigned)id >= (unsigned)p.cache.num_pages) {
+      raise_error(p.err, kErrDeviceArgument);
+      id = 0;
+    }
+    if (lane == 0) {
+      *reinterpret_cast<int4*>(&m->key0) = make_int4(key0, n, flags, seg.row0);
+      *reinterpret_cast<int2*>(&m->hk) = make_int2(seg.hk, 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0));
+      if (n > 0) {
+        const int y = ((id * p.Hkv + seg.hk) << p.cache.page_shift) + (key0 & ((1 << p.cache.page_shift) - 1));
+        const uint32_t dst = ring_s + slot * 2 * C::kHalf;
+        mbar_arrive_expect_tx(bar + 8 * slot, 2 * C::kHalf + (kE4M3 ? 32 : 0));
+#pragma unroll
+        for (int b = 0; b < C::kBoxes; ++b) tma_load_2d(dst + b * 2048, &p.tmap_k, b * (kE4M3 ? 128 : 64), y, bar + 8 * slot);
+        if constexpr (kE4M3) {
+          bulk_load(scale_s + slot * 32, p.cache.k_scale + y, 16, bar + 8 * slot);
+          bulk_load(scale_s + slot * 32 + 16, p.cache.v_scale + y, 16, bar + 8 * slot);
+        }
+#pragma unroll
+        for (int b = 0; b < C::kBoxes; ++b)
+          tma_load_2d(dst + C::kHalf + b * 2048, &p.tmap_v, b * (kE4M3 ? 128 : 64), y, bar + 8 * slot);
+      } else if (!dead) {
+        mbar_arrive(bar + 8 * slot);
+      }
+    }
+    gi += kWarps;
+    if (open) id = page_id(base + gi * kGroup);  // for the next call: its latency passes meanwhile
+  };
+  for (int i = 0; i < kSlots; ++i) issue(i);
+  __syncwarp();
+
+  // ---- the computing side
+  uint32_t q[kQ8][D / 8];        // Q^T fragments of the segment's key head
+  float qs[kQ8][2];              // log2 units of a score, for this lane's two query rows
+  float o[kQ8][kTiles][4];       // O^T: rows d, columns the two query rows
+  float m[kQ8][2], l[kQ8][2], r[kQ8][2];
+  int bad_slot = 0, bad_pass = 0;
+  for (int slot = 0, pass = 0;; pass ^= (slot == kSlots - 1), slot = slot == kSlots - 1 ? 0 : slot + 1) {
+    const int4 ga = *reinterpret_cast<const int4*>(&groups[slot].key0);
+    const int key0 = ga.x, n = ga.y, flags = ga.z, row0 = ga.w;
+    if (flags & kEnd) break;
+    const int2 gb = *reinterpret_cast<const int2*>(&groups[slot].hk);
+    const int hk = gb.x, part = gb.y;
+    if (flags & kFirst) {
+#pragma unroll
+      for (int a = 0; a < kQ8; ++a) {
+        const int row = a * 8 + g;
+        const uint16_t* src = p.q + ((long)row0 * p.Hq + hk * p.G + row) * D;
+        if constexpr (!kE4M3) {
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {  // 64-value column x / 2, its 16-byte piece 2 c + x % 2
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < p.G) v = __ldg(reinterpret_cast<const uint4*>(src + (x >> 1) * 64 + (2 * c + (x & 1)) * 8));
+            q[a][4 * x] = v.x;
+            q[a][4 * x + 1] = v.y;
+            q[a][4 * x + 2] = v.z;
+            q[a][4 * x + 3] = v.w;
+          }
+          qs[a][0] = qs[a][1] = p.scale_log2;
+        } else {
+          uint32_t top = 0;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x) {  // 128-value column x / 2, its 16-value piece 2 c + x % 2
+            uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (row < p.G) {
+              const uint4* s = reinterpret_cast<const uint4*>(src + (x >> 1) * 128 + (2 * c + (x & 1)) * 16);
+              v[0] = __ldg(s);
+              v[1] = __ldg(s + 1);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              q[a][8 * x + 4 * i] = v[i].x;
+              q[a][8 * x + 4 * i + 1] = v[i].y;
+              q[a][8 * x + 4 * i + 2] = v[i].z;
+              q[a][8 * x + 4 * i + 3] = v[i].w;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t lo = q[a][i] << 16 & 0x7FFFFFFFu, hi = q[a][i] & 0x7FFF0000u;
+            top = max(top, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+          }
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+          // the row divided by 2^e, e the exponent of its largest value (kept where both powers are normal)
+          const int e = min(max((int)(top >> 23) - 127, -120), 126);
+          const float inv = __uint_as_float((uint32_t)(127 - e) << 23), two = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            q[a][i] = pack_half2(__uint_as_float(q[a][i] << 16) * inv, __uint_as_float(q[a][i] & 0xFFFF0000u) * inv);
+          qs[a][0] = __shfl_sync(0xFFFFFFFFu, two, 8 * c) * p.scale_log2;  // rows 2 c, 2 c + 1 sit in lanes 4 (2 c), ..
+          qs[a][1] = __shfl_sync(0xFFFFFFFFu, two, 8 * c + 4) * p.scale_log2;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          m[a][i] = r[a][i] = -INFINITY;
+          l[a][i] = 0.f;
+        }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[a][t][i] = 0.f;
+      }
+    }
+    if (!dead && !__all_sync(0xFFFFFFFFu, mbar_wait(bar + 8 * slot, pass, kWaitLimit))) {
+      // nothing more is loaded or waited for; the walk goes on, for the other warps' barriers
+      raise_error(p.err, kErrTimeout);
+      dead = true;
+      bad_slot = slot;
+      bad_pass = pass;
+    }
+    if (n > 0 && !dead) {
+      const uint32_t ks = ring_s + slot * 2 * C::kHalf, vs = ks + C::kHalf;
+      if (n < kGroup) {  // value rows behind the last key may hold anything, and 0 * NaN is not 0
+        for (int i = lane; i < (kGroup - n) * 8 * C::kBoxes; i += 32) {
+          const int b = i / ((kGroup - n) * 8), x = i % ((kGroup - n) * 8);
+          *reinterpret_cast<uint4*>(ring + slot * 2 * C::kHalf + C::kHalf + b * 2048 + n * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      // S^T
+      float s[kQ8][2][4];
+#pragma unroll
+      for (int a = 0; a < kQ8; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[a][0][i] = s[a][1][i] = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2 * C::kBoxes; ++x) {  // column x / 2, 16-byte piece 2 c + x % 2 of rows g and g + 8
+        const uint32_t at = ks + (x >> 1) * 2048 + g * 128 + (((2 * c + (x & 1)) ^ g) << 4);
+        const uint4 u = lds128(at), w = lds128(at + 1024);
+        if constexpr (!kE4M3) {
+#pragma unroll
+          for (int a = 0; a < kQ8; ++a) {
+            mma16816<false>(s[a][0], u.x, w.x, u.y, w.y, q[a][4 * x], q[a][4 * x + 1]);
+            mma16816<false>(s[a][1], u.z, w.z, u.w, w.w, q[a][4 * x + 2], q[a][4 * x + 3]);
+          }
+        } else {
+          const uint32_t ur[4] = {u.x, u.y, u.z, u.w}, wr[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t a0 = e4m3x2_to_half2(ur[t] & 0xFFFFu), a1 = e4m3x2_to_half2(wr[t] & 0xFFFFu),
+                           a2 = e4m3x2_to_half2(ur[t] >> 16), a3 = e4m3x2_to_half2(wr[t] >> 16);
+#pragma unroll
+            for (int a = 0; a < kQ8; ++a)
+              mma16816<true>(s[a][t & 1], a0, a1, a2, a3, q[a][8 * x + 2 * t], q[a][8 * x + 2 * t + 1]);
+          }
+        }
+      }
+      // keys g and g + 8: their scales
+      float kf[2] = {1.f, 1.f}, vf[2] = {1.f, 1.f}, ev = 0.f;
+      if constexpr (kE4M3) {
+        const uint8_t* sc = scales + slot * 32;
+        uint32_t vb[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          kf[i] = e8m0_value(sc[g + 8 * i]);
+          vb[i] = g + 8 * i < n ? sc[16 + g + 8 * i] : 0u;
+        }
+        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(vb[0], vb[1]));
+        ev = (float)((int)top - 127);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int diff = (int)vb[i] - (int)top + (int)kWeight;  // the value's power over the group's, times 2^7
+          vf[i] = diff >= -126 ? __uint_as_float((uint32_t)(127 + diff) << 23) : 0.f;
+        }
+      }
+      uint32_t pb[kQ8][2];
+#pragma unroll
+      for (int a = 0; a < kQ8; ++a) {
+        float x[2][2];  // [key g, g + 8][query row]
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            x[i][k] = g + 8 * i < n ? (s[a][0][2 * i + k] + s[a][1][2 * i + k]) * (kE4M3 ? kf[i] : 1.f) * qs[a][k] : -INFINITY;
+        float top[2] = {fmaxf(x[0][0], x[1][0]), fmaxf(x[0][1], x[1][1])};
+        // m, and the unit r of O, are raised for the whole warp where one of its keys asks for it
+        bool more = top[0] > m[a][0] + kLazy || top[1] > m[a][1] + kLazy;
+        if constexpr (kE4M3) more = more || m[a][0] + ev > r[a][0] || m[a][1] + ev > r[a][1];
+        if (__any_sync(0xFFFFFFFFu, more)) {
+          float f[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], w));
+            if (top[k] > m[a][k]) {
+              l[a][k] *= ex2_approx(m[a][k] - top[k]);
+              m[a][k] = top[k];
+            }
+            const float e = m[a][k] + ev;
+            f[k] = e > r[a][k] ? ex2_approx(r[a][k] - e) : 1.f;
+            r[a][k] = fmaxf(r[a][k], e);
+          }
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            o[a][t][0] *= f[0];
+            o[a][t][1] *= f[1];
+            o[a][t][2] *= f[0];
+            o[a][t][3] *= f[1];
+          }
+        }
+        float w[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float mk = m[a][k];
+          // weights 2^(s - m + d), d <= 0 the distance of this group's unit from O's; cut off at -40 for l
+          float d = 0.f, rest = 1.f;
+          if constexpr (kE4M3) {
+            const float e = mk == -INFINITY ? 0.f : mk + ev - r[a][k];
+            d = fmaxf(e, -40.f);
+            rest = e < -40.f ? ex2_approx(e - d) : 1.f;
+          }
+          const float off = mk == -INFINITY ? 0.f : d - mk;
+          w[0][k] = ex2_approx(x[0][k] + off);
+          w[1][k] = ex2_approx(x[1][k] + off);
+          l[a][k] += kE4M3 ? (w[0][k] + w[1][k]) * ex2_approx(-d) : w[0][k] + w[1][k];
+          if constexpr (kE4M3) {
+            w[0][k] *= vf[0] * rest;
+            w[1][k] *= vf[1] * rest;
+          }
+        }
+        pb[a][0] = transpose8x8(kE4M3 ? pack_half2(w[0][0], w[0][1]) : pack_bf2(w[0][0], w[0][1]));
+        pb[a][1] = transpose8x8(kE4M3 ? pack_half2(w[1][0], w[1][1]) : pack_bf2(w[1][0], w[1][1]));
+      }
+      // O^T += V^T P^T
+      if constexpr (!kE4M3) {
+        const int key = (lane & 7) + ((lane >> 4) << 3), half = lane >> 3 & 1;  // matrices: keys 0-7 / 8-15, values 0-7 / 8-15
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          const int piece = 2 * t + half;
+          uint32_t v[4];
+          ldmatrix_x4_trans(vs + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4), v);
+#pragma unroll
+          for (int a = 0; a < kQ8; ++a) mma16816<false>(o[a][t], v[0], v[1], v[2], v[3], pb[a][0], pb[a][1]);
+        }
+      } else {
+        // 16 values (piece g of a column) of keys 2c, 2c + 1, 2c + 8, 2c + 9; tile t of the column takes
+        // values 2t (row g) and 2t + 1 (row g + 8)
+#pragma unroll
+        for (int b = 0; b < C::kBoxes; ++b) {
+          uint32_t v[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = 2 * c + (i & 1) + 8 * (i >> 1);
+            const uint4 x = lds128(vs + b * 2048 + key * 128 + ((g ^ (key & 7)) << 4));
+            v[i][0] = x.x;
+            v[i][1] = x.y;
+            v[i][2] = x.z;
+            v[i][3] = x.w;
+          }
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const uint32_t sel = t & 1 ? 0x7362u : 0x5140u;  // two values of two keys side by side
+            const uint32_t lo = __byte_perm(v[0][t >> 1], v[1][t >> 1], sel), hi = __byte_perm(v[2][t >> 1], v[3][t >> 1], sel);
+            const uint32_t a0 = e4m3x2_to_half2(lo & 0xFFFFu), a1 = e4m3x2_to_half2(lo >> 16),
+                           a2 = e4m3x2_to_half2(hi & 0xFFFFu), a3 = e4m3x2_to_half2(hi >> 16);
+#pragma unroll
+            for (int a = 0; a < kQ8; ++a) mma16816<true>(o[a][b * 8 + t], a0, a1, a2, a3, pb[a][0], pb[a][1]);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    issue(slot);
+    __syncwarp();
+    if (flags & kLastOfSegment) {
+      // ---- the warps' shares, joined pairwise
+      float4* mo = reinterpret_cast<float4*>(sm + C::kOffMerge);
+      float4* mml = reinterpret_cast<float4*>(sm + C::kOffMl);
+#pragma unroll
+      for (int a = 0; a < kQ8; ++a)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) l[a][k] += __shfl_xor_sync(0xFFFFFFFFu, l[a][k], w);
+          if constexpr (kE4M3) {  // O in units of 2^m (half the exponent at a time)
+            const float h = m[a][k] == -INFINITY ? 0.f : ex2_approx(0.5f * (r[a][k] - m[a][k] - kWeight));
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              o[a][t][k] = o[a][t][k] * h * h;
+              o[a][t][2 + k] = o[a][t][2 + k] * h * h;
+            }
+          }
+        }
+#pragma unroll 1
+      for (int h = kWarps / 2; h > 0; h >>= 1) {
+        if (warp >= h && warp < 2 * h) {
+          float4* to = mo + (warp - h) * kQ8 * kTiles * 32 + lane;
+#pragma unroll
+          for (int a = 0; a < kQ8; ++a) {
+            mml[((warp - h) * kQ8 + a) * 32 + lane] = make_float4(m[a][0], m[a][1], l[a][0], l[a][1]);
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) to[(a * kTiles + t) * 32] = make_float4(o[a][t][0], o[a][t][1], o[a][t][2], o[a][t][3]);
+          }
+        }
+        __syncthreads();
+        if (warp < h) {
+          const float4* from = mo + warp * kQ8 * kTiles * 32 + lane;
+#pragma unroll
+          for (int a = 0; a < kQ8; ++a) {
+            const float4 y = mml[(warp * kQ8 + a) * 32 + lane];
+            float f0[2], f1[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float mk = k ? y.y : y.x, lk = k ? y.w : y.z, m2 = fmaxf(m[a][k], mk), off = m2 == -INFINITY ? 0.f : m2;
+              f0[k] = ex2_approx(m[a][k] - off);
+              f1[k] = ex2_approx(mk - off);
+              l[a][k] = l[a][k] * f0[k] + lk * f1[k];
+              m[a][k] = m2;
+            }
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              const float4 x = from[(a * kTiles + t) * 32];
+              o[a][t][0] = o[a][t][0] * f0[0] + x.x * f1[0];
+              o[a][t][1] = o[a][t][1] * f0[1] + x.y * f1[1];
+              o[a][t][2] = o[a][t][2] * f0[0] + x.z * f1[0];
+              o[a][t][3] = o[a][t][3] * f0[1] + x.w * f1[1];
+            }
+          }
+        }
+        __syncthreads();
+      }
+      // ---- out: rows through shared memory, then 16 bytes a thread
+      constexpr int kPitch = D + 4;
+      float* rows = reinterpret_cast<float*>(mo);
+      if (warp == 0) {
+#pragma unroll
+        for (int a = 0; a < kQ8; ++a) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int row = a * 8 + 2 * c + k;
+            const float lk = l[a][k], f = flags & kWhole ? (lk == 0.f ? 0.f : 1.f / lk) : 1.f;
+            const bool none = lk == 0.f;  // no visible key: zero, whatever O holds
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+              const int d0 = kE4M3 ? (t >> 3) * 128 + g * 16 + (t & 7) * 2 : t * 16 + g, d1 = kE4M3 ? d0 + 1 : d0 + 8;
+              rows[row * kPitch + d0] = none ? 0.f : o[a][t][k] * f;
+              rows[row * kPitch + d1] = none ? 0.f : o[a][t][2 + k] * f;
+            }
+            if (!(flags & kWhole) && g == 0 && row < p.G) p.ml[(long)part * 256 + row] = make_float2(m[a][k], lk);
+          }
+        }
+        if (!(flags & kWhole) && lane == 0)
+          p.desc[part] = make_int4(row0, 1, hk, kPart | (flags & kEndsTile ? kPartLast : 0));
+      }
+      __syncthreads();
+      for (int i = tid; i < p.G * (D / 8); i += C::kThreads) {
+        const int row = i / (D / 8), d = i % (D / 8) * 8;
+        const float4 x = *reinterpret_cast<const float4*>(rows + row * kPitch + d),
+                     y = *reinterpret_cast<const float4*>(rows + row * kPitch + d + 4);
+        if (flags & kWhole) {
+          float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          const long h = hk * p.G + row;
+          if (p.z.p) {
+            const uint4 zz = __ldg(reinterpret_cast<const uint4*>(p.z.p + row0 * p.z.token + h * p.z.head + d));
+            const uint32_t zr[4] = {zz.x, zz.y, zz.z, zz.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[2 * k] *= sigmoid_fast(__uint_as_float(zr[k] << 16));
+              v[2 * k + 1] *= sigmoid_fast(__uint_as_float(zr[k] & 0xFFFF0000u));
+            }
+          }
+          *reinterpret_cast<uint4*>(p.out + ((long)row0 * p.Hq + h) * D + d) =
+              make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
+        } else {
+          float4* to = p.part + (long)part * (kPartBytes / sizeof(float4)) + (row * D + d) / 4;
+          to[0] = x;
+          to[1] = y;
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (dead)  // copies in flight land before the CTA ends
+    for (int i = 0; i < kSlots; ++i) mbar_wait(bar + 8 * i, i >= bad_slot ? bad_pass : bad_pass ^ 1, kWaitLimit);
+}
+
+template <int D, bool kE4M3, int kQ8>
+cudaError_t launch_one(const LaunchEnv& env, const AttnParams& p, int ctas) {
+  using C = DCfg<D, kE4M3, kQ8>;
+  static int done[64] = {0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(attn_decode_kernel<D, kE4M3, kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = 1;
+  }
+  attn_decode_kernel<D, kE4M3, kQ8><<<ctas, C::kThreads, C::kSmem, env.stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, bool kE4M3>
+cudaError_t launch_rows(const LaunchEnv& env, const AttnParams& p, int ctas) {
+  return p.G <= 8 ? launch_one<D, kE4M3, 1>(env, p, ctas) : launch_one<D, kE4M3, 2>(env, p, ctas);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const LaunchEnv& env, AttnParams& p, int D, int ctas) {
+  const uint64_t rows = ((uint64_t)p.cache.num_pages * p.Hkv) << p.cache.page_shift;
+  cudaError_t e;
+  if (p.cache.e4m3) {
+    e = encode_u8_2d_sw128(&p.tmap_k, p.cache.k, D, rows, D, 128, kGroup);
+    if (e == cudaSuccess) e = encode_u8_2d_sw128(&p.tmap_v, p.cache.v, D, rows, D, 128, kGroup);
+  } else {
+    e = encode_bf16_2d_sw128(&p.tmap_k, p.cache.k, D, rows, (uint64_t)D * 2, 64, kGroup);
+    if (e == cudaSuccess) e = encode_bf16_2d_sw128(&p.tmap_v, p.cache.v, D, rows, (uint64_t)D * 2, 64, kGroup);
+  }
+  if (e != cudaSuccess) return e;
+  if (p.cache.e4m3) return D == 128 ? launch_rows<128, true>(env, p, ctas) : launch_rows<256, true>(env, p, ctas);
+  return D == 128 ? launch_rows<128, false>(env, p, ctas) : launch_rows<256, false>(env, p, ctas);
+}
+
+}  // namespace gdn

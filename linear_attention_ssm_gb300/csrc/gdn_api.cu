@@ -740,6 +740,8 @@ gdn_status check_paged_cache(const gdn_kv_cache* c, const int32_t* block_table, 
   GDN_REQUIRE(c->v, "cache v");
   if (c->type == GDN_CACHE_E4M3 && (!c->k_scale || !c->v_scale))
     return fail(GDN_ERR_INVALID_ARGUMENT, "k_scale or v_scale is NULL");
+  if (c->type == GDN_CACHE_E4M3 && !(aligned16(c->k_scale) && aligned16(c->v_scale)))
+    return fail(GDN_ERR_MISALIGNED, "k_scale or v_scale is not 16-byte aligned");
   if (!block_table) return fail(GDN_ERR_INVALID_ARGUMENT, "block_table is NULL");
   if (reinterpret_cast<uintptr_t>(block_table) & 3u)
     return fail(GDN_ERR_MISALIGNED, "block_table is not 4-byte aligned");
