@@ -1,13 +1,13 @@
 // attn_decode.cu -- softmax attention of one new token of each sequence over its paged cache.
 //
 // A key head's at most 16 query rows do not fill a tcgen05 tile, and every cached byte is used once: HBM
-// bounds the kernel, so it is built to keep copies in flight and to finish a key quickly.  The keys of a
-// segment go round the CTA's warps 16 at a time.  A warp's groups arrive by TMA in a ring of its own, and
-// it takes them through both products with mma.sync (m16n8k16), transposed so that keys and values fill
-// the 16 rows and the query rows the 8 columns:
+// bounds the kernel, so it is built to keep copies in flight and to finish a key quickly.  One warp loads
+// keys and values by TMA into a ring of 32 KB stages (192 KB in flight on every SM); the others take a
+// stage's keys 16 at a time through both products with mma.sync (m16n8k16), transposed so that keys and
+// values fill the 16 rows and the query rows the 8 columns:
 //   S^T [16 keys x q] = K Q^T,   p = 2^(S - m),   O^T [D x q] += V^T P^T
-// with its own running m, l and O in registers: no barrier between the warps until the segment ends,
-// where they are joined pairwise.  (Work is cut into one piece for each SM as in the tile kernel.)
+// Each warp has its own running m, l and O in registers, so that the warps meet only where a segment
+// ends; there they are joined pairwise.  (Work is cut into one piece for each SM as in the tile kernel.)
 //
 // An e4m3 cache is widened between shared memory and the registers, two codes an instruction, to
 // binary16, which holds every code exactly.  The queries become binary16 too, each row divided by the
@@ -28,37 +28,41 @@ constexpr float kWeight = 7.f;   // log2 of the factor on binary16 weights
 
 template <int D, bool kE4M3, int kQ8>  // kQ8: columns of 8 query rows
 struct DCfg {
-  // A warp's ring needs three groups to cover HBM's latency; at D = 256 in bf16 (16 KB a group) shared
-  // memory holds that for four warps, which is enough for the bandwidth.
-  static constexpr int kWarps = !kE4M3 && D == 256 ? 4 : 8;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kRow = D * (kE4M3 ? 1 : 2);  // bytes of a key
-  static constexpr int kBoxes = kRow / 128;         // 128-byte columns of a group, [16 rows][128 bytes] swizzled
-  static constexpr int kHalf = kGroup * kRow;       // a group's keys, then its values
-  static constexpr int kTiles = D / 16;             // of O^T
+  static constexpr int kRow = D * (kE4M3 ? 1 : 2);    // bytes of a key
+  static constexpr int kBoxes = kRow / 128;           // 128-byte columns of a stage, [keys][128 bytes] swizzled
+  static constexpr int kKeys = 32768 / (2 * kRow);    // keys of a stage: 32 (bf16, D = 256) to 128 (e4m3, D = 128)
+  static constexpr int kHalf = kKeys * kRow;          // a stage's keys, then its values
+  // Warps that compute, 16 keys each; where a stage has fewer groups than that, its groups go to the
+  // warps in turn.  The fastest rows (128 bytes) want 16 warps.
+  static constexpr int kWarps = kE4M3 && D == 128 && kQ8 == 1 ? 16 : 8;
+  static constexpr int kGroups = kKeys / kGroup, kSets = kWarps / kGroups;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kTiles = D / 16;               // of O^T
   static constexpr int kMergeO = kWarps / 2 * kQ8 * 8 * D * 4, kMergeMl = kWarps / 2 * 32 * kQ8 * 16;
-  static constexpr int kFixed = kMergeO + kMergeMl + 1024 + 1024;  // and scan, start; alignment of the base
-  static constexpr int kPerSlot = 2 * kHalf + 32 + 32 + 8;         // ring, meta, scales, barrier
-  static constexpr int kFit = (232448 - kFixed) / (kWarps * kPerSlot);
-  static constexpr int kSlots = kFit < 8 ? kFit : 8;
-  static_assert(kSlots >= 2, "a ring of two groups at least");
-  static constexpr int kOffMerge = kWarps * kSlots * 2 * kHalf;
+  static constexpr int kQBytes = 2 * kQ8 * 8 * D * 2;  // two segments' queries
+  static constexpr int kScale = kE4M3 ? 2 * kKeys : 0;
+  static constexpr int kFixed = kMergeO + kMergeMl + kQBytes + 1024 + 1024;
+  static constexpr int kFit = (232448 - kFixed) / (2 * kHalf + 64 + kScale);
+  static constexpr int kSlots = kFit < 6 ? kFit : 6;
+  static_assert(kSlots >= 3, "stages to hide HBM's latency");
+  static constexpr int kOffMerge = kSlots * 2 * kHalf;
   static constexpr int kOffMl = kOffMerge + kMergeO;
-  static constexpr int kOffMeta = kOffMl + kMergeMl;
-  static constexpr int kOffScale = kOffMeta + kWarps * kSlots * 32;
-  static constexpr int kOffBar = kOffScale + kWarps * kSlots * 32;
-  static constexpr int kOffScan = kOffBar + kWarps * kSlots * 8;
+  static constexpr int kOffQ = kOffMl + kMergeMl;
+  static constexpr int kOffScale = kOffQ + kQBytes;
+  static constexpr int kOffMeta = kOffScale + kSlots * kScale;
+  static constexpr int kOffBar = kOffMeta + kSlots * 32;
+  static constexpr int kOffScan = kOffBar + 256;
   static constexpr int kSmem = kOffScan + 512 + 1024;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
-// What a slot of the ring holds.
-struct Group {
-  int key0, n;    // first key; keys, 0: none (a segment with fewer groups than warps)
+// What a stage holds.
+struct Stage {
+  int n;          // keys, 0: none (a segment whose token sees no key)
   int flags;
   int row0, hk;   // packed row, key head
   int part;       // slot of the segment's part in the workspace
-  int pad[2];
+  int pad[3];
 };
 enum : int { kFirst = 1, kLastOfSegment = 2, kEnd = 4, kWhole = 8, kEndsTile = 16 };
 
@@ -107,119 +111,153 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  uint8_t* ring = sm + warp * kSlots * 2 * C::kHalf;
-  Group* groups = reinterpret_cast<Group*>(sm + C::kOffMeta) + warp * kSlots;
-  uint8_t* scales = sm + C::kOffScale + warp * kSlots * 32;
-  const uint32_t ring_s = smem_u32(ring), scale_s = smem_u32(scales);
-  const uint32_t bar = smem_u32(sm + C::kOffBar) + warp * kSlots * 8;
+  Stage* stages = reinterpret_cast<Stage*>(sm + C::kOffMeta);
+  const uint32_t ring_s = smem_u32(sm);
+  const uint32_t full = smem_u32(sm + C::kOffBar), empty = full + 8 * kSlots, q_empty = empty + 8 * kSlots,
+                 meet = q_empty + 16;
   long* scan = reinterpret_cast<long*>(sm + C::kOffScan);
-  WalkStart* start = reinterpret_cast<WalkStart*>(scan + 16);
-  if (lane == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(bar + 8 * i, 1);
-    fence_mbar_init();
-    if (warp == 0) {
-      prefetch_tensormap(&p.tmap_k);
-      prefetch_tensormap(&p.tmap_v);
-      start->left = 0;
-      p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
-      p.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+  WalkStart* start = reinterpret_cast<WalkStart*>(scan + 20);
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, kWarps);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(q_empty + 8 * i, kWarps);
+    mbar_init(meet, kWarps);
+    fence_mbar_init();
+    prefetch_tensormap(&p.tmap_k);
+    prefetch_tensormap(&p.tmap_v);
+    start->left = 0;
+    p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+    p.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
   }
   find_start<C::kThreads>(p, 1, scan, start);
   __syncthreads();
-  Walk walk;
-  walk.left = start->left;
-  if (walk.left == 0) return;
-  walk.n = start->n;
-  walk.hk = start->hk;
-  walk.tile = start->tile;
-  walk.j = start->j;
-  walk.load(p, 1);
+  if (start->left == 0) return;
 
-  // ---- the loading side: the warp's next group into a slot
-  Segment seg = {};
-  bool dead = false;                      // a wait ran out
-  bool open = false;                      // a segment has groups left for this warp
-  int gi = 0, ng = 0, base = 0, lim = 0;  // next group, groups, first key, end of the segment
-  int id = 0;                             // page of group gi
-  auto page_id = [&](int key) {
-    return (int)__ldg(p.cache.table + (long)seg.n * p.cache.max_pages + (key >> p.cache.page_shift));
-  };
-  auto issue = [&](int slot) {
-    Group* m = groups + slot;
-    int flags = 0;
-    if (!open) {
-      if (!walk.next(p, 1, seg)) {
-        if (lane == 0) m->flags = kEnd;
-        return;
+  if (warp == kWarps) {
+    // ------------------------------------------------------------------ loading
+    Walk walk;
+    walk.left = start->left;
+    walk.n = start->n;
+    walk.hk = start->hk;
+    walk.tile = start->tile;
+    walk.j = start->j;
+    walk.load(p, 1);
+    const int shift = p.cache.page_shift, rows_shift = min(min(shift, 6), C::kKeys == 32 ? 5 : 6), rows = 1 << rows_shift;
+    Segment seg = {};
+    bool ok = true;
+    int slot = 0, pass = 0, used = 0, segs = 0;
+    auto await = [&](uint32_t b, uint32_t parity) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(b, parity, kWaitLimit))) {
+        raise_error(p.err, kErrTimeout);
+        ok = false;
       }
-      open = true;
-      flags = kFirst;
-      base = seg.j0 * kBlock;
-      lim = min(seg.keys, seg.j1 * kBlock);
-      ng = lim > base ? (lim - base + kGroup - 1) / kGroup : 0;
-      gi = warp;
-      if (gi < ng) id = page_id(base + gi * kGroup);
-    }
-    const int key0 = base + gi * kGroup, n = gi < ng && !dead ? min(kGroup, lim - key0) : 0;
-    if (gi + kWarps >= ng) {
-      flags |= kLastOfSegment;
-      open = false;
-    }
-    if (seg.j0 == 0 && seg.j1 == seg.nb) flags |= kWhole;
-    if (seg.j1 == seg.nb) flags |= kEndsTile;
-    if (n > 0 && (unsigned)id >= (unsigned)p.cache.num_pages) {
-      raise_error(p.err, kErrDeviceArgument);
-      id = 0;
-    }
-    if (lane == 0) {
-      *reinterpret_cast<int4*>(&m->key0) = make_int4(key0, n, flags, seg.row0);
-      *reinterpret_cast<int2*>(&m->hk) = make_int2(seg.hk, 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0));
-      if (n > 0) {
-        const int y = ((id * p.Hkv + seg.hk) << p.cache.page_shift) + (key0 & ((1 << p.cache.page_shift) - 1));
-        const uint32_t dst = ring_s + slot * 2 * C::kHalf;
-        mbar_arrive_expect_tx(bar + 8 * slot, 2 * C::kHalf + (kE4M3 ? 32 : 0));
-#pragma unroll
-        for (int b = 0; b < C::kBoxes; ++b) tma_load_2d(dst + b * 2048, &p.tmap_k, b * (kE4M3 ? 128 : 64), y, bar + 8 * slot);
-        if constexpr (kE4M3) {
-          bulk_load(scale_s + slot * 32, p.cache.k_scale + y, 16, bar + 8 * slot);
-          bulk_load(scale_s + slot * 32 + 16, p.cache.v_scale + y, 16, bar + 8 * slot);
+      return ok;
+    };
+    // page of this lane's rows of the stage that begins at key0
+    auto page_id = [&](int key0, int lim) {
+      const int key = key0 + (lane << rows_shift);
+      return (lane << rows_shift) < C::kKeys && key < lim
+                 ? (int)__ldg(p.cache.table + (long)seg.n * p.cache.max_pages + (key >> shift))
+                 : -1;
+    };
+    while (ok && walk.next(p, 1, seg)) {
+      const int first = seg.j0 * kBlock, lim = min(seg.keys, seg.j1 * kBlock);
+      const int mark = (seg.j0 == 0 && seg.j1 == seg.nb ? kWhole : 0) | (seg.j1 == seg.nb ? kEndsTile : 0);
+      const uint32_t q_bytes = p.G * D * 2;
+      int id = page_id(first, lim);
+      for (int key0 = first; key0 == first || key0 < lim; key0 += C::kKeys) {
+        if (!await(empty + 8 * slot, pass ^ 1)) break;
+        if (key0 == first && !await(q_empty + 8 * (segs & 1), (segs >> 1 & 1) ^ 1)) break;
+        const int n = min(max(lim - key0, 0), C::kKeys);
+        const bool mine = (lane << rows_shift) < n;
+        if (mine && (unsigned)id >= (unsigned)p.cache.num_pages) {
+          raise_error(p.err, kErrDeviceArgument);
+          id = 0;
         }
+        const int y = mine ? ((id * p.Hkv + seg.hk) << shift) + ((key0 + (lane << rows_shift)) & ((1 << shift) - 1)) : 0;
+        const uint32_t bar = full + 8 * slot, dst = ring_s + slot * 2 * C::kHalf + (uint32_t)(lane << rows_shift) * 128;
+        if (lane == 0) {
+          const int pieces = (n + rows - 1) >> rows_shift;
+          *reinterpret_cast<int4*>(&stages[slot]) =
+              make_int4(n, mark | (key0 == first ? kFirst : 0) | (key0 + C::kKeys >= lim ? kLastOfSegment : 0), seg.row0, seg.hk);
+          stages[slot].part = 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0);
+          mbar_arrive_expect_tx(bar, pieces * rows * (2 * C::kRow + (kE4M3 ? 2 : 0)) + (key0 == first ? q_bytes : 0));
+          if (key0 == first)
+            bulk_load(ring_s + C::kOffQ + (segs & 1) * (C::kQBytes / 2), p.q + ((long)seg.row0 * p.Hq + seg.hk * p.G) * D, q_bytes, bar);
+        }
+        __syncwarp();
+        if (mine) {
 #pragma unroll
-        for (int b = 0; b < C::kBoxes; ++b)
-          tma_load_2d(dst + C::kHalf + b * 2048, &p.tmap_v, b * (kE4M3 ? 128 : 64), y, bar + 8 * slot);
-      } else if (!dead) {
-        mbar_arrive(bar + 8 * slot);
+          for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_2d(dst + b * C::kKeys * 128, &p.tmap_k, b * (kE4M3 ? 128 : 64), y, bar);
+          if constexpr (kE4M3) {
+            const uint32_t sc = ring_s + C::kOffScale + slot * C::kScale + (lane << rows_shift);
+            bulk_load(sc, p.cache.k_scale + y, rows, bar);
+            bulk_load(sc + C::kKeys, p.cache.v_scale + y, rows, bar);
+          }
+#pragma unroll
+          for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_2d(dst + C::kHalf + b * C::kKeys * 128, &p.tmap_v, b * (kE4M3 ? 128 : 64), y, bar);
+        }
+        used |= 1 << slot;
+        if (key0 + C::kKeys < lim) id = page_id(key0 + C::kKeys, lim);  // its latency passes in the next wait
+        if (++slot == kSlots) {
+          slot = 0;
+          pass ^= 1;
+        }
       }
+      ++segs;
     }
-    gi += kWarps;
-    if (open) id = page_id(base + gi * kGroup);  // for the next call: its latency passes meanwhile
-  };
-  for (int i = 0; i < kSlots; ++i) issue(i);
-  __syncwarp();
+    if (ok && await(empty + 8 * slot, pass ^ 1)) {
+      if (lane == 0) {
+        stages[slot].flags = kEnd;
+        mbar_arrive(full + 8 * slot);
+      }
+    } else {  // copies in flight land before the CTA ends
+      for (int i = 0; i < kSlots; ++i)
+        if (used >> i & 1) mbar_wait(full + 8 * i, i < slot ? pass : pass ^ 1, kWaitLimit);
+    }
+    return;
+  }
 
-  // ---- the computing side
+  // ------------------------------------------------------------------ computing
+  // The computing warps' barrier: bounded like every wait here, so that a warp that gave up holds nobody.
+  uint32_t sync_par = 0;
+  bool ok = true;
+  const auto warps_sync = [&] {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(meet);
+    if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait(meet, sync_par, kWaitLimit))) {
+      raise_error(p.err, kErrTimeout);
+      ok = false;
+    }
+    sync_par ^= 1u;
+  };
   uint32_t q[kQ8][D / 8];        // Q^T fragments of the segment's key head
   float qs[kQ8][2];              // log2 units of a score, for this lane's two query rows
   float o[kQ8][kTiles][4];       // O^T: rows d, columns the two query rows
   float m[kQ8][2], l[kQ8][2], r[kQ8][2];
-  int bad_slot = 0, bad_pass = 0;
-  for (int slot = 0, pass = 0;; pass ^= (slot == kSlots - 1), slot = slot == kSlots - 1 ? 0 : slot + 1) {
-    const int4 ga = *reinterpret_cast<const int4*>(&groups[slot].key0);
-    const int key0 = ga.x, n = ga.y, flags = ga.z, row0 = ga.w;
+  int turn = 0, segs = 0;        // whose stage this is; segments begun
+  for (int slot = 0, pass = 0; ok; pass ^= (slot == kSlots - 1), slot = slot == kSlots - 1 ? 0 : slot + 1) {
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(full + 8 * slot, pass, kWaitLimit))) {
+      raise_error(p.err, kErrTimeout);
+      break;
+    }
+    const int4 ga = *reinterpret_cast<const int4*>(&stages[slot]);
+    const int all = ga.x, flags = ga.y, row0 = ga.z, hk = ga.w, part = stages[slot].part;
     if (flags & kEnd) break;
-    const int2 gb = *reinterpret_cast<const int2*>(&groups[slot].hk);
-    const int hk = gb.x, part = gb.y;
     if (flags & kFirst) {
 #pragma unroll
       for (int a = 0; a < kQ8; ++a) {
         const int row = a * 8 + g;
-        const uint16_t* src = p.q + ((long)row0 * p.Hq + hk * p.G + row) * D;
+        const uint8_t* src = sm + C::kOffQ + (segs & 1) * (C::kQBytes / 2) + row * D * 2;
         if constexpr (!kE4M3) {
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) {  // 64-value column x / 2, its 16-byte piece 2 c + x % 2
             uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < p.G) v = __ldg(reinterpret_cast<const uint4*>(src + (x >> 1) * 64 + (2 * c + (x & 1)) * 8));
+            if (row < p.G) v = *reinterpret_cast<const uint4*>(src + (x >> 1) * 128 + (2 * c + (x & 1)) * 16);
             q[a][4 * x] = v.x;
             q[a][4 * x + 1] = v.y;
             q[a][4 * x + 2] = v.z;
@@ -232,9 +270,9 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
           for (int x = 0; x < D / 64; ++x) {  // 128-value column x / 2, its 16-value piece 2 c + x % 2
             uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
             if (row < p.G) {
-              const uint4* s = reinterpret_cast<const uint4*>(src + (x >> 1) * 128 + (2 * c + (x & 1)) * 16);
-              v[0] = __ldg(s);
-              v[1] = __ldg(s + 1);
+              const uint4* s = reinterpret_cast<const uint4*>(src + (x >> 1) * 256 + (2 * c + (x & 1)) * 32);
+              v[0] = s[0];
+              v[1] = s[1];
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -270,20 +308,19 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[a][t][i] = 0.f;
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_empty + 8 * (segs & 1));
+      ++segs;
     }
-    if (!dead && !__all_sync(0xFFFFFFFFu, mbar_wait(bar + 8 * slot, pass, kWaitLimit))) {
-      // nothing more is loaded or waited for; the walk goes on, for the other warps' barriers
-      raise_error(p.err, kErrTimeout);
-      dead = true;
-      bad_slot = slot;
-      bad_pass = pass;
-    }
-    if (n > 0 && !dead) {
-      const uint32_t ks = ring_s + slot * 2 * C::kHalf, vs = ks + C::kHalf;
+    // this warp's group of the stage, if it has one
+    const int group = warp % C::kGroups, n = warp / C::kGroups == turn ? min(max(all - group * kGroup, 0), kGroup) : 0;
+    if (++turn == C::kSets) turn = 0;
+    if (n > 0) {
+      const uint32_t ks = ring_s + slot * 2 * C::kHalf + group * kGroup * 128, vs = ks + C::kHalf;
       if (n < kGroup) {  // value rows behind the last key may hold anything, and 0 * NaN is not 0
         for (int i = lane; i < (kGroup - n) * 8 * C::kBoxes; i += 32) {
           const int b = i / ((kGroup - n) * 8), x = i % ((kGroup - n) * 8);
-          *reinterpret_cast<uint4*>(ring + slot * 2 * C::kHalf + C::kHalf + b * 2048 + n * 128 + x * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(sm + (vs - ring_s) + b * C::kKeys * 128 + n * 128 + x * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -296,7 +333,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
         for (int i = 0; i < 4; ++i) s[a][0][i] = s[a][1][i] = 0.f;
 #pragma unroll
       for (int x = 0; x < 2 * C::kBoxes; ++x) {  // column x / 2, 16-byte piece 2 c + x % 2 of rows g and g + 8
-        const uint32_t at = ks + (x >> 1) * 2048 + g * 128 + (((2 * c + (x & 1)) ^ g) << 4);
+        const uint32_t at = ks + (x >> 1) * C::kKeys * 128 + g * 128 + (((2 * c + (x & 1)) ^ g) << 4);
         const uint4 u = lds128(at), w = lds128(at + 1024);
         if constexpr (!kE4M3) {
 #pragma unroll
@@ -319,12 +356,12 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
       // keys g and g + 8: their scales
       float kf[2] = {1.f, 1.f}, vf[2] = {1.f, 1.f}, ev = 0.f;
       if constexpr (kE4M3) {
-        const uint8_t* sc = scales + slot * 32;
+        const uint8_t* sc = sm + C::kOffScale + slot * C::kScale + group * kGroup;
         uint32_t vb[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           kf[i] = e8m0_value(sc[g + 8 * i]);
-          vb[i] = g + 8 * i < n ? sc[16 + g + 8 * i] : 0u;
+          vb[i] = g + 8 * i < n ? sc[C::kKeys + g + 8 * i] : 0u;
         }
         const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(vb[0], vb[1]));
         ev = (float)((int)top - 127);
@@ -399,7 +436,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
         for (int t = 0; t < kTiles; ++t) {
           const int piece = 2 * t + half;
           uint32_t v[4];
-          ldmatrix_x4_trans(vs + (piece >> 3) * 2048 + key * 128 + (((piece & 7) ^ (key & 7)) << 4), v);
+          ldmatrix_x4_trans(vs + (piece >> 3) * C::kKeys * 128 + key * 128 + (((piece & 7) ^ (key & 7)) << 4), v);
 #pragma unroll
           for (int a = 0; a < kQ8; ++a) mma16816<false>(o[a][t], v[0], v[1], v[2], v[3], pb[a][0], pb[a][1]);
         }
@@ -412,7 +449,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = 2 * c + (i & 1) + 8 * (i >> 1);
-            const uint4 x = lds128(vs + b * 2048 + key * 128 + ((g ^ (key & 7)) << 4));
+            const uint4 x = lds128(vs + b * C::kKeys * 128 + key * 128 + ((g ^ (key & 7)) << 4));
             v[i][0] = x.x;
             v[i][1] = x.y;
             v[i][2] = x.z;
@@ -431,8 +468,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
       }
     }
     __syncwarp();
-    issue(slot);
-    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + 8 * slot);
     if (flags & kLastOfSegment) {
       // ---- the warps' shares, joined pairwise
       float4* mo = reinterpret_cast<float4*>(sm + C::kOffMerge);
@@ -463,7 +499,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
             for (int t = 0; t < kTiles; ++t) to[(a * kTiles + t) * 32] = make_float4(o[a][t][0], o[a][t][1], o[a][t][2], o[a][t][3]);
           }
         }
-        __syncthreads();
+        warps_sync();
         if (warp < h) {
           const float4* from = mo + warp * kQ8 * kTiles * 32 + lane;
 #pragma unroll
@@ -488,7 +524,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
             }
           }
         }
-        __syncthreads();
+        warps_sync();
       }
       // ---- out: rows through shared memory, then 16 bytes a thread
       constexpr int kPitch = D + 4;
@@ -513,8 +549,8 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
         if (!(flags & kWhole) && lane == 0)
           p.desc[part] = make_int4(row0, 1, hk, kPart | (flags & kEndsTile ? kPartLast : 0));
       }
-      __syncthreads();
-      for (int i = tid; i < p.G * (D / 8); i += C::kThreads) {
+      warps_sync();
+      for (int i = tid; i < p.G * (D / 8); i += 32 * kWarps) {
         const int row = i / (D / 8), d = i % (D / 8) * 8;
         const float4 x = *reinterpret_cast<const float4*>(rows + row * kPitch + d),
                      y = *reinterpret_cast<const float4*>(rows + row * kPitch + d + 4);
@@ -538,11 +574,9 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
           to[1] = y;
         }
       }
-      __syncthreads();
+      warps_sync();
     }
   }
-  if (dead)  // copies in flight land before the CTA ends
-    for (int i = 0; i < kSlots; ++i) mbar_wait(bar + 8 * i, i >= bad_slot ? bad_pass : bad_pass ^ 1, kWaitLimit);
 }
 
 template <int D, bool kE4M3, int kQ8>
@@ -570,13 +604,15 @@ cudaError_t launch_rows(const LaunchEnv& env, const AttnParams& p, int ctas) {
 
 cudaError_t launch_attn_decode(const LaunchEnv& env, AttnParams& p, int D, int ctas) {
   const uint64_t rows = ((uint64_t)p.cache.num_pages * p.Hkv) << p.cache.page_shift;
+  // rows of one copy: a page's, at most 64 and a stage's keys (32 for bf16 at D = 256)
+  const int page = 1 << p.cache.page_shift, most = !p.cache.e4m3 && D == 256 ? 32 : 64, box = page < most ? page : most;
   cudaError_t e;
   if (p.cache.e4m3) {
-    e = encode_u8_2d_sw128(&p.tmap_k, p.cache.k, D, rows, D, 128, kGroup);
-    if (e == cudaSuccess) e = encode_u8_2d_sw128(&p.tmap_v, p.cache.v, D, rows, D, 128, kGroup);
+    e = encode_u8_2d_sw128(&p.tmap_k, p.cache.k, D, rows, D, 128, box);
+    if (e == cudaSuccess) e = encode_u8_2d_sw128(&p.tmap_v, p.cache.v, D, rows, D, 128, box);
   } else {
-    e = encode_bf16_2d_sw128(&p.tmap_k, p.cache.k, D, rows, (uint64_t)D * 2, 64, kGroup);
-    if (e == cudaSuccess) e = encode_bf16_2d_sw128(&p.tmap_v, p.cache.v, D, rows, (uint64_t)D * 2, 64, kGroup);
+    e = encode_bf16_2d_sw128(&p.tmap_k, p.cache.k, D, rows, (uint64_t)D * 2, 64, box);
+    if (e == cudaSuccess) e = encode_bf16_2d_sw128(&p.tmap_v, p.cache.v, D, rows, (uint64_t)D * 2, 64, box);
   }
   if (e != cudaSuccess) return e;
   if (p.cache.e4m3) return D == 128 ? launch_rows<128, true>(env, p, ctas) : launch_rows<256, true>(env, p, ctas);
