@@ -2,7 +2,7 @@
 //
 // A key head's at most 16 query rows do not fill a tcgen05 tile, and every cached byte is used once: HBM
 // bounds the kernel, so it is built to keep copies in flight and to finish a key quickly.  One warp loads
-// keys and values by TMA into a ring of 32 KB stages (192 KB in flight on every SM); the others take a
+// keys and one values by TMA into a ring of 32 KB stages (192 KB in flight on every SM); the others take a
 // stage's keys 16 at a time through both products with mma.sync (m16n8k16), transposed so that keys and
 // values fill the 16 rows and the query rows the 8 columns:
 //   S^T [16 keys x q] = K Q^T,   p = 2^(S - m),   O^T [D x q] += V^T P^T
@@ -23,7 +23,6 @@
 namespace gdn {
 namespace {
 
-constexpr int kGroup = 16;       // keys of a group: the rows of one mma
 constexpr float kWeight = 7.f;   // log2 of the factor on binary16 weights
 
 template <int D, bool kE4M3, int kQ8>  // kQ8: columns of 8 query rows
@@ -32,11 +31,12 @@ struct DCfg {
   static constexpr int kBoxes = kRow / 128;           // 128-byte columns of a stage, [keys][128 bytes] swizzled
   static constexpr int kKeys = 32768 / (2 * kRow);    // keys of a stage: 32 (bf16, D = 256) to 128 (e4m3, D = 128)
   static constexpr int kHalf = kKeys * kRow;          // a stage's keys, then its values
-  // Warps that compute, 16 keys each; where a stage has fewer groups than that, its groups go to the
-  // warps in turn.  The fastest rows (128 bytes) want 16 warps.
-  static constexpr int kWarps = kE4M3 && D == 128 && kQ8 == 1 ? 16 : 8;
+  // Warps that compute, a group of keys each; where a stage has fewer groups than warps, the stages go to
+  // sets of warps in turn.  A group is two mma tiles of 16 keys where registers allow and a stage has them.
+  static constexpr int kWarps = 8;
+  static constexpr int kTwo = kQ8 == 1 && kKeys >= 64 ? 2 : 1, kGroup = 16 * kTwo;
   static constexpr int kGroups = kKeys / kGroup, kSets = kWarps / kGroups;
-  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kThreads = 32 * (kWarps + 2);  // and one that loads the keys, one the values
   static constexpr int kTiles = D / 16;               // of O^T
   static constexpr int kMergeO = kWarps / 2 * kQ8 * 8 * D * 4, kMergeMl = kWarps / 2 * 32 * kQ8 * 16;
   static constexpr int kQBytes = 2 * kQ8 * 8 * D * 2;  // two segments' queries
@@ -89,14 +89,26 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// two e4m3 codes -> two binary16 values
-__device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t v) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((uint16_t)v, __NV_E4M3);
-  return (uint32_t)h.x | (uint32_t)h.y << 16;
+// four e4m3 codes -> two pairs of binary16 values, low codes first
+__device__ __forceinline__ uint2 e4m3x4_to_half4(uint32_t v) {
+  uint2 r;
+  asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\n"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\ncvt.rn.f16x2.e4m3x2 %1, hi;\n}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(v));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// this thread's arrival on the barrier once its cp.async copies so far have landed (the barrier's count
+// includes it)
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -107,7 +119,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
 template <int D, bool kE4M3, int kQ8>
 __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_kernel(const __grid_constant__ AttnParams p) {
   using C = DCfg<D, kE4M3, kQ8>;
-  constexpr int kWarps = C::kWarps, kSlots = C::kSlots, kTiles = C::kTiles;
+  constexpr int kWarps = C::kWarps, kSlots = C::kSlots, kTiles = C::kTiles, kTwo = C::kTwo, kGroup = C::kGroup;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = align1024(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -119,7 +131,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
   WalkStart* start = reinterpret_cast<WalkStart*>(scan + 20);
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(full + 8 * i, 1);
+      mbar_init(full + 8 * i, kE4M3 ? 2 + 64 : 2);  // both loading warps; their lanes' copies of the scales
       mbar_init(empty + 8 * i, kWarps);
     }
     for (int i = 0; i < 2; ++i) mbar_init(q_empty + 8 * i, kWarps);
@@ -135,8 +147,9 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
   __syncthreads();
   if (start->left == 0) return;
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------------ loading
+  if (warp >= kWarps) {
+    // ------------------------------------------------------------------ loading: keys, or values
+    const bool keys = warp == kWarps;
     Walk walk;
     walk.left = start->left;
     walk.n = start->n;
@@ -144,7 +157,10 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
     walk.tile = start->tile;
     walk.j = start->j;
     walk.load(p, 1);
-    const int shift = p.cache.page_shift, rows_shift = min(min(shift, 6), C::kKeys == 32 ? 5 : 6), rows = 1 << rows_shift;
+    const int shift = p.cache.page_shift, rows_shift = min(shift, C::kKeys == 32 ? 5 : 6), rows = 1 << rows_shift;
+    const CUtensorMap* map = keys ? &p.tmap_k : &p.tmap_v;
+    const uint8_t* scale = keys ? p.cache.k_scale : p.cache.v_scale;
+    const int row = lane << rows_shift;  // of the stage: this lane's first
     Segment seg = {};
     bool ok = true;
     int slot = 0, pass = 0, used = 0, segs = 0;
@@ -157,52 +173,51 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
     };
     // page of this lane's rows of the stage that begins at key0
     auto page_id = [&](int key0, int lim) {
-      const int key = key0 + (lane << rows_shift);
-      return (lane << rows_shift) < C::kKeys && key < lim
-                 ? (int)__ldg(p.cache.table + (long)seg.n * p.cache.max_pages + (key >> shift))
+      return row < C::kKeys && key0 + row < lim
+                 ? (int)__ldg(p.cache.table + (long)seg.n * p.cache.max_pages + ((key0 + row) >> shift))
                  : -1;
     };
     while (ok && walk.next(p, 1, seg)) {
       const int first = seg.j0 * kBlock, lim = min(seg.keys, seg.j1 * kBlock);
       const int mark = (seg.j0 == 0 && seg.j1 == seg.nb ? kWhole : 0) | (seg.j1 == seg.nb ? kEndsTile : 0);
-      const uint32_t q_bytes = p.G * D * 2;
       int id = page_id(first, lim);
       for (int key0 = first; key0 == first || key0 < lim; key0 += C::kKeys) {
-        if (!await(empty + 8 * slot, pass ^ 1)) break;
-        if (key0 == first && !await(q_empty + 8 * (segs & 1), (segs >> 1 & 1) ^ 1)) break;
         const int n = min(max(lim - key0, 0), C::kKeys);
-        const bool mine = (lane << rows_shift) < n;
+        const bool mine = row < n;
         if (mine && (unsigned)id >= (unsigned)p.cache.num_pages) {
           raise_error(p.err, kErrDeviceArgument);
           id = 0;
         }
-        const int y = mine ? ((id * p.Hkv + seg.hk) << shift) + ((key0 + (lane << rows_shift)) & ((1 << shift) - 1)) : 0;
-        const uint32_t bar = full + 8 * slot, dst = ring_s + slot * 2 * C::kHalf + (uint32_t)(lane << rows_shift) * 128;
+        const int y = mine ? ((id * p.Hkv + seg.hk) << shift) + ((key0 + row) & ((1 << shift) - 1)) : 0;
+        if (key0 + C::kKeys < lim) id = page_id(key0 + C::kKeys, lim);  // its latency passes in the wait
+        if (!await(empty + 8 * slot, pass ^ 1)) break;
+        if (keys && key0 == first && !await(q_empty + 8 * (segs & 1), (segs >> 1 & 1) ^ 1)) break;
+        const uint32_t bar = full + 8 * slot;
         if (lane == 0) {
-          const int pieces = (n + rows - 1) >> rows_shift;
-          *reinterpret_cast<int4*>(&stages[slot]) =
-              make_int4(n, mark | (key0 == first ? kFirst : 0) | (key0 + C::kKeys >= lim ? kLastOfSegment : 0), seg.row0, seg.hk);
-          stages[slot].part = 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0);
-          mbar_arrive_expect_tx(bar, pieces * rows * (2 * C::kRow + (kE4M3 ? 2 : 0)) + (key0 == first ? q_bytes : 0));
-          if (key0 == first)
-            bulk_load(ring_s + C::kOffQ + (segs & 1) * (C::kQBytes / 2), p.q + ((long)seg.row0 * p.Hq + seg.hk * p.G) * D, q_bytes, bar);
+          uint32_t bytes = ((n + rows - 1) >> rows_shift) * rows * C::kRow;
+          if (keys) {
+            *reinterpret_cast<int4*>(&stages[slot]) =
+                make_int4(n, mark | (key0 == first ? kFirst : 0) | (key0 + C::kKeys >= lim ? kLastOfSegment : 0), seg.row0, seg.hk);
+            stages[slot].part = 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0);
+            if (key0 == first) bytes += p.G * D * 2;
+          }
+          mbar_arrive_expect_tx(bar, bytes);
+          if (keys && key0 == first)
+            bulk_load(ring_s + C::kOffQ + (segs & 1) * (C::kQBytes / 2), p.q + ((long)seg.row0 * p.Hq + seg.hk * p.G) * D,
+                      p.G * D * 2, bar);
         }
         __syncwarp();
         if (mine) {
+          const uint32_t dst = ring_s + slot * 2 * C::kHalf + (keys ? 0 : C::kHalf) + (uint32_t)row * 128;
 #pragma unroll
-          for (int b = 0; b < C::kBoxes; ++b)
-            tma_load_2d(dst + b * C::kKeys * 128, &p.tmap_k, b * (kE4M3 ? 128 : 64), y, bar);
-          if constexpr (kE4M3) {
-            const uint32_t sc = ring_s + C::kOffScale + slot * C::kScale + (lane << rows_shift);
-            bulk_load(sc, p.cache.k_scale + y, rows, bar);
-            bulk_load(sc + C::kKeys, p.cache.v_scale + y, rows, bar);
-          }
-#pragma unroll
-          for (int b = 0; b < C::kBoxes; ++b)
-            tma_load_2d(dst + C::kHalf + b * C::kKeys * 128, &p.tmap_v, b * (kE4M3 ? 128 : 64), y, bar);
+          for (int b = 0; b < C::kBoxes; ++b) tma_load_2d(dst + b * C::kKeys * 128, map, b * (kE4M3 ? 128 : 64), y, bar);
+        }
+        if constexpr (kE4M3) {  // the rows' exponent bytes, 16 a lane
+          const int r16 = lane * 16, y16 = __shfl_sync(0xFFFFFFFFu, y, r16 >> rows_shift & 31) + (r16 & (rows - 1));
+          if (r16 < n) cp_async16(ring_s + C::kOffScale + slot * C::kScale + (keys ? 0 : C::kKeys) + r16, scale + y16);
+          cp_async_arrive(bar);
         }
         used |= 1 << slot;
-        if (key0 + C::kKeys < lim) id = page_id(key0 + C::kKeys, lim);  // its latency passes in the next wait
         if (++slot == kSlots) {
           slot = 0;
           pass ^= 1;
@@ -212,13 +227,15 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
     }
     if (ok && await(empty + 8 * slot, pass ^ 1)) {
       if (lane == 0) {
-        stages[slot].flags = kEnd;
+        if (keys) stages[slot].flags = kEnd;
         mbar_arrive(full + 8 * slot);
       }
+      if constexpr (kE4M3) cp_async_arrive(full + 8 * slot);
     } else {  // copies in flight land before the CTA ends
       for (int i = 0; i < kSlots; ++i)
         if (used >> i & 1) mbar_wait(full + 8 * i, i < slot ? pass : pass ^ 1, kWaitLimit);
     }
+    if constexpr (kE4M3) asm volatile("cp.async.wait_all;" ::: "memory");
     return;
   }
 
@@ -326,61 +343,76 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
         __syncwarp();
       }
       // S^T
-      float s[kQ8][2][4];
+      float s[kQ8][kTwo][2][4];
 #pragma unroll
       for (int a = 0; a < kQ8; ++a)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[a][0][i] = s[a][1][i] = 0.f;
+        for (int y = 0; y < kTwo; ++y)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[a][y][0][i] = s[a][y][1][i] = 0.f;
 #pragma unroll
       for (int x = 0; x < 2 * C::kBoxes; ++x) {  // column x / 2, 16-byte piece 2 c + x % 2 of rows g and g + 8
-        const uint32_t at = ks + (x >> 1) * C::kKeys * 128 + g * 128 + (((2 * c + (x & 1)) ^ g) << 4);
-        const uint4 u = lds128(at), w = lds128(at + 1024);
-        if constexpr (!kE4M3) {
 #pragma unroll
-          for (int a = 0; a < kQ8; ++a) {
-            mma16816<false>(s[a][0], u.x, w.x, u.y, w.y, q[a][4 * x], q[a][4 * x + 1]);
-            mma16816<false>(s[a][1], u.z, w.z, u.w, w.w, q[a][4 * x + 2], q[a][4 * x + 3]);
-          }
-        } else {
-          const uint32_t ur[4] = {u.x, u.y, u.z, u.w}, wr[4] = {w.x, w.y, w.z, w.w};
+        for (int y = 0; y < kTwo; ++y) {
+          const uint32_t at = ks + (x >> 1) * C::kKeys * 128 + (16 * y + g) * 128 + (((2 * c + (x & 1)) ^ g) << 4);
+          const uint4 u = lds128(at), w = lds128(at + 1024);
+          if constexpr (!kE4M3) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t a0 = e4m3x2_to_half2(ur[t] & 0xFFFFu), a1 = e4m3x2_to_half2(wr[t] & 0xFFFFu),
-                           a2 = e4m3x2_to_half2(ur[t] >> 16), a3 = e4m3x2_to_half2(wr[t] >> 16);
+            for (int a = 0; a < kQ8; ++a) {
+              mma16816<false>(s[a][y][0], u.x, w.x, u.y, w.y, q[a][4 * x], q[a][4 * x + 1]);
+              mma16816<false>(s[a][y][1], u.z, w.z, u.w, w.w, q[a][4 * x + 2], q[a][4 * x + 3]);
+            }
+          } else {
+            const uint32_t ur[4] = {u.x, u.y, u.z, u.w}, wr[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int a = 0; a < kQ8; ++a)
-              mma16816<true>(s[a][t & 1], a0, a1, a2, a3, q[a][8 * x + 2 * t], q[a][8 * x + 2 * t + 1]);
+            for (int t = 0; t < 4; ++t) {
+              const uint2 lo = e4m3x4_to_half4(ur[t]), hi = e4m3x4_to_half4(wr[t]);
+#pragma unroll
+              for (int a = 0; a < kQ8; ++a)
+                mma16816<true>(s[a][y][t & 1], lo.x, hi.x, lo.y, hi.y, q[a][8 * x + 2 * t], q[a][8 * x + 2 * t + 1]);
+            }
           }
         }
       }
-      // keys g and g + 8: their scales
-      float kf[2] = {1.f, 1.f}, vf[2] = {1.f, 1.f}, ev = 0.f;
+      // this lane's keys, 16 y + g and 16 y + g + 8: their scales
+      float kf[kTwo][2], vf[kTwo][2], ev = 0.f;
       if constexpr (kE4M3) {
         const uint8_t* sc = sm + C::kOffScale + slot * C::kScale + group * kGroup;
-        uint32_t vb[2];
+        uint32_t vb[kTwo][2], top = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          kf[i] = e8m0_value(sc[g + 8 * i]);
-          vb[i] = g + 8 * i < n ? sc[C::kKeys + g + 8 * i] : 0u;
-        }
-        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(vb[0], vb[1]));
+        for (int y = 0; y < kTwo; ++y)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int key = 16 * y + g + 8 * i;
+            kf[y][i] = e8m0_value(sc[key]);
+            vb[y][i] = key < n ? sc[C::kKeys + key] : 0u;
+            top = max(top, vb[y][i]);
+          }
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
         ev = (float)((int)top - 127);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int diff = (int)vb[i] - (int)top + (int)kWeight;  // the value's power over the group's, times 2^7
-          vf[i] = diff >= -126 ? __uint_as_float((uint32_t)(127 + diff) << 23) : 0.f;
-        }
+        for (int y = 0; y < kTwo; ++y)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int diff = (int)vb[y][i] - (int)top + (int)kWeight;  // the value's power over the group's, times 2^7
+            vf[y][i] = diff >= -126 ? __uint_as_float((uint32_t)(127 + diff) << 23) : 0.f;
+          }
       }
-      uint32_t pb[kQ8][2];
+      uint32_t pb[kQ8][kTwo][2];
 #pragma unroll
       for (int a = 0; a < kQ8; ++a) {
-        float x[2][2];  // [key g, g + 8][query row]
+        float x[kTwo][2][2];  // [key g, g + 8][query row]
+        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int y = 0; y < kTwo; ++y)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            x[i][k] = g + 8 * i < n ? (s[a][0][2 * i + k] + s[a][1][2 * i + k]) * (kE4M3 ? kf[i] : 1.f) * qs[a][k] : -INFINITY;
-        float top[2] = {fmaxf(x[0][0], x[1][0]), fmaxf(x[0][1], x[1][1])};
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float v = (s[a][y][0][2 * i + k] + s[a][y][1][2 * i + k]) * (kE4M3 ? kf[y][i] * qs[a][k] : qs[a][k]);
+              x[y][i][k] = 16 * y + g + 8 * i < n ? v : -INFINITY;
+              top[k] = fmaxf(top[k], x[y][i][k]);
+            }
         // m, and the unit r of O, are raised for the whole warp where one of its keys asks for it
         bool more = top[0] > m[a][0] + kLazy || top[1] > m[a][1] + kLazy;
         if constexpr (kE4M3) more = more || m[a][0] + ev > r[a][0] || m[a][1] + ev > r[a][1];
@@ -406,28 +438,32 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
             o[a][t][3] *= f[1];
           }
         }
-        float w[2][2];
+        // weights 2^(s - m + d), d <= 0 the distance of this group's unit from O's; cut off at -40 for l,
+        // lest a group of tiny values vanish from it
+        float off[2], back[2], rest[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float mk = m[a][k];
-          // weights 2^(s - m + d), d <= 0 the distance of this group's unit from O's; cut off at -40 for l
-          float d = 0.f, rest = 1.f;
-          if constexpr (kE4M3) {
-            const float e = mk == -INFINITY ? 0.f : mk + ev - r[a][k];
-            d = fmaxf(e, -40.f);
-            rest = e < -40.f ? ex2_approx(e - d) : 1.f;
-          }
-          const float off = mk == -INFINITY ? 0.f : d - mk;
-          w[0][k] = ex2_approx(x[0][k] + off);
-          w[1][k] = ex2_approx(x[1][k] + off);
-          l[a][k] += kE4M3 ? (w[0][k] + w[1][k]) * ex2_approx(-d) : w[0][k] + w[1][k];
-          if constexpr (kE4M3) {
-            w[0][k] *= vf[0] * rest;
-            w[1][k] *= vf[1] * rest;
-          }
+          const float mk = m[a][k], e = kE4M3 && mk > -INFINITY ? mk + ev - r[a][k] : 0.f, d = fmaxf(e, -40.f);
+          off[k] = mk > -INFINITY ? d - mk : 0.f;
+          back[k] = kE4M3 ? ex2_approx(-d) : 1.f;
+          rest[k] = e < d ? ex2_approx(e - d) : 1.f;
         }
-        pb[a][0] = transpose8x8(kE4M3 ? pack_half2(w[0][0], w[0][1]) : pack_bf2(w[0][0], w[0][1]));
-        pb[a][1] = transpose8x8(kE4M3 ? pack_half2(w[1][0], w[1][1]) : pack_bf2(w[1][0], w[1][1]));
+#pragma unroll
+        for (int y = 0; y < kTwo; ++y) {
+          float w[2][2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            w[0][k] = ex2_approx(x[y][0][k] + off[k]);
+            w[1][k] = ex2_approx(x[y][1][k] + off[k]);
+            l[a][k] = kE4M3 ? fmaf(w[0][k] + w[1][k], back[k], l[a][k]) : l[a][k] + (w[0][k] + w[1][k]);
+            if constexpr (kE4M3) {
+              w[0][k] *= vf[y][0] * rest[k];
+              w[1][k] *= vf[y][1] * rest[k];
+            }
+          }
+          pb[a][y][0] = transpose8x8(kE4M3 ? pack_half2(w[0][0], w[0][1]) : pack_bf2(w[0][0], w[0][1]));
+          pb[a][y][1] = transpose8x8(kE4M3 ? pack_half2(w[1][0], w[1][1]) : pack_bf2(w[1][0], w[1][1]));
+        }
       }
       // O^T += V^T P^T
       if constexpr (!kE4M3) {
@@ -435,34 +471,39 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           const int piece = 2 * t + half;
-          uint32_t v[4];
-          ldmatrix_x4_trans(vs + (piece >> 3) * C::kKeys * 128 + key * 128 + (((piece & 7) ^ (key & 7)) << 4), v);
 #pragma unroll
-          for (int a = 0; a < kQ8; ++a) mma16816<false>(o[a][t], v[0], v[1], v[2], v[3], pb[a][0], pb[a][1]);
+          for (int y = 0; y < kTwo; ++y) {
+            uint32_t v[4];
+            ldmatrix_x4_trans(vs + (piece >> 3) * C::kKeys * 128 + (16 * y + key) * 128 + (((piece & 7) ^ (key & 7)) << 4), v);
+#pragma unroll
+            for (int a = 0; a < kQ8; ++a) mma16816<false>(o[a][t], v[0], v[1], v[2], v[3], pb[a][y][0], pb[a][y][1]);
+          }
         }
       } else {
         // 16 values (piece g of a column) of keys 2c, 2c + 1, 2c + 8, 2c + 9; tile t of the column takes
         // values 2t (row g) and 2t + 1 (row g + 8)
 #pragma unroll
         for (int b = 0; b < C::kBoxes; ++b) {
-          uint32_t v[4][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = 2 * c + (i & 1) + 8 * (i >> 1);
-            const uint4 x = lds128(vs + b * C::kKeys * 128 + key * 128 + ((g ^ (key & 7)) << 4));
-            v[i][0] = x.x;
-            v[i][1] = x.y;
-            v[i][2] = x.z;
-            v[i][3] = x.w;
-          }
+          for (int y = 0; y < kTwo; ++y) {
+            uint32_t v[4][4];
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const uint32_t sel = t & 1 ? 0x7362u : 0x5140u;  // two values of two keys side by side
-            const uint32_t lo = __byte_perm(v[0][t >> 1], v[1][t >> 1], sel), hi = __byte_perm(v[2][t >> 1], v[3][t >> 1], sel);
-            const uint32_t a0 = e4m3x2_to_half2(lo & 0xFFFFu), a1 = e4m3x2_to_half2(lo >> 16),
-                           a2 = e4m3x2_to_half2(hi & 0xFFFFu), a3 = e4m3x2_to_half2(hi >> 16);
+            for (int i = 0; i < 4; ++i) {
+              const int key = 2 * c + (i & 1) + 8 * (i >> 1);
+              const uint4 x = lds128(vs + b * C::kKeys * 128 + (16 * y + key) * 128 + ((g ^ (key & 7)) << 4));
+              v[i][0] = x.x;
+              v[i][1] = x.y;
+              v[i][2] = x.z;
+              v[i][3] = x.w;
+            }
 #pragma unroll
-            for (int a = 0; a < kQ8; ++a) mma16816<true>(o[a][b * 8 + t], a0, a1, a2, a3, pb[a][0], pb[a][1]);
+            for (int t = 0; t < 8; ++t) {
+              const uint32_t sel = t & 1 ? 0x7362u : 0x5140u;  // two values of two keys side by side
+              const uint2 lo = e4m3x4_to_half4(__byte_perm(v[0][t >> 1], v[1][t >> 1], sel)),
+                          hi = e4m3x4_to_half4(__byte_perm(v[2][t >> 1], v[3][t >> 1], sel));
+#pragma unroll
+              for (int a = 0; a < kQ8; ++a) mma16816<true>(o[a][b * 8 + t], lo.x, lo.y, hi.x, hi.y, pb[a][y][0], pb[a][y][1]);
+            }
           }
         }
       }
