@@ -182,14 +182,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   Walk walk;
-  walk.left = start->left;
-  if (walk.left > 0) {
-    walk.n = start->n;
-    walk.hk = start->hk;
-    walk.tile = start->tile;
-    walk.j = start->j;
-    walk.load(p, step);
-  }
+  walk.begin(p, step, *start);
   Segment seg;
   bool ok = true;
   // A bounded wait of the whole warp, or (the products) of one thread.  After one that ran out the warp
@@ -795,14 +788,17 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
 }
 
 // Joins the parts of cut tiles: out = sum_c O_c 2^(m_c - m) / sum_c l_c 2^(m_c - m), c over the tile's
-// parts in the order of the line (so the result does not depend on who is first).  The CTAs of the
-// tile's first part do it, blockIdx.y takes a share of rows and columns.  The parts are listed first, so
-// that their loads do not wait for one another.
+// parts, always in the same order.  The CTAs of the tile's first part do it; blockIdx.y takes a share of
+// rows and columns, and where a tile has many parts the warps of a CTA share those.  The parts are listed
+// first and loaded four at a time, so that their loads do not wait for one another.
 //   kTiles 1, 2: parts [tile][D / 4][128 rows], lanes are rows;  kTiles 0: parts [row][D], lanes are columns
 template <int D, int kTiles>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p, int ctas) {
   __shared__ int s_slot[kMaxCtas + 1];
   __shared__ int s_n;
+  __shared__ float4 s_o[8][32];
+  __shared__ float2 s_ml[8][32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the kernel that writes the parts has ended
   const int4 d = p.desc[2 * blockIdx.x + 1];
   if (!(d.w & kPart)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -822,9 +818,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
   __syncthreads();
   const int parts = s_n;
+  const int ways = parts >= 16 ? 8 : parts >= 8 ? 4 : 1, way = warp % ways, each = 8 / ways;  // warps of an item; items at a time
   const int subs = kTiles == 2 && d.y > p.sub ? 2 : 1;
-  const int items = kTiles ? subs * 4 * (D / 4) : (p.G * (D / 4) + 31) / 32;  // of a warp each
-  for (int i = blockIdx.y * 8 + warp; i < items; i += gridDim.y * 8) {
+  const int items = kTiles ? subs * 4 * (D / 4) : (p.G * (D / 4) + 31) / 32;
+  for (int i0 = blockIdx.y * each; i0 < items; i0 += gridDim.y * each) {
+    const int i = i0 + warp / ways;
     int col, row, sub = 0, rows = p.G;
     if constexpr (kTiles > 0) {
       const int rw = i / (D / 4);
@@ -832,29 +830,56 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       sub = rw >> 2;
       row = (rw & 3) * 32 + lane;
       rows = min(p.sub, d.y - sub * p.sub) * p.G;
-      if ((rw & 3) * 32 >= rows) continue;
     } else {
       col = (i * 32 + lane) % (D / 4);
       row = (i * 32 + lane) / (D / 4);
     }
+    // a row of this warp exists at all (with lanes as rows: its first one)
+    const bool some = i < items && (kTiles == 0 ? row < rows : row - lane < rows);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (kTiles > 0 || row < rows) {
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) {
-        const long slot = s_slot[k];
-        const float2 ml = p.ml[slot * 256 + sub * 128 + row];
+    for (int k0 = way; k0 < parts; k0 += 4 * ways) {
+      float2 ml[4];
+      float4 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = some && k0 + u * ways < parts;
+        const long slot = s_slot[in ? k0 + u * ways : 0];
         const float4* part = p.part + slot * (long)(kPartBytes / sizeof(float4));
-        const float4 x = kTiles > 0 ? part[(sub * (D / 4) + col) * 128 + row] : part[row * (D / 4) + col];
-        const float m2 = fmaxf(m, ml.x);
-        const float off = m2 == -INFINITY ? 0.f : m2;
-        const float a = ex2_approx(m - off), b = ex2_approx(ml.x - off);
-        l = l * a + ml.y * b;
-        o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
+        ml[u] = make_float2(-INFINITY, 0.f);
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (in) {
+          ml[u] = __ldcg(p.ml + slot * 256 + sub * 128 + row);
+          x[u] = __ldcg(kTiles > 0 ? part + (sub * (D / 4) + col) * 128 + row : part + row * (D / 4) + col);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float m2 = fmaxf(m, ml[u].x), off = m2 == -INFINITY ? 0.f : m2;
+        const float a = ex2_approx(m - off), b = ex2_approx(ml[u].x - off);
+        l = l * a + ml[u].y * b;
+        o = make_float4(o.x * a + x[u].x * b, o.y * a + x[u].y * b, o.z * a + x[u].z * b, o.w * a + x[u].w * b);
         m = m2;
       }
     }
-    if (row < rows) {
+    if (ways > 1) {
+      s_ml[warp][lane] = make_float2(m, l);
+      s_o[warp][lane] = o;
+      __syncthreads();
+      if (way == 0) {
+        for (int w = 1; w < ways; ++w) {
+          const float2 y = s_ml[warp + w][lane];
+          const float4 x = s_o[warp + w][lane];
+          const float m2 = fmaxf(m, y.x), off = m2 == -INFINITY ? 0.f : m2;
+          const float a = ex2_approx(m - off), b = ex2_approx(y.x - off);
+          l = l * a + y.y * b;
+          o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
+          m = m2;
+        }
+      }
+      __syncthreads();
+    }
+    if (some && way == 0 && row < rows) {
       const int t = row / p.G, h = d.z * p.G + row - t * p.G;
       const long r = d.x + sub * p.sub + t;
       const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -881,8 +906,17 @@ cudaError_t encode_pages(CUtensorMap* map, const void* base, const PagedCache& c
 template <int D, int kTiles>
 cudaError_t launch_join(const LaunchEnv& env, const AttnParams& p, int ctas) {
   const int items = kTiles ? 4 * kTiles * (D / 4) : (p.G * (D / 4) + 31) / 32;
-  attn_join_kernel<D, kTiles><<<dim3(ctas, items < 64 ? (items + 7) / 8 : 8), 256, 0, env.stream>>>(p, ctas);
-  return cudaGetLastError();
+  // Its launch need not wait for the end of the kernel before it: it waits itself, before it reads.
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, items < 16 ? items : 16);
+  cfg.blockDim = dim3(256);
+  cfg.stream = env.stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, kTiles>, p, ctas);
 }
 
 template <int D, int kTiles, bool kE4M3>
@@ -935,6 +969,7 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   p.N = N;
   p.T = T;
   p.sub = 128 / p.G;
+  p.lead = 2;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.desc = reinterpret_cast<int4*>(ws);
   p.ml = reinterpret_cast<float2*>(ws + 2 * kMaxCtas * sizeof(int4));
@@ -947,6 +982,7 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   // 128-row tile, and HBM bounds the call.
   if (!cu && p.G <= 16) {
     p.sub = 1;
+    p.lead = cache.e4m3 && D == 128 ? 2 : 1;  // about a microsecond of HBM's time for an SM
     e = launch_attn_decode(env, p, D, ctas);
     if (e != cudaSuccess) return e;
     return D == 128 ? launch_join<128, 0>(env, p, ctas) : launch_join<256, 0>(env, p, ctas);

@@ -54,6 +54,7 @@ struct AttnParams {
   float scale_log2;
   int Hq, Hkv, G, N, T;
   int sub;       // tokens of one tile: 128 / G on the tcgen05 cores, 1 in the one-token kernel
+  int lead;      // blocks that beginning and ending a tile cost, in the line of work
   int4* desc;    // [2 * grid] what each part of a cut tile holds: packed row, tokens, key head, flags
   float2* ml;    // [2 * grid][256] maximum (log2 units) and sum of a row
   float4* part;  // [2 * grid][128 KB] unnormalised O
@@ -108,23 +109,25 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, bool rep
 }
 
 // Keys that the last token of tile i sees; blocks of that tile (one at least, so that rows without a
-// key are visited too); blocks of the tiles before tile i.
+// key are visited too); its length in the line of work, and that of the tiles before it: `lead` units
+// that stand for beginning and ending a tile, then one for each block.
 struct Tiles {
-  int p0, len, step;  // position of the first new token, new tokens, tokens of a tile
+  int p0, len, step, lead;  // position of the first new token, new tokens, tokens of a tile
   __device__ __forceinline__ int count() const { return (len + step - 1) / step; }
   __device__ __forceinline__ int keys(int i) const { return p0 + (int)min((long)(i + 1) * step, (long)len); }
   __device__ __forceinline__ int blocks(int i) const {
     const int k = keys(i);
     return k <= kBlock ? 1 : (int)(((long)k + kBlock - 1) / kBlock);
   }
+  __device__ __forceinline__ int units(int i) const { return blocks(i) + lead; }
   __device__ __forceinline__ long before(int i) const {
     const int last = count() - 1, full = min(i, last);
-    if (full <= 0) return i > last && last >= 0 ? blocks(last) : 0;
-    const long lead = (long)kBlock - p0;  // tiles with at most one block: (t + 1) step <= lead
-    const int t0 = lead < step ? 0 : (int)min((long)full, lead / step);
-    long s = t0;
+    if (full <= 0) return i > last && last >= 0 ? units(last) : 0;
+    const long ahead = (long)kBlock - p0;  // tiles with at most one block: (t + 1) step <= ahead
+    const int t0 = ahead < step ? 0 : (int)min((long)full, ahead / step);
+    long s = t0 + (long)full * lead;
     if (full > t0) s += floor_sum(full - t0, kBlock, step, (long)(t0 + 1) * step + p0 + kBlock - 1);
-    return s + (i > last ? blocks(last) : 0);
+    return s + (i > last ? units(last) : 0);
   }
 };
 
@@ -136,56 +139,69 @@ struct Segment {
   int j0, j1, nb;        // nb: the tile's blocks
 };
 
+struct WalkStart {
+  long left, rem;
+  int n, hk, tile, j;
+};
+
 // A CTA's piece of the line, segment by segment.  Every warp walks it by itself.
 struct Walk {
-  long left;  // blocks not yet taken
+  long left;  // units not yet taken
   int n, hk, tile, j;
   SeqInfo s;
   Tiles t;
 
   __device__ __forceinline__ void load(const AttnParams& p, int step) {
     s = seq_info(p, n, false);
-    t = {s.kv - s.len, s.len, step};
+    t = {s.kv - s.len, s.len, step, p.lead};
+  }
+  __device__ __forceinline__ void begin(const AttnParams& p, int step, const WalkStart& w) {
+    left = w.left;
+    if (left > 0) {
+      n = w.n;
+      hk = w.hk;
+      tile = w.tile;
+      j = w.j;
+      load(p, step);
+    }
   }
   __device__ __forceinline__ bool next(const AttnParams& p, int step, Segment& g) {
-    if (left <= 0) return false;
-    g.n = n;
-    g.hk = hk;
-    g.nb = t.blocks(tile);
-    g.row0 = s.first + tile * step;
-    g.ntok = min(step, s.len - tile * step);
-    g.pos0 = t.p0 + tile * step;
-    g.keys = t.keys(tile);
-    g.j0 = j;
-    g.j1 = (int)min((long)g.nb, j + left);
-    left -= g.j1 - g.j0;
-    j = g.j1;
-    if (left > 0) {  // the next tile, key head, sequence
-      j = 0;
-      if (++tile == t.count()) {
-        tile = 0;
-        if (++hk == p.Hkv) {
-          hk = 0;
-          do {
-            if (++n >= p.N) {
-              left = 0;
-              break;
-            }
-            load(p, step);
-          } while (s.len == 0);
+    for (;;) {
+      if (left <= 0) return false;
+      g.n = n;
+      g.hk = hk;
+      g.nb = t.blocks(tile);
+      g.row0 = s.first + tile * step;
+      g.ntok = min(step, s.len - tile * step);
+      g.pos0 = t.p0 + tile * step;
+      g.keys = t.keys(tile);
+      const int end = (int)min((long)g.nb + p.lead, j + left);
+      g.j0 = max(j - p.lead, 0);
+      g.j1 = end - p.lead;
+      left -= end - j;
+      j = end;
+      if (left > 0) {  // the next tile, key head, sequence
+        j = 0;
+        if (++tile == t.count()) {
+          tile = 0;
+          if (++hk == p.Hkv) {
+            hk = 0;
+            do {
+              if (++n >= p.N) {
+                left = 0;
+                break;
+              }
+              load(p, step);
+            } while (s.len == 0);
+          }
         }
       }
+      if (g.j1 > g.j0) return true;  // else the piece ends before the tile's first block
     }
-    return true;
   }
 };
 
-struct WalkStart {
-  long left, rem;
-  int n, hk, tile, j;
-};
-
-// This CTA's piece of the line: an equal share of all blocks, found by the whole CTA.  `scan`: one long
+// This CTA's piece of the line: an equal share of its units, found by the whole CTA.  `scan`: one long
 // for each warp; start->left is 0 before the call and stays 0 for a CTA without work.  The caller
 // synchronises before it reads *start.
 template <int kThreads>
@@ -194,7 +210,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* 
   long mine = 0;
   for (int n = tid; n < p.N; n += kThreads) {
     const SeqInfo s = seq_info(p, n, blockIdx.x == 0);
-    const Tiles t = {s.kv - s.len, s.len, step};
+    const Tiles t = {s.kv - s.len, s.len, step, p.lead};
     if (s.len > 0) mine += t.before(t.count());
   }
   mine *= p.Hkv;
@@ -208,13 +224,13 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* 
   const long u0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
   const long u1 = total / gridDim.x * (blockIdx.x + 1) + total % gridDim.x * (blockIdx.x + 1) / gridDim.x;
   if (u1 > u0) {
-    long base = 0;  // blocks of the sequences before this round's
+    long base = 0;  // units of the sequences before this round's
     for (int n0 = 0; n0 < p.N; n0 += kThreads) {
       const int n = n0 + tid;
       long u = 0;
       if (n < p.N) {
         const SeqInfo s = seq_info(p, n, false);
-        const Tiles t = {s.kv - s.len, s.len, step};
+        const Tiles t = {s.kv - s.len, s.len, step, p.lead};
         if (s.len > 0) u = t.before(t.count()) * p.Hkv;
       }
       long inc = u;
@@ -241,7 +257,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* 
     }
     // the key head, then the tile: every thread looks at one stretch of tiles
     const SeqInfo s = seq_info(p, start->n, false);
-    const Tiles t = {s.kv - s.len, s.len, step};
+    const Tiles t = {s.kv - s.len, s.len, step, p.lead};
     const int count = t.count(), stretch = (count + kThreads - 1) / kThreads;
     const long per = t.before(count), rem = start->rem % per;
     const int lo = min(tid * stretch, count), hi = min(lo + stretch, count);
@@ -249,7 +265,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* 
       long at = t.before(lo);
       if (rem >= at) {
         for (int i = lo; i < hi; ++i) {
-          const int nb = t.blocks(i);
+          const int nb = t.units(i);
           if (rem < at + nb) {
             start->hk = (int)(start->rem / per);
             start->tile = i;

@@ -7,7 +7,7 @@
 // values fill the 16 rows and the query rows the 8 columns:
 //   S^T [16 keys x q] = K Q^T,   p = 2^(S - m),   O^T [D x q] += V^T P^T
 // Each warp has its own running m, l and O in registers, so that the warps meet only where a segment
-// ends; there they are joined pairwise.  (Work is cut into one piece for each SM as in the tile kernel.)
+// ends; there they are joined.  (Work is cut into one piece for each SM as in the tile kernel.)
 //
 // An e4m3 cache is widened between shared memory and the registers, two codes an instruction, to
 // binary16, which holds every code exactly.  The queries become binary16 too, each row divided by the
@@ -151,12 +151,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
     // ------------------------------------------------------------------ loading: keys, or values
     const bool keys = warp == kWarps;
     Walk walk;
-    walk.left = start->left;
-    walk.n = start->n;
-    walk.hk = start->hk;
-    walk.tile = start->tile;
-    walk.j = start->j;
-    walk.load(p, 1);
+    walk.begin(p, 1, *start);
     const int shift = p.cache.page_shift, rows_shift = min(shift, C::kKeys == 32 ? 5 : 6), rows = 1 << rows_shift;
     const CUtensorMap* map = keys ? &p.tmap_k : &p.tmap_v;
     const uint8_t* scale = keys ? p.cache.k_scale : p.cache.v_scale;
@@ -511,7 +506,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
     __syncwarp();
     if (lane == 0) mbar_arrive(empty + 8 * slot);
     if (flags & kLastOfSegment) {
-      // ---- the warps' shares, joined pairwise
+      // ---- the warps' shares, joined
       float4* mo = reinterpret_cast<float4*>(sm + C::kOffMerge);
       float4* mml = reinterpret_cast<float4*>(sm + C::kOffMl);
 #pragma unroll
@@ -529,92 +524,88 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
             }
           }
         }
-#pragma unroll 1
-      for (int h = kWarps / 2; h > 0; h >>= 1) {
-        if (warp >= h && warp < 2 * h) {
-          float4* to = mo + (warp - h) * kQ8 * kTiles * 32 + lane;
+      // half of the warps hand theirs over, the others add their own
+      constexpr int kHalfWarps = kWarps / 2;
+      float4* slot_o = mo + (warp % kHalfWarps) * kQ8 * kTiles * 32 + lane;
+      float4* slot_ml = mml + (warp % kHalfWarps) * kQ8 * 32 + lane;
+      if (warp < kHalfWarps) warps_sync();
 #pragma unroll
-          for (int a = 0; a < kQ8; ++a) {
-            mml[((warp - h) * kQ8 + a) * 32 + lane] = make_float4(m[a][0], m[a][1], l[a][0], l[a][1]);
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) to[(a * kTiles + t) * 32] = make_float4(o[a][t][0], o[a][t][1], o[a][t][2], o[a][t][3]);
-          }
-        }
-        warps_sync();
-        if (warp < h) {
-          const float4* from = mo + warp * kQ8 * kTiles * 32 + lane;
-#pragma unroll
-          for (int a = 0; a < kQ8; ++a) {
-            const float4 y = mml[(warp * kQ8 + a) * 32 + lane];
-            float f0[2], f1[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float mk = k ? y.y : y.x, lk = k ? y.w : y.z, m2 = fmaxf(m[a][k], mk), off = m2 == -INFINITY ? 0.f : m2;
-              f0[k] = ex2_approx(m[a][k] - off);
-              f1[k] = ex2_approx(mk - off);
-              l[a][k] = l[a][k] * f0[k] + lk * f1[k];
-              m[a][k] = m2;
-            }
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              const float4 x = from[(a * kTiles + t) * 32];
-              o[a][t][0] = o[a][t][0] * f0[0] + x.x * f1[0];
-              o[a][t][1] = o[a][t][1] * f0[1] + x.y * f1[1];
-              o[a][t][2] = o[a][t][2] * f0[0] + x.z * f1[0];
-              o[a][t][3] = o[a][t][3] * f0[1] + x.w * f1[1];
-            }
-          }
-        }
-        warps_sync();
-      }
-      // ---- out: rows through shared memory, then 16 bytes a thread
-      constexpr int kPitch = D + 4;
-      float* rows = reinterpret_cast<float*>(mo);
-      if (warp == 0) {
-#pragma unroll
-        for (int a = 0; a < kQ8; ++a) {
+      for (int a = 0; a < kQ8; ++a) {
+        if (warp < kHalfWarps) {
+          const float4 y = slot_ml[a * 32];
+          float f0[2], f1[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int row = a * 8 + 2 * c + k;
-            const float lk = l[a][k], f = flags & kWhole ? (lk == 0.f ? 0.f : 1.f / lk) : 1.f;
-            const bool none = lk == 0.f;  // no visible key: zero, whatever O holds
+            const float mk = k ? y.y : y.x, lk = k ? y.w : y.z, m2 = fmaxf(m[a][k], mk), off = m2 == -INFINITY ? 0.f : m2;
+            f0[k] = ex2_approx(m[a][k] - off);
+            f1[k] = ex2_approx(mk - off);
+            l[a][k] = l[a][k] * f0[k] + lk * f1[k];
+            m[a][k] = m2;
+          }
 #pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-              const int d0 = kE4M3 ? (t >> 3) * 128 + g * 16 + (t & 7) * 2 : t * 16 + g, d1 = kE4M3 ? d0 + 1 : d0 + 8;
-              rows[row * kPitch + d0] = none ? 0.f : o[a][t][k] * f;
-              rows[row * kPitch + d1] = none ? 0.f : o[a][t][2 + k] * f;
-            }
-            if (!(flags & kWhole) && g == 0 && row < p.G) p.ml[(long)part * 256 + row] = make_float2(m[a][k], lk);
+          for (int t = 0; t < kTiles; ++t) {
+            const float4 x = slot_o[(a * kTiles + t) * 32];
+            slot_o[(a * kTiles + t) * 32] = make_float4(o[a][t][0] * f0[0] + x.x * f1[0], o[a][t][1] * f0[1] + x.y * f1[1],
+                                                        o[a][t][2] * f0[0] + x.z * f1[0], o[a][t][3] * f0[1] + x.w * f1[1]);
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) slot_o[(a * kTiles + t) * 32] = make_float4(o[a][t][0], o[a][t][1], o[a][t][2], o[a][t][3]);
+        }
+        slot_ml[a * 32] = make_float4(m[a][0], m[a][1], l[a][0], l[a][1]);
+      }
+      if (warp >= kHalfWarps) warps_sync();
+      warps_sync();
+      // ---- out: the sum of what is left, eight values a thread
+      const bool whole = flags & kWhole;
+      for (int i = tid; i < p.G * (D / 8); i += 32 * kWarps) {
+        const int row = i / (D / 8), d = i % (D / 8) * 8, a = row >> 3, at = (row & 7) >> 1, k = row & 1;
+        float mk[kHalfWarps], lk[kHalfWarps], mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kHalfWarps; ++w) {  // lanes of one c hold the same: lane c
+          const float* y = reinterpret_cast<const float*>(mml + (w * kQ8 + a) * 32 + at);
+          mk[w] = y[k];
+          lk[w] = y[2 + k];
+          mx = fmaxf(mx, mk[w]);
+        }
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, lx = 0.f;
+#pragma unroll
+        for (int w = 0; w < kHalfWarps; ++w) {
+          const float f = mx == -INFINITY ? 0.f : ex2_approx(mk[w] - mx);
+          lx += lk[w] * f;
+          const float* x = reinterpret_cast<const float*>(mo + (w * kQ8 + a) * kTiles * 32) + k;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            // where value d + e of this row sits: mma tile, lane row, half
+            const int t = kE4M3 ? (d >> 7) * 8 + ((d + e) >> 1 & 7) : d >> 4, lr = kE4M3 ? d >> 4 & 7 : e,
+                      hf = kE4M3 ? e & 1 : d >> 3 & 1;
+            v[e] += x[(t * 32 + 4 * lr + at) * 4 + 2 * hf] * f;
           }
         }
-        if (!(flags & kWhole) && lane == 0)
-          p.desc[part] = make_int4(row0, 1, hk, kPart | (flags & kEndsTile ? kPartLast : 0));
-      }
-      warps_sync();
-      for (int i = tid; i < p.G * (D / 8); i += 32 * kWarps) {
-        const int row = i / (D / 8), d = i % (D / 8) * 8;
-        const float4 x = *reinterpret_cast<const float4*>(rows + row * kPitch + d),
-                     y = *reinterpret_cast<const float4*>(rows + row * kPitch + d + 4);
-        if (flags & kWhole) {
-          float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        const float inv = whole ? (lx == 0.f ? 0.f : 1.f / lx) : 1.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = lx == 0.f ? 0.f : v[e] * inv;  // no visible key: zero, whatever O holds
+        if (whole) {
           const long h = hk * p.G + row;
           if (p.z.p) {
             const uint4 zz = __ldg(reinterpret_cast<const uint4*>(p.z.p + row0 * p.z.token + h * p.z.head + d));
             const uint32_t zr[4] = {zz.x, zz.y, zz.z, zz.w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              v[2 * k] *= sigmoid_fast(__uint_as_float(zr[k] << 16));
-              v[2 * k + 1] *= sigmoid_fast(__uint_as_float(zr[k] & 0xFFFF0000u));
+            for (int e = 0; e < 4; ++e) {
+              v[2 * e] *= sigmoid_fast(__uint_as_float(zr[e] << 16));
+              v[2 * e + 1] *= sigmoid_fast(__uint_as_float(zr[e] & 0xFFFF0000u));
             }
           }
           *reinterpret_cast<uint4*>(p.out + ((long)row0 * p.Hq + h) * D + d) =
               make_uint4(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]), pack_bf2(v[4], v[5]), pack_bf2(v[6], v[7]));
         } else {
           float4* to = p.part + (long)part * (kPartBytes / sizeof(float4)) + (row * D + d) / 4;
-          to[0] = x;
-          to[1] = y;
+          to[0] = make_float4(v[0], v[1], v[2], v[3]);
+          to[1] = make_float4(v[4], v[5], v[6], v[7]);
+          if (d == 0) p.ml[(long)part * 256 + row] = make_float2(mx, lx);
         }
       }
+      if (!whole && tid == 0) p.desc[part] = make_int4(row0, 1, hk, kPart | (flags & kEndsTile ? kPartLast : 0));
       warps_sync();
     }
   }
