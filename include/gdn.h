@@ -626,8 +626,9 @@ GDN_API size_t gdn_attn_workspace_size(const gdn_attn_geometry* geo);
  * too: gdn_attn_prepare first).  With p the token's position and j = 0 .. p:
  *   s_j = softmax_scale * q . k_j,   o = sum_j e^(s_j) v_j / sum_j e^(s_j)   (0 when p < 0),
  *   out = o, or o * sigmoid(z) where z is given.
- * Scores and sums are fp32 with a running maximum; the weights e^(s_j - max) -- for an e4m3 cache
- * times the power of two of v_j -- are rounded to bf16 for the product with v (with its codes).
+ * Scores and sums are fp32 with a running maximum; the weights e^(s_j - max) are rounded to bf16
+ * for the product with v.  An e4m3 cache is read as binary16, exactly; the queries (divided by a power of
+ * two) and the weights (times the power of two of v_j) are rounded to binary16 with it.
  *   q          [total_tokens, Hq, D] bf16
  *   z          Hq heads of D bf16 for each token, head h of token t at z + t * z_token_stride +
  *              h * z_head_stride (elements, multiples of 8), or NULL

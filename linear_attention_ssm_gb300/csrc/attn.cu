@@ -30,18 +30,32 @@ constexpr uint32_t kStage = 32768;
 
 // ---------------------------------------------------------------- layout of a CTA
 
+// e4m3: what the warps that widen the codes and those of the softmax need to know of a block of keys.
+struct BlockMeta {
+  float kf[kBlock];   // a key's power of two times the softmax scale: log2 units of its scores
+  float vf[kBlock];   // a value's power of two relative to the block's largest, times 2^kWeight
+  int row[8];         // pool row of each page's first key
+  float ev;           // log2 of the block's largest value scale
+  int have, flags;    // visible keys; kFirst, kLast: of a segment, kEnd: no more blocks
+  int pad;
+};
+enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
+constexpr int kMeta = 8;         // blocks that the pages and scales are ahead
+constexpr float kWeight = 7.f;   // log2 of the factor on binary16 weights
+
 template <int D, int kTiles, bool kE4M3>
 struct Cfg {
   static constexpr int kSoftWarps = 4 * kTiles;
   static constexpr int kConvWarps = kE4M3 ? (kTiles == 2 ? 4 : 8) : 0;
   static constexpr int kThreads = 32 * (kSoftWarps + 4 + kConvWarps);
   static constexpr uint32_t kQ = kTiles * 128 * D * 2;
-  // An e4m3 cache's loads wait in registers, so one stage less will do, and its place holds the scales.
+  // An e4m3 cache's loads wait in registers, so one stage less will do; its place holds the scales.
   static constexpr int kStages = (int)((224 * 1024 - kQ) / kStage) - (kE4M3 ? 1 : 0);
   static constexpr int kParts = D / 128;  // stages of a block's keys, and of its values
   static constexpr uint32_t kOffStage = kQ;
-  static constexpr uint32_t kOffScale = kOffStage + kStages * kStage;  // 4 blocks' scales
-  static constexpr uint32_t kOffBar = kOffScale + (kE4M3 ? 4 * 1024 : 0);
+  static constexpr uint32_t kOffScale = kOffStage + kStages * kStage;  // e4m3: the next blocks' pages and scales
+  static constexpr uint32_t kOffQs = kOffScale + (kE4M3 ? kMeta * sizeof(BlockMeta) : 0);
+  static constexpr uint32_t kOffBar = kOffQs + (kE4M3 ? kTiles * 512 : 0);
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;  // barriers; alignment of the base
   static constexpr uint32_t kColO = 256;                    // tensor memory: two S slots of 128 columns, then O
   // Registers: the softmax warps hold a row of 128 scores each, the others need few.  The shares of the
@@ -57,7 +71,7 @@ struct Cfg {
 };
 
 struct Bars {
-  uint32_t full, empty, tail, s_full, p_full, o_full, q_full, done, sc_full;  // shared addresses of the first of each kind
+  uint32_t full, empty, tail, s_full, p_full, o_full, q_full, done, meta_full, meta_empty;  // shared addresses of the first of each kind
 };
 
 // 64 columns of this warp's 32 lanes.  The wait for the load is a statement of its own (two loads, one
@@ -126,6 +140,10 @@ __device__ __forceinline__ uint32_t ld_ahead4(const void* p) {
   return v;
 }
 
+__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, kWaitLimit));
+}
+
 template <int kRegs>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -146,11 +164,11 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   const int step = kTiles * p.sub;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
-  WalkStart* start = reinterpret_cast<WalkStart*>(bars + 34);
-  long* scan = reinterpret_cast<long*>(bars + 40);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 44);
+  WalkStart* start = reinterpret_cast<WalkStart*>(bars + 46);
+  long* scan = reinterpret_cast<long*>(bars + 52);
   const uint32_t b0 = smem_u32(bars);
-  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26, b0 + 8 * 27};
+  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26, b0 + 8 * 27, b0 + 8 * 35};
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar.full + 8 * i, kE4M3 ? C::kConvWarps : 1);
@@ -164,7 +182,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       mbar_init(bar.q_full + 8 * i, 4);
     }
     mbar_init(bar.done, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(bar.sc_full + 8 * i, 1);
+    if constexpr (kE4M3) {
+      for (int i = 0; i < kMeta; ++i) {
+        mbar_init(bar.meta_full + 8 * i, 1);
+        mbar_init(bar.meta_empty + 8 * i, C::kConvWarps + C::kSoftWarps);
+      }
+    }
     fence_mbar_init();
     if constexpr (!kE4M3) {
       prefetch_tensormap(&p.tmap_k);
@@ -233,20 +256,43 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
         continue;
       }
-      // Q into shared memory; zeros in the other rows of a warp that has some (what the rest of the tile
-      // holds stays in rows that nobody reads)
-      {
-        const int filled = (rows + 31) & ~31;
+      // Q into shared memory, each warp its own rows; zeros in the rows beyond the tile's last (what a warp
+      // without rows leaves there stays in rows that nobody reads).  e4m3: in binary16, divided by the
+      // power of two of the row's largest value.
+      float unit = p.scale_log2;  // log2 units of this row's scores
+      if (w4 * 32 < rows) {
         constexpr int kPer = D / 8, kRowsAt = 32 / kPer;  // 16-byte pieces of a row, rows of a warp at a time
         const int piece = lane % kPer;
         const uint16_t* src = p.q + (long)hk * p.G * D + piece * 8;
+        float* qs = reinterpret_cast<float*>(sm + C::kOffQs) + sub * 128;
 #pragma unroll 4
-        for (int r = w4 * kRowsAt + lane / kPer; r < filled; r += 4 * kRowsAt) {
-          const int t = r / p.G;
+        for (int i = 0; i < 32; i += kRowsAt) {
+          const int r = w4 * 32 + i + lane / kPer, t = r / p.G;
           uint4 x = make_uint4(0, 0, 0, 0);
           if (r < rows)
             x = __ldg(reinterpret_cast<const uint4*>(src + ((long)(row0 + t) * p.Hq + (r - t * p.G)) * D));
+          if constexpr (kE4M3) {
+            uint32_t y[4] = {x.x, x.y, x.z, x.w}, top = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t lo = y[k] << 16 & 0x7FFFFFFFu, hi = y[k] & 0x7FFF0000u;
+              top = max(top, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+            }
+#pragma unroll
+            for (int w = kPer / 2; w > 0; w >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
+            const int e = min(max((int)(top >> 23) - 127, -120), 126);
+            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              y[k] = pack_half2(__uint_as_float(y[k] << 16) * inv, __uint_as_float(y[k] & 0xFFFF0000u) * inv);
+            x = make_uint4(y[0], y[1], y[2], y[3]);
+            if (piece == 0) qs[r] = __uint_as_float((uint32_t)(127 + e) << 23);
+          }
           *reinterpret_cast<uint4*>(sq + sw128_offset(r, piece * 8, 16384)) = x;
+        }
+        if constexpr (kE4M3) {
+          __syncwarp();
+          unit = qs[row];
         }
       }
       fence_proxy_async_smem();
@@ -257,6 +303,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       const bool busy = w4 * 32 < rows;                   // this warp has rows at all
       const uint32_t seg_blk = all_blk;
       all_blk += seg.j1 - seg.j0;
+      if (kE4M3 && rows <= 0) {  // this tile has no rows in the segment: its warps still let its blocks go
+        for (uint32_t b = seg_blk; b != all_blk && ok; ++b) {
+          if (!await(bar.meta_full + 8 * (b % kMeta), b / kMeta & 1u)) break;
+          if (lane == 0) mbar_arrive(bar.meta_empty + 8 * (b % kMeta));
+        }
+      }
       if (rows > 0) {
         uint32_t blk = seg_blk;
         for (int j = seg.j0; j < seg.j1; ++j, ++n_blk, ++blk) {
@@ -281,13 +333,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             const int lim = last + 1 - j * kBlock;  // columns from here on are not visible
             // e4m3: the codes' products become scores by the keys' powers of two
             float ev = 0.f;
-            const uint8_t* sc = sm + C::kOffScale + (blk & 3u) * 1024;
+            const BlockMeta* meta = reinterpret_cast<const BlockMeta*>(sm + C::kOffScale) + blk % kMeta;
             if constexpr (kE4M3) {
-              if (!await(bar.sc_full + 8 * (blk & 3u), (blk >> 2) & 1u)) break;
-              ev = *reinterpret_cast<const float*>(bars + 56 + (blk & 3u));
+              if (!await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) break;
+              ev = meta->ev;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const float4 k = *reinterpret_cast<const float4*>(sc + 16 * i);
+                const float4 k = *reinterpret_cast<const float4*>(meta->kf + 4 * i);
                 s[4 * i] *= k.x;
                 s[4 * i + 1] *= k.y;
                 s[4 * i + 2] *= k.z;
@@ -302,7 +354,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
             for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-            const float unit = kE4M3 ? 1.f : p.scale_log2;  // of s in log2 units (e4m3: already in the scales)
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * unit;
             if (top > m + kLazy) {
               l *= ex2_approx(m - top);
@@ -310,7 +361,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             }
             // O is held in units of 2^r: the row's maximum times the block's largest value scale
             const float e = m + ev;
-            const bool raise = e > r + kLazy;
+            const bool raise = e > r;
             if (__any_sync(0xFFFFFFFFu, raise)) {
               const float a = raise ? ex2_approx(r - e) : 1.f;
               if (raise) r = e;
@@ -327,14 +378,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
                 }
               }
             }
-            // weights 2^(s - m + d), d = e - r the distance of this block's unit from O's; d is cut off at
-            // -40 for them, lest a block of tiny values vanish from l, and the rest goes to P alone
-            float d = 0.f, rest = 1.f;
-            if constexpr (kE4M3) {
-              d = m == -INFINITY ? 0.f : fmaxf(e - r, -40.f);
-              rest = m == -INFINITY ? 1.f : ex2_approx(e - r - d);
-            }
-            const bool cut = kE4M3 && __any_sync(0xFFFFFFFFu, rest != 1.f);
+            // weights 2^(s - m + d), d = e - r <= 0 the distance of this block's unit from O's; cut off at -40,
+            // lest a block of tiny values vanish from l (P is zero in binary16 long before)
+            const float d = kE4M3 && m > -INFINITY ? fmaxf(e - r, -40.f) : 0.f;
             const float off = m == -INFINITY ? 0.f : d - m;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -345,28 +391,27 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
                 float x[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const float y = s[32 * h + 2 * i + k];
-                  x[k] = ex2_approx(kE4M3 ? y + off : fmaf(y, unit, off));
+                  x[k] = ex2_approx(fmaf(s[32 * h + 2 * i + k], unit, off));
                   sum[k] += x[k];
                 }
-                if constexpr (kE4M3) {  // the values' powers of two, relative to the block's largest
-                  const float4 v = *reinterpret_cast<const float4*>(sc + 512 + 128 * h + 8 * i);
+                if constexpr (kE4M3) {
+                  const float4 v = *reinterpret_cast<const float4*>(meta->vf + 32 * h + 2 * i);
                   x[0] *= v.x;
                   x[1] *= v.y;
                   x[2] *= v.z;
                   x[3] *= v.w;
-                  if (cut) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] *= rest;
-                  }
                 }
-                w[i] = __uint_as_float(pack_bf2(x[0], x[1]));
-                w[i + 1] = __uint_as_float(pack_bf2(x[2], x[3]));
+                w[i] = __uint_as_float(kE4M3 ? pack_half2(x[0], x[1]) : pack_bf2(x[0], x[1]));
+                w[i + 1] = __uint_as_float(kE4M3 ? pack_half2(x[2], x[3]) : pack_bf2(x[2], x[3]));
               }
               tmem_st16(t_s + 16 * h, w);
             }
             const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             l += kE4M3 ? all * ex2_approx(-d) : all;
+          }
+          if constexpr (kE4M3) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar.meta_empty + 8 * (blk % kMeta));
           }
           tc_fence_before();
           __syncwarp();
@@ -378,7 +423,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         tc_fence_after();
         const bool whole = seg.j0 == 0 && seg.j1 == seg.nb;
         // O in units of 2^m (half the exponent at a time where both ends of the range meet)
-        const float unit_o = kE4M3 && m > -INFINITY ? ex2_approx(0.5f * (r - m)) : 1.f;
+        const float unit_o = kE4M3 && m > -INFINITY ? ex2_approx(0.5f * (r - m - kWeight)) : 1.f;
         if (whole && busy) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const uint16_t* z = p.z.p + (long)(row0 + tok_in) * p.z.token + (long)(hk * p.G + g) * p.z.head;
@@ -434,107 +479,74 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   }
   if (kE4M3 && warp >= C::kSoftWarps + 4) {
     if constexpr (C::kSplit) regs_dec<C::kRegConv>();
-    // ------------------------------------------------------------------ e4m3: codes -> bf16 stages
+    // ------------------------------------------------------------------ e4m3: codes -> binary16 stages
     // 16 codes a load; the loads of the next kAhead stages wait in registers while this one's codes are
-    // widened (exactly) and written in the layout that the TMA gives a bf16 cache.
+    // widened (exactly, two an instruction) and written in the layout that the TMA gives a bf16 cache.
     constexpr int kConv = C::kConvWarps > 0 ? C::kConvWarps : 4, kUnits = 1024 / (32 * kConv), kAhead = kConv == 8 ? 3 : 2;
-    const int ct = tid - 32 * (C::kSoftWarps + 4), cw = ct >> 5;
+    const int ct = tid - 32 * (C::kSoftWarps + 4);
     const int shift = p.cache.page_shift;
+    const BlockMeta* metas = reinterpret_cast<const BlockMeta*>(sm + C::kOffScale);
     Ring<kStages> ring;
-    int op = 0, ops = 0, part = 0;           // of the segment: each op is a block's keys or values, in kParts stages
-    int id_k = 0, id_v = 0, id_next = 0;     // lane i: page of the i-th stretch of the block being fetched
-    uint32_t blk = 0;
-    uint4 raw[kAhead][kUnits];
-    int meta[kAhead];                        // -1: no more; bit 0: values, bits 1..: part
-    uint32_t kb[kAhead], vb[kAhead];         // warp 0, first stage of a block's keys: scale bytes of four keys a lane
-    int have[kAhead];                        // ... and the block's visible keys
-    auto page_of = [&](int j) {
-      const int key = j * kBlock + (lane << shift);
-      int id = 0;
-      if ((lane << shift) < kBlock && key < seg.keys) {
-        id = (int)ld_ahead4(p.cache.table + (long)seg.n * p.cache.max_pages + (key >> shift));
-        if ((unsigned)id >= (unsigned)p.cache.num_pages) {
-          raise_error(p.err, kErrDeviceArgument);
-          id = 0;
-        }
-      }
-      return id;
+    // The order of the stages, each operand of a block in kParts: K0 V0 K1 V1 .. with two tiles, with one
+    // K0 K1 V0 K2 V1 ..: after a block's keys come the values of the block before it, if the segment has
+    // one, and the block's own values, if it is the segment's last.
+    uint32_t blk = 0;          // the latest block whose keys were or are being fetched
+    int mode = 0, part = 0;    // 0: keys of blk, 1: values of the block before, 2: values of blk
+    int flags = 0;
+    uint4 raw[kAhead][kUnits] = {};
+    int what[kAhead] = {};     // 0: keys, 1: values, -1: no more
+    auto release = [&](uint32_t b) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar.meta_empty + 8 * (b % kMeta));
     };
-    auto fetch = [&](uint4 (&x)[kUnits], int& mt, uint32_t& k4, uint32_t& v4, int& hv) {
-      while (op == ops) {
-        if (!walk.next(p, step, seg)) {
-          mt = -1;
+    auto fetch = [&](uint4 (&x)[kUnits], int& is) {
+      is = -1;
+      if (mode == 0 && part == 0) {
+        if (!ok || !await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) return;
+        flags = metas[blk % kMeta].flags;
+        if (flags & kEnd) {
+          ok = false;  // nothing is waited for any more
           return;
         }
-        op = 0;
-        ops = seg.keys > 0 ? 2 * (seg.j1 - seg.j0) : 0;
-        if (ops) id_next = page_of(seg.j0);
       }
-      // the order of the stages: K0 V0 K1 V1 .. with two tiles, K0 K1 V0 K2 V1 .. with one
-      const bool value = kTiles == 2 ? op & 1 : op == ops - 1 || (op > 0 && !(op & 1));
-      const int j = seg.j0 + (kTiles == 2 ? op >> 1 : op == ops - 1 ? (ops >> 1) - 1 : value ? (op >> 1) - 1 : (op + 1) >> 1);
-      if (!value && part == 0) {
-        id_v = id_k;
-        id_k = id_next;
-        if (j + 1 < seg.j1) id_next = page_of(j + 1);
-      }
-      // with one tile the values fetched are those of the block before the latest keys, but for the last
-      const int ids = value && kTiles == 1 && op != ops - 1 ? id_v : id_k;
-      const bool wide = value && D == 256;  // 64 rows of 256 codes, else 128 rows of 128
+      const bool value = mode != 0, wide = value && D == 256;  // wide: 64 rows of 256 codes, else 128 rows of 128
+      const BlockMeta& meta = metas[(mode == 1 ? blk - 1 : blk) % kMeta];
       const uint8_t* src = static_cast<const uint8_t*>(value ? p.cache.v : p.cache.k);
+      const int have = meta.have;
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
         const int unit = u * 32 * kConv + ct;
         const int row = wide ? (unit >> 4) + part * 64 : unit >> 3;  // key of the block
         const int d = wide ? (unit & 15) * 16 : (unit & 7) * 16 + (value ? 0 : part * 128);
-        const int page = __shfl_sync(0xFFFFFFFFu, ids, row >> shift);
         x[u] = make_uint4(0, 0, 0, 0);
-        if (j * kBlock + row < seg.keys) {
-          const long at = (((long)page * p.Hkv + seg.hk) << shift) + (row & ((1 << shift) - 1));
-          x[u] = ld_ahead16(src + at * D + d);
-        }
+        if (row < have) x[u] = ld_ahead16(src + (long)(meta.row[row >> shift] + (row & ((1 << shift) - 1))) * D + d);
       }
-      mt = (value ? 1 : 0) | part << 1;
-      if (cw == 0 && !value && part == 0) {
-        const int page = __shfl_sync(0xFFFFFFFFu, ids, (lane * 4) >> shift);
-        hv = seg.keys - j * kBlock;
-        k4 = v4 = 0;
-        if (lane * 4 < hv) {
-          const long at = (((long)page * p.Hkv + seg.hk) << shift) + ((lane * 4) & ((1 << shift) - 1));
-          k4 = ld_ahead4(p.cache.k_scale + at);
-          v4 = ld_ahead4(p.cache.v_scale + at);
-        }
-      }
+      is = value;
       if (++part == kParts) {
         part = 0;
-        ++op;
+        if (mode == 1) release(blk - 1);
+        if (mode == 2) release(blk);
+        if (kTiles == 2) {
+          if (mode == 0) {
+            mode = 2;
+          } else {
+            mode = 0;
+            ++blk;
+          }
+        } else if (mode == 0 && !(flags & kFirst)) {
+          mode = 1;
+        } else if (mode != 2 && (flags & kLast)) {
+          mode = 2;
+        } else {
+          mode = 0;
+          ++blk;
+        }
       }
     };
-    auto process = [&](const uint4 (&x)[kUnits], int mt, uint32_t k4, uint32_t v4, int hv) {
-      if (!await(bar.empty + 8 * ring.i, ring.pass ^ 1u)) return false;
-      const bool value = mt & 1;
-      if (mt == 0) {  // a block's first stage: its scales
-        if (cw == 0) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top = max(top, lane * 4 + i < hv ? (v4 >> (8 * i)) & 255u : 0u);
-          top = __reduce_max_sync(0xFFFFFFFFu, top);
-          float kf[4], vf[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool in = lane * 4 + i < hv;
-            const int diff = (int)((v4 >> (8 * i)) & 255u) - (int)top;
-            kf[i] = in ? e8m0_value((k4 >> (8 * i)) & 255u) * p.scale_log2 : 0.f;
-            vf[i] = in && diff >= -126 ? __uint_as_float((uint32_t)(127 + diff) << 23) : 0.f;
-          }
-          uint8_t* sc = sm + C::kOffScale + (blk & 3u) * 1024;
-          reinterpret_cast<float4*>(sc)[lane] = make_float4(kf[0], kf[1], kf[2], kf[3]);
-          reinterpret_cast<float4*>(sc + 512)[lane] = make_float4(vf[0], vf[1], vf[2], vf[3]);
-          if (lane == 0) *reinterpret_cast<float*>(bars + 56 + (blk & 3u)) = (float)((int)top - 127);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar.sc_full + 8 * (blk & 3u));
-        }
-        ++blk;
+    auto process = [&](const uint4 (&x)[kUnits], bool value) {
+      if (!mbar_wait_all(bar.empty + 8 * ring.i, ring.pass ^ 1u)) {
+        raise_error(p.err, kErrTimeout);
+        return false;
       }
       const bool wide = value && D == 256;
       uint8_t* st = sm + C::kOffStage + ring.i * kStage;
@@ -542,17 +554,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       for (int u = 0; u < kUnits; ++u) {
         const int unit = u * 32 * kConv + ct;
         const int row = wide ? unit >> 4 : unit >> 3, d = wide ? (unit & 15) * 16 : (unit & 7) * 16;
-        const uint32_t c[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-        uint32_t o[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 a = e4m3x2_to_float2((uint16_t)(c[i] & 0xFFFFu)), b = e4m3x2_to_float2((uint16_t)(c[i] >> 16));
-          o[2 * i] = pack_bf2(a.x, a.y);
-          o[2 * i + 1] = pack_bf2(b.x, b.y);
-        }
+        const uint2 a = e4m3x4_to_half4(x[u].x), b = e4m3x4_to_half4(x[u].y), c = e4m3x4_to_half4(x[u].z), e = e4m3x4_to_half4(x[u].w);
+        const uint4 first = make_uint4(a.x, a.y, b.x, b.y), second = make_uint4(c.x, c.y, e.x, e.y);
         uint8_t* to = st + (d >> 6) * (wide ? 8192 : 16384) + row * 128;
         const int c0 = ((d & 63) >> 3) ^ (row & 7);
-        const uint4 first = make_uint4(o[0], o[1], o[2], o[3]), second = make_uint4(o[4], o[5], o[6], o[7]);
         // lanes of neighbouring 64-value blocks share banks: they write their halves in opposite order
         const bool odd = (d >> 6) & 1;
         *reinterpret_cast<uint4*>(to + ((odd ? c0 ^ 1 : c0) << 4)) = odd ? second : first;
@@ -564,17 +569,19 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       ring.step();
       return true;
     };
-    if (walk.left > 0) {
+    if (start->left > 0) {
+      // one copy of the code: the waiting loads move up by a place instead
+#pragma unroll 1
+      for (int have = 0;;) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) fetch(raw[i], meta[i], kb[i], vb[i], have[i]);
-      for (bool on = true; on;) {
+        for (int i = 0; i + 1 < kAhead; ++i) {
+          what[i] = what[i + 1];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (on) {
-            on = meta[i] >= 0 && process(raw[i], meta[i], kb[i], vb[i], have[i]);
-            if (on) fetch(raw[i], meta[i], kb[i], vb[i], have[i]);
-          }
+          for (int u = 0; u < kUnits; ++u) raw[i][u] = raw[i + 1][u];
         }
+        fetch(raw[kAhead - 1], what[kAhead - 1]);
+        if (++have < kAhead) continue;
+        if (what[0] < 0 || !process(raw[0], what[0])) break;
       }
     }
     finish();
@@ -584,7 +591,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   if (warp == C::kSoftWarps) {
     // ------------------------------------------------------------------ the products
     if (lane == 0) {
-      constexpr uint32_t kIdQK = idesc_bf16_f32(128, 128), kIdPV = idesc_bf16_f32_bmn(128, D);
+      // e4m3: both operands are binary16 (the format fields of the descriptor are zero)
+      constexpr uint32_t kF16 = kE4M3 ? ~((1u << 7) | (1u << 10)) : ~0u;
+      constexpr uint32_t kIdQK = idesc_bf16_f32(128, 128) & kF16, kIdPV = idesc_bf16_f32_bmn(128, D) & kF16;
       constexpr uint32_t kVBlock = D == 256 ? 8192 : 16384;  // bytes between 64-value blocks of a value stage
       Ring<kStages> ring;
       uint32_t q_par[2] = {0, 0}, n_blk[2] = {0, 0};
@@ -685,6 +694,65 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       // every product has ended, and every arrival it owes, before the CTA does
       mma_commit(bar.done);
       mbar_wait(bar.done, 0, kWaitLimit);
+    }
+  } else if (kE4M3 && warp == C::kSoftWarps + 1) {
+    // ------------------------------------------------------------------ e4m3: pages and scales of the blocks
+    const int shift = p.cache.page_shift;
+    BlockMeta* metas = reinterpret_cast<BlockMeta*>(sm + C::kOffScale);
+    uint32_t blk = 0;
+    auto page_of = [&](int j) {  // of the lane-th page of block j
+      const int key = j * kBlock + (lane << shift);
+      return (lane << shift) < kBlock && key < seg.keys
+                 ? (int)ld_ahead4(p.cache.table + (long)seg.n * p.cache.max_pages + (key >> shift))
+                 : 0;
+    };
+    while (ok && walk.next(p, step, seg)) {
+      if (seg.keys <= 0) continue;
+      int next = page_of(seg.j0);
+      for (int j = seg.j0; j < seg.j1; ++j, ++blk) {
+        int id = next;
+        if ((unsigned)id >= (unsigned)p.cache.num_pages) {
+          raise_error(p.err, kErrDeviceArgument);
+          id = 0;
+        }
+        if (j + 1 < seg.j1) next = page_of(j + 1);
+        const int row = (id * p.Hkv + seg.hk) << shift, have = min(seg.keys - j * kBlock, kBlock);
+        // the exponent bytes of four keys
+        const int at = __shfl_sync(0xFFFFFFFFu, row, (lane * 4) >> shift) + ((lane * 4) & ((1 << shift) - 1));
+        uint32_t k4 = 0, v4 = 0;
+        if (lane * 4 < have) {
+          k4 = ld_ahead4(p.cache.k_scale + at);
+          v4 = ld_ahead4(p.cache.v_scale + at);
+        }
+        if (!await(bar.meta_empty + 8 * (blk % kMeta), (blk / kMeta & 1u) ^ 1u)) break;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, lane * 4 + i < have ? (v4 >> (8 * i)) & 255u : 0u);
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        float kf[4], vf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = lane * 4 + i < have;
+          const int diff = (int)((v4 >> (8 * i)) & 255u) - (int)top + (int)kWeight;
+          kf[i] = in ? e8m0_value((k4 >> (8 * i)) & 255u) * p.scale_log2 : 0.f;
+          vf[i] = in && diff >= -126 ? __uint_as_float((uint32_t)(127 + diff) << 23) : 0.f;
+        }
+        BlockMeta& m = metas[blk % kMeta];
+        reinterpret_cast<float4*>(m.kf)[lane] = make_float4(kf[0], kf[1], kf[2], kf[3]);
+        reinterpret_cast<float4*>(m.vf)[lane] = make_float4(vf[0], vf[1], vf[2], vf[3]);
+        if (lane < 8) m.row[lane] = row;
+        if (lane == 0) {
+          m.ev = (float)((int)top - 127);
+          m.have = have;
+          m.flags = (j == seg.j0 ? kFirst : 0) | (j + 1 == seg.j1 ? kLast : 0);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.meta_full + 8 * (blk % kMeta));
+      }
+    }
+    if (ok && await(bar.meta_empty + 8 * (blk % kMeta), (blk / kMeta & 1u) ^ 1u) && lane == 0) {
+      metas[blk % kMeta].flags = kEnd;
+      mbar_arrive(bar.meta_full + 8 * (blk % kMeta));
     }
   } else if (!kE4M3 && warp == C::kSoftWarps + 1) {
     // ------------------------------------------------------------------ K and V by TMA

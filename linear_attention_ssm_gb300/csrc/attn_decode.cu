@@ -89,19 +89,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// four e4m3 codes -> two pairs of binary16 values, low codes first
-__device__ __forceinline__ uint2 e4m3x4_to_half4(uint32_t v) {
-  uint2 r;
-  asm("{\n.reg .b16 lo, hi;\nmov.b32 {lo, hi}, %2;\n"
-      "cvt.rn.f16x2.e4m3x2 %0, lo;\ncvt.rn.f16x2.e4m3x2 %1, hi;\n}"
-      : "=r"(r.x), "=r"(r.y)
-      : "r"(v));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -433,15 +420,14 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
             o[a][t][3] *= f[1];
           }
         }
-        // weights 2^(s - m + d), d <= 0 the distance of this group's unit from O's; cut off at -40 for l,
-        // lest a group of tiny values vanish from it
-        float off[2], back[2], rest[2];
+        // weights 2^(s - m + d), d <= 0 the distance of this group's unit from O's; cut off at -40, lest a
+        // group of tiny values vanish from l (P is zero in binary16 long before)
+        float off[2], back[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float mk = m[a][k], e = kE4M3 && mk > -INFINITY ? mk + ev - r[a][k] : 0.f, d = fmaxf(e, -40.f);
-          off[k] = mk > -INFINITY ? d - mk : 0.f;
-          back[k] = kE4M3 ? ex2_approx(-d) : 1.f;
-          rest[k] = e < d ? ex2_approx(e - d) : 1.f;
+          const float mk = m[a][k], e = kE4M3 && mk > -INFINITY ? fmaxf(mk + ev - r[a][k], -40.f) : 0.f;
+          off[k] = mk > -INFINITY ? e - mk : 0.f;
+          back[k] = kE4M3 ? ex2_approx(-e) : 1.f;
         }
 #pragma unroll
         for (int y = 0; y < kTwo; ++y) {
@@ -452,8 +438,8 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
             w[1][k] = ex2_approx(x[y][1][k] + off[k]);
             l[a][k] = kE4M3 ? fmaf(w[0][k] + w[1][k], back[k], l[a][k]) : l[a][k] + (w[0][k] + w[1][k]);
             if constexpr (kE4M3) {
-              w[0][k] *= vf[y][0] * rest[k];
-              w[1][k] *= vf[y][1] * rest[k];
+              w[0][k] *= vf[y][0];
+              w[1][k] *= vf[y][1];
             }
           }
           pb[a][y][0] = transpose8x8(kE4M3 ? pack_half2(w[0][0], w[0][1]) : pack_bf2(w[0][0], w[0][1]));

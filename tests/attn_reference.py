@@ -74,11 +74,15 @@ def attention(q, cache, table, q_lens, kv_lens, scale, z=None):
 
     Counted: scores are fp32 sums of D products (D * 2^-24 of the sum of magnitudes, and 2^-22 of
     the score's own size for its scaling and subtraction), so each weight is off by at most that
-    relatively; the weights (e4m3: each already times its value row's power of two, which is exact)
-    are rounded to bf16 (2^-8); numerator and denominator both carry the error; sums over n keys add
-    n * 2^-24; the result is rounded to bf16 (2^-8)."""
+    relatively; the weights are rounded to bf16 (2^-8); numerator and denominator both carry the error;
+    sums over n keys add n * 2^-24; the result is rounded to bf16 (2^-8).  e4m3: the queries are
+    rounded to binary16 after division by a power of two that leaves the largest below 2 (2^-25 of it
+    where they leave the normal range), the weights (times their value row's power of two over the
+    largest, times 2^7) to binary16: 2^-11, or 2^-25 of 2^-7 of a unit that is at most twice the
+    largest value, for each key."""
     hq, D = q.shape[1], q.shape[2]
     out, tol = [torch.zeros(q.shape, dtype=torch.float64, device=q.device) for _ in range(2)]
+    e4m3 = cache.k_scale is not None
     first = 0
     for n, (ql, kv) in enumerate(zip(q_lens, kv_lens)):
         lo, first = first, first + ql
@@ -99,7 +103,11 @@ def attention(q, cache, table, q_lens, kv_lens, scale, z=None):
         rel = (D * 2.0 ** -24 * mag + 2.0 ** -22 * (s.abs() + top.abs())).masked_fill(hidden, 0.0).amax(-1, keepdim=True)
         o = torch.einsum("hgtj,hjd->hgtd", w, v)
         size = torch.einsum("hgtj,hjd->hgtd", w, v.abs())
-        err = (2.0 ** -8 + 2 * rel + 2 * kv * 2.0 ** -24 + 2.0 ** -20) * size
+        if e4m3:
+            rel = rel + 2.0 ** -25 * scale * (qd.abs().amax(-1)[..., None] * k.abs().sum(-1)[:, None, None]).amax(-1, keepdim=True)
+        err = (2.0 ** (-11 if e4m3 else -8) + 2 * rel + 2 * kv * 2.0 ** -24 + 2.0 ** -20) * size
+        if e4m3:
+            err = err + kv * 2.0 ** -31 * v.abs().amax((1, 2))[:, None, None, None]
         pack = lambda x: x.permute(2, 0, 1, 3).reshape(ql, hq, D)  # noqa: E731
         o, err = pack(o), pack(err)
         if z is not None:
