@@ -11,9 +11,11 @@
 // tiles a CTA, a slot each (kTiles = 2: K and V are read once for 256 rows); otherwise the blocks of
 // one tile alternate between the slots (kTiles = 1; at D = 256 O alone fills half the tensor memory).
 //
-// Warps: four a tile for the softmax, one that issues the products, one that loads K and V by TMA
-// into a ring of 32 KB stages, one that zeroes the value rows behind the last key (a page's unused rows
-// may hold anything, and 0 * NaN is not 0).
+// Warps: four a tile for the softmax; two that issue products (a tile's each, or with one tile one for
+// the scores and one for O), so that one's waiting does not idle the tensor cores; one that loads Q, K and
+// V by TMA, K and V into a ring of 32 KB stages; one that zeroes the value rows behind the last key (a
+// page's unused rows may hold anything, and 0 * NaN is not 0).  An e4m3 cache has four or eight warps
+// that widen its codes into the stages instead of the last two, and one that reads pages and scales ahead.
 //
 // Work: the (tile, block) pairs of all sequences in one line, cut into one equal piece for each SM.  A
 // tile that a cut falls into leaves its parts (O, m, l) in the workspace for a second kernel to join,
@@ -57,6 +59,8 @@ struct Cfg {
   static constexpr uint32_t kOffQs = kOffScale + (kE4M3 ? kMeta * sizeof(BlockMeta) : 0);
   static constexpr uint32_t kOffBar = kOffQs + (kE4M3 ? kTiles * 512 : 0);
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;  // barriers; alignment of the base
+  // of the four warps behind the softmax's: the products (two), loads or scales, value rows behind the last key
+  static constexpr int kMma0 = kSoftWarps, kMma1 = kSoftWarps + 1, kLoad = kSoftWarps + 2, kTail = kSoftWarps + 3;
   static constexpr uint32_t kColO = 256;                    // tensor memory: two S slots of 128 columns, then O
   // Registers: the softmax warps hold a row of 128 scores each, the others need few.  The shares of the
   // warpgroups come to no more than the launch's: 512 threads of 128, 384 of 168; 256 threads have
@@ -71,7 +75,7 @@ struct Cfg {
 };
 
 struct Bars {
-  uint32_t full, empty, tail, s_full, p_full, o_full, q_full, done, meta_full, meta_empty;  // shared addresses of the first of each kind
+  uint32_t full, empty, tail, s_full, p_full, o_full, q_full, q_empty, done, meta_full, meta_empty;  // shared addresses of the first of each kind
 };
 
 // 64 columns of this warp's 32 lanes.  The wait for the load is a statement of its own (two loads, one
@@ -140,6 +144,18 @@ __device__ __forceinline__ uint32_t ld_ahead4(const void* p) {
   return v;
 }
 
+// 32 bytes of one thread (aligned to them): a whole sector
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, kWaitLimit));
 }
@@ -164,24 +180,25 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   const int step = kTiles * p.sub;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 44);
-  WalkStart* start = reinterpret_cast<WalkStart*>(bars + 46);
-  long* scan = reinterpret_cast<long*>(bars + 52);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 46);
+  WalkStart* start = reinterpret_cast<WalkStart*>(bars + 48);
+  long* scan = reinterpret_cast<long*>(bars + 56);
   const uint32_t b0 = smem_u32(bars);
-  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26, b0 + 8 * 27, b0 + 8 * 35};
+  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26, b0 + 8 * 28, b0 + 8 * 29, b0 + 8 * 37};
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar.full + 8 * i, kE4M3 ? C::kConvWarps : 1);
-      mbar_init(bar.empty + 8 * i, 1);
+      mbar_init(bar.empty + 8 * i, kTiles);
       mbar_init(bar.tail + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar.s_full + 8 * i, 1);
       mbar_init(bar.p_full + 8 * i, 4);
       mbar_init(bar.o_full + 8 * i, 1);
-      mbar_init(bar.q_full + 8 * i, 4);
+      mbar_init(bar.q_full + 8 * i, kE4M3 ? 4 : 1);
+      mbar_init(bar.q_empty + 8 * i, 1);
     }
-    mbar_init(bar.done, 1);
+    mbar_init(bar.done, 2);
     if constexpr (kE4M3) {
       for (int i = 0; i < kMeta; ++i) {
         mbar_init(bar.meta_full + 8 * i, 1);
@@ -192,6 +209,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     if constexpr (!kE4M3) {
       prefetch_tensormap(&p.tmap_k);
       prefetch_tensormap(&p.tmap_v);
+      prefetch_tensormap(&p.tmap_q);
     }
     start->left = 0;
     p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -256,48 +274,51 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
         continue;
       }
-      // Q into shared memory, each warp its own rows; zeros in the rows beyond the tile's last (what a warp
-      // without rows leaves there stays in rows that nobody reads).  e4m3: in binary16, divided by the
-      // power of two of the row's largest value.
       float unit = p.scale_log2;  // log2 units of this row's scores
-      if (w4 * 32 < rows) {
-        constexpr int kPer = D / 8, kRowsAt = 32 / kPer;  // 16-byte pieces of a row, rows of a warp at a time
-        const int piece = lane % kPer;
-        const uint16_t* src = p.q + (long)hk * p.G * D + piece * 8;
-        float* qs = reinterpret_cast<float*>(sm + C::kOffQs) + sub * 128;
-#pragma unroll 4
-        for (int i = 0; i < 32; i += kRowsAt) {
-          const int r = w4 * 32 + i + lane / kPer, t = r / p.G;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (r < rows)
-            x = __ldg(reinterpret_cast<const uint4*>(src + ((long)(row0 + t) * p.Hq + (r - t * p.G)) * D));
-          if constexpr (kE4M3) {
-            uint32_t y[4] = {x.x, x.y, x.z, x.w}, top = 0;
+      if constexpr (kE4M3) {
+        // Q into shared memory, each warp its own rows (zeros in those beyond the tile's last), in binary16,
+        // divided by the power of two of the row's largest value
+        if (w4 * 32 < rows) {
+          constexpr int kPer = D / 8, kRowsAt = 32 / kPer;  // 16-byte pieces of a row, rows of a warp at a time
+          const int piece = lane % kPer;
+          const uint16_t* src = p.q + (long)hk * p.G * D + piece * 8;
+          float* qs = reinterpret_cast<float*>(sm + C::kOffQs) + sub * 128;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 32; i0 += 8 * kRowsAt) {
+            uint4 x[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t lo = y[k] << 16 & 0x7FFFFFFFu, hi = y[k] & 0x7FFF0000u;
-              top = max(top, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+            for (int i = 0; i < 8; ++i) {
+              const int rr = w4 * 32 + i0 + i * kRowsAt + lane / kPer, t = (rr * p.inv_g) >> 16;
+              x[i] = make_uint4(0, 0, 0, 0);
+              if (rr < rows) x[i] = ld_ahead16(src + ((long)(row0 + t) * p.Hq + (rr - t * p.G)) * D);
             }
 #pragma unroll
-            for (int w = kPer / 2; w > 0; w >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
-            const int e = min(max((int)(top >> 23) - 127, -120), 126);
-            const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+            for (int i = 0; i < 8; ++i) {
+              const int rr = w4 * 32 + i0 + i * kRowsAt + lane / kPer;
+              uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, top = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              y[k] = pack_half2(__uint_as_float(y[k] << 16) * inv, __uint_as_float(y[k] & 0xFFFF0000u) * inv);
-            x = make_uint4(y[0], y[1], y[2], y[3]);
-            if (piece == 0) qs[r] = __uint_as_float((uint32_t)(127 + e) << 23);
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t lo = y[k] << 16 & 0x7FFFFFFFu, hi = y[k] & 0x7FFF0000u;
+                top = max(top, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+              }
+#pragma unroll
+              for (int w = kPer / 2; w > 0; w >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
+              const int e = min(max((int)(top >> 23) - 127, -120), 126);
+              const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                y[k] = pack_half2(__uint_as_float(y[k] << 16) * inv, __uint_as_float(y[k] & 0xFFFF0000u) * inv);
+              if (piece == 0) qs[rr] = __uint_as_float((uint32_t)(127 + e) << 23);
+              *reinterpret_cast<uint4*>(sq + sw128_offset(rr, piece * 8, 16384)) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
           }
-          *reinterpret_cast<uint4*>(sq + sw128_offset(r, piece * 8, 16384)) = x;
-        }
-        if constexpr (kE4M3) {
           __syncwarp();
           unit = qs[row];
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && rows > 0) mbar_arrive(bar.q_full + 8 * sub);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0 && rows > 0) mbar_arrive(bar.q_full + 8 * sub);
       float m = -INFINITY, l = 0.f, r = -INFINITY;
       const int last = seg.pos0 + sub * p.sub + tok_in;  // the row's position: its last visible key
       const bool busy = w4 * 32 < rows;                   // this warp has rows at all
@@ -424,48 +445,51 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         const bool whole = seg.j0 == 0 && seg.j1 == seg.nb;
         // O in units of 2^m (half the exponent at a time where both ends of the range meet)
         const float unit_o = kE4M3 && m > -INFINITY ? ex2_approx(0.5f * (r - m - kWeight)) : 1.f;
-        if (whole && busy) {
+        if (busy) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const uint16_t* z = p.z.p + (long)(row0 + tok_in) * p.z.token + (long)(hk * p.G + g) * p.z.head;
+          const int part = 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0);
+          float4* dst = p.part + (long)part * (kPartBytes / sizeof(float4)) + sub * (D / 4) * 128 + row;
+          if (!whole) p.ml[(long)part * 256 + sub * 128 + row] = make_float2(m, l);
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(t_o + c, o);
-            if (mine) {
+          for (int c = 0; c < D; c += 64) {
+            uint32_t o[64];
+            tmem_ld64_begin(t_o + c, o);
+            tmem_ld64_wait(o);
+            auto value = [&](int i) { return kE4M3 ? __uint_as_float(o[i]) * unit_o * unit_o : __uint_as_float(o[i]); };
+            if (!whole) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                float y[8];
+              for (int i = 0; i < 16; ++i)
+                dst[(c / 4 + i) * 128] = make_float4(value(4 * i), value(4 * i + 1), value(4 * i + 2), value(4 * i + 3));
+            } else if (mine) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0.f : kE4M3 ? o[i + k] * unit_o * inv * unit_o : o[i + k] * inv;  // no visible key: zero
-                if (p.z.p) {
-                  const uint4 zz = __ldg(reinterpret_cast<const uint4*>(z + c + i));
-                  const uint32_t zr[4] = {zz.x, zz.y, zz.z, zz.w};
+              for (int i = 0; i < 64; i += 16) {
+                uint32_t w[8];
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    y[2 * k] *= sigmoid_fast(__uint_as_float(zr[k] << 16));
-                    y[2 * k + 1] *= sigmoid_fast(__uint_as_float(zr[k] & 0xFFFF0000u));
+                for (int k = 0; k < 2; ++k) {
+                  float y[8];
+#pragma unroll
+                  for (int x = 0; x < 8; ++x) y[x] = l == 0.f ? 0.f : value(i + 8 * k + x) * inv;  // no visible key: zero
+                  if (p.z.p) {
+                    const uint4 zz = __ldg(reinterpret_cast<const uint4*>(z + c + i + 8 * k));
+                    const uint32_t zr[4] = {zz.x, zz.y, zz.z, zz.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                      y[2 * x] *= sigmoid_fast(__uint_as_float(zr[x] << 16));
+                      y[2 * x + 1] *= sigmoid_fast(__uint_as_float(zr[x] & 0xFFFF0000u));
+                    }
                   }
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) w[4 * k + x] = pack_bf2(y[2 * x], y[2 * x + 1]);
                 }
-                *reinterpret_cast<uint4*>(out + c + i) =
-                    make_uint4(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7]));
+                if (p.wide_out) {
+                  st_global32(out + c + i, w);
+                } else {
+                  *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                  *reinterpret_cast<uint4*>(out + c + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
               }
             }
-          }
-        } else if (busy) {
-          const int slot = 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0);
-          p.ml[(long)slot * 256 + sub * 128 + row] = make_float2(m, l);
-          float4* dst = p.part + (long)slot * (kPartBytes / sizeof(float4)) + sub * (D / 4) * 128 + row;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(t_o + c, o);
-            if constexpr (kE4M3) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = o[i] * unit_o * unit_o;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[(c / 4 + i) * 128] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
         if (!whole && warp == 0 && lane == 0)
@@ -493,6 +517,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     uint32_t blk = 0;          // the latest block whose keys were or are being fetched
     int mode = 0, part = 0;    // 0: keys of blk, 1: values of the block before, 2: values of blk
     int flags = 0;
+    // A thread's 16 codes of a stage, unit u: 128 rows of 128 codes (narrow), or 64 of 256 (a block's
+    // values at D = 256: wide).  Lanes 0-3 take a row's 64 neighbouring codes, lanes 4-7 those of the row
+    // below, so that the swizzle spreads eight lanes' stores over all banks.
+    const int piece = lane & 3, odd = lane >> 2 & 1, cw = ct >> 5;
+    const int row_narrow = cw * 4 + (lane >> 4) * 2 + odd, blk_narrow = lane >> 3 & 1, row_wide = cw * 2 + odd, blk_wide = lane >> 3;
+    const int d_narrow = blk_narrow * 64 + piece * 16, d_wide = blk_wide * 64 + piece * 16;
+    const int c_narrow = (2 * piece) ^ (row_narrow & 7), c_wide = (2 * piece) ^ (row_wide & 7);
+    const int to_narrow = blk_narrow * 16384 + row_narrow * 128 + c_narrow * 16, to_wide = blk_wide * 8192 + row_wide * 128 + c_wide * 16;
+    const int other_narrow = ((c_narrow ^ 1) - c_narrow) * 16, other_wide = ((c_wide ^ 1) - c_wide) * 16;  // to the second half
     uint4 raw[kAhead][kUnits] = {};
     int what[kAhead] = {};     // 0: keys, 1: values, -1: no more
     auto release = [&](uint32_t b) {
@@ -509,17 +542,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           return;
         }
       }
-      const bool value = mode != 0, wide = value && D == 256;  // wide: 64 rows of 256 codes, else 128 rows of 128
+      const bool value = mode != 0, wide = value && D == 256;
       const BlockMeta& meta = metas[(mode == 1 ? blk - 1 : blk) % kMeta];
-      const uint8_t* src = static_cast<const uint8_t*>(value ? p.cache.v : p.cache.k);
-      const int have = meta.have;
+      const uint8_t* src = static_cast<const uint8_t*>(value ? p.cache.v : p.cache.k) + (wide ? d_wide : d_narrow + (value ? 0 : part * 128));
+      const int first = wide ? row_wide + part * 64 : row_narrow, last = meta.have - 1;
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int unit = u * 32 * kConv + ct;
-        const int row = wide ? (unit >> 4) + part * 64 : unit >> 3;  // key of the block
-        const int d = wide ? (unit & 15) * 16 : (unit & 7) * 16 + (value ? 0 : part * 128);
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (row < have) x[u] = ld_ahead16(src + (long)(meta.row[row >> shift] + (row & ((1 << shift) - 1))) * D + d);
+        // key of the block; behind the last visible one that one again (its scores are masked, its weights 0)
+        const int row = min(first + u * (wide ? 2 * kConv : 4 * kConv), last);
+        x[u] = ld_ahead16(src + (long)(meta.row[row >> shift] + (row & ((1 << shift) - 1))) * D);
       }
       is = value;
       if (++part == kParts) {
@@ -549,19 +580,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         return false;
       }
       const bool wide = value && D == 256;
-      uint8_t* st = sm + C::kOffStage + ring.i * kStage;
+      uint8_t* to = sm + C::kOffStage + ring.i * kStage + (wide ? to_wide : to_narrow);
+      const int other = wide ? other_wide : other_narrow;
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
-        const int unit = u * 32 * kConv + ct;
-        const int row = wide ? unit >> 4 : unit >> 3, d = wide ? (unit & 15) * 16 : (unit & 7) * 16;
         const uint2 a = e4m3x4_to_half4(x[u].x), b = e4m3x4_to_half4(x[u].y), c = e4m3x4_to_half4(x[u].z), e = e4m3x4_to_half4(x[u].w);
-        const uint4 first = make_uint4(a.x, a.y, b.x, b.y), second = make_uint4(c.x, c.y, e.x, e.y);
-        uint8_t* to = st + (d >> 6) * (wide ? 8192 : 16384) + row * 128;
-        const int c0 = ((d & 63) >> 3) ^ (row & 7);
-        // lanes of neighbouring 64-value blocks share banks: they write their halves in opposite order
-        const bool odd = (d >> 6) & 1;
-        *reinterpret_cast<uint4*>(to + ((odd ? c0 ^ 1 : c0) << 4)) = odd ? second : first;
-        *reinterpret_cast<uint4*>(to + ((odd ? c0 : c0 ^ 1) << 4)) = odd ? first : second;
+        uint8_t* at = to + u * (wide ? 2 * kConv : 4 * kConv) * 128;
+        *reinterpret_cast<uint4*>(at) = make_uint4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<uint4*>(at + other) = make_uint4(c.x, c.y, e.x, e.y);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -570,123 +596,122 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       return true;
     };
     if (start->left > 0) {
-      // one copy of the code: the waiting loads move up by a place instead
-#pragma unroll 1
-      for (int have = 0;;) {
+      for (bool on = true, primed = false; on; primed = true) {
 #pragma unroll
-        for (int i = 0; i + 1 < kAhead; ++i) {
-          what[i] = what[i + 1];
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) raw[i][u] = raw[i + 1][u];
+        for (int i = 0; i < kAhead; ++i) {
+          if (on && primed) on = what[i] >= 0 && process(raw[i], what[i]);
+          if (on) fetch(raw[i], what[i]);
         }
-        fetch(raw[kAhead - 1], what[kAhead - 1]);
-        if (++have < kAhead) continue;
-        if (what[0] < 0 || !process(raw[0], what[0])) break;
       }
     }
     finish();
     return;
   }
   if constexpr (C::kSplit) regs_dec<C::kRegAux>();
-  if (warp == C::kSoftWarps) {
+  if (warp == C::kMma0 || warp == C::kMma1) {
     // ------------------------------------------------------------------ the products
     if (lane == 0) {
       // e4m3: both operands are binary16 (the format fields of the descriptor are zero)
       constexpr uint32_t kF16 = kE4M3 ? ~((1u << 7) | (1u << 10)) : ~0u;
       constexpr uint32_t kIdQK = idesc_bf16_f32(128, 128) & kF16, kIdPV = idesc_bf16_f32_bmn(128, D) & kF16;
       constexpr uint32_t kVBlock = D == 256 ? 8192 : 16384;  // bytes between 64-value blocks of a value stage
+      const int which = warp - C::kMma0;
       Ring<kStages> ring;
-      uint32_t q_par[2] = {0, 0}, n_blk[2] = {0, 0};
+      uint32_t q_par = 0, n_blk = 0;
+      // a stage's share of the scores, and of O
+      auto qk = [&](int sub, uint32_t slot, int part) {
+        const uint32_t q = sb + sub * 128 * D * 2, k = sb + C::kOffStage + ring.i * kStage;
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+          mma_bf16_k4<2, 2>(tmem + slot * 128, sw128_desc(q + (2 * part + d) * 16384), sw128_desc(k + d * 16384), kIdQK,
+                            part + d > 0);
+      };
+      auto pv = [&](int sub, uint32_t slot, int part, bool acc) {
+        const uint32_t v = sb + C::kOffStage + ring.i * kStage;
+        constexpr int kSteps = 2 / kParts;  // 64 keys each
+#pragma unroll
+        for (int d = 0; d < kSteps; ++d)
+          mma_bf16_k4_ta<128>(tmem + C::kColO + sub * D, tmem + slot * 128 + (part * kSteps + d) * 32,
+                              sw128_mn_desc(v + d * 8192, kVBlock), kIdPV, acc || d > 0);
+      };
       while (ok && walk.next(p, step, seg)) {
-        const int two = kTiles == 2 && seg.ntok > p.sub ? 2 : 1;
-        if (seg.keys > 0) {
-          for (int t = 0; t < two; ++t) {
-            await_one(bar.q_full + 8 * t, q_par[t]);
-            q_par[t] ^= 1u;
+        if (seg.keys <= 0) continue;
+        if constexpr (kTiles == 2) {
+          // this tile's K0 V0 K1 V1 ..; both tiles let go of every stage
+          const int t = which;
+          const bool mine = t == 0 || seg.ntok > p.sub;
+          if (mine) {
+            if (!await_one(bar.q_full + 8 * t, q_par)) break;
+            q_par ^= 1u;
           }
-          if (!ok) break;
-          tc_fence_after();
-          auto qk = [&](int sub, uint32_t slot, const Ring<kStages>& r, int part) {
-            const uint32_t q = sb + sub * 128 * D * 2, k = sb + C::kOffStage + r.i * kStage;
-#pragma unroll
-            for (int d = 0; d < 2; ++d)
-              mma_bf16_k4<2, 2>(tmem + slot * 128, sw128_desc(q + (2 * part + d) * 16384), sw128_desc(k + d * 16384),
-                                kIdQK, part + d > 0);
-          };
-          auto pv = [&](int sub, uint32_t slot, const Ring<kStages>& r, int part, bool acc) {
-            const uint32_t v = sb + C::kOffStage + r.i * kStage;
-            constexpr int kSteps = 2 / kParts;  // 64 keys each
-#pragma unroll
-            for (int d = 0; d < kSteps; ++d)
-              mma_bf16_k4_ta<128>(tmem + C::kColO + sub * D, tmem + slot * 128 + (part * kSteps + d) * 32,
-                                  sw128_mn_desc(v + d * 8192, kVBlock), kIdPV, acc || d > 0);
-          };
-          if constexpr (kTiles == 2) {
-            Ring<kStages> r = ring;
-            if (!await_one(bar.full + 8 * r.i, r.pass)) break;
-            tc_fence_after();
-            for (int t = 0; t < two; ++t) {
-              qk(t, t, r, 0);
-              mma_commit(bar.s_full + 8 * t);
-            }
-            mma_commit(bar.empty + 8 * r.i);
-            ring.step();
-            for (int j = seg.j0; j < seg.j1 && ok; ++j) {
-              const Ring<kStages> rv = ring;
-              Ring<kStages> rk = ring;
-              rk.step();
-              const bool more = j + 1 < seg.j1;
-              if (!await_one(bar.full + 8 * rv.i, rv.pass)) break;
-              for (int t = 0; t < two; ++t) {
-                if (!await_one(bar.p_full + 8 * t, n_blk[t] & 1u)) break;
-                ++n_blk[t];
+          const int last = seg.j1 - 1;
+          for (int j = seg.j0 - 1; j <= last && ok; ++j) {
+            if (j >= seg.j0) {
+              if (mine && !await_one(bar.p_full + 8 * t, n_blk & 1u)) break;
+              ++n_blk;
+              if (!await_one(bar.full + 8 * ring.i, ring.pass)) break;
+              if (mine) {
                 tc_fence_after();
-                pv(t, t, rv, 0, j > seg.j0);
+                pv(t, t, 0, j > seg.j0);
                 mma_commit(bar.o_full + 8 * t);
-                if (t == two - 1) mma_commit(bar.empty + 8 * rv.i);
-                if (more) {
-                  if (t == 0) {
-                    if (!await_one(bar.full + 8 * rk.i, rk.pass)) break;
-                    tc_fence_after();
-                  }
-                  qk(t, t, rk, 0);
-                  mma_commit(bar.s_full + 8 * t);
-                  if (t == two - 1) mma_commit(bar.empty + 8 * rk.i);
-                }
+                mma_commit(bar.empty + 8 * ring.i);
+              } else {
+                mbar_arrive(bar.empty + 8 * ring.i);
               }
               ring.step();
-              if (more) ring.step();
             }
-          } else {
-            uint32_t b_qk = n_blk[0];  // blocks whose scores have been issued: the slot goes by it
-            auto scores = [&]() {
-              for (int part = 0; part < kParts; ++part) {
-                if (!await_one(bar.full + 8 * ring.i, ring.pass)) return;
+            if (j < last) {
+              if (!await_one(bar.full + 8 * ring.i, ring.pass)) break;
+              if (mine) {
                 tc_fence_after();
-                qk(0, b_qk & 1u, ring, part);
+                qk(t, t, 0);
+                mma_commit(bar.s_full + 8 * t);
                 mma_commit(bar.empty + 8 * ring.i);
-                ring.step();
+                if (j + 1 == last) mma_commit(bar.q_empty + 8 * t);
+              } else {
+                mbar_arrive(bar.empty + 8 * ring.i);
               }
-              mma_commit(bar.s_full + 8 * (b_qk & 1u));
-              ++b_qk;
-            };
-            scores();
-            if (ok && seg.j0 + 1 < seg.j1) scores();
-            for (int j = seg.j0; j < seg.j1 && ok; ++j) {
-              const uint32_t slot = n_blk[0] & 1u;
-              if (!await_one(bar.p_full + 8 * slot, (n_blk[0] >> 1) & 1u)) break;
-              ++n_blk[0];
-              tc_fence_after();
+              ring.step();
+            }
+          }
+          if (!mine) n_blk -= seg.j1 - seg.j0;
+        } else {
+          // K0 K1 V0 K2 V1 ..: one warp the keys, one the values
+          const int n = seg.j1 - seg.j0;
+          if (which == 0) {
+            if (!await_one(bar.q_full, q_par)) break;
+            q_par ^= 1u;
+            for (int i = 0; i < n && ok; ++i, ++n_blk) {
+              const uint32_t slot = n_blk & 1u;
+              // the slot's weights have been used: the product of the block two before has ended
+              if (n_blk >= 2 && !await_one(bar.o_full + 8 * slot, ((n_blk - 2) >> 1) & 1u)) break;
               for (int part = 0; part < kParts; ++part) {
                 if (!await_one(bar.full + 8 * ring.i, ring.pass)) break;
                 tc_fence_after();
-                pv(0, slot, ring, part, j > seg.j0 || part > 0);
+                qk(0, slot, part);
+                mma_commit(bar.empty + 8 * ring.i);
+                ring.step();
+              }
+              if (!ok) break;
+              mma_commit(bar.s_full + 8 * slot);
+              if (i + 1 == n) mma_commit(bar.q_empty);
+              ring.skip(i == 0 ? (n == 1 ? kParts : 0) : i + 1 < n ? kParts : 2 * kParts);  // the values in between
+            }
+          } else {
+            ring.skip(n == 1 ? kParts : 2 * kParts);
+            for (int i = 0; i < n && ok; ++i, ++n_blk) {
+              const uint32_t slot = n_blk & 1u;
+              if (!await_one(bar.p_full + 8 * slot, (n_blk >> 1) & 1u)) break;
+              for (int part = 0; part < kParts; ++part) {
+                if (!await_one(bar.full + 8 * ring.i, ring.pass)) break;
+                tc_fence_after();
+                pv(0, slot, part, i > 0 || part > 0);
                 mma_commit(bar.empty + 8 * ring.i);
                 ring.step();
               }
               if (!ok) break;
               mma_commit(bar.o_full + 8 * slot);
-              if (j + 2 < seg.j1) scores();
+              if (i + 2 < n) ring.skip(kParts);
             }
           }
         }
@@ -695,7 +720,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       mma_commit(bar.done);
       mbar_wait(bar.done, 0, kWaitLimit);
     }
-  } else if (kE4M3 && warp == C::kSoftWarps + 1) {
+  } else if (kE4M3 && warp == C::kLoad) {
     // ------------------------------------------------------------------ e4m3: pages and scales of the blocks
     const int shift = p.cache.page_shift;
     BlockMeta* metas = reinterpret_cast<BlockMeta*>(sm + C::kOffScale);
@@ -754,11 +779,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       metas[blk % kMeta].flags = kEnd;
       mbar_arrive(bar.meta_full + 8 * (blk % kMeta));
     }
-  } else if (!kE4M3 && warp == C::kSoftWarps + 1) {
-    // ------------------------------------------------------------------ K and V by TMA
+  } else if (!kE4M3 && warp == C::kLoad) {
+    // ------------------------------------------------------------------ Q, K and V by TMA
     const int page = 1 << p.cache.page_shift, box = min(page, 64), box_shift = min(p.cache.page_shift, 6);
     Ring<kStages> ring;
     uint32_t tails = 0, tail_par = 0, used = 0;  // stages whose last copy went to the tail barrier, its parity; stages in use
+    uint32_t q_pass = 0, q_used = 0;             // bit t: parity of the next Q of tile t; Q was loaded at all
     while (ok && walk.next(p, step, seg)) {
       if (seg.keys > 0) {
         const int hk = seg.hk, keys = seg.keys;
@@ -800,6 +826,19 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             load(&p.tmap_v, j * kBlock + part * 64, 128 / kParts, 0, D / 64, D == 256 ? 8192 : 16384, true);
         };
         keys_of(seg.j0);
+        // the tile's queries (of a packed batch: the rows behind a sequence's last are the next one's, and
+        // stay in rows that nobody reads)
+        for (int t = 0; t < kTiles && ok && (t == 0 || seg.ntok > p.sub); ++t) {
+          if (!await(bar.q_empty + 8 * t, (q_pass >> t & 1u) ^ 1u)) break;
+          q_pass ^= 1u << t;
+          q_used |= 1u << t;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar.q_full + 8 * t, p.sub * p.G * D * 2);
+            for (int d = 0; d < D / 64; ++d)
+              tma_load_3d(sb + t * 128 * D * 2 + d * 16384, &p.tmap_q, d * 64, hk * p.G, seg.row0 + t * p.sub, bar.q_full + 8 * t);
+          }
+        }
+        __syncwarp();
         for (int j = seg.j0; j < seg.j1 && ok; ++j) {
           if (kTiles == 1) {
             if (j + 1 < seg.j1) keys_of(j + 1);
@@ -819,8 +858,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         if (tails >> i & 1u) mbar_wait(bar.tail + 8 * i, (tail_par >> i & 1u) ^ 1u, kWaitLimit);
         else mbar_wait(bar.full + 8 * i, i < ring.i ? ring.pass : ring.pass ^ 1u, kWaitLimit);
       }
+      for (int t = 0; t < kTiles; ++t)
+        if (q_used >> t & 1u) mbar_wait(bar.q_full + 8 * t, (q_pass >> t & 1u) ^ 1u, kWaitLimit);
     }
-  } else if (!kE4M3 && warp == C::kSoftWarps + 2) {
+  } else if (!kE4M3 && warp == C::kTail) {
     // ------------------------------------------------------------------ value rows behind the last key
     Ring<kStages> ring;
     uint32_t used[kStages] = {};  // parity of each stage's tail barrier
@@ -1038,6 +1079,8 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   p.T = T;
   p.sub = 128 / p.G;
   p.lead = 2;
+  p.inv_g = (65535 + p.G) / p.G;
+  p.wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.desc = reinterpret_cast<int4*>(ws);
   p.ml = reinterpret_cast<float2*>(ws + 2 * kMaxCtas * sizeof(int4));
@@ -1058,6 +1101,7 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   if (!cache.e4m3) {
     e = encode_pages(&p.tmap_k, cache.k, cache, Hkv, D);
     if (e == cudaSuccess) e = encode_pages(&p.tmap_v, cache.v, cache, Hkv, D);
+    if (e == cudaSuccess) e = encode_bf16_3d_sw128(&p.tmap_q, q, D, Hq, T, 64, p.G, p.sub);
     if (e != cudaSuccess) return e;
   }
   // two tiles a CTA where a sequence has more rows than one holds, on average

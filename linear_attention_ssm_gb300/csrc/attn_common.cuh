@@ -57,6 +57,7 @@ constexpr int kBlock = 128;     // keys of a block, the unit of work
 struct AttnParams {
   CUtensorMap tmap_k;  // pages as [pages * Hkv * page][D] bf16, box 64 x min(page, 64), 128-byte swizzle
   CUtensorMap tmap_v;
+  CUtensorMap tmap_q;  // [T][Hq][D] bf16, box 64 x G x sub, 128-byte swizzle
   const uint16_t* q;
   PagedCache cache;
   const int32_t* kv_lens;
@@ -67,6 +68,8 @@ struct AttnParams {
   float scale_log2;
   int Hq, Hkv, G, N, T;
   int sub;       // tokens of one tile: 128 / G on the tcgen05 cores, 1 in the one-token kernel
+  int inv_g;     // row / G is (row * inv_g) >> 16 for the rows of a tile
+  bool wide_out; // out is 32-byte aligned
   int lead;      // blocks that beginning and ending a tile cost, in the line of work
   int4* desc;    // [2 * grid] what each part of a cut tile holds: packed row, tokens, key head, flags
   float2* ml;    // [2 * grid][256] maximum (log2 units) and sum of a row
@@ -75,27 +78,29 @@ struct AttnParams {
 
 // ---------------------------------------------------------------- the line of work
 
-// sum_{i < n} floor((a i + b) / m), all arguments >= 0
-__device__ __forceinline__ long floor_sum(long n, long m, long a, long b) {
-  long s = 0;
-  while (n > 0) {
-    if (a >= m) {
-      s += n * (n - 1) / 2 * (a / m);
-      a %= m;
+// sum_{i < n} floor((a i + b) / 128), all arguments >= 0, n < 2^23, a <= 256: lattice points under a line,
+// with the roles of the axes exchanged as in Euclid's algorithm.
+__device__ __forceinline__ long floor_sum128(long n, int a, long b) {
+  long s = n * (n - 1) / 2 * (a >> 7) + n * (b >> 7);
+  uint32_t k = (uint32_t)n, m = 128, x = a & 127, c = (uint32_t)b & 127;
+  for (;;) {
+    const uint32_t y = x * k + c;
+    if (y < m) return s;
+    const uint32_t rows = y / m;
+    c = y - rows * m;
+    k = rows;
+    const uint32_t t = m;
+    m = x;
+    x = t;
+    const uint32_t q = x / m;  // 1 at least, from here on
+    s += (long)k * (k - 1) / 2 * q;
+    x -= q * m;
+    if (c >= m) {
+      const uint32_t r = c / m;
+      s += (long)k * r;
+      c -= r * m;
     }
-    if (b >= m) {
-      s += n * (b / m);
-      b %= m;
-    }
-    const long y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const long t = m;
-    m = a;
-    a = t;
   }
-  return s;
 }
 
 // One sequence's new tokens and cache.
@@ -139,7 +144,7 @@ struct Tiles {
     const long ahead = (long)kBlock - p0;  // tiles with at most one block: (t + 1) step <= ahead
     const int t0 = ahead < step ? 0 : (int)min((long)full, ahead / step);
     long s = t0 + (long)full * lead;
-    if (full > t0) s += floor_sum(full - t0, kBlock, step, (long)(t0 + 1) * step + p0 + kBlock - 1);
+    if (full > t0) s += floor_sum128(full - t0, step, (long)(t0 + 1) * step + p0 + kBlock - 1);
     return s + (i > last ? units(last) : 0);
   }
 };
@@ -214,80 +219,84 @@ struct Walk {
   }
 };
 
+__device__ __forceinline__ long divide(long a, long b) {  // both >= 0, b > 0
+  return (a | b) >> 32 ? a / b : (long)((uint32_t)a / (uint32_t)b);
+}
+
 // This CTA's piece of the line: an equal share of its units, found by the whole CTA.  `scan`: one long
 // for each warp; start->left is 0 before the call and stays 0 for a CTA without work.  The caller
 // synchronises before it reads *start.
 template <int kThreads>
 __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* scan, WalkStart* start) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  long mine = 0;
-  for (int n = tid; n < p.N; n += kThreads) {
-    const SeqInfo s = seq_info(p, n, blockIdx.x == 0);
+  // units of one key head of sequence n
+  auto units_of = [&](int n, bool report) {
+    const SeqInfo s = seq_info(p, n, report);
     const Tiles t = {s.kv - s.len, s.len, step, p.lead};
-    if (s.len > 0) mine += t.before(t.count());
-  }
-  mine *= p.Hkv;
-  long sum = mine;
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  if (lane == 0) scan[warp] = sum;
-  __syncthreads();
-  long total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) total += scan[w];
-  __syncthreads();
-  const long u0 = total / gridDim.x * blockIdx.x + total % gridDim.x * blockIdx.x / gridDim.x;
-  const long u1 = total / gridDim.x * (blockIdx.x + 1) + total % gridDim.x * (blockIdx.x + 1) / gridDim.x;
-  if (u1 > u0) {
-    long base = 0;  // units of the sequences before this round's
-    for (int n0 = 0; n0 < p.N; n0 += kThreads) {
-      const int n = n0 + tid;
-      long u = 0;
-      if (n < p.N) {
-        const SeqInfo s = seq_info(p, n, false);
-        const Tiles t = {s.kv - s.len, s.len, step, p.lead};
-        if (s.len > 0) u = t.before(t.count()) * p.Hkv;
-      }
-      long inc = u;
-      for (int o = 1; o < 32; o <<= 1) {
-        const long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      if (lane == 31) scan[warp] = inc;
-      __syncthreads();
-      long before = base, round = 0;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += scan[w];
-        round += scan[w];
-      }
-      const long lo = before + inc - u;
-      if (u > 0 && u0 >= lo && u0 < lo + u) {
-        start->left = u1 - u0;
-        start->rem = u0 - lo;
-        start->n = n;
-      }
-      base += round;
-      __syncthreads();
-      if (u0 < base) break;
+    return s.len > 0 ? t.before(t.count()) : 0L;
+  };
+  // prefix sums over the threads: this thread's, and everything
+  auto sums = [&](long u, long& before, long& all) {
+    long inc = u;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += x;
     }
-    // the key head, then the tile: every thread looks at one stretch of tiles
-    const SeqInfo s = seq_info(p, start->n, false);
-    const Tiles t = {s.kv - s.len, s.len, step, p.lead};
-    const int count = t.count(), stretch = (count + kThreads - 1) / kThreads;
-    const long per = t.before(count), rem = start->rem % per;
-    const int lo = min(tid * stretch, count), hi = min(lo + stretch, count);
-    if (lo < hi) {
-      long at = t.before(lo);
-      if (rem >= at) {
-        for (int i = lo; i < hi; ++i) {
-          const int nb = t.units(i);
-          if (rem < at + nb) {
-            start->hk = (int)(start->rem / per);
-            start->tile = i;
-            start->j = (int)(rem - at);
-            break;
-          }
-          at += nb;
-        }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    before = inc - u;
+    all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += scan[w];
+      all += scan[w];
+    }
+  };
+  long per = 0, mine = 0, before, total;
+  for (int n = tid; n < p.N; n += kThreads) {
+    per = units_of(n, blockIdx.x == 0);
+    mine += per * p.Hkv;
+  }
+  sums(mine, before, total);
+  const long share = divide(total, gridDim.x), extra = total - share * gridDim.x;
+  const long u0 = share * blockIdx.x + divide(extra * blockIdx.x, gridDim.x);
+  const long u1 = share * (blockIdx.x + 1) + divide(extra * (blockIdx.x + 1), gridDim.x);
+  if (u1 == u0) return;
+  long base = 0;  // units of the sequences before this round's (one round where every thread had one sequence)
+  for (int n0 = 0;; n0 += kThreads) {
+    const int n = n0 + tid;
+    if (p.N > kThreads) {
+      __syncthreads();
+      long all;
+      per = n < p.N ? units_of(n, false) : 0;
+      mine = per * p.Hkv;
+      sums(mine, before, all);
+      before += base;
+      base += all;
+    }
+    if (mine > 0 && u0 >= before && u0 < before + mine) {
+      start->left = u1 - u0;
+      start->n = n;
+      start->hk = (int)divide(u0 - before, per);
+      start->rem = u0 - before - start->hk * per;
+    }
+    if (p.N <= kThreads || u0 < base) break;
+  }
+  __syncthreads();
+  // the tile: every thread looks at one stretch of them
+  const SeqInfo s = seq_info(p, start->n, false);
+  const Tiles t = {s.kv - s.len, s.len, step, p.lead};
+  const int count = t.count(), stretch = (count + kThreads - 1) / kThreads;
+  const long rem = start->rem;
+  const int lo = min(tid * stretch, count), hi = min(lo + stretch, count);
+  if (lo < hi) {
+    long at = lo == 0 ? 0 : t.before(lo);
+    for (int i = lo; i < hi && rem >= at; ++i) {
+      const int nb = t.units(i);
+      if (rem < at + nb) {
+        start->tile = i;
+        start->j = (int)(rem - at);
       }
+      at += nb;
     }
   }
 }
