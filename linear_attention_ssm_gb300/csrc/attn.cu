@@ -156,6 +156,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// 16 columns of this warp's 32 lanes; tmem_st_wait: this thread's stores so far have been done
+__device__ __forceinline__ void tmem_st16_begin(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, kWaitLimit));
 }
@@ -322,6 +333,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       float m = -INFINITY, l = 0.f, r = -INFINITY;
       const int last = seg.pos0 + sub * p.sub + tok_in;  // the row's position: its last visible key
       const bool busy = w4 * 32 < rows;                   // this warp has rows at all
+      // columns at a time: a bf16 block's 128 scores stay in registers; for e4m3, whose code is longer and
+      // shares the instruction cache with the widening warps', 64, read twice
+      constexpr int kCols = kE4M3 ? 64 : kBlock;
       const uint32_t seg_blk = all_blk;
       all_blk += seg.j1 - seg.j0;
       if (kE4M3 && rows <= 0) {  // this tile has no rows in the segment: its warps still let its blocks go
@@ -338,43 +352,48 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           tc_fence_after();
           if (busy) {
             const uint32_t t_s = tmem + lanes + slot * 128;
-            float s[128];
-            {
-              uint32_t lo[64], hi[64];
-              tmem_ld64_begin(t_s, lo);
-              tmem_ld64_begin(t_s + 64, hi);
-              tmem_ld64_wait(lo);
-              tmem_ld64_wait(hi);
-#pragma unroll
-              for (int i = 0; i < 64; ++i) {
-                s[i] = __uint_as_float(lo[i]);
-                s[64 + i] = __uint_as_float(hi[i]);
-              }
-            }
             const int lim = last + 1 - j * kBlock;  // columns from here on are not visible
-            // e4m3: the codes' products become scores by the keys' powers of two
+            const bool masked = __any_sync(0xFFFFFFFFu, lim < kBlock);
             float ev = 0.f;
             const BlockMeta* meta = reinterpret_cast<const BlockMeta*>(sm + C::kOffScale) + blk % kMeta;
             if constexpr (kE4M3) {
               if (!await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) break;
               ev = meta->ev;
+            }
+            // kCols columns from c0 on: scores (e4m3: by the keys' powers of two), those out of sight -inf
+            auto load = [&](int c0, float (&s)[kCols]) {
+              uint32_t x[kCols / 64][64];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float4 k = *reinterpret_cast<const float4*>(meta->kf + 4 * i);
-                s[4 * i] *= k.x;
-                s[4 * i + 1] *= k.y;
-                s[4 * i + 2] *= k.z;
-                s[4 * i + 3] *= k.w;
+              for (int h = 0; h < kCols; h += 64) tmem_ld64_begin(t_s + c0 + h, x[h / 64]);
+#pragma unroll
+              for (int h = 0; h < kCols; h += 64) {
+                tmem_ld64_wait(x[h / 64]);
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s[h + i] = __uint_as_float(x[h / 64][i]);
               }
-            }
-            if (__any_sync(0xFFFFFFFFu, lim < kBlock)) {
+              if constexpr (kE4M3) {
 #pragma unroll
-              for (int i = 0; i < 128; ++i)
-                if (i >= lim) s[i] = -INFINITY;
-            }
-            float mx[4] = {s[0], s[1], s[2], s[3]};
+                for (int i = 0; i < kCols / 4; ++i) {
+                  const float4 k = *reinterpret_cast<const float4*>(meta->kf + c0 + 4 * i);
+                  s[4 * i] *= k.x;
+                  s[4 * i + 1] *= k.y;
+                  s[4 * i + 2] *= k.z;
+                  s[4 * i + 3] *= k.w;
+                }
+              }
+              if (masked) {
 #pragma unroll
-            for (int i = 4; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+                for (int i = 0; i < kCols; ++i)
+                  if (c0 + i >= lim) s[i] = -INFINITY;
+              }
+            };
+            float s[kCols], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int c0 = 0; c0 < kBlock; c0 += kCols) {
+              load(c0, s);
+#pragma unroll
+              for (int i = 0; i < kCols; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+            }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * unit;
             if (top > m + kLazy) {
               l *= ex2_approx(m - top);
@@ -404,29 +423,34 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             const float d = kE4M3 && m > -INFINITY ? fmaxf(e - r, -40.f) : 0.f;
             const float off = m == -INFINITY ? 0.f : d - m;
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int c0 = 0; c0 < kBlock; c0 += kCols) {
+              if (kCols < kBlock) load(c0, s);  // the weights go over scores that have been read
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              float w[16];
+              for (int h = 0; h < kCols / 32; ++h) {
+                float w[16];
 #pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                float x[4];
+                for (int i = 0; i < 16; i += 2) {
+                  float x[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  x[k] = ex2_approx(fmaf(s[32 * h + 2 * i + k], unit, off));
-                  sum[k] += x[k];
+                  for (int k = 0; k < 4; ++k) {
+                    x[k] = ex2_approx(fmaf(s[32 * h + 2 * i + k], unit, off));
+                    sum[k] += x[k];
+                  }
+                  if constexpr (kE4M3) {
+                    const float4 v = *reinterpret_cast<const float4*>(meta->vf + c0 + 32 * h + 2 * i);
+                    x[0] *= v.x;
+                    x[1] *= v.y;
+                    x[2] *= v.z;
+                    x[3] *= v.w;
+                  }
+                  w[i] = __uint_as_float(kE4M3 ? pack_half2(x[0], x[1]) : pack_bf2(x[0], x[1]));
+                  w[i + 1] = __uint_as_float(kE4M3 ? pack_half2(x[2], x[3]) : pack_bf2(x[2], x[3]));
                 }
-                if constexpr (kE4M3) {
-                  const float4 v = *reinterpret_cast<const float4*>(meta->vf + 32 * h + 2 * i);
-                  x[0] *= v.x;
-                  x[1] *= v.y;
-                  x[2] *= v.z;
-                  x[3] *= v.w;
-                }
-                w[i] = __uint_as_float(kE4M3 ? pack_half2(x[0], x[1]) : pack_bf2(x[0], x[1]));
-                w[i + 1] = __uint_as_float(kE4M3 ? pack_half2(x[2], x[3]) : pack_bf2(x[2], x[3]));
+                tmem_st16_begin(t_s + c0 / 2 + 16 * h, w);
               }
-              tmem_st16(t_s + 16 * h, w);
             }
+            tmem_st_wait();
             const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             l += kE4M3 ? all * ex2_approx(-d) : all;
           }
@@ -596,12 +620,18 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       return true;
     };
     if (start->left > 0) {
-      for (bool on = true, primed = false; on; primed = true) {
+      // one copy of the code (the instruction cache is short): the waiting loads move up by a place instead
+#pragma unroll 1
+      for (int have = 0;;) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          if (on && primed) on = what[i] >= 0 && process(raw[i], what[i]);
-          if (on) fetch(raw[i], what[i]);
+        for (int i = 0; i + 1 < kAhead; ++i) {
+          what[i] = what[i + 1];
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) raw[i][u] = raw[i + 1][u];
         }
+        fetch(raw[kAhead - 1], what[kAhead - 1]);
+        if (++have < kAhead) continue;
+        if (what[0] < 0 || !process(raw[0], what[0])) break;
       }
     }
     finish();
