@@ -34,12 +34,11 @@ constexpr uint32_t kStage = 32768;
 
 // e4m3: what the warps that widen the codes and those of the softmax need to know of a block of keys.
 struct BlockMeta {
-  float kf[kBlock];   // a key's power of two times the softmax scale: log2 units of its scores
-  float vf[kBlock];   // a value's power of two relative to the block's largest, times 2^kWeight
-  int row[8];         // pool row of each page's first key
-  float ev;           // log2 of the block's largest value scale
-  int have, flags;    // visible keys; kFirst, kLast: of a segment, kEnd: no more blocks
-  int pad;
+  uint32_t kf[kBlock];  // a key's power of two relative to the block's largest, twice in binary16
+  uint32_t vf[kBlock];  // the same of a value
+  int row[8];           // pool row of each page's first key
+  float ku, ev;         // the block's largest key scale times the softmax scale; log2 of its largest value scale
+  int have, flags;      // visible keys; kFirst, kLast: of a segment, kEnd: no more blocks
 };
 enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
 constexpr int kMeta = 8;         // blocks that the pages and scales are ahead
@@ -48,7 +47,8 @@ constexpr float kWeight = 7.f;   // log2 of the factor on binary16 weights
 template <int D, int kTiles, bool kE4M3>
 struct Cfg {
   static constexpr int kSoftWarps = 4 * kTiles;
-  static constexpr int kConvWarps = kE4M3 ? (kTiles == 2 ? 4 : 8) : 0;
+  static constexpr int kConvGroups = kE4M3 ? 3 - kTiles : 0;  // of four warps that widen codes, taking stages in turn
+  static constexpr int kConvWarps = 4 * kConvGroups;
   static constexpr int kThreads = 32 * (kSoftWarps + 4 + kConvWarps);
   static constexpr uint32_t kQ = kTiles * 128 * D * 2;
   // An e4m3 cache's loads wait in registers, so one stage less will do; its place holds the scales.
@@ -61,6 +61,8 @@ struct Cfg {
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;  // barriers; alignment of the base
   // of the four warps behind the softmax's: the products (two), loads or scales, value rows behind the last key
   static constexpr int kMma0 = kSoftWarps, kMma1 = kSoftWarps + 1, kLoad = kSoftWarps + 2, kTail = kSoftWarps + 3;
+  // Scores that a softmax warp holds at a time.
+  static constexpr int kCols = kE4M3 ? 32 : 128;
   static constexpr uint32_t kColO = 256;                    // tensor memory: two S slots of 128 columns, then O
   // Registers: the softmax warps hold a row of 128 scores each, the others need few.  The shares of the
   // warpgroups come to no more than the launch's: 512 threads of 128, 384 of 168; 256 threads have
@@ -156,6 +158,22 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+template <int kCols>
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[kCols]) {
+  if constexpr (kCols == 32) {
+    tmem_ld32(taddr, s);
+  } else {
+    uint32_t x[kCols / 64][64];
+#pragma unroll
+    for (int h = 0; h < kCols / 64; ++h) tmem_ld64_begin(taddr + 64 * h, x[h]);
+#pragma unroll
+    for (int h = 0; h < kCols / 64; ++h) {
+      tmem_ld64_wait(x[h]);
+#pragma unroll
+      for (int i = 0; i < 64; ++i) s[64 * h + i] = __uint_as_float(x[h][i]);
+    }
+  }
+}
 // 16 columns of this warp's 32 lanes; tmem_st_wait: this thread's stores so far have been done
 __device__ __forceinline__ void tmem_st16_begin(uint32_t taddr, const float (&v)[16]) {
   asm volatile(
@@ -169,6 +187,16 @@ __device__ __forceinline__ void tmem_st16_begin(uint32_t taddr, const float (&v)
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, kWaitLimit));
+}
+
+// 2^e, e <= 0, twice in binary16 (0 below its range)
+__device__ __forceinline__ uint32_t half2_power(int e) {
+  const uint32_t h = e >= -14 ? (uint32_t)(15 + e) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
+  return h | h << 16;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 template <int kRegs>
@@ -198,7 +226,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26, b0 + 8 * 28, b0 + 8 * 29, b0 + 8 * 37};
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar.full + 8 * i, kE4M3 ? C::kConvWarps : 1);
+      mbar_init(bar.full + 8 * i, kE4M3 ? 4 : 1);
       mbar_init(bar.empty + 8 * i, kTiles);
       mbar_init(bar.tail + 8 * i, 1);
     }
@@ -213,7 +241,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     if constexpr (kE4M3) {
       for (int i = 0; i < kMeta; ++i) {
         mbar_init(bar.meta_full + 8 * i, 1);
-        mbar_init(bar.meta_empty + 8 * i, C::kConvWarps + C::kSoftWarps);
+        mbar_init(bar.meta_empty + 8 * i, 4 * 2 * kParts + C::kSoftWarps);  // each stage's four warps, the softmax's
       }
     }
     fence_mbar_init();
@@ -285,7 +313,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
         continue;
       }
-      float unit = p.scale_log2;  // log2 units of this row's scores
+      float row_unit = p.scale_log2;  // e4m3: the power of two the row was divided by
       if constexpr (kE4M3) {
         // Q into shared memory, each warp its own rows (zeros in those beyond the tile's last), in binary16,
         // divided by the power of two of the row's largest value
@@ -324,7 +352,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             }
           }
           __syncwarp();
-          unit = qs[row];
+          row_unit = qs[row];
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -333,9 +361,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       float m = -INFINITY, l = 0.f, r = -INFINITY;
       const int last = seg.pos0 + sub * p.sub + tok_in;  // the row's position: its last visible key
       const bool busy = w4 * 32 < rows;                   // this warp has rows at all
-      // columns at a time: a bf16 block's 128 scores stay in registers; for e4m3, whose code is longer and
-      // shares the instruction cache with the widening warps', 64, read twice
-      constexpr int kCols = kE4M3 ? 64 : kBlock;
+      constexpr int kCols = C::kCols;
       const uint32_t seg_blk = all_blk;
       all_blk += seg.j1 - seg.j0;
       if (kE4M3 && rows <= 0) {  // this tile has no rows in the segment: its warps still let its blocks go
@@ -354,43 +380,22 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             const uint32_t t_s = tmem + lanes + slot * 128;
             const int lim = last + 1 - j * kBlock;  // columns from here on are not visible
             const bool masked = __any_sync(0xFFFFFFFFu, lim < kBlock);
-            float ev = 0.f;
+            float ev = 0.f, unit = row_unit;  // log2 of the block's value scale; log2 units of this row's scores
             const BlockMeta* meta = reinterpret_cast<const BlockMeta*>(sm + C::kOffScale) + blk % kMeta;
             if constexpr (kE4M3) {
               if (!await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) break;
               ev = meta->ev;
+              unit *= meta->ku;
             }
-            // kCols columns from c0 on: scores (e4m3: by the keys' powers of two), those out of sight -inf
-            auto load = [&](int c0, float (&s)[kCols]) {
-              uint32_t x[kCols / 64][64];
-#pragma unroll
-              for (int h = 0; h < kCols; h += 64) tmem_ld64_begin(t_s + c0 + h, x[h / 64]);
-#pragma unroll
-              for (int h = 0; h < kCols; h += 64) {
-                tmem_ld64_wait(x[h / 64]);
-#pragma unroll
-                for (int i = 0; i < 64; ++i) s[h + i] = __uint_as_float(x[h / 64][i]);
-              }
-              if constexpr (kE4M3) {
-#pragma unroll
-                for (int i = 0; i < kCols / 4; ++i) {
-                  const float4 k = *reinterpret_cast<const float4*>(meta->kf + c0 + 4 * i);
-                  s[4 * i] *= k.x;
-                  s[4 * i + 1] *= k.y;
-                  s[4 * i + 2] *= k.z;
-                  s[4 * i + 3] *= k.w;
-                }
-              }
+            float s[kCols], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int c0 = 0; c0 < kBlock; c0 += kCols) {
+              load_scores<kCols>(t_s + c0, s);
               if (masked) {
 #pragma unroll
                 for (int i = 0; i < kCols; ++i)
                   if (c0 + i >= lim) s[i] = -INFINITY;
               }
-            };
-            float s[kCols], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-            for (int c0 = 0; c0 < kBlock; c0 += kCols) {
-              load(c0, s);
 #pragma unroll
               for (int i = 0; i < kCols; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
             }
@@ -421,11 +426,18 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             // weights 2^(s - m + d), d = e - r <= 0 the distance of this block's unit from O's; cut off at -40,
             // lest a block of tiny values vanish from l (P is zero in binary16 long before)
             const float d = kE4M3 && m > -INFINITY ? fmaxf(e - r, -40.f) : 0.f;
-            const float off = m == -INFINITY ? 0.f : d - m;
+            const float off = (kE4M3 ? kWeight : 0.f) + (m == -INFINITY ? 0.f : d - m);
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
             for (int c0 = 0; c0 < kBlock; c0 += kCols) {
-              if (kCols < kBlock) load(c0, s);  // the weights go over scores that have been read
+              if (kCols < kBlock) {  // again: the weights go over scores that have been read
+                load_scores<kCols>(t_s + c0, s);
+                if (masked) {
+#pragma unroll
+                  for (int i = 0; i < kCols; ++i)
+                    if (c0 + i >= lim) s[i] = -INFINITY;
+                }
+              }
 #pragma unroll
               for (int h = 0; h < kCols / 32; ++h) {
                 float w[16];
@@ -437,13 +449,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
                     x[k] = ex2_approx(fmaf(s[32 * h + 2 * i + k], unit, off));
                     sum[k] += x[k];
                   }
-                  if constexpr (kE4M3) {
-                    const float4 v = *reinterpret_cast<const float4*>(meta->vf + c0 + 32 * h + 2 * i);
-                    x[0] *= v.x;
-                    x[1] *= v.y;
-                    x[2] *= v.z;
-                    x[3] *= v.w;
-                  }
                   w[i] = __uint_as_float(kE4M3 ? pack_half2(x[0], x[1]) : pack_bf2(x[0], x[1]));
                   w[i + 1] = __uint_as_float(kE4M3 ? pack_half2(x[2], x[3]) : pack_bf2(x[2], x[3]));
                 }
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             }
             tmem_st_wait();
             const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            l += kE4M3 ? all * ex2_approx(-d) : all;
+            l += kE4M3 ? all * ex2_approx(-d - kWeight) : all;
           }
           if constexpr (kE4M3) {
             __syncwarp();
@@ -528,99 +533,105 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   if (kE4M3 && warp >= C::kSoftWarps + 4) {
     if constexpr (C::kSplit) regs_dec<C::kRegConv>();
     // ------------------------------------------------------------------ e4m3: codes -> binary16 stages
-    // 16 codes a load; the loads of the next kAhead stages wait in registers while this one's codes are
-    // widened (exactly, two an instruction) and written in the layout that the TMA gives a bf16 cache.
-    constexpr int kConv = C::kConvWarps > 0 ? C::kConvWarps : 4, kUnits = 1024 / (32 * kConv), kAhead = kConv == 8 ? 3 : 2;
-    const int ct = tid - 32 * (C::kSoftWarps + 4);
+    // Four warps a stage, in groups that take the stages in turn; 16 codes a load, the loads of a group's
+    // next stage wait in registers while this one's codes are widened (exactly, two an instruction),
+    // multiplied by their row's power of two relative to the block's largest, and written in the layout
+    // that the TMA gives a bf16 cache.  (A product loses what lies below binary16: less than 2^-32 of the
+    // block's largest value.)
+    constexpr int kGroups = C::kConvGroups > 0 ? C::kConvGroups : 1, kUnits = 8, kAhead = 2;
+    const int cw = warp & 3, group = (warp - (C::kSoftWarps + 4)) >> 2;
     const int shift = p.cache.page_shift;
     const BlockMeta* metas = reinterpret_cast<const BlockMeta*>(sm + C::kOffScale);
-    Ring<kStages> ring;
-    // The order of the stages, each operand of a block in kParts: K0 V0 K1 V1 .. with two tiles, with one
-    // K0 K1 V0 K2 V1 ..: after a block's keys come the values of the block before it, if the segment has
-    // one, and the block's own values, if it is the segment's last.
-    uint32_t blk = 0;          // the latest block whose keys were or are being fetched
-    int mode = 0, part = 0;    // 0: keys of blk, 1: values of the block before, 2: values of blk
-    int flags = 0;
     // A thread's 16 codes of a stage, unit u: 128 rows of 128 codes (narrow), or 64 of 256 (a block's
     // values at D = 256: wide).  Lanes 0-3 take a row's 64 neighbouring codes, lanes 4-7 those of the row
     // below, so that the swizzle spreads eight lanes' stores over all banks.
-    const int piece = lane & 3, odd = lane >> 2 & 1, cw = ct >> 5;
+    const int piece = lane & 3, odd = lane >> 2 & 1;
     const int row_narrow = cw * 4 + (lane >> 4) * 2 + odd, blk_narrow = lane >> 3 & 1, row_wide = cw * 2 + odd, blk_wide = lane >> 3;
     const int d_narrow = blk_narrow * 64 + piece * 16, d_wide = blk_wide * 64 + piece * 16;
     const int c_narrow = (2 * piece) ^ (row_narrow & 7), c_wide = (2 * piece) ^ (row_wide & 7);
     const int to_narrow = blk_narrow * 16384 + row_narrow * 128 + c_narrow * 16, to_wide = blk_wide * 8192 + row_wide * 128 + c_wide * 16;
     const int other_narrow = ((c_narrow ^ 1) - c_narrow) * 16, other_wide = ((c_wide ^ 1) - c_wide) * 16;  // to the second half
-    uint4 raw[kAhead][kUnits] = {};
-    int what[kAhead] = {};     // 0: keys, 1: values, -1: no more
-    auto release = [&](uint32_t b) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar.meta_empty + 8 * (b % kMeta));
-    };
-    auto fetch = [&](uint4 (&x)[kUnits], int& is) {
-      is = -1;
-      if (mode == 0 && part == 0) {
-        if (!ok || !await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) return;
-        flags = metas[blk % kMeta].flags;
-        if (flags & kEnd) {
-          ok = false;  // nothing is waited for any more
-          return;
-        }
-      }
-      const bool value = mode != 0, wide = value && D == 256;
-      const BlockMeta& meta = metas[(mode == 1 ? blk - 1 : blk) % kMeta];
-      const uint8_t* src = static_cast<const uint8_t*>(value ? p.cache.v : p.cache.k) + (wide ? d_wide : d_narrow + (value ? 0 : part * 128));
-      const int first = wide ? row_wide + part * 64 : row_narrow, last = meta.have - 1;
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        // key of the block; behind the last visible one that one again (its scores are masked, its weights 0)
-        const int row = min(first + u * (wide ? 2 * kConv : 4 * kConv), last);
-        x[u] = ld_ahead16(src + (long)(meta.row[row >> shift] + (row & ((1 << shift) - 1))) * D);
-      }
-      is = value;
-      if (++part == kParts) {
+    // The order of the stages, each operand of a block in kParts: K0 V0 K1 V1 .. with two tiles, with one
+    // K0 K1 V0 K2 V1 ..: after a block's keys come the values of the block before it, if the segment has
+    // one, and the block's own values, if it is the segment's last.
+    uint32_t blk = 0;               // the latest block whose keys have been reached
+    int mode = 0, part = -1;        // 0: keys of blk, 1: values of the block before, 2: values of blk
+    int flags = 0;
+    auto next_stage = [&]() {
+      if (++part == kParts || mode < 0) {
         part = 0;
-        if (mode == 1) release(blk - 1);
-        if (mode == 2) release(blk);
-        if (kTiles == 2) {
-          if (mode == 0) {
-            mode = 2;
-          } else {
-            mode = 0;
-            ++blk;
-          }
-        } else if (mode == 0 && !(flags & kFirst)) {
+        if (kTiles == 1 && mode == 0 && !(flags & kFirst)) {
           mode = 1;
-        } else if (mode != 2 && (flags & kLast)) {
-          mode = 2;
+        } else if (mode == 0 || (kTiles == 1 && mode == 1)) {
+          mode = kTiles == 2 || (flags & kLast) ? 2 : 0;
+          if (mode == 0) ++blk;
         } else {
           mode = 0;
           ++blk;
         }
       }
+      if (mode == 0 && part == 0) {
+        if (!await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) return false;
+        flags = metas[blk % kMeta].flags;
+        if (flags & kEnd) {
+          ok = false;  // nothing is waited for any more
+          return false;
+        }
+      }
+      return true;
     };
-    auto process = [&](const uint4 (&x)[kUnits], bool value) {
+    Ring<kStages> ring;
+    ring.skip(group);
+    uint4 raw[kAhead][kUnits] = {};
+    int what[kAhead] = {};          // bit 0: values, bit 1: part, from bit 2: the block's place; -1: no more
+    auto fetch = [&](uint4 (&x)[kUnits], int& is, int ahead) {
+      is = -1;
+      for (int i = 0; i < ahead; ++i)
+        if (!ok || !next_stage()) return;
+      const bool value = mode != 0, wide = value && D == 256;
+      const uint32_t at = (mode == 1 ? blk - 1 : blk) % kMeta;
+      const BlockMeta& meta = metas[at];
+      const uint8_t* src = static_cast<const uint8_t*>(value ? p.cache.v : p.cache.k) + (wide ? d_wide : d_narrow + (value ? 0 : part * 128));
+      const int first = wide ? row_wide + part * 64 : row_narrow, last = meta.have - 1, mask = (1 << shift) - 1;
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) {
+        // key of the block; behind the last visible one that one again (its scores are masked, its weights 0)
+        const int row = min(first + u * (wide ? 8 : 16), last);
+        x[u] = ld_ahead16(src + (long)(meta.row[row >> shift] + (row & mask)) * D);
+      }
+      is = value | part << 1 | at << 2;
+    };
+    auto process = [&](const uint4 (&x)[kUnits], int is) {
       if (!mbar_wait_all(bar.empty + 8 * ring.i, ring.pass ^ 1u)) {
         raise_error(p.err, kErrTimeout);
         return false;
       }
-      const bool wide = value && D == 256;
+      const bool value = is & 1, wide = value && D == 256;
+      const BlockMeta& meta = metas[is >> 2];
+      const uint32_t* scale = value ? meta.vf : meta.kf;
+      const int first = wide ? row_wide + (is >> 1 & 1) * 64 : row_narrow;
       uint8_t* to = sm + C::kOffStage + ring.i * kStage + (wide ? to_wide : to_narrow);
       const int other = wide ? other_wide : other_narrow;
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) {
+        const uint32_t f = scale[first + u * (wide ? 8 : 16)];
         const uint2 a = e4m3x4_to_half4(x[u].x), b = e4m3x4_to_half4(x[u].y), c = e4m3x4_to_half4(x[u].z), e = e4m3x4_to_half4(x[u].w);
-        uint8_t* at = to + u * (wide ? 2 * kConv : 4 * kConv) * 128;
-        *reinterpret_cast<uint4*>(at) = make_uint4(a.x, a.y, b.x, b.y);
-        *reinterpret_cast<uint4*>(at + other) = make_uint4(c.x, c.y, e.x, e.y);
+        uint8_t* at = to + u * (wide ? 8 : 16) * 128;
+        *reinterpret_cast<uint4*>(at) = make_uint4(mul_half2(a.x, f), mul_half2(a.y, f), mul_half2(b.x, f), mul_half2(b.y, f));
+        *reinterpret_cast<uint4*>(at + other) = make_uint4(mul_half2(c.x, f), mul_half2(c.y, f), mul_half2(e.x, f), mul_half2(e.y, f));
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar.full + 8 * ring.i);
-      ring.step();
+      if (lane == 0) {
+        mbar_arrive(bar.full + 8 * ring.i);
+        mbar_arrive(bar.meta_empty + 8 * (is >> 2));
+      }
+      ring.skip(kGroups);
       return true;
     };
     if (start->left > 0) {
       // one copy of the code (the instruction cache is short): the waiting loads move up by a place instead
+      int step_by = group + 1;
 #pragma unroll 1
       for (int have = 0;;) {
 #pragma unroll
@@ -629,7 +640,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
 #pragma unroll
           for (int u = 0; u < kUnits; ++u) raw[i][u] = raw[i + 1][u];
         }
-        fetch(raw[kAhead - 1], what[kAhead - 1]);
+        fetch(raw[kAhead - 1], what[kAhead - 1], step_by);
+        step_by = kGroups;
         if (++have < kAhead) continue;
         if (what[0] < 0 || !process(raw[0], what[0])) break;
       }
@@ -780,24 +792,28 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           v4 = ld_ahead4(p.cache.v_scale + at);
         }
         if (!await(bar.meta_empty + 8 * (blk % kMeta), (blk / kMeta & 1u) ^ 1u)) break;
-        uint32_t top = 0;
+        uint32_t kt = 0, vt = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, lane * 4 + i < have ? (v4 >> (8 * i)) & 255u : 0u);
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        float kf[4], vf[4];
+        for (int i = 0; i < 4; ++i) {
+          kt = max(kt, lane * 4 + i < have ? (k4 >> (8 * i)) & 255u : 0u);
+          vt = max(vt, lane * 4 + i < have ? (v4 >> (8 * i)) & 255u : 0u);
+        }
+        kt = __reduce_max_sync(0xFFFFFFFFu, kt);
+        vt = __reduce_max_sync(0xFFFFFFFFu, vt);
+        uint32_t kf[4], vf[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool in = lane * 4 + i < have;
-          const int diff = (int)((v4 >> (8 * i)) & 255u) - (int)top + (int)kWeight;
-          kf[i] = in ? e8m0_value((k4 >> (8 * i)) & 255u) * p.scale_log2 : 0.f;
-          vf[i] = in && diff >= -126 ? __uint_as_float((uint32_t)(127 + diff) << 23) : 0.f;
+          kf[i] = in ? half2_power((int)((k4 >> (8 * i)) & 255u) - (int)kt) : 0u;
+          vf[i] = in ? half2_power((int)((v4 >> (8 * i)) & 255u) - (int)vt) : 0u;
         }
         BlockMeta& m = metas[blk % kMeta];
-        reinterpret_cast<float4*>(m.kf)[lane] = make_float4(kf[0], kf[1], kf[2], kf[3]);
-        reinterpret_cast<float4*>(m.vf)[lane] = make_float4(vf[0], vf[1], vf[2], vf[3]);
+        reinterpret_cast<uint4*>(m.kf)[lane] = make_uint4(kf[0], kf[1], kf[2], kf[3]);
+        reinterpret_cast<uint4*>(m.vf)[lane] = make_uint4(vf[0], vf[1], vf[2], vf[3]);
         if (lane < 8) m.row[lane] = row;
         if (lane == 0) {
-          m.ev = (float)((int)top - 127);
+          m.ku = e8m0_value(kt) * p.scale_log2;
+          m.ev = (float)((int)vt - 127);
           m.have = have;
           m.flags = (j == seg.j0 ? kFirst : 0) | (j + 1 == seg.j1 ? kLast : 0);
         }

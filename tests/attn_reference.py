@@ -77,9 +77,9 @@ def attention(q, cache, table, q_lens, kv_lens, scale, z=None):
     relatively; the weights are rounded to bf16 (2^-8); numerator and denominator both carry the error;
     sums over n keys add n * 2^-24; the result is rounded to bf16 (2^-8).  e4m3: the queries are
     rounded to binary16 after division by a power of two that leaves the largest below 2 (2^-25 of it
-    where they leave the normal range), the weights (times their value row's power of two over the
-    largest, times 2^7) to binary16: 2^-11, or 2^-25 of 2^-7 of a unit that is at most twice the
-    largest value, for each key."""
+    where they leave the normal range), the weights, times 2^7, to binary16: 2^-11, or 2^-25 of 2^-7 of a unit
+    that is at most twice the largest value, for each key; a key or value row far below the largest
+    may lose 2^-32 of that."""
     hq, D = q.shape[1], q.shape[2]
     out, tol = [torch.zeros(q.shape, dtype=torch.float64, device=q.device) for _ in range(2)]
     e4m3 = cache.k_scale is not None
@@ -104,6 +104,7 @@ def attention(q, cache, table, q_lens, kv_lens, scale, z=None):
         o = torch.einsum("hgtj,hjd->hgtd", w, v)
         size = torch.einsum("hgtj,hjd->hgtd", w, v.abs())
         if e4m3:
+            rel = rel + 2.0 ** -32 * scale * k.abs().max() * qd.abs().sum(-1, keepdim=True)
             rel = rel + 2.0 ** -25 * scale * (qd.abs().amax(-1)[..., None] * k.abs().sum(-1)[:, None, None]).amax(-1, keepdim=True)
         err = (2.0 ** (-11 if e4m3 else -8) + 2 * rel + 2 * kv * 2.0 ** -24 + 2.0 ** -20) * size
         if e4m3:
