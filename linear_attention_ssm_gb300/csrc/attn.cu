@@ -28,7 +28,7 @@
 namespace gdn {
 namespace {
 
-constexpr uint32_t kStage = 32768;
+constexpr uint32_t kStage = 32768, kRaw = 16384;
 
 // ---------------------------------------------------------------- layout of a CTA
 
@@ -36,7 +36,6 @@ constexpr uint32_t kStage = 32768;
 struct BlockMeta {
   uint32_t kf[kBlock];  // a key's power of two relative to the block's largest, twice in binary16
   uint32_t vf[kBlock];  // the same of a value
-  int row[8];           // pool row of each page's first key
   float ku, ev;         // the block's largest key scale times the softmax scale; log2 of its largest value scale
   int have, flags;      // visible keys; kFirst, kLast: of a segment, kEnd: no more blocks
 };
@@ -51,33 +50,29 @@ struct Cfg {
   static constexpr int kConvWarps = 4 * kConvGroups;
   static constexpr int kThreads = 32 * (kSoftWarps + 4 + kConvWarps);
   static constexpr uint32_t kQ = kTiles * 128 * D * 2;
-  // An e4m3 cache's loads wait in registers, so one stage less will do; its place holds the scales.
-  static constexpr int kStages = (int)((224 * 1024 - kQ) / kStage) - (kE4M3 ? 1 : 0);
+  // The rings' stages: the products' (32 KB); e4m3: fewer of those, and the codes' (16 KB).
+  static constexpr int kRawStages = kE4M3 ? 3 : 0;
+  static constexpr int kStages = (int)((224 * 1024 - kQ) / kStage) - (kE4M3 ? 2 : 0);
   static constexpr int kParts = D / 128;  // stages of a block's keys, and of its values
   static constexpr uint32_t kOffStage = kQ;
-  static constexpr uint32_t kOffScale = kOffStage + kStages * kStage;  // e4m3: the next blocks' pages and scales
-  static constexpr uint32_t kOffQs = kOffScale + (kE4M3 ? kMeta * sizeof(BlockMeta) : 0);
+  static constexpr uint32_t kOffRaw = kOffStage + kStages * kStage;
+  static constexpr uint32_t kOffMeta = kOffRaw + kRawStages * kRaw;
+  static constexpr uint32_t kOffQs = kOffMeta + (kE4M3 ? kMeta * sizeof(BlockMeta) : 0);
   static constexpr uint32_t kOffBar = kOffQs + (kE4M3 ? kTiles * 512 : 0);
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;  // barriers; alignment of the base
-  // of the four warps behind the softmax's: the products (two), loads or scales, value rows behind the last key
+  static_assert(kSmem <= 232448, "shared memory");
+  // of the four warps behind the softmax's: the products (two), Q, K and V by TMA, value rows behind the
+  // last key (e4m3: scales)
   static constexpr int kMma0 = kSoftWarps, kMma1 = kSoftWarps + 1, kLoad = kSoftWarps + 2, kTail = kSoftWarps + 3;
-  // Scores that a softmax warp holds at a time.
-  static constexpr int kCols = kE4M3 ? 32 : 128;
-  static constexpr uint32_t kColO = 256;                    // tensor memory: two S slots of 128 columns, then O
-  // Registers: the softmax warps hold a row of 128 scores each, the others need few.  The shares of the
-  // warpgroups come to no more than the launch's: 512 threads of 128, 384 of 168; 256 threads have
-  // enough as they are.
-  static constexpr int kRegLaunch = 65536 / kThreads / 8 * 8;
-  static constexpr bool kSplit = kThreads > 256;
-  static constexpr int kRegSoft = kTiles == 2 ? (kE4M3 ? 184 : 208) : 216;
-  static constexpr int kRegAux = kE4M3 ? 40 : 80;
-  static constexpr int kRegConv = kTiles == 2 ? 96 : 120;
-  static_assert(!kSplit || kSoftWarps * kRegSoft + 4 * kRegAux + kConvWarps * kRegConv <= kThreads / 32 * kRegLaunch,
-                "the shares exceed the launch's registers");
+  // Scores that a softmax warp holds at a time; the rest of a block's are read twice.  Few registers, and
+  // short code for the instruction cache that warps of several kinds share: 32 beat 128 by 2 % at D = 256
+  // and by a third for e4m3; two tiles were best with 64 (894 TFLOP/s, 875 with 32 or 128).
+  static constexpr int kCols = kTiles == 2 && !kE4M3 ? 64 : 32;
+  static constexpr uint32_t kColO = 256;  // tensor memory: two S slots of 128 columns, then O
 };
 
 struct Bars {
-  uint32_t full, empty, tail, s_full, p_full, o_full, q_full, q_empty, done, meta_full, meta_empty;  // shared addresses of the first of each kind
+  uint32_t full, empty, tail, s_full, p_full, o_full, q_full, q_empty, done, meta_full, meta_empty, q_ready, raw_full, raw_empty;  // shared addresses of the first of each kind
 };
 
 // 64 columns of this warp's 32 lanes.  The wait for the load is a statement of its own (two loads, one
@@ -199,15 +194,6 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-template <int kRegs>
-__device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
 template <int D, int kTiles, bool kE4M3>
 __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using C = Cfg<D, kTiles, kE4M3>;
@@ -219,11 +205,12 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   const int step = kTiles * p.sub;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 46);
-  WalkStart* start = reinterpret_cast<WalkStart*>(bars + 48);
-  long* scan = reinterpret_cast<long*>(bars + 56);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 54);
+  WalkStart* start = reinterpret_cast<WalkStart*>(bars + 56);
+  long* scan = reinterpret_cast<long*>(bars + 62);
   const uint32_t b0 = smem_u32(bars);
-  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26, b0 + 8 * 28, b0 + 8 * 29, b0 + 8 * 37};
+  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26, b0 + 8 * 28, b0 + 8 * 29, b0 + 8 * 37, b0 + 8 * 45,
+                    b0 + 8 * 47, b0 + 8 * 50};
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar.full + 8 * i, kE4M3 ? 4 : 1);
@@ -234,22 +221,25 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       mbar_init(bar.s_full + 8 * i, 1);
       mbar_init(bar.p_full + 8 * i, 4);
       mbar_init(bar.o_full + 8 * i, 1);
-      mbar_init(bar.q_full + 8 * i, kE4M3 ? 4 : 1);
+      mbar_init(bar.q_full + 8 * i, 1);
+      mbar_init(bar.q_ready + 8 * i, 4);
       mbar_init(bar.q_empty + 8 * i, 1);
     }
     mbar_init(bar.done, 2);
     if constexpr (kE4M3) {
+      for (int i = 0; i < C::kRawStages; ++i) {
+        mbar_init(bar.raw_full + 8 * i, 1);
+        mbar_init(bar.raw_empty + 8 * i, 4);
+      }
       for (int i = 0; i < kMeta; ++i) {
         mbar_init(bar.meta_full + 8 * i, 1);
         mbar_init(bar.meta_empty + 8 * i, 4 * 2 * kParts + C::kSoftWarps);  // each stage's four warps, the softmax's
       }
     }
     fence_mbar_init();
-    if constexpr (!kE4M3) {
-      prefetch_tensormap(&p.tmap_k);
-      prefetch_tensormap(&p.tmap_v);
-      prefetch_tensormap(&p.tmap_q);
-    }
+    prefetch_tensormap(&p.tmap_k);
+    prefetch_tensormap(&p.tmap_v);
+    prefetch_tensormap(&p.tmap_q);
     start->left = 0;
     p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     p.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
@@ -288,15 +278,14 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   };
 
   if (warp < C::kSoftWarps) {
-    if constexpr (C::kSplit) regs_inc<C::kRegSoft>();
     // ------------------------------------------------------------------ softmax: one thread for a row
     const int sub = kTiles == 2 ? warp >> 2 : 0, w4 = warp & 3, row = w4 * 32 + lane;
     const uint32_t lanes = (uint32_t)(w4 * 32) << 16;
     const uint32_t t_o = tmem + lanes + C::kColO + sub * D;
     const int g = row % p.G, tok_in = row / p.G;
     uint8_t* sq = sm + sub * 128 * D * 2;
-    // blocks of this tile so far (slot and parity go by it), its products with V, blocks of the CTA
-    uint32_t n_blk = 0, n_pv = 0, all_blk = 0;
+    // blocks of this tile so far (slot and parity go by it), its products with V, blocks of the CTA; segments with rows
+    uint32_t n_blk = 0, n_pv = 0, all_blk = 0, n_seg = 0;
     // The product of block b.  With one tile the next block's scores may be here before the product of
     // the block before them has ended: one barrier for even and one for odd blocks, so that no wait is
     // for a phase that could lie two behind.
@@ -314,27 +303,22 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         continue;
       }
       float row_unit = p.scale_log2;  // e4m3: the power of two the row was divided by
-      if constexpr (kE4M3) {
-        // Q into shared memory, each warp its own rows (zeros in those beyond the tile's last), in binary16,
-        // divided by the power of two of the row's largest value
+      if (kE4M3 && rows > 0) {
+        // Q becomes binary16 where it lies, each warp its own rows, a row divided by the power of two of its
+        // largest value
+        if (!await(bar.q_full + 8 * sub, n_seg++ & 1u)) break;
+        constexpr int kPer = D / 8, kRowsAt = 32 / kPer;  // 16-byte pieces of a row, rows of a warp at a time
+        const int piece = lane % kPer;
+        float* qs = reinterpret_cast<float*>(sm + C::kOffQs) + sub * 128;
         if (w4 * 32 < rows) {
-          constexpr int kPer = D / 8, kRowsAt = 32 / kPer;  // 16-byte pieces of a row, rows of a warp at a time
-          const int piece = lane % kPer;
-          const uint16_t* src = p.q + (long)hk * p.G * D + piece * 8;
-          float* qs = reinterpret_cast<float*>(sm + C::kOffQs) + sub * 128;
 #pragma unroll 1
-          for (int i0 = 0; i0 < 32; i0 += 8 * kRowsAt) {
-            uint4 x[8];
+          for (int i0 = 0; i0 < 32; i0 += 4 * kRowsAt) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rr = w4 * 32 + i0 + i * kRowsAt + lane / kPer, t = (rr * p.inv_g) >> 16;
-              x[i] = make_uint4(0, 0, 0, 0);
-              if (rr < rows) x[i] = ld_ahead16(src + ((long)(row0 + t) * p.Hq + (rr - t * p.G)) * D);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const int rr = w4 * 32 + i0 + i * kRowsAt + lane / kPer;
-              uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, top = 0;
+              uint4* at = reinterpret_cast<uint4*>(sq + sw128_offset(rr, piece * 8, 16384));
+              const uint4 x = *at;
+              uint32_t y[4] = {x.x, x.y, x.z, x.w}, top = 0;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t lo = y[k] << 16 & 0x7FFFFFFFu, hi = y[k] & 0x7FFF0000u;
@@ -348,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
               for (int k = 0; k < 4; ++k)
                 y[k] = pack_half2(__uint_as_float(y[k] << 16) * inv, __uint_as_float(y[k] & 0xFFFF0000u) * inv);
               if (piece == 0) qs[rr] = __uint_as_float((uint32_t)(127 + e) << 23);
-              *reinterpret_cast<uint4*>(sq + sw128_offset(rr, piece * 8, 16384)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *at = make_uint4(y[0], y[1], y[2], y[3]);
             }
           }
           __syncwarp();
@@ -356,7 +340,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && rows > 0) mbar_arrive(bar.q_full + 8 * sub);
+        if (lane == 0) mbar_arrive(bar.q_ready + 8 * sub);
       }
       float m = -INFINITY, l = 0.f, r = -INFINITY;
       const int last = seg.pos0 + sub * p.sub + tok_in;  // the row's position: its last visible key
@@ -381,7 +365,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             const int lim = last + 1 - j * kBlock;  // columns from here on are not visible
             const bool masked = __any_sync(0xFFFFFFFFu, lim < kBlock);
             float ev = 0.f, unit = row_unit;  // log2 of the block's value scale; log2 units of this row's scores
-            const BlockMeta* meta = reinterpret_cast<const BlockMeta*>(sm + C::kOffScale) + blk % kMeta;
+            const BlockMeta* meta = reinterpret_cast<const BlockMeta*>(sm + C::kOffMeta) + blk % kMeta;
             if constexpr (kE4M3) {
               if (!await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) break;
               ev = meta->ev;
@@ -480,42 +464,51 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           const int part = 2 * blockIdx.x + (seg.j0 == 0 ? 1 : 0);
           float4* dst = p.part + (long)part * (kPartBytes / sizeof(float4)) + sub * (D / 4) * 128 + row;
           if (!whole) p.ml[(long)part * 256 + sub * 128 + row] = make_float2(m, l);
+          uint4 zz[4];  // the gate of the next 32 values
+          const bool gated = whole && mine && p.z.p;
+          auto gate = [&](int c) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) zz[k] = gated ? __ldg(reinterpret_cast<const uint4*>(z + c + 8 * k)) : make_uint4(0, 0, 0, 0);
+          };
+          gate(0);
 #pragma unroll 1
-          for (int c = 0; c < D; c += 64) {
-            uint32_t o[64];
-            tmem_ld64_begin(t_o + c, o);
-            tmem_ld64_wait(o);
-            auto value = [&](int i) { return kE4M3 ? __uint_as_float(o[i]) * unit_o * unit_o : __uint_as_float(o[i]); };
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(t_o + c, o);
+            if constexpr (kE4M3) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = o[i] * unit_o * unit_o;
+            }
             if (!whole) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                dst[(c / 4 + i) * 128] = make_float4(value(4 * i), value(4 * i + 1), value(4 * i + 2), value(4 * i + 3));
-            } else if (mine) {
+              for (int i = 0; i < 8; ++i) dst[(c / 4 + i) * 128] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            } else {
 #pragma unroll
-              for (int i = 0; i < 64; i += 16) {
-                uint32_t w[8];
+              for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no visible key: zero
+              if (p.z.p) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t zr[4] = {zz[k].x, zz[k].y, zz[k].z, zz[k].w};
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) {
+                    o[8 * k + 2 * x] *= sigmoid_fast(__uint_as_float(zr[x] << 16));
+                    o[8 * k + 2 * x + 1] *= sigmoid_fast(__uint_as_float(zr[x] & 0xFFFF0000u));
+                  }
+                }
+                if (c + 32 < D) gate(c + 32);
+              }
+              if (mine) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                  float y[8];
+                  uint32_t w[8];
 #pragma unroll
-                  for (int x = 0; x < 8; ++x) y[x] = l == 0.f ? 0.f : value(i + 8 * k + x) * inv;  // no visible key: zero
-                  if (p.z.p) {
-                    const uint4 zz = __ldg(reinterpret_cast<const uint4*>(z + c + i + 8 * k));
-                    const uint32_t zr[4] = {zz.x, zz.y, zz.z, zz.w};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                      y[2 * x] *= sigmoid_fast(__uint_as_float(zr[x] << 16));
-                      y[2 * x + 1] *= sigmoid_fast(__uint_as_float(zr[x] & 0xFFFF0000u));
-                    }
+                  for (int x = 0; x < 8; ++x) w[x] = pack_bf2(o[16 * k + 2 * x], o[16 * k + 2 * x + 1]);
+                  if (p.wide_out) {
+                    st_global32(out + c + 16 * k, w);
+                  } else {
+                    *reinterpret_cast<uint4*>(out + c + 16 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(out + c + 16 * k + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                   }
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) w[4 * k + x] = pack_bf2(y[2 * x], y[2 * x + 1]);
-                }
-                if (p.wide_out) {
-                  st_global32(out + c + i, w);
-                } else {
-                  *reinterpret_cast<uint4*>(out + c + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                  *reinterpret_cast<uint4*>(out + c + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                 }
               }
             }
@@ -531,23 +524,21 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     return;
   }
   if (kE4M3 && warp >= C::kSoftWarps + 4) {
-    if constexpr (C::kSplit) regs_dec<C::kRegConv>();
     // ------------------------------------------------------------------ e4m3: codes -> binary16 stages
-    // Four warps a stage, in groups that take the stages in turn; 16 codes a load, the loads of a group's
-    // next stage wait in registers while this one's codes are widened (exactly, two an instruction),
-    // multiplied by their row's power of two relative to the block's largest, and written in the layout
-    // that the TMA gives a bf16 cache.  (A product loses what lies below binary16: less than 2^-32 of the
-    // block's largest value.)
-    constexpr int kGroups = C::kConvGroups > 0 ? C::kConvGroups : 1, kUnits = 8, kAhead = 2;
+    // Four warps a stage, in groups that take the stages in turn: a stage's codes are widened (exactly, two
+    // an instruction), multiplied by their row's power of two relative to the block's largest, and written
+    // in the layout that the TMA gives a bf16 cache.  (A product loses what lies below binary16: less than
+    // 2^-32 of the block's largest value.)
+    constexpr int kGroups = C::kConvGroups > 0 ? C::kConvGroups : 1, kUnits = 8;
+    constexpr int kRawStages = C::kRawStages > 0 ? C::kRawStages : 1;
     const int cw = warp & 3, group = (warp - (C::kSoftWarps + 4)) >> 2;
-    const int shift = p.cache.page_shift;
-    const BlockMeta* metas = reinterpret_cast<const BlockMeta*>(sm + C::kOffScale);
+    const BlockMeta* metas = reinterpret_cast<const BlockMeta*>(sm + C::kOffMeta);
     // A thread's 16 codes of a stage, unit u: 128 rows of 128 codes (narrow), or 64 of 256 (a block's
-    // values at D = 256: wide).  Lanes 0-3 take a row's 64 neighbouring codes, lanes 4-7 those of the row
-    // below, so that the swizzle spreads eight lanes' stores over all banks.
+    // values at D = 256: wide), in 64-code columns [rows][64].  Lanes 0-3 take a row's 64 codes, lanes 4-7
+    // those of the row below: eight lanes read 128 neighbouring bytes, and the swizzle spreads their
+    // stores over all banks.
     const int piece = lane & 3, odd = lane >> 2 & 1;
     const int row_narrow = cw * 4 + (lane >> 4) * 2 + odd, blk_narrow = lane >> 3 & 1, row_wide = cw * 2 + odd, blk_wide = lane >> 3;
-    const int d_narrow = blk_narrow * 64 + piece * 16, d_wide = blk_wide * 64 + piece * 16;
     const int c_narrow = (2 * piece) ^ (row_narrow & 7), c_wide = (2 * piece) ^ (row_wide & 7);
     const int to_narrow = blk_narrow * 16384 + row_narrow * 128 + c_narrow * 16, to_wide = blk_wide * 8192 + row_wide * 128 + c_wide * 16;
     const int other_narrow = ((c_narrow ^ 1) - c_narrow) * 16, other_wide = ((c_wide ^ 1) - c_wide) * 16;  // to the second half
@@ -558,7 +549,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     int mode = 0, part = -1;        // 0: keys of blk, 1: values of the block before, 2: values of blk
     int flags = 0;
     auto next_stage = [&]() {
-      if (++part == kParts || mode < 0) {
+      if (++part == kParts) {
         part = 0;
         if (kTiles == 1 && mode == 0 && !(flags & kFirst)) {
           mode = 1;
@@ -573,50 +564,36 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       if (mode == 0 && part == 0) {
         if (!await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) return false;
         flags = metas[blk % kMeta].flags;
-        if (flags & kEnd) {
-          ok = false;  // nothing is waited for any more
-          return false;
-        }
       }
-      return true;
+      return !(flags & kEnd);
     };
     Ring<kStages> ring;
+    Ring<kRawStages> raw;
     ring.skip(group);
-    uint4 raw[kAhead][kUnits] = {};
-    int what[kAhead] = {};          // bit 0: values, bit 1: part, from bit 2: the block's place; -1: no more
-    auto fetch = [&](uint4 (&x)[kUnits], int& is, int ahead) {
-      is = -1;
-      for (int i = 0; i < ahead; ++i)
-        if (!ok || !next_stage()) return;
+    raw.skip(group);
+    bool on = start->left > 0;
+    for (int ahead = group + 1; on; ahead = kGroups) {
+      for (int i = 0; i < ahead && on; ++i) on = next_stage();
+      if (!on || !await(bar.raw_full + 8 * raw.i, raw.pass) || !await(bar.empty + 8 * ring.i, ring.pass ^ 1u)) break;
       const bool value = mode != 0, wide = value && D == 256;
-      const uint32_t at = (mode == 1 ? blk - 1 : blk) % kMeta;
-      const BlockMeta& meta = metas[at];
-      const uint8_t* src = static_cast<const uint8_t*>(value ? p.cache.v : p.cache.k) + (wide ? d_wide : d_narrow + (value ? 0 : part * 128));
-      const int first = wide ? row_wide + part * 64 : row_narrow, last = meta.have - 1, mask = (1 << shift) - 1;
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u) {
-        // key of the block; behind the last visible one that one again (its scores are masked, its weights 0)
-        const int row = min(first + u * (wide ? 8 : 16), last);
-        x[u] = ld_ahead16(src + (long)(meta.row[row >> shift] + (row & mask)) * D);
-      }
-      is = value | part << 1 | at << 2;
-    };
-    auto process = [&](const uint4 (&x)[kUnits], int is) {
-      if (!mbar_wait_all(bar.empty + 8 * ring.i, ring.pass ^ 1u)) {
-        raise_error(p.err, kErrTimeout);
-        return false;
-      }
-      const bool value = is & 1, wide = value && D == 256;
-      const BlockMeta& meta = metas[is >> 2];
+      const uint32_t place = (mode == 1 ? blk - 1 : blk) % kMeta;
+      const BlockMeta& meta = metas[place];
       const uint32_t* scale = value ? meta.vf : meta.kf;
-      const int first = wide ? row_wide + (is >> 1 & 1) * 64 : row_narrow;
+      const int row0 = wide ? row_wide : row_narrow, base = wide ? part * 64 : 0, stride = wide ? 8 : 16;
+      // rows behind the last visible key read that one (their scores are masked, their weights 0, and what
+      // lies in them may be NaN)
+      const int last = min(meta.have - 1 - base, 127);
+      const uint8_t* from = sm + C::kOffRaw + raw.i * kRaw + (wide ? blk_wide * 4096 : blk_narrow * 8192) + piece * 16;
       uint8_t* to = sm + C::kOffStage + ring.i * kStage + (wide ? to_wide : to_narrow);
       const int other = wide ? other_wide : other_narrow;
-#pragma unroll
+#pragma unroll 4
       for (int u = 0; u < kUnits; ++u) {
-        const uint32_t f = scale[first + u * (wide ? 8 : 16)];
-        const uint2 a = e4m3x4_to_half4(x[u].x), b = e4m3x4_to_half4(x[u].y), c = e4m3x4_to_half4(x[u].z), e = e4m3x4_to_half4(x[u].w);
-        uint8_t* at = to + u * (wide ? 8 : 16) * 128;
+        const int row = row0 + u * stride;
+        uint4 x = make_uint4(0, 0, 0, 0);  // (a part without any visible key)
+        if (last >= 0) x = *reinterpret_cast<const uint4*>(from + min(row, last) * 64);
+        const uint32_t f = scale[base + row];
+        const uint2 a = e4m3x4_to_half4(x.x), b = e4m3x4_to_half4(x.y), c = e4m3x4_to_half4(x.z), e = e4m3x4_to_half4(x.w);
+        uint8_t* at = to + u * stride * 128;
         *reinterpret_cast<uint4*>(at) = make_uint4(mul_half2(a.x, f), mul_half2(a.y, f), mul_half2(b.x, f), mul_half2(b.y, f));
         *reinterpret_cast<uint4*>(at + other) = make_uint4(mul_half2(c.x, f), mul_half2(c.y, f), mul_half2(e.x, f), mul_half2(e.y, f));
       }
@@ -624,32 +601,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar.full + 8 * ring.i);
-        mbar_arrive(bar.meta_empty + 8 * (is >> 2));
+        mbar_arrive(bar.raw_empty + 8 * raw.i);
+        mbar_arrive(bar.meta_empty + 8 * place);
       }
       ring.skip(kGroups);
-      return true;
-    };
-    if (start->left > 0) {
-      // one copy of the code (the instruction cache is short): the waiting loads move up by a place instead
-      int step_by = group + 1;
-#pragma unroll 1
-      for (int have = 0;;) {
-#pragma unroll
-        for (int i = 0; i + 1 < kAhead; ++i) {
-          what[i] = what[i + 1];
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) raw[i][u] = raw[i + 1][u];
-        }
-        fetch(raw[kAhead - 1], what[kAhead - 1], step_by);
-        step_by = kGroups;
-        if (++have < kAhead) continue;
-        if (what[0] < 0 || !process(raw[0], what[0])) break;
-      }
+      raw.skip(kGroups);
     }
     finish();
     return;
   }
-  if constexpr (C::kSplit) regs_dec<C::kRegAux>();
   if (warp == C::kMma0 || warp == C::kMma1) {
     // ------------------------------------------------------------------ the products
     if (lane == 0) {
@@ -683,7 +643,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           const int t = which;
           const bool mine = t == 0 || seg.ntok > p.sub;
           if (mine) {
-            if (!await_one(bar.q_full + 8 * t, q_par)) break;
+            if (!await_one((kE4M3 ? bar.q_ready : bar.q_full) + 8 * t, q_par)) break;
             q_par ^= 1u;
           }
           const int last = seg.j1 - 1;
@@ -721,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           // K0 K1 V0 K2 V1 ..: one warp the keys, one the values
           const int n = seg.j1 - seg.j0;
           if (which == 0) {
-            if (!await_one(bar.q_full, q_par)) break;
+            if (!await_one(kE4M3 ? bar.q_ready : bar.q_full, q_par)) break;
             q_par ^= 1u;
             for (int i = 0; i < n && ok; ++i, ++n_blk) {
               const uint32_t slot = n_blk & 1u;
@@ -762,10 +722,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       mma_commit(bar.done);
       mbar_wait(bar.done, 0, kWaitLimit);
     }
-  } else if (kE4M3 && warp == C::kLoad) {
-    // ------------------------------------------------------------------ e4m3: pages and scales of the blocks
+  } else if (kE4M3 && warp == C::kTail) {
+    // ------------------------------------------------------------------ e4m3: scales of the blocks
     const int shift = p.cache.page_shift;
-    BlockMeta* metas = reinterpret_cast<BlockMeta*>(sm + C::kOffScale);
+    BlockMeta* metas = reinterpret_cast<BlockMeta*>(sm + C::kOffMeta);
     uint32_t blk = 0;
     auto page_of = [&](int j) {  // of the lane-th page of block j
       const int key = j * kBlock + (lane << shift);
@@ -810,7 +770,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         BlockMeta& m = metas[blk % kMeta];
         reinterpret_cast<uint4*>(m.kf)[lane] = make_uint4(kf[0], kf[1], kf[2], kf[3]);
         reinterpret_cast<uint4*>(m.vf)[lane] = make_uint4(vf[0], vf[1], vf[2], vf[3]);
-        if (lane < 8) m.row[lane] = row;
         if (lane == 0) {
           m.ku = e8m0_value(kt) * p.scale_log2;
           m.ev = (float)((int)vt - 127);
@@ -825,23 +784,28 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       metas[blk % kMeta].flags = kEnd;
       mbar_arrive(bar.meta_full + 8 * (blk % kMeta));
     }
-  } else if (!kE4M3 && warp == C::kLoad) {
+  } else if (warp == C::kLoad) {
     // ------------------------------------------------------------------ Q, K and V by TMA
+    // bf16: into the products' stages; e4m3: the codes into their own
+    constexpr int kRing = kE4M3 ? C::kRawStages : kStages;
+    constexpr uint32_t kBytes = kE4M3 ? kRaw : kStage, kPitch = kE4M3 ? 64 : 128;  // of a stage; of a row of a 64-value column
+    const uint32_t stage0 = sb + (kE4M3 ? C::kOffRaw : C::kOffStage);
+    const uint32_t bar_full = kE4M3 ? bar.raw_full : bar.full, bar_empty = kE4M3 ? bar.raw_empty : bar.empty;
     const int page = 1 << p.cache.page_shift, box = min(page, 64), box_shift = min(p.cache.page_shift, 6);
-    Ring<kStages> ring;
+    Ring<kRing> ring;
     uint32_t tails = 0, tail_par = 0, used = 0;  // stages whose last copy went to the tail barrier, its parity; stages in use
     uint32_t q_pass = 0, q_used = 0;             // bit t: parity of the next Q of tile t; Q was loaded at all
     while (ok && walk.next(p, step, seg)) {
       if (seg.keys > 0) {
         const int hk = seg.hk, keys = seg.keys;
         const int32_t* table = p.cache.table + (long)seg.n * p.cache.max_pages;
-        // One stage: `rows` keys from key0 on (those below `keys`, by whole boxes), kD 64-value blocks from
-        // d0 on, `pitch` bytes apart.
-        auto load = [&](const CUtensorMap* map, int key0, int rows, int d0, int nd, uint32_t pitch, bool value) {
-          if (!await(bar.empty + 8 * ring.i, ring.pass ^ 1u)) return;
+        // One stage: `rows` keys from key0 on (those below `keys`, by whole boxes), nd columns of 64 values
+        // from column d0 on.
+        auto load = [&](const CUtensorMap* map, int key0, int rows, int d0, int nd, bool value) {
+          if (!await(bar_empty + 8 * ring.i, ring.pass ^ 1u)) return;
           const int boxes = rows >> box_shift, have = min(max((keys - key0 + box - 1) >> box_shift, 0), boxes);
-          const bool tail = value && key0 + rows > keys;  // the warp that zeroes the rest passes it on
-          const uint32_t to = (tail ? bar.tail : bar.full) + 8 * ring.i, bit = 1u << ring.i;
+          const bool tail = !kE4M3 && value && key0 + rows > keys;  // the warp that zeroes the rest passes it on
+          const uint32_t to = (tail ? bar.tail : bar_full) + 8 * ring.i, bit = 1u << ring.i;
           used |= bit;
           tails = tail ? tails | bit : tails & ~bit;
           if (tail) tail_par ^= bit;
@@ -855,21 +819,20 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             }
             y = ((id * p.Hkv + hk) << p.cache.page_shift) + (key & (page - 1));
           }
-          if (lane == 0) mbar_arrive_expect_tx(to, (uint32_t)(have * box * nd * 128));
+          if (lane == 0) mbar_arrive_expect_tx(to, (uint32_t)(have * box * nd) * kPitch);
           __syncwarp();
           if (lane < have) {
-            const uint32_t dst = sb + C::kOffStage + ring.i * kStage + (uint32_t)(lane << box_shift) * 128;
-            for (int d = 0; d < nd; ++d) tma_load_2d(dst + d * pitch, map, (d0 + d) * 64, y, to);
+            const uint32_t dst = stage0 + ring.i * kBytes + (uint32_t)(lane << box_shift) * kPitch;
+            for (int d = 0; d < nd; ++d) tma_load_2d(dst + d * rows * kPitch, map, (d0 + d) * 64, y, to);
           }
           ring.step();
         };
         auto keys_of = [&](int j) {
-          for (int part = 0; part < kParts && ok; ++part)
-            load(&p.tmap_k, j * kBlock, 128, 2 * part, 2, 16384, false);
+          for (int part = 0; part < kParts && ok; ++part) load(&p.tmap_k, j * kBlock, 128, 2 * part, 2, false);
         };
         auto values_of = [&](int j) {
           for (int part = 0; part < kParts && ok; ++part)
-            load(&p.tmap_v, j * kBlock + part * 64, 128 / kParts, 0, D / 64, D == 256 ? 8192 : 16384, true);
+            load(&p.tmap_v, j * kBlock + part * 64, 128 / kParts, 0, D / 64, true);
         };
         keys_of(seg.j0);
         // the tile's queries (of a packed batch: the rows behind a sequence's last are the next one's, and
@@ -899,15 +862,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     // After a wait that ran out, the copies in flight land before the CTA ends: the last copy into stage
     // i went out on this pass over the ring for the stages before ring.i, on the last one for the rest.
     if (!ok) {
-      for (int i = 0; i < kStages; ++i) {
+      for (int i = 0; i < kRing; ++i) {
         if (!(used >> i & 1u)) continue;
         if (tails >> i & 1u) mbar_wait(bar.tail + 8 * i, (tail_par >> i & 1u) ^ 1u, kWaitLimit);
-        else mbar_wait(bar.full + 8 * i, i < ring.i ? ring.pass : ring.pass ^ 1u, kWaitLimit);
+        else mbar_wait(bar_full + 8 * i, i < ring.i ? ring.pass : ring.pass ^ 1u, kWaitLimit);
       }
       for (int t = 0; t < kTiles; ++t)
         if (q_used >> t & 1u) mbar_wait(bar.q_full + 8 * t, (q_pass >> t & 1u) ^ 1u, kWaitLimit);
     }
-  } else if (!kE4M3 && warp == C::kTail) {
+  } else if (warp == C::kTail) {
     // ------------------------------------------------------------------ value rows behind the last key
     Ring<kStages> ring;
     uint32_t used[kStages] = {};  // parity of each stage's tail barrier
@@ -1052,8 +1015,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
 }
 
-// Rows of K or V as the TMA sees them.
+// Rows of K or V as the TMA sees them: 64 values wide.
 cudaError_t encode_pages(CUtensorMap* map, const void* base, const PagedCache& c, int Hkv, int D) {
+  if (c.e4m3)
+    return encode_u8_2d(map, base, D, ((uint64_t)c.num_pages * Hkv) << c.page_shift, D, 64,
+                        c.page_shift > 6 ? 64 : 1u << c.page_shift);
   return encode_bf16_2d_sw128(map, base, D, ((uint64_t)c.num_pages * Hkv) << c.page_shift, (uint64_t)D * 2, 64,
                               c.page_shift > 6 ? 64 : 1u << c.page_shift);
 }
@@ -1084,11 +1050,6 @@ cudaError_t launch_tiles(const LaunchEnv& env, const AttnParams& p, int ctas) {
   if (dev >= 64 || !done[dev]) {
     e = cudaFuncSetAttribute(attn_kernel<D, kTiles, kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    // the warpgroups redistribute the registers of the launch: with fewer they would wait for ever
-    cudaFuncAttributes a;
-    e = cudaFuncGetAttributes(&a, attn_kernel<D, kTiles, kE4M3>);
-    if (e != cudaSuccess) return e;
-    if (C::kSplit && a.numRegs != C::kRegLaunch) return cudaErrorInvalidKernelImage;
     if (dev < 64) done[dev] = 1;
   }
   attn_kernel<D, kTiles, kE4M3><<<ctas, C::kThreads, C::kSmem, env.stream>>>(p);
@@ -1144,12 +1105,10 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
     if (e != cudaSuccess) return e;
     return D == 128 ? launch_join<128, 0>(env, p, ctas) : launch_join<256, 0>(env, p, ctas);
   }
-  if (!cache.e4m3) {
-    e = encode_pages(&p.tmap_k, cache.k, cache, Hkv, D);
-    if (e == cudaSuccess) e = encode_pages(&p.tmap_v, cache.v, cache, Hkv, D);
-    if (e == cudaSuccess) e = encode_bf16_3d_sw128(&p.tmap_q, q, D, Hq, T, 64, p.G, p.sub);
-    if (e != cudaSuccess) return e;
-  }
+  e = encode_pages(&p.tmap_k, cache.k, cache, Hkv, D);
+  if (e == cudaSuccess) e = encode_pages(&p.tmap_v, cache.v, cache, Hkv, D);
+  if (e == cudaSuccess) e = encode_bf16_3d_sw128(&p.tmap_q, q, D, Hq, T, 64, p.G, p.sub);
+  if (e != cudaSuccess) return e;
   // two tiles a CTA where a sequence has more rows than one holds, on average
   const bool two = (long)T * p.G > 128L * N;
   if (cache.e4m3) {

@@ -88,7 +88,9 @@ cudaError_t device_sm_count(int* sms);
 // a contiguous [outer][middle][inner] bf16 tensor with the 128-byte swizzle (box_inner 64)
 cudaError_t encode_bf16_3d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t middle, uint64_t outer,
                                  uint32_t box_inner, uint32_t box_middle, uint32_t box_outer);
-// the same for bytes with the 128-byte swizzle (box_inner 128)
+// rows of bytes, without a swizzle, and with the 128-byte one (box_inner 128)
+cudaError_t encode_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                         uint32_t box_inner, uint32_t box_outer);
 cudaError_t encode_u8_2d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                                uint32_t box_inner, uint32_t box_outer);
 // as encode_bf16_2d with the 128-byte swizzle (box_inner 64)
