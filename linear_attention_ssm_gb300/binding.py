@@ -769,71 +769,115 @@ class KVCache:
         return cls(k, v, ks, vs)
 
 
-class _on_device:
-    """Makes a tensor's device current for a call (nothing to do when it already is)."""
-
-    def __init__(self, device):
-        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-        return False
+_attn_geos = {}  # C structs of the head geometries seen so far
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the call is on {device}")
+def _attn_geo(hq: int, hkv: int, dim: int):
+    g = _attn_geos.get((hq, hkv, dim))
+    if g is None:
+        g = _attn_geos.setdefault((hq, hkv, dim), _AttnGeo(hq, hkv, dim))
+    return g
 
 
-def _cache_arg(cache: KVCache):
-    """Checks a cache and returns (its C struct, Hkv, D)."""
-    e4m3 = isinstance(cache.k, torch.Tensor) and cache.k.dtype == torch.float8_e4m3fn
-    kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
-    _dev(cache.k, kind, "cache.k")
-    if cache.k.dim() != 4:
-        raise ValueError("cache.k must be [num_pages, num_kv_heads, page_size, head_dim]")
-    pages, hkv, page, dim = cache.k.shape
-    _dev(cache.v, kind, "cache.v", (pages, hkv, page, dim))
-    ks = vs = None
-    if e4m3:
-        if cache.k_scale is None or cache.v_scale is None:
-            raise ValueError("an e4m3 cache needs k_scale and v_scale")
-        ks = _dev(cache.k_scale, torch.uint8, "cache.k_scale", (pages, hkv, page)).data_ptr()
-        vs = _dev(cache.v_scale, torch.uint8, "cache.v_scale", (pages, hkv, page)).data_ptr()
-    _same_device(cache.k.device, cache_v=cache.v, cache_k_scale=cache.k_scale if e4m3 else None,
-                 cache_v_scale=cache.v_scale if e4m3 else None)
-    return _Cache(int(e4m3), page, pages, cache.k.data_ptr(), cache.v.data_ptr(), ks, vs), hkv, dim
+def _refuse(t, dtype, name, shape, device):
+    """Says what is wrong with a tensor that _flat turned away."""
+    _dev(t, dtype, name, shape)
+    raise ValueError(f"{name} is on {t.device}, the call is on {device}")
 
 
-def _heads(t, name, T, H, D):
-    """A bf16 [T, H, D] tensor whose D values are contiguous: (pointer, token stride, head stride)."""
+def _flat(t, dtype, name, shape, device):
+    """Address of a contiguous tensor of this type and shape on the call's device (None: None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != device or \
+            not t.is_contiguous():
+        _refuse(t, dtype, name, shape, device)
+    return t.data_ptr()
+
+
+def _heads(t, name, T, H, D, device):
+    """A bf16 [T, H, D] tensor whose D values are contiguous: (address, token stride, head stride)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != (T, H, D):
+    if t.shape != (T, H, D):
         raise ValueError(f"{name} must have shape {(T, H, D)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call is on {device}")
     st, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"the values of a head of {name} must be contiguous")
     return t.data_ptr(), (st if T > 1 else H * D), (sh if H > 1 else D)
 
 
-def _attn_table(block_table, per_seq, name, cu_seqlens, T):
-    """Number of sequences of a call, its per-sequence arrays checked."""
-    N = T if cu_seqlens is None else cu_seqlens.numel() - 1
-    _dev(cu_seqlens, torch.int32, "cu_seqlens", (N + 1,))
-    _dev(per_seq, torch.int32, name, (N,))
-    _dev(block_table, torch.int32, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != N:
+def _rows_of(t, name):
+    """T and H of a [T, H, D] tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions, got {tuple(t.shape)}")
+    return t.shape[0], t.shape[1]
+
+
+def _cache_arg(cache: KVCache):
+    """Checks a cache and returns (its C struct, Hkv, D, device)."""
+    k = cache.k
+    if not isinstance(k, torch.Tensor) or not k.is_cuda:
+        raise TypeError("cache.k must be a CUDA tensor")
+    e4m3 = k.dtype is torch.float8_e4m3fn
+    kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    shape, device = k.shape, k.device
+    if len(shape) != 4:
+        raise ValueError("cache.k must be [num_pages, num_kv_heads, page_size, head_dim]")
+    kp, vp = _flat(k, kind, "cache.k", shape, device), _flat(cache.v, kind, "cache.v", shape, device)
+    ks = vs = None
+    if e4m3:
+        if cache.k_scale is None or cache.v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        ks = _flat(cache.k_scale, torch.uint8, "cache.k_scale", shape[:3], device)
+        vs = _flat(cache.v_scale, torch.uint8, "cache.v_scale", shape[:3], device)
+    pages, hkv, page, dim = shape
+    return _Cache(e4m3, page, pages, kp, vp, ks, vs), hkv, dim, device
+
+
+def _batch_args(block_table, per_seq, name, cu_seqlens, T, device):
+    """(sequences, addresses of table, per-sequence array and cu_seqlens, max_pages) of a call."""
+    if cu_seqlens is None:
+        N, cu = T, None
+    else:
+        if not isinstance(cu_seqlens, torch.Tensor):
+            raise TypeError("cu_seqlens must be a CUDA tensor")
+        N = cu_seqlens.numel() - 1
+        cu = _flat(cu_seqlens, torch.int32, "cu_seqlens", (N + 1,), device)
+    if not isinstance(block_table, torch.Tensor):
+        raise TypeError("block_table must be a CUDA tensor")
+    if block_table.dim() != 2:
         raise ValueError(f"block_table must have shape ({N}, max_pages), got {tuple(block_table.shape)}")
-    return N
+    pages = block_table.shape[1]
+    return (N, _flat(block_table, torch.int32, "block_table", (N, pages), device),
+            _flat(per_seq, torch.int32, name, (N,), device), cu, pages)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current; raises the library's error."""
+    index = device.index
+    if stream is not None:
+        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    elif _raw_stream is not None:
+        s = _raw_stream(index)
+    else:
+        s = torch.cuda.current_stream(device).cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s)
+    if status != GDN_OK:
+        _check(status)
 
 
 def gdn_attn_rope_frequencies(rot_dim: int, base: float, scaling: str = "plain", factor: float = 1.0,
@@ -858,86 +902,65 @@ def gdn_attn_prepare(q, k, v, cache: KVCache, block_table, kv_lens, cu_seqlens=N
     q [T, Hq, D], k, v [T, Hkv, D] bf16 with contiguous heads (views of one projection's output
     will do); rope_freqs [rot_dim / 2] float64 on the GPU, scaled cos and sin by rope_scale.
     """
-    lib = _L()
-    c, hkv, D = _cache_arg(cache)
-    T = k.shape[0]
-    kp, vp = _heads(k, "k", T, hkv, D), _heads(v, "v", T, hkv, D)
-    hq, qp = hkv, (None, 0, 0)
+    c, hkv, D, dev = _cache_arg(cache)
+    T, _ = _rows_of(k, "k")
+    kp, vp = _heads(k, "k", T, hkv, D, dev), _heads(v, "v", T, hkv, D, dev)
+    hq, qp, op = hkv, (None, 0, 0), None
     if q is not None:
-        hq = q.shape[1]
-        qp = _heads(q, "q", T, hq, D)
+        _, hq = _rows_of(q, "q")
+        qp = _heads(q, "q", T, hq, D, dev)
         if q_out is None:
-            q_out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device)
-        _dev(q_out, torch.bfloat16, "q_out", (T, hq, D))
+            q_out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=dev)
+        op = _flat(q_out, torch.bfloat16, "q_out", (T, hq, D), dev)
     else:
         q_out = None
-    N = _attn_table(block_table, kv_lens, "kv_lens", cu_seqlens, T)
-    _dev(q_norm_w, torch.bfloat16, "q_norm_w", (D,))
-    _dev(k_norm_w, torch.bfloat16, "k_norm_w", (D,))
+    N, table, lens, cu, pages = _batch_args(block_table, kv_lens, "kv_lens", cu_seqlens, T, dev)
     rope = None
     if rope_freqs is not None:
-        _dev(rope_freqs, torch.float64, "rope_freqs")
-        rope = ctypes.byref(_Rope(2 * rope_freqs.numel(), int(bool(rope_interleaved)), float(rope_scale),
-                                  rope_freqs.data_ptr()))
-    dev = cache.k.device
-    _same_device(dev, q=q, k=k, v=v, q_out=q_out, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens,
-                 q_norm_w=q_norm_w, k_norm_w=k_norm_w, rope_freqs=rope_freqs)
-    with _on_device(dev):
-        _check(lib.gdn_attn_prepare(ctypes.byref(_AttnGeo(hq, hkv, D)), *qp, *kp, *vp, _p(q_norm_w), _p(k_norm_w),
-                                    float(rms_eps), rope, ctypes.byref(c), _p(block_table), block_table.shape[1],
-                                    _p(kv_lens), _p(cu_seqlens), N, T, _p(q_out), _stream(stream)))
+        f = _flat(rope_freqs, torch.float64, "rope_freqs", rope_freqs.shape, dev)
+        rope = _Rope(2 * rope_freqs.numel(), bool(rope_interleaved), rope_scale, f)
+    _call(_L().gdn_attn_prepare, dev, stream, _attn_geo(hq, hkv, D), *qp, *kp, *vp,
+          _flat(q_norm_w, torch.bfloat16, "q_norm_w", (D,), dev), _flat(k_norm_w, torch.bfloat16, "k_norm_w", (D,), dev),
+          rms_eps, rope, c, table, pages, lens, cu, N, T, op)
     return q_out
 
 
 def gdn_attn_cache_read(cache: KVCache, block_table, cu_seqlens, k_out, v_out, starts=None, stream=None):
     """Rows of the cache as dense bf16: k_out, v_out [T, Hkv, D] receive, for every sequence, the
     positions from starts[n] (0 when None) on; returns (k_out, v_out)."""
-    lib = _L()
-    c, hkv, D = _cache_arg(cache)
-    T = k_out.shape[0]
-    _dev(k_out, torch.bfloat16, "k_out", (T, hkv, D))
-    _dev(v_out, torch.bfloat16, "v_out", (T, hkv, D))
-    N = _attn_table(block_table, starts, "starts", cu_seqlens, T)
-    dev = cache.k.device
-    _same_device(dev, k_out=k_out, v_out=v_out, block_table=block_table, starts=starts, cu_seqlens=cu_seqlens)
-    with _on_device(dev):
-        _check(lib.gdn_attn_cache_read(ctypes.byref(_AttnGeo(hkv, hkv, D)), ctypes.byref(c), _p(block_table),
-                                       block_table.shape[1], _p(starts), _p(cu_seqlens), N, T, _p(k_out), _p(v_out),
-                                       _stream(stream)))
+    c, hkv, D, dev = _cache_arg(cache)
+    T, _ = _rows_of(k_out, "k_out")
+    kp = _flat(k_out, torch.bfloat16, "k_out", (T, hkv, D), dev)
+    vp = _flat(v_out, torch.bfloat16, "v_out", (T, hkv, D), dev)
+    N, table, first, cu, pages = _batch_args(block_table, starts, "starts", cu_seqlens, T, dev)
+    _call(_L().gdn_attn_cache_read, dev, stream, _attn_geo(hkv, hkv, D), c, table, pages, first, cu, N, T, kp, vp)
     return k_out, v_out
 
 
 def gdn_attn_workspace_size(num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
-    return int(_L().gdn_attn_workspace_size(ctypes.byref(_AttnGeo(num_q_heads, num_kv_heads, head_dim))))
+    return int(_L().gdn_attn_workspace_size(_attn_geo(num_q_heads, num_kv_heads, head_dim)))
 
 
 def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out, workspace, stream):
     lib = _L()
-    c, hkv, D = _cache_arg(cache)
-    _dev(q, torch.bfloat16, "q")
-    if q.dim() != 3 or q.shape[2] != D:
-        raise ValueError(f"q must have shape (T, Hq, {D}), got {tuple(q.shape)}")
-    T, hq, _ = q.shape
-    N = _attn_table(block_table, kv_lens, "kv_lens", cu_seqlens, T)
-    zp = (None, 0, 0) if z is None else _heads(z, "z", T, hq, D)
+    c, hkv, D, dev = _cache_arg(cache)
+    T, hq = _rows_of(q, "q")
+    qp = _flat(q, torch.bfloat16, "q", (T, hq, D), dev)
+    N, table, lens, cu, pages = _batch_args(block_table, kv_lens, "kv_lens", cu_seqlens, T, dev)
+    zp = (None, 0, 0) if z is None else _heads(z, "z", T, hq, D, dev)
     if out is None:
-        out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=q.device)
-    _dev(out, torch.bfloat16, "out", (T, hq, D))
-    geo = ctypes.byref(_AttnGeo(hq, hkv, D))
+        out = torch.empty_like(q)
+    op = _flat(out, torch.bfloat16, "out", (T, hq, D), dev)
+    geo = _attn_geo(hq, hkv, D)
     if workspace is None:
-        workspace = torch.empty(lib.gdn_attn_workspace_size(geo), dtype=torch.uint8, device=q.device)
-    dev = cache.k.device
-    _same_device(dev, q=q, z=z, out=out, block_table=block_table, kv_lens=kv_lens, cu_seqlens=cu_seqlens,
-                 workspace=workspace)
-    with _on_device(dev):
-        args = (float(softmax_scale), *zp, _p(out), _p(workspace), workspace.numel() * workspace.element_size(),
-                _stream(stream))
-        if cu_seqlens is None:
-            _check(lib.gdn_attn_decode_step(geo, _p(q), ctypes.byref(c), _p(block_table), block_table.shape[1],
-                                            _p(kv_lens), T, *args))
-        else:
-            _check(lib.gdn_attn_prefill(geo, _p(q), ctypes.byref(c), _p(block_table), block_table.shape[1],
-                                        _p(kv_lens), _p(cu_seqlens), N, T, *args))
+        workspace = torch.empty(lib.gdn_attn_workspace_size(geo), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the call is on {dev}")
+    tail = (softmax_scale, *zp, op, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    if cu is None:
+        _call(lib.gdn_attn_decode_step, dev, stream, geo, qp, c, table, pages, lens, T, *tail)
+    else:
+        _call(lib.gdn_attn_prefill, dev, stream, geo, qp, c, table, pages, lens, cu, N, T, *tail)
     return out
 
 
