@@ -1,22 +1,18 @@
 // attn_cache.cu -- the paged key/value cache: queries and keys normalised and rotated, keys and values
 // written to their pages (bf16, or e4m3 with one power of two for a row) in one pass; rows read back.
 //
-// Both kernels move each byte once and do a few operations on it, so HBM bounds them: one warp (half
-// a warp at D = 128) holds one head row of a token, 16 bytes a lane, four rows in flight.
+// Both kernels move each byte once and do a few operations on it, so HBM bounds them, and instructions
+// next: a warp takes one token's heads (a share of them where tokens are few), so that the place in the
+// cache, the angles and the products of weights with their cosines and sines are formed once for all
+// heads, and a head costs a 16-byte load a lane, one reduction and two packed fused multiply-adds for
+// each pair of values.  Four heads' loads are in flight.
 #include "attn_common.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // tokens of one CTA
-constexpr int kUnroll = 4;     // rows whose loads a lane has in flight
-
-struct Place {
-  int seq;   // < 0: no sequence
-  int pos;   // position in the sequence
-  long row;  // page * rows per page slab: index of the head-0 row of the position; -1: no place in the cache
-};
+constexpr int kWarps = 8;
+constexpr int kUnroll = 4;  // loads that a lane has in flight
 
 struct PrepareParams {
   HeadRows q, k, v;
@@ -29,7 +25,7 @@ struct PrepareParams {
   unsigned* err;
   uint16_t* q_out;
   float eps;
-  int Hq, Hkv, N, T, tokens;  // tokens: of one CTA
+  int Hq, Hkv, N, T, split;  // split: warps of one token
 };
 
 // p * f turns, reduced to [-1/2, 1/2]: p is split into two factors that fp32 holds, each product with
@@ -91,159 +87,153 @@ __device__ __forceinline__ void store_e4m3(const float (&x)[8], uint8_t* codes, 
   if (lane == 0) *byte = (uint8_t)(e + 127);
 }
 
-template <int D, bool kE4M3>
-__global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant__ PrepareParams p) {
-  constexpr int kLanes = D / 8;              // lanes of a row
-  constexpr int kSlots = kThreads / kLanes;  // rows at a time
-  __shared__ Place s_place[kMaxTokens];
-  __shared__ __align__(16) float2 s_cs[kMaxTokens][D / 2];
-  const int tid = threadIdx.x, lane = tid % kLanes, slot = tid / kLanes;
-  const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
-
-  if (tid < nt) {
-    Place pl;
-    int first, len;
-    bool bad = false;
-    pl.seq = attn_seq_of(p.cu, p.N, p.T, t0 + tid, first, len);
-    pl.pos = 0;
-    pl.row = -1;
-    if (pl.seq >= 0) {
-      const int kv = __ldg(p.kv_lens + pl.seq);
-      if (kv < 0 || kv > (int)min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) {
-        bad = true;
-        pl.seq = -2;
-      } else {
-        pl.pos = kv - len + (t0 + tid - first);
-        if (pl.pos >= 0) pl.row = cache_row(p.cache, p.Hkv, pl.seq, pl.pos, bad);
-      }
-    } else if (pl.seq == -2) {
-      bad = true;
-    }
-    if (bad) raise_error(p.err, kErrDeviceArgument);
-    s_place[tid] = pl;
-  }
-  __syncthreads();
-  if (const int np = p.rope.rot / 2) {
-    const int groups = kThreads / np, j = tid % np;
-    if (tid < groups * np) {
-      const double f = __ldg(p.rope.freqs + j) * 0.15915494309189533577;  // turns of one position
-      const float hi = (float)f, lo = (float)(f - (double)hi);
-      for (int t = tid / np; t < nt; t += groups) {
-        float s, c;
-        sincospif(2.f * turns_of(s_place[t].pos, hi, lo), &s, &c);
-        s_cs[t][j] = make_float2(c * p.rope.magnitude, s * p.rope.magnitude);
-      }
-    }
-  }
-  // this lane's eight weights of the query and the key norm
-  uint4 qw = make_uint4(0, 0, 0, 0), kw = qw;
-  if (p.qw) qw = __ldg(reinterpret_cast<const uint4*>(p.qw) + lane);
-  if (p.kw) kw = __ldg(reinterpret_cast<const uint4*>(p.kw) + lane);
-  __syncthreads();
-
-  const int hq = p.q.p ? p.Hq : 0, per = hq + 2 * p.Hkv, rows = nt * per;
-  for (int base = slot; base < rows + slot; base += kSlots * kUnroll) {  // the same trips for every thread
+// Heads of one kind of a token, D / 8 lanes a head (two heads at a time at D = 128): loads, `work` on the
+// head's eight values of this lane (four words of two), `store`.  All lanes run every step.
+template <int D, typename Work, typename Store>
+__device__ __forceinline__ void each_head(const HeadRows& rows, long t, int heads, int first, int step, Work work, Store store) {
+  constexpr int kAt = 256 / D;  // heads of the warp at a time
+  const int lane = threadIdx.x & 31, mine = lane / (D / 8);
+  const uint16_t* src = rows.p + t * rows.token + (lane % (D / 8)) * 8;
+  for (int h0 = first * kAt; h0 < heads; h0 += step * kAt * kUnroll) {
     uint4 raw[kUnroll];
-    int tok[kUnroll], head[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int idx = base + u * kSlots;
-      tok[u] = idx / per;
-      head[u] = idx - tok[u] * per;
-      if (idx >= rows || s_place[tok[u]].seq < 0) tok[u] = -1;
+      const int h = h0 + u * step * kAt + mine;
       raw[u] = make_uint4(0, 0, 0, 0);
-      if (tok[u] >= 0) {
-        const int h = head[u];
-        const HeadRows& src = h < hq ? p.q : h < hq + p.Hkv ? p.k : p.v;
-        const int hh = h < hq ? h : h < hq + p.Hkv ? h - hq : h - hq - p.Hkv;
-        raw[u] = __ldcs(reinterpret_cast<const uint4*>(src.p + (t0 + tok[u]) * src.token + hh * src.head) + lane);
-      }
+      if (h < heads) raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + h * rows.head));
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (__all_sync(0xFFFFFFFFu, tok[u] < 0)) continue;
-      const bool is_q = head[u] < hq, is_k = !is_q && head[u] < hq + p.Hkv;
-      float x[8];
-      const uint32_t r[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      const int h = h0 + u * step * kAt;
+      if (h < heads) store(h + mine, work(raw[u]), h + mine < heads);
+    }
+  }
+}
+
+__device__ __forceinline__ float2 bf2_to_float2(uint32_t v) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+template <int D, bool kE4M3>
+__global__ void __launch_bounds__(32 * kWarps) prepare_kernel(const __grid_constant__ PrepareParams p) {
+  constexpr int kLanes = D / 8;  // lanes of a head
+  __shared__ __align__(16) float2 s_cs[kWarps][D / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
+  const long item = (long)blockIdx.x * kWarps + warp;
+  const int t = (int)(item / p.split), share = (int)(item - (long)t * p.split);
+  if (t >= p.T) return;
+  int first, len;
+  const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
+  if (seq < 0) {
+    if (seq == -2) raise_error(p.err, kErrDeviceArgument);
+    return;
+  }
+  const int kv = __ldg(p.kv_lens + seq);
+  if (kv < 0 || kv > min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) {
+    raise_error(p.err, kErrDeviceArgument);
+    return;
+  }
+  const int pos = kv - len + (t - first);
+  long place = -1;  // head-0 row of the position in the pool
+  bool bad = false;
+  if (pos >= 0) place = cache_row(p.cache, p.Hkv, seq, pos, bad);
+  if (bad) raise_error(p.err, kErrDeviceArgument);
+
+  // the token's cosines and sines
+  const int rot = p.rope.rot, half = rot / 2;
+  for (int j = lane; j < half; j += 32) {
+    const double f = __ldg(p.rope.freqs + j) * 0.15915494309189533577;  // turns of one position
+    const float hi = (float)f;
+    float s, c;
+    sincospif(2.f * turns_of(pos, hi, (float)(f - (double)hi)), &s, &c);
+    s_cs[warp][j] = make_float2(c * p.rope.magnitude, s * p.rope.magnitude);
+  }
+  __syncwarp();
+  // This lane's eight values of a head become x * a + y * b, y the values they are paired with (for halves
+  // another lane's, half / 8 lanes away, else neighbours), times the norm's factor.
+  const int d0 = sub * 8, away = half / 8;
+  const bool turned = d0 < rot, low = d0 < half;
+  const int partner = (lane - sub) + (!turned || p.rope.interleaved ? sub : low ? sub + away : sub - away);
+  auto run = [&](const HeadRows& rows, const uint16_t* w, int heads, auto store) {
+    float2 a[4], b[4];
+    {
+      float wx[8], wy[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int dy = p.rope.interleaved ? (d0 + i) ^ 1 : (partner % kLanes) * 8 + i;
+        wx[i] = w ? bf2f(__ldg(w + d0 + i)) : 1.f;
+        wy[i] = w ? bf2f(__ldg(w + dy)) : 1.f;
+      }
+      float fa[8], fb[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 cs = turned ? s_cs[warp][p.rope.interleaved ? (d0 + i) >> 1 : (low ? d0 : d0 - half) + i] : make_float2(1.f, 0.f);
+        const bool minus = p.rope.interleaved ? !(i & 1) : low;
+        fa[i] = wx[i] * cs.x;
+        fb[i] = wy[i] * (minus ? -cs.y : cs.y);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(r[i] << 16);
-        x[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
-      }
-      if (__any_sync(0xFFFFFFFFu, is_q || is_k)) {
-        const int t = max(tok[u], 0);
-        float y[8];
-        const uint16_t* w_on = is_q ? p.qw : p.kw;
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        const float rms = w_on ? rsqrtf(ss * (1.f / D) + p.eps) : 1.f;
-        const uint4 w4 = is_q ? qw : kw;
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          y[2 * i] = x[2 * i] * rms;
-          y[2 * i + 1] = x[2 * i + 1] * rms;
-          if (w_on) {
-            y[2 * i] *= __uint_as_float(w[i] << 16);
-            y[2 * i + 1] *= __uint_as_float(w[i] & 0xFFFF0000u);
-          }
-        }
-        if (p.rope.rot) {
-          const int d0 = lane * 8;
-          if (p.rope.interleaved) {
-            if (d0 < p.rope.rot) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 cs = s_cs[t][d0 / 2 + i];
-                const float a = y[2 * i], b = y[2 * i + 1];
-                y[2 * i] = fmaf(a, cs.x, -b * cs.y);
-                y[2 * i + 1] = fmaf(b, cs.x, a * cs.y);
-              }
-            }
-          } else {  // the other half of a pair sits rot / 16 lanes away
-            const int half = p.rope.rot / 2, off = half / 8;
-            const bool low = d0 < half, in = d0 < p.rope.rot;
-            const int src = in ? (low ? lane + off : lane - off) : lane;
-            float o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xFFFFFFFFu, y[i], src, kLanes);
-            if (in) {
-              const float2* cs = &s_cs[t][low ? d0 : d0 - half];
-#pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = fmaf(y[i], cs[i].x, (low ? -o[i] : o[i]) * cs[i].y);
-            }
-          }
-        }
-        if (is_q || is_k) {  // the one rounding to bf16
-          raw[u] = make_uint4(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7]));
-        }
-      }
-      const Place pl = s_place[max(tok[u], 0)];
-      if (tok[u] >= 0 && is_q)
-        *(reinterpret_cast<uint4*>(p.q_out + ((long)(t0 + tok[u]) * p.Hq + head[u]) * D) + lane) = raw[u];
-      const bool to_cache = tok[u] >= 0 && !is_q && pl.row >= 0;
-      const int h = is_k ? head[u] - hq : head[u] - hq - p.Hkv;
-      const long row = pl.row + ((long)h << p.cache.page_shift);
-      if constexpr (kE4M3) {
-        if (__any_sync(0xFFFFFFFFu, to_cache)) {
-          const uint32_t b[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(b[i] << 16);
-            x[2 * i + 1] = __uint_as_float(b[i] & 0xFFFF0000u);
-          }
-          uint8_t* codes = static_cast<uint8_t*>(is_k ? p.cache.k : p.cache.v) + row * D;
-          uint8_t* byte = (is_k ? p.cache.k_scale : p.cache.v_scale) + row;
-          store_e4m3<D>(x, codes, byte, lane, to_cache);
-        }
-      } else {
-        if (to_cache)
-          *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(is_k ? p.cache.k : p.cache.v) + row * D) + lane) = raw[u];
+        a[i] = make_float2(fa[2 * i], fa[2 * i + 1]);
+        b[i] = make_float2(fb[2 * i], fb[2 * i + 1]);
       }
     }
+    each_head<D>(rows, t, heads, share, p.split, [&](const uint4& raw) {
+      const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+      float2 x[4], y[4], ss = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = bf2_to_float2(r[i]);
+      if (rot && !p.rope.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = bf2_to_float2(__shfl_sync(0xFFFFFFFFu, r[i], partner));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = make_float2(x[i].y, x[i].x);
+      }
+      float rms = 1.f;
+      if (w) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss = __ffma2_rn(x[i], x[i], ss);
+        float s = ss.x + ss.y;
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        rms = rsqrtf(s * (1.f / D) + p.eps);
+      }
+      uint32_t out[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // without a rotation the paired value does not enter at all (it may be an infinity)
+        const float2 z = turned ? __ffma2_rn(x[i], a[i], __fmul2_rn(y[i], b[i])) : __fmul2_rn(x[i], a[i]);
+        out[i] = pack_bf2(z.x * rms, z.y * rms);  // the one rounding to bf16
+      }
+      return make_uint4(out[0], out[1], out[2], out[3]);
+    }, store);
+  };
+  auto to_cache = [&](void* pages, uint8_t* bytes) {
+    return [=, &p](int h, const uint4& v, bool in) {
+      const long row = place + ((long)h << p.cache.page_shift);
+      if constexpr (kE4M3) {
+        const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = bf2_to_float2(r[i]);
+          x[2 * i] = f.x;
+          x[2 * i + 1] = f.y;
+        }
+        store_e4m3<D>(x, static_cast<uint8_t*>(pages) + row * D, bytes + row, sub, in);
+      } else if (in) {
+        *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(pages) + row * D) + sub) = v;
+      }
+    };
+  };
+  if (p.q.p)
+    run(p.q, p.qw, p.Hq, [&](int h, const uint4& v, bool in) {
+      if (in) *(reinterpret_cast<uint4*>(p.q_out + ((long)t * p.Hq + h) * D) + sub) = v;
+    });
+  if (place >= 0) {
+    run(p.k, p.kw, p.Hkv, to_cache(p.cache.k, p.cache.k_scale));
+    each_head<D>(p.v, t, p.Hkv, share, p.split, [](const uint4& raw) { return raw; }, to_cache(p.cache.v, p.cache.v_scale));
   }
 }
 
@@ -254,80 +244,80 @@ struct ReadParams {
   unsigned* err;
   uint16_t* k_out;
   uint16_t* v_out;
-  int Hkv, N, T, tokens;
+  int Hkv, N, T, split;
 };
 
-// 16 bytes of the cache a lane: 8 bf16 values copied, or 16 codes widened.
+// 16 bytes of the cache a lane: 8 bf16 values copied, or 16 codes widened.  A warp's lanes hold a head's
+// keys and its values side by side (at D = 256 in bf16, one and then the other), or those of two heads.
 template <int D, bool kE4M3>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams p) {
-  constexpr int kVals = kE4M3 ? 16 : 8, kLanes = D / kVals, kSlots = kThreads / kLanes;
-  __shared__ long s_row[kMaxTokens];
-  const int tid = threadIdx.x, lane = tid % kLanes, slot = tid / kLanes;
-  const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
-  if (tid < nt) {
-    int first, len;
-    bool bad = false;
-    long row = -1;
-    const int seq = attn_seq_of(p.cu, p.N, p.T, t0 + tid, first, len);
-    if (seq >= 0) {
-      const long pos = (p.starts ? (long)__ldg(p.starts + seq) : 0L) + (t0 + tid - first);
-      if (pos < 0 || pos >= min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) bad = true;
-      else row = cache_row(p.cache, p.Hkv, seq, (int)pos, bad);
-    } else if (seq == -2) {
-      bad = true;
-    }
-    if (bad) raise_error(p.err, kErrDeviceArgument);
-    s_row[tid] = row;
+__global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int kVals = kE4M3 ? 16 : 8, kLanes = D / kVals, kAt = 32 / kLanes;  // rows at a time: 1, 2 or 4
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, mine = lane / kLanes;
+  const long item = (long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int t = (int)(item / p.split), share = (int)(item - (long)t * p.split);
+  if (t >= p.T) return;
+  int first, len;
+  bool bad = false;
+  long place = -1;
+  const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
+  if (seq >= 0) {
+    const long pos = (p.starts ? (long)__ldg(p.starts + seq) : 0L) + (t - first);
+    if (pos < 0 || pos >= min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) bad = true;
+    else place = cache_row(p.cache, p.Hkv, seq, (int)pos, bad);
+  } else if (seq == -2) {
+    bad = true;
   }
-  __syncthreads();
-  const int per = 2 * p.Hkv, rows = nt * per;
-  for (int base = slot; base < rows; base += kSlots * kUnroll) {
+  if (bad) raise_error(p.err, kErrDeviceArgument);
+  if (place < 0) return;
+  // row r of the token: head r / 2, its keys (even) or values (odd)
+  const bool keys0 = ((share * kAt + mine) & 1) == 0;
+  const int rows = 2 * p.Hkv, step = p.split * kAt;
+  for (int r0 = share * kAt; r0 < rows; r0 += step * kUnroll) {
     uint4 raw[kUnroll];
     uint32_t byte[kUnroll];
-    uint16_t* dst[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int idx = base + u * kSlots;
-      dst[u] = nullptr;
-      if (idx >= rows) continue;
-      const int tok = idx / per, hh = idx - tok * per, h = hh < p.Hkv ? hh : hh - p.Hkv;
-      if (s_row[tok] < 0) continue;
-      const bool is_k = hh < p.Hkv;
-      const long row = s_row[tok] + ((long)h << p.cache.page_shift);
-      const void* src = is_k ? p.cache.k : p.cache.v;
-      raw[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(src) + row * (D * (kE4M3 ? 1 : 2))) + lane);
-      if constexpr (kE4M3) byte[u] = __ldg((is_k ? p.cache.k_scale : p.cache.v_scale) + row);
-      dst[u] = (is_k ? p.k_out : p.v_out) + ((long)(t0 + tok) * p.Hkv + h) * D + lane * kVals;
+      const int r = r0 + u * step + mine;
+      const bool is_k = kAt > 1 ? keys0 : (r & 1) == 0;
+      const long row = place + ((long)(r >> 1) << p.cache.page_shift);
+      if (r < rows) {
+        raw[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(is_k ? p.cache.k : p.cache.v) +
+                                                       row * (D * (kE4M3 ? 1 : 2))) + sub);
+        if constexpr (kE4M3) byte[u] = __ldg((is_k ? p.cache.k_scale : p.cache.v_scale) + row);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (!dst[u]) continue;
+      const int r = r0 + u * step + mine;
+      if (r >= rows) continue;
+      const bool is_k = kAt > 1 ? keys0 : (r & 1) == 0;
+      uint16_t* dst = (is_k ? p.k_out : p.v_out) + ((long)t * p.Hkv + (r >> 1)) * D + sub * kVals;
       if constexpr (kE4M3) {
         const float s = e8m0_value(byte[u]);
-        const uint32_t r[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+        const uint32_t c[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
         uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 a = e4m3x2_to_float2((uint16_t)(r[i] & 0xFFFFu)), b = e4m3x2_to_float2((uint16_t)(r[i] >> 16));
+          const uint2 h = e4m3x4_to_half4(c[i]);
+          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
           o[2 * i] = pack_bf2(a.x * s, a.y * s);
           o[2 * i + 1] = pack_bf2(b.x * s, b.y * s);
         }
-        reinterpret_cast<uint4*>(dst[u])[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<uint4*>(dst[u])[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
       } else {
-        *reinterpret_cast<uint4*>(dst[u]) = raw[u];
+        *reinterpret_cast<uint4*>(dst) = raw[u];
       }
     }
   }
 }
 
-// Tokens of a CTA: one while that fills the GPU eight CTAs deep, then more, so that the rotation's
-// angles and the weights are formed for several tokens at a time.
-int tokens_per_cta(int T, int sms) {
-  const int t = (T + sms * 8 - 1) / (sms * 8);
-  return t < 1 ? 1 : t > kMaxTokens ? kMaxTokens : t;
+// Warps of one token: as many as bring sixteen warps to every SM, as long as each has loads to keep in
+// flight (`units`: steps of a warp that has the token alone).
+int warps_of_token(int T, int sms, int units) {
+  const int want = (16 * sms + T - 1) / T, most = units < 8 ? units : 8;
+  return want < 1 ? 1 : want > most ? most : want;
 }
-
 }  // namespace
 
 cudaError_t launch_attn_prepare(const LaunchEnv& env, int Hq, int Hkv, int D, const HeadRows& q, const HeadRows& k,
@@ -337,12 +327,12 @@ cudaError_t launch_attn_prepare(const LaunchEnv& env, int Hq, int Hkv, int D, co
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const int tokens = tokens_per_cta(T, sms);
-  const PrepareParams p = {q, k, v, qw, kw, cache, rope, kv_lens, cu, env.err, q_out, eps, Hq, Hkv, N, T, tokens};
-  const int grid = (T + tokens - 1) / tokens;
+  const int split = warps_of_token(T, sms, (Hq * D + 255) / 256);
+  const PrepareParams p = {q, k, v, qw, kw, cache, rope, kv_lens, cu, env.err, q_out, eps, Hq, Hkv, N, T, split};
+  const unsigned grid = (unsigned)(((long)T * split + kWarps - 1) / kWarps);
   auto kern = D == 128 ? (cache.e4m3 ? prepare_kernel<128, true> : prepare_kernel<128, false>)
                        : (cache.e4m3 ? prepare_kernel<256, true> : prepare_kernel<256, false>);
-  kern<<<grid, kThreads, 0, env.stream>>>(p);
+  kern<<<grid, 32 * kWarps, 0, env.stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -352,12 +342,12 @@ cudaError_t launch_attn_cache_read(const LaunchEnv& env, int Hkv, int D, const P
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const int tokens = tokens_per_cta(T, sms);
-  const ReadParams p = {cache, starts, cu, env.err, k_out, v_out, Hkv, N, T, tokens};
-  const int grid = (T + tokens - 1) / tokens;
+  const int split = warps_of_token(T, sms, (2 * Hkv * D * (cache.e4m3 ? 1 : 2) + 511) / 512);
+  const ReadParams p = {cache, starts, cu, env.err, k_out, v_out, Hkv, N, T, split};
+  const unsigned grid = (unsigned)(((long)T * split + kWarps - 1) / kWarps);
   auto kern = D == 128 ? (cache.e4m3 ? cache_read_kernel<128, true> : cache_read_kernel<128, false>)
                        : (cache.e4m3 ? cache_read_kernel<256, true> : cache_read_kernel<256, false>);
-  kern<<<grid, kThreads, 0, env.stream>>>(p);
+  kern<<<grid, 32 * kWarps, 0, env.stream>>>(p);
   return cudaGetLastError();
 }
 
