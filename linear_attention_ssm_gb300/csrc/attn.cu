@@ -128,25 +128,12 @@ struct Ring {
 
 // Loads that stay where they are written: the compiler may otherwise sink a read-only load to its use,
 // three stages later.
-__device__ __forceinline__ uint4 ld_ahead16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
 __device__ __forceinline__ uint32_t ld_ahead4(const void* p) {
   uint32_t v;
   asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 
-// 32 bytes of one thread (aligned to them): a whole sector
-__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
-               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -180,10 +167,6 @@ __device__ __forceinline__ void tmem_st16_begin(uint32_t taddr, const float (&v)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, kWaitLimit));
-}
-
 // 2^e, e <= 0, twice in binary16 (0 below its range)
 __device__ __forceinline__ uint32_t half2_power(int e) {
   const uint32_t h = e >= -14 ? (uint32_t)(15 + e) << 10 : e >= -24 ? 1u << (e + 24) : 0u;

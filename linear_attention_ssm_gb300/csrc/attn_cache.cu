@@ -11,7 +11,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;   // of a CTA: short ones, so that the last wave of CTAs is short too
 constexpr int kUnroll = 4;  // loads that a lane has in flight
 
 struct PrepareParams {
@@ -52,35 +52,45 @@ __device__ __forceinline__ long cache_row(const PagedCache& c, int Hkv, int seq,
   return (((long)page * Hkv) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
 }
 
-// Eight values of a row of which D / 8 neighbouring lanes hold one each: stores their codes and, by the
-// row's first lane, the exponent byte (where `store` is set: the shuffles want the whole warp).
+// Eight bf16 values of a row of which D / 8 neighbouring lanes hold eight each: stores their codes and, by
+// the row's first lane, the exponent byte (where `store` is set: the shuffles want the whole warp).
 template <int D>
-__device__ __forceinline__ void store_e4m3(const float (&x)[8], uint8_t* codes, uint8_t* byte, int lane,
-                                           bool store) {
-  uint32_t top = 0;  // the row's largest finite magnitude, as bits
+__device__ __forceinline__ void store_e4m3(const uint4& v, uint8_t* codes, uint8_t* byte, int lane, bool store) {
+  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+  auto row_max = [&](uint32_t top) {  // of two 16-bit magnitudes a lane
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-    top = max(top, b < 0x7F800000u ? b : 0u);
+    for (int o = D / 16; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    return max(top & 0xFFFFu, top >> 16);
+  };
+  uint32_t mag[4], top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    mag[i] = r[i] & 0x7FFF7FFFu;
+    top = __vmaxu2(top, mag[i]);
   }
+  top = row_max(top);
+  const bool odd = __any_sync(0xFFFFFFFFu, top >= 0x7F80u);  // some row has a value that is not finite
+  if (odd) {  // the largest of the others
+    uint32_t t = 0;
 #pragma unroll
-  for (int o = D / 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    for (int i = 0; i < 4; ++i) {
+      if ((mag[i] & 0xFFFFu) < 0x7F80u) t = max(t, mag[i] & 0xFFFFu);
+      if (mag[i] >> 16 < 0x7F80u) t = max(t, mag[i] >> 16);
+    }
+    top = row_max(t);
+  }
   // 448 = 1.75 * 2^8: the exponent of the magnitude less 8, one more when its significand is above 1.75
-  const int e = max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0), -117);
+  const int e = max((int)(top >> 7) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0), -117);
   const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-  uint32_t w[2];
+  uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t r = 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float2 y = make_float2(x[4 * i + 2 * j] * inv, x[4 * i + 2 * j + 1] * inv);
-      // the conversion saturates: what is not finite becomes NaN here
+  for (int i = 0; i < 4; ++i) {
+    float2 y = __fmul2_rn(make_float2(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u)), make_float2(inv, inv));
+    if (odd) {  // the conversion saturates: what is not finite becomes NaN here
       if (!isfinite(y.x)) y.x = __uint_as_float(0x7FFFFFFFu);
       if (!isfinite(y.y)) y.y = __uint_as_float(0x7FFFFFFFu);
-      r |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * j);
     }
-    w[i] = r;
+    w[i >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * (i & 1));
   }
   if (!store) return;
   *reinterpret_cast<uint2*>(codes + lane * 8) = make_uint2(w[0], w[1]);
@@ -115,13 +125,22 @@ __device__ __forceinline__ float2 bf2_to_float2(uint32_t v) {
 }
 
 template <int D, bool kE4M3>
-__global__ void __launch_bounds__(32 * kWarps) prepare_kernel(const __grid_constant__ PrepareParams p) {
+__global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_constant__ PrepareParams p) {
   constexpr int kLanes = D / 8;  // lanes of a head
   __shared__ __align__(16) float2 s_cs[kWarps][D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
   const long item = (long)blockIdx.x * kWarps + warp;
   const int t = (int)(item / p.split), share = (int)(item - (long)t * p.split);
   if (t >= p.T) return;
+  // the token's rows are on their way while its place in the cache is looked up
+  auto ahead = [&](const HeadRows& rows, int heads) {
+    const char* at = reinterpret_cast<const char*>(rows.p + t * rows.token);
+    for (int i = lane + 32 * share; i < heads * (D / 64); i += 32 * p.split)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(at + (i / (D / 64)) * rows.head * 2 + (i % (D / 64)) * 128));
+  };
+  if (p.q.p) ahead(p.q, p.Hq);
+  ahead(p.k, p.Hkv);
+  ahead(p.v, p.Hkv);
   int first, len;
   const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
   if (seq < 0) {
@@ -154,28 +173,29 @@ __global__ void __launch_bounds__(32 * kWarps) prepare_kernel(const __grid_const
   const int d0 = sub * 8, away = half / 8;
   const bool turned = d0 < rot, low = d0 < half;
   const int partner = (lane - sub) + (!turned || p.rope.interleaved ? sub : low ? sub + away : sub - away);
+  const uint32_t paired = turned ? 0xFFFFFFFFu : 0u;  // without a rotation b is 0, and y too: it might be an infinity
   auto run = [&](const HeadRows& rows, const uint16_t* w, int heads, auto store) {
     float2 a[4], b[4];
     {
-      float wx[8], wy[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int dy = p.rope.interleaved ? (d0 + i) ^ 1 : (partner % kLanes) * 8 + i;
-        wx[i] = w ? bf2f(__ldg(w + d0 + i)) : 1.f;
-        wy[i] = w ? bf2f(__ldg(w + dy)) : 1.f;
+      uint4 own = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), pair = own;  // bf16 ones
+      if (w) {
+        own = __ldg(reinterpret_cast<const uint4*>(w) + sub);
+        pair = p.rope.interleaved ? own : __ldg(reinterpret_cast<const uint4*>(w) + (partner % kLanes));
       }
-      float fa[8], fb[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 cs = turned ? s_cs[warp][p.rope.interleaved ? (d0 + i) >> 1 : (low ? d0 : d0 - half) + i] : make_float2(1.f, 0.f);
-        const bool minus = p.rope.interleaved ? !(i & 1) : low;
-        fa[i] = wx[i] * cs.x;
-        fb[i] = wy[i] * (minus ? -cs.y : cs.y);
-      }
+      const uint32_t wo[4] = {own.x, own.y, own.z, own.w}, wp[4] = {pair.x, pair.y, pair.z, pair.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        a[i] = make_float2(fa[2 * i], fa[2 * i + 1]);
-        b[i] = make_float2(fb[2 * i], fb[2 * i + 1]);
+        const float2 x = bf2_to_float2(wo[i]), y = bf2_to_float2(wp[i]);
+        float4 cs = make_float4(1.f, 0.f, 1.f, 0.f);  // cos, sin of the two values
+        if (turned && p.rope.interleaved) {
+          const float2 f = s_cs[warp][d0 / 2 + i];
+          cs = make_float4(f.x, -f.y, f.x, f.y);
+        } else if (turned) {
+          cs = *reinterpret_cast<const float4*>(&s_cs[warp][(low ? d0 : d0 - half) + 2 * i]);
+          if (low) cs.y = -cs.y, cs.w = -cs.w;
+        }
+        a[i] = make_float2(x.x * cs.x, x.y * cs.z);
+        b[i] = p.rope.interleaved ? make_float2(x.y * cs.y, x.x * cs.w) : make_float2(y.x * cs.y, y.y * cs.w);
       }
     }
     each_head<D>(rows, t, heads, share, p.split, [&](const uint4& raw) {
@@ -185,10 +205,10 @@ __global__ void __launch_bounds__(32 * kWarps) prepare_kernel(const __grid_const
       for (int i = 0; i < 4; ++i) x[i] = bf2_to_float2(r[i]);
       if (rot && !p.rope.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = bf2_to_float2(__shfl_sync(0xFFFFFFFFu, r[i], partner));
+        for (int i = 0; i < 4; ++i) y[i] = bf2_to_float2(__shfl_sync(0xFFFFFFFFu, r[i], partner) & paired);
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = make_float2(x[i].y, x[i].x);
+        for (int i = 0; i < 4; ++i) y[i] = turned ? make_float2(x[i].y, x[i].x) : make_float2(0.f, 0.f);
       }
       float rms = 1.f;
       if (w) {
@@ -202,9 +222,8 @@ __global__ void __launch_bounds__(32 * kWarps) prepare_kernel(const __grid_const
       uint32_t out[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        // without a rotation the paired value does not enter at all (it may be an infinity)
-        const float2 z = turned ? __ffma2_rn(x[i], a[i], __fmul2_rn(y[i], b[i])) : __fmul2_rn(x[i], a[i]);
-        out[i] = pack_bf2(z.x * rms, z.y * rms);  // the one rounding to bf16
+        const float2 z = __fmul2_rn(__ffma2_rn(x[i], a[i], __fmul2_rn(y[i], b[i])), make_float2(rms, rms));
+        out[i] = pack_bf2(z.x, z.y);  // the one rounding to bf16
       }
       return make_uint4(out[0], out[1], out[2], out[3]);
     }, store);
@@ -213,15 +232,7 @@ __global__ void __launch_bounds__(32 * kWarps) prepare_kernel(const __grid_const
     return [=, &p](int h, const uint4& v, bool in) {
       const long row = place + ((long)h << p.cache.page_shift);
       if constexpr (kE4M3) {
-        const uint32_t r[4] = {v.x, v.y, v.z, v.w};
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = bf2_to_float2(r[i]);
-          x[2 * i] = f.x;
-          x[2 * i + 1] = f.y;
-        }
-        store_e4m3<D>(x, static_cast<uint8_t*>(pages) + row * D, bytes + row, sub, in);
+        store_e4m3<D>(v, static_cast<uint8_t*>(pages) + row * D, bytes + row, sub, in);
       } else if (in) {
         *(reinterpret_cast<uint4*>(static_cast<uint16_t*>(pages) + row * D) + sub) = v;
       }
@@ -244,7 +255,8 @@ struct ReadParams {
   unsigned* err;
   uint16_t* k_out;
   uint16_t* v_out;
-  int Hkv, N, T, split;
+  int Hkv, N, T, tokens;  // tokens: of a warp, at most 32
+  bool wide;              // the outputs are 32-byte aligned
 };
 
 // 16 bytes of the cache a lane: 8 bf16 values copied, or 16 codes widened.  A warp's lanes hold a head's
@@ -253,45 +265,53 @@ template <int D, bool kE4M3>
 __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const __grid_constant__ ReadParams p) {
   constexpr int kVals = kE4M3 ? 16 : 8, kLanes = D / kVals, kAt = 32 / kLanes;  // rows at a time: 1, 2 or 4
   const int lane = threadIdx.x & 31, sub = lane % kLanes, mine = lane / kLanes;
-  const long item = (long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = (int)(item / p.split), share = (int)(item - (long)t * p.split);
-  if (t >= p.T) return;
-  int first, len;
-  bool bad = false;
+  // p.tokens tokens of a warp: their places are looked up side by side, a lane each
+  const long t0 = ((long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.tokens;
+  const int nt = (int)min((long)p.tokens, p.T - t0);
+  if (nt <= 0) return;
   long place = -1;
-  const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
-  if (seq >= 0) {
-    const long pos = (p.starts ? (long)__ldg(p.starts + seq) : 0L) + (t - first);
-    if (pos < 0 || pos >= min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) bad = true;
-    else place = cache_row(p.cache, p.Hkv, seq, (int)pos, bad);
-  } else if (seq == -2) {
-    bad = true;
+  if (lane < nt) {
+    const int t = (int)t0 + lane;
+    int first, len;
+    bool bad = false;
+    const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
+    if (seq >= 0) {
+      const long pos = (p.starts ? (long)__ldg(p.starts + seq) : 0L) + (t - first);
+      if (pos < 0 || pos >= min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) bad = true;
+      else place = cache_row(p.cache, p.Hkv, seq, (int)pos, bad);
+    } else if (seq == -2) {
+      bad = true;
+    }
+    if (bad) raise_error(p.err, kErrDeviceArgument);
   }
-  if (bad) raise_error(p.err, kErrDeviceArgument);
-  if (place < 0) return;
-  // row r of the token: head r / 2, its keys (even) or values (odd)
-  const bool keys0 = ((share * kAt + mine) & 1) == 0;
-  const int rows = 2 * p.Hkv, step = p.split * kAt;
-  for (int r0 = share * kAt; r0 < rows; r0 += step * kUnroll) {
+  // step s of the warp: rows (s % per) * kAt .. of token s / per; row r is head r / 2, its keys (even) or
+  // values (odd)
+  const int per = (2 * p.Hkv + kAt - 1) / kAt, steps = nt * per;
+  for (int s0 = 0, next = 0, tok_next = 0; s0 < steps; s0 += kUnroll) {
     uint4 raw[kUnroll];
     uint32_t byte[kUnroll];
+    uint16_t* dst[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * step + mine;
-      const bool is_k = kAt > 1 ? keys0 : (r & 1) == 0;
-      const long row = place + ((long)(r >> 1) << p.cache.page_shift);
-      if (r < rows) {
+      const int s = s0 + u, tok = tok_next, r = next * kAt + mine, h = r >> 1;
+      if (++next == per) {
+        next = 0;
+        ++tok_next;
+      }
+      const long at = __shfl_sync(0xFFFFFFFFu, place, tok & 31);
+      const bool is_k = (r & 1) == 0;
+      const long row = at + ((long)h << p.cache.page_shift);
+      dst[u] = nullptr;
+      if (s < steps && h < p.Hkv && at >= 0) {
         raw[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(is_k ? p.cache.k : p.cache.v) +
                                                        row * (D * (kE4M3 ? 1 : 2))) + sub);
         if constexpr (kE4M3) byte[u] = __ldg((is_k ? p.cache.k_scale : p.cache.v_scale) + row);
+        dst[u] = (is_k ? p.k_out : p.v_out) + ((t0 + tok) * p.Hkv + h) * D + sub * kVals;
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int r = r0 + u * step + mine;
-      if (r >= rows) continue;
-      const bool is_k = kAt > 1 ? keys0 : (r & 1) == 0;
-      uint16_t* dst = (is_k ? p.k_out : p.v_out) + ((long)t * p.Hkv + (r >> 1)) * D + sub * kVals;
+      if (!dst[u]) continue;
       if constexpr (kE4M3) {
         const float s = e8m0_value(byte[u]);
         const uint32_t c[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
@@ -300,13 +320,18 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const __grid_co
         for (int i = 0; i < 4; ++i) {
           const uint2 h = e4m3x4_to_half4(c[i]);
           const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
-          o[2 * i] = pack_bf2(a.x * s, a.y * s);
-          o[2 * i + 1] = pack_bf2(b.x * s, b.y * s);
+          const float2 x = __fmul2_rn(a, make_float2(s, s)), y = __fmul2_rn(b, make_float2(s, s));
+          o[2 * i] = pack_bf2(x.x, x.y);
+          o[2 * i + 1] = pack_bf2(y.x, y.y);
         }
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        if (p.wide) {
+          st_global32(dst[u], o);
+        } else {
+          reinterpret_cast<uint4*>(dst[u])[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<uint4*>(dst[u])[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
       } else {
-        *reinterpret_cast<uint4*>(dst) = raw[u];
+        *reinterpret_cast<uint4*>(dst[u]) = raw[u];
       }
     }
   }
@@ -342,9 +367,13 @@ cudaError_t launch_attn_cache_read(const LaunchEnv& env, int Hkv, int D, const P
   int sms = 0;
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const int split = warps_of_token(T, sms, (2 * Hkv * D * (cache.e4m3 ? 1 : 2) + 511) / 512);
-  const ReadParams p = {cache, starts, cu, env.err, k_out, v_out, Hkv, N, T, split};
-  const unsigned grid = (unsigned)(((long)T * split + kWarps - 1) / kWarps);
+  // eight loads a lane, or fewer tokens where that leaves SMs without sixteen warps
+  const int per = (2 * Hkv * D * (cache.e4m3 ? 1 : 2) + 511) / 512;
+  int tokens = per >= 8 ? 1 : 8 / per;
+  while (tokens > 1 && (long)T < 16L * sms * tokens) tokens /= 2;
+  const bool wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0;
+  const ReadParams p = {cache, starts, cu, env.err, k_out, v_out, Hkv, N, T, tokens, wide};
+  const unsigned grid = (unsigned)(((long)T + (long)tokens * kWarps - 1) / ((long)tokens * kWarps));
   auto kern = D == 128 ? (cache.e4m3 ? cache_read_kernel<128, true> : cache_read_kernel<128, false>)
                        : (cache.e4m3 ? cache_read_kernel<256, true> : cache_read_kernel<256, false>);
   kern<<<grid, 32 * kWarps, 0, env.stream>>>(p);
