@@ -68,7 +68,10 @@ struct Cfg {
   // short code for the instruction cache that warps of several kinds share: 32 beat 128 by 2 % at D = 256
   // and by a third for e4m3; two tiles were best with 64 (894 TFLOP/s, 875 with 32 or 128).
   static constexpr int kCols = kTiles == 2 && !kE4M3 ? 64 : 32;
-  static constexpr uint32_t kColO = 256;  // tensor memory: two S slots of 128 columns, then O
+  // Keys whose scores a slot holds: a block's, or with two tiles half of them.  A tile has two slots, so that
+  // its next scores are there when the weights of these are done.
+  static constexpr int kKeys = kTiles == 2 ? 64 : 128, kHalves = 128 / kKeys;
+  static constexpr uint32_t kColO = 256;  // tensor memory: the slots, 256 columns, then O
 };
 
 struct Bars {
@@ -188,22 +191,24 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   const int step = kTiles * p.sub;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 54);
-  WalkStart* start = reinterpret_cast<WalkStart*>(bars + 56);
-  long* scan = reinterpret_cast<long*>(bars + 62);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 59);
+  WalkStart* start = reinterpret_cast<WalkStart*>(bars + 60);
+  long* scan = reinterpret_cast<long*>(bars + 66);
   const uint32_t b0 = smem_u32(bars);
-  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 20, b0 + 8 * 22, b0 + 8 * 24, b0 + 8 * 26, b0 + 8 * 28, b0 + 8 * 29, b0 + 8 * 37, b0 + 8 * 45,
-                    b0 + 8 * 47, b0 + 8 * 50};
+  const Bars bar = {b0, b0 + 8 * 6, b0 + 8 * 12, b0 + 8 * 18, b0 + 8 * 22, b0 + 8 * 26, b0 + 8 * 30, b0 + 8 * 32, b0 + 8 * 34, b0 + 8 * 35, b0 + 8 * 43, b0 + 8 * 51,
+                    b0 + 8 * 53, b0 + 8 * 56};
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar.full + 8 * i, kE4M3 ? 4 : 1);
       mbar_init(bar.empty + 8 * i, kTiles);
       mbar_init(bar.tail + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * kTiles; ++i) {
       mbar_init(bar.s_full + 8 * i, 1);
       mbar_init(bar.p_full + 8 * i, 4);
       mbar_init(bar.o_full + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar.q_full + 8 * i, 1);
       mbar_init(bar.q_ready + 8 * i, 4);
       mbar_init(bar.q_empty + 8 * i, 1);
@@ -267,14 +272,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     const uint32_t t_o = tmem + lanes + C::kColO + sub * D;
     const int g = row % p.G, tok_in = row / p.G;
     uint8_t* sq = sm + sub * 128 * D * 2;
-    // blocks of this tile so far (slot and parity go by it), its products with V, blocks of the CTA; segments with rows
+    // steps of this tile so far (slot and parity go by it), its products with V, blocks of the CTA; segments with rows
     uint32_t n_blk = 0, n_pv = 0, all_blk = 0, n_seg = 0;
-    // The product of block b.  With one tile the next block's scores may be here before the product of
-    // the block before them has ended: one barrier for even and one for odd blocks, so that no wait is
-    // for a phase that could lie two behind.
-    auto await_pv = [&](uint32_t b) {
-      return kTiles == 2 ? await(bar.o_full + 8 * sub, b & 1u) : await(bar.o_full + 8 * (b & 1u), (b >> 1) & 1u);
-    };
+    // Step b's slot, its barriers' parity, and its product with V.  A slot has barriers of its own: the next
+    // scores may be here before the product of the step before them has ended, and no wait is for a phase that
+    // could lie two behind.
+    auto slot_of = [&](uint32_t b) { return 2 * sub + (b & 1u); };
+    auto await_pv = [&](uint32_t b) { return await(bar.o_full + 8 * slot_of(b), (b >> 1) & 1u); };
     while (ok && walk.next(p, step, seg)) {
       const int hk = seg.hk, ntok = min(p.sub, seg.ntok - sub * p.sub);  // tokens of this tile
       const int row0 = seg.row0 + sub * p.sub, rows = max(ntok, 0) * p.G;
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       float m = -INFINITY, l = 0.f, r = -INFINITY;
       const int last = seg.pos0 + sub * p.sub + tok_in;  // the row's position: its last visible key
       const bool busy = w4 * 32 < rows;                   // this warp has rows at all
-      constexpr int kCols = C::kCols;
+      constexpr int kCols = C::kCols, kKeys = C::kKeys, kHalves = C::kHalves;
       const uint32_t seg_blk = all_blk;
       all_blk += seg.j1 - seg.j0;
       if (kE4M3 && rows <= 0) {  // this tile has no rows in the segment: its warps still let its blocks go
@@ -338,15 +342,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         }
       }
       if (rows > 0) {
-        uint32_t blk = seg_blk;
-        for (int j = seg.j0; j < seg.j1; ++j, ++n_blk, ++blk) {
-          const uint32_t slot = kTiles == 2 ? sub : n_blk & 1u, par = kTiles == 2 ? n_blk & 1u : (n_blk >> 1) & 1u;
-          if (!await(bar.s_full + 8 * slot, par)) break;
+        const int i0 = seg.j0 * kHalves, i1 = seg.j1 * kHalves;  // steps of kKeys keys
+        for (int i = i0; i < i1; ++i, ++n_blk) {
+          const uint32_t slot = slot_of(n_blk), blk = seg_blk + (uint32_t)(i - i0) / kHalves;
+          if (!await(bar.s_full + 8 * slot, (n_blk >> 1) & 1u)) break;
           tc_fence_after();
           if (busy) {
-            const uint32_t t_s = tmem + lanes + slot * 128;
-            const int lim = last + 1 - j * kBlock;  // columns from here on are not visible
-            const bool masked = __any_sync(0xFFFFFFFFu, lim < kBlock);
+            const uint32_t t_s = tmem + lanes + slot * kKeys;
+            const int lim = last + 1 - i * kKeys;  // columns from here on are not visible
+            const bool masked = __any_sync(0xFFFFFFFFu, lim < kKeys);
             float ev = 0.f, unit = row_unit;  // log2 of the block's value scale; log2 units of this row's scores
             const BlockMeta* meta = reinterpret_cast<const BlockMeta*>(sm + C::kOffMeta) + blk % kMeta;
             if constexpr (kE4M3) {
@@ -356,15 +360,15 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             }
             float s[kCols], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-            for (int c0 = 0; c0 < kBlock; c0 += kCols) {
+            for (int c0 = 0; c0 < kKeys; c0 += kCols) {
               load_scores<kCols>(t_s + c0, s);
               if (masked) {
 #pragma unroll
-                for (int i = 0; i < kCols; ++i)
-                  if (c0 + i >= lim) s[i] = -INFINITY;
+                for (int k = 0; k < kCols; ++k)
+                  if (c0 + k >= lim) s[k] = -INFINITY;
               }
 #pragma unroll
-              for (int i = 0; i < kCols; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+              for (int k = 0; k < kCols; ++k) mx[k & 3] = fmaxf(mx[k & 3], s[k]);
             }
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * unit;
             if (top > m + kLazy) {
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             if (__any_sync(0xFFFFFFFFu, raise)) {
               const float a = raise ? ex2_approx(r - e) : 1.f;
               if (raise) r = e;
-              if (j > seg.j0) {  // O holds the blocks before this one: wait for their product, then scale
+              if (i > i0) {  // O holds the steps before this one: wait for their product, then scale
                 if (!await_pv(n_pv - 1)) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -396,13 +400,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             const float off = (kE4M3 ? kWeight : 0.f) + (m == -INFINITY ? 0.f : d - m);
             float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-            for (int c0 = 0; c0 < kBlock; c0 += kCols) {
-              if (kCols < kBlock) {  // again: the weights go over scores that have been read
+            for (int c0 = 0; c0 < kKeys; c0 += kCols) {
+              if (kCols < kKeys) {  // again: the weights go over scores that have been read
                 load_scores<kCols>(t_s + c0, s);
                 if (masked) {
 #pragma unroll
-                  for (int i = 0; i < kCols; ++i)
-                    if (c0 + i >= lim) s[i] = -INFINITY;
+                  for (int k = 0; k < kCols; ++k)
+                    if (c0 + k >= lim) s[k] = -INFINITY;
                 }
               }
 #pragma unroll
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           }
           if constexpr (kE4M3) {
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar.meta_empty + 8 * (blk % kMeta));
+            if (lane == 0 && (i + 1) % kHalves == 0) mbar_arrive(bar.meta_empty + 8 * (blk % kMeta));
           }
           tc_fence_before();
           __syncwarp();
@@ -598,25 +602,25 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     if (lane == 0) {
       // e4m3: both operands are binary16 (the format fields of the descriptor are zero)
       constexpr uint32_t kF16 = kE4M3 ? ~((1u << 7) | (1u << 10)) : ~0u;
-      constexpr uint32_t kIdQK = idesc_bf16_f32(128, 128) & kF16, kIdPV = idesc_bf16_f32_bmn(128, D) & kF16;
+      constexpr uint32_t kIdQK = idesc_bf16_f32(128, C::kKeys) & kF16, kIdPV = idesc_bf16_f32_bmn(128, D) & kF16;
       constexpr uint32_t kVBlock = D == 256 ? 8192 : 16384;  // bytes between 64-value blocks of a value stage
       const int which = warp - C::kMma0;
       Ring<kStages> ring;
       uint32_t q_par = 0, n_blk = 0;
-      // a stage's share of the scores, and of O
-      auto qk = [&](int sub, uint32_t slot, int part) {
-        const uint32_t q = sb + sub * 128 * D * 2, k = sb + C::kOffStage + ring.i * kStage;
+      // a stage's share of the scores, and of O: of a block, or of its `half`
+      auto qk = [&](int sub, uint32_t slot, int part, int half, const Ring<kStages>& at) {
+        const uint32_t q = sb + sub * 128 * D * 2, k = sb + C::kOffStage + at.i * kStage + half * 8192;
 #pragma unroll
         for (int d = 0; d < 2; ++d)
-          mma_bf16_k4<2, 2>(tmem + slot * 128, sw128_desc(q + (2 * part + d) * 16384), sw128_desc(k + d * 16384), kIdQK,
+          mma_bf16_k4<2, 2>(tmem + slot * C::kKeys, sw128_desc(q + (2 * part + d) * 16384), sw128_desc(k + d * 16384), kIdQK,
                             part + d > 0);
       };
-      auto pv = [&](int sub, uint32_t slot, int part, bool acc) {
-        const uint32_t v = sb + C::kOffStage + ring.i * kStage;
-        constexpr int kSteps = 2 / kParts;  // 64 keys each
+      auto pv = [&](int sub, uint32_t slot, int part, int half, const Ring<kStages>& at, bool acc) {
+        const uint32_t v = sb + C::kOffStage + at.i * kStage + half * 8192;
+        constexpr int kSteps = C::kKeys / kParts / 64;  // 64 keys each
 #pragma unroll
         for (int d = 0; d < kSteps; ++d)
-          mma_bf16_k4_ta<128>(tmem + C::kColO + sub * D, tmem + slot * 128 + (part * kSteps + d) * 32,
+          mma_bf16_k4_ta<128>(tmem + C::kColO + sub * D, tmem + slot * C::kKeys + (part * kSteps + d) * 32,
                               sw128_mn_desc(v + d * 8192, kVBlock), kIdPV, acc || d > 0);
       };
       while (ok && walk.next(p, step, seg)) {
@@ -631,33 +635,40 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           }
           const int last = seg.j1 - 1;
           for (int j = seg.j0 - 1; j <= last && ok; ++j) {
-            if (j >= seg.j0) {
-              if (mine && !await_one(bar.p_full + 8 * t, n_blk & 1u)) break;
-              ++n_blk;
-              if (!await_one(bar.full + 8 * ring.i, ring.pass)) break;
-              if (mine) {
-                tc_fence_after();
-                pv(t, t, 0, j > seg.j0);
-                mma_commit(bar.o_full + 8 * t);
-                mma_commit(bar.empty + 8 * ring.i);
-              } else {
-                mbar_arrive(bar.empty + 8 * ring.i);
+            // The values of block j and the keys of the one after it, by halves: a half's weights go into O,
+            // and the scores two halves on take their slot.
+            Ring<kStages> values = ring;
+            if (j >= seg.j0) ring.step();
+            const Ring<kStages> keys = ring;
+            if (j < last) ring.step();
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t slot = 2 * t + half;
+              if (j >= seg.j0) {
+                if (mine && !await_one(bar.p_full + 8 * slot, n_blk & 1u)) break;
+                if (half == 0 && !await_one(bar.full + 8 * values.i, values.pass)) break;
+                if (mine) {
+                  tc_fence_after();
+                  pv(t, slot, 0, half, values, j > seg.j0 || half > 0);
+                  mma_commit(bar.o_full + 8 * slot);
+                  if (half) mma_commit(bar.empty + 8 * values.i);
+                } else if (half) {
+                  mbar_arrive(bar.empty + 8 * values.i);
+                }
               }
-              ring.step();
-            }
-            if (j < last) {
-              if (!await_one(bar.full + 8 * ring.i, ring.pass)) break;
-              if (mine) {
-                tc_fence_after();
-                qk(t, t, 0);
-                mma_commit(bar.s_full + 8 * t);
-                mma_commit(bar.empty + 8 * ring.i);
-                if (j + 1 == last) mma_commit(bar.q_empty + 8 * t);
-              } else {
-                mbar_arrive(bar.empty + 8 * ring.i);
+              if (j < last) {
+                if (half == 0 && !await_one(bar.full + 8 * keys.i, keys.pass)) break;
+                if (mine) {
+                  tc_fence_after();
+                  qk(t, slot, 0, half, keys);
+                  mma_commit(bar.s_full + 8 * slot);
+                  if (half) mma_commit(bar.empty + 8 * keys.i);
+                  if (half && j + 1 == last) mma_commit(bar.q_empty + 8 * t);
+                } else if (half) {
+                  mbar_arrive(bar.empty + 8 * keys.i);
+                }
               }
-              ring.step();
             }
+            n_blk += j >= seg.j0;
           }
           if (!mine) n_blk -= seg.j1 - seg.j0;
         } else {
@@ -673,7 +684,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
               for (int part = 0; part < kParts; ++part) {
                 if (!await_one(bar.full + 8 * ring.i, ring.pass)) break;
                 tc_fence_after();
-                qk(0, slot, part);
+                qk(0, slot, part, 0, ring);
                 mma_commit(bar.empty + 8 * ring.i);
                 ring.step();
               }
@@ -690,7 +701,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
               for (int part = 0; part < kParts; ++part) {
                 if (!await_one(bar.full + 8 * ring.i, ring.pass)) break;
                 tc_fence_after();
-                pv(0, slot, part, i > 0 || part > 0);
+                pv(0, slot, part, 0, ring, i > 0 || part > 0);
                 mma_commit(bar.empty + 8 * ring.i);
                 ring.step();
               }
