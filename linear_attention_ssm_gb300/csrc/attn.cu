@@ -57,8 +57,7 @@ struct Cfg {
   static constexpr uint32_t kOffStage = kQ;
   static constexpr uint32_t kOffRaw = kOffStage + kStages * kStage;
   static constexpr uint32_t kOffMeta = kOffRaw + kRawStages * kRaw;
-  static constexpr uint32_t kOffQs = kOffMeta + (kE4M3 ? kMeta * sizeof(BlockMeta) : 0);
-  static constexpr uint32_t kOffBar = kOffQs + (kE4M3 ? kTiles * 512 : 0);
+  static constexpr uint32_t kOffBar = kOffMeta + (kE4M3 ? kMeta * sizeof(BlockMeta) : 0);
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;  // barriers; alignment of the base
   static_assert(kSmem <= 232448, "shared memory");
   // of the four warps behind the softmax's: the products (two), Q, K and V by TMA, value rows behind the
@@ -291,43 +290,46 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       }
       float row_unit = p.scale_log2;  // e4m3: the power of two the row was divided by
       if (kE4M3 && rows > 0) {
-        // Q becomes binary16 where it lies, each warp its own rows, a row divided by the power of two of its
-        // largest value
+        // Q becomes binary16 where it lies, each thread its own row, divided by the power of two of its largest
+        // finite value (a thread's pieces of 16 bytes lie in other banks than its neighbours')
         if (!await(bar.q_full + 8 * sub, n_seg++ & 1u)) break;
-        constexpr int kPer = D / 8, kRowsAt = 32 / kPer;  // 16-byte pieces of a row, rows of a warp at a time
-        const int piece = lane % kPer;
-        float* qs = reinterpret_cast<float*>(sm + C::kOffQs) + sub * 128;
         if (w4 * 32 < rows) {
+          auto at = [&](int c) { return reinterpret_cast<uint4*>(sq + sw128_offset(row, c * 8, 16384)); };
+          uint32_t two = 0;  // of the even and of the odd values
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = *at(c);
+            two = __vmaxu2(two, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+          }
+          uint32_t top = max(two & 0xFFFFu, two >> 16);
+          if (top >= 0x7F80u) {  // an infinity or NaN among them
+            top = 0;
 #pragma unroll 1
-          for (int i0 = 0; i0 < 32; i0 += 4 * kRowsAt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int rr = w4 * 32 + i0 + i * kRowsAt + lane / kPer;
-              uint4* at = reinterpret_cast<uint4*>(sq + sw128_offset(rr, piece * 8, 16384));
-              const uint4 x = *at;
-              uint32_t y[4] = {x.x, x.y, x.z, x.w}, top = 0;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t lo = y[k] << 16 & 0x7FFFFFFFu, hi = y[k] & 0x7FFF0000u;
-                top = max(top, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
-              }
-#pragma unroll
-              for (int w = kPer / 2; w > 0; w >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
-              const int e = min(max((int)(top >> 23) - 127, -120), 126);
-              const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                y[k] = pack_half2(__uint_as_float(y[k] << 16) * inv, __uint_as_float(y[k] & 0xFFFF0000u) * inv);
-              if (piece == 0) qs[rr] = __uint_as_float((uint32_t)(127 + e) << 23);
-              *at = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int c = 0; c < D; ++c) {
+              const uint32_t x = reinterpret_cast<const uint16_t*>(at(c >> 3))[c & 7] & 0x7FFFu;
+              if (x < 0x7F80u) top = max(top, x);
             }
           }
-          __syncwarp();
-          row_unit = qs[row];
+          const int e = min(max((int)(top >> 7) - 127, -120), 126);
+          const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 x = *at(c);
+            uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              y[k] = pack_half2(__uint_as_float(y[k] << 16) * inv, __uint_as_float(y[k] & 0xFFFF0000u) * inv);
+            *at(c) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+          row_unit = __uint_as_float((uint32_t)(127 + e) << 23);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar.q_ready + 8 * sub);
+      }
+      if (p.z.p && mine && seg.j0 == 0 && seg.j1 == seg.nb) {  // the gate on its way to L2
+        const uint16_t* z = p.z.p + (long)(row0 + tok_in) * p.z.token + (long)(hk * p.G + g) * p.z.head;
+        for (int c = 0; c < D; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(z + c));
       }
       float m = -INFINITY, l = 0.f, r = -INFINITY;
       const int last = seg.pos0 + sub * p.sub + tok_in;  // the row's position: its last visible key
@@ -573,16 +575,20 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       const uint8_t* from = sm + C::kOffRaw + raw.i * kRaw + (wide ? blk_wide * 4096 : blk_narrow * 8192) + piece * 16;
       uint8_t* to = sm + C::kOffStage + ring.i * kStage + (wide ? to_wide : to_narrow);
       const int other = wide ? other_wide : other_narrow;
-#pragma unroll 4
-      for (int u = 0; u < kUnits; ++u) {
-        const int row = row0 + u * stride;
-        uint4 x = make_uint4(0, 0, 0, 0);  // (a part without any visible key)
-        if (last >= 0) x = *reinterpret_cast<const uint4*>(from + min(row, last) * 64);
-        const uint32_t f = scale[base + row];
+      auto widen = [&](int u, const uint4& x) {
+        const uint32_t f = scale[base + row0 + u * stride];
         const uint2 a = e4m3x4_to_half4(x.x), b = e4m3x4_to_half4(x.y), c = e4m3x4_to_half4(x.z), e = e4m3x4_to_half4(x.w);
         uint8_t* at = to + u * stride * 128;
         *reinterpret_cast<uint4*>(at) = make_uint4(mul_half2(a.x, f), mul_half2(a.y, f), mul_half2(b.x, f), mul_half2(b.y, f));
         *reinterpret_cast<uint4*>(at + other) = make_uint4(mul_half2(c.x, f), mul_half2(c.y, f), mul_half2(e.x, f), mul_half2(e.y, f));
+      };
+      if (last >= 127 - base) {
+#pragma unroll 2
+        for (int u = 0; u < kUnits; ++u) widen(u, *reinterpret_cast<const uint4*>(from + (row0 + u * stride) * 64));
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < kUnits; ++u)  // (zero: a part without any visible key)
+          widen(u, last >= 0 ? *reinterpret_cast<const uint4*>(from + min(row0 + u * stride, last) * 64) : make_uint4(0, 0, 0, 0));
       }
       fence_proxy_async_smem();
       __syncwarp();
