@@ -594,7 +594,8 @@ GDN_API gdn_status gdn_attn_rope_frequencies(int32_t rot_dim, const gdn_rope_sca
  *   q_norm_w, k_norm_w  [D] bf16, or NULL for no norm
  *   rope       NULL or rot_dim 0: no rotation.  Angles are formed to about 2^-23 turns at positions below
  *              2^24 (2^-18 at any) without fp64 arithmetic in the token loop
- *   q_out      [total_tokens, Hq, D] bf16; may be q itself where q has that layout
+ *   q_out      [total_tokens, Hq, D] bf16; may be q itself where q has that layout, and overlaps nothing
+ *              else that the call reads
  */
 GDN_API gdn_status gdn_attn_prepare(const gdn_attn_geometry* geo, const gdn_bf16* q, int64_t q_token_stride,
                                     int64_t q_head_stride, const gdn_bf16* k, int64_t k_token_stride,
@@ -625,7 +626,7 @@ GDN_API size_t gdn_attn_workspace_size(const gdn_attn_geometry* geo);
  * Causal attention of the new tokens of packed sequences over their caches (which hold the new tokens
  * too: gdn_attn_prepare first).  With p the token's position and j = 0 .. p:
  *   s_j = softmax_scale * q . k_j,   o = sum_j e^(s_j) v_j / sum_j e^(s_j)   (0 when p < 0),
- *   out = o, or o * sigmoid(z) where z is given.
+ *   out = o, or o * sigmoid(z) where z is given; softmax_scale is positive, at most 1e38.
  * Scores and sums are fp32 with a running maximum; the weights e^(s_j - max) are rounded to bf16
  * for the product with v.  An e4m3 cache is read as binary16, exactly; the queries (divided by a power of
  * two) and the weights (times the power of two of v_j) are rounded to binary16 with it.

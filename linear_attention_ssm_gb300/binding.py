@@ -859,6 +859,16 @@ def _batch_args(block_table, per_seq, name, cu_seqlens, T, device):
             _flat(per_seq, torch.int32, name, (N,), device), cu, pages)
 
 
+def _empty(shape, dtype, device, stream):
+    """New memory for a call on `stream` (None: the current one), of that stream's part of the allocator."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -910,7 +920,7 @@ def gdn_attn_prepare(q, k, v, cache: KVCache, block_table, kv_lens, cu_seqlens=N
         _, hq = _rows_of(q, "q")
         qp = _heads(q, "q", T, hq, D, dev)
         if q_out is None:
-            q_out = torch.empty((T, hq, D), dtype=torch.bfloat16, device=dev)
+            q_out = _empty((T, hq, D), torch.bfloat16, dev, stream)
         op = _flat(q_out, torch.bfloat16, "q_out", (T, hq, D), dev)
     else:
         q_out = None
@@ -949,11 +959,11 @@ def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out
     N, table, lens, cu, pages = _batch_args(block_table, kv_lens, "kv_lens", cu_seqlens, T, dev)
     zp = (None, 0, 0) if z is None else _heads(z, "z", T, hq, D, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty((T, hq, D), torch.bfloat16, dev, stream)
     op = _flat(out, torch.bfloat16, "out", (T, hq, D), dev)
     geo = _attn_geo(hq, hkv, D)
     if workspace is None:
-        workspace = torch.empty(lib.gdn_attn_workspace_size(geo), dtype=torch.uint8, device=dev)
+        workspace = _empty(lib.gdn_attn_workspace_size(geo), torch.uint8, dev, stream)
     elif workspace.device != dev:
         raise ValueError(f"workspace is on {workspace.device}, the call is on {dev}")
     tail = (softmax_scale, *zp, op, workspace.data_ptr(), workspace.numel() * workspace.element_size())

@@ -783,6 +783,14 @@ gdn_status check_head_rows(const gdn_bf16* p, int64_t token, int64_t head, const
   return GDN_OK;
 }
 
+// Whether any of the heads' rows lies in the memory range [out, out + bytes).
+bool rows_overlap(const gdn_bf16* p, int64_t token, int64_t head, int64_t tokens, int64_t heads, int64_t dim,
+                  const void* out, size_t bytes) {
+  const int64_t t = (tokens - 1) * token, h = (heads - 1) * head;
+  const int64_t lo = (t < 0 ? t : 0) + (h < 0 ? h : 0), hi = (t > 0 ? t : 0) + (h > 0 ? h : 0) + dim;
+  return overlaps(p + lo, (size_t)(hi - lo) * 2, out, bytes);
+}
+
 gdn_status attention(const gdn_attn_geometry* geo, const gdn_bf16* q, const gdn_kv_cache* cache,
                      const int32_t* block_table, int32_t max_pages, const int32_t* kv_lens,
                      const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens, float softmax_scale,
@@ -799,10 +807,12 @@ gdn_status attention(const gdn_attn_geometry* geo, const gdn_bf16* q, const gdn_
   GDN_REQUIRE(q, "q");
   GDN_REQUIRE(out, "out");
   if (z && (s = check_head_rows(z, z_token_stride, z_head_stride, "z")) != GDN_OK) return s;
-  if (!(softmax_scale > 0.f) || softmax_scale > 3.4e38f)
-    return fail(GDN_ERR_INVALID_ARGUMENT, "softmax_scale must be positive and finite");
+  if (!(softmax_scale > 0.f) || softmax_scale > 1e38f)  // times log2(e) it is finite too
+    return fail(GDN_ERR_INVALID_ARGUMENT, "softmax_scale must be positive and at most 1e38");
   const size_t bytes = (size_t)total_tokens * geo->num_q_heads * geo->head_dim * 2;
   if (overlaps(q, bytes, out, bytes)) return fail(GDN_ERR_INVALID_ARGUMENT, "out overlaps q");
+  if (z && rows_overlap(z, z_token_stride, z_head_stride, total_tokens, geo->num_q_heads, geo->head_dim, out, bytes))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "out overlaps z");
   if ((int64_t)c.num_pages * geo->num_kv_heads * cache->page_size > 0x7FFFFFFFL)
     return fail(GDN_ERR_INVALID_ARGUMENT, "the pool has more than 2^31 rows");
   const size_t need = gdn::attn_workspace_bytes(geo->head_dim);
@@ -868,20 +878,21 @@ gdn_status gdn_attn_prepare(const gdn_attn_geometry* geo, const gdn_bf16* q, int
   gdn::PagedCache c;
   if ((s = check_paged_cache(cache, block_table, max_pages, &c)) != GDN_OK) return s;
   const int D = geo->head_dim;
+  const size_t out_bytes = (size_t)total_tokens * geo->num_q_heads * D * 2;
   if (q) {
     if ((s = check_head_rows(q, q_token_stride, q_head_stride, "q")) != GDN_OK) return s;
     GDN_REQUIRE(q_out, "q_out");
     // Each row is read whole before it is written, by the same lanes: q_out may be q itself, but rows
     // at other places would be overwritten before they are read.
     const bool same = q == q_out && q_head_stride == D && q_token_stride == (int64_t)D * geo->num_q_heads;
-    if (!same && q_token_stride >= 0 && q_head_stride >= 0) {
-      const size_t span = ((size_t)(total_tokens - 1) * q_token_stride + (size_t)(geo->num_q_heads - 1) * q_head_stride + D) * 2;
-      if (overlaps(q, span, q_out, (size_t)total_tokens * geo->num_q_heads * D * 2))
-        return fail(GDN_ERR_INVALID_ARGUMENT, "q_out overlaps q without being it");
-    }
+    if (!same && rows_overlap(q, q_token_stride, q_head_stride, total_tokens, geo->num_q_heads, D, q_out, out_bytes))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "q_out overlaps q without being it");
   }
   if ((s = check_head_rows(k, k_token_stride, k_head_stride, "k")) != GDN_OK) return s;
   if ((s = check_head_rows(v, v_token_stride, v_head_stride, "v")) != GDN_OK) return s;
+  if (q && (rows_overlap(k, k_token_stride, k_head_stride, total_tokens, geo->num_kv_heads, D, q_out, out_bytes) ||
+            rows_overlap(v, v_token_stride, v_head_stride, total_tokens, geo->num_kv_heads, D, q_out, out_bytes)))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "q_out overlaps k or v");
   GDN_OPTIONAL(q_norm_w, "q_norm_w");
   GDN_OPTIONAL(k_norm_w, "k_norm_w");
   if (!(rms_eps >= 0.f)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be >= 0");

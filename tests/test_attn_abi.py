@@ -142,3 +142,14 @@ def test_reference_quantiser_is_the_nearest_code():
     top = x.abs().amax(-1)
     assert bool((top <= 448 * two).all()) and bool(((top > 224 * two) | (byte == 10)).all())
     assert torch.equal(codes, (x / two[:, None]).float().to(torch.float8_e4m3fn).double())
+
+
+def test_outputs_that_overlap_what_is_read(lib):
+    def at(x):
+        return ctypes.c_void_p(x)
+    assert attend(lib, z=OTHER) == 1                                   # out is z
+    assert attend(lib, z=at(0x4000000 - 512), zs=(4096, 256)) == 1     # z's last rows reach into out
+    assert attend(lib, z=at(0x4000000 + 6 * 8192), zs=(-4096, 256)) == 1  # and its first ones, from behind
+    assert attend(lib, scale=2e38) == 1 and attend(lib, scale=float("inf")) == 1 and attend(lib, scale=float("nan")) == 1
+    assert prepare(lib, k=at(0x4000000 + 512)) == 1 and prepare(lib, v=OTHER) == 1
+    assert prepare(lib, k=at(0x4000000 - 52208)) == 1  # k spans (5 * 5120 + 256 + 256) * 2 = 52224 bytes
