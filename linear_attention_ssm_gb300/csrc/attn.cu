@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             // lest a block of tiny values vanish from l (P is zero in binary16 long before)
             const float d = kE4M3 && m > -INFINITY ? fmaxf(e - r, -40.f) : 0.f;
             const float off = (kE4M3 ? kWeight : 0.f) + (m == -INFINITY ? 0.f : d - m);
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 unit2 = make_float2(unit, unit), off2 = make_float2(off, off);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
             for (int c0 = 0; c0 < kKeys; c0 += kCols) {
               if (kCols < kKeys) {  // again: the weights go over scores that have been read
@@ -416,20 +417,20 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
                 float w[16];
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                  float x[4];
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    x[k] = ex2_approx(fmaf(s[32 * h + 2 * i + k], unit, off));
-                    sum[k] += x[k];
+                  for (int k = 0; k < 2; ++k) {
+                    const int at = 32 * h + 2 * (i + k);
+                    float2 x = __ffma2_rn(make_float2(s[at], s[at + 1]), unit2, off2);
+                    x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                    sum[k] = __fadd2_rn(sum[k], x);
+                    w[i + k] = __uint_as_float(kE4M3 ? pack_half2(x.x, x.y) : pack_bf2(x.x, x.y));
                   }
-                  w[i] = __uint_as_float(kE4M3 ? pack_half2(x[0], x[1]) : pack_bf2(x[0], x[1]));
-                  w[i + 1] = __uint_as_float(kE4M3 ? pack_half2(x[2], x[3]) : pack_bf2(x[2], x[3]));
                 }
                 tmem_st16_begin(t_s + c0 / 2 + 16 * h, w);
               }
             }
             tmem_st_wait();
-            const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             l += kE4M3 ? all * ex2_approx(-d - kWeight) : all;
           }
           if constexpr (kE4M3) {
@@ -464,24 +465,38 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           for (int c = 0; c < D; c += 32) {
             float o[32];
             tmem_ld32(t_o + c, o);
-            if constexpr (kE4M3) {
+            // two at a time: by both halves of the unit, the second with 1 / l in a tile that is whole
+            auto times = [&](float f) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = o[i] * unit_o * unit_o;
-            }
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = __fmul2_rn(make_float2(o[i], o[i + 1]), make_float2(f, f));
+                o[i] = y.x;
+                o[i + 1] = y.y;
+              }
+            };
+            if constexpr (kE4M3) times(unit_o);
             if (!whole) {
+              if constexpr (kE4M3) times(unit_o);
 #pragma unroll
               for (int i = 0; i < 8; ++i) dst[(c / 4 + i) * 128] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             } else {
+              times(kE4M3 ? unit_o * inv : inv);
+              if (__any_sync(0xFFFFFFFFu, l == 0.f)) {  // no visible key: zero
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;  // no visible key: zero
+                for (int i = 0; i < 32; ++i) o[i] = l == 0.f ? 0.f : o[i];
+              }
               if (p.z.p) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const uint32_t zr[4] = {zz[k].x, zz[k].y, zz[k].z, zz[k].w};
 #pragma unroll
                   for (int x = 0; x < 4; ++x) {
-                    o[8 * k + 2 * x] *= sigmoid_fast(__uint_as_float(zr[x] << 16));
-                    o[8 * k + 2 * x + 1] *= sigmoid_fast(__uint_as_float(zr[x] & 0xFFFF0000u));
+                    float2 e = __fmul2_rn(make_float2(__uint_as_float(zr[x] << 16), __uint_as_float(zr[x] & 0xFFFF0000u)),
+                                          make_float2(-kLog2e, -kLog2e));
+                    e = __fadd2_rn(make_float2(ex2_approx(e.x), ex2_approx(e.y)), make_float2(1.f, 1.f));
+                    const float2 y = __fmul2_rn(make_float2(o[8 * k + 2 * x], o[8 * k + 2 * x + 1]), make_float2(rcp_approx(e.x), rcp_approx(e.y)));
+                    o[8 * k + 2 * x] = y.x;
+                    o[8 * k + 2 * x + 1] = y.y;
                   }
                 }
                 if (c + 32 < D) gate(c + 32);
