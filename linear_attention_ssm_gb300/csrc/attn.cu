@@ -926,23 +926,26 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
 // Joins the parts of cut tiles: out = sum_c O_c 2^(m_c - m) / sum_c l_c 2^(m_c - m), c over the tile's
 // parts, always in the same order.  The CTAs of the tile's first part do it; blockIdx.y takes a share of
 // rows and columns, and where a tile has many parts the warps of a CTA share those.  The parts are listed
-// first and loaded four at a time, so that their loads do not wait for one another.
-//   kTiles 1, 2: parts [tile][D / 4][128 rows], lanes are rows;  kTiles 0: parts [row][D], lanes are columns
+// first and several are loaded at a time, so that their loads do not wait for one another.
+//   kTiles 1, 2: parts [tile][D / 4][128 rows], a lane has 16 columns of a row, a sector of the output;
+//   kTiles 0: parts [row][D], a lane has 4 columns
 template <int D, int kTiles>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p, int ctas) {
+  constexpr int kVec = kTiles ? 4 : 1, kAhead = kTiles ? 2 : 8;  // 16-byte pieces of a lane; parts in flight
   __shared__ int s_slot[kMaxCtas + 1];
   __shared__ int s_n;
-  __shared__ float4 s_o[8][32];
+  __shared__ float4 s_o[8][kVec][32];
   __shared__ float2 s_ml[8][32];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the kernel that writes the parts has ended
-  const int4 d = p.desc[2 * blockIdx.x + 1];
-  if (!(d.w & kPart)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 d = p.desc[2 * blockIdx.x + 1];
+  const int c1 = blockIdx.x + 1 + lane, w1 = warp == 0 && c1 < ctas ? p.desc[2 * c1].w : 0;
+  if (!(d.w & kPart)) return;
   if (warp == 0) {
     int n = 1;
     if (lane == 0) s_slot[0] = 2 * blockIdx.x + 1;
     for (int c = blockIdx.x + 1; c < ctas; c += 32) {  // CTAs without work lie between the parts of a short line
-      const int w = c + lane < ctas ? p.desc[2 * (c + lane)].w : 0;
+      const int w = c == blockIdx.x + 1 ? w1 : c + lane < ctas ? p.desc[2 * (c + lane)].w : 0;
       const unsigned last = __ballot_sync(0xFFFFFFFFu, w & kPartLast);
       unsigned have = __ballot_sync(0xFFFFFFFFu, w & kPart);
       if (last) have &= (last & -last) * 2u - 1u;  // up to the first that ends a tile
@@ -956,13 +959,13 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   const int parts = s_n;
   const int ways = parts >= 16 ? 8 : parts >= 8 ? 4 : 1, way = warp % ways, each = 8 / ways;  // warps of an item; items at a time
   const int subs = kTiles == 2 && d.y > p.sub ? 2 : 1;
-  const int items = kTiles ? subs * 4 * (D / 4) : (p.G * (D / 4) + 31) / 32;
+  const int items = kTiles ? subs * 4 * (D / 16) : (p.G * (D / 4) + 31) / 32;
   for (int i0 = blockIdx.y * each; i0 < items; i0 += gridDim.y * each) {
     const int i = i0 + warp / ways;
-    int col, row, sub = 0, rows = p.G;
+    int col, row, sub = 0, rows = p.G;  // col: in pieces
     if constexpr (kTiles > 0) {
-      const int rw = i / (D / 4);
-      col = i % (D / 4);
+      const int rw = i / (D / 16);
+      col = i % (D / 16) * 4;
       sub = rw >> 2;
       row = (rw & 3) * 32 + lane;
       rows = min(p.sub, d.y - sub * p.sub) * p.G;
@@ -970,65 +973,94 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       col = (i * 32 + lane) % (D / 4);
       row = (i * 32 + lane) / (D / 4);
     }
-    // a row of this warp exists at all (with lanes as rows: its first one)
-    const bool some = i < items && (kTiles == 0 ? row < rows : row - lane < rows);
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = way; k0 < parts; k0 += 4 * ways) {
-      float2 ml[4];
-      float4 x[4];
+    const bool some = i < items && row < rows;
+    const int t = row / p.G, h = d.z * p.G + row - t * p.G;
+    const long r = d.x + sub * p.sub + t;
+    uint2 zz[kVec];  // the gate, on its way with the parts
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+    for (int v = 0; v < kVec; v += kVec > 1 ? 2 : 1) {
+      if (!some || way != 0 || !p.z.p) continue;
+      const uint16_t* z = p.z.p + r * p.z.token + h * p.z.head + (col + v) * 4;
+      if constexpr (kVec > 1) {
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(z));
+        zz[v] = make_uint2(y.x, y.y);
+        zz[v + 1] = make_uint2(y.z, y.w);
+      } else {
+        zz[v] = __ldg(reinterpret_cast<const uint2*>(z));
+      }
+    }
+    float m = -INFINITY, l = 0.f;
+    float4 o[kVec];
+#pragma unroll
+    for (int v = 0; v < kVec; ++v) o[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float2& ml, const float4 (&x)[kVec]) {
+      const float m2 = fmaxf(m, ml.x), off = m2 == -INFINITY ? 0.f : m2;
+      const float a = ex2_approx(m - off), b = ex2_approx(ml.x - off);
+      l = l * a + ml.y * b;
+#pragma unroll
+      for (int v = 0; v < kVec; ++v)
+        o[v] = make_float4(o[v].x * a + x[v].x * b, o[v].y * a + x[v].y * b, o[v].z * a + x[v].z * b, o[v].w * a + x[v].w * b);
+      m = m2;
+    };
+    for (int k0 = way; k0 < parts; k0 += kAhead * ways) {
+      float2 ml[kAhead];
+      float4 x[kAhead][kVec];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
         const bool in = some && k0 + u * ways < parts;
         const long slot = s_slot[in ? k0 + u * ways : 0];
         const float4* part = p.part + slot * (long)(kPartBytes / sizeof(float4));
-        ml[u] = make_float2(-INFINITY, 0.f);
-        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (in) {
-          ml[u] = __ldcg(p.ml + slot * 256 + sub * 128 + row);
-          x[u] = __ldcg(kTiles > 0 ? part + (sub * (D / 4) + col) * 128 + row : part + row * (D / 4) + col);
-        }
+        ml[u] = in ? __ldcg(p.ml + slot * 256 + sub * 128 + row) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+          x[u][v] = !in ? make_float4(0.f, 0.f, 0.f, 0.f)
+                        : __ldcg(kTiles > 0 ? part + (sub * (D / 4) + col + v) * 128 + row : part + row * (D / 4) + col);
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float m2 = fmaxf(m, ml[u].x), off = m2 == -INFINITY ? 0.f : m2;
-        const float a = ex2_approx(m - off), b = ex2_approx(ml[u].x - off);
-        l = l * a + ml[u].y * b;
-        o = make_float4(o.x * a + x[u].x * b, o.y * a + x[u].y * b, o.z * a + x[u].z * b, o.w * a + x[u].w * b);
-        m = m2;
-      }
+      for (int u = 0; u < kAhead; ++u) add(ml[u], x[u]);
     }
     if (ways > 1) {
       s_ml[warp][lane] = make_float2(m, l);
-      s_o[warp][lane] = o;
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) s_o[warp][v][lane] = o[v];
       __syncthreads();
       if (way == 0) {
         for (int w = 1; w < ways; ++w) {
-          const float2 y = s_ml[warp + w][lane];
-          const float4 x = s_o[warp + w][lane];
-          const float m2 = fmaxf(m, y.x), off = m2 == -INFINITY ? 0.f : m2;
-          const float a = ex2_approx(m - off), b = ex2_approx(y.x - off);
-          l = l * a + y.y * b;
-          o = make_float4(o.x * a + x.x * b, o.y * a + x.y * b, o.z * a + x.z * b, o.w * a + x.w * b);
-          m = m2;
+          float4 x[kVec];
+#pragma unroll
+          for (int v = 0; v < kVec; ++v) x[v] = s_o[warp + w][v][lane];
+          add(s_ml[warp + w][lane], x);
         }
       }
       __syncthreads();
     }
-    if (some && way == 0 && row < rows) {
-      const int t = row / p.G, h = d.z * p.G + row - t * p.G;
-      const long r = d.x + sub * p.sub + t;
+    if (some && way == 0) {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      float y[4] = {o.x * inv, o.y * inv, o.z * inv, o.w * inv};
-      if (l == 0.f) y[0] = y[1] = y[2] = y[3] = 0.f;
-      if (p.z.p) {
-        const uint2 zz = __ldg(reinterpret_cast<const uint2*>(p.z.p + r * p.z.token + h * p.z.head + col * 4));
-        y[0] *= sigmoid_fast(__uint_as_float(zz.x << 16));
-        y[1] *= sigmoid_fast(__uint_as_float(zz.x & 0xFFFF0000u));
-        y[2] *= sigmoid_fast(__uint_as_float(zz.y << 16));
-        y[3] *= sigmoid_fast(__uint_as_float(zz.y & 0xFFFF0000u));
+      uint32_t out[2 * kVec];
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        float y[4] = {o[v].x * inv, o[v].y * inv, o[v].z * inv, o[v].w * inv};
+        if (l == 0.f) y[0] = y[1] = y[2] = y[3] = 0.f;
+        if (p.z.p) {
+          y[0] *= sigmoid_fast(__uint_as_float(zz[v].x << 16));
+          y[1] *= sigmoid_fast(__uint_as_float(zz[v].x & 0xFFFF0000u));
+          y[2] *= sigmoid_fast(__uint_as_float(zz[v].y << 16));
+          y[3] *= sigmoid_fast(__uint_as_float(zz[v].y & 0xFFFF0000u));
+        }
+        out[2 * v] = pack_bf2(y[0], y[1]);
+        out[2 * v + 1] = pack_bf2(y[2], y[3]);
       }
-      *reinterpret_cast<uint2*>(p.out + (r * p.Hq + h) * D + col * 4) = make_uint2(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]));
+      uint16_t* to = p.out + (r * p.Hq + h) * D + col * 4;
+      if constexpr (kVec > 1) {
+        if (p.wide_out) {
+          st_global32(to, out);
+        } else {
+          reinterpret_cast<uint4*>(to)[0] = make_uint4(out[0], out[1], out[2], out[3]);
+          reinterpret_cast<uint4*>(to)[1] = make_uint4(out[4], out[5], out[6], out[7]);
+        }
+      } else {
+        *reinterpret_cast<uint2*>(to) = make_uint2(out[0], out[1]);
+      }
     }
   }
 }
@@ -1044,7 +1076,7 @@ cudaError_t encode_pages(CUtensorMap* map, const void* base, const PagedCache& c
 
 template <int D, int kTiles>
 cudaError_t launch_join(const LaunchEnv& env, const AttnParams& p, int ctas) {
-  const int items = kTiles ? 4 * kTiles * (D / 4) : (p.G * (D / 4) + 31) / 32;
+  const int items = kTiles ? 4 * kTiles * (D / 16) : (p.G * (D / 4) + 31) / 32;
   // Its launch need not wait for the end of the kernel before it: it waits itself, before it reads.
   cudaLaunchAttribute early;
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1103,7 +1135,10 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   p.N = N;
   p.T = T;
   p.sub = 128 / p.G;
-  p.lead = 2;
+  // What beginning and ending a tile costs beside one block (D = 256, eight prompts' chunks: bf16 160 us with 2,
+  // 153 with 3, 144 with 4 and 5; e4m3 294, 285, 289, 292; D = 128, a prompt of 8192: 469 with 1, 450 with 2, 456
+  // with 3, and 511 us with none)
+  p.lead = D == 128 ? 2 : cache.e4m3 ? 3 : 4;
   p.inv_g = (65535 + p.G) / p.G;
   p.wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
