@@ -228,11 +228,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     prefetch_tensormap(&p.tmap_v);
     prefetch_tensormap(&p.tmap_q);
     start->left = 0;
-    p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
-    p.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
   }
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
-
+  await_grid();
+  if (tid < 2) p.desc[2 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
   find_start<C::kThreads>(p, step, scan, start);
   tc_fence_before();
   __syncthreads();
@@ -936,7 +935,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   __shared__ int s_n;
   __shared__ float4 s_o[8][kVec][32];
   __shared__ float2 s_ml[8][32];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the kernel that writes the parts has ended
+  await_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 d = p.desc[2 * blockIdx.x + 1];
   const int c1 = blockIdx.x + 1 + lane, w1 = warp == 0 && c1 < ctas ? p.desc[2 * c1].w : 0;
@@ -1077,17 +1076,7 @@ cudaError_t encode_pages(CUtensorMap* map, const void* base, const PagedCache& c
 template <int D, int kTiles>
 cudaError_t launch_join(const LaunchEnv& env, const AttnParams& p, int ctas) {
   const int items = kTiles ? 4 * kTiles * (D / 16) : (p.G * (D / 4) + 31) / 32;
-  // Its launch need not wait for the end of the kernel before it: it waits itself, before it reads.
-  cudaLaunchAttribute early;
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, items < 16 ? items : 16);
-  cfg.blockDim = dim3(256);
-  cfg.stream = env.stream;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, kTiles>, p, ctas);
+  return launch_early(attn_join_kernel<D, kTiles>, dim3(ctas, items < 16 ? items : 16), 256, 0, env.stream, p, ctas);
 }
 
 template <int D, int kTiles, bool kE4M3>
@@ -1102,8 +1091,7 @@ cudaError_t launch_tiles(const LaunchEnv& env, const AttnParams& p, int ctas) {
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = 1;
   }
-  attn_kernel<D, kTiles, kE4M3><<<ctas, C::kThreads, C::kSmem, env.stream>>>(p);
-  e = cudaGetLastError();
+  e = launch_early(attn_kernel<D, kTiles, kE4M3>, dim3(ctas), C::kThreads, C::kSmem, env.stream, p);
   if (e != cudaSuccess) return e;
   return launch_join<D, kTiles>(env, p, ctas);
 }

@@ -127,6 +127,7 @@ __device__ __forceinline__ float2 bf2_to_float2(uint32_t v) {
 template <int D, bool kE4M3>
 __global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_constant__ PrepareParams p) {
   constexpr int kLanes = D / 8;  // lanes of a head
+  await_grid();
   __shared__ __align__(16) float2 s_cs[kWarps][D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
   const long item = (long)blockIdx.x * kWarps + warp;
@@ -265,6 +266,7 @@ template <int D, bool kE4M3>
 __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const __grid_constant__ ReadParams p) {
   constexpr int kVals = kE4M3 ? 16 : 8, kLanes = D / kVals, kAt = 32 / kLanes;  // rows at a time: 1, 2 or 4
   const int lane = threadIdx.x & 31, sub = lane % kLanes, mine = lane / kLanes;
+  await_grid();
   // p.tokens tokens of a warp: their places are looked up side by side, a lane each
   const long t0 = ((long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * p.tokens;
   const int nt = (int)min((long)p.tokens, p.T - t0);
@@ -357,8 +359,7 @@ cudaError_t launch_attn_prepare(const LaunchEnv& env, int Hq, int Hkv, int D, co
   const unsigned grid = (unsigned)(((long)T * split + kWarps - 1) / kWarps);
   auto kern = D == 128 ? (cache.e4m3 ? prepare_kernel<128, true> : prepare_kernel<128, false>)
                        : (cache.e4m3 ? prepare_kernel<256, true> : prepare_kernel<256, false>);
-  kern<<<grid, 32 * kWarps, 0, env.stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(kern, dim3(grid), 32 * kWarps, 0, env.stream, p);
 }
 
 cudaError_t launch_attn_cache_read(const LaunchEnv& env, int Hkv, int D, const PagedCache& cache,
@@ -376,8 +377,7 @@ cudaError_t launch_attn_cache_read(const LaunchEnv& env, int Hkv, int D, const P
   const unsigned grid = (unsigned)(((long)T + (long)tokens * kWarps - 1) / ((long)tokens * kWarps));
   auto kern = D == 128 ? (cache.e4m3 ? cache_read_kernel<128, true> : cache_read_kernel<128, false>)
                        : (cache.e4m3 ? cache_read_kernel<256, true> : cache_read_kernel<256, false>);
-  kern<<<grid, 32 * kWarps, 0, env.stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(kern, dim3(grid), 32 * kWarps, 0, env.stream, p);
 }
 
 }  // namespace gdn

@@ -322,6 +322,24 @@ constexpr float kLazy = 8.f;  // a row's maximum is raised when a score exceeds 
 constexpr int kMaxCtas = 160;  // SMs of the largest part of this architecture
 constexpr size_t kPartBytes = 131072;
 
+// A launch that need not wait for the end of the kernel before it in the stream: the kernel calls await_grid()
+// before it reads or writes memory.
+template <typename... A>
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void await_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 cudaError_t launch_attn_decode(const LaunchEnv& env, AttnParams& p, int D, int ctas);
 
 }  // namespace gdn

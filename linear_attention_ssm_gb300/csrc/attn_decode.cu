@@ -127,9 +127,9 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
     prefetch_tensormap(&p.tmap_k);
     prefetch_tensormap(&p.tmap_v);
     start->left = 0;
-    p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
-    p.desc[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
   }
+  await_grid();
+  if (tid < 2) p.desc[2 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
   find_start<C::kThreads>(p, 1, scan, start);
   __syncthreads();
   if (start->left == 0) return;
@@ -609,8 +609,7 @@ cudaError_t launch_one(const LaunchEnv& env, const AttnParams& p, int ctas) {
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = 1;
   }
-  attn_decode_kernel<D, kE4M3, kQ8><<<ctas, C::kThreads, C::kSmem, env.stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(attn_decode_kernel<D, kE4M3, kQ8>, dim3(ctas), C::kThreads, C::kSmem, env.stream, p);
 }
 
 template <int D, bool kE4M3>

@@ -219,3 +219,46 @@ def test_a_captured_layer_advances_by_itself():
         want, tol = attention(qr, cache, table, [1] * n, now, 0.09)
         assert_within(out, want, tol, f"replay {i}")
     g.gdn_check_device_errors()
+
+
+def test_a_captured_step_on_two_branches():
+    """Queries from one branch of a graph, keys and values from another (the attention's first kernel has two
+    predecessors there, one of them a copy), replayed with new inputs."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(10)
+    hq, hkv, D, page, kv = 8, 2, 256, 32, [300, 7]
+    cache, table = make_cache(g, gen, [1, 1], kv, hkv, page, D, True)
+    q, k, v = randn(gen, 2, hq, D), randn(gen, 2, hkv, D), randn(gen, 2, hkv, D)
+    qin, qs, out = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+    dense = [torch.empty(4, hkv, D, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    lens, cu, starts = ints(kv), ints([0, 2, 4]), ints([100, 3])
+    ws = torch.empty(g.gdn_attn_workspace_size(hq, hkv, D), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            qs.copy_(q)
+            g.gdn_attn_cache_read(cache, table, cu, *dense, starts=starts)
+        g.gdn_attn_prepare(None, k, v, cache, table, lens)
+        qin.copy_(q)
+        here.wait_stream(side)
+        g.gdn_attn_decode_step(qs, cache, table, lens, 0.06, out=out, workspace=ws)
+    first = torch.cuda.Stream()
+    with torch.cuda.stream(first):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(5):
+        for x in (q, k, v):
+            x.copy_(randn(gen, *x.shape))
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        want, tol = attention(q, cache, table, [1, 1], kv, 0.06)
+        assert_within(out, want, tol, f"replay {i}")
+    assert torch.equal(dense[0][:2], dense_rows(cache, table[0], 102)[0][:, 100:].transpose(0, 1).bfloat16())
+    g.gdn_check_device_errors()
