@@ -7,9 +7,9 @@
 // in tensor memory.  m is raised (and O, l scaled down) only when a block exceeds it by more than 2^8:
 // the weights stay below 2^8 and the common block leaves O alone.
 //
-// Two S slots let one block's softmax run beside the other's products.  Long chunks at D = 128 take two
-// tiles a CTA, a slot each (kTiles = 2: K and V are read once for 256 rows); otherwise the blocks of
-// one tile alternate between the slots (kTiles = 1; at D = 256 O alone fills half the tensor memory).
+// A tile's two S slots let one step's softmax run beside the other's products.  Long chunks at D = 128 take two
+// tiles a CTA (kTiles = 2: K and V are read once for 256 rows) with slots of 64 keys, half a block; otherwise a CTA
+// has one tile and slots of a block (kTiles = 1; at D = 256 O alone fills half the tensor memory).
 //
 // Warps: four a tile for the softmax; two that issue products (a tile's each, or with one tile one for
 // the scores and one for O), so that one's waiting does not idle the tensor cores; one that loads Q, K and
@@ -20,6 +20,13 @@
 // Work: the (tile, block) pairs of all sequences in one line, cut into one equal piece for each SM.  A
 // tile that a cut falls into leaves its parts (O, m, l) in the workspace for a second kernel to join,
 // so a few long sequences spread over the whole GPU as a large batch does.
+//
+// Measured on a GB300 (of 1956 TFLOP/s of bf16 products): a prompt of 8192 tokens, 32 heads of 128, 436 us, 1.26
+// PFLOP/s, 64 % -- the tensor pipe is nine tenths busy, its 64-key products at half their rate; 2048 tokens after
+// 30001, 16 heads of 256, 701 us, 1.48 PFLOP/s, 76 % -- keys and values from L2, 128 KB a block for each SM; chunks
+// of eight prompts of 17 to 1500 tokens, 16 heads of 256, 126 us from bf16 pages, 917 TFLOP/s, and 270 us from e4m3
+// ones, 428 TFLOP/s -- widening the codes beside the softmax, whose instructions leave the caches between them; 17
+// tokens after 1000, 48 heads of 128, 17 us -- latency, of two launches.
 #include <cstring>
 
 #include "attn_common.cuh"
@@ -63,12 +70,15 @@ struct Cfg {
   // of the four warps behind the softmax's: the products (two), Q, K and V by TMA, value rows behind the
   // last key (e4m3: scales)
   static constexpr int kMma0 = kSoftWarps, kMma1 = kSoftWarps + 1, kLoad = kSoftWarps + 2, kTail = kSoftWarps + 3;
-  // Scores that a softmax warp holds at a time; the rest of a block's are read twice.  Few registers, and
+  // Scores that a softmax warp holds at a time; the rest of a step's are read twice.  Few registers, and
   // short code for the instruction cache that warps of several kinds share: 32 beat 128 by 2 % at D = 256
-  // and by a third for e4m3; two tiles were best with 64 (894 TFLOP/s, 875 with 32 or 128).
+  // and by a third for e4m3 (8192 prompt tokens at D = 128: 707 us with 32, 792 with 64); two bf16 tiles hold
+  // their 64 (468 us, 472 with 32).
   static constexpr int kCols = kTiles == 2 && !kE4M3 ? 64 : 32;
   // Keys whose scores a slot holds: a block's, or with two tiles half of them.  A tile has two slots, so that
-  // its next scores are there when the weights of these are done.
+  // its next scores are there when the weights of these are done (8192 prompt tokens 467 us; with a slot of 128
+  // keys for each tile 605, with both halves' scores from one product 579).  A product of 64 keys costs what one
+  // of 128 does (558 and 524 clocks at D = 128, measured alone): the tensor pipe is busy for nine tenths of that.
   static constexpr int kKeys = kTiles == 2 ? 64 : 128, kHalves = 128 / kKeys;
   static constexpr uint32_t kColO = 256;  // tensor memory: the slots, 256 columns, then O
 };
@@ -956,6 +966,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
   __syncthreads();
   const int parts = s_n;
+  // (one token at 4000 keys, 76 parts a tile: 16.2 us with, 19.4 without)
   const int ways = parts >= 16 ? 8 : parts >= 8 ? 4 : 1, way = warp % ways, each = 8 / ways;  // warps of an item; items at a time
   const int subs = kTiles == 2 && d.y > p.sub ? 2 : 1;
   const int items = kTiles ? subs * 4 * (D / 16) : (p.G * (D / 4) + 31) / 32;
@@ -1137,11 +1148,18 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  // One token of each sequence and at most 16 query heads to a key head: too few rows to fill a
-  // 128-row tile, and HBM bounds the call.
-  if (!cu && p.G <= 16) {
+  // One token of each sequence and few query heads to a key head: too few rows to fill a 128-row tile, and HBM
+  // bounds the call.  By groups of 8 heads, this kernel against the tiles' (64 sequences of 30 to 30000 keys at
+  // D = 256, 256 of 500 to 8000 at D = 128): D = 256 bf16 98 : 103 us, one sequence of 4000 keys 16 : 22; e4m3
+  // 62 : 156; D = 128 bf16 413 : 467, e4m3 256 : 896; with 16 heads D = 128 bf16 221 : 257, e4m3 193 : 452, but
+  // D = 256 bf16 169 : 107, e4m3 170 : 160.
+  if (!cu && p.G <= (D == 128 ? 16 : 8)) {
     p.sub = 1;
-    p.lead = cache.e4m3 && D == 128 ? 2 : 1;  // about a microsecond of HBM's time for an SM
+    // A tile's beginning and end, in blocks of HBM's time for an SM.  D = 256 bf16 with 1, 2, 3: 104, 98, 98 us, 400
+    // sequences of 30 to 3000 keys 127, 105, 107; e4m3 with 2, 4, 5, 6: 87, 66, 62, 62 (2048 tiles of 30 blocks:
+    // 519, 532, 544, 557).  D = 128 bf16 with 1, 2, 3: 424, 421, 429, short sequences 230, 191, 203; e4m3 with 2, 3,
+    // 4: 256, 261, 267, short ones 154, 136, 145.
+    p.lead = !cache.e4m3 ? 2 : D == 128 ? 3 : 5;
     e = launch_attn_decode(env, p, D, ctas);
     if (e != cudaSuccess) return e;
     return D == 128 ? launch_join<128, 0>(env, p, ctas) : launch_join<256, 0>(env, p, ctas);
@@ -1150,7 +1168,9 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   if (e == cudaSuccess) e = encode_pages(&p.tmap_v, cache.v, cache, Hkv, D);
   if (e == cudaSuccess) e = encode_bf16_3d_sw128(&p.tmap_q, q, D, Hq, T, 64, p.G, p.sub);
   if (e != cudaSuccess) return e;
-  // two tiles a CTA where a sequence has more rows than one holds, on average
+  // Two tiles a CTA where a sequence has more rows than one holds, on average.  64 sequences of 2000 keys, 96 rows
+  // for each: one tile 111 us, two 112 (e4m3 185 : 223); 160 rows: 200 : 123 (349 : 184); a prompt of 8192 tokens
+  // 732 : 436 (1216 : 640).
   const bool two = (long)T * p.G > 128L * N;
   if (cache.e4m3) {
     if (D == 256) return launch_tiles<256, 1, true>(env, p, ctas);
