@@ -22,7 +22,7 @@
 // so a few long sequences spread over the whole GPU as a large batch does.
 //
 // Measured on a GB300 (of 1956 TFLOP/s of bf16 products): a prompt of 8192 tokens, 32 heads of 128, 436 us, 1.26
-// PFLOP/s, 64 % -- the tensor pipe is nine tenths busy, its 64-key products at half their rate; 2048 tokens after
+// PFLOP/s, 64 % -- products, nine tenths of the time by their own clocks, those of 64 keys at half the rate; 2048 tokens after
 // 30001, 16 heads of 256, 701 us, 1.48 PFLOP/s, 76 % -- keys and values from L2, 128 KB a block for each SM; chunks
 // of eight prompts of 17 to 1500 tokens, 16 heads of 256, 126 us from bf16 pages, 917 TFLOP/s, and 270 us from e4m3
 // ones, 428 TFLOP/s -- widening the codes beside the softmax, whose instructions leave the caches between them; 17
@@ -78,7 +78,7 @@ struct Cfg {
   // Keys whose scores a slot holds: a block's, or with two tiles half of them.  A tile has two slots, so that
   // its next scores are there when the weights of these are done (8192 prompt tokens 467 us; with a slot of 128
   // keys for each tile 605, with both halves' scores from one product 579).  A product of 64 keys costs what one
-  // of 128 does (558 and 524 clocks at D = 128, measured alone): the tensor pipe is busy for nine tenths of that.
+  // of 128 does (558 and 524 clocks at D = 128, measured alone): products take nine tenths of the time by that.
   static constexpr int kKeys = kTiles == 2 ? 64 : 128, kHalves = 128 / kKeys;
   static constexpr uint32_t kColO = 256;  // tensor memory: the slots, 256 columns, then O
 };

@@ -267,7 +267,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* 
   const long u0 = share * blockIdx.x + divide(extra * blockIdx.x, gridDim.x);
   const long u1 = share * (blockIdx.x + 1) + divide(extra * (blockIdx.x + 1), gridDim.x);
   if (u1 == u0) return;
-  long base = 0;  // units of the sequences before this round's (one round where every thread had one sequence)
+  long base = 0;  // units of the sequences of the passes before (one pass where every thread had one sequence)
   for (int n0 = 0;; n0 += kThreads) {
     const int n = n0 + tid;
     if (p.N > kThreads) {
