@@ -166,6 +166,7 @@ struct Segment {
 struct WalkStart {
   long left, rem;
   int n, hk, tile, j;
+  SeqInfo s;  // of sequence n
 };
 
 // A CTA's piece of the line, segment by segment.  Every warp walks it by itself.
@@ -186,7 +187,8 @@ struct Walk {
       hk = w.hk;
       tile = w.tile;
       j = w.j;
-      load(p, step);
+      s = w.s;
+      t = {s.kv - s.len, s.len, step, p.lead};
     }
   }
   __device__ __forceinline__ bool next(const AttnParams& p, int step, Segment& g) {
@@ -236,8 +238,10 @@ template <int kThreads>
 __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* scan, WalkStart* start) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // units of one key head of sequence n
+  SeqInfo seen = {0, 0, 0};  // the last one
   auto units_of = [&](int n, bool report) {
     const SeqInfo s = seq_info(p, n, report);
+    seen = s;
     const Tiles t = {s.kv - s.len, s.len, step, p.lead};
     return s.len > 0 ? t.before(t.count()) : 0L;
   };
@@ -282,6 +286,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* 
     if (mine > 0 && u0 >= before && u0 < before + mine) {
       start->left = u1 - u0;
       start->n = n;
+      start->s = seen;
       start->hk = (int)divide(u0 - before, per);
       start->rem = u0 - before - start->hk * per;
     }
@@ -289,7 +294,7 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* 
   }
   __syncthreads();
   // the tile: every thread looks at one stretch of them
-  const SeqInfo s = seq_info(p, start->n, false);
+  const SeqInfo s = start->s;
   const Tiles t = {s.kv - s.len, s.len, step, p.lead};
   const int count = t.count(), stretch = (count + kThreads - 1) / kThreads;
   const long rem = start->rem;

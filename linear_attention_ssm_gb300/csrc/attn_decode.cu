@@ -43,7 +43,8 @@ struct DCfg {
   static constexpr int kGroups = kKeys / kGroup, kSets = kWarps / kGroups;
   static constexpr int kThreads = 32 * (kWarps + 2);  // and one that loads the keys, one the values
   static constexpr int kTiles = D / 16;               // of O^T
-  static constexpr int kMergeO = kWarps / 2 * kQ8 * 8 * D * 4, kMergeMl = kWarps / 2 * 32 * kQ8 * 16;
+  static constexpr int kMergeRow = 33;                // 16-byte pieces from one mma tile of O^T to the next, where it is merged
+  static constexpr int kMergeO = kWarps / 2 * kQ8 * kTiles * kMergeRow * 16, kMergeMl = kWarps / 2 * 32 * kQ8 * 16;
   static constexpr int kQBytes = 2 * kQ8 * 8 * D * 2;  // two segments' queries
   static constexpr int kScale = kE4M3 ? 2 * kKeys : 0;
   static constexpr int kFixed = kMergeO + kMergeMl + kQBytes + 1024 + 1024;
@@ -515,9 +516,12 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
             }
           }
         }
-      // half of the warps hand theirs over, the others add their own
+      // Half of the warps hand theirs over, the others add their own.  (Lane 4 r + c's piece lies where neither
+      // eight neighbouring lanes nor the eight r of one c share banks.)
+      auto place = [](int r, int c) { return (r >> 1) * 8 + ((2 * c + (r & 1)) ^ (2 * (r >> 1))); };
       constexpr int kHalfWarps = kWarps / 2;
-      float4* slot_o = mo + (warp % kHalfWarps) * kQ8 * kTiles * 32 + lane;
+      constexpr int kRow = C::kMergeRow;
+      float4* slot_o = mo + (warp % kHalfWarps) * kQ8 * kTiles * kRow + place(g, c);
       float4* slot_ml = mml + (warp % kHalfWarps) * kQ8 * 32 + lane;
       if (warp < kHalfWarps) warps_sync();
 #pragma unroll
@@ -535,13 +539,13 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
           }
 #pragma unroll
           for (int t = 0; t < kTiles; ++t) {
-            const float4 x = slot_o[(a * kTiles + t) * 32];
-            slot_o[(a * kTiles + t) * 32] = make_float4(o[a][t][0] * f0[0] + x.x * f1[0], o[a][t][1] * f0[1] + x.y * f1[1],
+            const float4 x = slot_o[(a * kTiles + t) * kRow];
+            slot_o[(a * kTiles + t) * kRow] = make_float4(o[a][t][0] * f0[0] + x.x * f1[0], o[a][t][1] * f0[1] + x.y * f1[1],
                                                         o[a][t][2] * f0[0] + x.z * f1[0], o[a][t][3] * f0[1] + x.w * f1[1]);
           }
         } else {
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) slot_o[(a * kTiles + t) * 32] = make_float4(o[a][t][0], o[a][t][1], o[a][t][2], o[a][t][3]);
+          for (int t = 0; t < kTiles; ++t) slot_o[(a * kTiles + t) * kRow] = make_float4(o[a][t][0], o[a][t][1], o[a][t][2], o[a][t][3]);
         }
         slot_ml[a * 32] = make_float4(m[a][0], m[a][1], l[a][0], l[a][1]);
       }
@@ -564,13 +568,13 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
         for (int w = 0; w < kHalfWarps; ++w) {
           const float f = mx == -INFINITY ? 0.f : ex2_approx(mk[w] - mx);
           lx += lk[w] * f;
-          const float* x = reinterpret_cast<const float*>(mo + (w * kQ8 + a) * kTiles * 32) + k;
+          const float* x = reinterpret_cast<const float*>(mo + (w * kQ8 + a) * kTiles * kRow) + k;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             // where value d + e of this row sits: mma tile, lane row, half
             const int t = kE4M3 ? (d >> 7) * 8 + ((d + e) >> 1 & 7) : d >> 4, lr = kE4M3 ? d >> 4 & 7 : e,
                       hf = kE4M3 ? e & 1 : d >> 3 & 1;
-            v[e] += x[(t * 32 + 4 * lr + at) * 4 + 2 * hf] * f;
+            v[e] += x[(t * kRow + place(lr, at)) * 4 + 2 * hf] * f;
           }
         }
         const float inv = whole ? (lx == 0.f ? 0.f : 1.f / lx) : 1.f;
