@@ -966,7 +966,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
   __syncthreads();
   const int parts = s_n;
-  // (one token at 4000 keys, 76 parts a tile: 16.2 us with, 19.4 without)
+  // (one token at 4000 keys, 76 parts a tile: 14.0 us with, 3 more without)
   const int ways = parts >= 16 ? 8 : parts >= 8 ? 4 : 1, way = warp % ways, each = 8 / ways;  // warps of an item; items at a time
   const int subs = kTiles == 2 && d.y > p.sub ? 2 : 1;
   const int items = kTiles ? subs * 4 * (D / 16) : (p.G * (D / 4) + 31) / 32;
@@ -1150,16 +1150,16 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   // One token of each sequence and few query heads to a key head: too few rows to fill a 128-row tile, and HBM
   // bounds the call.  By groups of 8 heads, this kernel against the tiles' (64 sequences of 30 to 30000 keys at
-  // D = 256, 256 of 500 to 8000 at D = 128): D = 256 bf16 98 : 103 us, one sequence of 4000 keys 16 : 22; e4m3
-  // 62 : 156; D = 128 bf16 413 : 467, e4m3 256 : 896; with 16 heads D = 128 bf16 221 : 257, e4m3 193 : 452, but
+  // D = 256, 256 of 500 to 8000 at D = 128): D = 256 bf16 97 : 103 us, one sequence of 4000 keys 14 : 22; e4m3
+  // 60 : 156; D = 128 bf16 421 : 467, e4m3 262 : 896; with 16 heads D = 128 bf16 221 : 257, e4m3 169 : 452, but
   // D = 256 bf16 169 : 107, e4m3 170 : 160.
   if (!cu && p.G <= (D == 128 ? 16 : 8)) {
     p.sub = 1;
-    // A tile's beginning and end, in blocks of HBM's time for an SM.  D = 256 bf16 with 1, 2, 3: 104, 98, 98 us, 400
-    // sequences of 30 to 3000 keys 127, 105, 107; e4m3 with 2, 4, 5, 6: 87, 66, 62, 62 (2048 tiles of 30 blocks:
-    // 519, 532, 544, 557).  D = 128 bf16 with 1, 2, 3: 424, 421, 429, short sequences 230, 191, 203; e4m3 with 2, 3,
-    // 4: 256, 261, 267, short ones 154, 136, 145.
-    p.lead = !cache.e4m3 ? 2 : D == 128 ? 3 : 5;
+    // A tile's beginning and end, in blocks of HBM's time for an SM ("short": 400 sequences of 30 to 3000 keys).  bf16
+    // with 1, 2, 3: D = 256 97, 98, 97 us, short 98, 99, 104; D = 128 421, 423, 428, short 179, 191, 205.  e4m3 at
+    // D = 256 with 3, 4, 5: 64, 60, 60, short 86, 82, 78 (2048 tiles of 30 blocks: 507, 518, 528); at D = 128 with
+    // 2, 3, 4: 256, 262, 267, short 146, 137, 146, with 16 heads to a key head 180, 169, 171.
+    p.lead = !cache.e4m3 ? 1 : D == 128 ? 3 : 4;
     e = launch_attn_decode(env, p, D, ctas);
     if (e != cudaSuccess) return e;
     return D == 128 ? launch_join<128, 0>(env, p, ctas) : launch_join<256, 0>(env, p, ctas);

@@ -16,9 +16,9 @@
 // with it).  Weights are at most 2^8: times 2^7 they still fit binary16, and only weights below 2^-21 of
 // a row's largest leave its normal range.
 //
-// Measured on a GB300 (of 6792 GB/s copied): 64 sequences of 30 to 30000 keys, 2 key heads of 256, bf16 99 us, 6.0
-// TB/s, 89 %, e4m3 62 us; 256 sequences of 500 to 8000 e4m3 keys, 8 of 128, 261 us, 5.5 TB/s, 81 %; one sequence of
-// 4000 keys 16 us -- the latency of two launches, HBM's share is 1.2.
+// Measured on a GB300 (of 6792 GB/s copied): 64 sequences of 30 to 30000 keys, 2 key heads of 256, bf16 97 us, 6.2
+// TB/s, 91 %, e4m3 60 us; 256 sequences of 500 to 8000 e4m3 keys, 8 of 128, 261 us, 5.5 TB/s, 81 %; one sequence of
+// 4000 keys 14 us -- the latency of two launches, HBM's share is 1.2.
 #include <cstring>
 
 #include "attn_common.cuh"
