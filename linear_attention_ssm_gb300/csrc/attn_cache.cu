@@ -7,8 +7,8 @@
 // heads, and a head costs a 16-byte load a lane, one reduction and two packed fused multiply-adds for
 // each pair of values.  Four heads' loads are in flight.
 //
-// Measured on a GB300 (of 6792 GB/s copied): 8192 tokens of 32 + 8 + 8 heads of 128 to bf16 pages 42 us, 4.8 TB/s;
-// 14538 of 16 + 2 + 2 heads of 256 to e4m3 pages 59 us, 4.8 TB/s; 64 such tokens 5.8 us; 32768 e4m3 rows of 2 heads
+// Measured on a GB300 (of 6792 GB/s copied): 8192 tokens of 32 + 8 + 8 heads of 128 to bf16 pages 39 us, 5.1 TB/s;
+// 14538 of 16 + 2 + 2 heads of 256 to e4m3 pages 58 us, 4.8 TB/s; 64 such tokens 5.8 us; 32768 e4m3 rows of 2 heads
 // of 256 read in 14.7 us, 6.9 TB/s (in a row of calls, which find part of their 101 MB in L2).
 #include "attn_common.cuh"
 
@@ -16,7 +16,7 @@ namespace gdn {
 namespace {
 
 constexpr int kWarps = 4;   // of a CTA: short ones, so that the last wave of CTAs is short too
-constexpr int kUnroll = 4;  // loads that a lane has in flight
+constexpr int kUnroll = 4;  // loads that a lane has in flight (8192 tokens: 41 us with 4, 47 with 8, 55 with 2)
 
 struct PrepareParams {
   HeadRows q, k, v;
@@ -137,15 +137,6 @@ __global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_co
   const long item = (long)blockIdx.x * kWarps + warp;
   const int t = (int)(item / p.split), share = (int)(item - (long)t * p.split);
   if (t >= p.T) return;
-  // the token's rows are on their way while its place in the cache is looked up
-  auto ahead = [&](const HeadRows& rows, int heads) {
-    const char* at = reinterpret_cast<const char*>(rows.p + t * rows.token);
-    for (int i = lane + 32 * share; i < heads * (D / 64); i += 32 * p.split)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(at + (i / (D / 64)) * rows.head * 2 + (i % (D / 64)) * 128));
-  };
-  if (p.q.p) ahead(p.q, p.Hq);
-  ahead(p.k, p.Hkv);
-  ahead(p.v, p.Hkv);
   int first, len;
   const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
   if (seq < 0) {
