@@ -7,8 +7,8 @@
 // heads, and a head costs a 16-byte load a lane, one reduction and two packed fused multiply-adds for
 // each pair of values.  Four heads' loads are in flight.
 //
-// Measured on a GB300 (of 6792 GB/s copied): 8192 tokens of 32 + 8 + 8 heads of 128 to bf16 pages 39 us, 5.1 TB/s;
-// 14538 of 16 + 2 + 2 heads of 256 to e4m3 pages 58 us, 4.8 TB/s; 64 such tokens 5.8 us; 32768 e4m3 rows of 2 heads
+// Measured on a GB300 (of 6792 GB/s copied): 8192 tokens of 32 + 8 + 8 heads of 128 to bf16 pages 38 us, 5.2 TB/s;
+// 14538 of 16 + 2 + 2 heads of 256 to e4m3 pages 59 us, 4.8 TB/s; 64 such tokens 5.7 us; 32768 e4m3 rows of 2 heads
 // of 256 read in 14.7 us, 6.9 TB/s (in a row of calls, which find part of their 101 MB in L2).
 #include "attn_common.cuh"
 
@@ -133,9 +133,18 @@ __global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_co
   constexpr int kLanes = D / 8;  // lanes of a head
   await_grid();
   __shared__ __align__(16) float2 s_cs[kWarps][D / 2];
+  __shared__ float2 s_turns[D / 2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % kLanes;
   const long item = (long)blockIdx.x * kWarps + warp;
   const int t = (int)(item / p.split), share = (int)(item - (long)t * p.split);
+  // turns of one position, in two parts: the only fp64 arithmetic, once for the CTA's tokens
+  const int rot = p.rope.rot, half = rot / 2;
+  for (int j = threadIdx.x; j < half; j += 32 * kWarps) {
+    const double f = __ldg(p.rope.freqs + j) * 0.15915494309189533577;
+    const float hi = (float)f;
+    s_turns[j] = make_float2(hi, (float)(f - (double)hi));
+  }
+  __syncthreads();
   if (t >= p.T) return;
   int first, len;
   const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
@@ -155,12 +164,9 @@ __global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_co
   if (bad) raise_error(p.err, kErrDeviceArgument);
 
   // the token's cosines and sines
-  const int rot = p.rope.rot, half = rot / 2;
   for (int j = lane; j < half; j += 32) {
-    const double f = __ldg(p.rope.freqs + j) * 0.15915494309189533577;  // turns of one position
-    const float hi = (float)f;
     float s, c;
-    sincospif(2.f * turns_of(pos, hi, (float)(f - (double)hi)), &s, &c);
+    sincospif(2.f * turns_of(pos, s_turns[j].x, s_turns[j].y), &s, &c);
     s_cs[warp][j] = make_float2(c * p.rope.magnitude, s * p.rope.magnitude);
   }
   __syncwarp();
@@ -336,8 +342,8 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const __grid_co
 
 // Warps of one token: as many as bring sixteen warps to every SM, as long as each has loads to keep in
 // flight (`units`: steps of a warp that has the token alone).  64 tokens of 16 + 2 + 2 heads of 256: 5.8 us
-// with eight warps a token, 10.1 with one; 600 of 32 + 8 + 8 heads of 128: 8.0 (four), 9.4 with eight, 9.8 with
-// one; 8192 of them: 42 us with one, 75 with eight.
+// with eight warps a token, 10.1 with one; 600 of 32 + 8 + 8 heads of 128: 7.2 (four; before a later
+// step 8.0, 9.4 with eight, 9.8 with one); 8192 of them: 38 us with one (then 42, 75 with eight).
 int warps_of_token(int T, int sms, int units) {
   const int want = (16 * sms + T - 1) / T, most = units < 8 ? units : 8;
   return want < 1 ? 1 : want > most ? most : want;
