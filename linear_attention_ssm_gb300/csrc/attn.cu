@@ -1138,7 +1138,10 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   // 153 with 3, 144 with 4 and 5; e4m3 294, 285, 289, 292; D = 128, a prompt of 8192: 469 with 1, 450 with 2, 456
   // with 3, and 511 us with none)
   p.lead = D == 128 ? 2 : cache.e4m3 ? 3 : 4;
-  p.inv_g = (65535 + p.G) / p.G;
+  // Fewer CTAs on a short line: a part costs its reader as much as a block.  17 tokens after 1000, 16 key heads of
+  // 128: 17.3 us with no such limit, 14.8 with 2, 15.5 with 3, 16.9 with 4; 16 tokens after 4000, 2 of 256: 32.2 us,
+  // 25.7, 24.0, 23.6.
+  p.least = p.lead;
   p.wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.desc = reinterpret_cast<int4*>(ws);
@@ -1160,6 +1163,7 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
     // D = 256 with 3, 4, 5: 64, 60, 60, short 86, 82, 78 (2048 tiles of 30 blocks: 507, 518, 528); at D = 128 with
     // 2, 3, 4: 256, 262, 267, short 146, 137, 146, with 16 heads to a key head 180, 169, 171.
     p.lead = !cache.e4m3 ? 1 : D == 128 ? 3 : 4;
+    p.least = 2;  // one sequence of 16000 keys 17.1 us with 1, 15.4 with 2, 16.8 with 3; of 4000 14.3, 14.7, 17.5
     e = launch_attn_decode(env, p, D, ctas);
     if (e != cudaSuccess) return e;
     return D == 128 ? launch_join<128, 0>(env, p, ctas) : launch_join<256, 0>(env, p, ctas);

@@ -74,9 +74,9 @@ struct AttnParams {
   float scale_log2;
   int Hq, Hkv, G, N, T;
   int sub;       // tokens of one tile: 128 / G on the tcgen05 cores, 1 in the one-token kernel
-  int inv_g;     // row / G is (row * inv_g) >> 16 for the rows of a tile
   bool wide_out; // out is 32-byte aligned
   int lead;      // blocks that beginning and ending a tile cost, in the line of work
+  int least;     // units of the line that a CTA takes, if it takes any
   int4* desc;    // [2 * grid] what each part of a cut tile holds: packed row, tokens, key head, flags
   float2* ml;    // [2 * grid][256] maximum (log2 units) and sum of a row
   float4* part;  // [2 * grid][128 KB] unnormalised O
@@ -231,7 +231,7 @@ __device__ __forceinline__ long divide(long a, long b) {  // both >= 0, b > 0
   return (a | b) >> 32 ? a / b : (long)((uint32_t)a / (uint32_t)b);
 }
 
-// This CTA's piece of the line: an equal share of its units, found by the whole CTA.  `scan`: one long
+// This CTA's piece of the line: an equal share of its units, p.least at least, found by the whole CTA.  `scan`: one long
 // for each warp; start->left is 0 before the call and stays 0 for a CTA without work.  The caller
 // synchronises before it reads *start.
 template <int kThreads>
@@ -267,9 +267,13 @@ __device__ __forceinline__ void find_start(const AttnParams& p, int step, long* 
     mine += per * p.Hkv;
   }
   sums(mine, before, total);
-  const long share = divide(total, gridDim.x), extra = total - share * gridDim.x;
-  const long u0 = share * blockIdx.x + divide(extra * blockIdx.x, gridDim.x);
-  const long u1 = share * (blockIdx.x + 1) + divide(extra * (blockIdx.x + 1), gridDim.x);
+  long share = divide(total, gridDim.x), extra = total - share * gridDim.x;
+  if (share < p.least) {  // a short line: the last CTAs have no work
+    share = p.least;
+    extra = 0;
+  }
+  const long u0 = min(total, share * blockIdx.x + divide(extra * blockIdx.x, gridDim.x));
+  const long u1 = min(total, share * (blockIdx.x + 1) + divide(extra * (blockIdx.x + 1), gridDim.x));
   if (u1 == u0) return;
   long base = 0;  // units of the sequences of the passes before (one pass where every thread had one sequence)
   for (int n0 = 0;; n0 += kThreads) {
