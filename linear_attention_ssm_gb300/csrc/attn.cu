@@ -21,12 +21,12 @@
 // tile that a cut falls into leaves its parts (O, m, l) in the workspace for a second kernel to join,
 // so a few long sequences spread over the whole GPU as a large batch does.
 //
-// Measured on a GB300 (of 1956 TFLOP/s of bf16 products): a prompt of 8192 tokens, 32 heads of 128, 436 us, 1.26
-// PFLOP/s, 64 % -- products, nine tenths of the time by their own clocks, those of 64 keys at half the rate; 2048 tokens after
-// 30001, 16 heads of 256, 701 us, 1.48 PFLOP/s, 76 % -- keys and values from L2, 128 KB a block for each SM; chunks
+// Measured on a GB300 (of 1956 TFLOP/s of bf16 products): a prompt of 8192 tokens, 32 heads of 128, 433 us, 1.27
+// PFLOP/s, 65 % -- products, nine tenths of the time by their own clocks, those of 64 keys at half the rate; 2048 tokens after
+// 30001, 16 heads of 256, 704 us, 1.48 PFLOP/s, 76 % -- keys and values from L2, 128 KB a block for each SM; chunks
 // of eight prompts of 17 to 1500 tokens, 16 heads of 256, 126 us from bf16 pages, 917 TFLOP/s, and 270 us from e4m3
 // ones, 428 TFLOP/s -- widening the codes beside the softmax, whose instructions leave the caches between them; 17
-// tokens after 1000, 48 heads of 128, 17 us -- latency, of two launches.
+// tokens after 1000, 48 heads of 128, 16 us -- latency, of two launches.
 #include <cstring>
 
 #include "attn_common.cuh"

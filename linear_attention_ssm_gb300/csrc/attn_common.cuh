@@ -1,5 +1,5 @@
 // attn_common.cuh -- what the kernels of the paged-cache attention share: where a token's row lies,
-// the e4m3 rows with their power of two.
+// e4m3 codes and their powers of two, the line of work and how it is cut, launches.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -32,12 +32,6 @@ __device__ __forceinline__ int attn_seq_of(const int32_t* cu, int N, int T, int 
 
 // 2^(b - 127) of an exponent byte
 __device__ __forceinline__ float e8m0_value(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x00400000u); }
-
-// two e4m3 codes (low byte first) -> two floats, exactly
-__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t v) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(v, __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 
 // 32 bytes of one thread (aligned to them): a whole sector
 __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
