@@ -24,8 +24,8 @@
 // Measured on a GB300 (of 1956 TFLOP/s of bf16 products): a prompt of 8192 tokens, 32 heads of 128, 433 us, 1.27
 // PFLOP/s, 65 % -- products, nine tenths of the time by their own clocks, those of 64 keys at half the rate; 2048 tokens after
 // 30001, 16 heads of 256, 704 us, 1.48 PFLOP/s, 76 % -- keys and values from L2, 128 KB a block for each SM; chunks
-// of eight prompts of 17 to 1500 tokens, 16 heads of 256, 126 us from bf16 pages, 917 TFLOP/s, and 270 us from e4m3
-// ones, 428 TFLOP/s -- widening the codes beside the softmax, whose instructions leave the caches between them; 17
+// of eight prompts of 17 to 1500 tokens, 16 heads of 256, 126 us from bf16 pages, 917 TFLOP/s, and 253 us from e4m3
+// ones, 455 TFLOP/s -- widening the codes beside the softmax, whose instructions leave the caches between them; 17
 // tokens after 1000, 48 heads of 128, 16 us -- latency, of two launches.
 #include <cstring>
 
@@ -555,29 +555,28 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     const int c_narrow = (2 * piece) ^ (row_narrow & 7), c_wide = (2 * piece) ^ (row_wide & 7);
     const int to_narrow = blk_narrow * 16384 + row_narrow * 128 + c_narrow * 16, to_wide = blk_wide * 8192 + row_wide * 128 + c_wide * 16;
     const int other_narrow = ((c_narrow ^ 1) - c_narrow) * 16, other_wide = ((c_wide ^ 1) - c_wide) * 16;  // to the second half
-    // The order of the stages, each operand of a block in kParts: K0 V0 K1 V1 .. with two tiles, with one
-    // K0 K1 V0 K2 V1 ..: after a block's keys come the values of the block before it, if the segment has
-    // one, and the block's own values, if it is the segment's last.
-    uint32_t blk = 0;               // the latest block whose keys have been reached
-    int mode = 0, part = -1;        // 0: keys of blk, 1: values of the block before, 2: values of blk
-    int flags = 0;
-    auto next_stage = [&]() {
-      if (++part == kParts) {
-        part = 0;
-        if (kTiles == 1 && mode == 0 && !(flags & kFirst)) {
-          mode = 1;
-        } else if (mode == 0 || (kTiles == 1 && mode == 1)) {
-          mode = kTiles == 2 || (flags & kLast) ? 2 : 0;
-          if (mode == 0) ++blk;
-        } else {
-          mode = 0;
-          ++blk;
-        }
+    // The order of the operands, each in kParts stages: K0 V0 K1 V1 .. with two tiles, with one K0 K1 V0 K2 V1 ..:
+    // after a block's keys come the values of the block before it, if the segment has one, and the block's own
+    // values, if it is the segment's last.  Where an operand has a stage for each group, a group has the same part
+    // of every one; else the groups take the operands in turn.
+    constexpr int kTurn = kGroups > kParts ? kGroups / kParts : 1;  // operands from one of this group's stages to its next
+    static_assert(!kE4M3 || kGroups % kParts == 0, "a part of an operand for each group, or whole operands");
+    const int part = kParts > 1 ? group : 0;
+    uint32_t blk = 0xFFFFFFFFu;     // the latest block whose keys have been reached
+    int mode = 2, flags = 0;        // 0: keys of blk, 1: values of the block before, 2: values of blk
+    auto next_operand = [&]() {
+      if (kTiles == 1 && mode == 0 && !(flags & kFirst)) {
+        mode = 1;
+        return true;
       }
-      if (mode == 0 && part == 0) {
-        if (!await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) return false;
-        flags = metas[blk % kMeta].flags;
+      if (mode != 2 && (kTiles == 2 || (flags & kLast))) {
+        mode = 2;
+        return true;
       }
+      mode = 0;
+      ++blk;
+      if (!await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) return false;
+      flags = metas[blk % kMeta].flags;
       return !(flags & kEnd);
     };
     Ring<kStages> ring;
@@ -585,8 +584,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     ring.skip(group);
     raw.skip(group);
     bool on = start->left > 0;
-    for (int ahead = group + 1; on; ahead = kGroups) {
-      for (int i = 0; i < ahead && on; ++i) on = next_stage();
+    for (int ahead = kParts > 1 ? 1 : group + 1; on; ahead = kTurn) {
+      for (int i = 0; i < ahead && on; ++i) on = next_operand();
       if (!on || !await(bar.raw_full + 8 * raw.i, raw.pass) || !await(bar.empty + 8 * ring.i, ring.pass ^ 1u)) break;
       const bool value = mode != 0, wide = value && D == 256;
       const uint32_t place = (mode == 1 ? blk - 1 : blk) % kMeta;
