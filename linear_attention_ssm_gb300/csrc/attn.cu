@@ -67,6 +67,7 @@ struct Cfg {
   static constexpr uint32_t kOffBar = kOffMeta + (kE4M3 ? kMeta * sizeof(BlockMeta) : 0);
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;  // barriers; alignment of the base
   static_assert(kSmem <= 232448, "shared memory");
+  static_assert(kStages <= 6 && kRawStages <= 3 && kThreads <= 32 * 60, "places of the barriers and of the scan");
   // of the four warps behind the softmax's: the products (two), Q, K and V by TMA, value rows behind the
   // last key (e4m3: scales)
   static constexpr int kMma0 = kSoftWarps, kMma1 = kSoftWarps + 1, kLoad = kSoftWarps + 2, kTail = kSoftWarps + 3;
@@ -605,8 +606,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         *reinterpret_cast<uint4*>(at + other) = make_uint4(mul_half2(c.x, f), mul_half2(c.y, f), mul_half2(e.x, f), mul_half2(e.y, f));
       };
       if (last >= 127 - base) {
-        // Short loops: the kernel's roles share the instruction caches (D = 256: 292 us for the chunks of eight
-        // prompts, 302 with one unit a pass, 330 with four; two tiles: 654 us for 8192 tokens, 698 with two)
+        // Short loops: the kernel's roles share the instruction caches (D = 256: 253 us for the chunks of eight
+        // prompts, 261 with one unit a pass, 299 with four; two tiles: 640 us for 8192 tokens, 746 with four)
 #pragma unroll(kTiles == 2 ? 1 : 2)
         for (int u = 0; u < kUnits; ++u)
           widen(u, *reinterpret_cast<const uint4*>(from + (row0 + u * stride) * 64), scale[base + row0 + u * stride]);
