@@ -870,6 +870,14 @@ def _empty(shape, dtype, device, stream):
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_spare_workspaces = {}  # (device, stream): the attention workspace of the last call there
+
+
+def _take_workspace(key, need, device):
+    """Scratch for a call on the current stream: the last call's there, whose kernels run before this one's, or new
+    memory.  Taken out of the dict for the time of the call: another thread's call on the stream gets its own."""
+    w = _spare_workspaces.pop(key, None)
+    return w if w is not None and w.numel() >= need else torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def _call(fn, device, stream, *args):
@@ -962,8 +970,15 @@ def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out
         out = _empty((T, hq, D), torch.bfloat16, dev, stream)
     op = _flat(out, torch.bfloat16, "out", (T, hq, D), dev)
     geo = _attn_geo(hq, hkv, D)
+    key = None
     if workspace is None:
-        workspace = _empty(lib.gdn_attn_workspace_size(geo), torch.uint8, dev, stream)
+        need = lib.gdn_attn_workspace_size(geo)
+        if stream is None and _raw_stream is not None and dev.index == torch.cuda.current_device() and \
+                not torch.cuda.is_current_stream_capturing():  # a graph's memory is its own
+            key = dev.index, _raw_stream(dev.index)
+            workspace = _take_workspace(key, need, dev)
+        else:
+            workspace = _empty(need, torch.uint8, dev, stream)
     elif workspace.device != dev:
         raise ValueError(f"workspace is on {workspace.device}, the call is on {dev}")
     tail = (softmax_scale, *zp, op, workspace.data_ptr(), workspace.numel() * workspace.element_size())
@@ -971,13 +986,16 @@ def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out
         _call(lib.gdn_attn_decode_step, dev, stream, geo, qp, c, table, pages, lens, T, *tail)
     else:
         _call(lib.gdn_attn_prefill, dev, stream, geo, qp, c, table, pages, lens, cu, N, T, *tail)
+    if key is not None:
+        _spare_workspaces[key] = workspace
     return out
 
 
 def gdn_attn_prefill(q, cache: KVCache, block_table, kv_lens, cu_seqlens, softmax_scale, z=None, out=None,
                      workspace=None, stream=None):
     """Causal attention of packed new tokens over their caches (which hold them too), optionally
-    gated by sigmoid(z); q, z, out [T, Hq, D] bf16.  Returns out."""
+    gated by sigmoid(z); q, z, out [T, Hq, D] bf16.  Returns out.  Without a workspace the call keeps
+    one for each stream (43 MB) between calls; in a graph's capture it is the graph's own."""
     if cu_seqlens is None:
         raise TypeError("cu_seqlens must be a CUDA tensor")
     return _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out, workspace, stream)

@@ -3,6 +3,7 @@ last key, outputs on 16-byte boundaries, more sequences than a CTA has threads, 
 shared pages, a stream given by the caller, empty batches, a graph of several calls."""
 from __future__ import annotations
 
+import concurrent.futures
 import math
 
 import pytest
@@ -262,3 +263,58 @@ def test_a_captured_step_on_two_branches():
         assert_within(out, want, tol, f"replay {i}")
     assert torch.equal(dense[0][:2], dense_rows(cache, table[0], 102)[0][:, 100:].transpose(0, 1).bfloat16())
     g.gdn_check_device_errors()
+
+
+def test_threads_that_share_a_stream():
+    """Calls from several threads on one stream, whose kernels interleave there: no call works in another's memory."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(11)
+    hq, hkv, D, page = 8, 2, 128, 32
+    q_lens, kv_lens = [40, 3], [3000, 900]
+    cases = []
+    for i in range(4):
+        cache, table = make_cache(g, gen, q_lens, kv_lens, hkv, page, D, bool(i & 1))
+        cases.append((cache, table, randn(gen, 43, hq, D)))
+    kv, cu = ints(kv_lens), cu_of(q_lens)
+    torch.cuda.synchronize()
+
+    def work(i):
+        cache, table, q = cases[i]
+        return [g.gdn_attn_prefill(q, cache, table, kv, cu, 0.08) for _ in range(30)]
+    with concurrent.futures.ThreadPoolExecutor(4) as pool:
+        outs = list(pool.map(work, range(4)))
+    torch.cuda.synchronize()
+    g.gdn_check_device_errors()
+    for (cache, table, q), got in zip(cases, outs):
+        want, tol = attention(q, cache, table, q_lens, kv_lens, 0.08)
+        for o in got:
+            assert_within(o, want, tol, "thread")
+
+
+def test_two_graphs_replayed_at_once():
+    """Graphs captured without a workspace of the caller's have one each."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    hq, hkv, D, page = 16, 2, 256, 64
+    q_lens, kv_lens = [50], [6000]
+    graphs = []
+    for i in range(2):
+        cache, table = make_cache(g, gen, q_lens, kv_lens, hkv, page, D, False)
+        q, out = randn(gen, 50, hq, D), torch.empty(50, hq, D, dtype=torch.bfloat16, device=DEV)
+        kv, cu = ints(kv_lens), cu_of(q_lens)
+        g.gdn_attn_prefill(q, cache, table, kv, cu, 0.06, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            g.gdn_attn_prefill(q, cache, table, kv, cu, 0.06, out=out)
+        graphs.append((graph, torch.cuda.Stream(), cache, table, q, out, kv, cu))
+    for _ in range(10):
+        for graph, stream, *_ in graphs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        g.gdn_attn_prefill(*[graphs[0][i] for i in (4, 2, 3, 6, 7)], 0.06)  # and a call beside them
+    torch.cuda.synchronize()
+    g.gdn_check_device_errors()
+    for _, _, cache, table, q, out, *_ in graphs:
+        want, tol = attention(q, cache, table, q_lens, kv_lens, 0.06)
+        assert_within(out, want, tol, "graph")
