@@ -49,6 +49,7 @@ struct BlockMeta {
 enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
 constexpr int kMeta = 8;         // blocks that the pages and scales are ahead
 constexpr float kWeight = 7.f;   // log2 of the factor on binary16 weights
+constexpr float kUnitMin = 0x1p-126f, kUnitMax = 0x1.fffffep127f;  // bounds of a score's unit
 
 template <int D, int kTiles, bool kE4M3>
 struct Cfg {
@@ -368,7 +369,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             if constexpr (kE4M3) {
               if (!await(bar.meta_full + 8 * (blk % kMeta), blk / kMeta & 1u)) break;
               ev = meta->ev;
-              unit *= meta->ku;
+              // A finite unit above zero: -inf (a masked score) times zero is NaN, and so is zero times infinity.  The
+              // unit of a row of zeros over keys of zeros is 2^-237; where the bound acts, scores are below 2^-108.
+              unit = fminf(fmaxf(unit * meta->ku, kUnitMin), kUnitMax);
             }
             float s[kCols], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
