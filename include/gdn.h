@@ -627,6 +627,7 @@ GDN_API size_t gdn_attn_workspace_size(const gdn_attn_geometry* geo);
  * too: gdn_attn_prepare first).  With p the token's position and j = 0 .. p:
  *   s_j = softmax_scale * q . k_j,   o = sum_j e^(s_j) v_j / sum_j e^(s_j)   (0 when p < 0),
  *   out = o, or o * sigmoid(z) where z is given; softmax_scale is positive, at most 1e38.
+ * A key or value that is not finite reaches the tokens that see its position, and no others.
  * Scores and sums are fp32 with a running maximum; the weights e^(s_j - max) are rounded to bf16
  * for the product with v.  An e4m3 cache is read as binary16, exactly; the queries (divided by a power of
  * two) and the weights (times the power of two of v_j) are rounded to binary16 with it.

@@ -13,9 +13,14 @@
 //
 // Warps: four a tile for the softmax; two that issue products (a tile's each, or with one tile one for
 // the scores and one for O), so that one's waiting does not idle the tensor cores; one that loads Q, K and
-// V by TMA, K and V into a ring of 32 KB stages; one that zeroes the value rows behind the last key (a
-// page's unused rows may hold anything, and 0 * NaN is not 0).  An e4m3 cache has four or eight warps
-// that widen its codes into the stages instead of the last two, and one that reads pages and scales ahead.
+// V by TMA, K and V into a ring of 32 KB stages; one that goes over the value rows that some row of the tile
+// does not see.  An e4m3 cache has four or eight warps that widen its codes into the stages instead of the
+// last two, and one that reads pages and scales ahead.
+//
+// A value that a row does not see has the weight 0 there, and 0 * NaN is not 0.  Value rows behind the last key
+// (a page's unused rows may hold anything) are zeroes in their stage, and so are infinities and NaN in rows that
+// some of the tile's tokens come before; the rows that do see those get them back at the segment's end
+// (add_odd_values), which costs time only where there are any.
 //
 // Work: the (tile, block) pairs of all sequences in one line, cut into one equal piece for each SM.  A
 // tile that a cut falls into leaves its parts (O, m, l) in the workspace for a second kernel to join,
@@ -44,9 +49,9 @@ struct BlockMeta {
   uint32_t kf[kBlock];  // a key's power of two relative to the block's largest, twice in binary16
   uint32_t vf[kBlock];  // the same of a value
   float ku, ev;         // the block's largest key scale times the softmax scale; log2 of its largest value scale
-  int have, flags;      // visible keys; kFirst, kLast: of a segment, kEnd: no more blocks
+  int have, flags;      // visible keys; kFirst, kLast: of a segment, kEnd: no more blocks; from kSeen on: keys that every row sees
 };
-enum : int { kFirst = 1, kLast = 2, kEnd = 4 };
+enum : int { kFirst = 1, kLast = 2, kEnd = 4, kSeen = 3 };
 constexpr int kMeta = 8;         // blocks that the pages and scales are ahead
 constexpr float kWeight = 7.f;   // log2 of the factor on binary16 weights
 constexpr float kUnitMin = 0x1p-126f, kUnitMax = 0x1.fffffep127f;  // bounds of a score's unit
@@ -69,8 +74,8 @@ struct Cfg {
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;  // barriers; alignment of the base
   static_assert(kSmem <= 232448, "shared memory");
   static_assert(kStages <= 6 && kRawStages <= 3 && kThreads <= 32 * 60, "places of the barriers and of the scan");
-  // of the four warps behind the softmax's: the products (two), Q, K and V by TMA, value rows behind the
-  // last key (e4m3: scales)
+  // of the four warps behind the softmax's: the products (two), Q, K and V by TMA, value rows that some row
+  // does not see (e4m3: scales)
   static constexpr int kMma0 = kSoftWarps, kMma1 = kSoftWarps + 1, kLoad = kSoftWarps + 2, kTail = kSoftWarps + 3;
   // Scores that a softmax warp holds at a time; the rest of a step's are read twice.  Few registers, and
   // short code for the instruction cache that warps of several kinds share: 32 beat 128 by 2 % at D = 256
@@ -191,6 +196,59 @@ __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+constexpr uint32_t kInfBf16 = 0x7F807F80u;  // two magnitudes from here on are not finite
+__device__ __forceinline__ uint32_t top_bf16(const uint4& x) {  // the largest of the even, of the odd magnitudes
+  return __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+}
+// Eight bf16 values, or 16 e4m3 codes, with those that are not finite as zeroes (codes: whether there were any).
+__device__ __forceinline__ uint4 zero_odd_bf16(const uint4& x) {
+  return make_uint4(x.x & ~__vcmpgeu2(x.x & 0x7FFF7FFFu, kInfBf16), x.y & ~__vcmpgeu2(x.y & 0x7FFF7FFFu, kInfBf16),
+                    x.z & ~__vcmpgeu2(x.z & 0x7FFF7FFFu, kInfBf16), x.w & ~__vcmpgeu2(x.w & 0x7FFF7FFFu, kInfBf16));
+}
+__device__ __forceinline__ bool zero_odd_e4m3(uint4& x) {
+  const uint32_t odd[4] = {__vcmpeq4(x.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu), __vcmpeq4(x.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu),
+                           __vcmpeq4(x.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu), __vcmpeq4(x.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu)};
+  x = make_uint4(x.x & ~odd[0], x.y & ~odd[1], x.z & ~odd[2], x.w & ~odd[3]);
+  return (odd[0] | odd[1] | odd[2] | odd[3]) != 0;
+}
+
+// O of this warp's 32 rows plus the infinities and NaN among the values of keys key0 .. key1 - 1 of sequence n, up
+// to each row's last one (any positive weight leaves them what they are).
+template <int D, bool kE4M3>
+__device__ __forceinline__ void add_odd_values(const AttnParams& p, uint32_t t_o, int n, int hk, int key0, int key1, int last) {
+  key1 = min(key1, __reduce_max_sync(0xFFFFFFFFu, last) + 1);
+  const int shift = p.cache.page_shift;
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    float o[16];
+    tmem_ld16(t_o + c, o);
+#pragma unroll 1
+    for (int key = key0; key < key1; ++key) {
+      int id = p.cache.table[(long)n * p.cache.max_pages + (key >> shift)];
+      if ((unsigned)id >= (unsigned)p.cache.num_pages) id = 0;
+      const long row = (((long)id * p.Hkv + hk) << shift) + (key & ((1 << shift) - 1));
+      if (key > last) continue;
+      if constexpr (kE4M3) {
+        const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.cache.v) + row * D + c);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if ((w[i >> 2] >> (8 * (i & 3)) & 0x7Fu) == 0x7Fu) o[i] = __uint_as_float(0x7FFFFFFFu);
+      } else {
+        const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache.v) + row * D + c);
+        const uint4 x = at[0], y = at[1];
+        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t v = i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16;
+          if ((v & 0x7F800000u) == 0x7F800000u) o[i] += __uint_as_float(v);
+        }
+      }
+    }
+    tmem_st16(t_o + c, o);
+  }
+}
+
 template <int D, int kTiles, bool kE4M3>
 __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams p) {
   using C = Cfg<D, kTiles, kE4M3>;
@@ -203,6 +261,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 59);
+  volatile uint32_t* odd_seen = tmem_slot + 1;  // set where a value was zeroed that some row sees, and not cleared
   WalkStart* start = reinterpret_cast<WalkStart*>(bars + 60);
   long* scan = reinterpret_cast<long*>(bars + 66);
   const uint32_t b0 = smem_u32(bars);
@@ -240,6 +299,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
     prefetch_tensormap(&p.tmap_v);
     prefetch_tensormap(&p.tmap_q);
     start->left = 0;
+    *odd_seen = 0;
   }
   if (warp == 0) tmem_alloc(smem_u32(tmem_slot), 512);
   await_grid();
@@ -310,7 +370,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
 #pragma unroll 2
           for (int c = 0; c < D / 8; ++c) {
             const uint4 x = *at(c);
-            two = __vmaxu2(two, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+            two = __vmaxu2(two, top_bf16(x));
           }
           uint32_t top = max(two & 0xFFFFu, two >> 16);
           if (top >= 0x7F80u) {  // an infinity or NaN among them
@@ -458,6 +518,19 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         if (!ok) break;
         if (!await_pv(n_pv - 1)) break;
         tc_fence_after();
+        if (busy && __any_sync(0xFFFFFFFFu, *odd_seen != 0)) {
+          // bf16: the sequence and the tile's first position from values that the loop holds anyway; kept for this
+          // through the loop they cost it registers (2048 tokens after 30001: 707 us, 716 with them kept).  e4m3 the
+          // other way round: the kernel is short of instruction cache (8192 prompt tokens: 646 us, 689 with the lookup).
+          int n = seg.n, key0 = seg.pos0 + 1;
+          if constexpr (!kE4M3) {
+            int first, len;
+            // (lane 0 has a row; below 0: bad cu_seqlens, whose rows are unspecified)
+            n = max(attn_seq_of(p.cu, p.N, p.T, row0 + __shfl_sync(0xFFFFFFFFu, tok_in, 0), first, len), 0);
+            key0 = last - sub * p.sub - tok_in + 1;
+          }
+          add_odd_values<D, kE4M3>(p, t_o, n, hk, max(key0, seg.j0 * kBlock), seg.j1 * kBlock, mine ? last : -1);
+        }
         const bool whole = seg.j0 == 0 && seg.j1 == seg.nb;
         // O in units of 2^m (half the exponent at a time where both ends of the range meet)
         const float unit_o = kE4M3 && m > -INFINITY ? ex2_approx(0.5f * (r - m - kWeight)) : 1.f;
@@ -596,9 +669,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
       const BlockMeta& meta = metas[place];
       const uint32_t* scale = value ? meta.vf : meta.kf;
       const int row0 = wide ? row_wide : row_narrow, base = wide ? part * 64 : 0, stride = wide ? 8 : 16;
-      // rows behind the last visible key read that one (their scores are masked, their weights 0, and what
-      // lies in them may be NaN)
-      const int last = min(meta.have - 1 - base, 127);
+      // rows behind the last visible key become zeroes (their scores are masked, their weights 0, and what lies
+      // in them may be NaN), and so do NaN among values that some row does not see
+      const int last = min(meta.have - 1 - base, 127), seen = (meta.flags >> kSeen) - base;
       const uint8_t* from = sm + C::kOffRaw + raw.i * kRaw + (wide ? blk_wide * 4096 : blk_narrow * 8192) + piece * 16;
       uint8_t* to = sm + C::kOffStage + ring.i * kStage + (wide ? to_wide : to_narrow);
       const int other = wide ? other_wide : other_narrow;
@@ -608,7 +681,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         *reinterpret_cast<uint4*>(at) = make_uint4(mul_half2(a.x, f), mul_half2(a.y, f), mul_half2(b.x, f), mul_half2(b.y, f));
         *reinterpret_cast<uint4*>(at + other) = make_uint4(mul_half2(c.x, f), mul_half2(c.y, f), mul_half2(e.x, f), mul_half2(e.y, f));
       };
-      if (last >= 127 - base) {
+      if (value ? seen >= (wide ? 64 : 128) : last >= 127) {  // (keys have base 0)
         // Short loops: the kernel's roles share the instruction caches (D = 256: 253 us for the chunks of eight
         // prompts, 261 with one unit a pass, 299 with four; two tiles: 640 us for 8192 tokens, 746 with four)
 #pragma unroll(kTiles == 2 ? 1 : 2)
@@ -616,9 +689,13 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           widen(u, *reinterpret_cast<const uint4*>(from + (row0 + u * stride) * 64), scale[base + row0 + u * stride]);
       } else {
 #pragma unroll 1
-        for (int u = 0; u < kUnits; ++u)  // (zero: a part without any visible key)
-          widen(u, last >= 0 ? *reinterpret_cast<const uint4*>(from + min(row0 + u * stride, last) * 64) : make_uint4(0, 0, 0, 0),
-                scale[base + row0 + u * stride]);
+        for (int u = 0; u < kUnits; ++u) {
+          const int row = row0 + u * stride;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (row <= last) x = *reinterpret_cast<const uint4*>(from + row * 64);
+          if (value && row >= seen && zero_odd_e4m3(x)) *odd_seen = 1;
+          widen(u, x, scale[base + row]);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -804,7 +881,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           m.ku = e8m0_value(kt) * p.scale_log2;
           m.ev = (float)((int)vt - 127);
           m.have = have;
-          m.flags = (j == seg.j0 ? kFirst : 0) | (j + 1 == seg.j1 ? kLast : 0);
+          m.flags = (j == seg.j0 ? kFirst : 0) | (j + 1 == seg.j1 ? kLast : 0) | min(max(seg.pos0 + 1 - j * kBlock, 0), kBlock) << kSeen;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar.meta_full + 8 * (blk % kMeta));
@@ -834,7 +911,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         auto load = [&](const CUtensorMap* map, int key0, int rows, int d0, int nd, bool value) {
           if (!await(bar_empty + 8 * ring.i, ring.pass ^ 1u)) return;
           const int boxes = rows >> box_shift, have = min(max((keys - key0 + box - 1) >> box_shift, 0), boxes);
-          const bool tail = !kE4M3 && value && key0 + rows > keys;  // the warp that zeroes the rest passes it on
+          const bool tail = !kE4M3 && value && key0 + rows > seg.pos0 + 1;  // the warp that goes over it passes it on
           const uint32_t to = (tail ? bar.tail : bar_full) + 8 * ring.i, bit = 1u << ring.i;
           used |= bit;
           tails = tail ? tails | bit : tails & ~bit;
@@ -901,35 +978,55 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         if (q_used >> t & 1u) mbar_wait(bar.q_full + 8 * t, (q_pass >> t & 1u) ^ 1u, kWaitLimit);
     }
   } else if (warp == C::kTail) {
-    // ------------------------------------------------------------------ value rows behind the last key
+    // ------------------------------------------------------------------ value rows that some row does not see
     Ring<kStages> ring;
     uint32_t used[kStages] = {};  // parity of each stage's tail barrier
     while (ok && walk.next(p, step, seg)) {
-      if (seg.keys > 0) {
-        const long stages = (long)(seg.j1 - seg.j0) * 2 * kParts;
-        ring.skip(stages - kParts);
-        for (int part = 0; part < kParts; ++part, ring.step()) {
-          constexpr int kRows = 128 / kParts;
-          const int key0 = (seg.j1 - 1) * kBlock + part * kRows;
-          const int have = max(seg.keys - key0, 0);
-          if (have >= kRows) continue;
+      if (seg.keys <= 0) continue;
+      constexpr int kRows = 128 / kParts;
+      const int n = seg.j1 - seg.j0, seen = seg.pos0 + 1;  // keys that every row sees
+      int at = 0;                                         // stages of the segment passed
+      auto pass = [&](int to) {
+        ring.skip(to - at);
+        at = to;
+      };
+      for (int i = max((max(seen, 0) >> 7) - seg.j0, 0); i < n && ok; ++i) {
+        pass((kTiles == 1 && i + 1 < n ? 2 * i + 2 : 2 * i + 1) * kParts);
+        for (int part = 0; part < kParts; ++part, pass(at + 1)) {
+          const int key0 = (seg.j0 + i) * kBlock + part * kRows;
+          if (key0 + kRows <= seen) continue;
+          const int have = min(max(seg.keys - key0, 0), kRows), from = min(max(seen - key0, 0), have);
           uint32_t par = 0;
 #pragma unroll
-          for (int i = 0; i < kStages; ++i)
-            if (i == ring.i) {
-              par = used[i];
-              used[i] ^= 1u;
+          for (int k = 0; k < kStages; ++k)
+            if (k == ring.i) {
+              par = used[k];
+              used[k] ^= 1u;
             }
           if (!await(bar.tail + 8 * ring.i, par)) break;
           uint8_t* st = sm + C::kOffStage + ring.i * kStage;
+          constexpr int kCol = D == 256 ? 512 : 1024;  // 16-byte pieces of a 64-value column
+          uint4* col = reinterpret_cast<uint4*>(st);
           for (int d = 0; d < D / 64; ++d)
-            for (int i = have * 8 + lane; i < kRows * 8; i += 32)
-              *reinterpret_cast<uint4*>(st + d * (D == 256 ? 8192 : 16384) + i * 16) = make_uint4(0, 0, 0, 0);
+            for (int k = have * 8 + lane; k < kRows * 8; k += 32) col[d * kCol + k] = make_uint4(0, 0, 0, 0);
+          for (int k0 = from * 8 + lane; k0 < have * 8; k0 += 32) {
+            uint4 x[D / 64];
+            uint32_t top = 0;
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d) x[d] = col[d * kCol + k0];
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d) top = __vmaxu2(top, top_bf16(x[d]));
+            if (__vcmpgeu2(top, kInfBf16) == 0) continue;
+#pragma unroll
+            for (int d = 0; d < D / 64; ++d) col[d * kCol + k0] = zero_odd_bf16(x[d]);
+            *odd_seen = 1;
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar.full + 8 * ring.i);
         }
       }
+      pass(2 * n * kParts);
     }
   }
   finish();

@@ -1,5 +1,8 @@
-"""The paged-cache attention layer at values where its forms differ: rows of zeros and of tiny values."""
+"""The paged-cache attention layer at values where its forms differ: rows of zeros and of tiny values,
+values that are not finite behind a token's own position."""
 from __future__ import annotations
+
+import math
 
 import pytest
 import torch
@@ -61,3 +64,89 @@ def test_single_rows_of_zeros_among_others(q_lens, kv_lens, hq, hkv, D):
     g.gdn_check_device_errors()
     want, tol = attention(q, cache, table, q_lens, kv_lens, D ** -0.5)
     assert_within(out, want, tol, "attention")
+
+
+# ------------------------------------------------------------------------------------ behind a token's own position
+
+def seen_marks(bad, q_lens, kv_lens, hq):
+    """Whether a row sees a marked value: bad (a list, for each sequence [Hkv, positions, D] bool) -> [T, Hq, D]."""
+    rows = []
+    for b, ql, kv in zip(bad, q_lens, kv_lens):
+        upto = b.long().cumsum(1)  # marked values among the first positions
+        pos = torch.arange(kv - ql, kv, device=DEV)
+        n = torch.where((pos >= 0)[None, :, None], upto[:, pos.clamp(min=0)], torch.zeros((), dtype=torch.long, device=DEV))
+        rows.append((n > 0).repeat_interleave(hq // b.shape[0], 0).transpose(0, 1))
+    return torch.cat(rows)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv,D", FORMS + [([9, 260], [4, 257], 6, 2, 128), ([100], [2500], 64, 1, 128)])
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(q_lens, kv_lens, hq, hkv, D, page, e4m3):
+    """Infinities and NaN in value rows of new tokens: the tokens before them stay as they are, the others have them."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(22)
+    cache, table = make_cache(g, gen, q_lens, kv_lens, hkv, page, D, e4m3)
+    clean = g.KVCache(cache.k, cache.v.clone(), cache.k_scale, cache.v_scale)
+    marks = []  # of NaN, of +inf, of -inf (an e4m3 code has NaN alone)
+    for n, (ql, kv) in enumerate(zip(q_lens, kv_lens)):
+        m = torch.zeros(3, hkv, kv, D, dtype=torch.bool, device=DEV)
+        lo = max(kv - ql, 0)
+        for i, p in enumerate(sorted({lo, lo + 1, lo + (kv - lo) // 3, lo + (kv - lo) // 2, lo + 2 * (kv - lo) // 3, kv - 2, kv - 1} - {-1})):
+            m[0 if e4m3 else i % 3, i % hkv, min(p, kv - 1), 7 * i + 1::D // 2] = True
+        m[0, 0, kv - 1, 100] = True
+        if kv - ql > 200:
+            m[0, 0, 50, 5] = True  # before every new token
+        marks.append(m)
+        for p in m.any(0).any(0).any(-1).nonzero().flatten().tolist():
+            row = cache.v[int(table[n, p // page]), :, p % page]
+            row, at = (row.view(torch.uint8), m[:, :, p]) if e4m3 else (row, m[:, :, p])
+            for value, w in zip((0x7F,) if e4m3 else (math.nan, math.inf, -math.inf), at):
+                row[w] = value
+    q = randn(gen, sum(q_lens), hq, D) * 0.3
+    out = call(g, q, cache, table, q_lens, kv_lens, D ** -0.5).double()
+    g.gdn_check_device_errors()
+    nan, up, down = (seen_marks([m[i] for m in marks], q_lens, kv_lens, hq) for i in range(3))
+    nan = nan | (up & down)
+    assert torch.equal(torch.isnan(out), nan)
+    assert torch.equal(torch.isposinf(out), up & ~nan) and torch.equal(torch.isneginf(out), down & ~nan)
+    # the rest: as if those values were not there (their rows' other values and weights are)
+    for n, m in enumerate(marks):
+        for p in m.any(0).any(0).any(-1).nonzero().flatten().tolist():
+            row = clean.v[int(table[n, p // page]), :, p % page]
+            (row.view(torch.uint8) if e4m3 else row)[m[:, :, p].any(0)] = 0
+    want, tol = attention(q, clean, table, q_lens, kv_lens, D ** -0.5)
+    fine = torch.isfinite(out)
+    assert bool(((out - want).abs() <= tol)[fine].all())
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_gated_row_beside_values_that_are_not_finite(e4m3):
+    """With a gate, and rows cut into parts: only the last token has the NaN."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(23)
+    for q_lens, kv_lens, hq, hkv, D in (([20], [6000], 16, 2, 256), ([90], [9000], 8, 2, 128)):
+        cache, table = make_cache(g, gen, q_lens, kv_lens, hkv, 64, D, e4m3)
+        q, z = randn(gen, q_lens[0], hq, D), randn(gen, q_lens[0], hq, D)
+        want, tol = attention(q, cache, table, q_lens, kv_lens, D ** -0.5, z)
+        p = kv_lens[0] - 1
+        row = cache.v[int(table[0, p // 64]), :, p % 64]
+        row.copy_(torch.full(row.shape, math.nan, device=DEV).to(row.dtype))
+        out = g.gdn_attn_prefill(q, cache, table, ints(kv_lens), cu_of(q_lens), D ** -0.5, z=z)
+        g.gdn_check_device_errors()
+        assert bool(torch.isnan(out[-1]).all())
+        assert_within(out[:-1], want[:-1], tol[:-1], "attention")
+
+
+def test_values_that_are_not_finite_under_bad_cu_seqlens():
+    """Sequences that overlap and decrease: reported, whatever the values are."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(27)
+    cache, table = make_cache(g, gen, [4, 4, 4], [40, 40, 40], 2, 16, 128, False)
+    cache.v[:] = math.nan
+    q = randn(gen, 12, 8, 128)
+    for cu in ([0, 8, 3, 12], [0, 12, 2, 5], [0, -4, 6, 12], [5, 4, 12, 3]):
+        g.gdn_attn_prefill(q, cache, table, ints([40, 40, 40]), ints(cu), 0.1)
+        with pytest.raises(g.GdnError) as e:
+            g.gdn_check_device_errors()
+        assert e.value.status == 6
