@@ -629,8 +629,12 @@ GDN_API size_t gdn_attn_workspace_size(const gdn_attn_geometry* geo);
  *   out = o, or o * sigmoid(z) where z is given; softmax_scale is positive, at most 1e38.
  * A key or value that is not finite reaches the tokens that see its position, and no others.
  * Scores and sums are fp32 with a running maximum; the weights e^(s_j - max) are rounded to bf16
- * for the product with v.  An e4m3 cache is read as binary16, exactly; the queries (divided by a power of
- * two) and the weights (times the power of two of v_j) are rounded to binary16 with it.
+ * for the product with v.  Beside an e4m3 cache the matrix operands are binary16, which holds every code
+ * exactly: the queries are rounded to it (divided by a power of two), and the weights.  Few query heads and one
+ * token a sequence: the weights times the power of two of v_j, relative to the largest of 16 or 32 keys (2^-32
+ * of the largest value there is lost at most).  Otherwise: keys and values relative to the largest power of
+ * two of a block of 128; rows up to 2^22 below it are exact, and rows 2^32 or more below it count as zero
+ * (less than 2^-30 of the block's largest key or value).
  *   q          [total_tokens, Hq, D] bf16
  *   z          Hq heads of D bf16 for each token, head h of token t at z + t * z_token_stride +
  *              h * z_head_stride (elements, multiples of 8), or NULL

@@ -46,7 +46,7 @@ constexpr uint32_t kStage = 32768, kRaw = 16384;
 
 // e4m3: what the warps that widen the codes and those of the softmax need to know of a block of keys.
 struct BlockMeta {
-  uint32_t kf[kBlock];  // a key's power of two relative to the block's largest, twice in binary16
+  uint32_t kf[kBlock];  // a key's power of two relative to the block's largest, times 2^kWiden, twice in binary16
   uint32_t vf[kBlock];  // the same of a value
   float ku, ev;         // the block's largest key scale times the softmax scale; log2 of its largest value scale
   int have, flags;      // visible keys; kFirst, kLast: of a segment, kEnd: no more blocks; from kSeen on: keys that every row sees
@@ -54,6 +54,7 @@ struct BlockMeta {
 enum : int { kFirst = 1, kLast = 2, kEnd = 4, kSeen = 3 };
 constexpr int kMeta = 8;         // blocks that the pages and scales are ahead
 constexpr float kWeight = 7.f;   // log2 of the factor on binary16 weights
+constexpr int kWiden = 7;        // and of that on widened codes: 448 * 2^7 is the most that binary16 takes
 constexpr float kUnitMin = 0x1p-126f, kUnitMax = 0x1.fffffep127f;  // bounds of a score's unit
 
 template <int D, int kTiles, bool kE4M3>
@@ -186,7 +187,7 @@ __device__ __forceinline__ void tmem_st16_begin(uint32_t taddr, const float (&v)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// 2^e, e <= 0, twice in binary16 (0 below its range)
+// 2^e, e <= 15, twice in binary16 (0 below its range)
 __device__ __forceinline__ uint32_t half2_power(int e) {
   const uint32_t h = e >= -14 ? (uint32_t)(15 + e) << 10 : e >= -24 ? 1u << (e + 24) : 0u;
   return h | h << 16;
@@ -359,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(out)[c] = make_uint4(0, 0, 0, 0);
         continue;
       }
-      float row_unit = p.scale_log2;  // e4m3: the power of two the row was divided by
+      float row_unit = p.scale_log2;  // e4m3: the power of two the row was divided by, less the factor on the keys
       if (kE4M3 && rows > 0) {
         // Q becomes binary16 where it lies, each thread its own row, divided by the power of two of its largest
         // finite value (a thread's pieces of 16 bytes lie in other banks than its neighbours')
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
               y[k] = pack_half2(__uint_as_float(y[k] << 16) * inv, __uint_as_float(y[k] & 0xFFFF0000u) * inv);
             *at(c) = make_uint4(y[0], y[1], y[2], y[3]);
           }
-          row_unit = __uint_as_float((uint32_t)(127 + e) << 23);
+          row_unit = __uint_as_float((uint32_t)(127 + e) << 23) * (1.f / (1 << kWiden));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         }
         const bool whole = seg.j0 == 0 && seg.j1 == seg.nb;
         // O in units of 2^m (half the exponent at a time where both ends of the range meet)
-        const float unit_o = kE4M3 && m > -INFINITY ? ex2_approx(0.5f * (r - m - kWeight)) : 1.f;
+        const float unit_o = kE4M3 && m > -INFINITY ? ex2_approx(0.5f * (r - m - kWeight - kWiden)) : 1.f;
         if (busy) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const uint16_t* z = p.z.p + (long)(row0 + tok_in) * p.z.token + (long)(hk * p.G + g) * p.z.head;
@@ -616,9 +617,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
   if (kE4M3 && warp >= C::kSoftWarps + 4) {
     // ------------------------------------------------------------------ e4m3: codes -> binary16 stages
     // Four warps a stage, in groups that take the stages in turn: a stage's codes are widened (exactly, two
-    // an instruction), multiplied by their row's power of two relative to the block's largest, and written
-    // in the layout that the TMA gives a bf16 cache.  (A product loses what lies below binary16: less than
-    // 2^-32 of the block's largest value.)
+    // an instruction), multiplied by 2^kWiden and their row's power of two relative to the block's largest, and
+    // written in the layout that the TMA gives a bf16 cache.  Products are exact for rows at most 2^22 below the
+    // block's largest; down to 2^31 below they lose at most 2^-39 of its largest value, and rows further below are
+    // zeroes, less than 2^-30 of it.
     constexpr int kGroups = C::kConvGroups > 0 ? C::kConvGroups : 1, kUnits = 8;
     constexpr int kRawStages = C::kRawStages > 0 ? C::kRawStages : 1;
     const int cw = warp & 3, group = (warp - (C::kSoftWarps + 4)) >> 2;
@@ -871,8 +873,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool in = lane * 4 + i < have;
-          kf[i] = in ? half2_power((int)((k4 >> (8 * i)) & 255u) - (int)kt) : 0u;
-          vf[i] = in ? half2_power((int)((v4 >> (8 * i)) & 255u) - (int)vt) : 0u;
+          kf[i] = in ? half2_power((int)((k4 >> (8 * i)) & 255u) - (int)kt + kWiden) : 0u;
+          vf[i] = in ? half2_power((int)((v4 >> (8 * i)) & 255u) - (int)vt + kWiden) : 0u;
         }
         BlockMeta& m = metas[blk % kMeta];
         reinterpret_cast<uint4*>(m.kf)[lane] = make_uint4(kf[0], kf[1], kf[2], kf[3]);

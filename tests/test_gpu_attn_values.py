@@ -1,5 +1,5 @@
 """The paged-cache attention layer at values where its forms differ: rows of zeros and of tiny values,
-values that are not finite behind a token's own position."""
+values that are not finite behind a token's own position, rows of very different sizes in one block."""
 from __future__ import annotations
 
 import math
@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from tests.attn_reference import DEV, assert_within, attention
+from tests.attn_reference import DEV, assert_within, attention, dense_rows
 from tests.gpu_common import lib
 from tests.test_gpu_attn import cu_of, ints, make_cache
 from tests.test_gpu_attn_edges import call, randn
@@ -150,3 +150,38 @@ def test_values_that_are_not_finite_under_bad_cu_seqlens():
         with pytest.raises(g.GdnError) as e:
             g.gdn_check_device_errors()
         assert e.value.status == 6
+
+
+# ------------------------------------------------------------------------------------ rows of very different sizes
+
+@pytest.mark.parametrize("apart", [10, 20, 24, 28])
+@pytest.mark.parametrize("hq,hkv,D,q_len", [(8, 2, 128, 120), (2, 2, 128, 120), (4, 1, 256, 120)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_rows_do_not_go_by_the_size_of_later_ones(hq, hkv, D, q_len, e4m3, apart):
+    """Keys and values of the first 60 positions 2^-apart of those behind them in the same block: the first rows come
+    out as they would alone (the error counted from what they see)."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(24)
+    k, v, q = randn(gen, q_len, hkv, D), randn(gen, q_len, hkv, D), randn(gen, q_len, hq, D)
+    half = 2.0 ** (apart // 2)
+    k[:60] /= half
+    v[:60] /= half
+    k[60:] *= half
+    v[60:] *= half
+    q[:60] *= half
+    q[60:] /= half
+    cache, table = written(g, k, v, [q_len], [q_len], 32, e4m3)
+    out = g.gdn_attn_prefill(q, cache, table, ints([q_len]), ints([0, q_len]), D ** -0.5)
+    g.gdn_check_device_errors()
+    want, tol = attention(q[:60], cache, table, [60], [60], D ** -0.5)
+    if e4m3 and apart > 20:
+        # Widened codes carry 2^7 and their row's power of two relative to the block's largest.  The largest row's top
+        # code is 224 or more, 2^14.8 with the factor; rows more than 2^22 below round in steps of 2^-24, by 2^-25 at most:
+        # less than 2^-39 of the block's largest value, and as much of its largest key in every term of a score (a
+        # relative change of a weight, in numerator and denominator), then the rounding of the result.
+        kd, vd = dense_rows(cache, table[0], q_len)
+        rel = 2.0 ** -39 * D ** -0.5 * kd.abs().max() * q[:60].double().abs().sum(-1, keepdim=True)
+        tol = tol + (1 + 2.0 ** -8) * (2.0 ** -39 * vd.abs().max() + 2 * rel * vd[:, :60].abs().max())
+    assert_within(out[:60], want, tol, "first rows")
+    want, tol = attention(q, cache, table, [q_len], [q_len], D ** -0.5)
+    assert_within(out[60:], want[60:], tol[60:], "last rows")
