@@ -161,7 +161,10 @@ __global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_co
   long place = -1;  // head-0 row of the position in the pool
   bool bad = false;
   if (pos >= 0) place = cache_row(p.cache, p.Hkv, seq, pos, bad);
-  if (bad) raise_error(p.err, kErrDeviceArgument);
+  if (bad) {  // nothing of the token is written, its queries neither
+    raise_error(p.err, kErrDeviceArgument);
+    return;
+  }
 
   // the token's cosines and sines
   for (int j = lane; j < half; j += 32) {

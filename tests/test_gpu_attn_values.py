@@ -1,5 +1,6 @@
 """The paged-cache attention layer at values where its forms differ: rows of zeros and of tiny values,
-values that are not finite behind a token's own position, rows of very different sizes in one block."""
+values that are not finite behind a token's own position, rows of very different sizes in one block,
+tokens whose page does not exist."""
 from __future__ import annotations
 
 import math
@@ -185,3 +186,26 @@ def test_rows_do_not_go_by_the_size_of_later_ones(hq, hkv, D, q_len, e4m3, apart
     assert_within(out[:60], want, tol, "first rows")
     want, tol = attention(q, cache, table, [q_len], [q_len], D ** -0.5)
     assert_within(out[60:], want[60:], tol[60:], "last rows")
+
+
+# ------------------------------------------------------------------------------------ faults
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_nothing_is_written_for_a_token_without_a_page(e4m3, in_place):
+    """A page outside the pool, a length beyond the table: the queries of those tokens are left as well."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(26)
+    cache, table = make_cache(g, gen, [1] * 4, [40] * 4, 2, 16, 128, e4m3)
+    q, k, v = randn(gen, 4, 4, 128), randn(gen, 4, 2, 128), randn(gen, 4, 2, 128)
+    w = torch.full((128,), 2.0, dtype=torch.bfloat16, device=DEV)
+    good = g.gdn_attn_prepare(q, k, v, cache, table, ints([40] * 4), q_norm_w=w)
+    g.gdn_check_device_errors()
+    table[1, 2], table[2, 2] = -1, cache.k.shape[0]
+    q_out = q.clone() if in_place else torch.full_like(q, 7.0)
+    before = q_out.clone()
+    g.gdn_attn_prepare(q_out if in_place else q, k, v, cache, table, ints([40, 40, 40, 16 * table.shape[1] + 1]), q_norm_w=w, q_out=q_out)
+    with pytest.raises(g.GdnError) as e:
+        g.gdn_check_device_errors()
+    assert e.value.status == 6
+    assert torch.equal(q_out[0], good[0]) and torch.equal(q_out[1:], before[1:])
