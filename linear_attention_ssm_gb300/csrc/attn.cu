@@ -146,14 +146,6 @@ struct Ring {
   }
 };
 
-// Loads that stay where they are written: the compiler may otherwise sink a read-only load to its use,
-// three stages later.
-__device__ __forceinline__ uint32_t ld_ahead4(const void* p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
-}
-
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -545,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           const bool gated = whole && mine && p.z.p;
           auto gate = [&](int c) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) zz[k] = gated ? __ldg(reinterpret_cast<const uint4*>(z + c + 8 * k)) : make_uint4(0, 0, 0, 0);
+            for (int k = 0; k < 4; ++k) zz[k] = gated ? *reinterpret_cast<const uint4*>(z + c + 8 * k) : make_uint4(0, 0, 0, 0);
           };
           gate(0);
 #pragma unroll 1
@@ -911,8 +903,10 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         // One stage: `rows` keys from key0 on (those below `keys`, by whole boxes), nd columns of 64 values
         // from column d0 on.
         auto load = [&](const CUtensorMap* map, int key0, int rows, int d0, int nd, bool value) {
-          if (!await(bar_empty + 8 * ring.i, ring.pass ^ 1u)) return;
           const int boxes = rows >> box_shift, have = min(max((keys - key0 + box - 1) >> box_shift, 0), boxes);
+          const int key = key0 + (lane << box_shift);
+          int id = lane < have ? (int)ld_ahead4(table + (key >> p.cache.page_shift)) : 0;  // its latency passes in the wait
+          if (!await(bar_empty + 8 * ring.i, ring.pass ^ 1u)) return;
           const bool tail = !kE4M3 && value && key0 + rows > seg.pos0 + 1;  // the warp that goes over it passes it on
           const uint32_t to = (tail ? bar.tail : bar_full) + 8 * ring.i, bit = 1u << ring.i;
           used |= bit;
@@ -920,8 +914,6 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
           if (tail) tail_par ^= bit;
           int y = 0;
           if (lane < have) {
-            const int key = key0 + (lane << box_shift);
-            int id = __ldg(table + (key >> p.cache.page_shift));
             if ((unsigned)id >= (unsigned)p.cache.num_pages) {
               raise_error(p.err, kErrDeviceArgument);
               id = 0;
@@ -1094,11 +1086,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
       if (!some || way != 0 || !p.z.p) continue;
       const uint16_t* z = p.z.p + r * p.z.token + h * p.z.head + (col + v) * 4;
       if constexpr (kVec > 1) {
-        const uint4 y = __ldg(reinterpret_cast<const uint4*>(z));
+        const uint4 y = *reinterpret_cast<const uint4*>(z);
         zz[v] = make_uint2(y.x, y.y);
         zz[v + 1] = make_uint2(y.z, y.w);
       } else {
-        zz[v] = __ldg(reinterpret_cast<const uint2*>(z));
+        zz[v] = *reinterpret_cast<const uint2*>(z);
       }
     }
     float m = -INFINITY, l = 0.f;
@@ -1122,11 +1114,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         const bool in = some && k0 + u * ways < parts;
         const long slot = s_slot[in ? k0 + u * ways : 0];
         const float4* part = p.part + slot * (long)(kPartBytes / sizeof(float4));
-        ml[u] = in ? __ldcg(p.ml + slot * 256 + sub * 128 + row) : make_float2(-INFINITY, 0.f);
+        ml[u] = in ? ld_l2(p.ml + slot * 256 + sub * 128 + row) : make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int v = 0; v < kVec; ++v)
           x[u][v] = !in ? make_float4(0.f, 0.f, 0.f, 0.f)
-                        : __ldcg(kTiles > 0 ? part + (sub * (D / 4) + col + v) * 128 + row : part + row * (D / 4) + col);
+                        : ld_l2(kTiles > 0 ? part + (sub * (D / 4) + col + v) * 128 + row : part + row * (D / 4) + col);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) add(ml[u], x[u]);

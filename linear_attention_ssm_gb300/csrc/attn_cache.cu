@@ -48,7 +48,7 @@ __device__ __forceinline__ float turns_of(int p, float hi, float lo) {
 
 // Row of the cache of position pos: its page's head-0 row, or -1.
 __device__ __forceinline__ long cache_row(const PagedCache& c, int Hkv, int seq, int pos, bool& bad) {
-  const int page = __ldg(c.table + (long)seq * c.max_pages + (pos >> c.page_shift));
+  const int page = c.table[(long)seq * c.max_pages + (pos >> c.page_shift)];
   if ((unsigned)page >= (unsigned)c.num_pages) {
     bad = true;
     return -1;
@@ -114,7 +114,7 @@ __device__ __forceinline__ void each_head(const HeadRows& rows, long t, int head
     for (int u = 0; u < kUnroll; ++u) {
       const int h = h0 + u * step * kAt + mine;
       raw[u] = make_uint4(0, 0, 0, 0);
-      if (h < heads) raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + h * rows.head));
+      if (h < heads) raw[u] = ld_once(src + h * rows.head);
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_co
   // turns of one position, in two parts: the only fp64 arithmetic, once for the CTA's tokens
   const int rot = p.rope.rot, half = rot / 2;
   for (int j = threadIdx.x; j < half; j += 32 * kWarps) {
-    const double f = __ldg(p.rope.freqs + j) * 0.15915494309189533577;
+    const double f = p.rope.freqs[j] * 0.15915494309189533577;
     const float hi = (float)f;
     s_turns[j] = make_float2(hi, (float)(f - (double)hi));
   }
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_co
     if (seq == -2) raise_error(p.err, kErrDeviceArgument);
     return;
   }
-  const int kv = __ldg(p.kv_lens + seq);
+  const int kv = p.kv_lens[seq];
   if (kv < 0 || kv > min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) {
     raise_error(p.err, kErrDeviceArgument);
     return;
@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_co
     {
       uint4 own = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), pair = own;  // bf16 ones
       if (w) {
-        own = __ldg(reinterpret_cast<const uint4*>(w) + sub);
-        pair = p.rope.interleaved ? own : __ldg(reinterpret_cast<const uint4*>(w) + (partner % kLanes));
+        own = reinterpret_cast<const uint4*>(w)[sub];
+        pair = p.rope.interleaved ? own : reinterpret_cast<const uint4*>(w)[partner % kLanes];
       }
       const uint32_t wo[4] = {own.x, own.y, own.z, own.w}, wp[4] = {pair.x, pair.y, pair.z, pair.w};
 #pragma unroll
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const __grid_co
     bool bad = false;
     const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
     if (seq >= 0) {
-      const long pos = (p.starts ? (long)__ldg(p.starts + seq) : 0L) + (t - first);
+      const long pos = (p.starts ? (long)p.starts[seq] : 0L) + (t - first);
       if (pos < 0 || pos >= min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) bad = true;
       else place = cache_row(p.cache, p.Hkv, seq, (int)pos, bad);
     } else if (seq == -2) {
@@ -309,9 +309,8 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const __grid_co
       const long row = at + ((long)h << p.cache.page_shift);
       dst[u] = nullptr;
       if (s < steps && h < p.Hkv && at >= 0) {
-        raw[u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(is_k ? p.cache.k : p.cache.v) +
-                                                       row * (D * (kE4M3 ? 1 : 2))) + sub);
-        if constexpr (kE4M3) byte[u] = __ldg((is_k ? p.cache.k_scale : p.cache.v_scale) + row);
+        raw[u] = ld_once(static_cast<const uint8_t*>(is_k ? p.cache.k : p.cache.v) + row * (D * (kE4M3 ? 1 : 2)) + sub * 16);
+        if constexpr (kE4M3) byte[u] = (is_k ? p.cache.k_scale : p.cache.v_scale)[row];
         dst[u] = (is_k ? p.k_out : p.v_out) + ((t0 + tok) * p.Hkv + h) * D + sub * kVals;
       }
     }

@@ -18,12 +18,12 @@ __device__ __forceinline__ int attn_seq_of(const int32_t* cu, int N, int T, int 
   int lo = 0, hi = N;  // the last index with cu[index] <= t, if cu is sorted
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu + mid) <= t) lo = mid;
+    if (cu[mid] <= t) lo = mid;
     else hi = mid - 1;
   }
-  const int a = __ldg(cu + lo);
+  const int a = cu[lo];
   if (lo == N) return a >= 0 && a <= t ? -1 : -2;
-  const int b = __ldg(cu + lo + 1);
+  const int b = cu[lo + 1];
   if (a < 0 || t < a || t >= b || b > T) return -2;
   first = a;
   len = b - a;
@@ -32,6 +32,31 @@ __device__ __forceinline__ int attn_seq_of(const int32_t* cu, int N, int T, int 
 
 // 2^(b - 127) of an exponent byte
 __device__ __forceinline__ float e8m0_value(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x00400000u); }
+
+// Loads that stay where they are written: not sunk to their use (ld_ahead4), not ahead of await_grid (all).  None is
+// of the non-coherent kind, see launch_early.
+__device__ __forceinline__ uint32_t ld_ahead4(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// past L1
+__device__ __forceinline__ float4 ld_l2(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float2 ld_l2(const float2* p) {
+  float2 v;
+  asm volatile("ld.global.cg.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
 
 // 32 bytes of one thread (aligned to them): a whole sector
 __device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {
@@ -112,12 +137,12 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, bool rep
   SeqInfo s = {n, 1, 0};
   bool bad = false;
   if (p.cu) {
-    const int a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1);
+    const int a = p.cu[n], b = p.cu[n + 1];
     bad = a < 0 || b < a || b > p.T;
     s.first = a;
     s.len = bad ? 0 : b - a;
   }
-  s.kv = __ldg(p.kv_lens + n);
+  s.kv = p.kv_lens[n];
   if (s.kv < 0 || s.kv > ((long)p.cache.max_pages << p.cache.page_shift)) {
     bad = true;
     s.kv = 0;
@@ -325,8 +350,12 @@ constexpr float kLazy = 8.f;  // a row's maximum is raised when a score exceeds 
 constexpr int kMaxCtas = 160;  // SMs of the largest part of this architecture
 constexpr size_t kPartBytes = 131072;
 
-// A launch that need not wait for the end of the kernel before it in the stream: the kernel calls await_grid()
-// before it reads or writes memory.
+// A launch that need not wait for the end of the kernel before it in the stream: every thread of the kernel calls
+// await_grid() before it reads or writes memory, which waits for that kernel's end and its writes.  Those writes
+// happen during this kernel's lifetime, so it reads nothing that another kernel may have written (lengths, pages, cu_seqlens,
+// scales, gates, norms) through the non-coherent path (ld.global.nc, __ldg), which is for memory that stays as it
+// is for a kernel's whole life, and which a compiler may move past the wait; plain loads and volatile asm stay behind it.
+// No kernel here signals its dependents before it ends.
 template <typename... A>
 cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchAttribute early;

@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
     // page of this lane's rows of the stage that begins at key0
     auto page_id = [&](int key0, int lim) {
       return row < C::kKeys && key0 + row < lim
-                 ? (int)__ldg(p.cache.table + (long)seg.n * p.cache.max_pages + ((key0 + row) >> shift))
+                 ? p.cache.table[(long)seg.n * p.cache.max_pages + ((key0 + row) >> shift)]
                  : -1;
     };
     while (ok && walk.next(p, 1, seg)) {
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
         if (whole) {
           const long h = hk * p.G + row;
           if (p.z.p) {
-            const uint4 zz = __ldg(reinterpret_cast<const uint4*>(p.z.p + row0 * p.z.token + h * p.z.head + d));
+            const uint4 zz = *reinterpret_cast<const uint4*>(p.z.p + row0 * p.z.token + h * p.z.head + d);
             const uint32_t zr[4] = {zz.x, zz.y, zz.z, zz.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
