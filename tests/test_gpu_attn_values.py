@@ -1,6 +1,6 @@
 """The paged-cache attention layer at values where its forms differ: rows of zeros and of tiny values,
 values that are not finite behind a token's own position, rows of very different sizes in one block,
-tokens whose page does not exist."""
+tokens whose page does not exist, nine to sixteen query heads to a key head in the single-token form."""
 from __future__ import annotations
 
 import math
@@ -10,8 +10,8 @@ import torch
 
 from tests.attn_reference import DEV, assert_within, attention, dense_rows
 from tests.gpu_common import lib
-from tests.test_gpu_attn import cu_of, ints, make_cache
-from tests.test_gpu_attn_edges import call, randn
+from tests.test_gpu_attn import cu_of, ints, make_cache, run_attention
+from tests.test_gpu_attn_edges import call, poison, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -209,3 +209,32 @@ def test_nothing_is_written_for_a_token_without_a_page(e4m3, in_place):
         g.gdn_check_device_errors()
     assert e.value.status == 6
     assert torch.equal(q_out[0], good[0]) and torch.equal(q_out[1:], before[1:])
+
+
+# ------------------------------------------------------------------------------------ nine to sixteen heads to a key head
+
+@pytest.mark.parametrize("kv_lens", [[1], [0, 1, 127, 128, 129, 5000], [20000, 3], [700] * 33])
+@pytest.mark.parametrize("page,gate", [(16, True), (64, False), (128, True)])
+@pytest.mark.parametrize("hq,hkv,D", [(9, 1, 128), (24, 2, 128), (16, 1, 128), (15, 1, 128), (64, 4, 128), (17, 1, 128), (9, 1, 256), (32, 2, 256)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_decode_step_with_more_heads_to_a_key_head(kv_lens, page, gate, hq, hkv, D, e4m3):
+    """The single-token kernel's form of two columns of eight rows (D = 128, 9 to 16 heads), and both sides of the
+    borders where larger groups go to tiles."""
+    run_attention(lib(), [1] * len(kv_lens), kv_lens, hq, hkv, D, page, e4m3, gate, decode=True, seed=hq)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("hq", [9, 12, 16])
+def test_decode_step_with_more_heads_behind_the_last_key(hq, e4m3):
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(25)
+    kv_lens = [130, 1, 64, 33, 3000]
+    cache, table = make_cache(g, gen, [1] * 5, kv_lens, 1, 32, 128, e4m3)
+    poison(cache, table, kv_lens, 32)
+    q = randn(gen, 5, hq, 128) * 6
+    out = g.gdn_attn_decode_step(q, cache, table, ints(kv_lens), 0.09)
+    again = g.gdn_attn_decode_step(q, cache, table, ints(kv_lens), 0.09)
+    g.gdn_check_device_errors()
+    want, tol = attention(q, cache, table, [1] * 5, kv_lens, 0.09)
+    assert_within(out, want, tol, "attention")
+    assert torch.equal(out, again)
