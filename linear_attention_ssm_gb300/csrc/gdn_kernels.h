@@ -84,23 +84,21 @@ size_t chunk_prefill_workspace_bytes(int N);
 size_t split_workspace_bytes(int N, int T, int Hk, int Hv);
 
 cudaError_t device_sm_count(int* sms);
-// Tiled 2D tensor map of a row-major bf16 matrix (no swizzle, zero fill out of bounds).
-// a contiguous [outer][middle][inner] bf16 tensor with the 128-byte swizzle (box_inner 64)
-cudaError_t encode_bf16_3d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t middle, uint64_t outer,
-                                 uint32_t box_inner, uint32_t box_middle, uint32_t box_outer);
-// rows of bytes, without a swizzle, and with the 128-byte one (box_inner 128)
-cudaError_t encode_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
-                         uint32_t box_inner, uint32_t box_outer);
-cudaError_t encode_u8_2d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
-                               uint32_t box_inner, uint32_t box_outer);
-// as encode_bf16_2d with the 128-byte swizzle (box_inner 64)
-cudaError_t encode_bf16_2d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
-                                 uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+// Tiled tensor maps, zero fill out of bounds.  Row-major matrices without a swizzle:
 cudaError_t encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                           uint32_t box_inner, uint32_t box_outer);
-// Tiled 2D tensor map of a row-major fp32 matrix (no swizzle, zero fill out of bounds).
 cudaError_t encode_f32_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                          uint32_t box_inner, uint32_t box_outer);
+cudaError_t encode_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                         uint32_t box_inner, uint32_t box_outer);
+// with the 128-byte swizzle (box_inner 64 bf16 values, 128 bytes):
+cudaError_t encode_bf16_2d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                                 uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+cudaError_t encode_u8_2d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
+                               uint32_t box_inner, uint32_t box_outer);
+// of a contiguous [outer][middle][inner] tensor:
+cudaError_t encode_bf16_3d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t middle, uint64_t outer,
+                                 uint32_t box_inner, uint32_t box_middle, uint32_t box_outer);
 cudaError_t encode_chunk_tensor_maps(CUtensorMap* qkv_map, CUtensorMap* z_map, const uint16_t* qkv,
                                      const uint16_t* z, int T, int Hk, int Hv);
 cudaError_t launch_chunk_schedule(cudaStream_t stream, const int32_t* cu, int N, int32_t* order, unsigned* counter,
