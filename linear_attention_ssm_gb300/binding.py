@@ -859,8 +859,29 @@ def _batch_args(block_table, per_seq, name, cu_seqlens, T, device):
             _flat(per_seq, torch.int32, name, (N,), device), cu, pages)
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_PER_THREAD = 2  # cudaStreamPerThread: one handle for every thread, a queue of its own in each
+
+
+def _handle(device, stream):
+    """The CUDA handle of a call's stream (None: the device's current one)."""
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 def _empty(shape, dtype, device, stream):
-    """New memory for a call on `stream` (None: the current one), of that stream's part of the allocator."""
+    """New memory for a call on `stream` (None: the current one), of that stream's part of the allocator.
+
+    The allocator knows a stream by its handle.  That is no queue for the per-thread stream: its memory comes from the
+    default stream, with which it is ordered, and goes back when what this thread has queued so far is done.  A stream
+    made elsewhere has to be idle before it is destroyed, since its handle may return as another stream's.
+    """
+    if _handle(device, stream) == _PER_THREAD and not torch.cuda.is_current_stream_capturing():
+        with torch.cuda.stream(torch.cuda.default_stream(device)):
+            t = torch.empty(shape, dtype=dtype, device=device)
+        t.record_stream(torch.cuda.ExternalStream(_PER_THREAD, device=device))
+        return t
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
@@ -869,26 +890,25 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_spare_workspaces = {}  # (device, stream): the attention workspace of the last call there
+_kept_workspaces = {}  # by device: the attention workspace of the last call on its default stream
 
 
-def _take_workspace(key, need, device):
-    """Scratch for a call on the current stream: the last call's there, whose kernels run before this one's, or new
-    memory.  Taken out of the dict for the time of the call: another thread's call on the stream gets its own."""
-    w = _spare_workspaces.pop(key, None)
-    return w if w is not None and w.numel() >= need else torch.empty(need, dtype=torch.uint8, device=device)
+def _take_workspace(index, need, device, stream):
+    """Scratch for a call on the default stream: the last call's there, whose kernels run before this one's, or new
+    memory.  Taken out of the dict for the time of the call: another thread's call gets its own."""
+    w = _kept_workspaces.pop(index, None)
+    return w if w is not None and w.numel() >= need else _empty(need, torch.uint8, device, stream)
+
+
+def gdn_attn_release_workspaces():
+    """Gives the workspaces that the attention calls keep (43 MB a device) back to PyTorch's allocator."""
+    _kept_workspaces.clear()
 
 
 def _call(fn, device, stream, *args):
     """fn(*args, stream) with the tensors' device current; raises the library's error."""
     index = device.index
-    if stream is not None:
-        s = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    elif _raw_stream is not None:
-        s = _raw_stream(index)
-    else:
-        s = torch.cuda.current_stream(device).cuda_stream
+    s = _handle(device, stream)
     if index == torch.cuda.current_device():
         status = fn(*args, s)
     else:
@@ -973,10 +993,11 @@ def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out
     key = None
     if workspace is None:
         need = lib.gdn_attn_workspace_size(geo)
-        if stream is None and _raw_stream is not None and dev.index == torch.cuda.current_device() and \
-                not torch.cuda.is_current_stream_capturing():  # a graph's memory is its own
-            key = dev.index, _raw_stream(dev.index)
-            workspace = _take_workspace(key, need, dev)
+        # Kept between calls on the default stream alone: another handle may be one queue now and another one later
+        # (or, the per-thread stream, in another thread).  The default stream is never captured.
+        if _handle(dev, stream) == 0 and dev.index == torch.cuda.current_device():
+            key = dev.index
+            workspace = _take_workspace(key, need, dev, stream)
         else:
             workspace = _empty(need, torch.uint8, dev, stream)
     elif workspace.device != dev:
@@ -987,15 +1008,16 @@ def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out
     else:
         _call(lib.gdn_attn_prefill, dev, stream, geo, qp, c, table, pages, lens, cu, N, T, *tail)
     if key is not None:
-        _spare_workspaces[key] = workspace
+        _kept_workspaces[key] = workspace
     return out
 
 
 def gdn_attn_prefill(q, cache: KVCache, block_table, kv_lens, cu_seqlens, softmax_scale, z=None, out=None,
                      workspace=None, stream=None):
     """Causal attention of packed new tokens over their caches (which hold them too), optionally
-    gated by sigmoid(z); q, z, out [T, Hq, D] bf16.  Returns out.  Without a workspace the call keeps
-    one for each stream (43 MB) between calls; in a graph's capture it is the graph's own."""
+    gated by sigmoid(z); q, z, out [T, Hq, D] bf16.  Returns out.  Without a workspace the call takes one
+    from PyTorch's allocator (43 MB); on the default stream it is kept for the next call
+    (gdn_attn_release_workspaces), in a graph's capture it is the graph's own."""
     if cu_seqlens is None:
         raise TypeError("cu_seqlens must be a CUDA tensor")
     return _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out, workspace, stream)
