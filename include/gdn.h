@@ -595,7 +595,7 @@ GDN_API gdn_status gdn_attn_rope_frequencies(int32_t rot_dim, const gdn_rope_sca
  *   rope       NULL or rot_dim 0: no rotation.  Angles are formed to about 2^-23 turns at positions below
  *              2^24 (2^-18 at any) without fp64 arithmetic in the token loop
  *   q_out      [total_tokens, Hq, D] bf16; may be q itself where q has that layout, and overlaps nothing
- *              else that the call reads
+ *              else that the call reads or writes
  */
 GDN_API gdn_status gdn_attn_prepare(const gdn_attn_geometry* geo, const gdn_bf16* q, int64_t q_token_stride,
                                     int64_t q_head_stride, const gdn_bf16* k, int64_t k_token_stride,
@@ -609,7 +609,7 @@ GDN_API gdn_status gdn_attn_prepare(const gdn_attn_geometry* geo, const gdn_bf16
 /*
  * Rows of the cache as dense bf16 (exact for both cache types): output rows cu_seqlens[n] ..
  * cu_seqlens[n+1]-1 receive positions starts[n], starts[n] + 1, ... of sequence n (starts NULL: 0).
- *   k_out, v_out  [total_tokens, Hkv, D] bf16
+ *   k_out, v_out  [total_tokens, Hkv, D] bf16; must not overlap each other or the cache
  * Positions outside [0, max_pages * page_size) or on a bad page set GDN_ERR_DEVICE_ARGUMENT; their
  * rows are left as they were.
  */
@@ -638,7 +638,7 @@ GDN_API size_t gdn_attn_workspace_size(const gdn_attn_geometry* geo);
  *   q          [total_tokens, Hq, D] bf16
  *   z          Hq heads of D bf16 for each token, head h of token t at z + t * z_token_stride +
  *              h * z_head_stride (elements, multiples of 8), or NULL
- *   out        [total_tokens, Hq, D] bf16; must not overlap q or z
+ *   out        [total_tokens, Hq, D] bf16; must not overlap q, z or the cache
  *   workspace  256-byte aligned device memory of gdn_attn_workspace_size() bytes; calls that may
  *              overlap on the GPU (other streams, graphs replayed together) need one each
  */

@@ -791,6 +791,14 @@ bool rows_overlap(const gdn_bf16* p, int64_t token, int64_t head, int64_t tokens
   return overlaps(p + lo, (size_t)(hi - lo) * 2, out, bytes);
 }
 
+// Whether the memory range [out, out + bytes) has any of the pool's pages or scales.
+bool overlaps_pool(const gdn_attn_geometry* geo, const gdn_kv_cache* c, const void* out, size_t bytes) {
+  const size_t rows = (size_t)c->num_pages * geo->num_kv_heads * c->page_size;
+  const size_t pool = rows * geo->head_dim * (c->type == GDN_CACHE_E4M3 ? 1 : 2);
+  if (overlaps(c->k, pool, out, bytes) || overlaps(c->v, pool, out, bytes)) return true;
+  return c->type == GDN_CACHE_E4M3 && (overlaps(c->k_scale, rows, out, bytes) || overlaps(c->v_scale, rows, out, bytes));
+}
+
 gdn_status attention(const gdn_attn_geometry* geo, const gdn_bf16* q, const gdn_kv_cache* cache,
                      const int32_t* block_table, int32_t max_pages, const int32_t* kv_lens,
                      const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens, float softmax_scale,
@@ -813,6 +821,7 @@ gdn_status attention(const gdn_attn_geometry* geo, const gdn_bf16* q, const gdn_
   if (overlaps(q, bytes, out, bytes)) return fail(GDN_ERR_INVALID_ARGUMENT, "out overlaps q");
   if (z && rows_overlap(z, z_token_stride, z_head_stride, total_tokens, geo->num_q_heads, geo->head_dim, out, bytes))
     return fail(GDN_ERR_INVALID_ARGUMENT, "out overlaps z");
+  if (overlaps_pool(geo, cache, out, bytes)) return fail(GDN_ERR_INVALID_ARGUMENT, "out overlaps the cache");
   if ((int64_t)c.num_pages * geo->num_kv_heads * cache->page_size > 0x7FFFFFFFL)
     return fail(GDN_ERR_INVALID_ARGUMENT, "the pool has more than 2^31 rows");
   const size_t need = gdn::attn_workspace_bytes(geo->head_dim);
@@ -893,6 +902,7 @@ gdn_status gdn_attn_prepare(const gdn_attn_geometry* geo, const gdn_bf16* q, int
   if (q && (rows_overlap(k, k_token_stride, k_head_stride, total_tokens, geo->num_kv_heads, D, q_out, out_bytes) ||
             rows_overlap(v, v_token_stride, v_head_stride, total_tokens, geo->num_kv_heads, D, q_out, out_bytes)))
     return fail(GDN_ERR_INVALID_ARGUMENT, "q_out overlaps k or v");
+  if (q && overlaps_pool(geo, cache, q_out, out_bytes)) return fail(GDN_ERR_INVALID_ARGUMENT, "q_out overlaps the cache");
   GDN_OPTIONAL(q_norm_w, "q_norm_w");
   GDN_OPTIONAL(k_norm_w, "k_norm_w");
   if (!(rms_eps >= 0.f)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be >= 0");
@@ -927,6 +937,10 @@ gdn_status gdn_attn_cache_read(const gdn_attn_geometry* geo, const gdn_kv_cache*
   if ((s = check_paged_cache(cache, block_table, max_pages, &c)) != GDN_OK) return s;
   GDN_REQUIRE(k_out, "k_out");
   GDN_REQUIRE(v_out, "v_out");
+  const size_t bytes = (size_t)total_tokens * geo->num_kv_heads * geo->head_dim * 2;
+  if (overlaps(k_out, bytes, v_out, bytes)) return fail(GDN_ERR_INVALID_ARGUMENT, "v_out overlaps k_out");
+  if (overlaps_pool(geo, cache, k_out, bytes) || overlaps_pool(geo, cache, v_out, bytes))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "k_out or v_out overlaps the cache");
   gdn::LaunchEnv env;
   if ((s = make_env(stream, &env)) != GDN_OK) return s;
   return launched(gdn::launch_attn_cache_read(env, geo->num_kv_heads, geo->head_dim, c, starts, cu_seqlens, num_seqs,
