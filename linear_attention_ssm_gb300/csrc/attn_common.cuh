@@ -139,6 +139,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, bool rep
   if (p.cu) {
     const int a = p.cu[n], b = p.cu[n + 1];
     bad = a < 0 || b < a || b > p.T;
+    if (n == 0 && a > 0 && report) raise_error(p.err, kErrDeviceArgument);  // the rows before are nobody's
     s.first = a;
     s.len = bad ? 0 : b - a;
   }

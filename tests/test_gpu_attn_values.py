@@ -211,6 +211,27 @@ def test_nothing_is_written_for_a_token_without_a_page(e4m3, in_place):
     assert torch.equal(q_out[0], good[0]) and torch.equal(q_out[1:], before[1:])
 
 
+def test_rows_before_the_first_sequence_are_reported():
+    """cu_seqlens that does not begin at 0: an error in every call, the sequences themselves as ever."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(28)
+    cache, table = make_cache(g, gen, [3, 4], [40, 50], 2, 16, 128, False)
+    q, kv = randn(gen, 9, 4, 128), randn(gen, 9, 2, 128)
+    lens, cu = ints([40, 50]), ints([2, 5, 9])
+    out = torch.full_like(q, 7.0)
+    g.gdn_attn_prefill(q, cache, table, lens, cu, 0.1, out=out)
+    with pytest.raises(g.GdnError) as e:
+        g.gdn_check_device_errors()
+    assert e.value.status == 6 and bool((out[:2] == 7.0).all())
+    want, tol = attention(q[2:], cache, table, [3, 4], [40, 50], 0.1)
+    assert_within(out[2:], want, tol, "attention")
+    for call_it in (lambda: g.gdn_attn_prepare(q, kv, kv, cache, table, lens, cu),
+                    lambda: g.gdn_attn_cache_read(cache, table, cu, kv, kv.clone())):
+        call_it()
+        with pytest.raises(g.GdnError):
+            g.gdn_check_device_errors()
+
+
 # ------------------------------------------------------------------------------------ nine to sixteen heads to a key head
 
 @pytest.mark.parametrize("kv_lens", [[1], [0, 1, 127, 128, 129, 5000], [20000, 3], [700] * 33])
