@@ -526,7 +526,7 @@ GDN_API gdn_status gdn_chunk_prefill_noalloc(const gdn_geometry* geo, const gdn_
  * Pages.  Position p of sequence n lies in page block_table[n * max_pages + p / page_size], row
  * p % page_size.  Pages may be shared by sequences that only read them; two tokens of one call must
  * not write the same row.  Device-side faults -- a page that is needed and lies outside
- * [0, num_pages), kv_lens[n] outside [0, max_pages * page_size], bad cu_seqlens -- set
+ * [0, num_pages), kv_lens[n] outside [0, max_pages * page_size] or above 2^31 - 256, bad cu_seqlens -- set
  * GDN_ERR_DEVICE_ARGUMENT in the device error word; nothing is written for those tokens by
  * gdn_attn_prepare, and the rows of such a sequence are unspecified in the other calls.
  *

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(32 * kWarps, 8) prepare_kernel(const __grid_co
     return;
   }
   const int kv = p.kv_lens[seq];
-  if (kv < 0 || kv > min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) {
+  if (kv < 0 || kv > min((long)p.cache.max_pages << p.cache.page_shift, (long)kMaxKeys)) {
     raise_error(p.err, kErrDeviceArgument);
     return;
   }
@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(32 * kWarps) cache_read_kernel(const __grid_co
     const int seq = attn_seq_of(p.cu, p.N, p.T, t, first, len);
     if (seq >= 0) {
       const long pos = (p.starts ? (long)p.starts[seq] : 0L) + (t - first);
-      if (pos < 0 || pos >= min((long)p.cache.max_pages << p.cache.page_shift, 0x7FFFFFFFL)) bad = true;
+      if (pos < 0 || pos >= min((long)p.cache.max_pages << p.cache.page_shift, (long)kMaxKeys)) bad = true;
       else place = cache_row(p.cache, p.Hkv, seq, (int)pos, bad);
     } else if (seq == -2) {
       bad = true;

@@ -78,6 +78,7 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 constexpr int kBlock = 128;     // keys of a block, the unit of work
+constexpr int kMaxKeys = 0x7FFFFF00;  // of a sequence: a block or two further is within 31 bits too
 
 struct AttnParams {
   CUtensorMap tmap_k;  // pages as [pages * Hkv * page][D] bf16, box 64 x min(page, 64), 128-byte swizzle
@@ -144,7 +145,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int n, bool rep
     s.len = bad ? 0 : b - a;
   }
   s.kv = p.kv_lens[n];
-  if (s.kv < 0 || s.kv > ((long)p.cache.max_pages << p.cache.page_shift)) {
+  if (s.kv < 0 || s.kv > min((long)p.cache.max_pages << p.cache.page_shift, (long)kMaxKeys)) {
     bad = true;
     s.kv = 0;
   }

@@ -232,6 +232,27 @@ def test_rows_before_the_first_sequence_are_reported():
             g.gdn_check_device_errors()
 
 
+@pytest.mark.parametrize("D,e4m3", [(128, False), (256, True)])
+def test_more_positions_than_31_bits_hold_blocks_of(D, e4m3):
+    """A table of 2^24 pages of 128 rows (all the same one): the last 255 of its lengths are refused by every call."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(29)
+    cache, _ = make_cache(g, gen, [1], [100], 2, 128, D, e4m3)
+    table = torch.zeros(1, 2 ** 24, dtype=torch.int32, device=DEV)
+    q, kv = randn(gen, 3, 8, D), randn(gen, 3, 2, D)
+    for length in (2 ** 31 - 255, 2 ** 31 - 1):
+        lens, cu = ints([length]), ints([0, 3])
+        for call_it in (lambda: g.gdn_attn_prefill(q, cache, table, lens, cu, 0.1), lambda: g.gdn_attn_prepare(q, kv, kv, cache, table, lens, cu),
+                        lambda: g.gdn_attn_decode_step(q[:1].clone(), cache, table, lens, 0.1),
+                        lambda: g.gdn_attn_cache_read(cache, table, cu, kv, kv.clone(), starts=ints([length]))):
+            call_it()
+            with pytest.raises(g.GdnError) as e:
+                g.gdn_check_device_errors()
+            assert e.value.status == 6
+    g.gdn_attn_prepare(q, kv, kv, cache, table, ints([2 ** 31 - 256]), ints([0, 3]))  # the last that has a place
+    g.gdn_check_device_errors()
+
+
 # ------------------------------------------------------------------------------------ nine to sixteen heads to a key head
 
 @pytest.mark.parametrize("kv_lens", [[1], [0, 1, 127, 128, 129, 5000], [20000, 3], [700] * 33])
