@@ -78,11 +78,10 @@ struct Cfg {
   // of the four warps behind the softmax's: the products (two), Q, K and V by TMA, value rows that some row
   // does not see (e4m3: scales)
   static constexpr int kMma0 = kSoftWarps, kMma1 = kSoftWarps + 1, kLoad = kSoftWarps + 2, kTail = kSoftWarps + 3;
-  // Scores that a softmax warp holds at a time; the rest of a step's are read twice.  Few registers, and
-  // short code for the instruction cache that warps of several kinds share: 32 beat 128 by 2 % at D = 256
-  // and by a third for e4m3 (8192 prompt tokens at D = 128: 707 us with 32, 792 with 64); two bf16 tiles hold
-  // their 64 (468 us, 472 with 32).
-  static constexpr int kCols = kTiles == 2 && !kE4M3 ? 64 : 32;
+  // Scores that a softmax warp holds at a time; a step's are read twice, for the maximum and for the weights.  Few
+  // registers, and short code for the instruction cache that warps of several kinds share: with 64, 8192 prompt
+  // tokens take 435 us (434 with 32), from e4m3 pages 688 (634); eight prompts' chunks at D = 256 154 (130), e4m3 271 (242).
+  static constexpr int kCols = 32;
   // Keys whose scores a slot holds: a block's, or with two tiles half of them.  A tile has two slots, so that
   // its next scores are there when the weights of these are done (8192 prompt tokens 467 us; with a slot of 128
   // keys for each tile 605, with both halves' scores from one product 579).  A product of 64 keys costs what one
@@ -94,39 +93,6 @@ struct Cfg {
 struct Bars {
   uint32_t full, empty, tail, s_full, p_full, o_full, q_full, q_empty, done, meta_full, meta_empty, q_ready, raw_full, raw_empty;  // shared addresses of the first of each kind
 };
-
-// 64 columns of this warp's 32 lanes.  The wait for the load is a statement of its own (two loads, one
-// wait): tmem_ld64_wait hands the values on, so that no use of them is moved ahead of it.
-__device__ __forceinline__ void tmem_ld64_begin(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
-      "%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,"
-      "%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld64_wait(uint32_t (&r)[64]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
-        "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
-        "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
-        "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
-        "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
-               :
-               : "memory");
-}
 
 // A position in the ring of stages: which stage, and which pass over the ring.
 template <int kStages>
@@ -151,22 +117,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
-}
-template <int kCols>
-__device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[kCols]) {
-  if constexpr (kCols == 32) {
-    tmem_ld32(taddr, s);
-  } else {
-    uint32_t x[kCols / 64][64];
-#pragma unroll
-    for (int h = 0; h < kCols / 64; ++h) tmem_ld64_begin(taddr + 64 * h, x[h]);
-#pragma unroll
-    for (int h = 0; h < kCols / 64; ++h) {
-      tmem_ld64_wait(x[h]);
-#pragma unroll
-      for (int i = 0; i < 64; ++i) s[64 * h + i] = __uint_as_float(x[h][i]);
-    }
-  }
 }
 // 16 columns of this warp's 32 lanes; tmem_st_wait: this thread's stores so far have been done
 __device__ __forceinline__ void tmem_st16_begin(uint32_t taddr, const float (&v)[16]) {
@@ -429,7 +379,7 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             float s[kCols], mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
             for (int c0 = 0; c0 < kKeys; c0 += kCols) {
-              load_scores<kCols>(t_s + c0, s);
+              tmem_ld32(t_s + c0, s);
               if (masked) {
 #pragma unroll
                 for (int k = 0; k < kCols; ++k)
@@ -470,30 +420,27 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
             for (int c0 = 0; c0 < kKeys; c0 += kCols) {
-              if (kCols < kKeys) {  // again: the weights go over scores that have been read
-                load_scores<kCols>(t_s + c0, s);
-                if (masked) {
+              tmem_ld32(t_s + c0, s);  // again: the weights go over scores that have been read
+              if (masked) {
 #pragma unroll
-                  for (int k = 0; k < kCols; ++k)
-                    if (c0 + k >= lim) s[k] = -INFINITY;
+                for (int k = 0; k < kCols; ++k)
+                  if (c0 + k >= lim) s[k] = -INFINITY;
+              }
+              float w[16];
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int at = 2 * (i + k);
+                  float2 x = __ffma2_rn(make_float2(s[at], s[at + 1]), unit2, off2);
+                  x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                  sum[k] = __fadd2_rn(sum[k], x);
+                  // The weights' one rounding: the matrix instructions take both operands in one type, that of the cache
+                  // (bf16: 2^-8 of a weight at most, while the sum l keeps fp32), or binary16 beside e4m3 codes (2^-11 where it is normal).
+                  w[i + k] = __uint_as_float(kE4M3 ? pack_half2(x.x, x.y) : pack_bf2(x.x, x.y));
                 }
               }
-#pragma unroll
-              for (int h = 0; h < kCols / 32; ++h) {
-                float w[16];
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-#pragma unroll
-                  for (int k = 0; k < 2; ++k) {
-                    const int at = 32 * h + 2 * (i + k);
-                    float2 x = __ffma2_rn(make_float2(s[at], s[at + 1]), unit2, off2);
-                    x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                    sum[k] = __fadd2_rn(sum[k], x);
-                    w[i + k] = __uint_as_float(kE4M3 ? pack_half2(x.x, x.y) : pack_bf2(x.x, x.y));
-                  }
-                }
-                tmem_st16_begin(t_s + c0 / 2 + 16 * h, w);
-              }
+              tmem_st16_begin(t_s + c0 / 2, w);
             }
             tmem_st_wait();
             const float all = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -676,9 +623,9 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         *reinterpret_cast<uint4*>(at + other) = make_uint4(mul_half2(c.x, f), mul_half2(c.y, f), mul_half2(e.x, f), mul_half2(e.y, f));
       };
       if (value ? seen >= (wide ? 64 : 128) : last >= 127) {  // (keys have base 0)
-        // Short loops: the kernel's roles share the instruction caches (D = 256: 253 us for the chunks of eight
-        // prompts, 261 with one unit a pass, 299 with four; two tiles: 640 us for 8192 tokens, 746 with four)
-#pragma unroll(kTiles == 2 ? 1 : 2)
+        // A short loop: the kernel's roles share the instruction caches (8192 prompt tokens 633 us, 660 with two units a
+        // pass, 740 with four; D = 256, eight prompts' chunks: 243, 242, 253)
+#pragma unroll 1
         for (int u = 0; u < kUnits; ++u)
           widen(u, *reinterpret_cast<const uint4*>(from + (row0 + u * stride) * 64), scale[base + row0 + u * stride]);
       } else {
