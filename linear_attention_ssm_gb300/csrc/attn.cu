@@ -26,12 +26,13 @@
 // tile that a cut falls into leaves its parts (O, m, l) in the workspace for a second kernel to join,
 // so a few long sequences spread over the whole GPU as a large batch does.
 //
-// Measured on a GB300 (of 1956 TFLOP/s of bf16 products): a prompt of 8192 tokens, 32 heads of 128, 433 us, 1.27
-// PFLOP/s, 65 % -- products, nine tenths of the time by their own clocks, those of 64 keys at half the rate; 2048 tokens after
-// 30001, 16 heads of 256, 704 us, 1.48 PFLOP/s, 76 % -- keys and values from L2, 128 KB a block for each SM; chunks
-// of eight prompts of 17 to 1500 tokens, 16 heads of 256, 126 us from bf16 pages, 917 TFLOP/s, and 253 us from e4m3
-// ones, 455 TFLOP/s -- widening the codes beside the softmax, whose instructions leave the caches between them; 17
-// tokens after 1000, 48 heads of 128, 16 us -- latency, of two launches.
+// Measured on a GB300 (of 1956 TFLOP/s of bf16 products; calls in a CUDA graph): a prompt of 8192 tokens, 32 heads of
+// 128, 435 us, 1.26 PFLOP/s, 65 % -- products, nine tenths of the time by their own clocks, those of 64 keys at half the
+// rate; from e4m3 pages 634 us.  2048 tokens after 30001, 16 heads of 256, 707 us, 1.47 PFLOP/s, 75 % (758 us in a row of
+// calls, which meet the power limit) -- keys and values from L2, 128 KB a block for each SM.  Chunks of eight prompts of 17
+// to 1500 tokens, 16 heads of 256, 131 us from bf16 pages, 880 TFLOP/s, and 244 us from e4m3 ones, 472 TFLOP/s --
+// widening the codes, once for each tile, beside the softmax, whose instructions leave the caches between them.  17
+// tokens after 1000, 48 heads of 128, 15 us -- latency, of two launches.
 #include <cstring>
 
 #include "attn_common.cuh"
@@ -1007,7 +1008,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
   __syncthreads();
   const int parts = s_n;
-  // (one token at 4000 keys, 76 parts a tile: 14.0 us with, 3 more without)
+  // (one token at 4000 keys, 76 parts a tile: 15.1 us with, 16.4 without)
   const int ways = parts >= 16 ? 8 : parts >= 8 ? 4 : 1, way = warp % ways, each = 8 / ways;  // warps of an item; items at a time
   const int subs = kTiles == 2 && d.y > p.sub ? 2 : 1;
   const int items = kTiles ? subs * 4 * (D / 16) : (p.G * (D / 4) + 31) / 32;
@@ -1175,13 +1176,13 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   p.N = N;
   p.T = T;
   p.sub = 128 / p.G;
-  // What beginning and ending a tile costs beside one block (D = 256, eight prompts' chunks: bf16 160 us with 2,
-  // 153 with 3, 144 with 4 and 5; e4m3 294, 285, 289, 292; D = 128, a prompt of 8192: 469 with 1, 450 with 2, 456
-  // with 3, and 511 us with none)
-  p.lead = D == 128 ? 2 : cache.e4m3 ? 3 : 4;
+  // What beginning and ending a tile costs beside one block, with 1 to 5: D = 256, eight prompts' chunks, bf16 173,
+  // 148, 139, 130, 131 us, e4m3 299, 256, 249, 243, 239 (sixteen prompts of 50 to 900 tokens 139 with 3, 138, 145); D
+  // = 128, a prompt of 8192, 457, 435, 440, 447, 455 us (497 with none), e4m3 687, 634, 625, 632, 641.
+  p.lead = D == 128 ? 2 : 4;
   // Fewer CTAs on a short line: a part costs its reader as much as a block.  17 tokens after 1000, 16 key heads of
-  // 128: 17.3 us with no such limit, 14.8 with 2, 15.5 with 3, 16.9 with 4; 16 tokens after 4000, 2 of 256: 32.2 us,
-  // 25.7, 24.0, 23.6.
+  // 128: 17.1 us with no such limit, 15.5 with 2, 16.0 with 3, 16.7 with 4; 16 tokens after 4000, 2 of 256: 31.7 us,
+  // 26.6, 26.1, 27.6.
   p.least = p.lead;
   p.wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1194,9 +1195,9 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   // One token of each sequence and few query heads to a key head: too few rows to fill a 128-row tile, and HBM
   // bounds the call.  By groups of 8 heads, this kernel against the tiles' (64 sequences of 30 to 30000 keys at
-  // D = 256, 256 of 500 to 8000 at D = 128): D = 256 bf16 97 : 103 us, one sequence of 4000 keys 14 : 22; e4m3
-  // 60 : 156; D = 128 bf16 421 : 467, e4m3 262 : 896; with 16 heads D = 128 bf16 221 : 257, e4m3 169 : 452, but
-  // D = 256 bf16 169 : 107, e4m3 170 : 160.
+  // D = 256, 256 of 500 to 8000 at D = 128): D = 256 bf16 97 : 105 us, one sequence of 4000 keys 15 : 20; e4m3
+  // 60 : 154; D = 128 bf16 426 : 463, e4m3 264 : 871; with 16 heads D = 128 bf16 223 : 256, e4m3 168 : 468, but
+  // D = 256 bf16 169 : 107, e4m3 170 : 157 (a form of this kernel for them, which is not kept).
   if (!cu && p.G <= (D == 128 ? 16 : 8)) {
     p.sub = 1;
     // A tile's beginning and end, in blocks of HBM's time for an SM ("short": 400 sequences of 30 to 3000 keys).  bf16
@@ -1213,9 +1214,9 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
   if (e == cudaSuccess) e = encode_pages(&p.tmap_v, cache.v, cache, Hkv, D);
   if (e == cudaSuccess) e = encode_bf16_3d_sw128(&p.tmap_q, q, D, Hq, T, 64, p.G, p.sub);
   if (e != cudaSuccess) return e;
-  // Two tiles a CTA where a sequence has more rows than one holds, on average.  64 sequences of 2000 keys, 96 rows
-  // for each: one tile 111 us, two 112 (e4m3 185 : 223); 160 rows: 200 : 123 (349 : 184); a prompt of 8192 tokens
-  // 732 : 436 (1216 : 640).
+  // Two tiles a CTA where a sequence has more rows than one holds, on average.  64 sequences of 2000 keys, 2 key
+  // heads, 96 rows for each: one tile 43 us, two 46 (e4m3 53 : 59); 160 rows: 63 : 52 (99 : 65); a prompt of 8192
+  // tokens, 8 key heads, 699 : 437 (1202 : 634).
   const bool two = (long)T * p.G > 128L * N;
   if (cache.e4m3) {
     if (D == 256) return launch_tiles<256, 1, true>(env, p, ctas);

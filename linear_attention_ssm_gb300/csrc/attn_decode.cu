@@ -17,8 +17,8 @@
 // a row's largest leave its normal range.
 //
 // Measured on a GB300 (of 6792 GB/s copied): 64 sequences of 30 to 30000 keys, 2 key heads of 256, bf16 97 us, 6.2
-// TB/s, 91 %, e4m3 60 us; 256 sequences of 500 to 8000 e4m3 keys, 8 of 128, 261 us, 5.5 TB/s, 81 %; one sequence of
-// 4000 keys 14 us -- the latency of two launches, HBM's share is 1.2.
+// TB/s, 91 %, e4m3 60 us; 256 sequences of 500 to 8000 e4m3 keys, 8 of 128, 263 us, 5.5 TB/s, 81 %; one sequence of
+// 4000 keys 15 us -- the latency of two launches, HBM's share is 1.2.
 #include <cstring>
 
 #include "attn_common.cuh"
@@ -448,6 +448,7 @@ __global__ void __launch_bounds__(DCfg<D, kE4M3, kQ8>::kThreads, 1) attn_decode_
               w[1][k] *= vf[y][1];
             }
           }
+          // the weights' one rounding: the matrix instructions take both operands in one type, bf16 or binary16 (l keeps fp32)
           pb[a][y][0] = transpose8x8(kE4M3 ? pack_half2(w[0][0], w[0][1]) : pack_bf2(w[0][0], w[0][1]));
           pb[a][y][1] = transpose8x8(kE4M3 ? pack_half2(w[1][0], w[1][1]) : pack_bf2(w[1][0], w[1][1]));
         }
