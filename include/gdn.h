@@ -631,7 +631,7 @@ GDN_API size_t gdn_attn_workspace_size(const gdn_attn_geometry* geo);
  * Scores and sums are fp32 with a running maximum; the weights e^(s_j - max) are rounded to bf16
  * for the product with v.  Beside an e4m3 cache the matrix operands are binary16, which holds every code
  * exactly: the queries are rounded to it (divided by a power of two), and the weights.  Few query heads and one
- * token a sequence: the weights times the power of two of v_j, relative to the largest of 16 or 32 keys (2^-32
+ * token a sequence: the weights times the power of two of v_j, relative to the largest of 16 or 32 keys (2^-31
  * of the largest value there is lost at most).  Otherwise: keys and values relative to the largest power of
  * two of a block of 128; rows up to 2^22 below it are exact, and rows 2^32 or more below it count as zero
  * (less than 2^-30 of the block's largest key or value).
