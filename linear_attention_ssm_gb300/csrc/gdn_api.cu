@@ -892,8 +892,9 @@ gdn_status gdn_attn_prepare(const gdn_attn_geometry* geo, const gdn_bf16* q, int
     if ((s = check_head_rows(q, q_token_stride, q_head_stride, "q")) != GDN_OK) return s;
     GDN_REQUIRE(q_out, "q_out");
     // Each row is read whole before it is written, by the same lanes: q_out may be q itself, but rows
-    // at other places would be overwritten before they are read.
-    const bool same = q == q_out && q_head_stride == D && q_token_stride == (int64_t)D * geo->num_q_heads;
+    // at other places would be overwritten before they are read.  (One token or head has no stride.)
+    const bool same = q == q_out && (q_head_stride == D || geo->num_q_heads == 1) &&
+                      (q_token_stride == (int64_t)D * geo->num_q_heads || total_tokens == 1);
     if (!same && rows_overlap(q, q_token_stride, q_head_stride, total_tokens, geo->num_q_heads, D, q_out, out_bytes))
       return fail(GDN_ERR_INVALID_ARGUMENT, "q_out overlaps q without being it");
   }

@@ -6,7 +6,7 @@ import ctypes
 import pytest
 
 from linear_attention_ssm_gb300 import binding
-from tests.test_attn_abi import OTHER, attend, cache, lib, prepare, read  # noqa: F401
+from tests.test_attn_abi import OTHER, attend, cache, geo, lib, prepare, read  # noqa: F401
 
 POOL, SCALES = 4 * 2 * 64 * 256, 4 * 2 * 64  # values and rows of the four pages of two heads
 K, V, KS, VS = 0x10000000, 0x20000000, 0x30000000, 0x40000000
@@ -42,3 +42,14 @@ def test_read_into_one_place(lib):  # noqa: F811
     assert read(lib, c=pool, k=OTHER, v=OTHER) == 1
     assert read(lib, c=pool, k=OTHER, v=at(OTHER.value + kv - 16)) == 1
     assert read(lib, c=pool, k=at(OTHER.value + 16), v=OTHER) == 1
+
+
+def test_queries_in_place(lib):  # noqa: F811
+    """q_out is q where every row lies at its own place: a stride that no row uses does not matter."""
+    pool, bad_rope = cache(0, k=K, v=V), ctypes.byref(binding._Rope(24, 0, 1.0, 0x10000))
+
+    def call(**kw):
+        return prepare(lib, c=pool, q=OTHER, out=OTHER, rope=bad_rope, **kw)
+    assert call(qs=(4096, 256)) == 2 and call(qs=(5120, 256)) == 1 and call(qs=(4096, 264)) == 1
+    assert call(qs=(5120, 256), n=1, t=1) == 2 and call(qs=(5120, 264), n=1, t=1) == 1
+    assert call(g=geo(1, 1), qs=(256, 5120)) == 2 and call(g=geo(1, 1), qs=(512, 256)) == 1
