@@ -461,8 +461,8 @@ __global__ void __launch_bounds__(Cfg<D, kTiles, kE4M3>::kThreads, 1) attn_kerne
         tc_fence_after();
         if (busy && __any_sync(0xFFFFFFFFu, *odd_seen != 0)) {
           // bf16: the sequence and the tile's first position from values that the loop holds anyway; kept for this
-          // through the loop they cost it registers (2048 tokens after 30001: 707 us, 716 with them kept).  e4m3 the
-          // other way round: the kernel is short of instruction cache (8192 prompt tokens: 646 us, 689 with the lookup).
+          // through the loop they cost it registers (2048 tokens after 30001: 706 us, 714 with them kept).  e4m3 the
+          // other way round: the kernel is short of instruction cache (8192 prompt tokens: 633 us, 677 with the lookup).
           int n = seg.n, key0 = seg.pos0 + 1;
           if constexpr (!kE4M3) {
             int first, len;
