@@ -172,6 +172,13 @@ def prepare(case, seed):
     s["result"] = torch.empty(t, h, dtype=torch.bfloat16, device="cuda")
     s["ids"] = torch.empty(t, k, dtype=torch.int32, device="cuda")
     s["chosen_weights"] = torch.empty(t, k, dtype=torch.float32, device="cuda")
+    if own:
+        import linear_attention_ssm_gb300 as gdn
+        s["experts"] = gdn.Experts(
+            s["gate_up"], s["down"], s["gate_up_scale"], s["down_scale"], router=s["router"], router_bias=s["router_bias"],
+            shared_gate_up=s["shared_gate_up"], shared_down=s["shared_down"],
+            shared_gate_up_scale=s["shared_gate_up_scale"], shared_down_scale=s["shared_down_scale"],
+            shared_gate=s["shared_gate"])
     return s
 
 
@@ -193,11 +200,7 @@ def _own(s):
         return {"codes": codes, "scales": scales}
     if s["op"] == "product":
         return gdn.gdn_fp8_matmul(s["xc"], s["xs"], s["wc"], s["ws"], out=s["result"])
-    experts = gdn.Experts(s["gate_up"], s["down"], s["gate_up_scale"], s["down_scale"], router=s["router"],
-                          router_bias=s["router_bias"], shared_gate_up=s["shared_gate_up"], shared_down=s["shared_down"],
-                          shared_gate_up_scale=s["shared_gate_up_scale"], shared_down_scale=s["shared_down_scale"],
-                          shared_gate=s["shared_gate"])
-    out = gdn.gdn_moe_step(s["x"], experts, s["k"], scoring=s["score"], renormalise=True, scale=ROUTED_SCALE,
+    out = gdn.gdn_moe_step(s["x"], s["experts"], s["k"], scoring=s["score"], renormalise=True, scale=ROUTED_SCALE,
                            out=s["result"], ids=s["ids"], weights=s["chosen_weights"])
     return {"out": out, "ids": s["ids"], "weights": s["chosen_weights"]}
 
