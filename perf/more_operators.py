@@ -105,7 +105,8 @@ def _quantise(x, block_rows):
     br, bc = -(-r // block_rows), _blocks(c)
     x = torch.nn.functional.pad(x.float(), (0, bc * BLOCK - c, 0, br * block_rows - r))
     x = x.unflatten(-1, (bc, BLOCK)).unflatten(-3, (br, block_rows))
-    scale = (x.abs().amax((-3, -1)) / TOP).clamp(min=LEAST)
+    top = x.abs().amax((-3, -1))
+    scale = (top / torch.full_like(top, TOP)).clamp(min=LEAST)  # a division in earnest: by a number it is a product
     codes = (x / scale[..., :, None, :, None]).clamp(-TOP, TOP).to(torch.float8_e4m3fn)
     return codes.flatten(-2, -1).flatten(-3, -2)[..., :r, :c], scale
 
