@@ -657,10 +657,135 @@ GDN_API gdn_status gdn_attn_decode_step(const gdn_attn_geometry* geo, const gdn_
                                         int64_t z_head_stride, gdn_bf16* out, void* workspace,
                                         size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * What stands around the layers in 8 bits: the projections' products and the expert layers (Qwen3.8 kernel
+ * architecture and TDD ledger, "Current dense-27B kernel map": 8-bit projections; spark_model layer_struct.rs: per-group
+ * activation quantisation, 8-bit products; GLM-5.3-Flash and Flash-Next ledgers: expert layers).
+ *
+ *   x --gdn_fp8_quantize--> codes, scales --gdn_fp8_matmul--> rows of the product
+ *   x --gdn_moe_step--> the expert layer's rows, for a few tokens
+ *
+ * A matrix in 8 bits is e4m3 codes with an fp32 scale for each block of GDN_FP8_BLOCK columns and 1 row (activations) or
+ * GDN_FP8_BLOCK rows (weights); the last blocks of a row or column may be narrower.  An element's value is
+ * code * scale. */
+#define GDN_FP8_BLOCK 128
+
+/*
+ * Codes and scales of bf16 rows.  Over each block of block_rows x 128 elements
+ *   scale = max(max |x| / 448, 2^-126),   code = x / scale rounded to the nearest e4m3 (ties to even), at most 448,
+ * in IEEE fp32 divisions.  A block with a NaN has the scale NaN; one with an infinity the scale infinity, and the
+ * infinity's code is NaN: a product with it is NaN in that row, and in that row alone.
+ *   x            rows x cols bf16, row r at x + r * x_row_stride (elements, any stride >= cols)
+ *   block_rows   1 or GDN_FP8_BLOCK
+ *   codes        row r at codes + r * codes_row_stride (bytes, a multiple of 16, >= cols); the bytes between cols and
+ *                the stride are left as they were
+ *   scales       [ceil(rows / block_rows), ceil(cols / 128)] fp32
+ * The outputs overlap neither x nor one another.  rows == 0 is a no-op that returns GDN_OK; cols >= 1.
+ */
+GDN_API gdn_status gdn_fp8_quantize(const gdn_bf16* x, int64_t x_row_stride, int32_t rows, int32_t cols,
+                                    int32_t block_rows, uint8_t* codes, int64_t codes_row_stride, float* scales,
+                                    void* stream);
+
+#define GDN_OUT_BF16 0
+#define GDN_OUT_F32 1
+
+/*
+ * Activations times weights, both in 8 bits:
+ *   out[t, j] = sum_b x_scale[t, b] w_scale[j / 128, b] sum_{i in block b} x[t, i] w[j, i]
+ * Each block's products are summed in fp32 on the tensor cores, scaled by the product of the two scales in fp32, and added
+ * up in fp32; the sum is rounded once to bf16, or not at all.  The order of the sums depends on the sizes alone.
+ *   x        tokens rows of k codes, x_row_stride bytes apart (a multiple of 16, >= k)
+ *   x_scale  [tokens, ceil(k / 128)] fp32
+ *   w        n rows of k codes, w_row_stride bytes apart (a multiple of 16, >= k)
+ *   w_scale  [ceil(n / 128), ceil(k / 128)] fp32
+ *   out      tokens rows of n bf16 or fp32 values, out_row_stride elements apart (>= n, any); overlaps no input.  What
+ *            lies between n and the stride is left as it was
+ * k codes that are NaN (or scales that are not finite) make the rows and columns they belong to NaN, and no others.
+ * tokens == 0 or n == 0 is a no-op that returns GDN_OK; k >= 1.
+ */
+GDN_API gdn_status gdn_fp8_matmul(const uint8_t* x, int64_t x_row_stride, const float* x_scale, const uint8_t* w,
+                                  int64_t w_row_stride, const float* w_scale, int32_t tokens, int32_t n, int32_t k,
+                                  int32_t out_type, void* out, int64_t out_row_stride, void* stream);
+
+/* The sizes of an expert layer: H, I and Is multiples of 16, at most GDN_MOE_MAX_WIDTH; Is = 0: no shared expert. */
+typedef struct {
+  int32_t hidden;       /* H  */
+  int32_t inter;        /* I, of an expert */
+  int32_t num_experts;  /* E, at most GDN_MOE_MAX_EXPERTS */
+  int32_t shared_inter; /* Is, of the expert that every token passes */
+} gdn_moe_geometry;
+#define GDN_MOE_MAX_WIDTH 16384
+#define GDN_MOE_MAX_EXPERTS 1024
+#define GDN_MOE_MAX_TOKENS 64
+#define GDN_MOE_MAX_TOP_K 16
+
+#define GDN_WEIGHT_BF16 0
+#define GDN_WEIGHT_E4M3 1 /* with a scale for each block of 128 x 128 of every [I, H] or [H, I] matrix */
+
+typedef struct {
+  int32_t type;                      /* of the experts' matrices, GDN_WEIGHT_* */
+  const gdn_bf16* router;            /* [E, H] */
+  const float* router_bias;          /* [E] added to the scores for the choice alone, or NULL */
+  const void* gate_up;               /* [E, 2, I, H]: the gate's matrix, then the up projection's */
+  const void* down;                  /* [E, H, I] */
+  const float* gate_up_scale;        /* [E, 2, ceil(I / 128), ceil(H / 128)] (E4M3), else NULL */
+  const float* down_scale;           /* [E, ceil(H / 128), ceil(I / 128)] */
+  const void* shared_gate_up;        /* [2, Is, H], or NULL without a shared expert */
+  const void* shared_down;           /* [H, Is] */
+  const float* shared_gate_up_scale; /* [2, ceil(Is / 128), ceil(H / 128)] */
+  const float* shared_down_scale;    /* [ceil(H / 128), ceil(Is / 128)] */
+  const gdn_bf16* shared_gate;       /* [H]: its output is multiplied by sigmoid(x . shared_gate); NULL: by 1 */
+} gdn_moe_weights;
+
+#define GDN_SCORE_SOFTMAX 0 /* over all E experts */
+#define GDN_SCORE_SIGMOID 1
+typedef struct {
+  int32_t top_k;       /* at most GDN_MOE_MAX_TOP_K and E */
+  int32_t scoring;     /* GDN_SCORE_* */
+  int32_t renormalise; /* nonzero: a token's chosen scores are divided by their sum */
+  float scale;         /* multiplies the weights; finite */
+} gdn_moe_routing;
+
+/* Bytes of device workspace of the two calls for this many tokens and experts a token (0 for an unsupported geometry);
+ * it needs no initialisation and is dead when the call's kernels finish. */
+GDN_API size_t gdn_moe_workspace_size(const gdn_moe_geometry* geo, int32_t tokens, int32_t top_k);
+
+/*
+ * A whole mixture-of-experts layer for at most GDN_MOE_MAX_TOKENS tokens (a decode step, a speculative one):
+ *   logits = x router^T;   s = softmax(logits) or sigmoid(logits);   chosen: the top_k largest s + router_bias (the
+ *   logits themselves without a bias), ties to the lowest index, NaN last;   weight_e = s_e, or s_e / sum of the
+ *   chosen s, times scale;
+ *   f_e(x) = down_e (silu(gate_e x) * up_e x);
+ *   out = sum over the chosen weight_e f_e(x) + sigmoid(x . shared_gate) f_shared(x).
+ * Logits and sums are fp32, an expert's silu(gate) * up keeps 16 bits of its significand, and out is rounded once to bf16.
+ * The order of the sums depends on the call's arguments alone: two calls give the same bits.
+ *   x        tokens rows of H bf16, x_row_stride elements apart (a multiple of 8)
+ *   ids      [tokens, top_k] int32, receives the chosen experts, largest first, or NULL
+ *   weights  [tokens, top_k] fp32, receives their weights, or NULL
+ *   out      [tokens, H] bf16; overlaps neither x, the weights, ids nor weights
+ *   workspace  256-byte aligned device memory of gdn_moe_workspace_size() bytes; calls that may overlap on the GPU
+ *              (other streams, graphs replayed together) need one each
+ * A token whose x is not finite has a row that is not finite, and changes no other row.  tokens == 0 is a no-op.
+ */
+GDN_API gdn_status gdn_moe_step(const gdn_moe_geometry* geo, const gdn_moe_weights* w, const gdn_moe_routing* routing,
+                                const gdn_bf16* x, int64_t x_row_stride, int32_t tokens, int32_t* ids, float* weights,
+                                gdn_bf16* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The same with the routing given: token t passes the experts ids[t, 0 .. top_k-1] with weights[t, 0 .. top_k-1].  A
+ * negative id stands for no expert (one that another device has, or none: the row is the shared expert's alone, or 0);
+ * an expert named twice counts with the sum of its weights.  An id >= E counts as none and sets
+ * GDN_ERR_DEVICE_ARGUMENT in the device error word.  router and router_bias are not read and may be NULL.
+ */
+GDN_API gdn_status gdn_moe_step_routed(const gdn_moe_geometry* geo, const gdn_moe_weights* w, const int32_t* ids,
+                                       const float* weights, int32_t top_k, const gdn_bf16* x, int64_t x_row_stride,
+                                       int32_t tokens, gdn_bf16* out, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
 /*
  * Waits for `stream`, then reads and clears the library's device error word.  Returns GDN_OK,
  * GDN_ERR_DEVICE_ARGUMENT (a kernel skipped a sequence with bad cu_seqlens entries, or a bad page or
- * length of a paged cache),
+ * length of a paged cache, or an expert that is not there),
  * GDN_ERR_TIMEOUT (a bounded in-kernel wait ran out) or GDN_ERR_CUDA.  The word is per device
  * and shared by all streams; the kernels only ever set bits in it.
  */

@@ -65,10 +65,26 @@ class _RopeScaling(ctypes.Structure):
                 ("original_positions", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double)]
 
 
+class _MoeGeo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("hidden", "inter", "num_experts", "shared_inter")]
+
+
+class _MoeWeights(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+        "router", "router_bias", "gate_up", "down", "gate_up_scale", "down_scale", "shared_gate_up", "shared_down",
+        "shared_gate_up_scale", "shared_down_scale", "shared_gate")]
+
+
+class _MoeRouting(ctypes.Structure):
+    _fields_ = [("top_k", ctypes.c_int32), ("scoring", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 def _configure(lib, debug: bool):
     P, I, F, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
     L = ctypes.c_int64
     G, A, C = ctypes.POINTER(_Geo), ctypes.POINTER(_AttnGeo), ctypes.POINTER(_Cache)
+    MG, MW, MR = ctypes.POINTER(_MoeGeo), ctypes.POINTER(_MoeWeights), ctypes.POINTER(_MoeRouting)
     sig = {
         "gdn_status_string": ([ctypes.c_int], ctypes.c_char_p),
         "gdn_last_error_message": ([], ctypes.c_char_p),
@@ -102,6 +118,11 @@ def _configure(lib, debug: bool):
         "gdn_attn_workspace_size": ([A], S),
         "gdn_attn_prefill": ([A, P, C, P, I, P, P, I, I, F, P, L, L, P, P, S, P], ctypes.c_int),
         "gdn_attn_decode_step": ([A, P, C, P, I, P, I, F, P, L, L, P, P, S, P], ctypes.c_int),
+        "gdn_fp8_quantize": ([P, L, I, I, I, P, L, P, P], ctypes.c_int),
+        "gdn_fp8_matmul": ([P, L, P, P, L, P, I, I, I, I, P, L, P], ctypes.c_int),
+        "gdn_moe_workspace_size": ([MG, I, I], S),
+        "gdn_moe_step": ([MG, MW, MR, P, L, I, P, P, P, P, S, P], ctypes.c_int),
+        "gdn_moe_step_routed": ([MG, MW, P, P, I, P, L, I, P, P, S, P], ctypes.c_int),
         "gdn_check_device_errors": ([P], ctypes.c_int),
     }
     if debug:
@@ -1027,3 +1048,188 @@ def gdn_attn_decode_step(q, cache: KVCache, block_table, kv_lens, softmax_scale,
                          stream=None):
     """gdn_attn_prefill for one new token of every sequence: row n of q [B, Hq, D] is sequence n's."""
     return _attention(q, cache, block_table, kv_lens, None, softmax_scale, z, out, workspace, stream)
+
+
+# ------------------------------------------------------------ 8-bit products and expert layers
+
+FP8_BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def _matrix(t, name, device=None, shape=None):
+    """Address and row stride (elements) of a two-dimensional CUDA tensor whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {shape or '[rows, cols]'}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call is on {device}")
+    stride, one = t.stride()
+    if one != 1 and t.shape[1] > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), stride
+
+
+def _codes(t, name, device=None, shape=None):
+    """_matrix of e4m3 codes; the stride of a single row is of no account."""
+    p, stride = _matrix(t, name, device, shape)
+    if t.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"{name} must be {torch.float8_e4m3fn}, got {t.dtype}")
+    return p, (stride if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16)
+
+
+def gdn_fp8_quantize(x, block_rows=1, codes=None, scales=None, stream=None):
+    """e4m3 codes and fp32 scales of bf16 rows x [rows, cols] (contiguous rows, any stride), a scale for each block of
+    block_rows (1: activations, 128: weights) x 128.  Returns (codes [rows, cols] float8_e4m3fn, whose rows are a multiple
+    of 16 bytes apart, scales [ceil(rows / block_rows), ceil(cols / 128)] float32)."""
+    xp, xs = _matrix(x, "x")
+    if x.dtype is not torch.bfloat16:
+        raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")
+    if block_rows not in (1, FP8_BLOCK):
+        raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}, got {block_rows}")
+    (rows, cols), dev = x.shape, x.device
+    if codes is None:
+        codes = _empty((rows, -(-cols // 16) * 16), torch.float8_e4m3fn, dev, stream)[:, :cols]
+    cp, cs = _codes(codes, "codes", dev, (rows, cols))
+    shape = (-(-rows // block_rows), _blocks(cols))
+    if scales is None:
+        scales = _empty(shape, torch.float32, dev, stream)
+    sp = _flat(scales, torch.float32, "scales", shape, dev)
+    _call(_L().gdn_fp8_quantize, dev, stream, xp, xs if rows > 1 else cols, rows, cols, block_rows, cp, cs, sp)
+    return codes, scales
+
+
+def gdn_fp8_matmul(x, x_scale, w, w_scale, out=None, out_dtype=torch.bfloat16, stream=None):
+    """Activations x [T, K] times weights w [N, K], both e4m3 codes whose rows are a multiple of 16 bytes apart, with
+    scales x_scale [T, ceil(K / 128)] and w_scale [ceil(N / 128), ceil(K / 128)] float32.  Returns out [T, N], bf16 or
+    float32 (contiguous rows, any stride)."""
+    xp, xs = _codes(x, "x")
+    dev = x.device
+    wp, ws = _codes(w, "w", dev)
+    (T, K), N = x.shape, w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"x and w must have the same number of columns, got {K} and {w.shape[1]}")
+    if out is None:
+        out = _empty((T, N), out_dtype, dev, stream)
+    op, os_ = _matrix(out, "out", dev, (T, N))
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"out must be {torch.bfloat16} or {torch.float32}, got {out.dtype}")
+    _call(_L().gdn_fp8_matmul, dev, stream, xp, xs, _flat(x_scale, torch.float32, "x_scale", (T, _blocks(K)), dev), wp, ws,
+          _flat(w_scale, torch.float32, "w_scale", (_blocks(N), _blocks(K)), dev), T, N, K,
+          out.dtype is torch.float32, op, os_ if T > 1 else N)
+    return out
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+@dataclass(frozen=True, eq=False)
+class Experts:
+    """The weights of one mixture-of-experts layer, checked once: a handle for gdn_moe_step and gdn_moe_step_routed.
+
+    gate_up [E, 2, I, H] and down [E, H, I], bf16 or float8_e4m3fn with a float32 scale for each block of 128 x 128 of
+    every matrix (gate_up_scale [E, 2, ceil(I / 128), ceil(H / 128)], down_scale [E, ceil(H / 128), ceil(I / 128)]);
+    router [E, H] bf16 (not needed where the routing is given) and router_bias [E] float32; a shared expert of width Is
+    the same way (shared_gate_up [2, Is, H], shared_down [H, Is]), its output times sigmoid(x . shared_gate [H] bf16).
+    The tensors' values may change between calls; their memory may not (Tensor.data, resize_).
+    """
+    gate_up: torch.Tensor
+    down: torch.Tensor
+    gate_up_scale: torch.Tensor | None = None
+    down_scale: torch.Tensor | None = None
+    router: torch.Tensor | None = None
+    router_bias: torch.Tensor | None = None
+    shared_gate_up: torch.Tensor | None = None
+    shared_down: torch.Tensor | None = None
+    shared_gate_up_scale: torch.Tensor | None = None
+    shared_down_scale: torch.Tensor | None = None
+    shared_gate: torch.Tensor | None = None
+
+    def __post_init__(self):
+        w = self.gate_up
+        if not isinstance(w, torch.Tensor) or not w.is_cuda:
+            raise TypeError("gate_up must be a CUDA tensor")
+        if w.dim() != 4 or w.shape[1] != 2:
+            raise ValueError(f"gate_up must have shape [E, 2, I, H], got {tuple(w.shape)}")
+        e4m3, dev = w.dtype is torch.float8_e4m3fn, w.device
+        kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+        E, _, I, H = w.shape
+        Is = 0
+        if self.shared_gate_up is not None:
+            if not isinstance(self.shared_gate_up, torch.Tensor) or self.shared_gate_up.dim() != 3:
+                raise ValueError("shared_gate_up must have shape [2, Is, H]")
+            Is = self.shared_gate_up.shape[1]
+        hb, ib, sb = _blocks(H), _blocks(I), _blocks(Is)
+        f32 = torch.float32
+        shapes = {"router": (torch.bfloat16, (E, H)), "router_bias": (f32, (E,)), "gate_up": (kind, (E, 2, I, H)),
+                  "down": (kind, (E, H, I)), "gate_up_scale": (f32, (E, 2, ib, hb)), "down_scale": (f32, (E, hb, ib)),
+                  "shared_gate_up": (kind, (2, Is, H)), "shared_down": (kind, (H, Is)),
+                  "shared_gate_up_scale": (f32, (2, sb, hb)), "shared_down_scale": (f32, (hb, sb)),
+                  "shared_gate": (torch.bfloat16, (H,))}
+        for name in shapes:
+            t = getattr(self, name)
+            scale, shared = name.endswith("_scale"), name.startswith("shared")
+            needed = not name.startswith("router") and name != "shared_gate" and (not scale or e4m3) and (not shared or Is)
+            if needed and t is None:
+                raise ValueError(f"{name} is missing")
+            if t is not None and ((scale and not e4m3) or (shared and not Is)):
+                raise ValueError(f"{name} goes with {'e4m3 weights' if scale and not e4m3 else 'a shared expert'} alone")
+        ptrs = [_flat(getattr(self, n), dtype, n, shape, dev) for n, (dtype, shape) in shapes.items()]
+        object.__setattr__(self, "_device", dev)
+        object.__setattr__(self, "_geo", _MoeGeo(H, I, E, Is))
+        object.__setattr__(self, "_weights", _MoeWeights(int(e4m3), *ptrs))
+
+
+def gdn_moe_workspace_size(experts: Experts, tokens: int, top_k: int) -> int:
+    return int(_L().gdn_moe_workspace_size(experts._geo, tokens, top_k))
+
+
+def _moe(fn, x, experts, top_k, head, tail, out, workspace, stream):
+    """A call of the expert layer: fn(geometry, weights, *head, x, stride, tokens, *tail, out, workspace, bytes)."""
+    dev, H = experts._device, experts._geo.hidden
+    xp, xs = _matrix(x, "x", dev, (x.shape[0], H) if isinstance(x, torch.Tensor) and x.dim() == 2 else None)
+    if x.dtype is not torch.bfloat16:
+        raise TypeError(f"x must be {torch.bfloat16}, got {x.dtype}")
+    T = x.shape[0]
+    if out is None:
+        out = _empty((T, H), torch.bfloat16, dev, stream)
+    op = _flat(out, torch.bfloat16, "out", (T, H), dev)
+    if workspace is None:
+        need = _L().gdn_moe_workspace_size(experts._geo, T, top_k)
+        workspace = _empty(max(need, 1), torch.uint8, dev, stream)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, the call is on {dev}")
+    _call(fn, dev, stream, experts._geo, experts._weights, *head, xp, xs if T > 1 else H, T, *tail, op,
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out
+
+
+def gdn_moe_step(x, experts: Experts, top_k, scoring="softmax", renormalise=True, scale=1.0, out=None, ids=None,
+                 weights=None, workspace=None, stream=None):
+    """A whole mixture-of-experts layer for a few tokens (at most 64): x [T, H] bf16 with contiguous rows, a multiple of 8
+    values apart.  Scores are "softmax" or "sigmoid" of the router's logits; each token takes its top_k experts, weighted by
+    their scores (divided by their sum where renormalise) times scale.  ids [T, top_k] int32 and weights [T, top_k] float32
+    receive the choice where given.  Returns out [T, H] bf16.  Without a workspace the call takes one from PyTorch's
+    allocator."""
+    if scoring not in _SCORES:
+        raise ValueError(f"scoring must be one of {sorted(_SCORES)}, got {scoring!r}")
+    if experts.router is None:
+        raise ValueError("gdn_moe_step needs the experts' router")
+    shape, dev = (x.shape[0], top_k) if isinstance(x, torch.Tensor) else None, experts._device
+    ip, wp = _flat(ids, torch.int32, "ids", shape, dev), _flat(weights, torch.float32, "weights", shape, dev)
+    routing = _MoeRouting(top_k, _SCORES[scoring], bool(renormalise), scale)
+    return _moe(_L().gdn_moe_step, x, experts, top_k, (routing,), (ip, wp), out, workspace, stream)
+
+
+def gdn_moe_step_routed(x, experts: Experts, ids, weights, out=None, workspace=None, stream=None):
+    """gdn_moe_step with the routing given: ids [T, top_k] int32 (negative: no expert) and weights [T, top_k] float32."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise TypeError("ids must be a CUDA tensor [T, top_k]")
+    shape, dev = (x.shape[0] if isinstance(x, torch.Tensor) else None, ids.shape[1]), experts._device
+    if weights is None:
+        raise TypeError("weights must be a CUDA tensor")
+    ip, wp = _flat(ids, torch.int32, "ids", shape, dev), _flat(weights, torch.float32, "weights", shape, dev)
+    return _moe(_L().gdn_moe_step_routed, x, experts, shape[1], (ip, wp, shape[1]), (), out, workspace, stream)

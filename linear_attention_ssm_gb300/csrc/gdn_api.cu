@@ -973,6 +973,238 @@ gdn_status gdn_attn_decode_step(const gdn_attn_geometry* geo, const gdn_bf16* q,
 
 }  // extern "C"
 
+namespace {
+
+constexpr int64_t kMaxStride = (int64_t)1 << 40;  // bytes: what a tensor map holds
+
+size_t span(int64_t rows, int64_t stride, int64_t cols) { return (size_t)((rows - 1) * stride + cols); }
+
+// rows of codes
+gdn_status check_codes(const uint8_t* p, int64_t stride, int32_t cols, const char* name) {
+  GDN_REQUIRE(p, name);
+  if (stride < cols || stride >= kMaxStride)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "the row stride of %s (%lld) must be at least its %d columns and below 2^40",
+                name, (long long)stride, cols);
+  if (stride & 15)
+    return fail(GDN_ERR_MISALIGNED, "the row stride of %s (%lld) must be a multiple of 16 bytes", name, (long long)stride);
+  return GDN_OK;
+}
+
+gdn_status check_moe_geometry(const gdn_moe_geometry* geo) {
+  if (!geo) return fail(GDN_ERR_INVALID_ARGUMENT, "geometry is NULL");
+  const struct {
+    int v;
+    const char* name;
+    int least;
+  } widths[3] = {{geo->hidden, "hidden", 16}, {geo->inter, "inter", 16}, {geo->shared_inter, "shared_inter", 0}};
+  for (const auto& w : widths)
+    if (w.v < w.least || w.v > GDN_MOE_MAX_WIDTH || w.v % 16)
+      return fail(GDN_ERR_UNSUPPORTED_GEOMETRY, "%s (%d) must be a multiple of 16 from %d to %d", w.name, w.v, w.least,
+                  GDN_MOE_MAX_WIDTH);
+  if (geo->num_experts < 1 || geo->num_experts > GDN_MOE_MAX_EXPERTS)
+    return fail(GDN_ERR_UNSUPPORTED_GEOMETRY, "num_experts (%d) must be 1 to %d", geo->num_experts, GDN_MOE_MAX_EXPERTS);
+  return GDN_OK;
+}
+
+gdn_status check_moe_size(int32_t tokens, int32_t top_k) {
+  if (tokens < 0 || tokens > GDN_MOE_MAX_TOKENS)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "tokens (%d) must be 0 to %d", tokens, GDN_MOE_MAX_TOKENS);
+  if (top_k < 1 || top_k > GDN_MOE_MAX_TOP_K)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "top_k (%d) must be 1 to %d", top_k, GDN_MOE_MAX_TOP_K);
+  return GDN_OK;
+}
+
+gdn::Moe moe_of(const gdn_moe_geometry* g, const gdn_moe_weights* w) {
+  return {g->hidden, g->inter, g->num_experts, g->shared_inter,
+          w ? w->router : nullptr, w ? w->router_bias : nullptr, w ? w->gate_up : nullptr, w ? w->down : nullptr,
+          w ? w->shared_gate_up : nullptr, w ? w->shared_down : nullptr, w ? w->gate_up_scale : nullptr,
+          w ? w->down_scale : nullptr, w ? w->shared_gate_up_scale : nullptr, w ? w->shared_down_scale : nullptr,
+          w ? w->shared_gate : nullptr};
+}
+
+// Both calls of the expert layer; `c` has the routing.
+gdn_status moe_step(const gdn_moe_geometry* geo, const gdn_moe_weights* w, gdn::MoeCall c, const gdn_bf16* x,
+                    int64_t x_row_stride, int32_t tokens, gdn_bf16* out, void* workspace, size_t workspace_bytes,
+                    void* stream) {
+  gdn_status s;
+  if (tokens == 0) return ok();
+  if (!w) return fail(GDN_ERR_INVALID_ARGUMENT, "weights is NULL");
+  if (w->type != GDN_WEIGHT_BF16 && w->type != GDN_WEIGHT_E4M3)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "unknown weight type %d", w->type);
+  const bool e4m3 = w->type == GDN_WEIGHT_E4M3, shared = geo->shared_inter > 0;
+  const size_t H = geo->hidden, I = geo->inter, E = geo->num_experts, Is = geo->shared_inter, T = tokens;
+  const size_t K = c.top_k, size = e4m3 ? 1 : 2, hb = (H + 127) / 128, ib = (I + 127) / 128, sb = (Is + 127) / 128;
+  GDN_REQUIRE(x, "x");
+  GDN_REQUIRE(out, "out");
+  if (x_row_stride & 7)
+    return fail(GDN_ERR_MISALIGNED, "the row stride of x (%lld) must be a multiple of 8 elements", (long long)x_row_stride);
+  if (tokens > 1 && (x_row_stride < geo->hidden || x_row_stride >= kMaxStride / 2))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "the row stride of x (%lld) must be at least hidden (%d) and below 2^39",
+                (long long)x_row_stride, geo->hidden);
+  const struct {
+    const void* p;
+    size_t bytes;
+    const char* name;
+    bool needed, allowed;
+  } parts[] = {{w->router, E * H * 2, "router", !c.ids_in, !c.ids_in},
+               {w->router_bias, E * 4, "router_bias", false, !c.ids_in},
+               {w->gate_up, E * 2 * I * H * size, "gate_up", true, true},
+               {w->down, E * I * H * size, "down", true, true},
+               {w->gate_up_scale, E * 2 * ib * hb * 4, "gate_up_scale", e4m3, e4m3},
+               {w->down_scale, E * ib * hb * 4, "down_scale", e4m3, e4m3},
+               {w->shared_gate_up, 2 * Is * H * size, "shared_gate_up", shared, shared},
+               {w->shared_down, Is * H * size, "shared_down", shared, shared},
+               {w->shared_gate_up_scale, 2 * sb * hb * 4, "shared_gate_up_scale", shared && e4m3, shared && e4m3},
+               {w->shared_down_scale, sb * hb * 4, "shared_down_scale", shared && e4m3, shared && e4m3},
+               {w->shared_gate, H * 2, "shared_gate", false, shared},
+               {x, span(T, T > 1 ? x_row_stride : geo->hidden, geo->hidden) * 2, "x", true, true},
+               {c.ids_in, T * K * 4, "ids", false, true},
+               {c.weights_in, T * K * 4, "weights", false, true}};
+  const struct {
+    const void* p;
+    size_t bytes;
+    const char* name;
+  } outs[] = {{out, T * H * 2, "out"}, {c.ids_out, T * K * 4, "ids"}, {c.weights_out, T * K * 4, "weights"}};
+  for (const auto& a : parts) {
+    if (!a.allowed) continue;  // not read
+    if (a.needed) GDN_REQUIRE(a.p, a.name);
+    GDN_OPTIONAL(a.p, a.name);
+    for (const auto& o : outs)
+      if (a.p && o.p && overlaps(a.p, a.bytes, o.p, o.bytes))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "%s overlaps %s", o.name, a.name);
+  }
+  for (int i = 0; i < 3; ++i) {
+    GDN_OPTIONAL(outs[i].p, outs[i].name);
+    for (int j = 0; j < i; ++j)
+      if (outs[i].p && outs[j].p && overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
+        return fail(GDN_ERR_INVALID_ARGUMENT, "%s overlaps %s", outs[i].name, outs[j].name);
+  }
+  const gdn::Moe m = moe_of(geo, w);
+  const size_t need = gdn::moe_workspace_bytes(m, tokens, c.top_k);
+  if (!workspace || workspace_bytes < need)
+    return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, workspace ? workspace_bytes : 0);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(GDN_ERR_MISALIGNED, "workspace is not 256-byte aligned");
+  for (const auto& a : parts)
+    if (a.allowed && a.p && overlaps(a.p, a.bytes, workspace, need))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "workspace overlaps %s", a.name);
+  for (const auto& o : outs)
+    if (o.p && overlaps(o.p, o.bytes, workspace, need))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "workspace overlaps %s", o.name);
+  c.x = x;
+  c.x_stride = tokens > 1 ? x_row_stride : geo->hidden;
+  c.T = tokens;
+  c.out = out;
+  gdn::LaunchEnv env;
+  if ((s = make_env(stream, &env)) != GDN_OK) return s;
+  return launched(gdn::launch_moe(env, m, c, workspace), "expert layer launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_fp8_quantize(const gdn_bf16* x, int64_t x_row_stride, int32_t rows, int32_t cols, int32_t block_rows,
+                            uint8_t* codes, int64_t codes_row_stride, float* scales, void* stream) {
+  gdn_status s;
+  if (rows < 0 || cols < 1)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "rows (%d) must not be negative, cols (%d) must be positive", rows, cols);
+  if (block_rows != 1 && block_rows != GDN_FP8_BLOCK)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "block_rows (%d) must be 1 or %d", block_rows, GDN_FP8_BLOCK);
+  if (rows == 0) return ok();
+  GDN_REQUIRE(x, "x");
+  if (x_row_stride < cols || x_row_stride >= kMaxStride)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "the row stride of x (%lld) must be at least its %d columns and below 2^40",
+                (long long)x_row_stride, cols);
+  if ((s = check_codes(codes, codes_row_stride, cols, "codes")) != GDN_OK) return s;
+  GDN_REQUIRE(scales, "scales");
+  const size_t nx = span(rows, x_row_stride, cols) * 2, nc = span(rows, codes_row_stride, cols);
+  const size_t ns = (size_t)(((int64_t)rows + block_rows - 1) / block_rows) * (((int64_t)cols + 127) / 128) * 4;
+  if (overlaps(x, nx, codes, nc) || overlaps(x, nx, scales, ns))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "codes or scales overlap x");
+  if (overlaps(codes, nc, scales, ns)) return fail(GDN_ERR_INVALID_ARGUMENT, "scales overlap codes");
+  gdn::LaunchEnv env;
+  if ((s = make_env(stream, &env)) != GDN_OK) return s;
+  return launched(gdn::launch_fp8_quantize(env, x, x_row_stride, rows, cols, block_rows, codes, codes_row_stride, scales),
+                  "quantisation launch");
+}
+
+gdn_status gdn_fp8_matmul(const uint8_t* x, int64_t x_row_stride, const float* x_scale, const uint8_t* w,
+                          int64_t w_row_stride, const float* w_scale, int32_t tokens, int32_t n, int32_t k,
+                          int32_t out_type, void* out, int64_t out_row_stride, void* stream) {
+  gdn_status s;
+  if (tokens < 0 || n < 0 || k < 1)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "tokens (%d) and n (%d) must not be negative, k (%d) must be positive", tokens, n,
+                k);
+  if (out_type != GDN_OUT_BF16 && out_type != GDN_OUT_F32)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "unknown output type %d", out_type);
+  if (tokens == 0 || n == 0) return ok();
+  if ((s = check_codes(x, x_row_stride, k, "x")) != GDN_OK) return s;
+  if ((s = check_codes(w, w_row_stride, k, "w")) != GDN_OK) return s;
+  GDN_REQUIRE(x_scale, "x_scale");
+  GDN_REQUIRE(w_scale, "w_scale");
+  GDN_REQUIRE(out, "out");
+  if (out_row_stride < n || out_row_stride >= kMaxStride)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "the row stride of out (%lld) must be at least its %d columns and below 2^40",
+                (long long)out_row_stride, n);
+  const size_t kb = ((size_t)k + 127) / 128, nb = ((size_t)n + 127) / 128;
+  const size_t no = span(tokens, out_row_stride, n) * (out_type == GDN_OUT_F32 ? 4 : 2);
+  if (overlaps(x, span(tokens, x_row_stride, k), out, no) || overlaps(w, span(n, w_row_stride, k), out, no) ||
+      overlaps(x_scale, tokens * kb * 4, out, no) || overlaps(w_scale, nb * kb * 4, out, no))
+    return fail(GDN_ERR_INVALID_ARGUMENT, "out overlaps an input");
+  gdn::LaunchEnv env;
+  if ((s = make_env(stream, &env)) != GDN_OK) return s;
+  return launched(gdn::launch_fp8_matmul(env, {x, x_row_stride, x_scale, w, w_row_stride, w_scale, tokens, n, k, out,
+                                               out_row_stride, out_type == GDN_OUT_F32}),
+                  "8-bit product launch");
+}
+
+size_t gdn_moe_workspace_size(const gdn_moe_geometry* geo, int32_t tokens, int32_t top_k) {
+  if (check_moe_geometry(geo) != GDN_OK || check_moe_size(tokens, top_k) != GDN_OK || tokens == 0) return 0;
+  return gdn::moe_workspace_bytes(moe_of(geo, nullptr), tokens, top_k);
+}
+
+gdn_status gdn_moe_step(const gdn_moe_geometry* geo, const gdn_moe_weights* w, const gdn_moe_routing* routing,
+                        const gdn_bf16* x, int64_t x_row_stride, int32_t tokens, int32_t* ids, float* weights,
+                        gdn_bf16* out, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_status s = check_moe_geometry(geo);
+  if (s != GDN_OK) return s;
+  if (!routing) return fail(GDN_ERR_INVALID_ARGUMENT, "routing is NULL");
+  if ((s = check_moe_size(tokens, routing->top_k)) != GDN_OK) return s;
+  if (routing->top_k > geo->num_experts)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "top_k (%d) exceeds the %d experts", routing->top_k, geo->num_experts);
+  if (routing->scoring != GDN_SCORE_SOFTMAX && routing->scoring != GDN_SCORE_SIGMOID)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "unknown scoring %d", routing->scoring);
+  if (!std::isfinite(routing->scale)) return fail(GDN_ERR_INVALID_ARGUMENT, "scale must be finite");
+  gdn::MoeCall c = {};
+  c.top_k = routing->top_k;
+  c.sigmoid = routing->scoring == GDN_SCORE_SIGMOID;
+  c.renormalise = routing->renormalise != 0;
+  c.scale = routing->scale;
+  c.ids_out = ids;
+  c.weights_out = weights;
+  return moe_step(geo, w, c, x, x_row_stride, tokens, out, workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_moe_step_routed(const gdn_moe_geometry* geo, const gdn_moe_weights* w, const int32_t* ids,
+                               const float* weights, int32_t top_k, const gdn_bf16* x, int64_t x_row_stride,
+                               int32_t tokens, gdn_bf16* out, void* workspace, size_t workspace_bytes, void* stream) {
+  gdn_status s = check_moe_geometry(geo);
+  if (s != GDN_OK) return s;
+  if ((s = check_moe_size(tokens, top_k)) != GDN_OK) return s;
+  if (tokens == 0) return ok();
+  GDN_REQUIRE(ids, "ids");
+  GDN_REQUIRE(weights, "weights");
+  gdn::MoeCall c = {};
+  c.top_k = top_k;
+  c.scale = 1.f;
+  c.ids_in = ids;
+  c.weights_in = weights;
+  return moe_step(geo, w, c, x, x_row_stride, tokens, out, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
 extern "C" {
 
 gdn_status gdn_check_device_errors(void* stream) {
@@ -991,7 +1223,7 @@ gdn_status gdn_check_device_errors(void* stream) {
   }
   if (word & gdn::kErrTimeout) return fail(GDN_ERR_TIMEOUT, "an in-kernel wait ran out (word 0x%x)", word);
   if (word & gdn::kErrDeviceArgument)
-    return fail(GDN_ERR_DEVICE_ARGUMENT, "a kernel rejected cu_seqlens, page or length contents (word 0x%x)", word);
+    return fail(GDN_ERR_DEVICE_ARGUMENT, "a kernel rejected cu_seqlens, page, length or expert contents (word 0x%x)", word);
   return ok();
 }
 

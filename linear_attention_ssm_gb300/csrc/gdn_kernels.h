@@ -158,4 +158,46 @@ cudaError_t launch_attn(const LaunchEnv& env, int Hq, int Hkv, int D, const uint
                         const int32_t* kv_lens, const int32_t* cu, int N, int T, float scale, const HeadRows& z,
                         uint16_t* out, void* workspace);
 
+// 8-bit products (fp8_quantize.cu, fp8_matmul.cu): e4m3 codes with fp32 scales by blocks of 128.
+cudaError_t launch_fp8_quantize(const LaunchEnv& env, const uint16_t* x, long x_stride, int rows, int cols, int block_rows,
+                                uint8_t* codes, long codes_stride, float* scales);
+struct Fp8Matmul {
+  const uint8_t* x;  // [tokens] rows of k codes
+  long x_stride;
+  const float* x_scale;  // [tokens][ceil(k / 128)]
+  const uint8_t* w;      // [n] rows of k codes
+  long w_stride;
+  const float* w_scale;  // [ceil(n / 128)][ceil(k / 128)]
+  int tokens, n, k;
+  void* out;  // [tokens] rows of n, bf16 or fp32
+  long out_stride;
+  bool out_f32;
+};
+cudaError_t launch_fp8_matmul(const LaunchEnv& env, const Fp8Matmul& p);
+
+// A mixture-of-experts layer for a few tokens (moe.cu).
+struct Moe {
+  int H, I, E, Is;  // Is: the shared expert's width, 0 without one
+  const uint16_t* router;
+  const float* router_bias;
+  const void *gate_up, *down, *shared_gate_up, *shared_down;  // bf16, or e4m3 where scales are given
+  const float *gate_up_scale, *down_scale, *shared_gate_up_scale, *shared_down_scale;
+  const uint16_t* shared_gate;
+};
+struct MoeCall {
+  const uint16_t* x;
+  long x_stride;
+  int T, top_k;
+  bool sigmoid, renormalise;
+  float scale;
+  const int32_t* ids_in;  // set: the routing is given, with weights_in
+  const float* weights_in;
+  int32_t* ids_out;  // or NULL
+  float* weights_out;
+  uint16_t* out;
+  unsigned* err;
+};
+size_t moe_workspace_bytes(const Moe& m, int T, int top_k);
+cudaError_t launch_moe(const LaunchEnv& env, const Moe& m, MoeCall c, void* workspace);
+
 }  // namespace gdn
