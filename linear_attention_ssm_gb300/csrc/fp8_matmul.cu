@@ -17,6 +17,14 @@ namespace {
 constexpr int kBlockK = 128;  // codes of a stage's row, one scale block
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before giving up
 
+// One lane of the warp.  What it issues has operands that are the same in every lane, so that they need not be gathered
+// from one: four products and two arrivals take 340 cycles of the issuing warp this way, 560 under `lane == 0`.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one;
+}
+
 // Instruction descriptor: D fp32, A and B e4m3, both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -41,10 +49,14 @@ __device__ __forceinline__ void mma_e4m3_k4(uint32_t d_tmem, uint64_t a_desc, ui
 struct MatmulParams {
   CUtensorMap tmap_x;  // [tokens][k] codes, 128-byte swizzle
   CUtensorMap tmap_w;  // [n][k]
+  const uint8_t *x, *w;
+  long x_stride, w_stride;
   const float* x_scale;
   const float* w_scale;
-  int tokens, n, blocks;  // blocks: of k
+  int tokens, n, k, blocks;  // blocks: of k
   int split;              // CTAs that share a tile's k
+  int tiles_m, tiles_n;
+  int wide_out;           // rows of out are whole 32-byte sectors
   void* out;
   long out_stride;
   int out_f32;
@@ -72,17 +84,138 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
+// ---------------------------------------------------------------- up to 16 tokens: weights through the registers once
+
+// D += A B, m16n8k16 with binary16 operands and fp32 sums.  Lane l has rows l / 4 and l / 4 + 8 of A at the k of its
+// place l % 4, column l / 4 of B at the same k, and columns 2 (l % 4), + 1 of D's two rows.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float code_value(const uint8_t* p) {
+  uint32_t b;
+  asm volatile("ld.global.u8 %0, [%1];" : "=r"(b) : "l"(p));
+  return __half2float(__ushort_as_half((unsigned short)e4m3x4_to_half4(b).x));
+}
+
+constexpr int kFewWarps = 8;
+
+// One CTA: 16 rows of w and up to 8 kTiles tokens; its warps share the blocks of k.  A lane takes 16 codes of its two rows
+// and of its token at a time and widens them to binary16, which holds them exactly; which of a quad's lanes has which k does
+// not matter as long as both operands agree.  HBM bounds the kernel: 16 KB of weights in flight for each CTA, several CTAs an
+// SM, no barrier before the sums meet.
+template <int kTiles>
+__global__ void __launch_bounds__(kFewWarps * 32, kTiles == 1 ? 3 : 2) few_kernel(const __grid_constant__ MatmulParams p) {
+  __shared__ float parts[kFewWarps][kTiles][4][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const long n0 = (long)blockIdx.x * 16;
+  await_grid();
+  float acc[kTiles][4];
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  const uint8_t *wa = p.w + (n0 + r) * p.w_stride, *wb = wa + 8 * p.w_stride;
+  const bool has_a = n0 + r < p.n, has_b = n0 + r + 8 < p.n;
+  const float* sw = p.w_scale + (n0 >> 7) * p.blocks;
+
+  constexpr int kAhead = 2;  // blocks loaded together
+  const int whole = p.k & ~15;  // codes that come 16 at a time
+  for (int b0 = warp * kAhead; b0 < p.blocks; b0 += kFewWarps * kAhead) {
+    uint4 a[kAhead][4], x[kAhead][kTiles][2];
+    float s[kAhead][kTiles][2];
+    const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int b = b0 + u, k0 = b * kBlockK + c * 16, k1 = k0 + 64;
+      const bool in = b < p.blocks;
+      a[u][0] = in && has_a && k0 < whole ? ld_once(wa + k0) : none;
+      a[u][1] = in && has_b && k0 < whole ? ld_once(wb + k0) : none;
+      a[u][2] = in && has_a && k1 < whole ? ld_once(wa + k1) : none;
+      a[u][3] = in && has_b && k1 < whole ? ld_once(wb + k1) : none;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        const long t = i * 8 + r;
+        const uint8_t* row = p.x + t * p.x_stride;
+        const bool has = in && t < p.tokens;
+        x[u][i][0] = has && k0 < whole ? ld_once(row + k0) : none;
+        x[u][i][1] = has && k1 < whole ? ld_once(row + k1) : none;
+        const long q = i * 8 + 2 * c;
+        s[u][i][0] = in && q < p.tokens ? p.x_scale[q * p.blocks + b] * sw[b] : 0.f;
+        s[u][i][1] = in && q + 1 < p.tokens ? p.x_scale[(q + 1) * p.blocks + b] * sw[b] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float d[kTiles][4];
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t va[4] = {a[u][2 * h].x, a[u][2 * h].y, a[u][2 * h].z, a[u][2 * h].w};
+        const uint32_t vb[4] = {a[u][2 * h + 1].x, a[u][2 * h + 1].y, a[u][2 * h + 1].z, a[u][2 * h + 1].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint2 fa = e4m3x4_to_half4(va[q]), fb = e4m3x4_to_half4(vb[q]);
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i) {
+            const uint32_t vx[4] = {x[u][i][h].x, x[u][i][h].y, x[u][i][h].z, x[u][i][h].w};
+            const uint2 fx = e4m3x4_to_half4(vx[q]);
+            mma_f16(d[i], fa.x, fb.x, fa.y, fb.y, fx.x, fx.y);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(d[i][j], s[u][i][j & 1], acc[i][j]);
+    }
+  }
+  if (whole < p.k && warp == 0) {  // the last codes of a row, one by one
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const long t = i * 8 + 2 * c + (j & 1);
+        if (t >= p.tokens || !(j < 2 ? has_a : has_b)) continue;
+        float d = 0.f;
+        for (int k = whole; k < p.k; ++k) d = fmaf(code_value((j < 2 ? wa : wb) + k), code_value(p.x + t * p.x_stride + k), d);
+        acc[i][j] = fmaf(d, p.x_scale[t * p.blocks + p.blocks - 1] * sw[p.blocks - 1], acc[i][j]);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) parts[warp][i][j][lane] = acc[i][j];
+  __syncthreads();
+  // value v of the tile: row v % 16 of the weights, token v / 16
+  for (int v = threadIdx.x; v < kTiles * 128; v += kFewWarps * 32) {
+    const int row = v & 15, t = v >> 4;
+    if (n0 + row >= p.n || t >= p.tokens) continue;
+    const int j = (row >> 3) * 2 + (t & 1), l = (row & 7) * 4 + (t & 7) / 2;
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kFewWarps; ++w) y += parts[w][t >> 3][j][l];
+    store_out(p, t, n0 + row, y);
+  }
+}
+
 // ---------------------------------------------------------------- few tokens: weights as the rows of a tile
 
 template <int kTokens>
 struct Narrow {
   static constexpr int kStageBytes = (128 + kTokens) * kBlockK;
   static constexpr int kStages = kTokens <= 16 ? 6 : kTokens <= 32 ? 5 : kTokens <= 64 ? 4 : 3;
-  static constexpr int kColumns = 2 * kTokens < 32 ? 32 : 2 * kTokens;  // of tensor memory
+  static constexpr int kBufs = kTokens <= 32 ? 8 : 256 / kTokens;  // results of blocks in tensor memory
+  static constexpr int kColumns = kBufs * kTokens;
   static constexpr int kParts = kTokens > 64 ? 2 : 1;  // of a row's sums, each in a thread of its own
   static constexpr int kCols = kTokens / kParts;
   static constexpr int kThreads = 64 + 128 * kParts;  // loads, products, sums
-  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + 4 * 2 * kTokens * 4 + 256;
+  static constexpr int kAhead = 8;  // blocks whose scales are fetched together, one such group ahead
+  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + 2 * kAhead * kTokens * 4 + 256;
   static_assert(kTokens * 128 * 4 <= kStages * kStageBytes, "the sums lie in the ring at the end");
 };
 
@@ -93,10 +226,10 @@ __global__ void __launch_bounds__(Narrow<kTokens>::kThreads, 2) narrow_kernel(co
   using C = Narrow<kTokens>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  float* scales = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);  // [warps][2][kCols]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scales + 4 * 2 * kTokens);
+  float* scales = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);  // [kParts][2][kAhead][kCols]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scales + 2 * C::kAhead * kTokens);
   __shared__ uint32_t tmem_slot;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, done = empty + 8 * C::kStages, taken = done + 16;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, done = empty + 8 * C::kStages, taken = done + 8 * C::kBufs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = p.split, rank = blockIdx.x % split;
   const long n0 = (long)(blockIdx.x / split) * 128, t0 = (long)blockIdx.y * kTokens;
@@ -106,7 +239,7 @@ __global__ void __launch_bounds__(Narrow<kTokens>::kThreads, 2) narrow_kernel(co
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(done + 8 * i, 1);
       mbar_init(taken + 8 * i, 4 * C::kParts);
     }
@@ -127,84 +260,91 @@ __global__ void __launch_bounds__(Narrow<kTokens>::kThreads, 2) narrow_kernel(co
 #pragma unroll
   for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
   bool ok = true;
-  // A bounded wait; after one that ran out this warp takes no more work, and the others' waits run out in turn.
+  // A bounded wait of the whole warp; after one that ran out it takes no more work, and the others' waits run out in
+  // turn.
   auto await = [&](uint32_t bar, uint32_t parity) {
     if (ok && !mbar_wait(bar, parity, kWaitLimit)) {
       raise_error(p.err, kErrTimeout);
       ok = false;
     }
-    return ok;
+    return ok = __all_sync(~0u, ok);
   };
   if (warp == 0) {
-    if (lane == 0) {
-      int b = b0;
-      for (; b < b1; ++b) {
-        const int i = (b - b0) % C::kStages, pass = (b - b0) / C::kStages;
-        if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
-        const uint32_t at = smem_u32(smem + i * C::kStageBytes);
+    int b = b0;
+    for (; b < b1; ++b) {
+      const int i = (b - b0) % C::kStages, pass = (b - b0) / C::kStages;
+      if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
+      const uint32_t at = smem_u32(smem + i * C::kStageBytes);
+      if (elect_one()) {
         mbar_arrive_expect_tx(full + 8 * i, C::kStageBytes);
         tma_load_2d(at, &p.tmap_w, b * kBlockK, (int)n0, full + 8 * i);
         tma_load_2d(at + 128 * kBlockK, &p.tmap_x, b * kBlockK, (int)t0, full + 8 * i);
       }
-      // copies in flight land before the CTA ends, after a wait that ran out too
-      for (int c = max(b0, b - C::kStages); c < b; ++c)
-        mbar_wait(full + 8 * ((c - b0) % C::kStages), ((c - b0) / C::kStages) & 1, kWaitLimit);
+      __syncwarp();
     }
-    __syncwarp();
+    // copies in flight land before the CTA ends, after a wait that ran out too
+    for (int c = max(b0, b - C::kStages); c < b; ++c)
+      mbar_wait(full + 8 * ((c - b0) % C::kStages), ((c - b0) / C::kStages) & 1, kWaitLimit);
   } else if (warp == 1) {
-    if (lane == 0) {
-      for (int b = b0; b < b1; ++b) {
-        const int j = b - b0, i = j % C::kStages, half = j & 1;
-        if (!await(full + 8 * i, (j / C::kStages) & 1)) break;
-        if (j >= 2 && !await(taken + 8 * half, ((j >> 1) - 1) & 1)) break;
-        tc_fence_after();
-        const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-        mma_e4m3_k4(tmem + half * kTokens, sw128_desc(at), sw128_desc(at + 128 * kBlockK), idesc_e4m3_f32(128, kTokens));
+    for (int b = b0; b < b1; ++b) {
+      const int j = b - b0, i = j % C::kStages, buf = j % C::kBufs;
+      if (!await(full + 8 * i, (j / C::kStages) & 1)) break;
+      if (j >= C::kBufs && !await(taken + 8 * buf, (j / C::kBufs - 1) & 1)) break;
+      tc_fence_after();
+      const uint32_t at = smem_u32(smem + i * C::kStageBytes);
+      if (elect_one()) {
+        mma_e4m3_k4(tmem + buf * kTokens, sw128_desc(at), sw128_desc(at + 128 * kBlockK), idesc_e4m3_f32(128, kTokens));
         mma_commit(empty + 8 * i);
-        mma_commit(done + 8 * half);
+        mma_commit(done + 8 * buf);
       }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     const int quarter = warp & 3;
-    float* mine = scales + (warp - 2) * 2 * kCols;
-    constexpr int kOwn = (kCols + 31) / 32;  // tokens whose scales a lane fetches
-    float next[kOwn], next_w = 0.f;
+    constexpr int kAhead = C::kAhead, kOwn = (kCols * kAhead + 127) / 128;
+    const int part = C::kParts > 1 && warp >= 6, thread = threadIdx.x - 64 - part * 128;
+    float* mine = scales + part * 2 * kAhead * kCols;
+    // the products of the two scales for blocks b .. b + 7: a thread has every 128th
+    float next[kOwn];
     auto fetch = [&](int b) {
-      if (b >= b1) return;
-      next_w = p.w_scale[(n0 >> 7) * p.blocks + b];
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
-        const int c = lane + 32 * i;
+        const int at = thread + 128 * i, ahead = at % kAhead, c = at / kAhead;
         const long t = t0 + col0 + c;
-        next[i] = c < kCols && t < p.tokens ? p.x_scale[t * p.blocks + b] : 0.f;
+        next[i] = 0.f;
+        if (c < kCols && t < p.tokens && b + ahead < b1)
+          next[i] = p.x_scale[t * p.blocks + b + ahead] * p.w_scale[(n0 >> 7) * p.blocks + b + ahead];
       }
     };
     fetch(b0);
-    for (int b = b0; b < b1 && ok; ++b) {
-      const int j = b - b0, half = j & 1;
+    for (int b = b0; b < b1; ++b) {  // to the end after a wait that ran out too: the others are at the barrier
+      const int j = b - b0, buf = j % C::kBufs;
+      const float* now = mine + (j / kAhead & 1) * kAhead * kCols + j % kAhead * kCols;
+      if (j % kAhead == 0) {
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i)
-        if (lane + 32 * i < kCols) mine[half * kCols + lane + 32 * i] = next[i] * next_w;
-      fetch(b + 1);
-      await(done + 8 * half, (j >> 1) & 1);
-      ok = __all_sync(~0u, ok);
-      if (!ok) break;
-      __syncwarp();
+        for (int i = 0; i < kOwn; ++i) {
+          const int at = thread + 128 * i, ahead = at % kAhead, c = at / kAhead;
+          if (c < kCols) mine[(j / kAhead & 1) * kAhead * kCols + ahead * kCols + c] = next[i];
+        }
+        // the group before the last one was read before the last one's barrier
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+        fetch(b + kAhead);
+      }
+      if (!await(done + 8 * buf, (j / C::kBufs) & 1)) continue;
       tc_fence_after();
       constexpr int kStep = kCols < 32 || C::kParts > 1 ? 16 : 32;  // the registers hold no more beside the sums
 #pragma unroll
       for (int c = 0; c < kCols; c += kStep) {
         float d[kStep];
-        tmem_ld_cols<kStep>(tmem + ((uint32_t)(quarter * 32) << 16) + half * kTokens + col0 + c, d);
+        tmem_ld_cols<kStep>(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTokens + col0 + c, d);
         if (c + kStep == kCols) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(taken + 8 * half);
+          if (lane == 0) mbar_arrive(taken + 8 * buf);
         }
 #pragma unroll
         for (int i = 0; i < kStep; i += 4) {
-          const float4 s = *reinterpret_cast<const float4*>(mine + half * kCols + c + i);
+          const float4 s = *reinterpret_cast<const float4*>(now + c + i);
           acc[c + i] = fmaf(d[i], s.x, acc[c + i]);
           acc[c + i + 1] = fmaf(d[i + 1], s.y, acc[c + i + 1]);
           acc[c + i + 2] = fmaf(d[i + 2], s.z, acc[c + i + 2]);
@@ -283,11 +423,331 @@ cudaError_t launch_narrow(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul
   return cudaLaunchKernelEx(&cfg, narrow_kernel<kTokens>, p);
 }
 
+// ---------------------------------------------------------------- many tokens: tokens as the rows of a tile
+
+// kPair: two CTAs of a cluster share a tile of 256 tokens x 256 rows of w.  Each holds 128 of either, their tensor cores
+// read both halves of w (cta_group::2), and each has the sums of its own 128 tokens.  Otherwise a CTA has a tile of 128 x
+// 256 to itself.
+template <bool kPair>
+struct Wide {
+  static constexpr int kTileN = 256, kTileM = kPair ? 256 : 128;
+  static constexpr int kRowsW = kPair ? 128 : 256;  // of w, in a CTA's stage
+  static constexpr int kStageBytes = (128 + kRowsW) * kBlockK;
+  static constexpr int kStages = kPair ? 5 : 3;
+  static constexpr int kWarps = 8;  // of sums: each has 32 tokens x 128 columns
+  static constexpr int kThreads = 64 + 32 * kWarps;
+  static constexpr int kPitch = 33;  // of a warp's 32 x 32 values on their way out
+  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kWarps * 32 * kPitch * 4 + 256;
+};
+
+// as mma_e4m3_k4, by the pair of CTAs
+__device__ __forceinline__ void mma_e4m3_k4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n.reg .pred p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      "setp.ne.b32 p, 0, 0;\n"
+      "setp.ne.b32 q, 1, 0;\n"
+      "add.s64 a1, %1, 2;\nadd.s64 a2, %1, 4;\nadd.s64 a3, %1, 6;\n"
+      "add.s64 b1, %2, 2;\nadd.s64 b2, %2, 4;\nadd.s64 b3, %2, 6;\n"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, q;\n"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, q;\n"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, q;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc)
+      : "memory");
+}
+// mma_commit for the pair: an arrival at the same place in both CTAs
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// a load into this CTA's shared memory that is counted by a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint32_t limit) {
+  for (uint32_t i = 0; i < limit; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+
+// Tile `id` of the grid of tiles: eight rows of tiles at a time, so that the tiles that are worked on together share both
+// operands in L2.
+__device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& m, int& n) {
+  const int group = 8 * tiles_n, g = id / group, in = id - g * group, rows = min(8, tiles_m - 8 * g);
+  n = in / rows;
+  m = 8 * g + in - n * rows;
+}
+
+template <bool kPair>
+__global__ void __launch_bounds__(Wide<kPair>::kThreads, 1) wide_kernel(const __grid_constant__ MatmulParams p) {
+  using C = Wide<kPair>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  float* stage_out = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage_out + C::kWarps * 32 * C::kPitch);
+  __shared__ uint32_t tmem_slot;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, done = empty + 8 * C::kStages, taken = done + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kPair ? blockIdx.x & 1 : 0, first = kPair ? blockIdx.x >> 1 : blockIdx.x,
+            step = kPair ? gridDim.x >> 1 : gridDim.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(done + 8 * i, 1);
+      mbar_init(taken + 8 * i, C::kWarps * (kPair ? 2 : 1));
+    }
+    fence_mbar_init();
+    prefetch_tensormap(&p.tmap_x);
+    prefetch_tensormap(&p.tmap_w);
+  }
+  if (warp == 1) {
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(smem_u32(&tmem_slot), 512);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (kPair) cluster_sync();  // the other CTA's barriers are there
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  await_grid();
+
+  bool ok = true;
+  auto await = [&](uint32_t bar, uint32_t parity) {
+    if (ok && !(kPair ? mbar_wait_cluster(bar, parity, kWaitLimit) : mbar_wait(bar, parity, kWaitLimit))) {
+      raise_error(p.err, kErrTimeout);
+      ok = false;
+    }
+    return ok = __all_sync(~0u, ok);
+  };
+  const int tiles = p.tiles_m * p.tiles_n;
+  if (warp == 0) {
+    int i = 0, pass = 0;  // stage, passes over the ring
+    const uint32_t count = kPair ? in_cta(full, 0) : full;  // loads are counted by the first CTA's barriers
+    for (int id = first; id < tiles && ok; id += step) {
+      int m, n;
+      tile_of(id, p.tiles_m, p.tiles_n, m, n);
+      const int t0 = m * C::kTileM + rank * 128, n0 = n * C::kTileN + rank * 128;
+      for (int b = 0; b < p.blocks; ++b) {
+        if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
+        const uint32_t at = smem_u32(smem + i * C::kStageBytes);
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(full + 8 * i, C::kStageBytes * (kPair ? 2 : 1));
+          if constexpr (kPair) {
+            tma_load_2d_pair(at, &p.tmap_x, b * kBlockK, t0, count + 8 * i);
+            tma_load_2d_pair(at + 128 * kBlockK, &p.tmap_w, b * kBlockK, n0, count + 8 * i);
+          } else {
+            tma_load_2d(at, &p.tmap_x, b * kBlockK, t0, count + 8 * i);
+            tma_load_2d(at + 128 * kBlockK, &p.tmap_w, b * kBlockK, n0, count + 8 * i);
+          }
+        }
+        __syncwarp();
+        if (++i == C::kStages) i = 0, ++pass;
+      }
+    }
+    // copies in flight land before the CTAs end, after a wait that ran out too
+    if (rank == 0)
+      for (int c = 0; c < C::kStages; ++c) {
+        const int passes = pass + (c < i);  // loads into stage c
+        if (passes) mbar_wait(full + 8 * c, (passes - 1) & 1, kWaitLimit);
+      }
+  } else if (warp == 1) {
+    if (rank == 0) {
+      int i = 0, pass = 0, j = 0;
+      for (int id = first; id < tiles && ok; id += step)
+        for (int b = 0; b < p.blocks; ++b, ++j) {
+          const int half = j & 1;
+          if (!await(full + 8 * i, pass & 1)) break;
+          if (j >= 2 && !await(taken + 8 * half, ((j >> 1) - 1) & 1)) break;
+          tc_fence_after();
+          const uint64_t a = sw128_desc(smem_u32(smem + i * C::kStageBytes));
+          const uint64_t w = sw128_desc(smem_u32(smem + i * C::kStageBytes + 128 * kBlockK));
+          if (elect_one()) {
+            if constexpr (kPair) {
+              mma_e4m3_k4_pair(tmem + half * 256, a, w, idesc_e4m3_f32(256, 256));
+              mma_commit_pair(empty + 8 * i);
+              mma_commit_pair(done + 8 * half);
+            } else {
+              mma_e4m3_k4(tmem + half * 256, a, w, idesc_e4m3_f32(128, 256));
+              mma_commit(empty + 8 * i);
+              mma_commit(done + 8 * half);
+            }
+          }
+          __syncwarp();
+          if (++i == C::kStages) i = 0, ++pass;
+        }
+    }
+  } else {
+    const int quarter = warp & 3, side = (warp - 2) >> 2;  // of the columns
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + side * 128;
+    const uint32_t taken_at = kPair ? in_cta(taken, 0) : taken;
+    float* mine = stage_out + (warp - 2) * 32 * C::kPitch;
+    int j = 0;
+    for (int id = first; id < tiles && ok; id += step) {
+      int m, n;
+      tile_of(id, p.tiles_m, p.tiles_n, m, n);
+      const long t0 = (long)m * C::kTileM + rank * 128 + quarter * 32, t = t0 + lane;
+      const long n0 = (long)n * C::kTileN + side * 128;
+      const float* sx = p.x_scale + t * p.blocks;
+      const float* sw = p.w_scale + (n0 >> 7) * p.blocks;
+      const bool in = t < p.tokens && n0 < p.n;
+      float2 acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+      auto scale = [&](int b) { return in && b < p.blocks ? sx[b] * sw[b] : 0.f; };
+      float s0 = scale(0), s1 = scale(1), s2 = scale(2);  // of this block and the next ones
+#pragma unroll 1
+      for (int b = 0; b < p.blocks; ++b, ++j) {
+        const int half = j & 1;
+        if (!await(done + 8 * half, (j >> 1) & 1)) break;
+        tc_fence_after();
+        const float2 s = make_float2(s0, s0);
+        s0 = s1;
+        s1 = s2;
+        s2 = scale(b + 3);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float d[32];
+          tmem_ld32(lanes + half * 256 + c * 32, d);
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (kPair) mbar_arrive_cluster(taken_at + 8 * half);
+              else mbar_arrive(taken_at + 8 * half);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c * 16 + i] = __ffma2_rn(make_float2(d[2 * i], d[2 * i + 1]), s, acc[c * 16 + i]);
+        }
+      }
+      if (!ok) break;
+      if (p.wide_out) {  // whole sectors of a row from its thread
+        if (t < p.tokens) {
+          const long at = t * p.out_stride + n0;
+          if (p.out_f32) {
+            float* to = static_cast<float*>(p.out) + at;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t v[8];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                v[2 * q] = __float_as_uint(acc[4 * i + q].x);
+                v[2 * q + 1] = __float_as_uint(acc[4 * i + q].y);
+              }
+              if (n0 + 8 * i < p.n) st_global32(to + 8 * i, v);
+            }
+          } else {
+            uint16_t* to = static_cast<uint16_t*>(p.out) + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t v[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) v[q] = pack_bf2(acc[8 * i + q].x, acc[8 * i + q].y);
+              if (n0 + 16 * i < p.n) st_global32(to + 16 * i, v);
+            }
+          }
+        }
+      } else {  // rows of any alignment: 32 x 32 values at a time through shared memory
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            mine[lane * C::kPitch + 2 * i] = acc[c * 16 + i].x;
+            mine[lane * C::kPitch + 2 * i + 1] = acc[c * 16 + i].y;
+          }
+          __syncwarp();
+          if (n0 + c * 32 + lane < p.n)
+            for (int r = 0; r < 32 && t0 + r < p.tokens; ++r) store_out(p, t0 + r, n0 + c * 32 + lane, mine[r * C::kPitch + lane]);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (kPair) cluster_sync();  // what the other CTA still signals here has come
+  if (warp == 1) {
+    if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    else tmem_dealloc(tmem, 512);
+  }
+}
+
+template <bool kPair>
+cudaError_t launch_wide(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul& m) {
+  using C = Wide<kPair>;
+  static int done[64] = {0};
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(wide_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = 1;
+  }
+  e = encode_u8_2d_sw128(&p.tmap_x, m.x, m.k, m.tokens, m.x_stride, kBlockK, 128);
+  if (e == cudaSuccess) e = encode_u8_2d_sw128(&p.tmap_w, m.w, m.k, m.n, m.w_stride, kBlockK, C::kRowsW);
+  if (e != cudaSuccess) return e;
+  p.tiles_m = (int)((m.tokens + (long)C::kTileM - 1) / C::kTileM);
+  p.tiles_n = (int)((m.n + (long)C::kTileN - 1) / C::kTileN);
+  const long bytes = m.out_f32 ? 4 : 2;
+  p.wide_out = (reinterpret_cast<uintptr_t>(m.out) & 31u) == 0 && m.out_stride * bytes % 32 == 0 && m.n * bytes % 32 == 0;
+  const long tiles = (long)p.tiles_m * p.tiles_n;
+  const int slots = kPair ? sms / 2 : sms;
+  const int ctas = (int)(tiles < slots ? tiles : slots) * (kPair ? 2 : 1);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPair ? 2 : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = env.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, wide_kernel<kPair>, p);
+}
+
 }  // namespace
 
 cudaError_t launch_fp8_matmul(const LaunchEnv& env, const Fp8Matmul& m) {
   MatmulParams p;
   memset(&p, 0, sizeof p);
+  p.x = m.x;
+  p.w = m.w;
+  p.x_stride = m.x_stride;
+  p.w_stride = m.w_stride;
+  p.k = m.k;
   p.x_scale = m.x_scale;
   p.w_scale = m.w_scale;
   p.tokens = m.tokens;
@@ -297,6 +757,10 @@ cudaError_t launch_fp8_matmul(const LaunchEnv& env, const Fp8Matmul& m) {
   p.out_stride = m.out_stride;
   p.out_f32 = m.out_f32;
   p.err = env.err;
+  if (getenv("GDN_WIDE") && m.tokens > 128) return atoi(getenv("GDN_WIDE")) == 2 ? launch_wide<true>(env, p, m) : launch_wide<false>(env, p, m);
+  const unsigned few = (unsigned)((m.n + 15L) / 16);
+  if (m.tokens <= 8) return launch_early(few_kernel<1>, dim3(few), kFewWarps * 32, 0, env.stream, p);
+  if (m.tokens <= 16 && !getenv("GDN_NOFEW2")) return launch_early(few_kernel<2>, dim3(few), kFewWarps * 32, 0, env.stream, p);
   cudaError_t e = encode_u8_2d_sw128(&p.tmap_w, m.w, m.k, m.n, m.w_stride, kBlockK, 128);
   if (e != cudaSuccess) return e;
   if (m.tokens <= 16) return launch_narrow<16>(env, p, m);
