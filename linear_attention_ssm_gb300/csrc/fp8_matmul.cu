@@ -17,12 +17,44 @@ namespace {
 constexpr int kBlockK = 128;  // codes of a stage's row, one scale block
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before giving up
 
-// One lane of the warp.  What it issues has operands that are the same in every lane, so that they need not be gathered
-// from one: four products and two arrivals take 340 cycles of the issuing warp this way, 560 under `lane == 0`.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(one));
-  return one;
+// A whole warp works on barriers, copies and products without a branch: every lane polls, and what one lane issues stands
+// under a predicate of elect.sync in one piece of assembly.  Measured for a warp: a poll that finds its phase complete takes
+// 58 cycles this way, 255 in a branch of one lane; four products and two arrivals 270, 340 in a branch of the elected lane
+// and 560 in one of `lane == 0`, whose operands have to be gathered from that lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool cluster) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t done;
+    if (cluster)
+      asm volatile(
+          "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+          : "=r"(done)
+          : "r"(bar), "r"(parity)
+          : "memory");
+    else
+      asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                   : "=r"(done)
+                   : "r"(bar), "r"(parity)
+                   : "memory");
+    if (__all_sync(~0u, done)) return true;
+  }
+  return false;
+}
+// The two loads of a stage, `bytes` of them counted by `bar` (0: counted elsewhere).
+__device__ __forceinline__ void warp_load_stage(uint32_t bar, uint32_t bytes, uint32_t dst0, const void* map0, int y0,
+                                                uint32_t dst1, const void* map1, int y1, int x) {
+  asm volatile(
+      "{\n.reg .pred e;\n"
+      "elect.sync _|e, 0xFFFFFFFF;\n"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%8, %4}], [%0];\n"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%5], [%6, {%8, %7}], [%0];\n"
+      "}" ::"r"(bar),
+      "r"(bytes), "r"(dst0), "l"(map0), "r"(y0), "r"(dst1), "l"(map1), "r"(y1), "r"(x)
+      : "memory");
+}
+__device__ __forceinline__ void first_lane_arrive(uint32_t bar, int lane) {
+  asm volatile("{\n.reg .pred p;\nsetp.eq.s32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(lane)
+               : "memory");
 }
 
 // Instruction descriptor: D fp32, A and B e4m3, both K-major.
@@ -30,19 +62,24 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D[tmem] = A[smem] B[smem]^T over one stage: four steps of 32 codes, the first one on nothing.
-__device__ __forceinline__ void mma_e4m3_k4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+// D[tmem] = A[smem] B[smem]^T over one stage, by the whole warp: four steps of 32 codes, the first one on nothing.  The two
+// barriers get an arrival each when it is done.
+__device__ __forceinline__ void warp_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t bar0,
+                                              uint32_t bar1) {
   asm volatile(
-      "{\n.reg .pred p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      "{\n.reg .pred e, p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      "elect.sync _|e, 0xFFFFFFFF;\n"
       "setp.ne.b32 p, 0, 0;\n"
       "setp.ne.b32 q, 1, 0;\n"
       "add.s64 a1, %1, 2;\nadd.s64 a2, %1, 4;\nadd.s64 a3, %1, 6;\n"
       "add.s64 b1, %2, 2;\nadd.s64 b2, %2, 4;\nadd.s64 b3, %2, 6;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, q;\n"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc)
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, q;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(bar0), "r"(bar1)
       : "memory");
 }
 
@@ -260,14 +297,13 @@ __global__ void __launch_bounds__(Narrow<kTokens>::kThreads, 2) narrow_kernel(co
 #pragma unroll
   for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
   bool ok = true;
-  // A bounded wait of the whole warp; after one that ran out it takes no more work, and the others' waits run out in
-  // turn.
+  // A bounded wait; after one that ran out the warp takes no more work, and the others' waits run out in turn.
   auto await = [&](uint32_t bar, uint32_t parity) {
-    if (ok && !mbar_wait(bar, parity, kWaitLimit)) {
+    if (ok && !warp_wait(bar, parity, false)) {
       raise_error(p.err, kErrTimeout);
       ok = false;
     }
-    return ok = __all_sync(~0u, ok);
+    return ok;
   };
   if (warp == 0) {
     int b = b0;
@@ -275,12 +311,8 @@ __global__ void __launch_bounds__(Narrow<kTokens>::kThreads, 2) narrow_kernel(co
       const int i = (b - b0) % C::kStages, pass = (b - b0) / C::kStages;
       if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
       const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-      if (elect_one()) {
-        mbar_arrive_expect_tx(full + 8 * i, C::kStageBytes);
-        tma_load_2d(at, &p.tmap_w, b * kBlockK, (int)n0, full + 8 * i);
-        tma_load_2d(at + 128 * kBlockK, &p.tmap_x, b * kBlockK, (int)t0, full + 8 * i);
-      }
-      __syncwarp();
+      warp_load_stage(full + 8 * i, C::kStageBytes, at, &p.tmap_w, (int)n0, at + 128 * kBlockK, &p.tmap_x, (int)t0,
+                      b * kBlockK);
     }
     // copies in flight land before the CTA ends, after a wait that ran out too
     for (int c = max(b0, b - C::kStages); c < b; ++c)
@@ -292,12 +324,8 @@ __global__ void __launch_bounds__(Narrow<kTokens>::kThreads, 2) narrow_kernel(co
       if (j >= C::kBufs && !await(taken + 8 * buf, (j / C::kBufs - 1) & 1)) break;
       tc_fence_after();
       const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-      if (elect_one()) {
-        mma_e4m3_k4(tmem + buf * kTokens, sw128_desc(at), sw128_desc(at + 128 * kBlockK), idesc_e4m3_f32(128, kTokens));
-        mma_commit(empty + 8 * i);
-        mma_commit(done + 8 * buf);
-      }
-      __syncwarp();
+      warp_mma_e4m3(tmem + buf * kTokens, sw128_desc(at), sw128_desc(at + 128 * kBlockK), idesc_e4m3_f32(128, kTokens),
+                    empty + 8 * i, done + 8 * buf);
     }
   } else {
     const int quarter = warp & 3;
@@ -339,8 +367,7 @@ __global__ void __launch_bounds__(Narrow<kTokens>::kThreads, 2) narrow_kernel(co
         tmem_ld_cols<kStep>(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTokens + col0 + c, d);
         if (c + kStep == kCols) {
           tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(taken + 8 * buf);
+          first_lane_arrive(taken + 8 * buf, lane);
         }
 #pragma unroll
         for (int i = 0; i < kStep; i += 4) {
@@ -425,67 +452,46 @@ cudaError_t launch_narrow(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul
 
 // ---------------------------------------------------------------- many tokens: tokens as the rows of a tile
 
-// kPair: two CTAs of a cluster share a tile of 256 tokens x 256 rows of w.  Each holds 128 of either, their tensor cores
-// read both halves of w (cta_group::2), and each has the sums of its own 128 tokens.  Otherwise a CTA has a tile of 128 x
-// 256 to itself.
-template <bool kPair>
 struct Wide {
-  static constexpr int kTileN = 256, kTileM = kPair ? 256 : 128;
-  static constexpr int kRowsW = kPair ? 128 : 256;  // of w, in a CTA's stage
-  static constexpr int kStageBytes = (128 + kRowsW) * kBlockK;
-  static constexpr int kStages = kPair ? 5 : 3;
+  static constexpr int kTileM = 128, kTileN = 256;  // tokens, rows of w
+  static constexpr int kStageBytes = (kTileM + kTileN) * kBlockK;
+  static constexpr int kStages = 4;
   static constexpr int kWarps = 8;  // of sums: each has 32 tokens x 128 columns
-  static constexpr int kThreads = 64 + 32 * kWarps;
-  static constexpr int kPitch = 33;  // of a warp's 32 x 32 values on their way out
-  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kWarps * 32 * kPitch * 4 + 256;
+  static constexpr int kThreads = 128 + 32 * kWarps;  // one warp loads, one issues products, two stand by
+  static constexpr int kPitch = 17;  // of a warp's 32 x 16 values on their way out
+  static constexpr int kAhead = 8;  // blocks whose scales are fetched together, one such group ahead
+  static constexpr int kScales = 2 * kAhead * (32 * kWarps + 8);  // a token's for its two threads; the weights' for a warp
+  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kWarps * 32 * kPitch * 4 + kScales * 4 + 256;
 };
 
-// as mma_e4m3_k4, by the pair of CTAs
-__device__ __forceinline__ void mma_e4m3_k4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+// four bytes to shared memory, without waiting for them
+__device__ __forceinline__ void copy4(float* dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// tmem_ld32 in two steps: the values are there after the second one
+__device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "{\n.reg .pred p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
-      "setp.ne.b32 p, 0, 0;\n"
-      "setp.ne.b32 q, 1, 0;\n"
-      "add.s64 a1, %1, 2;\nadd.s64 a2, %1, 4;\nadd.s64 a3, %1, 6;\n"
-      "add.s64 b1, %2, 2;\nadd.s64 b2, %2, 4;\nadd.s64 b3, %2, 6;\n"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a1, b1, %3, q;\n"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a2, b2, %3, q;\n"
-      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a3, b3, %3, q;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc)
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
       : "memory");
 }
-// mma_commit for the pair: an arrival at the same place in both CTAs
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-// a load into this CTA's shared memory that is counted by a barrier of either CTA of the pair
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-      "[%4];" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint32_t limit) {
-  for (uint32_t i = 0; i < limit; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        "selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
-  return false;
+__device__ __forceinline__ void tmem_ld32_end(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+                 "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
 // Tile `id` of the grid of tiles: eight rows of tiles at a time, so that the tiles that are worked on together share both
@@ -496,155 +502,146 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& m
   m = 8 * g + in - n * rows;
 }
 
-template <bool kPair>
-__global__ void __launch_bounds__(Wide<kPair>::kThreads, 1) wide_kernel(const __grid_constant__ MatmulParams p) {
-  using C = Wide<kPair>;
+__global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_constant__ MatmulParams p) {
+  using C = Wide;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   float* stage_out = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stage_out + C::kWarps * 32 * C::kPitch);
+  float* scales = stage_out + C::kWarps * 32 * C::kPitch;  // [2][kAhead][kWarps][32], then [2][kWarps][kAhead]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scales + C::kScales);
   __shared__ uint32_t tmem_slot;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, done = empty + 8 * C::kStages, taken = done + 16;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, done = empty + 8 * C::kStages, taken = done + 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = kPair ? blockIdx.x & 1 : 0, first = kPair ? blockIdx.x >> 1 : blockIdx.x,
-            step = kPair ? gridDim.x >> 1 : gridDim.x;
+  const int first = blockIdx.x, step = gridDim.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(empty + 8 * i, 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(done + 8 * i, 1);
-      mbar_init(taken + 8 * i, C::kWarps * (kPair ? 2 : 1));
+      mbar_init(taken + 8 * i, C::kWarps / 2);
     }
     fence_mbar_init();
     prefetch_tensormap(&p.tmap_x);
     prefetch_tensormap(&p.tmap_w);
   }
-  if (warp == 1) {
-    if constexpr (kPair) {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot)) : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-      tmem_alloc(smem_u32(&tmem_slot), 512);
-    }
-  }
+  if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();  // the other CTA's barriers are there
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   await_grid();
 
   bool ok = true;
   auto await = [&](uint32_t bar, uint32_t parity) {
-    if (ok && !(kPair ? mbar_wait_cluster(bar, parity, kWaitLimit) : mbar_wait(bar, parity, kWaitLimit))) {
+    if (ok && !warp_wait(bar, parity, false)) {
       raise_error(p.err, kErrTimeout);
       ok = false;
     }
-    return ok = __all_sync(~0u, ok);
+    return ok;
   };
   const int tiles = p.tiles_m * p.tiles_n;
+  // 384 threads are launched with 168 registers each; 56 in the first four warps leave 224 for those of the sums
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     int i = 0, pass = 0;  // stage, passes over the ring
-    const uint32_t count = kPair ? in_cta(full, 0) : full;  // loads are counted by the first CTA's barriers
     for (int id = first; id < tiles && ok; id += step) {
       int m, n;
       tile_of(id, p.tiles_m, p.tiles_n, m, n);
-      const int t0 = m * C::kTileM + rank * 128, n0 = n * C::kTileN + rank * 128;
       for (int b = 0; b < p.blocks; ++b) {
         if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
         const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-        if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(full + 8 * i, C::kStageBytes * (kPair ? 2 : 1));
-          if constexpr (kPair) {
-            tma_load_2d_pair(at, &p.tmap_x, b * kBlockK, t0, count + 8 * i);
-            tma_load_2d_pair(at + 128 * kBlockK, &p.tmap_w, b * kBlockK, n0, count + 8 * i);
-          } else {
-            tma_load_2d(at, &p.tmap_x, b * kBlockK, t0, count + 8 * i);
-            tma_load_2d(at + 128 * kBlockK, &p.tmap_w, b * kBlockK, n0, count + 8 * i);
-          }
-        }
-        __syncwarp();
+        warp_load_stage(full + 8 * i, C::kStageBytes, at, &p.tmap_x, m * C::kTileM, at + C::kTileM * kBlockK, &p.tmap_w,
+                        n * C::kTileN, b * kBlockK);
         if (++i == C::kStages) i = 0, ++pass;
       }
     }
-    // copies in flight land before the CTAs end, after a wait that ran out too
-    if (rank == 0)
+    // copies in flight land before the CTA ends, after a wait that ran out too
       for (int c = 0; c < C::kStages; ++c) {
         const int passes = pass + (c < i);  // loads into stage c
         if (passes) mbar_wait(full + 8 * c, (passes - 1) & 1, kWaitLimit);
       }
-  } else if (warp == 1) {
-    if (rank == 0) {
-      int i = 0, pass = 0, j = 0;
-      for (int id = first; id < tiles && ok; id += step)
-        for (int b = 0; b < p.blocks; ++b, ++j) {
-          const int half = j & 1;
-          if (!await(full + 8 * i, pass & 1)) break;
-          if (j >= 2 && !await(taken + 8 * half, ((j >> 1) - 1) & 1)) break;
-          tc_fence_after();
-          const uint64_t a = sw128_desc(smem_u32(smem + i * C::kStageBytes));
-          const uint64_t w = sw128_desc(smem_u32(smem + i * C::kStageBytes + 128 * kBlockK));
-          if (elect_one()) {
-            if constexpr (kPair) {
-              mma_e4m3_k4_pair(tmem + half * 256, a, w, idesc_e4m3_f32(256, 256));
-              mma_commit_pair(empty + 8 * i);
-              mma_commit_pair(done + 8 * half);
-            } else {
-              mma_e4m3_k4(tmem + half * 256, a, w, idesc_e4m3_f32(128, 256));
-              mma_commit(empty + 8 * i);
-              mma_commit(done + 8 * half);
-            }
-          }
-          __syncwarp();
-          if (++i == C::kStages) i = 0, ++pass;
-        }
-    }
+  } else if (warp < 3) {
+    // each of these warps issues the products of one half of the columns
+    const int side = warp - 1;
+    int i = 0, pass = 0, j = 0;
+    for (int id = first; id < tiles && ok; id += step)
+      for (int b = 0; b < p.blocks; ++b, ++j) {
+        const int buf = 2 * side + (j & 1);
+        if (!await(full + 8 * i, pass & 1)) break;
+        if (j >= 2 && !await(taken + 8 * buf, ((j >> 1) - 1) & 1)) break;
+        tc_fence_after();
+        const uint32_t at = smem_u32(smem + i * C::kStageBytes);
+        warp_mma_e4m3(tmem + buf * 128, sw128_desc(at), sw128_desc(at + (C::kTileM + side * 128) * kBlockK),
+                      idesc_e4m3_f32(128, 128), empty + 8 * i, done + 8 * buf);
+        if (++i == C::kStages) i = 0, ++pass;
+      }
+  }
   } else {
-    const int quarter = warp & 3, side = (warp - 2) >> 2;  // of the columns
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + side * 128;
-    const uint32_t taken_at = kPair ? in_cta(taken, 0) : taken;
-    float* mine = stage_out + (warp - 2) * 32 * C::kPitch;
-    int j = 0;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int quarter = warp & 3, side = (warp - 4) >> 2;  // of the columns
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + side * 256;
+    float* mine = stage_out + (warp - 4) * 32 * C::kPitch;
+    constexpr int kAhead = C::kAhead;
+    float* own_x = scales + (warp - 4) * 32 + lane;  // this token's scales, a row for each block of two groups
+    float* own_w = scales + 2 * kAhead * 32 * C::kWarps + (warp - 4) * kAhead;
+    int j = 0, group = 0;
     for (int id = first; id < tiles && ok; id += step) {
       int m, n;
       tile_of(id, p.tiles_m, p.tiles_n, m, n);
-      const long t0 = (long)m * C::kTileM + rank * 128 + quarter * 32, t = t0 + lane;
+      const long t0 = (long)m * C::kTileM + quarter * 32, t = t0 + lane;
       const long n0 = (long)n * C::kTileN + side * 128;
-      const float* sx = p.x_scale + t * p.blocks;
-      const float* sw = p.w_scale + (n0 >> 7) * p.blocks;
-      const bool in = t < p.tokens && n0 < p.n;
+      // tokens and columns behind the last ones take the last ones' scales: what they are multiplied with is not written
+      const float* sx = p.x_scale + min(t, (long)p.tokens - 1) * p.blocks;
+      const float* sw = p.w_scale + (min(n0, (long)p.n - 1) >> 7) * p.blocks;
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      auto scale = [&](int b) { return in && b < p.blocks ? sx[b] * sw[b] : 0.f; };
-      float s0 = scale(0), s1 = scale(1), s2 = scale(2);  // of this block and the next ones
+      auto fetch = [&](int b, int to) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (b + i < p.blocks) copy4(own_x + (to * kAhead + i) * 32 * C::kWarps, sx + b + i);
+        if (lane < kAhead && b + lane < p.blocks) copy4(own_w + to * kAhead * C::kWarps + lane, sw + b + lane);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      fetch(0, group & 1);
+      for (int b0 = 0; b0 < p.blocks && ok; b0 += kAhead, ++group) {
+        fetch(b0 + kAhead, ~group & 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const float* now_x = own_x + (group & 1) * kAhead * 32 * C::kWarps;
+        const float* now_w = own_w + (group & 1) * kAhead * C::kWarps;
+        const int count = min(kAhead, p.blocks - b0);
 #pragma unroll 1
-      for (int b = 0; b < p.blocks; ++b, ++j) {
-        const int half = j & 1;
-        if (!await(done + 8 * half, (j >> 1) & 1)) break;
-        tc_fence_after();
-        const float2 s = make_float2(s0, s0);
-        s0 = s1;
-        s1 = s2;
-        s2 = scale(b + 3);
+        for (int u = 0; u < count; ++u, ++j) {
+          const int buf = 2 * side + (j & 1);
+          const float s1 = now_x[u * 32 * C::kWarps] * now_w[u];
+          const float2 s = make_float2(s1, s1);
+          if (!await(done + 8 * buf, (j >> 1) & 1)) break;
+          tc_fence_after();
+          const uint32_t at = lanes + (j & 1) * 128;
+          // 32 columns are on their way while the 32 before them are added
+          uint32_t d[2][32];
+          tmem_ld32_begin(at, d[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float d[32];
-          tmem_ld32(lanes + half * 256 + c * 32, d);
-          if (c == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (kPair) mbar_arrive_cluster(taken_at + 8 * half);
-              else mbar_arrive(taken_at + 8 * half);
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32_end(d[c & 1]);
+            if (c < 3) {
+              tmem_ld32_begin(at + (c + 1) * 32, d[~c & 1]);
+            } else {
+              tc_fence_before();
+              first_lane_arrive(taken + 8 * buf, lane);
             }
-          }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c * 16 + i] = __ffma2_rn(make_float2(d[2 * i], d[2 * i + 1]), s, acc[c * 16 + i]);
+            for (int i = 0; i < 16; ++i)
+              acc[c * 16 + i] = __ffma2_rn(make_float2(__uint_as_float(d[c & 1][2 * i]), __uint_as_float(d[c & 1][2 * i + 1])),
+                                           s, acc[c * 16 + i]);
+          }
         }
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       if (!ok) break;
       if (p.wide_out) {  // whole sectors of a row from its thread
         if (t < p.tokens) {
@@ -652,7 +649,7 @@ __global__ void __launch_bounds__(Wide<kPair>::kThreads, 1) wide_kernel(const __
           if (p.out_f32) {
             float* to = static_cast<float*>(p.out) + at;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 128 / 8; ++i) {
               uint32_t v[8];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
@@ -664,7 +661,7 @@ __global__ void __launch_bounds__(Wide<kPair>::kThreads, 1) wide_kernel(const __
           } else {
             uint16_t* to = static_cast<uint16_t*>(p.out) + at;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 128 / 16; ++i) {
               uint32_t v[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) v[q] = pack_bf2(acc[8 * i + q].x, acc[8 * i + q].y);
@@ -672,18 +669,20 @@ __global__ void __launch_bounds__(Wide<kPair>::kThreads, 1) wide_kernel(const __
             }
           }
         }
-      } else {  // rows of any alignment: 32 x 32 values at a time through shared memory
+      } else {  // rows of any alignment: 32 x 16 values at a time through shared memory, half a row a store
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 128 / 16; ++c) {
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            mine[lane * C::kPitch + 2 * i] = acc[c * 16 + i].x;
-            mine[lane * C::kPitch + 2 * i + 1] = acc[c * 16 + i].y;
+          for (int i = 0; i < 8; ++i) {
+            mine[lane * C::kPitch + 2 * i] = acc[c * 8 + i].x;
+            mine[lane * C::kPitch + 2 * i + 1] = acc[c * 8 + i].y;
           }
           __syncwarp();
-          if (n0 + c * 32 + lane < p.n)
-            for (int r = 0; r < 32 && t0 + r < p.tokens; ++r) store_out(p, t0 + r, n0 + c * 32 + lane, mine[r * C::kPitch + lane]);
+          const int col = lane & 15;
+          if (n0 + c * 16 + col < p.n)
+            for (int r = lane >> 4; r < 32 && t0 + r < p.tokens; r += 2)
+              store_out(p, t0 + r, n0 + c * 16 + col, mine[r * C::kPitch + col]);
         }
       }
     }
@@ -691,51 +690,30 @@ __global__ void __launch_bounds__(Wide<kPair>::kThreads, 1) wide_kernel(const __
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if constexpr (kPair) cluster_sync();  // what the other CTA still signals here has come
-  if (warp == 1) {
-    if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-    else tmem_dealloc(tmem, 512);
-  }
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <bool kPair>
 cudaError_t launch_wide(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul& m) {
-  using C = Wide<kPair>;
+  using C = Wide;
   static int done[64] = {0};
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !done[dev]) {
-    e = cudaFuncSetAttribute(wide_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    e = cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = 1;
   }
-  e = encode_u8_2d_sw128(&p.tmap_x, m.x, m.k, m.tokens, m.x_stride, kBlockK, 128);
-  if (e == cudaSuccess) e = encode_u8_2d_sw128(&p.tmap_w, m.w, m.k, m.n, m.w_stride, kBlockK, C::kRowsW);
+  e = encode_u8_2d_sw128(&p.tmap_x, m.x, m.k, m.tokens, m.x_stride, kBlockK, C::kTileM);
+  if (e == cudaSuccess) e = encode_u8_2d_sw128(&p.tmap_w, m.w, m.k, m.n, m.w_stride, kBlockK, C::kTileN);
   if (e != cudaSuccess) return e;
   p.tiles_m = (int)((m.tokens + (long)C::kTileM - 1) / C::kTileM);
   p.tiles_n = (int)((m.n + (long)C::kTileN - 1) / C::kTileN);
   const long bytes = m.out_f32 ? 4 : 2;
   p.wide_out = (reinterpret_cast<uintptr_t>(m.out) & 31u) == 0 && m.out_stride * bytes % 32 == 0 && m.n * bytes % 32 == 0;
   const long tiles = (long)p.tiles_m * p.tiles_n;
-  const int slots = kPair ? sms / 2 : sms;
-  const int ctas = (int)(tiles < slots ? tiles : slots) * (kPair ? 2 : 1);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kPair ? 2 : 1;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = env.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, wide_kernel<kPair>, p);
+  return launch_early(wide_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), C::kThreads, C::kSmem, env.stream, p);
 }
 
 }  // namespace
@@ -757,7 +735,7 @@ cudaError_t launch_fp8_matmul(const LaunchEnv& env, const Fp8Matmul& m) {
   p.out_stride = m.out_stride;
   p.out_f32 = m.out_f32;
   p.err = env.err;
-  if (getenv("GDN_WIDE") && m.tokens > 128) return atoi(getenv("GDN_WIDE")) == 2 ? launch_wide<true>(env, p, m) : launch_wide<false>(env, p, m);
+  if (getenv("GDN_WIDE") && atoi(getenv("GDN_WIDE")) && m.tokens > 128) return launch_wide(env, p, m);
   const unsigned few = (unsigned)((m.n + 15L) / 16);
   if (m.tokens <= 8) return launch_early(few_kernel<1>, dim3(few), kFewWarps * 32, 0, env.stream, p);
   if (m.tokens <= 16 && !getenv("GDN_NOFEW2")) return launch_early(few_kernel<2>, dim3(few), kFewWarps * 32, 0, env.stream, p);
