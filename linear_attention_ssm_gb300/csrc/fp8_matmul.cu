@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + side * 256;
     float* mine = stage_out + (warp - 4) * 32 * C::kPitch;
     constexpr int kAhead = C::kAhead;
-    float* own_x = scales + (warp - 4) * 32 + lane;  // this token's scales, a row for each block of two groups
+    float* own_x = scales + (warp - 4) * 32;  // its tokens' scales, a row for each block of two groups
     float* own_w = scales + 2 * kAhead * 32 * C::kWarps + (warp - 4) * kAhead;
     int j = 0, group = 0;
     for (int id = first; id < tiles && ok; id += step) {
@@ -594,54 +594,66 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
       const long t0 = (long)m * C::kTileM + quarter * 32, t = t0 + lane;
       const long n0 = (long)n * C::kTileN + side * 128;
       // tokens and columns behind the last ones take the last ones' scales: what they are multiplied with is not written
-      const float* sx = p.x_scale + min(t, (long)p.tokens - 1) * p.blocks;
       const float* sw = p.w_scale + (min(n0, (long)p.n - 1) >> 7) * p.blocks;
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      auto fetch = [&](int b, int to) {
+      // a group of blocks' scales, eight blocks of four tokens at a time: a sector of each token's row
+      auto fetch = [&](int b) {
+        const int to = (group + (b > 0)) & 1, u = lane & 7;
+        if (b + u < p.blocks) {
+          const float* from = p.x_scale + b + u;
+          float* x_to = own_x + (to * kAhead + u) * 32 * C::kWarps;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (b + i < p.blocks) copy4(own_x + (to * kAhead + i) * 32 * C::kWarps, sx + b + i);
-        if (lane < kAhead && b + lane < p.blocks) copy4(own_w + to * kAhead * C::kWarps + lane, sw + b + lane);
+          for (int i = lane >> 3; i < 32; i += 4) copy4(x_to + i, from + min(t0 + i, (long)p.tokens - 1) * p.blocks);
+          if (lane < kAhead) copy4(own_w + to * kAhead * C::kWarps + u, sw + b + u);
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      fetch(0, group & 1);
-      for (int b0 = 0; b0 < p.blocks && ok; b0 += kAhead, ++group) {
-        fetch(b0 + kAhead, ~group & 1);
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
-        __syncwarp();
-        const float* now_x = own_x + (group & 1) * kAhead * 32 * C::kWarps;
-        const float* now_w = own_w + (group & 1) * kAhead * C::kWarps;
-        const int count = min(kAhead, p.blocks - b0);
+      fetch(0);
+      float2 s = make_float2(0.f, 0.f);
+      uint32_t d[2][32];
+      // Block b's products are there: its scale, and the first 32 of its columns on their way.
+      auto begin = [&](int b) {
+        if (b % kAhead == 0) {
+          if (b) ++group;
+          fetch(b + kAhead);
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          __syncwarp();
+        }
+        const int at = (group & 1) * kAhead + b % kAhead;
+        const float v = own_x[at * 32 * C::kWarps + lane] * own_w[((group & 1) * C::kWarps) * kAhead + b % kAhead];
+        s = make_float2(v, v);
+        if (!await(done + 8 * (2 * side + (j & 1)), (j >> 1) & 1)) return;
+        tc_fence_after();
+        tmem_ld32_begin(lanes + (j & 1) * 128, d[0]);
+      };
+      begin(0);
 #pragma unroll 1
-        for (int u = 0; u < count; ++u, ++j) {
-          const int buf = 2 * side + (j & 1);
-          const float s1 = now_x[u * 32 * C::kWarps] * now_w[u];
-          const float2 s = make_float2(s1, s1);
-          if (!await(done + 8 * buf, (j >> 1) & 1)) break;
-          tc_fence_after();
-          const uint32_t at = lanes + (j & 1) * 128;
-          // 32 columns are on their way while the 32 before them are added
-          uint32_t d[2][32];
-          tmem_ld32_begin(at, d[0]);
+      for (int b = 0; b < p.blocks && ok; ++b) {
+        const float2 now = s;
+        const uint32_t at = lanes + (j & 1) * 128;
+        // 32 columns are on their way while the 32 before them are added: the next block's first ones beside its last
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32_end(d[c & 1]);
-            if (c < 3) {
-              tmem_ld32_begin(at + (c + 1) * 32, d[~c & 1]);
-            } else {
-              tc_fence_before();
-              first_lane_arrive(taken + 8 * buf, lane);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              acc[c * 16 + i] = __ffma2_rn(make_float2(__uint_as_float(d[c & 1][2 * i]), __uint_as_float(d[c & 1][2 * i + 1])),
-                                           s, acc[c * 16 + i]);
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32_end(d[c & 1]);
+          if (c < 3) {
+            tmem_ld32_begin(at + (c + 1) * 32, d[~c & 1]);
+          } else {
+            tc_fence_before();
+            first_lane_arrive(taken + 8 * (2 * side + (j & 1)), lane);
+            ++j;
+            if (b + 1 < p.blocks) begin(b + 1);
           }
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            acc[c * 16 + i] = __ffma2_rn(make_float2(__uint_as_float(d[c & 1][2 * i]), __uint_as_float(d[c & 1][2 * i + 1])),
+                                         now, acc[c * 16 + i]);
         }
       }
+      ++group;
       asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
       if (!ok) break;
       if (p.wide_out) {  // whole sectors of a row from its thread
         if (t < p.tokens) {
