@@ -5,6 +5,7 @@
 // The inner sum is four tcgen05 instructions on one 128-byte-wide stage of each operand; its result lies in tensor memory
 // and is taken into the running fp32 sums of the registers with the block's scales, while the next block's products run
 // into the other half of the accumulators.
+#include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
 
@@ -39,18 +40,32 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool cl
   }
   return false;
 }
-// The two loads of a stage, `bytes` of them counted by `bar` (0: counted elsewhere).
+// The two loads of a stage, `bytes` in all, counted by `bar`; the second one goes to the same place of kShare CTAs, named by
+// the bits of `all`, and is counted in each.
+template <int kShare>
 __device__ __forceinline__ void warp_load_stage(uint32_t bar, uint32_t bytes, uint32_t dst0, const void* map0, int y0,
-                                                uint32_t dst1, const void* map1, int y1, int x) {
-  asm volatile(
-      "{\n.reg .pred e;\n"
-      "elect.sync _|e, 0xFFFFFFFF;\n"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
-      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%8, %4}], [%0];\n"
-      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%5], [%6, {%8, %7}], [%0];\n"
-      "}" ::"r"(bar),
-      "r"(bytes), "r"(dst0), "l"(map0), "r"(y0), "r"(dst1), "l"(map1), "r"(y1), "r"(x)
-      : "memory");
+                                                uint32_t dst1, const void* map1, int y1, int x, uint16_t all) {
+  if constexpr (kShare == 1)
+    asm volatile(
+        "{\n.reg .pred e;\n"
+        "elect.sync _|e, 0xFFFFFFFF;\n"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%8, %4}], [%0];\n"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%5], [%6, {%8, %7}], [%0];\n"
+        "}" ::"r"(bar),
+        "r"(bytes), "r"(dst0), "l"(map0), "r"(y0), "r"(dst1), "l"(map1), "r"(y1), "r"(x)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred e;\n"
+        "elect.sync _|e, 0xFFFFFFFF;\n"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%8, %4}], [%0];\n"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%5], "
+        "[%6, {%8, %7}], [%0], %9;\n"
+        "}" ::"r"(bar),
+        "r"(bytes), "r"(dst0), "l"(map0), "r"(y0), "r"(dst1), "l"(map1), "r"(y1), "r"(x), "h"(all)
+        : "memory");
 }
 __device__ __forceinline__ void first_lane_arrive(uint32_t bar, int lane) {
   asm volatile("{\n.reg .pred p;\nsetp.eq.s32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(lane)
@@ -62,11 +77,13 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D[tmem] = A[smem] B[smem]^T over one stage, by the whole warp: four steps of 32 codes, the first one on nothing.  The two
-// barriers get an arrival each when it is done.
-__device__ __forceinline__ void warp_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t bar0,
-                                              uint32_t bar1) {
-  asm volatile(
+// D[tmem] = A[smem] B[smem]^T over one stage, by the whole warp: four steps of 32 codes, the first one on nothing.  When it
+// is done `stage` gets an arrival, in each of the kShare CTAs named by the bits of `all`, and `result` one.
+template <int kShare = 1>
+__device__ __forceinline__ void warp_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t stage, uint32_t result, uint16_t all = 1) {
+  if constexpr (kShare == 1)
+    asm volatile(
       "{\n.reg .pred e, p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
       "elect.sync _|e, 0xFFFFFFFF;\n"
       "setp.ne.b32 p, 0, 0;\n"
@@ -79,7 +96,23 @@ __device__ __forceinline__ void warp_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, 
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(bar0), "r"(bar1)
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(stage), "r"(result)
+      : "memory");
+  else
+    asm volatile(
+      "{\n.reg .pred e, p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      "elect.sync _|e, 0xFFFFFFFF;\n"
+      "setp.ne.b32 p, 0, 0;\n"
+      "setp.ne.b32 q, 1, 0;\n"
+      "add.s64 a1, %1, 2;\nadd.s64 a2, %1, 4;\nadd.s64 a3, %1, 6;\n"
+      "add.s64 b1, %2, 2;\nadd.s64 b2, %2, 4;\nadd.s64 b3, %2, 6;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, q;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], %6;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(stage), "r"(result), "h"(all)
       : "memory");
 }
 
@@ -311,8 +344,8 @@ __global__ void __launch_bounds__(Narrow<kTokens>::kThreads, 2) narrow_kernel(co
       const int i = (b - b0) % C::kStages, pass = (b - b0) / C::kStages;
       if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
       const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-      warp_load_stage(full + 8 * i, C::kStageBytes, at, &p.tmap_w, (int)n0, at + 128 * kBlockK, &p.tmap_x, (int)t0,
-                      b * kBlockK);
+      warp_load_stage<1>(full + 8 * i, C::kStageBytes, at, &p.tmap_w, (int)n0, at + 128 * kBlockK, &p.tmap_x, (int)t0,
+                         b * kBlockK, 1);
     }
     // copies in flight land before the CTA ends, after a wait that ran out too
     for (int c = max(b0, b - C::kStages); c < b; ++c)
@@ -502,6 +535,8 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& m
   m = 8 * g + in - n * rows;
 }
 
+// kShare CTAs of a cluster take tiles of the same rows of w, above one another: each loads its share of them for all.
+template <int kShare>
 __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_constant__ MatmulParams p) {
   using C = Wide;
   extern __shared__ uint8_t smem_raw[];
@@ -512,11 +547,12 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
   __shared__ uint32_t tmem_slot;
   const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, done = empty + 8 * C::kStages, taken = done + 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int first = blockIdx.x, step = gridDim.x;
+  const int rank = blockIdx.x % kShare, first = blockIdx.x / kShare, step = gridDim.x / kShare;
+  constexpr uint16_t kAll = (1 << kShare) - 1;  // the cluster's CTAs
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 2);
+      mbar_init(empty + 8 * i, 2 * kShare);
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(done + 8 * i, 1);
@@ -529,6 +565,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
   if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
+  if constexpr (kShare > 1) cluster_sync();  // the others' barriers are there
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   await_grid();
@@ -553,8 +590,10 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
       for (int b = 0; b < p.blocks; ++b) {
         if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
         const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-        warp_load_stage(full + 8 * i, C::kStageBytes, at, &p.tmap_x, m * C::kTileM, at + C::kTileM * kBlockK, &p.tmap_w,
-                        n * C::kTileN, b * kBlockK);
+        constexpr int kPart = C::kTileN / kShare;
+        warp_load_stage<kShare>(full + 8 * i, C::kStageBytes, at, &p.tmap_x, (m * kShare + rank) * C::kTileM,
+                                at + (C::kTileM + rank * kPart) * kBlockK, &p.tmap_w, n * C::kTileN + rank * kPart, b * kBlockK,
+                                kAll);
         if (++i == C::kStages) i = 0, ++pass;
       }
     }
@@ -574,8 +613,8 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
         if (j >= 2 && !await(taken + 8 * buf, ((j >> 1) - 1) & 1)) break;
         tc_fence_after();
         const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-        warp_mma_e4m3(tmem + buf * 128, sw128_desc(at), sw128_desc(at + (C::kTileM + side * 128) * kBlockK),
-                      idesc_e4m3_f32(128, 128), empty + 8 * i, done + 8 * buf);
+        warp_mma_e4m3<kShare>(tmem + buf * 128, sw128_desc(at), sw128_desc(at + (C::kTileM + side * 128) * kBlockK),
+                      idesc_e4m3_f32(128, 128), empty + 8 * i, done + 8 * buf, kAll);
         if (++i == C::kStages) i = 0, ++pass;
       }
   }
@@ -591,7 +630,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
     for (int id = first; id < tiles && ok; id += step) {
       int m, n;
       tile_of(id, p.tiles_m, p.tiles_n, m, n);
-      const long t0 = (long)m * C::kTileM + quarter * 32, t = t0 + lane;
+      const long t0 = (long)(m * kShare + rank) * C::kTileM + quarter * 32, t = t0 + lane;
       const long n0 = (long)n * C::kTileN + side * 128;
       // tokens and columns behind the last ones take the last ones' scales: what they are multiplied with is not written
       const float* sw = p.w_scale + (min(n0, (long)p.n - 1) >> 7) * p.blocks;
@@ -702,30 +741,56 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if constexpr (kShare > 1) cluster_sync();  // what the others load and signal here has come
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+template <int kShare>
 cudaError_t launch_wide(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul& m) {
   using C = Wide;
-  static int done[64] = {0};
-  int dev = 0, sms = 0;
+  static int clusters[64] = {0};  // that fit the device
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !done[dev]) {
-    e = cudaFuncSetAttribute(wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kShare;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kShare);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = env.stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = kShare > 1 ? 2 : 1;
+  int fit = dev < 64 ? clusters[dev] : 0;
+  if (!fit) {
+    e = cudaFuncSetAttribute(wide_kernel<kShare>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    if (dev < 64) done[dev] = 1;
+    if (kShare == 1) e = device_sm_count(&fit);
+    else {
+      cudaLaunchConfig_t q = cfg;
+      q.attrs = attr + 1;
+      q.numAttrs = 1;
+      e = cudaOccupancyMaxActiveClusters(&fit, wide_kernel<kShare>, &q);
+    }
+    if (e != cudaSuccess) return e;
+    if (getenv("GDN_VERBOSE")) fprintf(stderr, "clusters of %d: %d\n", kShare, fit);
+    if (dev < 64) clusters[dev] = fit;
   }
   e = encode_u8_2d_sw128(&p.tmap_x, m.x, m.k, m.tokens, m.x_stride, kBlockK, C::kTileM);
-  if (e == cudaSuccess) e = encode_u8_2d_sw128(&p.tmap_w, m.w, m.k, m.n, m.w_stride, kBlockK, C::kTileN);
+  if (e == cudaSuccess) e = encode_u8_2d_sw128(&p.tmap_w, m.w, m.k, m.n, m.w_stride, kBlockK, C::kTileN / kShare);
   if (e != cudaSuccess) return e;
-  p.tiles_m = (int)((m.tokens + (long)C::kTileM - 1) / C::kTileM);
+  p.tiles_m = (int)((m.tokens + (long)C::kTileM * kShare - 1) / (C::kTileM * kShare));
   p.tiles_n = (int)((m.n + (long)C::kTileN - 1) / C::kTileN);
   const long bytes = m.out_f32 ? 4 : 2;
   p.wide_out = (reinterpret_cast<uintptr_t>(m.out) & 31u) == 0 && m.out_stride * bytes % 32 == 0 && m.n * bytes % 32 == 0;
   const long tiles = (long)p.tiles_m * p.tiles_n;
-  return launch_early(wide_kernel, dim3((unsigned)(tiles < sms ? tiles : sms)), C::kThreads, C::kSmem, env.stream, p);
+  cfg.gridDim = dim3((unsigned)(tiles < fit ? tiles : fit) * kShare);
+  return cudaLaunchKernelEx(&cfg, wide_kernel<kShare>, p);
 }
 
 }  // namespace
@@ -747,7 +812,7 @@ cudaError_t launch_fp8_matmul(const LaunchEnv& env, const Fp8Matmul& m) {
   p.out_stride = m.out_stride;
   p.out_f32 = m.out_f32;
   p.err = env.err;
-  if (getenv("GDN_WIDE") && atoi(getenv("GDN_WIDE")) && m.tokens > 128) return launch_wide(env, p, m);
+  if (getenv("GDN_WIDE") && atoi(getenv("GDN_WIDE")) && m.tokens > 128) { const int s = atoi(getenv("GDN_WIDE")); return s == 4 ? launch_wide<4>(env, p, m) : s == 2 ? launch_wide<2>(env, p, m) : launch_wide<1>(env, p, m); }
   const unsigned few = (unsigned)((m.n + 15L) / 16);
   if (m.tokens <= 8) return launch_early(few_kernel<1>, dim3(few), kFewWarps * 32, 0, env.stream, p);
   if (m.tokens <= 16 && !getenv("GDN_NOFEW2")) return launch_early(few_kernel<2>, dim3(few), kFewWarps * 32, 0, env.stream, p);
