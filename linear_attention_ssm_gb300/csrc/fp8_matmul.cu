@@ -40,32 +40,18 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool cl
   }
   return false;
 }
-// The two loads of a stage, `bytes` in all, counted by `bar`; the second one goes to the same place of kShare CTAs, named by
-// the bits of `all`, and is counted in each.
-template <int kShare>
+// The two loads of a stage, `bytes` in all, counted by `bar`.
 __device__ __forceinline__ void warp_load_stage(uint32_t bar, uint32_t bytes, uint32_t dst0, const void* map0, int y0,
-                                                uint32_t dst1, const void* map1, int y1, int x, uint16_t all) {
-  if constexpr (kShare == 1)
-    asm volatile(
-        "{\n.reg .pred e;\n"
-        "elect.sync _|e, 0xFFFFFFFF;\n"
-        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
-        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%8, %4}], [%0];\n"
-        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%5], [%6, {%8, %7}], [%0];\n"
-        "}" ::"r"(bar),
-        "r"(bytes), "r"(dst0), "l"(map0), "r"(y0), "r"(dst1), "l"(map1), "r"(y1), "r"(x)
-        : "memory");
-  else
-    asm volatile(
-        "{\n.reg .pred e;\n"
-        "elect.sync _|e, 0xFFFFFFFF;\n"
-        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
-        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%8, %4}], [%0];\n"
-        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%5], "
-        "[%6, {%8, %7}], [%0], %9;\n"
-        "}" ::"r"(bar),
-        "r"(bytes), "r"(dst0), "l"(map0), "r"(y0), "r"(dst1), "l"(map1), "r"(y1), "r"(x), "h"(all)
-        : "memory");
+                                                uint32_t dst1, const void* map1, int y1, int x) {
+  asm volatile(
+      "{\n.reg .pred e;\n"
+      "elect.sync _|e, 0xFFFFFFFF;\n"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%8, %4}], [%0];\n"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%5], [%6, {%8, %7}], [%0];\n"
+      "}" ::"r"(bar),
+      "r"(bytes), "r"(dst0), "l"(map0), "r"(y0), "r"(dst1), "l"(map1), "r"(y1), "r"(x)
+      : "memory");
 }
 __device__ __forceinline__ void first_lane_arrive(uint32_t bar, int lane) {
   asm volatile("{\n.reg .pred p;\nsetp.eq.s32 p, %1, 0;\n@p mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar), "r"(lane)
@@ -78,12 +64,10 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
 }
 
 // D[tmem] = A[smem] B[smem]^T over one stage, by the whole warp: four steps of 32 codes, the first one on nothing.  When it
-// is done `stage` gets an arrival, in each of the kShare CTAs named by the bits of `all`, and `result` one.
-template <int kShare = 1>
+// is done `stage` and `result` get an arrival each.
 __device__ __forceinline__ void warp_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t stage, uint32_t result, uint16_t all = 1) {
-  if constexpr (kShare == 1)
-    asm volatile(
+                                              uint32_t stage, uint32_t result) {
+  asm volatile(
       "{\n.reg .pred e, p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
       "elect.sync _|e, 0xFFFFFFFF;\n"
       "setp.ne.b32 p, 0, 0;\n"
@@ -98,22 +82,6 @@ __device__ __forceinline__ void warp_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, 
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(stage), "r"(result)
       : "memory");
-  else
-    asm volatile(
-      "{\n.reg .pred e, p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
-      "elect.sync _|e, 0xFFFFFFFF;\n"
-      "setp.ne.b32 p, 0, 0;\n"
-      "setp.ne.b32 q, 1, 0;\n"
-      "add.s64 a1, %1, 2;\nadd.s64 a2, %1, 4;\nadd.s64 a3, %1, 6;\n"
-      "add.s64 b1, %2, 2;\nadd.s64 b2, %2, 4;\nadd.s64 b3, %2, 6;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, q;\n"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%4], %6;\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(stage), "r"(result), "h"(all)
-      : "memory");
 }
 
 struct MatmulParams {
@@ -126,7 +94,8 @@ struct MatmulParams {
   int tokens, n, k, blocks;  // blocks: of k
   int split;              // CTAs that share a tile's k
   int tiles_m, tiles_n;
-  int wide_out;           // rows of out are whole 32-byte sectors
+  int rows_x, stages;  // tokens of a stage, stages of the ring
+  int whole_out;           // rows of out are whole 32-byte sectors
   void* out;
   long out_stride;
   int out_f32;
@@ -148,9 +117,12 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
@@ -273,228 +245,28 @@ __global__ void __launch_bounds__(kFewWarps * 32, kTiles == 1 ? 3 : 2) few_kerne
   }
 }
 
-// ---------------------------------------------------------------- few tokens: weights as the rows of a tile
+// ---------------------------------------------------------------- more tokens: tiles of 128 tokens x 64 or 256 rows of w
 
-template <int kTokens>
-struct Narrow {
-  static constexpr int kStageBytes = (128 + kTokens) * kBlockK;
-  static constexpr int kStages = kTokens <= 16 ? 6 : kTokens <= 32 ? 5 : kTokens <= 64 ? 4 : 3;
-  static constexpr int kBufs = kTokens <= 32 ? 8 : 256 / kTokens;  // results of blocks in tensor memory
-  static constexpr int kColumns = kBufs * kTokens;
-  static constexpr int kParts = kTokens > 64 ? 2 : 1;  // of a row's sums, each in a thread of its own
-  static constexpr int kCols = kTokens / kParts;
-  static constexpr int kThreads = 64 + 128 * kParts;  // loads, products, sums
-  static constexpr int kAhead = 8;  // blocks whose scales are fetched together, one such group ahead
-  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + 2 * kAhead * kTokens * 4 + 256;
-  static_assert(kTokens * 128 * 4 <= kStages * kStageBytes, "the sums lie in the ring at the end");
-};
+constexpr int kMaxSplit = 4;
 
-// One CTA: 128 rows of w times kTokens tokens over its cluster rank's part of k; the parts are added up in the order of
-// the ranks through the cluster's shared memory.
-template <int kTokens>
-__global__ void __launch_bounds__(Narrow<kTokens>::kThreads, 2) narrow_kernel(const __grid_constant__ MatmulParams p) {
-  using C = Narrow<kTokens>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align1024(smem_raw);
-  float* scales = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);  // [kParts][2][kAhead][kCols]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scales + 2 * C::kAhead * kTokens);
-  __shared__ uint32_t tmem_slot;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, done = empty + 8 * C::kStages, taken = done + 8 * C::kBufs;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = p.split, rank = blockIdx.x % split;
-  const long n0 = (long)(blockIdx.x / split) * 128, t0 = (long)blockIdx.y * kTokens;
-  const int b0 = (int)((long)p.blocks * rank / split), b1 = (int)((long)p.blocks * (rank + 1) / split);
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
-    }
-    for (int i = 0; i < C::kBufs; ++i) {
-      mbar_init(done + 8 * i, 1);
-      mbar_init(taken + 8 * i, 4 * C::kParts);
-    }
-    fence_mbar_init();
-    prefetch_tensormap(&p.tmap_x);
-    prefetch_tensormap(&p.tmap_w);
-  }
-  if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), C::kColumns);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  await_grid();
-
-  constexpr int kCols = C::kCols;
-  const int col0 = C::kParts > 1 && warp >= 6 ? kCols : 0;
-  float acc[kCols];
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-  bool ok = true;
-  // A bounded wait; after one that ran out the warp takes no more work, and the others' waits run out in turn.
-  auto await = [&](uint32_t bar, uint32_t parity) {
-    if (ok && !warp_wait(bar, parity, false)) {
-      raise_error(p.err, kErrTimeout);
-      ok = false;
-    }
-    return ok;
-  };
-  if (warp == 0) {
-    int b = b0;
-    for (; b < b1; ++b) {
-      const int i = (b - b0) % C::kStages, pass = (b - b0) / C::kStages;
-      if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
-      const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-      warp_load_stage<1>(full + 8 * i, C::kStageBytes, at, &p.tmap_w, (int)n0, at + 128 * kBlockK, &p.tmap_x, (int)t0,
-                         b * kBlockK, 1);
-    }
-    // copies in flight land before the CTA ends, after a wait that ran out too
-    for (int c = max(b0, b - C::kStages); c < b; ++c)
-      mbar_wait(full + 8 * ((c - b0) % C::kStages), ((c - b0) / C::kStages) & 1, kWaitLimit);
-  } else if (warp == 1) {
-    for (int b = b0; b < b1; ++b) {
-      const int j = b - b0, i = j % C::kStages, buf = j % C::kBufs;
-      if (!await(full + 8 * i, (j / C::kStages) & 1)) break;
-      if (j >= C::kBufs && !await(taken + 8 * buf, (j / C::kBufs - 1) & 1)) break;
-      tc_fence_after();
-      const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-      warp_mma_e4m3(tmem + buf * kTokens, sw128_desc(at), sw128_desc(at + 128 * kBlockK), idesc_e4m3_f32(128, kTokens),
-                    empty + 8 * i, done + 8 * buf);
-    }
-  } else {
-    const int quarter = warp & 3;
-    constexpr int kAhead = C::kAhead, kOwn = (kCols * kAhead + 127) / 128;
-    const int part = C::kParts > 1 && warp >= 6, thread = threadIdx.x - 64 - part * 128;
-    float* mine = scales + part * 2 * kAhead * kCols;
-    // the products of the two scales for blocks b .. b + 7: a thread has every 128th
-    float next[kOwn];
-    auto fetch = [&](int b) {
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        const int at = thread + 128 * i, ahead = at % kAhead, c = at / kAhead;
-        const long t = t0 + col0 + c;
-        next[i] = 0.f;
-        if (c < kCols && t < p.tokens && b + ahead < b1)
-          next[i] = p.x_scale[t * p.blocks + b + ahead] * p.w_scale[(n0 >> 7) * p.blocks + b + ahead];
-      }
-    };
-    fetch(b0);
-    for (int b = b0; b < b1; ++b) {  // to the end after a wait that ran out too: the others are at the barrier
-      const int j = b - b0, buf = j % C::kBufs;
-      const float* now = mine + (j / kAhead & 1) * kAhead * kCols + j % kAhead * kCols;
-      if (j % kAhead == 0) {
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) {
-          const int at = thread + 128 * i, ahead = at % kAhead, c = at / kAhead;
-          if (c < kCols) mine[(j / kAhead & 1) * kAhead * kCols + ahead * kCols + c] = next[i];
-        }
-        // the group before the last one was read before the last one's barrier
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
-        fetch(b + kAhead);
-      }
-      if (!await(done + 8 * buf, (j / C::kBufs) & 1)) continue;
-      tc_fence_after();
-      constexpr int kStep = kCols < 32 || C::kParts > 1 ? 16 : 32;  // the registers hold no more beside the sums
-#pragma unroll
-      for (int c = 0; c < kCols; c += kStep) {
-        float d[kStep];
-        tmem_ld_cols<kStep>(tmem + ((uint32_t)(quarter * 32) << 16) + buf * kTokens + col0 + c, d);
-        if (c + kStep == kCols) {
-          tc_fence_before();
-          first_lane_arrive(taken + 8 * buf, lane);
-        }
-#pragma unroll
-        for (int i = 0; i < kStep; i += 4) {
-          const float4 s = *reinterpret_cast<const float4*>(now + c + i);
-          acc[c + i] = fmaf(d[i], s.x, acc[c + i]);
-          acc[c + i + 1] = fmaf(d[i + 1], s.y, acc[c + i + 1]);
-          acc[c + i + 2] = fmaf(d[i + 2], s.z, acc[c + i + 2]);
-          acc[c + i + 3] = fmaf(d[i + 3], s.w, acc[c + i + 3]);
-        }
-      }
-    }
-  }
-  __syncwarp();
-  const int row = (warp & 3) * 32 + lane;
-  if (split == 1) {
-    if (warp >= 2 && n0 + row < p.n) {
-#pragma unroll
-      for (int i = 0; i < kCols; ++i)
-        if (t0 + col0 + i < p.tokens) store_out(p, t0 + col0 + i, n0 + row, acc[i]);
-    }
-  } else {
-    // every product of this CTA is done when its sums are: the ring is free
-    float* sums = reinterpret_cast<float*>(smem);
-    __syncthreads();
-    if (warp >= 2) {
-#pragma unroll
-      for (int i = 0; i < kCols; ++i) sums[(col0 + i) * 128 + row] = acc[i];
-    }
-    cluster_sync();
-    if (warp >= 2 && n0 + row < p.n) {
-      const int c1 = kTokens * (rank + 1) / split;
-      for (int c = kTokens * rank / split + (col0 != 0); c < c1 && t0 + c < p.tokens; c += C::kParts) {
-        const uint32_t at = smem_u32(sums + c * 128 + row);
-        float y = 0.f;
-        for (int r = 0; r < split; ++r) y += ld_cluster(in_cta(at, r));
-        store_out(p, t0 + c, n0 + row, y);
-      }
-    }
-    __syncwarp();
-    cluster_sync();
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, C::kColumns);
-}
-
-template <int kTokens>
-cudaError_t launch_narrow(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul& m) {
-  using C = Narrow<kTokens>;
-  static int done[64] = {0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !done[dev]) {
-    e = cudaFuncSetAttribute(narrow_kernel<kTokens>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) done[dev] = 1;
-  }
-  e = encode_u8_2d_sw128(&p.tmap_x, m.x, m.k, m.tokens, m.x_stride, kBlockK, kTokens);
-  if (e != cudaSuccess) return e;
-  const long tiles = (m.n + 127) / 128, groups = (m.tokens + kTokens - 1) / kTokens;
-  int split = 1;
-  if (getenv("GDN_S")) split = atoi(getenv("GDN_S"));
-  else while (split < 8 && 2 * split <= p.blocks && tiles * groups * split * 2 <= 304) split *= 2;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = split;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  p.split = split;
-  cfg.gridDim = dim3((unsigned)(split * tiles), (unsigned)groups);
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = env.stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, narrow_kernel<kTokens>, p);
-}
-
-// ---------------------------------------------------------------- many tokens: tokens as the rows of a tile
-
-struct Wide {
-  static constexpr int kTileM = 128, kTileN = 256;  // tokens, rows of w
-  static constexpr int kStageBytes = (kTileM + kTileN) * kBlockK;
-  static constexpr int kStages = 4;
-  static constexpr int kWarps = 8;  // of sums: each has 32 tokens x 128 columns
-  static constexpr int kThreads = 128 + 32 * kWarps;  // one warp loads, one issues products, two stand by
+template <int kN>
+struct Tiles {
+  static constexpr bool kLarge = kN == 256;
+  static constexpr int kTileM = 128, kTileN = kN;  // tokens, rows of w
+  static constexpr int kRing = 4 * (kTileM + kTileN) * kBlockK;  // four stages, or up to eight of fewer tokens
+  static constexpr int kMaxStages = 8;
+  static constexpr int kBufs = kLarge ? 2 : 4;  // results of blocks in tensor memory, at most as many as stages
+  static constexpr int kFirst = kLarge ? 4 : 2;  // warps before those of the sums: one loads, one issues products
+  static constexpr int kWarps = 8;               // of sums: each has 32 tokens x half the columns
+  static constexpr int kCols = kTileN / 2, kChunk = kLarge ? 32 : 16;
+  static constexpr int kThreads = 32 * (kFirst + kWarps);
   static constexpr int kPitch = 17;  // of a warp's 32 x 16 values on their way out
-  static constexpr int kAhead = 8;  // blocks whose scales are fetched together, one such group ahead
-  static constexpr int kScales = 2 * kAhead * (32 * kWarps + 8);  // a token's for its two threads; the weights' for a warp
-  static constexpr size_t kSmem = 1024 + kStages * kStageBytes + kWarps * 32 * kPitch * 4 + kScales * 4 + 256;
+  static constexpr int kPartPitch = kTileN + 4;  // of a part's sums, in the ring
+  static_assert(kTileM * kPartPitch * 4 <= kRing, "");
+  static constexpr int kAhead = kLarge ? 8 : 4;  // blocks whose scales are fetched together, one such group ahead
+  static constexpr int kScales = 2 * kAhead * 33 * kWarps;  // a token's for its two threads; the weights' for a warp
+  // rows on their way out lie in the ring where a CTA has one tile only
+  static constexpr size_t kSmem = 1024 + kRing + (kLarge ? kWarps * 32 * kPitch * 4 : 0) + kScales * 4 + 256;
 };
 
 // four bytes to shared memory, without waiting for them
@@ -502,8 +274,8 @@ __device__ __forceinline__ void copy4(float* dst, const float* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// tmem_ld32 in two steps: the values are there after the second one
-__device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, uint32_t (&r)[32]) {
+// tmem_ld_cols in two steps: the values are there after the second one
+__device__ __forceinline__ void tmem_ld_begin(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -516,7 +288,25 @@ __device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, uint32_t (&r)[32
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32_end(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_begin(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_end(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_end(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
@@ -535,37 +325,39 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& m
   m = 8 * g + in - n * rows;
 }
 
-// kShare CTAs of a cluster take tiles of the same rows of w, above one another: each loads its share of them for all.
-template <int kShare>
-__global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_constant__ MatmulParams p) {
-  using C = Wide;
+// kSplit: the CTAs of a cluster share a tile, each a part of its blocks; the parts are added up through the cluster's shared
+// memory, each CTA its share of the tokens, beginning with its own part (all at once from one CTA they would queue there).  Otherwise a CTA takes tile after tile.
+template <int kN, bool kSplit>
+__global__ void __launch_bounds__(Tiles<kN>::kThreads, Tiles<kN>::kLarge ? 1 : 2) tile_kernel(const __grid_constant__ MatmulParams p) {
+  using C = Tiles<kN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  float* stage_out = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
-  float* scales = stage_out + C::kWarps * 32 * C::kPitch;  // [2][kAhead][kWarps][32], then [2][kWarps][kAhead]
+  float* stage_out = reinterpret_cast<float*>(smem + C::kRing);
+  float* scales = C::kLarge ? stage_out + C::kWarps * 32 * C::kPitch : stage_out;  // [2][kAhead][kWarps][32], then [2][kWarps][kAhead]
   uint64_t* bars = reinterpret_cast<uint64_t*>(scales + C::kScales);
   __shared__ uint32_t tmem_slot;
-  const uint32_t full = smem_u32(bars), empty = full + 8 * C::kStages, done = empty + 8 * C::kStages, taken = done + 32;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * C::kMaxStages, done = empty + 8 * C::kMaxStages;
+  // a stage: rows_x tokens, then the rows of w.  Products take 128 tokens all the same: what lies behind the last one
+  // reaches rows of the result that are not written
+  const int stages = p.stages, x_bytes = p.rows_x * kBlockK, stage_bytes = x_bytes + kN * kBlockK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % kShare, first = blockIdx.x / kShare, step = gridDim.x / kShare;
-  constexpr uint16_t kAll = (1 << kShare) - 1;  // the cluster's CTAs
+  const int split = kSplit ? p.split : 1, rank = kSplit ? blockIdx.x % split : 0;
+  const int first = kSplit ? blockIdx.x / split : blockIdx.x, step = kSplit ? gridDim.x / split : gridDim.x;
+  const int begin = kSplit ? (int)((long)p.blocks * rank / split) : 0;  // this CTA's blocks
+  const int end = kSplit ? (int)((long)p.blocks * (rank + 1) / split) : p.blocks;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 2 * kShare);
+    for (int i = 0; i < stages; ++i) {
+      mbar_init(full + 8 * i, 1 + C::kWarps);
+      mbar_init(empty + 8 * i, 1);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(done + 8 * i, 1);
-      mbar_init(taken + 8 * i, C::kWarps / 2);
-    }
+    for (int i = 0; i < C::kBufs; ++i) mbar_init(done + 8 * i, 1);
     fence_mbar_init();
     prefetch_tensormap(&p.tmap_x);
     prefetch_tensormap(&p.tmap_w);
   }
-  if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), 512);
+  if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), C::kBufs * kN);
   tc_fence_before();
   __syncthreads();
-  if constexpr (kShare > 1) cluster_sync();  // the others' barriers are there
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   await_grid();
@@ -579,128 +371,140 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
     return ok;
   };
   const int tiles = p.tiles_m * p.tiles_n;
-  // 384 threads are launched with 168 registers each; 56 in the first four warps leave 224 for those of the sums
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  // large tiles: 384 threads are launched with 168 registers each; 56 in the first four warps leave 224 for the sums'
+  if (warp < C::kFirst) {
+    if constexpr (C::kLarge) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     int i = 0, pass = 0;  // stage, passes over the ring
     for (int id = first; id < tiles && ok; id += step) {
       int m, n;
       tile_of(id, p.tiles_m, p.tiles_n, m, n);
-      for (int b = 0; b < p.blocks; ++b) {
+      for (int b = begin; b < end; ++b) {
         if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
-        const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-        constexpr int kPart = C::kTileN / kShare;
-        warp_load_stage<kShare>(full + 8 * i, C::kStageBytes, at, &p.tmap_x, (m * kShare + rank) * C::kTileM,
-                                at + (C::kTileM + rank * kPart) * kBlockK, &p.tmap_w, n * C::kTileN + rank * kPart, b * kBlockK,
-                                kAll);
-        if (++i == C::kStages) i = 0, ++pass;
+        const uint32_t at = smem_u32(smem) + i * stage_bytes;
+        warp_load_stage(full + 8 * i, stage_bytes, at, &p.tmap_x, m * C::kTileM, at + x_bytes, &p.tmap_w, n * C::kTileN,
+                        b * kBlockK);
+        if (++i == stages) i = 0, ++pass;
       }
     }
     // copies in flight land before the CTA ends, after a wait that ran out too
-      for (int c = 0; c < C::kStages; ++c) {
-        const int passes = pass + (c < i);  // loads into stage c
-        if (passes) mbar_wait(full + 8 * c, (passes - 1) & 1, kWaitLimit);
-      }
-  } else if (warp < 3) {
-    // each of these warps issues the products of one half of the columns
-    const int side = warp - 1;
+    for (int c = 0; c < stages; ++c) {
+      const int passes = pass + (c < i);  // loads into stage c
+      if (passes) mbar_wait(full + 8 * c, (passes - 1) & 1, kWaitLimit);
+    }
+  } else if (warp == 1) {
+    // A full stage has its loads and the word of the sums that they have read what lay in its place of tensor memory: one wait
+    // for each block.  The tensor cores hold about two instructions ahead, and a wait takes 150 cycles beside them: with
+    // two the products of a block took 711 cycles instead of 552.
     int i = 0, pass = 0, j = 0;
     for (int id = first; id < tiles && ok; id += step)
-      for (int b = 0; b < p.blocks; ++b, ++j) {
-        const int buf = 2 * side + (j & 1);
+      for (int b = begin; b < end; ++b, ++j) {
         if (!await(full + 8 * i, pass & 1)) break;
-        if (j >= 2 && !await(taken + 8 * buf, ((j >> 1) - 1) & 1)) break;
         tc_fence_after();
-        const uint32_t at = smem_u32(smem + i * C::kStageBytes);
-        warp_mma_e4m3<kShare>(tmem + buf * 128, sw128_desc(at), sw128_desc(at + (C::kTileM + side * 128) * kBlockK),
-                      idesc_e4m3_f32(128, 128), empty + 8 * i, done + 8 * buf, kAll);
-        if (++i == C::kStages) i = 0, ++pass;
+        const uint32_t at = smem_u32(smem) + i * stage_bytes;
+        warp_mma_e4m3(tmem + j % C::kBufs * kN, sw128_desc(at), sw128_desc(at + x_bytes),
+                      idesc_e4m3_f32(C::kTileM, kN), empty + 8 * i, done + 8 * (j % C::kBufs));
+        if (++i == stages) i = 0, ++pass;
       }
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    const int quarter = warp & 3, side = (warp - 4) >> 2;  // of the columns
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + side * 256;
-    float* mine = stage_out + (warp - 4) * 32 * C::kPitch;
+    if constexpr (C::kLarge) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int quarter = warp & 3, own = warp - C::kFirst, side = own >> 2;  // side: of the columns
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + side * C::kCols;
+    for (int i = 0; i < C::kBufs; ++i) first_lane_arrive(full + 8 * i, lane);  // tensor memory is free at first
+    int stage = C::kBufs % stages;  // of the block that goes to the place just read
+    float* mine = (C::kLarge ? stage_out : reinterpret_cast<float*>(smem)) + own * 32 * C::kPitch;
     constexpr int kAhead = C::kAhead;
-    float* own_x = scales + (warp - 4) * 32;  // its tokens' scales, a row for each block of two groups
-    float* own_w = scales + 2 * kAhead * 32 * C::kWarps + (warp - 4) * kAhead;
+    float* own_x = scales + own * 32;  // its tokens' scales, a row for each block of two groups
+    float* own_w = scales + 2 * kAhead * 32 * C::kWarps + own * kAhead;
     int j = 0, group = 0;
     for (int id = first; id < tiles && ok; id += step) {
       int m, n;
       tile_of(id, p.tiles_m, p.tiles_n, m, n);
-      const long t0 = (long)(m * kShare + rank) * C::kTileM + quarter * 32, t = t0 + lane;
-      const long n0 = (long)n * C::kTileN + side * 128;
+      const long t0 = (long)m * C::kTileM + quarter * 32, t = t0 + lane;
+      const long n0 = (long)n * C::kTileN + side * C::kCols;
       // tokens and columns behind the last ones take the last ones' scales: what they are multiplied with is not written
       const float* sw = p.w_scale + (min(n0, (long)p.n - 1) >> 7) * p.blocks;
-      float2 acc[64];
+      float2 acc[C::kCols / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      // a group of blocks' scales, eight blocks of four tokens at a time: a sector of each token's row
+      for (int i = 0; i < C::kCols / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      // a group of blocks' scales, neighbours of a token's row by neighbouring lanes
       auto fetch = [&](int b) {
-        const int to = (group + (b > 0)) & 1, u = lane & 7;
-        if (b + u < p.blocks) {
+        const int to = (group + (b > begin)) & 1, u = lane % kAhead;
+        if (b + u < end) {
           const float* from = p.x_scale + b + u;
           float* x_to = own_x + (to * kAhead + u) * 32 * C::kWarps;
 #pragma unroll
-          for (int i = lane >> 3; i < 32; i += 4) copy4(x_to + i, from + min(t0 + i, (long)p.tokens - 1) * p.blocks);
+          for (int i = lane / kAhead; i < 32; i += 32 / kAhead) copy4(x_to + i, from + min(t0 + i, (long)p.tokens - 1) * p.blocks);
           if (lane < kAhead) copy4(own_w + to * kAhead * C::kWarps + u, sw + b + u);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      fetch(0);
+      fetch(begin);
       float2 s = make_float2(0.f, 0.f);
-      uint32_t d[2][32];
-      // Block b's products are there: its scale, and the first 32 of its columns on their way.
-      auto begin = [&](int b) {
-        if (b % kAhead == 0) {
-          if (b) ++group;
+      constexpr int kChunk = C::kChunk, kChunks = C::kCols / kChunk;
+      static_assert(kChunks % 2 == 0, "");
+      uint32_t d[2][kChunk];
+      // Block b's products are there: its scale, and the first of its columns on their way.
+      auto start = [&](int b) {
+        const int u = (b - begin) % kAhead;
+        if (u == 0) {
+          if (b > begin) ++group;
           fetch(b + kAhead);
           asm volatile("cp.async.wait_group 1;" ::: "memory");
           __syncwarp();
         }
-        const int at = (group & 1) * kAhead + b % kAhead;
-        const float v = own_x[at * 32 * C::kWarps + lane] * own_w[((group & 1) * C::kWarps) * kAhead + b % kAhead];
+        const float v = own_x[((group & 1) * kAhead + u) * 32 * C::kWarps + lane] * own_w[(group & 1) * C::kWarps * kAhead + u];
         s = make_float2(v, v);
-        if (!await(done + 8 * (2 * side + (j & 1)), (j >> 1) & 1)) return;
+        if (!await(done + 8 * (j % C::kBufs), j / C::kBufs & 1)) return;
         tc_fence_after();
-        tmem_ld32_begin(lanes + (j & 1) * 128, d[0]);
+        tmem_ld_begin(lanes + j % C::kBufs * kN, d[0]);
       };
-      begin(0);
+      if (begin < end) start(begin);
 #pragma unroll 1
-      for (int b = 0; b < p.blocks && ok; ++b) {
+      for (int b = begin; b < end && ok; ++b) {
         const float2 now = s;
-        const uint32_t at = lanes + (j & 1) * 128;
-        // 32 columns are on their way while the 32 before them are added: the next block's first ones beside its last
+        const uint32_t at = lanes + j % C::kBufs * kN;
+        // a chunk of columns is on its way while the one before it is added: the next block's first one beside its last
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32_end(d[c & 1]);
-          if (c < 3) {
-            tmem_ld32_begin(at + (c + 1) * 32, d[~c & 1]);
+        for (int c = 0; c < kChunks; ++c) {
+          tmem_ld_end(d[c & 1]);
+          if (c < kChunks - 1) {
+            tmem_ld_begin(at + (c + 1) * kChunk, d[~c & 1]);
           } else {
             tc_fence_before();
-            first_lane_arrive(taken + 8 * (2 * side + (j & 1)), lane);
+            first_lane_arrive(full + 8 * stage, lane);
+            if (++stage == stages) stage = 0;
             ++j;
-            if (b + 1 < p.blocks) begin(b + 1);
+            if (b + 1 < end) start(b + 1);
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            acc[c * 16 + i] = __ffma2_rn(make_float2(__uint_as_float(d[c & 1][2 * i]), __uint_as_float(d[c & 1][2 * i + 1])),
-                                         now, acc[c * 16 + i]);
+          for (int i = 0; i < kChunk / 2; ++i)
+            acc[c * (kChunk / 2) + i] =
+                __ffma2_rn(make_float2(__uint_as_float(d[c & 1][2 * i]), __uint_as_float(d[c & 1][2 * i + 1])), now,
+                           acc[c * (kChunk / 2) + i]);
         }
       }
       ++group;
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncwarp();
+      if constexpr (kSplit) {  // every product of this CTA is done when its sums are: the ring is free
+        float* part = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * C::kPartPitch + side * C::kCols;
+        asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
+        if (t < p.tokens)
+#pragma unroll
+        for (int i = 0; i < C::kCols / 4; ++i)
+          reinterpret_cast<float4*>(part)[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+        break;
+      }
       if (!ok) break;
-      if (p.wide_out) {  // whole sectors of a row from its thread
+      if (p.whole_out) {  // whole sectors of a row from its thread
         if (t < p.tokens) {
           const long at = t * p.out_stride + n0;
           if (p.out_f32) {
             float* to = static_cast<float*>(p.out) + at;
 #pragma unroll
-            for (int i = 0; i < 128 / 8; ++i) {
+            for (int i = 0; i < C::kCols / 8; ++i) {
               uint32_t v[8];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
@@ -712,7 +516,7 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
           } else {
             uint16_t* to = static_cast<uint16_t*>(p.out) + at;
 #pragma unroll
-            for (int i = 0; i < 128 / 16; ++i) {
+            for (int i = 0; i < C::kCols / 16; ++i) {
               uint32_t v[8];
 #pragma unroll
               for (int q = 0; q < 8; ++q) v[q] = pack_bf2(acc[8 * i + q].x, acc[8 * i + q].y);
@@ -721,8 +525,10 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
           }
         }
       } else {  // rows of any alignment: 32 x 16 values at a time through shared memory, half a row a store
+        // a small tile's CTA has no other one: the ring is free
+        if constexpr (!C::kLarge) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
 #pragma unroll
-        for (int c = 0; c < 128 / 16; ++c) {
+        for (int c = 0; c < C::kCols / 16; ++c) {
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -739,58 +545,124 @@ __global__ void __launch_bounds__(Wide::kThreads, 1) wide_kernel(const __grid_co
     }
   }
   __syncwarp();
+  if constexpr (kSplit) {
+    cluster_sync();
+    if (warp >= C::kFirst) {  // kN / 8 lanes take a token, a lane eight columns
+      int m, n;
+      tile_of(first, p.tiles_m, p.tiles_n, m, n);
+      constexpr int kLanes = kN / 8, kTokens = 32 / kLanes;
+      const int rows = (int)min((long)C::kTileM, p.tokens - (long)m * C::kTileM), last = rows * (rank + 1) / split;
+      const long n0 = (long)n * C::kTileN + lane % kLanes * 8;
+#pragma unroll 2
+      for (int r = rows * rank / split + (warp - C::kFirst) * kTokens + lane / kLanes; r < last; r += C::kWarps * kTokens) {
+        const long t = (long)m * C::kTileM + r;
+        const uint32_t at = smem_u32(reinterpret_cast<float*>(smem) + r * C::kPartPitch + lane % kLanes * 8);
+        float4 part[kMaxSplit][2];
+#pragma unroll
+        for (int i = 0; i < kMaxSplit; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            part[i][h] = i < split ? ld_cluster(in_cta(at + 16 * h, (rank + i) & (split - 1))) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kMaxSplit; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            y[4 * h] += part[i][h].x;
+            y[4 * h + 1] += part[i][h].y;
+            y[4 * h + 2] += part[i][h].z;
+            y[4 * h + 3] += part[i][h].w;
+          }
+        if (p.whole_out) {
+          if (n0 < p.n) {
+            if (p.out_f32) {
+              float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.out) + t * p.out_stride + n0);
+              to[0] = make_float4(y[0], y[1], y[2], y[3]);
+              to[1] = make_float4(y[4], y[5], y[6], y[7]);
+            } else {
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + t * p.out_stride + n0) =
+                  make_uint4(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]), pack_bf2(y[4], y[5]), pack_bf2(y[6], y[7]));
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (n0 + i < p.n) store_out(p, t, n0 + i, y[i]);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // the others have read this CTA's part
+  }
   tc_fence_before();
   __syncthreads();
-  if constexpr (kShare > 1) cluster_sync();  // what the others load and signal here has come
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, C::kBufs * kN);
 }
 
-template <int kShare>
-cudaError_t launch_wide(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul& m) {
-  using C = Wide;
-  static int clusters[64] = {0};  // that fit the device
+template <int kN, bool kSplit>
+cudaError_t launch_tiles(const LaunchEnv& env, const MatmulParams& p, long ctas) {
+  using C = Tiles<kN>;
+  static int done[64] = {0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(tile_kernel<kN, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = 1;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kShare;
+  attr[1].val.clusterDim.x = p.split;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kShare);
+  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = env.stream;
   cfg.attrs = attr;
-  cfg.numAttrs = kShare > 1 ? 2 : 1;
-  int fit = dev < 64 ? clusters[dev] : 0;
-  if (!fit) {
-    e = cudaFuncSetAttribute(wide_kernel<kShare>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
-    if (e != cudaSuccess) return e;
-    if (kShare == 1) e = device_sm_count(&fit);
-    else {
-      cudaLaunchConfig_t q = cfg;
-      q.attrs = attr + 1;
-      q.numAttrs = 1;
-      e = cudaOccupancyMaxActiveClusters(&fit, wide_kernel<kShare>, &q);
-    }
-    if (e != cudaSuccess) return e;
-    if (getenv("GDN_VERBOSE")) fprintf(stderr, "clusters of %d: %d\n", kShare, fit);
-    if (dev < 64) clusters[dev] = fit;
-  }
-  e = encode_u8_2d_sw128(&p.tmap_x, m.x, m.k, m.tokens, m.x_stride, kBlockK, C::kTileM);
-  if (e == cudaSuccess) e = encode_u8_2d_sw128(&p.tmap_w, m.w, m.k, m.n, m.w_stride, kBlockK, C::kTileN / kShare);
+  cfg.numAttrs = kSplit ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, tile_kernel<kN, kSplit>, p);
+}
+
+template <int kN>
+cudaError_t encode_tiles(MatmulParams& p, const Fp8Matmul& m) {
+  p.tiles_m = (int)((m.tokens + 127L) / 128);
+  p.tiles_n = (int)((m.n + (long)kN - 1) / kN);
+  // Rows of x that are not there are not asked for: filling them with zeroes takes the time of loads (17 tokens x 16384 x
+  // 2048: FIGURES).  What the stage holds in their place reaches rows of the result that are not written.
+  p.rows_x = m.tokens < 128 ? (m.tokens + 7) / 8 * 8 : 128;
+  const int fit = Tiles<kN>::kRing / ((p.rows_x + kN) * kBlockK);
+  p.stages = fit < Tiles<kN>::kMaxStages ? fit : Tiles<kN>::kMaxStages;
+  const cudaError_t e = encode_u8_2d_sw128(&p.tmap_x, m.x, m.k, m.tokens, m.x_stride, kBlockK, p.rows_x);
+  return e == cudaSuccess ? encode_u8_2d_sw128(&p.tmap_w, m.w, m.k, m.n, m.w_stride, kBlockK, kN) : e;
+}
+
+cudaError_t launch_many(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul& m) {
+  int sms = 0;
+  cudaError_t e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
-  p.tiles_m = (int)((m.tokens + (long)C::kTileM * kShare - 1) / (C::kTileM * kShare));
-  p.tiles_n = (int)((m.n + (long)C::kTileN - 1) / C::kTileN);
   const long bytes = m.out_f32 ? 4 : 2;
-  p.wide_out = (reinterpret_cast<uintptr_t>(m.out) & 31u) == 0 && m.out_stride * bytes % 32 == 0 && m.n * bytes % 32 == 0;
+  p.whole_out = (reinterpret_cast<uintptr_t>(m.out) & 31u) == 0 && m.out_stride * bytes % 32 == 0 && m.n * bytes % 32 == 0;
+  const long small = ((m.tokens + 127L) / 128) * ((m.n + 63L) / 64);
+  bool use_small = small <= sms;
+  if (getenv("GDN_SM")) use_small = atoi(getenv("GDN_SM"));
+  if (use_small) {
+    e = encode_tiles<64>(p, m);
+    if (e != cudaSuccess) return e;
+    p.split = 1;
+    while (p.split < kMaxSplit && 2 * p.split <= p.blocks && 2 * p.split * small <= sms) p.split *= 2;
+    if (getenv("GDN_S")) p.split = atoi(getenv("GDN_S"));
+    if (p.split > 1) return launch_tiles<64, true>(env, p, small * p.split);
+    return launch_tiles<64, false>(env, p, small);
+  }
+  e = encode_tiles<256>(p, m);
+  if (e != cudaSuccess) return e;
   const long tiles = (long)p.tiles_m * p.tiles_n;
-  cfg.gridDim = dim3((unsigned)(tiles < fit ? tiles : fit) * kShare);
-  return cudaLaunchKernelEx(&cfg, wide_kernel<kShare>, p);
+  return launch_tiles<256, false>(env, p, tiles < sms ? tiles : sms);
 }
 
 }  // namespace
@@ -812,16 +684,10 @@ cudaError_t launch_fp8_matmul(const LaunchEnv& env, const Fp8Matmul& m) {
   p.out_stride = m.out_stride;
   p.out_f32 = m.out_f32;
   p.err = env.err;
-  if (getenv("GDN_WIDE") && atoi(getenv("GDN_WIDE")) && m.tokens > 128) { const int s = atoi(getenv("GDN_WIDE")); return s == 4 ? launch_wide<4>(env, p, m) : s == 2 ? launch_wide<2>(env, p, m) : launch_wide<1>(env, p, m); }
   const unsigned few = (unsigned)((m.n + 15L) / 16);
   if (m.tokens <= 8) return launch_early(few_kernel<1>, dim3(few), kFewWarps * 32, 0, env.stream, p);
-  if (m.tokens <= 16 && !getenv("GDN_NOFEW2")) return launch_early(few_kernel<2>, dim3(few), kFewWarps * 32, 0, env.stream, p);
-  cudaError_t e = encode_u8_2d_sw128(&p.tmap_w, m.w, m.k, m.n, m.w_stride, kBlockK, 128);
-  if (e != cudaSuccess) return e;
-  if (m.tokens <= 16) return launch_narrow<16>(env, p, m);
-  if (m.tokens <= 32) return launch_narrow<32>(env, p, m);
-  if (m.tokens <= 64) return launch_narrow<64>(env, p, m);
-  return launch_narrow<128>(env, p, m);
+  if (m.tokens <= 16) return launch_early(few_kernel<2>, dim3(few), kFewWarps * 32, 0, env.stream, p);
+  return launch_many(env, p, m);
 }
 
 }  // namespace gdn
