@@ -5,8 +5,6 @@
 // The inner sum is four tcgen05 instructions on one 128-byte-wide stage of each operand; its result lies in tensor memory
 // and is taken into the running fp32 sums of the registers with the block's scales, while the next block's products run
 // into the other half of the accumulators.
-#include <stdio.h>
-#include <stdlib.h>
 #include <string.h>
 
 #include "attn_common.cuh"
@@ -64,12 +62,13 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
 }
 
 // D[tmem] = A[smem] B[smem]^T over one stage, by the whole warp: four steps of 32 codes, the first one on nothing.  When it
-// is done `stage` and `result` get an arrival each.
+// is done `stage` gets an arrival, and `result` too where `last`.
 __device__ __forceinline__ void warp_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                              uint32_t stage, uint32_t result) {
+                                              uint32_t stage, uint32_t result, bool last) {
   asm volatile(
-      "{\n.reg .pred e, p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      "{\n.reg .pred e, f, p, q;\n.reg .b64 a1, a2, a3, b1, b2, b3;\n"
       "elect.sync _|e, 0xFFFFFFFF;\n"
+      "setp.ne.and.b32 f, %6, 0, e;\n"
       "setp.ne.b32 p, 0, 0;\n"
       "setp.ne.b32 q, 1, 0;\n"
       "add.s64 a1, %1, 2;\nadd.s64 a2, %1, 4;\nadd.s64 a3, %1, 6;\n"
@@ -79,8 +78,8 @@ __device__ __forceinline__ void warp_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, 
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, q;\n"
       "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, q;\n"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%4];\n"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(stage), "r"(result)
+      "@f tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(stage), "r"(result), "r"((int)last)
       : "memory");
 }
 
@@ -253,20 +252,23 @@ template <int kN>
 struct Tiles {
   static constexpr bool kLarge = kN == 256;
   static constexpr int kTileM = 128, kTileN = kN;  // tokens, rows of w
-  static constexpr int kRing = 4 * (kTileM + kTileN) * kBlockK;  // four stages, or up to eight of fewer tokens
-  static constexpr int kMaxStages = 8;
-  static constexpr int kBufs = kLarge ? 2 : 4;  // results of blocks in tensor memory, at most as many as stages
+  static constexpr int kRing = 196608;  // bytes: at least four (eight) stages, more of fewer tokens
+  static constexpr int kMaxStages = 16;
+  static constexpr int kBufs = 512 / kN;  // results of blocks in tensor memory, at most as many as stages
+  // Blocks whose results are taken together.  A word between the warps or a load from tensor memory is 100 to 200 cycles on
+  // its way: small tiles' 64 columns are added in less.
+  static constexpr int kGroup = kLarge ? 1 : 2;
   static constexpr int kFirst = kLarge ? 4 : 2;  // warps before those of the sums: one loads, one issues products
   static constexpr int kWarps = 8;               // of sums: each has 32 tokens x half the columns
-  static constexpr int kCols = kTileN / 2, kChunk = kLarge ? 32 : 16;
+  static constexpr int kCols = kTileN / 2;
   static constexpr int kThreads = 32 * (kFirst + kWarps);
   static constexpr int kPitch = 17;  // of a warp's 32 x 16 values on their way out
   static constexpr int kPartPitch = kTileN + 4;  // of a part's sums, in the ring
   static_assert(kTileM * kPartPitch * 4 <= kRing, "");
-  static constexpr int kAhead = kLarge ? 8 : 4;  // blocks whose scales are fetched together, one such group ahead
+  static constexpr int kAhead = 8;  // blocks whose scales are fetched together, one such group ahead
   static constexpr int kScales = 2 * kAhead * 33 * kWarps;  // a token's for its two threads; the weights' for a warp
   // rows on their way out lie in the ring where a CTA has one tile only
-  static constexpr size_t kSmem = 1024 + kRing + (kLarge ? kWarps * 32 * kPitch * 4 : 0) + kScales * 4 + 256;
+  static constexpr size_t kSmem = 1024 + kRing + (kLarge ? kWarps * 32 * kPitch * 4 : 0) + kScales * 4 + 384;
 };
 
 // four bytes to shared memory, without waiting for them
@@ -287,24 +289,6 @@ __device__ __forceinline__ void tmem_ld_begin(uint32_t taddr, uint32_t (&r)[32])
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
-}
-__device__ __forceinline__ void tmem_ld_begin(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld_end(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-                 "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
 }
 __device__ __forceinline__ void tmem_ld_end(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -328,7 +312,7 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& m
 // kSplit: the CTAs of a cluster share a tile, each a part of its blocks; the parts are added up through the cluster's shared
 // memory, each CTA its share of the tokens, beginning with its own part (all at once from one CTA they would queue there).  Otherwise a CTA takes tile after tile.
 template <int kN, bool kSplit>
-__global__ void __launch_bounds__(Tiles<kN>::kThreads, Tiles<kN>::kLarge ? 1 : 2) tile_kernel(const __grid_constant__ MatmulParams p) {
+__global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __grid_constant__ MatmulParams p) {
   using C = Tiles<kN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -350,7 +334,7 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, Tiles<kN>::kLarge ? 1 : 2
       mbar_init(full + 8 * i, 1 + C::kWarps);
       mbar_init(empty + 8 * i, 1);
     }
-    for (int i = 0; i < C::kBufs; ++i) mbar_init(done + 8 * i, 1);
+    for (int i = 0; i < C::kBufs / C::kGroup; ++i) mbar_init(done + 8 * i, 1);
     fence_mbar_init();
     prefetch_tensormap(&p.tmap_x);
     prefetch_tensormap(&p.tmap_w);
@@ -403,7 +387,8 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, Tiles<kN>::kLarge ? 1 : 2
         tc_fence_after();
         const uint32_t at = smem_u32(smem) + i * stage_bytes;
         warp_mma_e4m3(tmem + j % C::kBufs * kN, sw128_desc(at), sw128_desc(at + x_bytes),
-                      idesc_e4m3_f32(C::kTileM, kN), empty + 8 * i, done + 8 * (j % C::kBufs));
+                      idesc_e4m3_f32(C::kTileM, kN), empty + 8 * i, done + 8 * (j % C::kBufs / C::kGroup),
+                      C::kGroup == 1 || j % C::kGroup == C::kGroup - 1 || b + 1 == end);
         if (++i == stages) i = 0, ++pass;
       }
   }
@@ -441,12 +426,8 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, Tiles<kN>::kLarge ? 1 : 2
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
       fetch(begin);
-      float2 s = make_float2(0.f, 0.f);
-      constexpr int kChunk = C::kChunk, kChunks = C::kCols / kChunk;
-      static_assert(kChunks % 2 == 0, "");
-      uint32_t d[2][kChunk];
-      // Block b's products are there: its scale, and the first of its columns on their way.
-      auto start = [&](int b) {
+      // the scale of block b; at the first one of a group, the next group's are fetched
+      auto scale = [&](int b) {
         const int u = (b - begin) % kAhead;
         if (u == 0) {
           if (b > begin) ++group;
@@ -454,35 +435,64 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, Tiles<kN>::kLarge ? 1 : 2
           asm volatile("cp.async.wait_group 1;" ::: "memory");
           __syncwarp();
         }
-        const float v = own_x[((group & 1) * kAhead + u) * 32 * C::kWarps + lane] * own_w[(group & 1) * C::kWarps * kAhead + u];
-        s = make_float2(v, v);
-        if (!await(done + 8 * (j % C::kBufs), j / C::kBufs & 1)) return;
-        tc_fence_after();
-        tmem_ld_begin(lanes + j % C::kBufs * kN, d[0]);
+        return own_x[((group & 1) * kAhead + u) * 32 * C::kWarps + lane] * own_w[(group & 1) * C::kWarps * kAhead + u];
       };
-      if (begin < end) start(begin);
+      auto add = [&](const uint32_t(&d)[32], int c, float s) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          acc[c * 16 + i] = __ffma2_rn(make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])),
+                                       make_float2(s, s), acc[c * 16 + i]);
+      };
+      auto read = [&]() {  // a block's results are read: its place is free
+        first_lane_arrive(full + 8 * stage, lane);
+        if (++stage == stages) stage = 0;
+        ++j;
+      };
+      uint32_t d[2][32];
+      if constexpr (C::kLarge) {
+        float s = 0.f;
+        // Block b's products are there: its scale, and the first 32 of its columns on their way.
+        auto start = [&](int b) {
+          s = scale(b);
+          if (!await(done + 8 * (j & 1), j >> 1 & 1)) return;
+          tc_fence_after();
+          tmem_ld_begin(lanes + (j & 1) * kN, d[0]);
+        };
+        if (begin < end) start(begin);
 #pragma unroll 1
-      for (int b = begin; b < end && ok; ++b) {
-        const float2 now = s;
-        const uint32_t at = lanes + j % C::kBufs * kN;
-        // a chunk of columns is on its way while the one before it is added: the next block's first one beside its last
+        for (int b = begin; b < end && ok; ++b) {
+          const float now = s;
+          const uint32_t at = lanes + (j & 1) * kN;
+          // 32 columns are on their way while the 32 before them are added: the next block's first ones beside its last
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-          tmem_ld_end(d[c & 1]);
-          if (c < kChunks - 1) {
-            tmem_ld_begin(at + (c + 1) * kChunk, d[~c & 1]);
-          } else {
-            tc_fence_before();
-            first_lane_arrive(full + 8 * stage, lane);
-            if (++stage == stages) stage = 0;
-            ++j;
-            if (b + 1 < end) start(b + 1);
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld_end(d[c & 1]);
+            if (c < 3) {
+              tmem_ld_begin(at + (c + 1) * 32, d[~c & 1]);
+            } else {
+              tc_fence_before();
+              read();
+              if (b + 1 < end) start(b + 1);
+            }
+            add(d[c & 1], c, now);
           }
-#pragma unroll
-          for (int i = 0; i < kChunk / 2; ++i)
-            acc[c * (kChunk / 2) + i] =
-                __ffma2_rn(make_float2(__uint_as_float(d[c & 1][2 * i]), __uint_as_float(d[c & 1][2 * i + 1])), now,
-                           acc[c * (kChunk / 2) + i]);
+        }
+      } else {
+#pragma unroll 1
+        for (int b = begin; b < end; b += 2) {
+          const bool two = b + 1 < end;
+          const float s0 = scale(b), s1 = two ? scale(b + 1) : 0.f;
+          if (!await(done + 8 * (j % C::kBufs / 2), j / C::kBufs & 1)) break;
+          tc_fence_after();
+          tmem_ld_begin(lanes + j % C::kBufs * kN, d[0]);
+          if (two) tmem_ld_begin(lanes + (j + 1) % C::kBufs * kN, d[1]);
+          tmem_ld_end(d[0]);
+          tmem_ld_end(d[1]);
+          tc_fence_before();
+          read();
+          if (two) read();
+          add(d[0], 0, s0);
+          if (two) add(d[1], 0, s1);
         }
       }
       ++group;
@@ -632,8 +642,8 @@ template <int kN>
 cudaError_t encode_tiles(MatmulParams& p, const Fp8Matmul& m) {
   p.tiles_m = (int)((m.tokens + 127L) / 128);
   p.tiles_n = (int)((m.n + (long)kN - 1) / kN);
-  // Rows of x that are not there are not asked for: filling them with zeroes takes the time of loads (17 tokens x 16384 x
-  // 2048: FIGURES).  What the stage holds in their place reaches rows of the result that are not written.
+  // Rows of x that are not there are not asked for: filling them with zeroes takes the time of loads (17 tokens x
+  // 16384 x 2048 in tiles of 64 rows: 17.8 us with them, 12.5 without).  What the stage holds in their place reaches rows of the result that are not written.
   p.rows_x = m.tokens < 128 ? (m.tokens + 7) / 8 * 8 : 128;
   const int fit = Tiles<kN>::kRing / ((p.rows_x + kN) * kBlockK);
   p.stages = fit < Tiles<kN>::kMaxStages ? fit : Tiles<kN>::kMaxStages;
@@ -647,15 +657,16 @@ cudaError_t launch_many(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul& 
   if (e != cudaSuccess) return e;
   const long bytes = m.out_f32 ? 4 : 2;
   p.whole_out = (reinterpret_cast<uintptr_t>(m.out) & 31u) == 0 && m.out_stride * bytes % 32 == 0 && m.n * bytes % 32 == 0;
+  // Tiles of 64 rows of w, a CTA each, while every one has an SM; a block costs them 0.27 us, the large ones' 0.5 us for four
+  // times the products.  256 tokens x 4096 x 4096 (128 small tiles): 11.5 us, large 18.9; x 10240 (320): 33 : 19.9; 64 x
+  // 16384 x 2048 (256): 14.7 : 11.8.  Few tiles share their k: 64 x 2048 x 6144 (32 tiles) 23 us with one CTA a tile,
+  // 13.7 with two, 9.8 with four, 11 with eight; 128 x 4096 x 4096 (64 tiles) 16.8, 11.2, 13.4 (256 CTAs).
   const long small = ((m.tokens + 127L) / 128) * ((m.n + 63L) / 64);
-  bool use_small = small <= sms;
-  if (getenv("GDN_SM")) use_small = atoi(getenv("GDN_SM"));
-  if (use_small) {
+  if (small <= sms) {
     e = encode_tiles<64>(p, m);
     if (e != cudaSuccess) return e;
     p.split = 1;
     while (p.split < kMaxSplit && 2 * p.split <= p.blocks && 2 * p.split * small <= sms) p.split *= 2;
-    if (getenv("GDN_S")) p.split = atoi(getenv("GDN_S"));
     if (p.split > 1) return launch_tiles<64, true>(env, p, small * p.split);
     return launch_tiles<64, false>(env, p, small);
   }
