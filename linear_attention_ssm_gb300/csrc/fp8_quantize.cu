@@ -41,6 +41,11 @@ __device__ __forceinline__ void load16(const QuantizeParams& p, const uint16_t* 
     for (int i = 0; i < 8; ++i) v[i] = 0;
     return;
   }
+  if (off == 0 && count >= 16) {
+    const uint4 a = ld_once(piece), b = ld_once(piece + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    return;
+  }
   if (reinterpret_cast<const uint16_t*>(piece + pieces) <= p.x_end) {
     const uint4 a = ld_once(piece), b = ld_once(piece + 1), z = make_uint4(0, 0, 0, 0), d = off ? ld_once(piece + 2) : z;
     uint32_t w[13] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, d.x, d.y, d.z, d.w, 0};
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const QuantizeP
 }
 
 // One 128 x 128 block a CTA; its values stay in the registers between their maximum and their codes.
-__global__ void __launch_bounds__(kThreads) quantize_blocks_kernel(const QuantizeParams p) {
+__global__ void __launch_bounds__(kThreads, 5) quantize_blocks_kernel(const QuantizeParams p) {
   __shared__ uint32_t tops[kThreads / 32];
   await_grid();
   const int lane = threadIdx.x % kRowLanes, c = blockIdx.x * kCols + lane * 16;
