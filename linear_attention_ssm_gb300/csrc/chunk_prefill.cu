@@ -820,6 +820,14 @@ cudaError_t encode_bf16_3d_sw128(CUtensorMap* map, const void* base, uint64_t in
   return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+cudaError_t encode_u8_3d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t middle, uint64_t outer,
+                               uint32_t box_inner, uint32_t box_middle, uint32_t box_outer) {
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)middle, (cuuint64_t)outer};
+  const cuuint64_t strides[2] = {(cuuint64_t)inner, (cuuint64_t)inner * middle};
+  const cuuint32_t box[3] = {box_inner, box_middle, box_outer};
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 cudaError_t encode_chunk_tensor_maps(CUtensorMap* qkv_map, CUtensorMap* z_map, const uint16_t* qkv,
                                      const uint16_t* z, int T, int Hk, int Hv) {
   const int C = 2 * Hk * kHeadDim + Hv * kHeadDim;

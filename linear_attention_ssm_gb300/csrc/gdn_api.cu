@@ -1079,7 +1079,9 @@ gdn_status moe_step(const gdn_moe_geometry* geo, const gdn_moe_weights* w, gdn::
       if (outs[i].p && outs[j].p && overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes))
         return fail(GDN_ERR_INVALID_ARGUMENT, "%s overlaps %s", outs[i].name, outs[j].name);
   }
-  const gdn::Moe m = moe_of(geo, w);
+  gdn::Moe m = moe_of(geo, w);
+  if (!e4m3) m.gate_up_scale = m.down_scale = m.shared_gate_up_scale = m.shared_down_scale = nullptr;
+  if (!shared) m.shared_gate = nullptr;
   const size_t need = gdn::moe_workspace_bytes(m, tokens, c.top_k);
   if (!workspace || workspace_bytes < need)
     return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes required (got %zu)", need, workspace ? workspace_bytes : 0);

@@ -99,6 +99,8 @@ cudaError_t encode_u8_2d_sw128(CUtensorMap* map, const void* base, uint64_t inne
 // of a contiguous [outer][middle][inner] tensor:
 cudaError_t encode_bf16_3d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t middle, uint64_t outer,
                                  uint32_t box_inner, uint32_t box_middle, uint32_t box_outer);
+cudaError_t encode_u8_3d_sw128(CUtensorMap* map, const void* base, uint64_t inner, uint64_t middle, uint64_t outer,
+                               uint32_t box_inner, uint32_t box_middle, uint32_t box_outer);
 cudaError_t encode_chunk_tensor_maps(CUtensorMap* qkv_map, CUtensorMap* z_map, const uint16_t* qkv,
                                      const uint16_t* z, int T, int Hk, int Hv);
 cudaError_t launch_chunk_schedule(cudaStream_t stream, const int32_t* cu, int N, int32_t* order, unsigned* counter,

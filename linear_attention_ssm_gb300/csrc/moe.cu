@@ -1,154 +1,775 @@
-// moe.cu -- a mixture-of-experts layer for a few tokens.
+// moe.cu -- a mixture-of-experts layer for a few tokens, in two kernels.
 //
 //   l = x Wr^T,  score = softmax(l) or sigmoid(l),  chosen = the top_k of score + bias
 //   h_e = silu(x G_e^T) * (x U_e^T),  out = sum_e weight_e h_e D_e^T + sigmoid(x . g) shared(x)
-#include <cuda_fp8.h>
-#include <math.h>
+//
+// The first kernel forms the logits and lays the tokens out for the second one, which streams the chosen experts' weights
+// once: HBM bounds it.  Every warp of it takes units of work from one list by an atomic counter -- first 8 rows of a gate
+// matrix with the 8 rows of the up projection beside them, over all of H (h for those 8 places and every token of the
+// expert), then 16 rows of a down projection over all of I -- and copies their weights by TMA into a ring of its own, which
+// runs ahead over the ends of units and from the first kind to the second: the wait for all of h falls into that time.
+// A unit is waited for only when it is a down one, and then every unit of the first kind has been taken by a warp that runs
+// and waits for nothing, so the kernel ends however few of its CTAs run at a time.
+//
+// Products are m16n8k16 of mma.sync: weights fill the 16 rows, an expert's tokens the 8 columns.  Both operands of a lane may
+// come from any places of k as long as they are the same ones; a lane reads 16-byte chunks of its rows, and the tokens lie in
+// memory in that order.  e4m3 weights become binary16 beside the tokens (exact; a token is divided by a power of two that
+// brings its largest value to 2^14 .. 2^15: values down to 2^-32 of the largest are exact, and what others lose is below
+// 2^-40 of it) and bf16 beside h, which has no bound known beforehand: it is held as a bf16 and the bf16 of what that lost,
+// 16 bits together, in two products.
+#include <string.h>
 
+#include "attn_common.cuh"
 #include "gdn_kernels.h"
 
 namespace gdn {
 namespace {
 
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kMaxTokens = 64, kMaxTopK = 16, kMaxExperts = 1024;
+constexpr int kMaxSlots = kMaxTokens * (kMaxTopK + 1);  // (token, expert) pairs
+constexpr int kStageBytes = 2048;                       // 16 rows of 128 bytes
+constexpr int kStages = 12;
+constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before giving up
+constexpr uint32_t kSpinLimit = 1u << 22;  // polls of the counter of finished units
 constexpr int kBlock = 128;
-constexpr int kWarps = 8;
 
 struct Layout {  // of the workspace
-  size_t logits, ids, weights, hidden, bytes;
+  size_t counters, logits, x, x_scale, hidden, shared_hidden, y, bytes;
 };
+__host__ __device__ inline int pad128(int n) { return (n + 127) & ~127; }
 Layout layout(const Moe& m, int T, int k) {
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   Layout l;
-  l.logits = 0;
-  l.ids = l.logits + up((size_t)T * (m.E + 1) * 4);
-  l.weights = l.ids + up((size_t)T * k * 4);
-  l.hidden = l.weights + up((size_t)T * k * 4);
-  l.bytes = l.hidden + up((size_t)T * ((size_t)k * m.I + m.Is) * 4);
+  l.counters = 0;
+  l.logits = l.counters + up((2 + m.H / 16) * 4);
+  l.x = l.logits + up((size_t)T * (m.E + 1) * 4);
+  l.x_scale = l.x + up((size_t)T * pad128(m.H) * 2);
+  l.hidden = l.x_scale + up((size_t)T * 4);
+  l.shared_hidden = l.hidden + up((size_t)T * k * pad128(m.I) * 4);
+  l.y = l.shared_hidden + up((size_t)T * pad128(m.Is) * 4);
+  l.bytes = l.y + up((size_t)T * (k + (m.Is ? 1 : 0)) * m.H * 4);
   return l;
 }
 
-__device__ __forceinline__ float weight_at(const void* w, bool e4m3, size_t at) {
-  if (!e4m3) return bf2f(static_cast<const uint16_t*>(w)[at]);
-  return __half2float(__nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(w)[at], __NV_E4M3));
+struct MoeParams {
+  CUtensorMap gate_up, down, shared_gate_up, shared_down;  // boxes of 128 bytes x 8 rows x 2 halves, or x 16 rows x 1
+  Moe m;
+  MoeCall c;
+  unsigned* counters;  // next unit; first units done; for each 16 rows of the output, down units done
+  float* logits;       // [T][E + 1], the shared gate's behind the experts'
+  uint16_t* x;         // [T][pad128(H)] tokens in the products' order, bf16 or binary16
+  float* x_scale;      // [T] what a binary16 token is multiplied with
+  uint16_t* hidden;    // [T * top_k][2][pad128(I)] in the products' order: bf16, then the rest
+  uint16_t* shared_hidden;
+  float* y;            // [slots][H] weighted rows of the experts
+};
+
+// Where 8 values from k on (a multiple of 8) lie in the products' order.  A 128-byte piece of a row of weights has 8 chunks of
+// 16 bytes, of which lane c of a quad reads 2 c and 2 c + 1; the tokens' values beside them come 16 bytes a lane and load.
+template <bool kE4M3>
+__host__ __device__ __forceinline__ int place(int k) {
+  const int g = (k >> 3) & 15;
+  return (k & ~127) + 8 * (kE4M3 ? (g & 3) * 4 + (g >> 2) : (((g >> 3) * 2 + (g & 1)) * 4 + ((g >> 1) & 3)));
 }
+
+// Loads of what other kernels or CTAs wrote, or read often: where they are written, through L1.
+__device__ __forceinline__ uint4 ld_here(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
-__device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
-// An order of floats as unsigned numbers: NaN is 0, below all others.
+// An order of floats as unsigned numbers above 1: NaN is 1, below all others; 0 stands for none.
 __device__ __forceinline__ uint32_t order_key(float f) {
-  if (f != f) return 0;
+  if (f != f) return 1;
   const uint32_t b = __float_as_uint(f + 0.f);
-  return b >> 31 ? ~b : b | 0x80000000u;
+  return (b >> 31 ? ~b : b | 0x80000000u) + 1;
 }
 
-__global__ void route_kernel(const Moe m, const MoeCall c, float* logits, int32_t* ids, float* weights) {
-  const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float* l = logits + (size_t)t * (m.E + 1);
-  const uint16_t* x = c.x + t * c.x_stride;
-  for (int e = warp; e <= m.E; e += kWarps) {
-    const uint16_t* w = e < m.E ? m.router + (size_t)e * m.H : m.shared_gate;
-    if (e < m.E ? c.ids_in != nullptr : w == nullptr) continue;
-    float s = 0.f;
-    for (int i = lane; i < m.H; i += 32) s = fmaf(bf2f(x[i]), bf2f(w[i]), s);
-    s = warp_sum(s);
-    if (lane == 0) l[e] = s;
+// ---------------------------------------------------------------- tokens and logits
+
+// A CTA for each token's layout, then a warp for the dot products of one expert's row of the router (the shared gate's behind
+// the last) with up to 8 tokens.
+template <bool kE4M3>
+__global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant__ MoeParams p) {
+  __shared__ float tops[kWarps];
+  await_grid();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = p.m.H;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < 2 + H / 16; i += kThreads) p.counters[i] = 0;
+  if (blockIdx.x < p.c.T) {
+    const int t = blockIdx.x;
+    const uint16_t* x = p.c.x + t * p.c.x_stride;
+    uint16_t* to = p.x + (size_t)t * pad128(H);
+    float scale = 1.f;
+    if (kE4M3) {
+      float top = 0.f;  // the largest finite magnitude
+      for (int k = threadIdx.x * 8; k < H; k += kThreads * 8) {
+        const uint4 v = ld_once(x + k);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = fabsf(__uint_as_float(w[i] << 16)), b = fabsf(__uint_as_float(w[i] & 0xFFFF0000u));
+          if (a < INFINITY) top = fmaxf(top, a);
+          if (b < INFINITY) top = fmaxf(top, b);
+        }
+      }
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      if (lane == 0) tops[warp] = top;
+      __syncthreads();
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
+      // the largest value's exponent, raised to where the power of two has a reciprocal
+      const int e = max((int)(__float_as_uint(top) >> 23), 15);
+      scale = __uint_as_float((uint32_t)(e - 14) << 23);
+      const float inverse = __uint_as_float((uint32_t)(254 - (e - 14)) << 23);
+      for (int k = threadIdx.x * 8; k < H; k += kThreads * 8) {
+        const uint4 v = ld_once(x + k);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          h[i] = pack_half2(__uint_as_float(w[i] << 16) * inverse, __uint_as_float(w[i] & 0xFFFF0000u) * inverse);
+        *reinterpret_cast<uint4*>(to + place<kE4M3>(k)) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    } else {
+      for (int k = threadIdx.x * 8; k < H; k += kThreads * 8) *reinterpret_cast<uint4*>(to + place<kE4M3>(k)) = ld_once(x + k);
+    }
+    if (threadIdx.x == 0) p.x_scale[t] = scale;
+    return;
+  }
+  // rows of the router, unless the routing is given, then the shared gate
+  const int groups = (p.c.T + 7) / 8, item = (blockIdx.x - p.c.T) * kWarps + warp;
+  const int e = (p.c.ids_in ? p.m.E : 0) + item / groups, t0 = item % groups * 8;
+  const uint16_t* w = e < p.m.E ? p.m.router + (size_t)e * H : p.m.shared_gate;
+  if (e > p.m.E || !w) return;
+  const int count = min(8, p.c.T - t0);
+  float sum[8] = {};
+#pragma unroll 2
+  for (int k = lane * 8; k < H; k += 256) {
+    const uint4 a = ld_once(w + k);
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= count) break;
+      const uint4 b = ld_here(p.c.x + (t0 + i) * p.c.x_stride + k);
+      const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        sum[i] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), sum[i]);
+        sum[i] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), sum[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (i >= count) break;
+    const float s = warp_sum(sum[i]);
+    if (lane == 0) p.logits[(size_t)(t0 + i) * (p.m.E + 1) + e] = s;
+  }
+}
+
+// ---------------------------------------------------------------- the choice
+
+// What every CTA works out for itself: the tokens' experts and the experts' tokens.
+struct Lists {
+  unsigned long long mask[kMaxExperts];  // tokens of an expert
+  float weight[kMaxSlots];
+  float x_scale[kMaxTokens];
+  float chosen_weight[kMaxTokens * kMaxTopK];
+  uint32_t sums[kWarps];
+  int active;                       // experts that have tokens
+  uint16_t expert[kMaxExperts];     // of an active expert
+  uint16_t first[kMaxExperts + 2];  // its first slot
+  uint16_t index[kMaxExperts];      // the active expert's number
+  uint16_t slot_of[kMaxTokens][kMaxTopK + 1];  // kNone: none; the shared expert's last
+  int16_t chosen[kMaxTokens * kMaxTopK];       // negative: none
+  uint8_t token[kMaxSlots];
+};
+constexpr uint16_t kNone = 0xFFFF;
+
+// One warp: token t's top_k experts and their weights.  `keys`: a word for each expert.
+__device__ __forceinline__ void choose(const MoeParams& p, Lists& s, uint32_t* keys, int t, int lane) {
+  const MoeCall& c = p.c;
+  const int E = p.m.E;
+  const float* l = p.logits + (size_t)t * (E + 1);
+  float top = -INFINITY, sum = 0.f;
+  if (!c.sigmoid && (p.m.router_bias || !c.renormalise)) {
+    for (int e = lane; e < E; e += 32) top = fmaxf(top, ld_f32(l + e));
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    for (int e = lane; e < E; e += 32) sum += expf(ld_f32(l + e) - top);
+    sum = warp_sum(sum);
+  }
+  auto score = [&](float a) { return c.sigmoid ? 1.f / (1.f + expf(-a)) : expf(a - top) / sum; };
+  uint32_t best = 0;  // this lane's largest key and its expert
+  int at = E;
+  for (int e = lane; e < E; e += 32) {
+    const float a = ld_f32(l + e);
+    const uint32_t k = order_key(p.m.router_bias ? score(a) + ld_f32(p.m.router_bias + e) : a);
+    keys[e] = k;
+    if (k > best) best = k, at = e;
+  }
+  float mine = 0.f;  // lane j: the logit of choice j
+  int id = 0;
+  for (int j = 0; j < c.top_k; ++j) {
+    const uint32_t k = __reduce_max_sync(~0u, best);
+    const int e = __reduce_min_sync(~0u, best == k ? at : kMaxExperts);
+    if (lane == j) {
+      id = e;
+      mine = ld_f32(l + e);
+    }
+    if (e == at) {  // the lane that had it looks for its next one
+      keys[e] = 0;
+      best = 0;
+      at = E;
+      for (int i = lane; i < E; i += 32)
+        if (keys[i] > best) best = keys[i], at = i;
+    }
+  }
+  const bool chosen = lane < c.top_k;
+  float w;
+  if (c.renormalise) {
+    // in logarithms, relative to the largest: no score underflows before its sum is formed
+    const float a = !c.sigmoid ? mine : fminf(mine, 0.f) - log1pf(expf(-fabsf(mine)));
+    float high = chosen ? a : -INFINITY;
+    for (int o = 16; o; o >>= 1) high = fmaxf(high, __shfl_xor_sync(~0u, high, o));
+    const float x = chosen ? expf(a - high) : 0.f;
+    w = x / warp_sum(x);
+  } else {
+    w = score(mine);
+  }
+  w *= c.scale;
+  if (chosen) {
+    s.chosen[t * c.top_k + lane] = (int16_t)id;
+    s.chosen_weight[t * c.top_k + lane] = w;
+    if (blockIdx.x == 0) {
+      if (c.ids_out) c.ids_out[t * c.top_k + lane] = id;
+      if (c.weights_out) c.weights_out[t * c.top_k + lane] = w;
+    }
+  }
+}
+
+// The whole CTA; `scratch`: kWarps * E words.
+__device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s, uint32_t* scratch) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.c.T, k = p.c.top_k, E = p.m.E, entries = T * k;
+  for (int e = tid; e < E; e += kThreads) s.mask[e] = 0;
+  if (tid < T) s.x_scale[tid] = ld_f32(p.x_scale + tid);
+  if (p.c.ids_in) {
+    for (int i = tid; i < entries; i += kThreads) {
+      int id;
+      asm volatile("ld.global.b32 %0, [%1];" : "=r"(id) : "l"(p.c.ids_in + i));
+      if (id >= E) {
+        if (blockIdx.x == 0) raise_error(p.c.err, kErrDeviceArgument);
+        id = -1;
+      }
+      s.chosen[i] = (int16_t)max(id, -1);
+      s.chosen_weight[i] = ld_f32(p.c.weights_in + i);
+    }
+  } else {
+    for (int t = warp; t < T; t += kWarps) choose(p, s, scratch + warp * E, t, lane);
   }
   __syncthreads();
-  if (threadIdx.x) return;
-  for (int j = 0; j < c.top_k; ++j) {
-    const size_t at = (size_t)t * c.top_k + j;
-    if (c.ids_in) {
-      const int id = c.ids_in[at];
-      if (id >= m.E) raise_error(c.err, kErrDeviceArgument);
-      ids[at] = id < m.E ? id : -1;
-      weights[at] = c.weights_in[at];
-      continue;
+  for (int i = tid; i < entries; i += kThreads)
+    if (s.chosen[i] >= 0) atomicOr(&s.mask[s.chosen[i]], 1ull << i / k);
+  __syncthreads();
+  // experts that have tokens, in order: each thread has some neighbours; experts above, slots below in a word
+  constexpr int kOwn = kMaxExperts / kThreads;
+  uint32_t own = 0;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int e = tid * kOwn + i, n = e < E ? __popcll(s.mask[e]) : 0;
+    own += n ? 0x10000u + n : 0;
+  }
+  uint32_t before = own;
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(~0u, before, o);
+    if (lane >= o) before += x;
+  }
+  if (lane == 31) s.sums[warp] = before;
+  __syncthreads();
+  uint32_t all = 0;
+  before -= own;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s.sums[w];
+    all += s.sums[w];
+  }
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int e = tid * kOwn + i, n = e < E ? __popcll(s.mask[e]) : 0;
+    if (n) {
+      s.expert[before >> 16] = (uint16_t)e;
+      s.first[before >> 16] = (uint16_t)(before & 0xFFFF);
+      s.index[e] = (uint16_t)(before >> 16);
+      before += 0x10000u + n;
     }
-    uint32_t best = 0;
-    int at_best = -1;
-    float top = -INFINITY, sum = 0.f;
-    for (int e = 0; e < m.E; ++e) top = fmaxf(top, l[e]);
-    for (int e = 0; e < m.E; ++e) sum += expf(l[e] - top);
-    for (int e = 0; e < m.E; ++e) {
-      bool taken = false;
-      for (int i = 0; i < j; ++i) taken |= ids[(size_t)t * c.top_k + i] == e;
-      if (taken) continue;
-      float s = l[e];
-      if (m.router_bias) s = (c.sigmoid ? 1.f / (1.f + expf(-s)) : expf(s - top) / sum) + m.router_bias[e];
-      if (at_best < 0 || order_key(s) > best) best = order_key(s), at_best = e;
+  }
+  const int active = all >> 16, slots = all & 0xFFFF;
+  if (tid == 0) {
+    s.active = active;
+    s.first[active] = (uint16_t)slots;  // the shared expert's slots are behind the others'
+    s.first[active + 1] = (uint16_t)(slots + T);
+  }
+  __syncthreads();
+  for (int i = tid; i < entries; i += kThreads) {
+    const int t = i / k, j = i - t * k, e = s.chosen[i];
+    bool again = e < 0;
+    float w = 0.f;
+    for (int q = 0; q < k; ++q)
+      if (s.chosen[t * k + q] == e) {
+        w += s.chosen_weight[t * k + q];
+        again |= q < j;
+      }
+    int slot = kNone;
+    if (!again) {
+      slot = s.first[s.index[e]] + __popcll(s.mask[e] & ((1ull << t) - 1));
+      s.token[slot] = (uint8_t)t;
+      s.weight[slot] = w;
     }
-    ids[at] = at_best;
-    const float a = l[at_best];
-    if (c.renormalise) weights[at] = c.sigmoid ? fminf(a, 0.f) - log1pf(expf(-fabsf(a))) : a;
-    else weights[at] = c.scale * (c.sigmoid ? 1.f / (1.f + expf(-a)) : expf(a - top) / sum);
+    s.slot_of[t][j] = (uint16_t)slot;
   }
-  float* w = weights + (size_t)t * c.top_k;
-  if (!c.ids_in && c.renormalise) {
-    float top = -INFINITY, sum = 0.f;
-    for (int j = 0; j < c.top_k; ++j) top = fmaxf(top, w[j]);
-    for (int j = 0; j < c.top_k; ++j) sum += w[j] = expf(w[j] - top);
-    for (int j = 0; j < c.top_k; ++j) w[j] = c.scale * (w[j] / sum);
+  if (tid < T) {
+    s.slot_of[tid][kMaxTopK] = p.m.Is ? (uint16_t)(slots + tid) : kNone;
+    if (p.m.Is) {
+      s.token[slots + tid] = (uint8_t)tid;
+      s.weight[slots + tid] =
+          p.m.shared_gate ? 1.f / (1.f + expf(-ld_f32(p.logits + (size_t)tid * (p.m.E + 1) + p.m.E))) : 1.f;
+    }
   }
-  for (int j = 0; j < c.top_k; ++j) {
-    if (c.ids_out) c.ids_out[(size_t)t * c.top_k + j] = ids[(size_t)t * c.top_k + j];
-    if (c.weights_out) c.weights_out[(size_t)t * c.top_k + j] = w[j];
-  }
+  __syncthreads();
 }
 
-// A warp's dot product of row `row` of a [rows, cols] matrix with a vector of bf16 or fp32 values.
-template <typename X>
-__device__ __forceinline__ float dot(const void* w, const float* scale, size_t matrix, int rows, int cols, int row, const X* x,
-                                     int lane) {
-  const size_t base = (matrix * rows + row) * cols;
-  const int rb = (rows + kBlock - 1) / kBlock, cb = (cols + kBlock - 1) / kBlock;
-  float s = 0.f;
-  for (int b = 0; b < cb; ++b) {
-    float d = 0.f;
-    for (int i = b * kBlock + lane; i < min(cols, (b + 1) * kBlock); i += 32) {
-      const float v = sizeof(X) == 2 ? bf2f((uint16_t)x[i]) : (float)x[i];
-      d = fmaf(weight_at(w, scale != nullptr, base + i), v, d);
+// ---------------------------------------------------------------- the experts
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four finite e4m3 codes -> two pairs of bf16, low codes first: the code's exponent and significand at their places of a
+// bf16 stand for its value times 2^-120, subnormals too, and the product with 2^120 is exact.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t v) {
+  auto two = [](uint32_t p) {
+    const uint32_t r = (p >> 4 & 0x07F007F0u) | (p & 0x80008000u);
+    const __nv_bfloat162 up = __nv_bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r), up);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  };
+  return make_uint2(two(__byte_perm(v, 0, 0x1404)), two(__byte_perm(v, 0, 0x3424)));
+}
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t done;
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    if (__all_sync(~0u, done)) return true;
+  }
+  return false;
+}
+// a stage's load, by one lane of the warp
+__device__ __forceinline__ void warp_load(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\n"
+      "elect.sync _|e, 0xFFFFFFFF;\n"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%4, %5, %6}], [%0];\n"
+      "}" ::"r"(bar),
+      "r"(kStageBytes), "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// A unit of work.
+struct Unit {
+  int kind;    // 0: 8 rows of gate and up, 1: 16 rows of down
+  int a;       // the active expert, `active` for the shared one
+  bool shared;
+  int row, k;  // first row; length of a row
+};
+
+template <bool kE4M3>
+struct Worker {
+  static constexpr int kPiece = kE4M3 ? 128 : 64;  // values of a 128-byte piece of a row
+  const MoeParams& p;
+  Lists& s;
+  const int lane;
+  const uint32_t ring, bars;  // this warp's stages and barriers
+  int* queue;                 // units on their way
+  int units_a, units;         // of the first kind, of both
+  int hidden_units, out_units, shared_rows;  // units of an expert of either kind; of the shared one's first kind
+  // loading
+  unsigned ticket;
+  int loaded, left, x, y, z, pushed;
+  const void* map;
+  bool more;
+  // working
+  int worked;
+  bool hidden_done, ok;
+
+  __device__ __forceinline__ Unit unit_of(int u) const {
+    Unit n;
+    n.kind = u >= units_a;
+    const int v = n.kind ? u - units_a : u, each = n.kind ? out_units : hidden_units;
+    n.a = min((unsigned)v / (unsigned)each, (unsigned)s.active);
+    n.shared = n.a == s.active;
+    n.row = (v - n.a * each) * (n.kind ? 16 : 8);
+    n.k = !n.kind ? p.m.H : n.shared ? p.m.Is : p.m.I;
+    return n;
+  }
+  __device__ __forceinline__ void take() {  // the next unit's number, known a unit later
+    if (lane == 0) ticket = atomicAdd(p.counters, 1u);
+  }
+  // loads one stage, if there is something to load
+  __device__ __forceinline__ void push() {
+    if (left == 0) {
+      if (!more) return;
+      const unsigned u = __shfl_sync(~0u, ticket, 0);
+      if (u >= (unsigned)units) {
+        more = false;
+        return;
+      }
+      take();
+      if (lane == 0) queue[pushed & 15] = (int)u;
+      ++pushed;
+      const Unit n = unit_of((int)u);
+      const int e = n.shared ? 0 : s.expert[n.a];
+      map = n.kind ? (n.shared ? &p.shared_down : &p.down) : (n.shared ? &p.shared_gate_up : &p.gate_up);
+      x = 0;
+      y = n.row;
+      z = n.kind ? e : 2 * e;
+      left = (n.k + kPiece - 1) / kPiece;
+      if (kE4M3) {  // its scales, towards L2
+        const int blocks = (n.k + kBlock - 1) / kBlock;
+        const float *g, *u2;
+        scales_of(n, g, u2);
+        if (lane * 8 < blocks) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(g + lane * 8));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(u2 + lane * 8));
+        }
+      }
     }
-    s = fmaf(d, scale ? scale[(matrix * rb + row / kBlock) * cb + b] : 1.f, s);
+    const int i = loaded % kStages;
+    warp_load(ring + i * kStageBytes, map, x, y, z, bars + 8 * i);
+    ++loaded;
+    x += kPiece;
+    --left;
   }
-  return warp_sum(s);
+  // the scales of a unit's rows by blocks of k: its upper and lower 8
+  __device__ __forceinline__ void scales_of(const Unit& n, const float*& upper, const float*& lower) const {
+    const int kb = (n.k + kBlock - 1) / kBlock;
+    if (n.kind) {
+      const int rb = (p.m.H + kBlock - 1) / kBlock;
+      const float* base = n.shared ? p.m.shared_down_scale : p.m.down_scale + (size_t)s.expert[n.a] * rb * kb;
+      upper = lower = base + (size_t)(n.row / kBlock) * kb;
+    } else {
+      const int rb = ((n.shared ? p.m.Is : p.m.I) + kBlock - 1) / kBlock;
+      const float* base = n.shared ? p.m.shared_gate_up_scale : p.m.gate_up_scale + (size_t)s.expert[n.a] * 2 * rb * kb;
+      upper = base + (size_t)(n.row / kBlock) * kb;
+      lower = upper + (size_t)rb * kb;
+    }
+  }
+
+  // One unit for up to 8 kTiles tokens of its expert from rank t0 on; the last pass over the unit's stages frees them.
+  template <int kKind, int kTiles>
+  __device__ __forceinline__ void work(const Unit& n) {
+    const int r = lane >> 2, c = lane & 3, first = s.first[n.a], count = s.first[n.a + 1] - first;
+    const int width = pad128(n.k);
+    // where this lane's token of each tile has its values (behind the last token: none)
+    const uint16_t* src[kTiles];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) {
+      const int rank = 8 * i + r;
+      src[i] = rank >= count ? nullptr
+               : kKind == 0  ? p.x + (size_t)s.token[first + rank] * width
+               : n.shared    ? p.shared_hidden + (size_t)rank * 2 * width
+                             : p.hidden + (size_t)(first + rank) * 2 * width;
+    }
+    float acc[kTiles][4], part[kTiles][4];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = part[i][j] = 0.f;
+    const float *upper = nullptr, *lower = nullptr;
+    float su = 1.f, sl = 1.f;  // lane i: block i's scales, of 32
+    if (kE4M3) scales_of(n, upper, lower);
+    constexpr int kLoads = kE4M3 ? 4 : 2;            // of a lane from a token for a piece
+    constexpr int kParts = kKind == 0 ? 1 : 2;       // h is held in two
+    const int pieces = (n.k + kPiece - 1) / kPiece;
+    auto value = [&](int i, int piece, int load, int half) {
+      const int k = piece * kPiece + c * (kPiece / 4) + load * 8;  // of the first of eight
+      const int at = kE4M3 ? piece * 128 + (load * 4 + c) * 8 : (piece >> 1) * 128 + (((piece & 1) * 2 + load) * 4 + c) * 8;
+      return src[i] && k < n.k ? ld_here(src[i] + half * width + at) : make_uint4(0, 0, 0, 0);
+    };
+    constexpr bool kAhead = kTiles == 1;  // a piece ahead
+    uint4 b[kParts][kLoads];
+    if (kAhead)
+#pragma unroll
+      for (int h = 0; h < kParts; ++h)
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) b[h][q] = value(0, 0, q, h);
+#pragma unroll 1
+    for (int piece = 0; piece < pieces; ++piece) {
+      if (kE4M3 && (piece & 31) == 0) {
+        const int at = piece + lane;
+        su = at < pieces ? ld_f32(upper + at) : 0.f;
+        sl = at < pieces ? ld_f32(lower + at) : 0.f;
+      }
+      const int st = worked % kStages;
+      if (ok && !warp_wait(bars + 8 * st, worked / kStages & 1)) {
+        raise_error(p.c.err, kErrTimeout);
+        ok = false;
+      }
+      if (!ok) return;
+      // rows r and r + 8, chunks 2 c and 2 c + 1 of the swizzled piece
+      uint4 w[2][2];
+      const uint32_t at = ring + st * kStageBytes + r * 128;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[j][h] = lds128(at + h * 1024 + (((2 * c + j) ^ r) << 4));
+      ++worked;
+      __syncwarp();
+      push();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t u[4] = {w[j][0].x, w[j][0].y, w[j][0].z, w[j][0].w}, l[4] = {w[j][1].x, w[j][1].y, w[j][1].z, w[j][1].w};
+        constexpr int kSteps = kE4M3 ? 4 : 2;  // products of a chunk
+        uint2 fu[kSteps], fl[kSteps];
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q) {
+          if constexpr (!kE4M3) {
+            fu[q] = make_uint2(u[2 * q], u[2 * q + 1]);
+            fl[q] = make_uint2(l[2 * q], l[2 * q + 1]);
+          } else if constexpr (kKind == 0) {
+            fu[q] = e4m3x4_to_half4(u[q]);
+            fl[q] = e4m3x4_to_half4(l[q]);
+          } else {
+            fu[q] = e4m3x4_to_bf16x4(u[q]);
+            fl[q] = e4m3x4_to_bf16x4(l[q]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int h = 0; h < kParts; ++h)
+#pragma unroll
+            for (int g = 0; g < kLoads / 2; ++g) {
+              const uint4 v = kAhead ? b[h][j * (kLoads / 2) + g] : value(i, piece, j * (kLoads / 2) + g, h);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                const uint2 &a0 = fu[2 * g + q], &a1 = fl[2 * g + q];
+                const uint32_t b0 = q ? v.z : v.x, b1 = q ? v.w : v.y;
+                if (kE4M3 && kKind == 0) mma_f16(part[i], a0.x, a1.x, a0.y, a1.y, b0, b1);
+                else mma_bf16_16816(part[i], a0.x, a1.x, a0.y, a1.y, b0, b1);
+              }
+            }
+      }
+      if (kAhead && piece + 1 < pieces)
+#pragma unroll
+        for (int h = 0; h < kParts; ++h)
+#pragma unroll
+          for (int q = 0; q < kLoads; ++q) b[h][q] = value(0, piece + 1, q, h);
+      if (kE4M3 || (piece & 1) || piece + 1 == pieces) {  // a block of 128 is summed by itself, then scaled
+        const float fu = kE4M3 ? __shfl_sync(~0u, su, piece & 31) : 1.f, fl = kE4M3 ? __shfl_sync(~0u, sl, piece & 31) : 1.f;
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[i][j] = fmaf(part[i][j], j < 2 ? fu : fl, acc[i][j]);
+            part[i][j] = 0.f;
+          }
+      }
+    }
+    if constexpr (kKind == 0) {  // silu(gate) * up for places row + r, tokens 8 i + 2 c and the next
+      uint16_t* hidden = n.shared ? p.shared_hidden : p.hidden;
+      const int base = n.shared ? 0 : first, wide = pad128(n.shared ? p.m.Is : p.m.I), at = place<kE4M3>(n.row) + r;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int rank = 8 * i + 2 * c + j;
+          if (rank >= count) continue;
+          const float xs = kE4M3 ? s.x_scale[s.token[first + rank]] : 1.f, g = acc[i][j] * xs, u = acc[i][2 + j] * xs;
+          const float h = g / (1.f + expf(-g)) * u;
+          const uint16_t hi = f2bf(h);
+          uint16_t* to = hidden + (size_t)(base + rank) * 2 * wide + at;
+          to[0] = hi;
+          // what the first part lost; nothing where it is not finite
+          to[wide] = (hi & 0x7F80u) == 0x7F80u ? 0 : f2bf(h - bf2f(hi));
+        }
+      __syncwarp();
+      if (lane == 0) {
+        __threadfence();
+        atomicAdd(p.counters + 1, 1u);
+      }
+    } else {  // rows row + r and row + 8 + r
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int rank = 8 * i + 2 * c + (j & 1);
+          if (rank < count)
+            p.y[(size_t)(first + rank) * p.m.H + n.row + (j >> 1) * 8 + r] = acc[i][j] * s.weight[first + rank];
+        }
+      __syncwarp();
+      unsigned before = 0;
+      if (lane == 0) {
+        __threadfence();
+        before = atomicAdd(p.counters + 2 + n.row / 16, 1u);
+        __threadfence();
+      }
+      if (__shfl_sync(~0u, before, 0) + 1 == (unsigned)(s.active + (p.m.Is ? 1 : 0))) join(n.row);
+    }
+  }
+
+  // 16 columns of the output, from the experts' rows in the order of the choice: the last of their units does it
+  __device__ __forceinline__ void join(int row) {
+    const int col = row + (lane & 3) * 4;
+    for (int t = lane >> 2; t < p.c.T; t += 8) {
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int j = 0; j <= p.c.top_k; ++j) {
+        const int slot = s.slot_of[t][j == p.c.top_k ? kMaxTopK : j];
+        if (slot == kNone) continue;
+        const float4 v = ld_l2(reinterpret_cast<const float4*>(p.y + (size_t)slot * p.m.H + col));
+        y.x += v.x;
+        y.y += v.y;
+        y.z += v.z;
+        y.w += v.w;
+      }
+      *reinterpret_cast<uint2*>(p.c.out + (size_t)t * p.m.H + col) = make_uint2(pack_bf2(y.x, y.y), pack_bf2(y.z, y.w));
+    }
+  }
+
+  template <int kKind>
+  __device__ __forceinline__ void work_any(const Unit& n) {
+    const int tiles = (s.first[n.a + 1] - s.first[n.a] + 7) / 8;
+    if (tiles == 1) work<kKind, 1>(n);
+    else if (tiles == 2) work<kKind, 2>(n);
+    else if (tiles <= 4) work<kKind, 4>(n);
+    else work<kKind, 8>(n);
+  }
+
+  __device__ __forceinline__ void run() {
+    for (int i = 0; i < kStages; ++i) push();
+    for (int taken = 0; ok && taken != pushed; ++taken) {
+      __syncwarp();
+      const Unit n = unit_of(queue[taken & 15]);
+      __syncwarp();
+      if (n.kind && !hidden_done) {  // every unit of the first kind is in the hands of a warp that waits for nothing
+        for (uint32_t i = 0; ok; ++i) {
+          const unsigned done = (unsigned)ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1));
+          if (__all_sync(~0u, done >= (unsigned)units_a)) break;
+          if (i == kSpinLimit) {
+            raise_error(p.c.err, kErrTimeout);
+            ok = false;
+          }
+          __nanosleep(32);
+        }
+        hidden_done = true;
+      }
+      if (!ok) break;
+      if (n.kind) work_any<1>(n);
+      else work_any<0>(n);
+    }
+    // copies in flight land before the CTA ends, after a wait that ran out too
+    for (; worked < loaded; ++worked) warp_wait(bars + 8 * (worked % kStages), worked / kStages & 1);
+  }
+};
+
+constexpr size_t kSmem = 1024 + (size_t)kWarps * kStages * kStageBytes + sizeof(Lists) + kWarps * (16 * 4 + kStages * 8) + 64;
+
+template <bool kE4M3>
+__global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ MoeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  constexpr int kRing = kStages * kStageBytes;
+  Lists& s = *reinterpret_cast<Lists*>(smem + kWarps * kRing);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uintptr_t>(smem + kWarps * kRing + sizeof(Lists) + 15) & ~(uintptr_t)15);
+  int* queues = reinterpret_cast<int*>(bars + kWarps * kStages);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x < kWarps * kStages) mbar_init(smem_u32(bars + threadIdx.x), 1);
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&p.gate_up);
+    prefetch_tensormap(&p.down);
+  }
+  fence_mbar_init();
+  await_grid();
+  Worker<kE4M3> w = {p, s, lane, smem_u32(smem + warp * kRing), smem_u32(bars + warp * kStages), queues + warp * 16};
+  w.take();
+  make_lists(p, s, reinterpret_cast<uint32_t*>(smem));
+  // the lists' scratch was written by ordinary stores, the ring is by copies
+  fence_proxy_async_smem();
+  __syncthreads();
+  w.hidden_units = p.m.I / 8;
+  w.out_units = p.m.H / 16;
+  w.units_a = s.active * w.hidden_units + p.m.Is / 8;
+  w.units = w.units_a + (s.active + (p.m.Is ? 1 : 0)) * w.out_units;
+  w.loaded = w.left = w.x = w.y = w.z = w.pushed = w.worked = 0;
+  w.map = nullptr;
+  w.more = w.ok = true;
+  w.hidden_done = false;
+  if (w.units == 0) {  // no token has an expert
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.c.T * p.m.H / 8; i += gridDim.x * kThreads)
+      reinterpret_cast<uint4*>(p.c.out)[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  w.run();
 }
 
-__global__ void hidden_kernel(const Moe m, const MoeCall c, const int32_t* ids, float* hidden) {
-  const int slot = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int routed = c.T * c.top_k;
-  const bool shared = slot >= routed;
-  const int t = shared ? slot - routed : slot / c.top_k, I = shared ? m.Is : m.I;
-  const int i = blockIdx.x * kWarps + warp, e = shared ? 0 : ids[slot];
-  if (i >= I || e < 0) return;
-  const void* w = shared ? m.shared_gate_up : m.gate_up;
-  const float* sc = shared ? m.shared_gate_up_scale : m.gate_up_scale;
-  const uint16_t* x = c.x + t * c.x_stride;
-  const float g = dot(w, sc, 2 * (size_t)e, I, m.H, i, x, lane), u = dot(w, sc, 2 * (size_t)e + 1, I, m.H, i, x, lane);
-  float* h = shared ? hidden + (size_t)routed * m.I + (size_t)t * m.Is : hidden + (size_t)slot * m.I;
-  if (lane == 0) h[i] = silu(g) * u;
+template <bool kE4M3>
+cudaError_t encode(CUtensorMap* map, const void* base, int k, int rows, int matrices, bool halves) {
+  if (!base || !rows || !k) return cudaSuccess;
+  return kE4M3 ? encode_u8_3d_sw128(map, base, k, rows, matrices, 128, halves ? 8 : 16, halves ? 2 : 1)
+               : encode_bf16_3d_sw128(map, base, k, rows, matrices, 64, halves ? 8 : 16, halves ? 2 : 1);
 }
 
-__global__ void out_kernel(const Moe m, const MoeCall c, const float* logits, const int32_t* ids, const float* weights,
-                           const float* hidden) {
-  const int t = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * kWarps + warp;
-  if (row >= m.H) return;
-  float y = 0.f;
-  for (int j = 0; j < c.top_k; ++j) {
-    const size_t slot = (size_t)t * c.top_k + j;
-    const int e = ids[slot];
-    if (e < 0) continue;
-    y = fmaf(weights[slot], dot(m.down, m.down_scale, e, m.H, m.I, row, hidden + slot * m.I, lane), y);
+template <bool kE4M3>
+cudaError_t launch(const LaunchEnv& env, MoeParams& p) {
+  static int done[64] = {0};
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = device_sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(experts_kernel<kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = 1;
   }
-  if (m.Is) {
-    const float* h = hidden + (size_t)c.T * c.top_k * m.I + (size_t)t * m.Is;
-    const float g = m.shared_gate ? 1.f / (1.f + expf(-logits[(size_t)t * (m.E + 1) + m.E])) : 1.f;
-    y = fmaf(g, dot(m.shared_down, m.shared_down_scale, 0, m.H, m.Is, row, h, lane), y);
-  }
-  if (lane == 0) c.out[(size_t)t * m.H + row] = f2bf(y);
+  const Moe& m = p.m;
+  e = encode<kE4M3>(&p.gate_up, m.gate_up, m.H, m.I, 2 * m.E, true);
+  if (e == cudaSuccess) e = encode<kE4M3>(&p.down, m.down, m.I, m.H, m.E, false);
+  if (e == cudaSuccess) e = encode<kE4M3>(&p.shared_gate_up, m.Is ? m.shared_gate_up : nullptr, m.H, m.Is, 2, true);
+  if (e == cudaSuccess) e = encode<kE4M3>(&p.shared_down, m.Is ? m.shared_down : nullptr, m.Is, m.H, 1, false);
+  if (e != cudaSuccess) return e;
+  const int dots = ((p.c.ids_in ? 0 : m.E) + (m.shared_gate ? 1 : 0)) * ((p.c.T + 7) / 8);
+  e = launch_early(prepare_kernel<kE4M3>, dim3(p.c.T + (dots + kWarps - 1) / kWarps), kThreads, 0, env.stream, p);
+  if (e != cudaSuccess) return e;
+  return launch_early(experts_kernel<kE4M3>, dim3(sms), kThreads, kSmem, env.stream, p);
 }
 
 }  // namespace
@@ -156,18 +777,21 @@ __global__ void out_kernel(const Moe m, const MoeCall c, const float* logits, co
 size_t moe_workspace_bytes(const Moe& m, int T, int top_k) { return layout(m, T, top_k).bytes; }
 
 cudaError_t launch_moe(const LaunchEnv& env, const Moe& m, MoeCall c, void* workspace) {
+  MoeParams p;
+  memset(&p, 0, sizeof p);
   c.err = env.err;
+  p.m = m;
+  p.c = c;
   const Layout l = layout(m, c.T, c.top_k);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  float* logits = reinterpret_cast<float*>(ws + l.logits);
-  int32_t* ids = reinterpret_cast<int32_t*>(ws + l.ids);
-  float* weights = reinterpret_cast<float*>(ws + l.weights);
-  float* hidden = reinterpret_cast<float*>(ws + l.hidden);
-  route_kernel<<<c.T, kWarps * 32, 0, env.stream>>>(m, c, logits, ids, weights);
-  const int widest = m.I > m.Is ? m.I : m.Is, slots = c.T * c.top_k + (m.Is ? c.T : 0);
-  hidden_kernel<<<dim3((widest + kWarps - 1) / kWarps, slots), kWarps * 32, 0, env.stream>>>(m, c, ids, hidden);
-  out_kernel<<<dim3((m.H + kWarps - 1) / kWarps, c.T), kWarps * 32, 0, env.stream>>>(m, c, logits, ids, weights, hidden);
-  return cudaGetLastError();
+  p.counters = reinterpret_cast<unsigned*>(ws + l.counters);
+  p.logits = reinterpret_cast<float*>(ws + l.logits);
+  p.x = reinterpret_cast<uint16_t*>(ws + l.x);
+  p.x_scale = reinterpret_cast<float*>(ws + l.x_scale);
+  p.hidden = reinterpret_cast<uint16_t*>(ws + l.hidden);
+  p.shared_hidden = reinterpret_cast<uint16_t*>(ws + l.shared_hidden);
+  p.y = reinterpret_cast<float*>(ws + l.y);
+  return m.gate_up_scale ? launch<true>(env, p) : launch<false>(env, p);
 }
 
 }  // namespace gdn
