@@ -160,19 +160,26 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant
   if (e > p.m.E || !w) return;
   const int count = min(8, p.c.T - t0);
   float sum[8] = {};
-#pragma unroll 2
-  for (int k = lane * 8; k < H; k += 256) {
-    const uint4 a = ld_once(w + k);
-    const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
+  constexpr int kAhead = 4;  // pieces of a row in flight
+  for (int k0 = lane * 8; k0 < H; k0 += 256 * kAhead) {
+    uint4 a[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) a[j] = k0 + 256 * j < H ? ld_once(w + k0 + 256 * j) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i >= count) break;
-      const uint4 b = ld_here(p.c.x + (t0 + i) * p.c.x_stride + k);
-      const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+      uint4 b[kAhead];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        sum[i] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), sum[i]);
-        sum[i] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), sum[i]);
+      for (int j = 0; j < kAhead; ++j)
+        b[j] = k0 + 256 * j < H ? ld_here(p.c.x + (t0 + i) * p.c.x_stride + k0 + 256 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const uint32_t aw[4] = {a[j].x, a[j].y, a[j].z, a[j].w}, bw[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          sum[i] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), sum[i]);
+          sum[i] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), sum[i]);
+        }
       }
     }
   }
@@ -191,72 +198,76 @@ struct Lists {
   unsigned long long mask[kMaxExperts];  // tokens of an expert
   float weight[kMaxSlots];
   float x_scale[kMaxTokens];
-  float chosen_weight[kMaxTokens * kMaxTopK];
+  float chosen_weight[kMaxTokens][kMaxTopK];
   uint32_t sums[kWarps];
   int active;                       // experts that have tokens
   uint16_t expert[kMaxExperts];     // of an active expert
   uint16_t first[kMaxExperts + 2];  // its first slot
   uint16_t index[kMaxExperts];      // the active expert's number
   uint16_t slot_of[kMaxTokens][kMaxTopK + 1];  // kNone: none; the shared expert's last
-  int16_t chosen[kMaxTokens * kMaxTopK];       // negative: none
+  int16_t chosen[kMaxTokens][kMaxTopK];        // negative: none
   uint8_t token[kMaxSlots];
 };
 constexpr uint16_t kNone = 0xFFFF;
 
-// One warp: token t's top_k experts and their weights.  `keys`: a word for each expert.
-__device__ __forceinline__ void choose(const MoeParams& p, Lists& s, uint32_t* keys, int t, int lane) {
+// One warp: token t's top_k experts and their weights.  A lane holds the keys of every 32nd expert.
+template <int kOwn>
+__device__ __forceinline__ void choose(const MoeParams& p, Lists& s, int t, int lane) {
   const MoeCall& c = p.c;
   const int E = p.m.E;
   const float* l = p.logits + (size_t)t * (E + 1);
-  float top = -INFINITY, sum = 0.f;
+  float a[kOwn], top = -INFINITY, sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) a[i] = lane + 32 * i < E ? ld_f32(l + lane + 32 * i) : -INFINITY;
   if (!c.sigmoid && (p.m.router_bias || !c.renormalise)) {
-    for (int e = lane; e < E; e += 32) top = fmaxf(top, ld_f32(l + e));
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) top = fmaxf(top, a[i]);
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    for (int e = lane; e < E; e += 32) sum += expf(ld_f32(l + e) - top);
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) sum += lane + 32 * i < E ? expf(a[i] - top) : 0.f;
     sum = warp_sum(sum);
   }
-  auto score = [&](float a) { return c.sigmoid ? 1.f / (1.f + expf(-a)) : expf(a - top) / sum; };
-  uint32_t best = 0;  // this lane's largest key and its expert
-  int at = E;
-  for (int e = lane; e < E; e += 32) {
-    const float a = ld_f32(l + e);
-    const uint32_t k = order_key(p.m.router_bias ? score(a) + ld_f32(p.m.router_bias + e) : a);
-    keys[e] = k;
-    if (k > best) best = k, at = e;
+  auto score = [&](float v) { return c.sigmoid ? 1.f / (1.f + expf(-v)) : expf(v - top) / sum; };
+  uint32_t key[kOwn];  // 0: taken, or none
+  if (p.m.router_bias) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      key[i] = lane + 32 * i < E ? order_key(score(a[i]) + ld_f32(p.m.router_bias + lane + 32 * i)) : 0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) key[i] = lane + 32 * i < E ? order_key(a[i]) : 0;
   }
-  float mine = 0.f;  // lane j: the logit of choice j
-  int id = 0;
+  int id = 0;  // lane j: choice j
   for (int j = 0; j < c.top_k; ++j) {
+    uint32_t best = 0;
+    int at = kMaxExperts;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (key[i] > best) best = key[i], at = lane + 32 * i;
     const uint32_t k = __reduce_max_sync(~0u, best);
     const int e = __reduce_min_sync(~0u, best == k ? at : kMaxExperts);
-    if (lane == j) {
-      id = e;
-      mine = ld_f32(l + e);
-    }
-    if (e == at) {  // the lane that had it looks for its next one
-      keys[e] = 0;
-      best = 0;
-      at = E;
-      for (int i = lane; i < E; i += 32)
-        if (keys[i] > best) best = keys[i], at = i;
-    }
+    if (lane == j) id = e;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (e == lane + 32 * i) key[i] = 0;
   }
   const bool chosen = lane < c.top_k;
+  const float mine = chosen ? ld_f32(l + id) : 0.f;
   float w;
   if (c.renormalise) {
     // in logarithms, relative to the largest: no score underflows before its sum is formed
-    const float a = !c.sigmoid ? mine : fminf(mine, 0.f) - log1pf(expf(-fabsf(mine)));
-    float high = chosen ? a : -INFINITY;
+    const float v = !c.sigmoid ? mine : fminf(mine, 0.f) - log1pf(expf(-fabsf(mine)));
+    float high = chosen ? v : -INFINITY;
     for (int o = 16; o; o >>= 1) high = fmaxf(high, __shfl_xor_sync(~0u, high, o));
-    const float x = chosen ? expf(a - high) : 0.f;
+    const float x = chosen ? expf(v - high) : 0.f;
     w = x / warp_sum(x);
   } else {
     w = score(mine);
   }
   w *= c.scale;
   if (chosen) {
-    s.chosen[t * c.top_k + lane] = (int16_t)id;
-    s.chosen_weight[t * c.top_k + lane] = w;
+    s.chosen[t][lane] = (int16_t)id;
+    s.chosen_weight[t][lane] = w;
     if (blockIdx.x == 0) {
       if (c.ids_out) c.ids_out[t * c.top_k + lane] = id;
       if (c.weights_out) c.weights_out[t * c.top_k + lane] = w;
@@ -264,28 +275,35 @@ __device__ __forceinline__ void choose(const MoeParams& p, Lists& s, uint32_t* k
   }
 }
 
-// The whole CTA; `scratch`: kWarps * E words.
-__device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s, uint32_t* scratch) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.c.T, k = p.c.top_k, E = p.m.E, entries = T * k;
+// The whole CTA.
+__device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.c.T, k = p.c.top_k, E = p.m.E;
+  constexpr int kPass = kThreads / kMaxTopK;  // tokens at a time, a thread for each of their choices
+  const int j = tid % kMaxTopK, t0 = tid / kMaxTopK;
   for (int e = tid; e < E; e += kThreads) s.mask[e] = 0;
   if (tid < T) s.x_scale[tid] = ld_f32(p.x_scale + tid);
   if (p.c.ids_in) {
-    for (int i = tid; i < entries; i += kThreads) {
+    for (int t = t0; t < T && j < k; t += kPass) {
       int id;
-      asm volatile("ld.global.b32 %0, [%1];" : "=r"(id) : "l"(p.c.ids_in + i));
+      asm volatile("ld.global.b32 %0, [%1];" : "=r"(id) : "l"(p.c.ids_in + t * k + j));
       if (id >= E) {
         if (blockIdx.x == 0) raise_error(p.c.err, kErrDeviceArgument);
         id = -1;
       }
-      s.chosen[i] = (int16_t)max(id, -1);
-      s.chosen_weight[i] = ld_f32(p.c.weights_in + i);
+      s.chosen[t][j] = (int16_t)max(id, -1);
+      s.chosen_weight[t][j] = ld_f32(p.c.weights_in + t * k + j);
     }
   } else {
-    for (int t = warp; t < T; t += kWarps) choose(p, s, scratch + warp * E, t, lane);
+    for (int t = warp; t < T; t += kWarps) {
+      if (E <= 64) choose<2>(p, s, t, lane);
+      else if (E <= 128) choose<4>(p, s, t, lane);
+      else if (E <= 320) choose<10>(p, s, t, lane);
+      else choose<32>(p, s, t, lane);
+    }
   }
   __syncthreads();
-  for (int i = tid; i < entries; i += kThreads)
-    if (s.chosen[i] >= 0) atomicOr(&s.mask[s.chosen[i]], 1ull << i / k);
+  for (int t = t0; t < T && j < k; t += kPass)
+    if (s.chosen[t][j] >= 0) atomicOr(&s.mask[s.chosen[t][j]], 1ull << t);
   __syncthreads();
   // experts that have tokens, in order: each thread has some neighbours; experts above, slots below in a word
   constexpr int kOwn = kMaxExperts / kThreads;
@@ -304,6 +322,7 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s, uint32_
   __syncthreads();
   uint32_t all = 0;
   before -= own;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s.sums[w];
     all += s.sums[w];
@@ -325,13 +344,13 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s, uint32_
     s.first[active + 1] = (uint16_t)(slots + T);
   }
   __syncthreads();
-  for (int i = tid; i < entries; i += kThreads) {
-    const int t = i / k, j = i - t * k, e = s.chosen[i];
+  for (int t = t0; t < T && j < k; t += kPass) {
+    const int e = s.chosen[t][j];
     bool again = e < 0;
     float w = 0.f;
     for (int q = 0; q < k; ++q)
-      if (s.chosen[t * k + q] == e) {
-        w += s.chosen_weight[t * k + q];
+      if (s.chosen[t][q] == e) {
+        w += s.chosen_weight[t][q];
         again |= q < j;
       }
     int slot = kNone;
@@ -423,11 +442,12 @@ struct Worker {
   int hidden_units, out_units, shared_rows;  // units of an expert of either kind; of the shared one's first kind
   // loading
   unsigned ticket;
-  int loaded, left, x, y, z, pushed;
+  int loaded, left, x, y, z, pushed, load_stage;
   const void* map;
   bool more;
   // working
-  int worked;
+  int worked, stage, pass;  // stages worked on; the next one and its phase
+  int owed;                 // what the last unit has still to tell: 0 nothing, 1 that its h is written, 2 + row of its output
   bool hidden_done, ok;
 
   __device__ __forceinline__ Unit unit_of(int u) const {
@@ -472,8 +492,8 @@ struct Worker {
         }
       }
     }
-    const int i = loaded % kStages;
-    warp_load(ring + i * kStageBytes, map, x, y, z, bars + 8 * i);
+    warp_load(ring + load_stage * kStageBytes, map, x, y, z, bars + 8 * load_stage);
+    if (++load_stage == kStages) load_stage = 0;
     ++loaded;
     x += kPiece;
     --left;
@@ -508,11 +528,16 @@ struct Worker {
                : n.shared    ? p.shared_hidden + (size_t)rank * 2 * width
                              : p.hidden + (size_t)(first + rank) * 2 * width;
     }
-    float acc[kTiles][4], part[kTiles][4];
+    constexpr int kChains = kTiles == 1 ? 4 : kTiles == 2 ? 2 : 1;  // sums that do not wait for one another
+    float acc[kTiles][4], part[kChains][kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = part[i][j] = 0.f;
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = 0.f;
+#pragma unroll
+        for (int h = 0; h < kChains; ++h) part[h][i][j] = 0.f;
+      }
     const float *upper = nullptr, *lower = nullptr;
     float su = 1.f, sl = 1.f;  // lane i: block i's scales, of 32
     if (kE4M3) scales_of(n, upper, lower);
@@ -524,13 +549,15 @@ struct Worker {
       const int at = kE4M3 ? piece * 128 + (load * 4 + c) * 8 : (piece >> 1) * 128 + (((piece & 1) * 2 + load) * 4 + c) * 8;
       return src[i] && k < n.k ? ld_here(src[i] + half * width + at) : make_uint4(0, 0, 0, 0);
     };
-    constexpr bool kAhead = kTiles == 1;  // a piece ahead
-    uint4 b[kParts][kLoads];
+    constexpr bool kAhead = kTiles == 1;  // one tile's values are loaded two pieces ahead
+    uint4 b[2][kParts][kLoads];
     if (kAhead)
 #pragma unroll
-      for (int h = 0; h < kParts; ++h)
+      for (int d = 0; d < 2; ++d)
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) b[h][q] = value(0, 0, q, h);
+        for (int h = 0; h < kParts; ++h)
+#pragma unroll
+          for (int q = 0; q < kLoads; ++q) b[d][h][q] = value(0, d, q, h);
 #pragma unroll 1
     for (int piece = 0; piece < pieces; ++piece) {
       if (kE4M3 && (piece & 31) == 0) {
@@ -538,8 +565,8 @@ struct Worker {
         su = at < pieces ? ld_f32(upper + at) : 0.f;
         sl = at < pieces ? ld_f32(lower + at) : 0.f;
       }
-      const int st = worked % kStages;
-      if (ok && !warp_wait(bars + 8 * st, worked / kStages & 1)) {
+      const int st = stage;
+      if (ok && !warp_wait(bars + 8 * st, pass)) {
         raise_error(p.c.err, kErrTimeout);
         ok = false;
       }
@@ -552,8 +579,10 @@ struct Worker {
 #pragma unroll
         for (int h = 0; h < 2; ++h) w[j][h] = lds128(at + h * 1024 + (((2 * c + j) ^ r) << 4));
       ++worked;
+      if (++stage == kStages) stage = 0, pass ^= 1;
       __syncwarp();
       push();
+      if (piece == kLate) tell();
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t u[4] = {w[j][0].x, w[j][0].y, w[j][0].z, w[j][0].w}, l[4] = {w[j][1].x, w[j][1].y, w[j][1].z, w[j][1].w};
@@ -578,29 +607,37 @@ struct Worker {
           for (int h = 0; h < kParts; ++h)
 #pragma unroll
             for (int g = 0; g < kLoads / 2; ++g) {
-              const uint4 v = kAhead ? b[h][j * (kLoads / 2) + g] : value(i, piece, j * (kLoads / 2) + g, h);
+              const uint4 v = kAhead ? b[0][h][j * (kLoads / 2) + g] : value(i, piece, j * (kLoads / 2) + g, h);
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
                 const uint2 &a0 = fu[2 * g + q], &a1 = fl[2 * g + q];
                 const uint32_t b0 = q ? v.z : v.x, b1 = q ? v.w : v.y;
-                if (kE4M3 && kKind == 0) mma_f16(part[i], a0.x, a1.x, a0.y, a1.y, b0, b1);
-                else mma_bf16_16816(part[i], a0.x, a1.x, a0.y, a1.y, b0, b1);
+                float(&d)[4] = part[(2 * j + q) % kChains][i];
+                if (kE4M3 && kKind == 0) mma_f16(d, a0.x, a1.x, a0.y, a1.y, b0, b1);
+                else mma_bf16_16816(d, a0.x, a1.x, a0.y, a1.y, b0, b1);
               }
             }
       }
-      if (kAhead && piece + 1 < pieces)
+      if (kAhead)
 #pragma unroll
         for (int h = 0; h < kParts; ++h)
 #pragma unroll
-          for (int q = 0; q < kLoads; ++q) b[h][q] = value(0, piece + 1, q, h);
+          for (int q = 0; q < kLoads; ++q) {
+            b[0][h][q] = b[1][h][q];
+            b[1][h][q] = value(0, piece + 2, q, h);
+          }
       if (kE4M3 || (piece & 1) || piece + 1 == pieces) {  // a block of 128 is summed by itself, then scaled
         const float fu = kE4M3 ? __shfl_sync(~0u, su, piece & 31) : 1.f, fl = kE4M3 ? __shfl_sync(~0u, sl, piece & 31) : 1.f;
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            acc[i][j] = fmaf(part[i][j], j < 2 ? fu : fl, acc[i][j]);
-            part[i][j] = 0.f;
+            float d = part[0][i][j];
+#pragma unroll
+            for (int h = 1; h < kChains; ++h) d += part[h][i][j];
+            acc[i][j] = fmaf(d, j < 2 ? fu : fl, acc[i][j]);
+#pragma unroll
+            for (int h = 0; h < kChains; ++h) part[h][i][j] = 0.f;
           }
       }
     }
@@ -621,11 +658,7 @@ struct Worker {
           // what the first part lost; nothing where it is not finite
           to[wide] = (hi & 0x7F80u) == 0x7F80u ? 0 : f2bf(h - bf2f(hi));
         }
-      __syncwarp();
-      if (lane == 0) {
-        __threadfence();
-        atomicAdd(p.counters + 1, 1u);
-      }
+      owed = 1;
     } else {  // rows row + r and row + 8 + r
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
@@ -635,15 +668,25 @@ struct Worker {
           if (rank < count)
             p.y[(size_t)(first + rank) * p.m.H + n.row + (j >> 1) * 8 + r] = acc[i][j] * s.weight[first + rank];
         }
-      __syncwarp();
-      unsigned before = 0;
-      if (lane == 0) {
-        __threadfence();
-        before = atomicAdd(p.counters + 2 + n.row / 16, 1u);
-        __threadfence();
-      }
-      if (__shfl_sync(~0u, before, 0) + 1 == (unsigned)(s.active + (p.m.Is ? 1 : 0))) join(n.row);
+      owed = 2 + n.row;
     }
+  }
+
+  // What the last unit wrote is made known when it is written, some stages into the next unit: a fence right behind the
+  // stores would wait for them.
+  static constexpr int kLate = 3;
+  __device__ __forceinline__ void tell() {
+    if (owed == 0) return;
+    __syncwarp();
+    unsigned before = 0;
+    if (lane == 0) {
+      __threadfence();
+      before = atomicAdd(owed == 1 ? p.counters + 1 : p.counters + 2 + (owed - 2) / 16, 1u);
+      __threadfence();
+    }
+    const int row = owed - 2;
+    owed = 0;
+    if (row >= 0 && __shfl_sync(~0u, before, 0) + 1 == (unsigned)(s.active + (p.m.Is ? 1 : 0))) join(row);
   }
 
   // 16 columns of the output, from the experts' rows in the order of the choice: the last of their units does it
@@ -680,7 +723,8 @@ struct Worker {
       __syncwarp();
       const Unit n = unit_of(queue[taken & 15]);
       __syncwarp();
-      if (n.kind && !hidden_done) {  // every unit of the first kind is in the hands of a warp that waits for nothing
+      if (n.kind && !hidden_done) {
+        tell();  // every unit of the first kind is in the hands of a warp that waits for nothing
         for (uint32_t i = 0; ok; ++i) {
           const unsigned done = (unsigned)ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1));
           if (__all_sync(~0u, done >= (unsigned)units_a)) break;
@@ -693,9 +737,11 @@ struct Worker {
         hidden_done = true;
       }
       if (!ok) break;
+      if ((n.k + kPiece - 1) / kPiece <= kLate) tell();  // too short a unit to do it underway
       if (n.kind) work_any<1>(n);
       else work_any<0>(n);
     }
+    tell();
     // copies in flight land before the CTA ends, after a wait that ran out too
     for (; worked < loaded; ++worked) warp_wait(bars + 8 * (worked % kStages), worked / kStages & 1);
   }
@@ -721,15 +767,12 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
   await_grid();
   Worker<kE4M3> w = {p, s, lane, smem_u32(smem + warp * kRing), smem_u32(bars + warp * kStages), queues + warp * 16};
   w.take();
-  make_lists(p, s, reinterpret_cast<uint32_t*>(smem));
-  // the lists' scratch was written by ordinary stores, the ring is by copies
-  fence_proxy_async_smem();
-  __syncthreads();
+  make_lists(p, s);
   w.hidden_units = p.m.I / 8;
   w.out_units = p.m.H / 16;
   w.units_a = s.active * w.hidden_units + p.m.Is / 8;
   w.units = w.units_a + (s.active + (p.m.Is ? 1 : 0)) * w.out_units;
-  w.loaded = w.left = w.x = w.y = w.z = w.pushed = w.worked = 0;
+  w.loaded = w.left = w.x = w.y = w.z = w.pushed = w.load_stage = w.worked = w.stage = w.pass = w.owed = 0;
   w.map = nullptr;
   w.more = w.ok = true;
   w.hidden_done = false;
