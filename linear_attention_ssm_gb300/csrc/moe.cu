@@ -25,11 +25,11 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kMaxTokens = 64, kMaxTopK = 16, kMaxExperts = 1024;
 constexpr int kMaxSlots = kMaxTokens * (kMaxTopK + 1);  // (token, expert) pairs
 constexpr int kStageBytes = 2048;                       // 16 rows of 128 bytes
-constexpr int kStages = 12;
+constexpr int kStages = 6;  // of a warp
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before giving up
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls of the counter of finished units
 constexpr int kBlock = 128;
@@ -104,15 +104,17 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 
 // ---------------------------------------------------------------- tokens and logits
 
+constexpr int kPrepareWarps = 8, kPrepareThreads = kPrepareWarps * 32;
+
 // A CTA for each token's layout, then a warp for the dot products of one expert's row of the router (the shared gate's behind
 // the last) with up to 8 tokens.
 template <bool kE4M3>
-__global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant__ MoeParams p) {
-  __shared__ float tops[kWarps];
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ MoeParams p) {
+  __shared__ float tops[kPrepareWarps];
   await_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = p.m.H;
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < 2 + H / 16; i += kThreads) p.counters[i] = 0;
+    for (int i = threadIdx.x; i < 2 + H / 16; i += kPrepareThreads) p.counters[i] = 0;
   if (blockIdx.x < p.c.T) {
     const int t = blockIdx.x;
     const uint16_t* x = p.c.x + t * p.c.x_stride;
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant
     float scale = 1.f;
     if (kE4M3) {
       float top = 0.f;  // the largest finite magnitude
-      for (int k = threadIdx.x * 8; k < H; k += kThreads * 8) {
+      for (int k = threadIdx.x * 8; k < H; k += kPrepareThreads * 8) {
         const uint4 v = ld_once(x + k);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -133,12 +135,12 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
       if (lane == 0) tops[warp] = top;
       __syncthreads();
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, tops[w]);
+      for (int w = 0; w < kPrepareWarps; ++w) top = fmaxf(top, tops[w]);
       // the largest value's exponent, raised to where the power of two has a reciprocal
       const int e = max((int)(__float_as_uint(top) >> 23), 15);
       scale = __uint_as_float((uint32_t)(e - 14) << 23);
       const float inverse = __uint_as_float((uint32_t)(254 - (e - 14)) << 23);
-      for (int k = threadIdx.x * 8; k < H; k += kThreads * 8) {
+      for (int k = threadIdx.x * 8; k < H; k += kPrepareThreads * 8) {
         const uint4 v = ld_once(x + k);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t h[4];
@@ -148,13 +150,23 @@ __global__ void __launch_bounds__(kThreads) prepare_kernel(const __grid_constant
         *reinterpret_cast<uint4*>(to + place<kE4M3>(k)) = make_uint4(h[0], h[1], h[2], h[3]);
       }
     } else {
-      for (int k = threadIdx.x * 8; k < H; k += kThreads * 8) *reinterpret_cast<uint4*>(to + place<kE4M3>(k)) = ld_once(x + k);
+      for (int k = threadIdx.x * 8; k < H; k += kPrepareThreads * 8) *reinterpret_cast<uint4*>(to + place<kE4M3>(k)) = ld_once(x + k);
     }
     if (threadIdx.x == 0) p.x_scale[t] = scale;
+    // zeroes behind the ends of rows, as the copies of weights have them
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int wide = pad128(p.m.I), shared_wide = pad128(p.m.Is);
+    for (int k = H + threadIdx.x * 8; k < pad128(H); k += kPrepareThreads * 8) *reinterpret_cast<uint4*>(to + place<kE4M3>(k)) = zero;
+    for (int s = 0; s < 2 * p.c.top_k; ++s)
+      for (int k = p.m.I + threadIdx.x * 8; k < wide; k += kPrepareThreads * 8)
+        *reinterpret_cast<uint4*>(p.hidden + ((size_t)t * 2 * p.c.top_k + s) * wide + place<kE4M3>(k)) = zero;
+    for (int s = 0; s < 2; ++s)
+      for (int k = p.m.Is + threadIdx.x * 8; k < shared_wide; k += kPrepareThreads * 8)
+        *reinterpret_cast<uint4*>(p.shared_hidden + ((size_t)t * 2 + s) * shared_wide + place<kE4M3>(k)) = zero;
     return;
   }
   // rows of the router, unless the routing is given, then the shared gate
-  const int groups = (p.c.T + 7) / 8, item = (blockIdx.x - p.c.T) * kWarps + warp;
+  const int groups = (p.c.T + 7) / 8, item = (blockIdx.x - p.c.T) * kPrepareWarps + warp;
   const int e = (p.c.ids_in ? p.m.E : 0) + item / groups, t0 = item % groups * 8;
   const uint16_t* w = e < p.m.E ? p.m.router + (size_t)e * H : p.m.shared_gate;
   if (e > p.m.E || !w) return;
@@ -244,8 +256,9 @@ __device__ __forceinline__ void choose(const MoeParams& p, Lists& s, int t, int 
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
       if (key[i] > best) best = key[i], at = lane + 32 * i;
-    const uint32_t k = __reduce_max_sync(~0u, best);
-    const int e = __reduce_min_sync(~0u, best == k ? at : kMaxExperts);
+    const uint32_t k = __reduce_max_sync(~0u, best), with = __ballot_sync(~0u, best == k);
+    int e = __shfl_sync(~0u, at, __ffs(with) - 1);
+    if (with & (with - 1)) e = __reduce_min_sync(~0u, best == k ? at : kMaxExperts);  // a tie
     if (lane == j) id = e;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
@@ -374,17 +387,33 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
 
 // ---------------------------------------------------------------- the experts
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// D = A B, or D += A B: m16n8k16 with binary16 or bf16 operands and fp32 sums.  Lane l has rows l / 4 and l / 4 + 8 of A at
+// the k of its place l % 4, column l / 4 of B at the same k, and columns 2 (l % 4), + 1 of D's two rows.
+template <bool kHalf, bool kFirst>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint2& upper, const uint2& lower, uint32_t b0, uint32_t b1) {
+  const float z = 0.f;
+  if constexpr (kHalf && kFirst)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(upper.x), "r"(lower.x), "r"(upper.y), "r"(lower.y), "r"(b0), "r"(b1), "f"(z));
+  else if constexpr (kHalf)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(upper.x), "r"(lower.x), "r"(upper.y), "r"(lower.y), "r"(b0), "r"(b1));
+  else if constexpr (kFirst)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(upper.x), "r"(lower.x), "r"(upper.y), "r"(lower.y), "r"(b0), "r"(b1), "f"(z));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(upper.x), "r"(lower.x), "r"(upper.y), "r"(lower.y), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                               uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// 16 bytes where `there`, else what v holds
+__device__ __forceinline__ void ld_if(uint4& v, const void* p, bool there) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\n@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+               : "l"(p), "r"((int)there));
 }
 
 // Four finite e4m3 codes -> two pairs of bf16, low codes first: the code's exponent and significand at their places of a
@@ -439,16 +468,17 @@ struct Worker {
   const uint32_t ring, bars;  // this warp's stages and barriers
   int* queue;                 // units on their way
   int units_a, units;         // of the first kind, of both
-  int hidden_units, out_units, shared_rows;  // units of an expert of either kind; of the shared one's first kind
-  // loading
+  int hidden_units, out_units;  // units of an expert of either kind
+  // loading: the unit that is being loaded, and the one after it
   unsigned ticket;
-  int loaded, left, x, y, z, pushed, load_stage;
+  int pushed, load_stage, left, x, y, z, next, next_left, next_y, next_z, next_map;
   const void* map;
   bool more;
   // working
-  int worked, stage, pass;  // stages worked on; the next one and its phase
-  int owed;                 // what the last unit has still to tell: 0 nothing, 1 that its h is written, 2 + row of its output
-  bool hidden_done, ok;
+  int ahead, worked, stage, pass;  // stages loaded and not worked on; units done; the next stage and its phase
+  int hidden_done;   // units of the first kind done and not yet told
+  int owed, owed_row;  // units of the second kind not yet told; lane i: the row of unit i
+  bool hidden_ready, ok;
 
   __device__ __forceinline__ Unit unit_of(int u) const {
     Unit n;
@@ -460,43 +490,59 @@ struct Worker {
     n.k = !n.kind ? p.m.H : n.shared ? p.m.Is : p.m.I;
     return n;
   }
-  __device__ __forceinline__ void take() {  // the next unit's number, known a unit later
+  __device__ __forceinline__ void take() {  // the next unit's number, known later
     if (lane == 0) ticket = atomicAdd(p.counters, 1u);
+  }
+  // makes the next unit ready to be loaded
+  __device__ __forceinline__ void prepare_next() {
+    if (next_left || !more) return;
+    next = (int)__shfl_sync(~0u, ticket, 0);
+    if ((unsigned)next >= (unsigned)units) {
+      more = false;
+      return;
+    }
+    take();
+    const Unit n = unit_of(next);
+    const int e = n.shared ? 0 : s.expert[n.a];
+    next_map = n.kind * 2 + n.shared;
+    next_y = n.row;
+    next_z = n.kind ? e : 2 * e;
+    next_left = (n.k + kPiece - 1) / kPiece;
+    if (kE4M3) {  // its scales, towards L2
+      const int blocks = (n.k + kBlock - 1) / kBlock;
+      const float *upper, *lower;
+      scales_of(n, upper, lower);
+      if (lane * 8 < blocks) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(upper + lane * 8));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(lower + lane * 8));
+      }
+    }
   }
   // loads one stage, if there is something to load
   __device__ __forceinline__ void push() {
     if (left == 0) {
-      if (!more) return;
-      const unsigned u = __shfl_sync(~0u, ticket, 0);
-      if (u >= (unsigned)units) {
-        more = false;
-        return;
-      }
-      take();
-      if (lane == 0) queue[pushed & 15] = (int)u;
+      if (next_left == 0) return;
+      if (lane == 0) queue[pushed & 7] = next;
       ++pushed;
-      const Unit n = unit_of((int)u);
-      const int e = n.shared ? 0 : s.expert[n.a];
-      map = n.kind ? (n.shared ? &p.shared_down : &p.down) : (n.shared ? &p.shared_gate_up : &p.gate_up);
+      map = next_map == 0 ? &p.gate_up : next_map == 1 ? &p.shared_gate_up : next_map == 2 ? &p.down : &p.shared_down;
       x = 0;
-      y = n.row;
-      z = n.kind ? e : 2 * e;
-      left = (n.k + kPiece - 1) / kPiece;
-      if (kE4M3) {  // its scales, towards L2
-        const int blocks = (n.k + kBlock - 1) / kBlock;
-        const float *g, *u2;
-        scales_of(n, g, u2);
-        if (lane * 8 < blocks) {
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(g + lane * 8));
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(u2 + lane * 8));
-        }
-      }
+      y = next_y;
+      z = next_z;
+      left = next_left;
+      next_left = 0;
     }
     warp_load(ring + load_stage * kStageBytes, map, x, y, z, bars + 8 * load_stage);
     if (++load_stage == kStages) load_stage = 0;
-    ++loaded;
+    ++ahead;
     x += kPiece;
     --left;
+  }
+  __device__ __forceinline__ void fill() {
+    for (;;) {
+      prepare_next();
+      if (ahead == kStages || (left == 0 && next_left == 0)) break;
+      push();
+    }
   }
   // the scales of a unit's rows by blocks of k: its upper and lower 8
   __device__ __forceinline__ void scales_of(const Unit& n, const float*& upper, const float*& lower) const {
@@ -513,80 +559,75 @@ struct Worker {
     }
   }
 
-  // One unit for up to 8 kTiles tokens of its expert from rank t0 on; the last pass over the unit's stages frees them.
+  // One unit, for an expert of up to 8 kTiles tokens.
   template <int kKind, int kTiles>
   __device__ __forceinline__ void work(const Unit& n) {
     const int r = lane >> 2, c = lane & 3, first = s.first[n.a], count = s.first[n.a + 1] - first;
-    const int width = pad128(n.k);
-    // where this lane's token of each tile has its values (behind the last token: none)
+    const int width = pad128(n.k), pieces = (n.k + kPiece - 1) / kPiece;
+    constexpr int kLoads = kE4M3 ? 4 : 2;       // of a lane from a token for a piece, 32 values apart
+    constexpr int kParts = kKind == 0 ? 1 : 2;  // h is held in two
+    constexpr int kSteps = kE4M3 ? 4 : 2;       // products of a chunk
+    constexpr int kChains = kTiles == 1 ? 2 : 1;  // sums that do not wait for one another
+    // this lane's token of each tile (behind the last token: none, and zeroes)
     const uint16_t* src[kTiles];
+    bool there[kTiles];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       const int rank = 8 * i + r;
-      src[i] = rank >= count ? nullptr
-               : kKind == 0  ? p.x + (size_t)s.token[first + rank] * width
-               : n.shared    ? p.shared_hidden + (size_t)rank * 2 * width
-                             : p.hidden + (size_t)(first + rank) * 2 * width;
+      there[i] = rank < count;
+      const size_t row = !there[i] ? 0 : kKind == 0 ? s.token[first + rank] : (size_t)2 * (n.shared ? rank : first + rank);
+      src[i] = (kKind == 0 ? p.x : n.shared ? p.shared_hidden : p.hidden) + row * width + c * 8;
     }
-    constexpr int kChains = kTiles == 1 ? 4 : kTiles == 2 ? 2 : 1;  // sums that do not wait for one another
-    float acc[kTiles][4], part[kChains][kTiles][4];
+    float acc[kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[i][j] = 0.f;
-#pragma unroll
-        for (int h = 0; h < kChains; ++h) part[h][i][j] = 0.f;
-      }
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
     const float *upper = nullptr, *lower = nullptr;
     float su = 1.f, sl = 1.f;  // lane i: block i's scales, of 32
     if (kE4M3) scales_of(n, upper, lower);
-    constexpr int kLoads = kE4M3 ? 4 : 2;            // of a lane from a token for a piece
-    constexpr int kParts = kKind == 0 ? 1 : 2;       // h is held in two
-    const int pieces = (n.k + kPiece - 1) / kPiece;
-    auto value = [&](int i, int piece, int load, int half) {
-      const int k = piece * kPiece + c * (kPiece / 4) + load * 8;  // of the first of eight
-      const int at = kE4M3 ? piece * 128 + (load * 4 + c) * 8 : (piece >> 1) * 128 + (((piece & 1) * 2 + load) * 4 + c) * 8;
-      return src[i] && k < n.k ? ld_here(src[i] + half * width + at) : make_uint4(0, 0, 0, 0);
-    };
+    const uint32_t place0 = r * 128 + ((2 * c ^ r) << 4), place1 = r * 128 + (((2 * c + 1) ^ r) << 4);
+    const uint4 none = make_uint4(0, 0, 0, 0);
     constexpr bool kAhead = kTiles == 1;  // one tile's values are loaded two pieces ahead
     uint4 b[2][kParts][kLoads];
-    if (kAhead)
+    auto fetch = [&](uint4(&to)[kParts][kLoads], int piece) {
 #pragma unroll
-      for (int d = 0; d < 2; ++d)
+      for (int h = 0; h < kParts; ++h)
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) ld_if(to[h][q], src[0] + h * width + piece * kPiece + q * 32, there[0]);
+    };
+    if (kAhead) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
 #pragma unroll
         for (int h = 0; h < kParts; ++h)
 #pragma unroll
-          for (int q = 0; q < kLoads; ++q) b[d][h][q] = value(0, d, q, h);
-#pragma unroll 1
-    for (int piece = 0; piece < pieces; ++piece) {
+          for (int q = 0; q < kLoads; ++q) b[d][h][q] = none;
+        if (d < pieces) fetch(b[d], d);
+      }
+    }
+    auto step = [&](int piece, uint4(&mine)[kParts][kLoads]) {
       if (kE4M3 && (piece & 31) == 0) {
         const int at = piece + lane;
         su = at < pieces ? ld_f32(upper + at) : 0.f;
-        sl = at < pieces ? ld_f32(lower + at) : 0.f;
+        if (kKind == 0) sl = at < pieces ? ld_f32(lower + at) : 0.f;
       }
-      const int st = stage;
-      if (ok && !warp_wait(bars + 8 * st, pass)) {
+      if (!warp_wait(bars + 8 * stage, pass)) {
         raise_error(p.c.err, kErrTimeout);
         ok = false;
+        return;
       }
-      if (!ok) return;
       // rows r and r + 8, chunks 2 c and 2 c + 1 of the swizzled piece
-      uint4 w[2][2];
-      const uint32_t at = ring + st * kStageBytes + r * 128;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) w[j][h] = lds128(at + h * 1024 + (((2 * c + j) ^ r) << 4));
-      ++worked;
+      const uint32_t at = ring + stage * kStageBytes;
+      const uint4 w[2][2] = {{lds128(at + place0), lds128(at + 1024 + place0)}, {lds128(at + place1), lds128(at + 1024 + place1)}};
       if (++stage == kStages) stage = 0, pass ^= 1;
+      --ahead;
       __syncwarp();
       push();
-      if (piece == kLate) tell();
+      float part[kChains][kTiles][4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t u[4] = {w[j][0].x, w[j][0].y, w[j][0].z, w[j][0].w}, l[4] = {w[j][1].x, w[j][1].y, w[j][1].z, w[j][1].w};
-        constexpr int kSteps = kE4M3 ? 4 : 2;  // products of a chunk
         uint2 fu[kSteps], fl[kSteps];
 #pragma unroll
         for (int q = 0; q < kSteps; ++q) {
@@ -607,40 +648,37 @@ struct Worker {
           for (int h = 0; h < kParts; ++h)
 #pragma unroll
             for (int g = 0; g < kLoads / 2; ++g) {
-              const uint4 v = kAhead ? b[0][h][j * (kLoads / 2) + g] : value(i, piece, j * (kLoads / 2) + g, h);
+              uint4 v = none;
+              if (kAhead) v = mine[h][j * (kLoads / 2) + g];
+              else ld_if(v, src[i] + h * width + piece * kPiece + (j * (kLoads / 2) + g) * 32, there[i]);
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
-                const uint2 &a0 = fu[2 * g + q], &a1 = fl[2 * g + q];
-                const uint32_t b0 = q ? v.z : v.x, b1 = q ? v.w : v.y;
-                float(&d)[4] = part[(2 * j + q) % kChains][i];
-                if (kE4M3 && kKind == 0) mma_f16(d, a0.x, a1.x, a0.y, a1.y, b0, b1);
-                else mma_bf16_16816(d, a0.x, a1.x, a0.y, a1.y, b0, b1);
+                const int nth = ((j * kParts + h) * (kLoads / 2) + g) * 2 + q, chain = nth % kChains;
+                float(&d)[4] = part[chain][i];
+                if (nth < kChains) mma_16816<kE4M3 && kKind == 0, true>(d, fu[2 * g + q], fl[2 * g + q], q ? v.z : v.x, q ? v.w : v.y);
+                else mma_16816<kE4M3 && kKind == 0, false>(d, fu[2 * g + q], fl[2 * g + q], q ? v.z : v.x, q ? v.w : v.y);
               }
             }
       }
-      if (kAhead)
+      if (kAhead && piece + 2 < pieces) fetch(mine, piece + 2);
+      // a piece is summed by itself, then scaled
+      const float fu = kE4M3 ? __shfl_sync(~0u, su, piece & 31) : 1.f;
+      const float fl = !kE4M3 ? 1.f : kKind == 0 ? __shfl_sync(~0u, sl, piece & 31) : fu;
 #pragma unroll
-        for (int h = 0; h < kParts; ++h)
+      for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-          for (int q = 0; q < kLoads; ++q) {
-            b[0][h][q] = b[1][h][q];
-            b[1][h][q] = value(0, piece + 2, q, h);
-          }
-      if (kE4M3 || (piece & 1) || piece + 1 == pieces) {  // a block of 128 is summed by itself, then scaled
-        const float fu = kE4M3 ? __shfl_sync(~0u, su, piece & 31) : 1.f, fl = kE4M3 ? __shfl_sync(~0u, sl, piece & 31) : 1.f;
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float d = part[0][i][j];
-#pragma unroll
-            for (int h = 1; h < kChains; ++h) d += part[h][i][j];
-            acc[i][j] = fmaf(d, j < 2 ? fu : fl, acc[i][j]);
-#pragma unroll
-            for (int h = 0; h < kChains; ++h) part[h][i][j] = 0.f;
-          }
-      }
+        for (int j = 0; j < 4; ++j) {
+          float d = part[0][i][j];
+          if (kChains > 1) d += part[kChains - 1][i][j];
+          acc[i][j] = fmaf(d, j < 2 ? fu : fl, acc[i][j]);
+        }
+    };
+#pragma unroll 1
+    for (int piece = 0; piece < pieces && ok; piece += 2) {
+      step(piece, b[0]);
+      if (piece + 1 < pieces && ok) step(piece + 1, b[1]);
     }
+    if (!ok) return;
     if constexpr (kKind == 0) {  // silu(gate) * up for places row + r, tokens 8 i + 2 c and the next
       uint16_t* hidden = n.shared ? p.shared_hidden : p.hidden;
       const int base = n.shared ? 0 : first, wide = pad128(n.shared ? p.m.Is : p.m.I), at = place<kE4M3>(n.row) + r;
@@ -658,7 +696,7 @@ struct Worker {
           // what the first part lost; nothing where it is not finite
           to[wide] = (hi & 0x7F80u) == 0x7F80u ? 0 : f2bf(h - bf2f(hi));
         }
-      owed = 1;
+      ++hidden_done;
     } else {  // rows row + r and row + 8 + r
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
@@ -668,25 +706,34 @@ struct Worker {
           if (rank < count)
             p.y[(size_t)(first + rank) * p.m.H + n.row + (j >> 1) * 8 + r] = acc[i][j] * s.weight[first + rank];
         }
-      owed = 2 + n.row;
+      if (lane == owed) owed_row = n.row;
+      ++owed;
     }
   }
 
-  // What the last unit wrote is made known when it is written, some stages into the next unit: a fence right behind the
-  // stores would wait for them.
-  static constexpr int kLate = 3;
-  __device__ __forceinline__ void tell() {
+  // A fence waits for the stores before it: what units wrote is made known several units at a time.
+  __device__ __forceinline__ void tell_hidden() {
+    __syncwarp();
+    if (lane == 0 && hidden_done) {
+      __threadfence();
+      atomicAdd(p.counters + 1, (unsigned)hidden_done);
+    }
+    hidden_done = 0;
+  }
+  static constexpr int kOwed = 4;
+  __device__ __forceinline__ void tell_rows() {
     if (owed == 0) return;
     __syncwarp();
     unsigned before = 0;
-    if (lane == 0) {
+    if (lane < owed) {
       __threadfence();
-      before = atomicAdd(owed == 1 ? p.counters + 1 : p.counters + 2 + (owed - 2) / 16, 1u);
+      before = atomicAdd(p.counters + 2 + owed_row / 16, 1u);
       __threadfence();
     }
-    const int row = owed - 2;
+    const unsigned last = __ballot_sync(~0u, lane < owed && before + 1 == (unsigned)(s.active + (p.m.Is ? 1 : 0)));
+    for (int i = 0; i < kOwed; ++i)
+      if (last >> i & 1) join(__shfl_sync(~0u, owed_row, i));
     owed = 0;
-    if (row >= 0 && __shfl_sync(~0u, before, 0) + 1 == (unsigned)(s.active + (p.m.Is ? 1 : 0))) join(row);
   }
 
   // 16 columns of the output, from the experts' rows in the order of the choice: the last of their units does it
@@ -718,13 +765,13 @@ struct Worker {
   }
 
   __device__ __forceinline__ void run() {
-    for (int i = 0; i < kStages; ++i) push();
-    for (int taken = 0; ok && taken != pushed; ++taken) {
+    fill();
+    for (worked = 0; ok && worked != pushed; ++worked) {
       __syncwarp();
-      const Unit n = unit_of(queue[taken & 15]);
+      const Unit n = unit_of(queue[worked & 7]);
       __syncwarp();
-      if (n.kind && !hidden_done) {
-        tell();  // every unit of the first kind is in the hands of a warp that waits for nothing
+      if (n.kind && !hidden_ready) {  // every unit of the first kind is in the hands of a warp that waits for nothing
+        tell_hidden();
         for (uint32_t i = 0; ok; ++i) {
           const unsigned done = (unsigned)ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1));
           if (__all_sync(~0u, done >= (unsigned)units_a)) break;
@@ -734,20 +781,25 @@ struct Worker {
           }
           __nanosleep(32);
         }
-        hidden_done = true;
+        hidden_ready = true;
+        if (!ok) break;
       }
-      if (!ok) break;
-      if ((n.k + kPiece - 1) / kPiece <= kLate) tell();  // too short a unit to do it underway
       if (n.kind) work_any<1>(n);
       else work_any<0>(n);
+      if (owed == kOwed) tell_rows();
+      fill();
     }
-    tell();
+    tell_hidden();
+    tell_rows();
     // copies in flight land before the CTA ends, after a wait that ran out too
-    for (; worked < loaded; ++worked) warp_wait(bars + 8 * (worked % kStages), worked / kStages & 1);
+    for (; ahead; --ahead) {
+      warp_wait(bars + 8 * stage, pass);
+      if (++stage == kStages) stage = 0, pass ^= 1;
+    }
   }
 };
 
-constexpr size_t kSmem = 1024 + (size_t)kWarps * kStages * kStageBytes + sizeof(Lists) + kWarps * (16 * 4 + kStages * 8) + 64;
+constexpr size_t kSmem = 1024 + (size_t)kWarps * kStages * kStageBytes + sizeof(Lists) + kWarps * (8 * 4 + kStages * 8) + 64;
 
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ MoeParams p) {
@@ -765,17 +817,18 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
   }
   fence_mbar_init();
   await_grid();
-  Worker<kE4M3> w = {p, s, lane, smem_u32(smem + warp * kRing), smem_u32(bars + warp * kStages), queues + warp * 16};
+  Worker<kE4M3> w = {p, s, lane, smem_u32(smem + warp * kRing), smem_u32(bars + warp * kStages), queues + warp * 8};
   w.take();
   make_lists(p, s);
   w.hidden_units = p.m.I / 8;
   w.out_units = p.m.H / 16;
   w.units_a = s.active * w.hidden_units + p.m.Is / 8;
   w.units = w.units_a + (s.active + (p.m.Is ? 1 : 0)) * w.out_units;
-  w.loaded = w.left = w.x = w.y = w.z = w.pushed = w.load_stage = w.worked = w.stage = w.pass = w.owed = 0;
+  w.pushed = w.load_stage = w.left = w.x = w.y = w.z = w.next = w.next_left = w.next_y = w.next_z = w.next_map = 0;
+  w.ahead = w.worked = w.stage = w.pass = w.hidden_done = w.owed = w.owed_row = 0;
   w.map = nullptr;
   w.more = w.ok = true;
-  w.hidden_done = false;
+  w.hidden_ready = false;
   if (w.units == 0) {  // no token has an expert
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.c.T * p.m.H / 8; i += gridDim.x * kThreads)
       reinterpret_cast<uint4*>(p.c.out)[i] = make_uint4(0, 0, 0, 0);
@@ -810,7 +863,7 @@ cudaError_t launch(const LaunchEnv& env, MoeParams& p) {
   if (e == cudaSuccess) e = encode<kE4M3>(&p.shared_down, m.Is ? m.shared_down : nullptr, m.Is, m.H, 1, false);
   if (e != cudaSuccess) return e;
   const int dots = ((p.c.ids_in ? 0 : m.E) + (m.shared_gate ? 1 : 0)) * ((p.c.T + 7) / 8);
-  e = launch_early(prepare_kernel<kE4M3>, dim3(p.c.T + (dots + kWarps - 1) / kWarps), kThreads, 0, env.stream, p);
+  e = launch_early(prepare_kernel<kE4M3>, dim3(p.c.T + (dots + kPrepareWarps - 1) / kPrepareWarps), kPrepareThreads, 0, env.stream, p);
   if (e != cudaSuccess) return e;
   return launch_early(experts_kernel<kE4M3>, dim3(sms), kThreads, kSmem, env.stream, p);
 }
