@@ -25,11 +25,11 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 16, kThreads = kWarps * 32;
+constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kMaxTokens = 64, kMaxTopK = 16, kMaxExperts = 1024;
 constexpr int kMaxSlots = kMaxTokens * (kMaxTopK + 1);  // (token, expert) pairs
-constexpr int kStageBytes = 2048;                       // 16 rows of 128 bytes
-constexpr int kStages = 6;  // of a warp
+constexpr int kStageBytes = 4096;                       // 16 rows of two pieces of 128 bytes
+constexpr int kStages = 6;                              // of a warp
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before giving up
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls of the counter of finished units
 constexpr int kBlock = 128;
@@ -37,17 +37,17 @@ constexpr int kBlock = 128;
 struct Layout {  // of the workspace
   size_t counters, logits, x, x_scale, hidden, shared_hidden, y, bytes;
 };
-__host__ __device__ inline int pad128(int n) { return (n + 127) & ~127; }
+__host__ __device__ inline int pad256(int n) { return (n + 255) & ~255; }
 Layout layout(const Moe& m, int T, int k) {
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   Layout l;
   l.counters = 0;
   l.logits = l.counters + up((2 + m.H / 16) * 4);
   l.x = l.logits + up((size_t)T * (m.E + 1) * 4);
-  l.x_scale = l.x + up((size_t)T * pad128(m.H) * 2);
+  l.x_scale = l.x + up((size_t)T * pad256(m.H) * 2);
   l.hidden = l.x_scale + up((size_t)T * 4);
-  l.shared_hidden = l.hidden + up((size_t)T * k * pad128(m.I) * 4);
-  l.y = l.shared_hidden + up((size_t)T * pad128(m.Is) * 4);
+  l.shared_hidden = l.hidden + up((size_t)T * k * pad256(m.I) * 4);
+  l.y = l.shared_hidden + up((size_t)T * pad256(m.Is) * 4);
   l.bytes = l.y + up((size_t)T * (k + (m.Is ? 1 : 0)) * m.H * 4);
   return l;
 }
@@ -58,9 +58,9 @@ struct MoeParams {
   MoeCall c;
   unsigned* counters;  // next unit; first units done; for each 16 rows of the output, down units done
   float* logits;       // [T][E + 1], the shared gate's behind the experts'
-  uint16_t* x;         // [T][pad128(H)] tokens in the products' order, bf16 or binary16
+  uint16_t* x;         // [T][pad256(H)] tokens in the products' order, bf16 or binary16
   float* x_scale;      // [T] what a binary16 token is multiplied with
-  uint16_t* hidden;    // [T * top_k][2][pad128(I)] in the products' order: bf16, then the rest
+  uint16_t* hidden;    // [T * top_k][2][pad256(I)] in the products' order: bf16, then the rest
   uint16_t* shared_hidden;
   float* y;            // [slots][H] weighted rows of the experts
 };
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
   if (blockIdx.x < p.c.T) {
     const int t = blockIdx.x;
     const uint16_t* x = p.c.x + t * p.c.x_stride;
-    uint16_t* to = p.x + (size_t)t * pad128(H);
+    uint16_t* to = p.x + (size_t)t * pad256(H);
     float scale = 1.f;
     if (kE4M3) {
       float top = 0.f;  // the largest finite magnitude
@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     if (threadIdx.x == 0) p.x_scale[t] = scale;
     // zeroes behind the ends of rows, as the copies of weights have them
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    const int wide = pad128(p.m.I), shared_wide = pad128(p.m.Is);
-    for (int k = H + threadIdx.x * 8; k < pad128(H); k += kPrepareThreads * 8) *reinterpret_cast<uint4*>(to + place<kE4M3>(k)) = zero;
+    const int wide = pad256(p.m.I), shared_wide = pad256(p.m.Is);
+    for (int k = H + threadIdx.x * 8; k < pad256(H); k += kPrepareThreads * 8) *reinterpret_cast<uint4*>(to + place<kE4M3>(k)) = zero;
     for (int s = 0; s < 2 * p.c.top_k; ++s)
       for (int k = p.m.I + threadIdx.x * 8; k < wide; k += kPrepareThreads * 8)
         *reinterpret_cast<uint4*>(p.hidden + ((size_t)t * 2 * p.c.top_k + s) * wide + place<kE4M3>(k)) = zero;
@@ -319,7 +319,7 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
     if (s.chosen[t][j] >= 0) atomicOr(&s.mask[s.chosen[t][j]], 1ull << t);
   __syncthreads();
   // experts that have tokens, in order: each thread has some neighbours; experts above, slots below in a word
-  constexpr int kOwn = kMaxExperts / kThreads;
+  constexpr int kOwn = (kMaxExperts + kThreads - 1) / kThreads;
   uint32_t own = 0;
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
@@ -439,15 +439,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   }
   return false;
 }
-// a stage's load, by one lane of the warp
-__device__ __forceinline__ void warp_load(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
+// a stage's two loads, by one lane of the warp
+__device__ __forceinline__ void warp_load(uint32_t dst, const void* map, int x0, int x1, int y, int z, uint32_t bar) {
   asm volatile(
-      "{\n.reg .pred e;\n"
+      "{\n.reg .pred e;\n.reg .b32 d;\n"
       "elect.sync _|e, 0xFFFFFFFF;\n"
+      "add.s32 d, %2, 2048;\n"
       "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%4, %5, %6}], [%0];\n"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%4, %6, %7}], [%0];\n"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [d], [%3, {%5, %6, %7}], [%0];\n"
       "}" ::"r"(bar),
-      "r"(kStageBytes), "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z)
+      "r"(kStageBytes), "r"(dst), "l"(map), "r"(x0), "r"(x1), "r"(y), "r"(z)
       : "memory");
 }
 
@@ -507,7 +509,7 @@ struct Worker {
     next_map = n.kind * 2 + n.shared;
     next_y = n.row;
     next_z = n.kind ? e : 2 * e;
-    next_left = (n.k + kPiece - 1) / kPiece;
+    next_left = (n.k + 2 * kPiece - 1) / (2 * kPiece);
     if (kE4M3) {  // its scales, towards L2
       const int blocks = (n.k + kBlock - 1) / kBlock;
       const float *upper, *lower;
@@ -522,7 +524,7 @@ struct Worker {
   __device__ __forceinline__ void push() {
     if (left == 0) {
       if (next_left == 0) return;
-      if (lane == 0) queue[pushed & 7] = next;
+      if (lane == 0) queue[pushed & 15] = next;
       ++pushed;
       map = next_map == 0 ? &p.gate_up : next_map == 1 ? &p.shared_gate_up : next_map == 2 ? &p.down : &p.shared_down;
       x = 0;
@@ -531,10 +533,10 @@ struct Worker {
       left = next_left;
       next_left = 0;
     }
-    warp_load(ring + load_stage * kStageBytes, map, x, y, z, bars + 8 * load_stage);
+    warp_load(ring + load_stage * kStageBytes, map, x, x + kPiece, y, z, bars + 8 * load_stage);
     if (++load_stage == kStages) load_stage = 0;
     ++ahead;
-    x += kPiece;
+    x += 2 * kPiece;
     --left;
   }
   __device__ __forceinline__ void fill() {
@@ -563,7 +565,7 @@ struct Worker {
   template <int kKind, int kTiles>
   __device__ __forceinline__ void work(const Unit& n) {
     const int r = lane >> 2, c = lane & 3, first = s.first[n.a], count = s.first[n.a + 1] - first;
-    const int width = pad128(n.k), pieces = (n.k + kPiece - 1) / kPiece;
+    const int width = pad256(n.k), count_k = (n.k + 2 * kPiece - 1) / (2 * kPiece);  // stages
     constexpr int kLoads = kE4M3 ? 4 : 2;       // of a lane from a token for a piece, 32 values apart
     constexpr int kParts = kKind == 0 ? 1 : 2;  // h is held in two
     constexpr int kSteps = kE4M3 ? 4 : 2;       // products of a chunk
@@ -588,100 +590,117 @@ struct Worker {
     if (kE4M3) scales_of(n, upper, lower);
     const uint32_t place0 = r * 128 + ((2 * c ^ r) << 4), place1 = r * 128 + (((2 * c + 1) ^ r) << 4);
     const uint4 none = make_uint4(0, 0, 0, 0);
-    constexpr bool kAhead = kTiles == 1;  // one tile's values are loaded two pieces ahead
-    uint4 b[2][kParts][kLoads];
-    auto fetch = [&](uint4(&to)[kParts][kLoads], int piece) {
+    constexpr bool kAhead = kTiles == 1;  // one tile's values are loaded a stage ahead
+    uint4 b[2][2][kParts][kLoads];
+    auto fetch = [&](uint4(&to)[2][kParts][kLoads], int st) {
 #pragma unroll
-      for (int h = 0; h < kParts; ++h)
-#pragma unroll
-        for (int q = 0; q < kLoads; ++q) ld_if(to[h][q], src[0] + h * width + piece * kPiece + q * 32, there[0]);
-    };
-    if (kAhead) {
-#pragma unroll
-      for (int d = 0; d < 2; ++d) {
+      for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
         for (int h = 0; h < kParts; ++h)
 #pragma unroll
-          for (int q = 0; q < kLoads; ++q) b[d][h][q] = none;
-        if (d < pieces) fetch(b[d], d);
-      }
+          for (int q = 0; q < kLoads; ++q)
+            ld_if(to[piece][h][q], src[0] + h * width + (2 * st + piece) * kPiece + q * 32, there[0]);
+    };
+    if (kAhead) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d)
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+          for (int h = 0; h < kParts; ++h)
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) b[d][piece][h][q] = none;
+      fetch(b[0], 0);
     }
-    auto step = [&](int piece, uint4(&mine)[kParts][kLoads]) {
-      if (kE4M3 && (piece & 31) == 0) {
-        const int at = piece + lane;
-        su = at < pieces ? ld_f32(upper + at) : 0.f;
-        if (kKind == 0) sl = at < pieces ? ld_f32(lower + at) : 0.f;
+    auto step = [&](int st, uint4(&mine)[2][kParts][kLoads], uint4(&other)[2][kParts][kLoads]) {
+      if (kE4M3 && (st & 15) == 0) {
+        const int at = 2 * st + lane, blocks = (n.k + kBlock - 1) / kBlock;
+        su = at < blocks ? ld_f32(upper + at) : 0.f;
+        if (kKind == 0) sl = at < blocks ? ld_f32(lower + at) : 0.f;
       }
+      if (kAhead && st + 1 < count_k) fetch(other, st + 1);
       if (!warp_wait(bars + 8 * stage, pass)) {
         raise_error(p.c.err, kErrTimeout);
         ok = false;
         return;
       }
-      // rows r and r + 8, chunks 2 c and 2 c + 1 of the swizzled piece
+      // rows r and r + 8, chunks 2 c and 2 c + 1 of the swizzled pieces
       const uint32_t at = ring + stage * kStageBytes;
-      const uint4 w[2][2] = {{lds128(at + place0), lds128(at + 1024 + place0)}, {lds128(at + place1), lds128(at + 1024 + place1)}};
+      uint4 w[2][2][2];
+#pragma unroll
+      for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w[piece][0][h] = lds128(at + piece * 2048 + h * 1024 + place0);
+          w[piece][1][h] = lds128(at + piece * 2048 + h * 1024 + place1);
+        }
       if (++stage == kStages) stage = 0, pass ^= 1;
       --ahead;
       __syncwarp();
       push();
-      float part[kChains][kTiles][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t u[4] = {w[j][0].x, w[j][0].y, w[j][0].z, w[j][0].w}, l[4] = {w[j][1].x, w[j][1].y, w[j][1].z, w[j][1].w};
-        uint2 fu[kSteps], fl[kSteps];
+      for (int piece = 0; piece < 2; ++piece) {
+        float part[kChains][kTiles][4];
 #pragma unroll
-        for (int q = 0; q < kSteps; ++q) {
-          if constexpr (!kE4M3) {
-            fu[q] = make_uint2(u[2 * q], u[2 * q + 1]);
-            fl[q] = make_uint2(l[2 * q], l[2 * q + 1]);
-          } else if constexpr (kKind == 0) {
-            fu[q] = e4m3x4_to_half4(u[q]);
-            fl[q] = e4m3x4_to_half4(l[q]);
-          } else {
-            fu[q] = e4m3x4_to_bf16x4(u[q]);
-            fl[q] = e4m3x4_to_bf16x4(l[q]);
+        for (int j = 0; j < 2; ++j) {
+          const uint4 &up = w[piece][j][0], &low = w[piece][j][1];
+          const uint32_t u[4] = {up.x, up.y, up.z, up.w}, l[4] = {low.x, low.y, low.z, low.w};
+          uint2 fu[kSteps], fl[kSteps];
+#pragma unroll
+          for (int q = 0; q < kSteps; ++q) {
+            if constexpr (!kE4M3) {
+              fu[q] = make_uint2(u[2 * q], u[2 * q + 1]);
+              fl[q] = make_uint2(l[2 * q], l[2 * q + 1]);
+            } else if constexpr (kKind == 0) {
+              fu[q] = e4m3x4_to_half4(u[q]);
+              fl[q] = e4m3x4_to_half4(l[q]);
+            } else {
+              fu[q] = e4m3x4_to_bf16x4(u[q]);
+              fl[q] = e4m3x4_to_bf16x4(l[q]);
+            }
           }
+#pragma unroll
+          for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+            for (int h = 0; h < kParts; ++h)
+#pragma unroll
+              for (int g = 0; g < kLoads / 2; ++g) {
+                uint4 v = none;
+                if (kAhead) v = mine[piece][h][j * (kLoads / 2) + g];
+                else ld_if(v, src[i] + h * width + (2 * st + piece) * kPiece + (j * (kLoads / 2) + g) * 32, there[i]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const int nth = ((j * kParts + h) * (kLoads / 2) + g) * 2 + q;
+                  float(&d)[4] = part[nth % kChains][i];
+                  const uint2 &a0 = fu[2 * g + q], &a1 = fl[2 * g + q];
+                  if (nth < kChains) mma_16816<kE4M3 && kKind == 0, true>(d, a0, a1, q ? v.z : v.x, q ? v.w : v.y);
+                  else mma_16816<kE4M3 && kKind == 0, false>(d, a0, a1, q ? v.z : v.x, q ? v.w : v.y);
+                }
+              }
         }
+        // a piece is summed by itself, then scaled
+        const int block = 2 * st + piece & 31;
+        const float fu = kE4M3 ? __shfl_sync(~0u, su, block) : 1.f;
+        const float fl = !kE4M3 ? 1.f : kKind == 0 ? __shfl_sync(~0u, sl, block) : fu;
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-          for (int h = 0; h < kParts; ++h)
-#pragma unroll
-            for (int g = 0; g < kLoads / 2; ++g) {
-              uint4 v = none;
-              if (kAhead) v = mine[h][j * (kLoads / 2) + g];
-              else ld_if(v, src[i] + h * width + piece * kPiece + (j * (kLoads / 2) + g) * 32, there[i]);
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int nth = ((j * kParts + h) * (kLoads / 2) + g) * 2 + q, chain = nth % kChains;
-                float(&d)[4] = part[chain][i];
-                if (nth < kChains) mma_16816<kE4M3 && kKind == 0, true>(d, fu[2 * g + q], fl[2 * g + q], q ? v.z : v.x, q ? v.w : v.y);
-                else mma_16816<kE4M3 && kKind == 0, false>(d, fu[2 * g + q], fl[2 * g + q], q ? v.z : v.x, q ? v.w : v.y);
-              }
-            }
+          for (int j = 0; j < 4; ++j) {
+            float d = part[0][i][j];
+            if (kChains > 1) d += part[kChains - 1][i][j];
+            acc[i][j] = fmaf(d, j < 2 ? fu : fl, acc[i][j]);
+          }
       }
-      if (kAhead && piece + 2 < pieces) fetch(mine, piece + 2);
-      // a piece is summed by itself, then scaled
-      const float fu = kE4M3 ? __shfl_sync(~0u, su, piece & 31) : 1.f;
-      const float fl = !kE4M3 ? 1.f : kKind == 0 ? __shfl_sync(~0u, sl, piece & 31) : fu;
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float d = part[0][i][j];
-          if (kChains > 1) d += part[kChains - 1][i][j];
-          acc[i][j] = fmaf(d, j < 2 ? fu : fl, acc[i][j]);
-        }
     };
 #pragma unroll 1
-    for (int piece = 0; piece < pieces && ok; piece += 2) {
-      step(piece, b[0]);
-      if (piece + 1 < pieces && ok) step(piece + 1, b[1]);
+    for (int st = 0; st < count_k && ok; st += 2) {
+      step(st, b[0], b[1]);
+      if (st + 1 < count_k && ok) step(st + 1, b[1], b[0]);
     }
     if (!ok) return;
     if constexpr (kKind == 0) {  // silu(gate) * up for places row + r, tokens 8 i + 2 c and the next
       uint16_t* hidden = n.shared ? p.shared_hidden : p.hidden;
-      const int base = n.shared ? 0 : first, wide = pad128(n.shared ? p.m.Is : p.m.I), at = place<kE4M3>(n.row) + r;
+      const int base = n.shared ? 0 : first, wide = pad256(n.shared ? p.m.Is : p.m.I), at = place<kE4M3>(n.row) + r;
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -768,7 +787,7 @@ struct Worker {
     fill();
     for (worked = 0; ok && worked != pushed; ++worked) {
       __syncwarp();
-      const Unit n = unit_of(queue[worked & 7]);
+      const Unit n = unit_of(queue[worked & 15]);
       __syncwarp();
       if (n.kind && !hidden_ready) {  // every unit of the first kind is in the hands of a warp that waits for nothing
         tell_hidden();
@@ -799,7 +818,7 @@ struct Worker {
   }
 };
 
-constexpr size_t kSmem = 1024 + (size_t)kWarps * kStages * kStageBytes + sizeof(Lists) + kWarps * (8 * 4 + kStages * 8) + 64;
+constexpr size_t kSmem = 1024 + (size_t)kWarps * kStages * kStageBytes + sizeof(Lists) + kWarps * (16 * 4 + kStages * 8) + 64;
 
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ MoeParams p) {
@@ -817,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
   }
   fence_mbar_init();
   await_grid();
-  Worker<kE4M3> w = {p, s, lane, smem_u32(smem + warp * kRing), smem_u32(bars + warp * kStages), queues + warp * 8};
+  Worker<kE4M3> w = {p, s, lane, smem_u32(smem + warp * kRing), smem_u32(bars + warp * kStages), queues + warp * 16};
   w.take();
   make_lists(p, s);
   w.hidden_units = p.m.I / 8;
