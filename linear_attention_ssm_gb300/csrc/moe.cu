@@ -28,8 +28,11 @@ namespace {
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kMaxTokens = 64, kMaxTopK = 16, kMaxExperts = 1024;
 constexpr int kMaxSlots = kMaxTokens * (kMaxTopK + 1);  // (token, expert) pairs
-constexpr int kStageBytes = 4096;                       // 16 rows of two pieces of 128 bytes
-constexpr int kStages = 6;                              // of a warp
+constexpr int kStageBytes = 4096;  // of weights: 16 rows of two pieces of 128 bytes
+constexpr int kRing = 24576;       // of a warp
+constexpr int kEntries = 8;        // barriers of a ring: more than stages fit
+constexpr int kQueue = 8;          // units on their way: more than stages fit, and the one in hand
+constexpr int kScales = 32;        // of a unit's scales of either kind, as many blocks as are kept at hand
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before giving up
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls of the counter of finished units
 constexpr int kBlock = 128;
@@ -207,17 +210,22 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
 
 // What every CTA works out for itself: the tokens' experts and the experts' tokens.
 struct Lists {
-  unsigned long long mask[kMaxExperts];  // tokens of an expert
+  union {
+    struct {                                         // until the lists are there
+      unsigned long long mask[kMaxExperts];          // tokens of an expert
+      float chosen_weight[kMaxTokens][kMaxTopK];
+      uint16_t index[kMaxExperts];                   // the active expert's number
+      int16_t chosen[kMaxTokens][kMaxTopK];          // negative: none
+    };
+    float scales[kWarps][kQueue * 2 * kScales];      // then: of the units on their way
+  };
   float weight[kMaxSlots];
   float x_scale[kMaxTokens];
-  float chosen_weight[kMaxTokens][kMaxTopK];
   uint32_t sums[kWarps];
   int active;                       // experts that have tokens
   uint16_t expert[kMaxExperts];     // of an active expert
   uint16_t first[kMaxExperts + 2];  // its first slot
-  uint16_t index[kMaxExperts];      // the active expert's number
   uint16_t slot_of[kMaxTokens][kMaxTopK + 1];  // kNone: none; the shared expert's last
-  int16_t chosen[kMaxTokens][kMaxTopK];        // negative: none
   uint8_t token[kMaxSlots];
 };
 constexpr uint16_t kNone = 0xFFFF;
@@ -439,8 +447,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   }
   return false;
 }
-// a stage's two loads, by one lane of the warp
-__device__ __forceinline__ void warp_load(uint32_t dst, const void* map, int x0, int x1, int y, int z, uint32_t bar) {
+// a stage's two loads of weights, by one lane of the warp; `bytes` in all are counted by the barrier
+__device__ __forceinline__ void warp_load(uint32_t dst, const void* map, int x0, int x1, int y, int z, uint32_t bar,
+                                          uint32_t bytes) {
   asm volatile(
       "{\n.reg .pred e;\n.reg .b32 d;\n"
       "elect.sync _|e, 0xFFFFFFFF;\n"
@@ -449,36 +458,61 @@ __device__ __forceinline__ void warp_load(uint32_t dst, const void* map, int x0,
       "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%4, %6, %7}], [%0];\n"
       "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [d], [%3, {%5, %6, %7}], [%0];\n"
       "}" ::"r"(bar),
-      "r"(kStageBytes), "r"(dst), "l"(map), "r"(x0), "r"(x1), "r"(y), "r"(z)
+      "r"(bytes), "r"(dst), "l"(map), "r"(x0), "r"(x1), "r"(y), "r"(z)
       : "memory");
+}
+__device__ __forceinline__ void bulk_load_if(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, bool mine) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar), "r"((int)mine)
+      : "memory");
+}
+// 16 bytes of shared memory where `there`, else zeroes
+__device__ __forceinline__ uint4 lds128_if(uint32_t addr, bool there) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\n@q ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+               : "r"(addr), "r"((int)there)
+               : "memory");
+  return v;
 }
 
 // A unit of work.
 struct Unit {
-  int kind;    // 0: 8 rows of gate and up, 1: 16 rows of down
-  int a;       // the active expert, `active` for the shared one
+  int kind;            // 0: 8 rows of gate and up, 1: 16 rows of down
+  int a;               // the active expert, `active` for the shared one
   bool shared;
-  int row, k;  // first row; length of a row
+  int row, k;          // first row; length of a row
+  int first, count;    // the expert's slots
 };
 
+// A warp.  A stage of its ring has 4 KB of weights and behind them, for an expert of up to 8 tokens, the tokens' values for
+// the same k (loads through the cache take several thousand cycles while the copies fill the memory's queues).
 template <bool kE4M3>
 struct Worker {
   static constexpr int kPiece = kE4M3 ? 128 : 64;  // values of a 128-byte piece of a row
+  static constexpr int kStageK = 2 * kPiece;       // of a stage
+  static constexpr int kRowBytes = 2 * kStageK;    // of a token in a stage
   const MoeParams& p;
   Lists& s;
   const int lane;
   const uint32_t ring, bars;  // this warp's stages and barriers
   int* queue;                 // units on their way
+  float* scales;              // theirs: [kQueue][2][kScales]
   int units_a, units;         // of the first kind, of both
   int hidden_units, out_units;  // units of an expert of either kind
   // loading: the unit that is being loaded, and the one after it
   unsigned ticket;
-  int pushed, load_stage, left, x, y, z, next, next_left, next_y, next_z, next_map;
+  int pushed, left, x, y, z, load_size, load_tokens, next;
+  const uint16_t* load_src;  // lane i: token i's values
   const void* map;
-  bool more;
+  float next_upper, next_lower;
+  bool more, next_ready;
+  int tail, used, entry;  // of the ring: where the next stage goes, bytes in use, its barrier
   // working
-  int ahead, worked, stage, pass;  // stages loaded and not worked on; units done; the next stage and its phase
-  int hidden_done;   // units of the first kind done and not yet told
+  int head, ahead, worked, now, pass;  // where the next stage lies, stages loaded, units done, the next stage's barrier and phase
+  int hidden_done;     // units of the first kind done and not yet told
   int owed, owed_row;  // units of the second kind not yet told; lane i: the row of unit i
   bool hidden_ready, ok;
 
@@ -490,61 +524,17 @@ struct Worker {
     n.shared = n.a == s.active;
     n.row = (v - n.a * each) * (n.kind ? 16 : 8);
     n.k = !n.kind ? p.m.H : n.shared ? p.m.Is : p.m.I;
+    n.first = s.first[n.a];
+    n.count = s.first[n.a + 1] - n.first;
     return n;
   }
-  __device__ __forceinline__ void take() {  // the next unit's number, known later
-    if (lane == 0) ticket = atomicAdd(p.counters, 1u);
+  __device__ __forceinline__ int size_of(const Unit& n) const {  // of a stage
+    return n.count > 8 ? kStageBytes : (kStageBytes + n.count * (n.kind + 1) * kRowBytes + 1023) & ~1023;
   }
-  // makes the next unit ready to be loaded
-  __device__ __forceinline__ void prepare_next() {
-    if (next_left || !more) return;
-    next = (int)__shfl_sync(~0u, ticket, 0);
-    if ((unsigned)next >= (unsigned)units) {
-      more = false;
-      return;
-    }
-    take();
-    const Unit n = unit_of(next);
-    const int e = n.shared ? 0 : s.expert[n.a];
-    next_map = n.kind * 2 + n.shared;
-    next_y = n.row;
-    next_z = n.kind ? e : 2 * e;
-    next_left = (n.k + 2 * kPiece - 1) / (2 * kPiece);
-    if (kE4M3) {  // its scales, towards L2
-      const int blocks = (n.k + kBlock - 1) / kBlock;
-      const float *upper, *lower;
-      scales_of(n, upper, lower);
-      if (lane * 8 < blocks) {
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(upper + lane * 8));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(lower + lane * 8));
-      }
-    }
-  }
-  // loads one stage, if there is something to load
-  __device__ __forceinline__ void push() {
-    if (left == 0) {
-      if (next_left == 0) return;
-      if (lane == 0) queue[pushed & 15] = next;
-      ++pushed;
-      map = next_map == 0 ? &p.gate_up : next_map == 1 ? &p.shared_gate_up : next_map == 2 ? &p.down : &p.shared_down;
-      x = 0;
-      y = next_y;
-      z = next_z;
-      left = next_left;
-      next_left = 0;
-    }
-    warp_load(ring + load_stage * kStageBytes, map, x, x + kPiece, y, z, bars + 8 * load_stage);
-    if (++load_stage == kStages) load_stage = 0;
-    ++ahead;
-    x += 2 * kPiece;
-    --left;
-  }
-  __device__ __forceinline__ void fill() {
-    for (;;) {
-      prepare_next();
-      if (ahead == kStages || (left == 0 && next_left == 0)) break;
-      push();
-    }
+  // where token `rank` of the unit has its values
+  __device__ __forceinline__ const uint16_t* values_of(const Unit& n, int rank) const {
+    const size_t row = n.kind == 0 ? s.token[n.first + rank] : 2 * (size_t)(n.shared ? rank : n.first + rank);
+    return (n.kind == 0 ? p.x : n.shared ? p.shared_hidden : p.hidden) + row * pad256(n.k);
   }
   // the scales of a unit's rows by blocks of k: its upper and lower 8
   __device__ __forceinline__ void scales_of(const Unit& n, const float*& upper, const float*& lower) const {
@@ -560,73 +550,130 @@ struct Worker {
       lower = upper + (size_t)rb * kb;
     }
   }
+  __device__ __forceinline__ void take() {  // the next unit's number, known later
+    if (lane == 0) ticket = atomicAdd(p.counters, 1u);
+  }
+  // the unit after the one that is being loaded: its scales are asked for
+  __device__ __forceinline__ void prepare_next() {
+    if (next_ready || !more) return;
+    next = (int)__shfl_sync(~0u, ticket, 0);
+    if ((unsigned)next >= (unsigned)units) {
+      more = false;
+      return;
+    }
+    take();
+    next_ready = true;
+    if (kE4M3) {
+      const Unit n = unit_of(next);
+      const float *upper, *lower;
+      scales_of(n, upper, lower);
+      const bool in = lane < (n.k + kBlock - 1) / kBlock;
+      next_upper = in ? ld_f32(upper + lane) : 0.f;
+      next_lower = in ? ld_f32(lower + lane) : 0.f;
+    }
+  }
+  // goes on to the prepared unit
+  __device__ __forceinline__ void begin_next() {
+    const Unit n = unit_of(next);
+    const int q = pushed % kQueue;
+    if (lane == 0) queue[q] = next;
+    if (kE4M3) {
+      scales[q * 2 * kScales + lane] = next_upper;
+      scales[q * 2 * kScales + kScales + lane] = next_lower;
+    }
+    ++pushed;
+    map = n.kind ? (n.shared ? &p.shared_down : &p.down) : (n.shared ? &p.shared_gate_up : &p.gate_up);
+    const int e = n.shared ? 0 : s.expert[n.a];
+    x = 0;
+    y = n.row;
+    z = n.kind ? e : 2 * e;
+    left = (n.k + kStageK - 1) / kStageK;
+    load_size = size_of(n);
+    load_tokens = n.count > 8 ? 0 : n.count;
+    load_src = lane < load_tokens ? values_of(n, lane) : nullptr;
+    next_ready = false;
+  }
+  // the tokens' values of a stage at `at`: of `count` tokens, from place k on; h in two parts
+  __device__ __forceinline__ void load_values(uint32_t at, const uint16_t* src, int count, int k, int kind, int width, uint32_t bar) {
+    bulk_load_if(at + kStageBytes + lane * kRowBytes, src + k, kRowBytes, bar, lane < count);
+    if (kind) bulk_load_if(at + kStageBytes + (count + lane) * kRowBytes, src + width + k, kRowBytes, bar, lane < count);
+  }
+  // loads stages while there is room and something to load
+  __device__ __forceinline__ void fill() {
+    for (;;) {
+      if (left == 0) {
+        if (!next_ready) return;
+        begin_next();
+        prepare_next();
+      }
+      const int at = tail + load_size > kRing ? 0 : tail, taken = load_size + (at == 0 && tail ? kRing - tail : 0);
+      if (used + taken > kRing) return;
+      const int kind = map == &p.down || map == &p.shared_down;
+      const uint32_t bar = bars + 8 * entry;
+      warp_load(ring + at, map, x, x + kPiece, y, z, bar, kStageBytes + load_tokens * (kind + 1) * kRowBytes);
+      if (load_tokens && (!kind || hidden_ready))
+        load_values(ring + at, load_src, load_tokens, x, kind, pad256(map == &p.shared_down ? p.m.Is : p.m.I), bar);
+      tail = at + load_size;
+      used += taken;
+      if (++entry == kEntries) entry = 0;
+      ++ahead;
+      x += kStageK;
+      --left;
+    }
+  }
+  // The stages that were loaded before h was there get its values.
+  __device__ __forceinline__ void load_late() {
+    int at = head, e = now, w = worked, st = 0;
+    Unit n = unit_of(queue[w % kQueue]);
+    for (int i = 0; i < ahead; ++i) {
+      const int size = size_of(n);
+      if (at + size > kRing) at = 0;
+      if (n.count <= 8)
+        load_values(ring + at, lane < n.count ? values_of(n, lane) : nullptr, n.count, st * kStageK, 1, pad256(n.k), bars + 8 * e);
+      at += size;
+      if (++e == kEntries) e = 0;
+      if (++st == (n.k + kStageK - 1) / kStageK && i + 1 < ahead) {
+        st = 0;
+        n = unit_of(queue[++w % kQueue]);
+      }
+    }
+  }
 
-  // One unit, for an expert of up to 8 kTiles tokens.
-  template <int kKind, int kTiles>
+  // One unit; kFew: of at most 8 tokens, whose values are in the ring, else of up to 64.
+  template <int kKind, bool kFew>
   __device__ __forceinline__ void work(const Unit& n) {
-    const int r = lane >> 2, c = lane & 3, first = s.first[n.a], count = s.first[n.a + 1] - first;
-    const int width = pad256(n.k), count_k = (n.k + 2 * kPiece - 1) / (2 * kPiece);  // stages
+    const int r = lane >> 2, c = lane & 3, width = pad256(n.k), stages = (n.k + kStageK - 1) / kStageK, size = size_of(n);
+    constexpr int kTiles = kFew ? 1 : 8;
     constexpr int kLoads = kE4M3 ? 4 : 2;       // of a lane from a token for a piece, 32 values apart
     constexpr int kParts = kKind == 0 ? 1 : 2;  // h is held in two
     constexpr int kSteps = kE4M3 ? 4 : 2;       // products of a chunk
-    constexpr int kChains = kTiles == 1 ? 2 : 1;  // sums that do not wait for one another
+    constexpr int kChains = kFew ? 2 : 1;       // sums that do not wait for one another
+    const int tiles = kFew ? 1 : (n.count + 7) / 8;
     // this lane's token of each tile (behind the last token: none, and zeroes)
     const uint16_t* src[kTiles];
-    bool there[kTiles];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const int rank = 8 * i + r;
-      there[i] = rank < count;
-      const size_t row = !there[i] ? 0 : kKind == 0 ? s.token[first + rank] : (size_t)2 * (n.shared ? rank : first + rank);
-      src[i] = (kKind == 0 ? p.x : n.shared ? p.shared_hidden : p.hidden) + row * width + c * 8;
-    }
+    for (int i = 0; i < kTiles; ++i) src[i] = 8 * i + r < n.count && !kFew ? values_of(n, 8 * i + r) + c * 8 : nullptr;
     float acc[kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    const float* at_hand = scales + worked % kQueue * 2 * kScales;
     const float *upper = nullptr, *lower = nullptr;
-    float su = 1.f, sl = 1.f;  // lane i: block i's scales, of 32
-    if (kE4M3) scales_of(n, upper, lower);
+    if (kE4M3 && n.k > kScales * kBlock) scales_of(n, upper, lower);
     const uint32_t place0 = r * 128 + ((2 * c ^ r) << 4), place1 = r * 128 + (((2 * c + 1) ^ r) << 4);
-    const uint4 none = make_uint4(0, 0, 0, 0);
-    constexpr bool kAhead = kTiles == 1;  // one tile's values are loaded a stage ahead
-    uint4 b[2][2][kParts][kLoads];
-    auto fetch = [&](uint4(&to)[2][kParts][kLoads], int st) {
-#pragma unroll
-      for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-        for (int h = 0; h < kParts; ++h)
-#pragma unroll
-          for (int q = 0; q < kLoads; ++q)
-            ld_if(to[piece][h][q], src[0] + h * width + (2 * st + piece) * kPiece + q * 32, there[0]);
-    };
-    if (kAhead) {
-#pragma unroll
-      for (int d = 0; d < 2; ++d)
-#pragma unroll
-        for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-          for (int h = 0; h < kParts; ++h)
-#pragma unroll
-            for (int q = 0; q < kLoads; ++q) b[d][piece][h][q] = none;
-      fetch(b[0], 0);
-    }
-    auto step = [&](int st, uint4(&mine)[2][kParts][kLoads], uint4(&other)[2][kParts][kLoads]) {
-      if (kE4M3 && (st & 15) == 0) {
-        const int at = 2 * st + lane, blocks = (n.k + kBlock - 1) / kBlock;
-        su = at < blocks ? ld_f32(upper + at) : 0.f;
-        if (kKind == 0) sl = at < blocks ? ld_f32(lower + at) : 0.f;
-      }
-      if (kAhead && st + 1 < count_k) fetch(other, st + 1);
-      if (!warp_wait(bars + 8 * stage, pass)) {
+    const uint32_t values0 = kStageBytes + r * kRowBytes + c * 16, part_bytes = n.count * kRowBytes;
+#pragma unroll 1
+    for (int st = 0; st < stages; ++st) {
+      if (!warp_wait(bars + 8 * now, pass)) {
         raise_error(p.c.err, kErrTimeout);
         ok = false;
         return;
       }
+      const bool wraps = head + size > kRing;
+      const uint32_t at = ring + (wraps ? 0 : head);
       // rows r and r + 8, chunks 2 c and 2 c + 1 of the swizzled pieces
-      const uint32_t at = ring + stage * kStageBytes;
-      uint4 w[2][2][2];
+      uint4 w[2][2][2], b[2][kParts][kLoads];
 #pragma unroll
       for (int piece = 0; piece < 2; ++piece)
 #pragma unroll
@@ -634,10 +681,20 @@ struct Worker {
           w[piece][0][h] = lds128(at + piece * 2048 + h * 1024 + place0);
           w[piece][1][h] = lds128(at + piece * 2048 + h * 1024 + place1);
         }
-      if (++stage == kStages) stage = 0, pass ^= 1;
+      if (kFew)
+#pragma unroll
+        for (int piece = 0; piece < 2; ++piece)
+#pragma unroll
+          for (int h = 0; h < kParts; ++h)
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q)
+              b[piece][h][q] = lds128_if(at + values0 + h * part_bytes + piece * (kRowBytes / 2) + q * 64, r < n.count);
+      used -= size + (wraps ? kRing - head : 0);
+      head = (wraps ? 0 : head) + size;
+      if (++now == kEntries) now = 0, pass ^= 1;
       --ahead;
       __syncwarp();
-      push();
+      fill();
 #pragma unroll
       for (int piece = 0; piece < 2; ++piece) {
         float part[kChains][kTiles][4];
@@ -660,14 +717,15 @@ struct Worker {
             }
           }
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i)
+          for (int i = 0; i < kTiles; ++i) {
+            if (!kFew && i >= tiles) break;
 #pragma unroll
             for (int h = 0; h < kParts; ++h)
 #pragma unroll
               for (int g = 0; g < kLoads / 2; ++g) {
-                uint4 v = none;
-                if (kAhead) v = mine[piece][h][j * (kLoads / 2) + g];
-                else ld_if(v, src[i] + h * width + (2 * st + piece) * kPiece + (j * (kLoads / 2) + g) * 32, there[i]);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (kFew) v = b[piece][h][j * (kLoads / 2) + g];
+                else if (src[i]) v = ld_here(src[i] + h * width + (2 * st + piece) * kPiece + (j * (kLoads / 2) + g) * 32);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                   const int nth = ((j * kParts + h) * (kLoads / 2) + g) * 2 + q;
@@ -677,37 +735,43 @@ struct Worker {
                   else mma_16816<kE4M3 && kKind == 0, false>(d, a0, a1, q ? v.z : v.x, q ? v.w : v.y);
                 }
               }
+          }
         }
         // a piece is summed by itself, then scaled
-        const int block = 2 * st + piece & 31;
-        const float fu = kE4M3 ? __shfl_sync(~0u, su, block) : 1.f;
-        const float fl = !kE4M3 ? 1.f : kKind == 0 ? __shfl_sync(~0u, sl, block) : fu;
+        const int block = 2 * st + piece;
+        float fu = 1.f, fl = 1.f;
+        if (kE4M3) {
+          const bool here = block < kScales;
+          if (here || block * kBlock < n.k) {
+            fu = here ? at_hand[block] : ld_f32(upper + block);
+            fl = kKind == 1 ? fu : here ? at_hand[kScales + block] : ld_f32(lower + block);
+          } else {
+            fu = fl = 0.f;
+          }
+        }
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i)
+        for (int i = 0; i < kTiles; ++i) {
+          if (!kFew && i >= tiles) break;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float d = part[0][i][j];
             if (kChains > 1) d += part[kChains - 1][i][j];
             acc[i][j] = fmaf(d, j < 2 ? fu : fl, acc[i][j]);
           }
+        }
       }
-    };
-#pragma unroll 1
-    for (int st = 0; st < count_k && ok; st += 2) {
-      step(st, b[0], b[1]);
-      if (st + 1 < count_k && ok) step(st + 1, b[1], b[0]);
     }
-    if (!ok) return;
     if constexpr (kKind == 0) {  // silu(gate) * up for places row + r, tokens 8 i + 2 c and the next
       uint16_t* hidden = n.shared ? p.shared_hidden : p.hidden;
-      const int base = n.shared ? 0 : first, wide = pad256(n.shared ? p.m.Is : p.m.I), at = place<kE4M3>(n.row) + r;
+      const int base = n.shared ? 0 : n.first, wide = pad256(n.shared ? p.m.Is : p.m.I), at = place<kE4M3>(n.row) + r;
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
+      for (int i = 0; i < kTiles; ++i) {
+        if (!kFew && i >= tiles) break;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int rank = 8 * i + 2 * c + j;
-          if (rank >= count) continue;
-          const float xs = kE4M3 ? s.x_scale[s.token[first + rank]] : 1.f, g = acc[i][j] * xs, u = acc[i][2 + j] * xs;
+          if (rank >= n.count) continue;
+          const float xs = kE4M3 ? s.x_scale[s.token[n.first + rank]] : 1.f, g = acc[i][j] * xs, u = acc[i][2 + j] * xs;
           const float h = g / (1.f + expf(-g)) * u;
           const uint16_t hi = f2bf(h);
           uint16_t* to = hidden + (size_t)(base + rank) * 2 * wide + at;
@@ -715,25 +779,30 @@ struct Worker {
           // what the first part lost; nothing where it is not finite
           to[wide] = (hi & 0x7F80u) == 0x7F80u ? 0 : f2bf(h - bf2f(hi));
         }
+      }
       ++hidden_done;
     } else {  // rows row + r and row + 8 + r
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
+      for (int i = 0; i < kTiles; ++i) {
+        if (!kFew && i >= tiles) break;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int rank = 8 * i + 2 * c + (j & 1);
-          if (rank < count)
-            p.y[(size_t)(first + rank) * p.m.H + n.row + (j >> 1) * 8 + r] = acc[i][j] * s.weight[first + rank];
+          if (rank < n.count)
+            p.y[(size_t)(n.first + rank) * p.m.H + n.row + (j >> 1) * 8 + r] = acc[i][j] * s.weight[n.first + rank];
         }
+      }
       if (lane == owed) owed_row = n.row;
       ++owed;
     }
   }
 
-  // A fence waits for the stores before it: what units wrote is made known several units at a time.
+  // A fence waits for the stores before it: what units wrote is made known several units at a time.  h goes to copies.
   __device__ __forceinline__ void tell_hidden() {
+    if (!hidden_done) return;
+    asm volatile("fence.proxy.async.global;" ::: "memory");
     __syncwarp();
-    if (lane == 0 && hidden_done) {
+    if (lane == 0) {
       __threadfence();
       atomicAdd(p.counters + 1, (unsigned)hidden_done);
     }
@@ -774,21 +843,12 @@ struct Worker {
     }
   }
 
-  template <int kKind>
-  __device__ __forceinline__ void work_any(const Unit& n) {
-    const int tiles = (s.first[n.a + 1] - s.first[n.a] + 7) / 8;
-    if (tiles == 1) work<kKind, 1>(n);
-    else if (tiles == 2) work<kKind, 2>(n);
-    else if (tiles <= 4) work<kKind, 4>(n);
-    else work<kKind, 8>(n);
-  }
-
   __device__ __forceinline__ void run() {
+    prepare_next();
     fill();
     for (worked = 0; ok && worked != pushed; ++worked) {
       __syncwarp();
-      const Unit n = unit_of(queue[worked & 15]);
-      __syncwarp();
+      const Unit n = unit_of(queue[worked % kQueue]);
       if (n.kind && !hidden_ready) {  // every unit of the first kind is in the hands of a warp that waits for nothing
         tell_hidden();
         for (uint32_t i = 0; ok; ++i) {
@@ -801,53 +861,70 @@ struct Worker {
           __nanosleep(32);
         }
         hidden_ready = true;
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        load_late();
         if (!ok) break;
       }
-      if (n.kind) work_any<1>(n);
-      else work_any<0>(n);
+      if (n.kind == 0) {
+        if (n.count <= 8) work<0, true>(n);
+        else work<0, false>(n);
+      } else {
+        if (n.count <= 8) work<1, true>(n);
+        else work<1, false>(n);
+      }
       if (owed == kOwed) tell_rows();
+      prepare_next();
       fill();
     }
     tell_hidden();
     tell_rows();
+    if (!ok && !hidden_ready) load_late();  // a stage that lacks its values would never be full
     // copies in flight land before the CTA ends, after a wait that ran out too
     for (; ahead; --ahead) {
-      warp_wait(bars + 8 * stage, pass);
-      if (++stage == kStages) stage = 0, pass ^= 1;
+      warp_wait(bars + 8 * now, pass);
+      if (++now == kEntries) now = 0, pass ^= 1;
     }
   }
 };
 
-constexpr size_t kSmem = 1024 + (size_t)kWarps * kStages * kStageBytes + sizeof(Lists) + kWarps * (16 * 4 + kStages * 8) + 64;
+struct Rings {  // behind the warps' stages
+  Lists lists;
+  uint64_t bars[kWarps][kEntries];
+  int queues[kWarps][kQueue];
+};
+constexpr size_t kSmem = 1024 + (size_t)kWarps * kRing + sizeof(Rings);
+static_assert(kSmem <= 232448, "");
+static_assert(kRing / kStageBytes < kEntries && kRing / kStageBytes < kQueue, "");
 
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  constexpr int kRing = kStages * kStageBytes;
-  Lists& s = *reinterpret_cast<Lists*>(smem + kWarps * kRing);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uintptr_t>(smem + kWarps * kRing + sizeof(Lists) + 15) & ~(uintptr_t)15);
-  int* queues = reinterpret_cast<int*>(bars + kWarps * kStages);
+  Rings& rings = *reinterpret_cast<Rings*>(smem + kWarps * kRing);
+  Lists& s = rings.lists;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x < kWarps * kStages) mbar_init(smem_u32(bars + threadIdx.x), 1);
+  if (threadIdx.x < kWarps * kEntries) mbar_init(smem_u32(&rings.bars[0][0] + threadIdx.x), 1);
   if (threadIdx.x == 0) {
     prefetch_tensormap(&p.gate_up);
     prefetch_tensormap(&p.down);
   }
   fence_mbar_init();
   await_grid();
-  Worker<kE4M3> w = {p, s, lane, smem_u32(smem + warp * kRing), smem_u32(bars + warp * kStages), queues + warp * 16};
+  asm volatile("fence.proxy.async.global;" ::: "memory");  // tokens are read by copies
+  Worker<kE4M3> w = {p, s, lane, smem_u32(smem + warp * kRing), smem_u32(rings.bars[warp]), rings.queues[warp], s.scales[warp]};
   w.take();
   make_lists(p, s);
   w.hidden_units = p.m.I / 8;
   w.out_units = p.m.H / 16;
   w.units_a = s.active * w.hidden_units + p.m.Is / 8;
   w.units = w.units_a + (s.active + (p.m.Is ? 1 : 0)) * w.out_units;
-  w.pushed = w.load_stage = w.left = w.x = w.y = w.z = w.next = w.next_left = w.next_y = w.next_z = w.next_map = 0;
-  w.ahead = w.worked = w.stage = w.pass = w.hidden_done = w.owed = w.owed_row = 0;
+  w.pushed = w.left = w.x = w.y = w.z = w.load_size = w.load_tokens = w.next = w.tail = w.used = w.entry = 0;
+  w.head = w.ahead = w.worked = w.now = w.pass = w.hidden_done = w.owed = w.owed_row = 0;
+  w.load_src = nullptr;
   w.map = nullptr;
+  w.next_upper = w.next_lower = 0.f;
   w.more = w.ok = true;
-  w.hidden_ready = false;
+  w.next_ready = w.hidden_ready = false;
   if (w.units == 0) {  // no token has an expert
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.c.T * p.m.H / 8; i += gridDim.x * kThreads)
       reinterpret_cast<uint4*>(p.c.out)[i] = make_uint4(0, 0, 0, 0);
