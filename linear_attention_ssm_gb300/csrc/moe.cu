@@ -25,12 +25,12 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kTeams = 8, kWarps = 2 * kTeams, kThreads = kWarps * 32;  // two warps share a ring
 constexpr int kMaxTokens = 64, kMaxTopK = 16, kMaxExperts = 1024;
 constexpr int kMaxSlots = kMaxTokens * (kMaxTopK + 1);  // (token, expert) pairs
-constexpr int kStageBytes = 4096;  // of weights: 16 rows of two pieces of 128 bytes
-constexpr int kRing = 24576;       // of a warp
-constexpr int kEntries = 8;        // barriers of a ring: more than stages fit
+constexpr int kStageBytes = 4096;  // of weights: 32 rows of 128 bytes
+constexpr int kRing = 24576;       // of a team: 4 stages with 2 KB of values, or 3 with 4 KB
+constexpr int kStages = 4;
 constexpr int kQueue = 8;          // units on their way: more than stages fit, and the one in hand
 constexpr int kScales = 32;        // of a unit's scales of either kind, as many blocks as are kept at hand
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before giving up
@@ -56,7 +56,7 @@ Layout layout(const Moe& m, int T, int k) {
 }
 
 struct MoeParams {
-  CUtensorMap gate_up, down, shared_gate_up, shared_down;  // boxes of 128 bytes x 8 rows x 2 halves, or x 16 rows x 1
+  CUtensorMap gate_up, down, shared_gate_up, shared_down;  // boxes of 128 bytes x 16 rows x 2 halves, or x 32 rows x 1
   Moe m;
   MoeCall c;
   unsigned* counters;  // next unit; first units done; for each 16 rows of the output, down units done
@@ -217,12 +217,13 @@ struct Lists {
       uint16_t index[kMaxExperts];                   // the active expert's number
       int16_t chosen[kMaxTokens][kMaxTopK];          // negative: none
     };
-    float scales[kWarps][kQueue * 2 * kScales];      // then: of the units on their way
+    float scales[kTeams][kQueue * 2 * kScales];      // then: of the units on their way
   };
   float weight[kMaxSlots];
   float x_scale[kMaxTokens];
   uint32_t sums[kWarps];
   int active;                       // experts that have tokens
+  int most;                         // tokens of one, among those of up to 8
   uint16_t expert[kMaxExperts];     // of an active expert
   uint16_t first[kMaxExperts + 2];  // its first slot
   uint16_t slot_of[kMaxTokens][kMaxTopK + 1];  // kNone: none; the shared expert's last
@@ -302,6 +303,7 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
   constexpr int kPass = kThreads / kMaxTopK;  // tokens at a time, a thread for each of their choices
   const int j = tid % kMaxTopK, t0 = tid / kMaxTopK;
   for (int e = tid; e < E; e += kThreads) s.mask[e] = 0;
+  if (tid == 0) s.most = p.m.Is && T <= 8 ? T : 0;
   if (tid < T) s.x_scale[tid] = ld_f32(p.x_scale + tid);
   if (p.c.ids_in) {
     for (int t = t0; t < T && j < k; t += kPass) {
@@ -328,18 +330,23 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
   __syncthreads();
   // experts that have tokens, in order: each thread has some neighbours; experts above, slots below in a word
   constexpr int kOwn = (kMaxExperts + kThreads - 1) / kThreads;
-  uint32_t own = 0;
+  uint32_t own = 0, most = 0;
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
     const int e = tid * kOwn + i, n = e < E ? __popcll(s.mask[e]) : 0;
     own += n ? 0x10000u + n : 0;
+    if (n <= 8) most = max(most, (uint32_t)n);
   }
   uint32_t before = own;
   for (int o = 1; o < 32; o <<= 1) {
     const uint32_t x = __shfl_up_sync(~0u, before, o);
     if (lane >= o) before += x;
   }
-  if (lane == 31) s.sums[warp] = before;
+  most = __reduce_max_sync(~0u, most);
+  if (lane == 31) {
+    s.sums[warp] = before;
+    if (most) atomicMax(&s.most, (int)most);
+  }
   __syncthreads();
   uint32_t all = 0;
   before -= own;
@@ -417,23 +424,20 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint2& upper, con
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(upper.x), "r"(lower.x), "r"(upper.y), "r"(lower.y), "r"(b0), "r"(b1));
 }
-// 16 bytes where `there`, else what v holds
-__device__ __forceinline__ void ld_if(uint4& v, const void* p, bool there) {
-  asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\n@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-               : "l"(p), "r"((int)there));
-}
-
-// Four finite e4m3 codes -> two pairs of bf16, low codes first: the code's exponent and significand at their places of a
-// bf16 stand for its value times 2^-120, subnormals too, and the product with 2^120 is exact.
+// Four finite e4m3 codes -> pairs of bf16, codes 0 and 2, then 1 and 3: the code's exponent and significand at their places
+// of a bf16 stand for its value times 2^-120, subnormals too, and the product with 2^120 is exact.
 __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t v) {
-  auto two = [](uint32_t p) {
-    const uint32_t r = (p >> 4 & 0x07F007F0u) | (p & 0x80008000u);
+  auto scaled = [](uint32_t r) {
     const __nv_bfloat162 up = __nv_bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));
     const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r), up);
     return *reinterpret_cast<const uint32_t*>(&y);
   };
-  return make_uint2(two(__byte_perm(v, 0, 0x1404)), two(__byte_perm(v, 0, 0x3424)));
+  return make_uint2(scaled((v * 16 & 0x07F007F0u) | (v * 256 & 0x80008000u)), scaled((v >> 4 & 0x07F007F0u) | (v & 0x80008000u)));
+}
+// where the products' order of h has the i-th of 8 places
+template <bool kE4M3>
+__device__ __forceinline__ int place_of_8(int i) {
+  return kE4M3 ? (i & 4) | (i & 1) << 1 | (i >> 1 & 1) : i;
 }
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
@@ -447,89 +451,91 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   }
   return false;
 }
-// a stage's two loads of weights, by one lane of the warp; `bytes` in all are counted by the barrier
-__device__ __forceinline__ void warp_load(uint32_t dst, const void* map, int x0, int x1, int y, int z, uint32_t bar,
-                                          uint32_t bytes) {
+// A stage's load of weights, by one lane of the warp.
+__device__ __forceinline__ void warp_load(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
-      "{\n.reg .pred e;\n.reg .b32 d;\n"
+      "{\n.reg .pred e;\n"
       "elect.sync _|e, 0xFFFFFFFF;\n"
-      "add.s32 d, %2, 2048;\n"
-      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], [%3, {%4, %6, %7}], [%0];\n"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [d], [%3, {%5, %6, %7}], [%0];\n"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %6;\n"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%1], [%2, {%3, %4, %5}], [%0];\n"
       "}" ::"r"(bar),
-      "r"(bytes), "r"(dst), "l"(map), "r"(x0), "r"(x1), "r"(y), "r"(z)
+      "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "n"(kStageBytes)
       : "memory");
 }
-__device__ __forceinline__ void bulk_load_if(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, bool mine) {
+__device__ __forceinline__ void copy_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// every lane's: its copies up to here have landed
+__device__ __forceinline__ void copies_done_to(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+// both warps of a team have come here, and whether both are `ok`
+__device__ __forceinline__ bool team_sync(int team, bool ok) {
+  uint32_t both;
   asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}" ::"r"(dst),
-      "l"(src), "r"(bytes), "r"(bar), "r"((int)mine)
+      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %2, 0;\nbarrier.cta.red.and.pred q, %1, 64, p;\nselp.u32 %0, 1, 0, q;\n}"
+      : "=r"(both)
+      : "r"(team + 1), "r"((int)ok)
       : "memory");
-}
-// 16 bytes of shared memory where `there`, else zeroes
-__device__ __forceinline__ uint4 lds128_if(uint32_t addr, bool there) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\n@q ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
-               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-               : "r"(addr), "r"((int)there)
-               : "memory");
-  return v;
+  return both;
 }
 
 // A unit of work.
 struct Unit {
-  int kind;            // 0: 8 rows of gate and up, 1: 16 rows of down
+  int kind;            // 0: 16 rows of gate and up, 1: 32 rows of down
   int a;               // the active expert, `active` for the shared one
   bool shared;
   int row, k;          // first row; length of a row
   int first, count;    // the expert's slots
 };
 
-// A warp.  A stage of its ring has 4 KB of weights and behind them, for an expert of up to 8 tokens, the tokens' values for
-// the same k (loads through the cache take several thousand cycles while the copies fill the memory's queues).
+// A warp of a team of two.  A stage of their ring has 4 KB of weights and behind them, for an expert of up to 8 tokens, the
+// tokens' values for the same k (loads through the cache take several thousand cycles while the copies fill the memory's
+// queues).  Each warp has the products of half of a stage's rows; the first one loads.
 template <bool kE4M3>
 struct Worker {
-  static constexpr int kPiece = kE4M3 ? 128 : 64;  // values of a 128-byte piece of a row
-  static constexpr int kStageK = 2 * kPiece;       // of a stage
-  static constexpr int kRowBytes = 2 * kStageK;    // of a token in a stage
+  static constexpr int kStageK = kE4M3 ? 128 : 64;  // of a stage
+  static constexpr int kRowBytes = 2 * kStageK;     // of a token in a stage
   const MoeParams& p;
   Lists& s;
-  const int lane;
-  const uint32_t ring, bars;  // this warp's stages and barriers
+  const int lane, team, half;
+  const uint32_t ring, bars;  // the team's stages and barriers
   int* queue;                 // units on their way
   float* scales;              // theirs: [kQueue][2][kScales]
+  int halves_a;               // halves of units of the first kind that have rows
   int units_a, units;         // of the first kind, of both
-  int hidden_units, out_units;  // units of an expert of either kind
+  int stages;                 // of the ring
+  uint32_t stage_bytes;
+  int hidden_units, out_units, shared_units;  // units of an expert of either kind; of the shared one's first kind
   // loading: the unit that is being loaded, and the one after it
   unsigned ticket;
-  int pushed, left, x, y, z, load_size, load_tokens, next;
-  const uint16_t* load_src;  // lane i: token i's values
+  int pushed, left, x, z, next, pieces;  // 16-byte pieces of values of a stage
+  uint32_t first_to;       // where this lane's first one goes in a stage
+  const uint16_t* values;  // and where from; the unit's values
   const void* map;
+  Unit load;
   float next_upper, next_lower;
   bool more, next_ready;
-  int tail, used, entry;  // of the ring: where the next stage goes, bytes in use, its barrier
+  int slot;                   // the next stage to load
   // working
-  int head, ahead, worked, now, pass;  // where the next stage lies, stages loaded, units done, the next stage's barrier and phase
+  int ahead, worked, now, pass;  // stages loaded, units done, the next stage and its phase
+  int stopped;         // after a wait that ran out: stages done of the unit in hand
   int hidden_done;     // units of the first kind done and not yet told
   int owed, owed_row;  // units of the second kind not yet told; lane i: the row of unit i
   bool hidden_ready, ok;
 
-  __device__ __forceinline__ Unit unit_of(int u) const {
+  __device__ __forceinline__ Unit unit_of(int u) const {  // the shared expert's are first: they take longest
     Unit n;
     n.kind = u >= units_a;
-    const int v = n.kind ? u - units_a : u, each = n.kind ? out_units : hidden_units;
-    n.a = min((unsigned)v / (unsigned)each, (unsigned)s.active);
-    n.shared = n.a == s.active;
-    n.row = (v - n.a * each) * (n.kind ? 16 : 8);
+    const int each = n.kind ? out_units : hidden_units, ahead_of = p.m.Is ? (n.kind ? out_units : shared_units) : 0;
+    const int v = (n.kind ? u - units_a : u) - ahead_of;
+    n.shared = v < 0;
+    n.a = n.shared ? s.active : (unsigned)v / (unsigned)each;
+    n.row = (n.shared ? v + ahead_of : v - n.a * each) * (n.kind ? 32 : 16);
     n.k = !n.kind ? p.m.H : n.shared ? p.m.Is : p.m.I;
     n.first = s.first[n.a];
     n.count = s.first[n.a + 1] - n.first;
     return n;
-  }
-  __device__ __forceinline__ int size_of(const Unit& n) const {  // of a stage
-    return n.count > 8 ? kStageBytes : (kStageBytes + n.count * (n.kind + 1) * kRowBytes + 1023) & ~1023;
   }
   // where token `rank` of the unit has its values
   __device__ __forceinline__ const uint16_t* values_of(const Unit& n, int rank) const {
@@ -572,6 +578,15 @@ struct Worker {
       next_lower = in ? ld_f32(lower + lane) : 0.f;
     }
   }
+  // the unit whose values are loaded
+  __device__ __forceinline__ void aim(const Unit& n) {
+    load = n;
+    constexpr int kPieces = kRowBytes / 16;
+    const int i = lane / kPieces, piece = lane % kPieces, width = pad256(n.k);
+    pieces = n.count > 8 ? 0 : n.count * (n.kind + 1) * kPieces;
+    first_to = kStageBytes + i * kRowBytes + ((piece ^ (n.kind ? i & 2 : (i & 1) << 1) << 1) << 4);
+    if (lane < pieces) values = (n.kind ? values_of(n, 0) + (size_t)i * width : values_of(n, i)) + piece * 8;
+  }
   // goes on to the prepared unit
   __device__ __forceinline__ void begin_next() {
     const Unit n = unit_of(next);
@@ -582,40 +597,43 @@ struct Worker {
       scales[q * 2 * kScales + kScales + lane] = next_lower;
     }
     ++pushed;
-    map = n.kind ? (n.shared ? &p.shared_down : &p.down) : (n.shared ? &p.shared_gate_up : &p.gate_up);
     const int e = n.shared ? 0 : s.expert[n.a];
     x = 0;
-    y = n.row;
     z = n.kind ? e : 2 * e;
     left = (n.k + kStageK - 1) / kStageK;
-    load_size = size_of(n);
-    load_tokens = n.count > 8 ? 0 : n.count;
-    load_src = lane < load_tokens ? values_of(n, lane) : nullptr;
+    aim(n);
+    map = n.kind ? (n.shared ? &p.shared_down : &p.down) : (n.shared ? &p.shared_gate_up : &p.gate_up);
     next_ready = false;
   }
-  // the tokens' values of a stage at `at`: of `count` tokens, from place k on; h in two parts
-  __device__ __forceinline__ void load_values(uint32_t at, const uint16_t* src, int count, int k, int kind, int width, uint32_t bar) {
-    bulk_load_if(at + kStageBytes + lane * kRowBytes, src + k, kRowBytes, bar, lane < count);
-    if (kind) bulk_load_if(at + kStageBytes + (count + lane) * kRowBytes, src + width + k, kRowBytes, bar, lane < count);
+  // The tokens' values of a stage: rows of 16-byte pieces, pieces 4 apart swapped for odd tokens (a quarter warp reads 4 pieces
+  // of two tokens); h in two parts.
+  __device__ __forceinline__ void load_values(uint32_t at, int k, uint32_t bar) {
+    if (lane < pieces) copy_16(at + first_to, values + k);
+    if (pieces > 32) {
+      constexpr int kPieces = kRowBytes / 16;
+      const int piece = lane % kPieces, width = pad256(load.k);
+#pragma unroll 1
+      for (int q = lane + 32; q < pieces; q += 32) {
+        const int i = q / kPieces, swap = load.kind ? i & 2 : (i & 1) << 1;
+        const uint16_t* from = load.kind ? values + (size_t)(i - lane / kPieces) * width : values_of(load, i) + piece * 8;
+        copy_16(at + kStageBytes + i * kRowBytes + ((piece ^ swap << 1) << 4), from + k);
+      }
+    }
+    copies_done_to(bar);
   }
   // loads stages while there is room and something to load
   __device__ __forceinline__ void fill() {
-    for (;;) {
+    while (ahead < stages) {
       if (left == 0) {
         if (!next_ready) return;
         begin_next();
         prepare_next();
       }
-      const int at = tail + load_size > kRing ? 0 : tail, taken = load_size + (at == 0 && tail ? kRing - tail : 0);
-      if (used + taken > kRing) return;
-      const int kind = map == &p.down || map == &p.shared_down;
-      const uint32_t bar = bars + 8 * entry;
-      warp_load(ring + at, map, x, x + kPiece, y, z, bar, kStageBytes + load_tokens * (kind + 1) * kRowBytes);
-      if (load_tokens && (!kind || hidden_ready))
-        load_values(ring + at, load_src, load_tokens, x, kind, pad256(map == &p.shared_down ? p.m.Is : p.m.I), bar);
-      tail = at + load_size;
-      used += taken;
-      if (++entry == kEntries) entry = 0;
+      const uint32_t bar = bars + 8 * slot, at = ring + slot * stage_bytes;
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // values that lay there came by plain copies
+      warp_load(at, map, x, load.row, z, bar);
+      if (load.kind == 0 || hidden_ready) load_values(at, x, bar);
+      if (++slot == stages) slot = 0;
       ++ahead;
       x += kStageK;
       --left;
@@ -623,36 +641,30 @@ struct Worker {
   }
   // The stages that were loaded before h was there get its values.
   __device__ __forceinline__ void load_late() {
-    int at = head, e = now, w = worked, st = 0;
-    Unit n = unit_of(queue[w % kQueue]);
+    const Unit loading = load;
+    int e = now, w = worked, st = stopped;
     for (int i = 0; i < ahead; ++i) {
-      const int size = size_of(n);
-      if (at + size > kRing) at = 0;
-      if (n.count <= 8)
-        load_values(ring + at, lane < n.count ? values_of(n, lane) : nullptr, n.count, st * kStageK, 1, pad256(n.k), bars + 8 * e);
-      at += size;
-      if (++e == kEntries) e = 0;
-      if (++st == (n.k + kStageK - 1) / kStageK && i + 1 < ahead) {
-        st = 0;
-        n = unit_of(queue[++w % kQueue]);
+      if (i == 0 || st == (load.k + kStageK - 1) / kStageK) {
+        if (i) st = 0, ++w;
+        aim(unit_of(queue[w % kQueue]));
       }
+      if (load.kind) load_values(ring + e * stage_bytes, st * kStageK, bars + 8 * e);
+      if (++e == stages) e = 0;
+      ++st;
     }
+    aim(loading);
   }
 
   // One unit; kFew: of at most 8 tokens, whose values are in the ring, else of up to 64.
   template <int kKind, bool kFew>
   __device__ __forceinline__ void work(const Unit& n) {
-    const int r = lane >> 2, c = lane & 3, width = pad256(n.k), stages = (n.k + kStageK - 1) / kStageK, size = size_of(n);
+    const int r = lane >> 2, c = lane & 3, width = pad256(n.k), steps = (n.k + kStageK - 1) / kStageK;
     constexpr int kTiles = kFew ? 1 : 8;
     constexpr int kLoads = kE4M3 ? 4 : 2;       // of a lane from a token for a piece, 32 values apart
     constexpr int kParts = kKind == 0 ? 1 : 2;  // h is held in two
     constexpr int kSteps = kE4M3 ? 4 : 2;       // products of a chunk
     constexpr int kChains = kFew ? 2 : 1;       // sums that do not wait for one another
     const int tiles = kFew ? 1 : (n.count + 7) / 8;
-    // this lane's token of each tile (behind the last token: none, and zeroes)
-    const uint16_t* src[kTiles];
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) src[i] = 8 * i + r < n.count && !kFew ? values_of(n, 8 * i + r) + c * 8 : nullptr;
     float acc[kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
@@ -661,146 +673,134 @@ struct Worker {
     const float* at_hand = scales + worked % kQueue * 2 * kScales;
     const float *upper = nullptr, *lower = nullptr;
     if (kE4M3 && n.k > kScales * kBlock) scales_of(n, upper, lower);
-    const uint32_t place0 = r * 128 + ((2 * c ^ r) << 4), place1 = r * 128 + (((2 * c + 1) ^ r) << 4);
-    const uint32_t values0 = kStageBytes + r * kRowBytes + c * 16, part_bytes = n.count * kRowBytes;
+    const uint32_t rows = half * (kKind == 0 ? 1024 : 2048) + r * 128, apart = kKind == 0 ? 2048 : 1024;
+    const uint32_t place0 = rows + ((2 * c ^ r) << 4), place1 = rows + (((2 * c + 1) ^ r) << 4);
+    // columns behind the last token repeat it, and are not stored
+    const int rank = min(r, n.count - 1);
+    const uint32_t values0 = kStageBytes + rank * kParts * kRowBytes + c * 16 + (rank & 1) * 64;
 #pragma unroll 1
-    for (int st = 0; st < stages; ++st) {
+    for (int st = 0; st < steps; ++st) {
       if (!warp_wait(bars + 8 * now, pass)) {
         raise_error(p.c.err, kErrTimeout);
         ok = false;
-        return;
       }
-      const bool wraps = head + size > kRing;
-      const uint32_t at = ring + (wraps ? 0 : head);
-      // rows r and r + 8, chunks 2 c and 2 c + 1 of the swizzled pieces
-      uint4 w[2][2][2], b[2][kParts][kLoads];
+      const uint32_t at = ring + now * stage_bytes;
+      // rows r and r + 8, chunks 2 c and 2 c + 1, swizzled
+      uint4 w[2][2], b[kParts][kLoads];
 #pragma unroll
-      for (int piece = 0; piece < 2; ++piece)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          w[piece][0][h] = lds128(at + piece * 2048 + h * 1024 + place0);
-          w[piece][1][h] = lds128(at + piece * 2048 + h * 1024 + place1);
-        }
+      for (int h = 0; h < 2; ++h) {
+        w[0][h] = lds128(at + h * apart + place0);
+        w[1][h] = lds128(at + h * apart + place1);
+      }
       if (kFew)
 #pragma unroll
-        for (int piece = 0; piece < 2; ++piece)
+        for (int h = 0; h < kParts; ++h)
+#pragma unroll
+          for (int q = 0; q < kLoads; ++q) b[h][q] = lds128((at + values0 + h * kRowBytes) ^ q * 64);
+      ok = team_sync(team, ok);
+      if (!ok) {
+        stopped = st;
+        return;
+      }
+      if (++now == stages) now = 0, pass ^= 1;
+      --ahead;
+      if (half == 0) fill();
+      float fu = 1.f, fl = 1.f;
+      if (kE4M3) {
+        const bool here = st < kScales;
+        fu = here ? at_hand[st] : ld_f32(upper + st);
+        fl = kKind == 1 ? fu : here ? at_hand[kScales + st] : ld_f32(lower + st);
+      }
+      uint2 a[2][kSteps][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t u[4] = {w[j][h].x, w[j][h].y, w[j][h].z, w[j][h].w};
+#pragma unroll
+          for (int q = 0; q < kSteps; ++q) {
+            if constexpr (!kE4M3) a[j][q][h] = make_uint2(u[2 * q], u[2 * q + 1]);
+            else if constexpr (kKind == 0) a[j][q][h] = e4m3x4_to_half4(u[q]);
+            else a[j][q][h] = e4m3x4_to_bf16x4(u[q]);
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) {
+        if (!kFew && i >= tiles) break;
+        if (!kFew) {
+          const uint16_t* src = values_of(n, min(8 * i + r, n.count - 1)) + c * 8 + st * kStageK;
 #pragma unroll
           for (int h = 0; h < kParts; ++h)
 #pragma unroll
-            for (int q = 0; q < kLoads; ++q)
-              b[piece][h][q] = lds128_if(at + values0 + h * part_bytes + piece * (kRowBytes / 2) + q * 64, r < n.count);
-      used -= size + (wraps ? kRing - head : 0);
-      head = (wraps ? 0 : head) + size;
-      if (++now == kEntries) now = 0, pass ^= 1;
-      --ahead;
-      __syncwarp();
-      fill();
+            for (int q = 0; q < kLoads; ++q) b[h][q] = ld_here(src + h * width + q * 32);
+        }
+        float part[kChains][4];
+        int nth = 0;
 #pragma unroll
-      for (int piece = 0; piece < 2; ++piece) {
-        float part[kChains][kTiles][4];
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint4 &up = w[piece][j][0], &low = w[piece][j][1];
-          const uint32_t u[4] = {up.x, up.y, up.z, up.w}, l[4] = {low.x, low.y, low.z, low.w};
-          uint2 fu[kSteps], fl[kSteps];
+          for (int h = 0; h < kParts; ++h)
 #pragma unroll
-          for (int q = 0; q < kSteps; ++q) {
-            if constexpr (!kE4M3) {
-              fu[q] = make_uint2(u[2 * q], u[2 * q + 1]);
-              fl[q] = make_uint2(l[2 * q], l[2 * q + 1]);
-            } else if constexpr (kKind == 0) {
-              fu[q] = e4m3x4_to_half4(u[q]);
-              fl[q] = e4m3x4_to_half4(l[q]);
-            } else {
-              fu[q] = e4m3x4_to_bf16x4(u[q]);
-              fl[q] = e4m3x4_to_bf16x4(l[q]);
+            for (int q = 0; q < kSteps; ++q, ++nth) {
+              const uint4& v = b[h][j * (kLoads / 2) + q / 2];
+              if (nth < kChains) mma_16816<kE4M3 && kKind == 0, true>(part[nth % kChains], a[j][q][0], a[j][q][1], q & 1 ? v.z : v.x, q & 1 ? v.w : v.y);
+              else mma_16816<kE4M3 && kKind == 0, false>(part[nth % kChains], a[j][q][0], a[j][q][1], q & 1 ? v.z : v.x, q & 1 ? v.w : v.y);
             }
-          }
+        // a block of k is summed by itself, then scaled
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i) {
-            if (!kFew && i >= tiles) break;
-#pragma unroll
-            for (int h = 0; h < kParts; ++h)
-#pragma unroll
-              for (int g = 0; g < kLoads / 2; ++g) {
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (kFew) v = b[piece][h][j * (kLoads / 2) + g];
-                else if (src[i]) v = ld_here(src[i] + h * width + (2 * st + piece) * kPiece + (j * (kLoads / 2) + g) * 32);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const int nth = ((j * kParts + h) * (kLoads / 2) + g) * 2 + q;
-                  float(&d)[4] = part[nth % kChains][i];
-                  const uint2 &a0 = fu[2 * g + q], &a1 = fl[2 * g + q];
-                  if (nth < kChains) mma_16816<kE4M3 && kKind == 0, true>(d, a0, a1, q ? v.z : v.x, q ? v.w : v.y);
-                  else mma_16816<kE4M3 && kKind == 0, false>(d, a0, a1, q ? v.z : v.x, q ? v.w : v.y);
-                }
-              }
-          }
-        }
-        // a piece is summed by itself, then scaled
-        const int block = 2 * st + piece;
-        float fu = 1.f, fl = 1.f;
-        if (kE4M3) {
-          const bool here = block < kScales;
-          if (here || block * kBlock < n.k) {
-            fu = here ? at_hand[block] : ld_f32(upper + block);
-            fl = kKind == 1 ? fu : here ? at_hand[kScales + block] : ld_f32(lower + block);
-          } else {
-            fu = fl = 0.f;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          if (!kFew && i >= tiles) break;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float d = part[0][i][j];
-            if (kChains > 1) d += part[kChains - 1][i][j];
-            acc[i][j] = fmaf(d, j < 2 ? fu : fl, acc[i][j]);
-          }
+        for (int j = 0; j < 4; ++j) {
+          float d = part[0][j];
+          if (kChains > 1) d += part[kChains - 1][j];
+          acc[i][j] = fmaf(d, j < 2 ? fu : fl, acc[i][j]);
         }
       }
     }
-    if constexpr (kKind == 0) {  // silu(gate) * up for places row + r, tokens 8 i + 2 c and the next
-      uint16_t* hidden = n.shared ? p.shared_hidden : p.hidden;
-      const int base = n.shared ? 0 : n.first, wide = pad256(n.shared ? p.m.Is : p.m.I), at = place<kE4M3>(n.row) + r;
+    const int row = n.row + half * (kKind == 0 ? 8 : 16);
+    if (row >= (kKind == 1 ? p.m.H : n.shared ? p.m.Is : p.m.I)) return;  // the last unit's half
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        if (!kFew && i >= tiles) break;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int rank = 8 * i + 2 * c + j;
-          if (rank >= n.count) continue;
-          const float xs = kE4M3 ? s.x_scale[s.token[n.first + rank]] : 1.f, g = acc[i][j] * xs, u = acc[i][2 + j] * xs;
-          const float h = g / (1.f + expf(-g)) * u;
-          const uint16_t hi = f2bf(h);
-          uint16_t* to = hidden + (size_t)(base + rank) * 2 * wide + at;
-          to[0] = hi;
-          // what the first part lost; nothing where it is not finite
-          to[wide] = (hi & 0x7F80u) == 0x7F80u ? 0 : f2bf(h - bf2f(hi));
-        }
-      }
+    for (int i = 0; i < kTiles; ++i) {
+      if (!kFew && i >= tiles) break;
+      finish<kKind>(n, row, 8 * i, acc[i]);
+    }
+    if (kKind == 0) {
       ++hidden_done;
-    } else {  // rows row + r and row + 8 + r
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        if (!kFew && i >= tiles) break;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int rank = 8 * i + 2 * c + (j & 1);
-          if (rank < n.count)
-            p.y[(size_t)(n.first + rank) * p.m.H + n.row + (j >> 1) * 8 + r] = acc[i][j] * s.weight[n.first + rank];
-        }
-      }
-      if (lane == owed) owed_row = n.row;
+    } else {
+      if (lane == owed) owed_row = row;
       ++owed;
     }
   }
+  // what comes of a unit's sums for tokens `first` to `first` + 7
+  template <int kKind>
+  __device__ __forceinline__ void finish(const Unit& n, int row, int first, const float (&acc)[4]) {
+    const int r = lane >> 2, c = lane & 3;
+    if constexpr (kKind == 0) {  // silu(gate) * up for places row + r, tokens 2 c and the next
+      uint16_t* hidden = n.shared ? p.shared_hidden : p.hidden;
+      const int base = n.shared ? 0 : n.first, wide = pad256(n.shared ? p.m.Is : p.m.I);
+      const int at = place<kE4M3>(row) + place_of_8<kE4M3>(r);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int rank = first + 2 * c + j;
+        if (rank >= n.count) continue;
+        const float xs = kE4M3 ? s.x_scale[s.token[n.first + rank]] : 1.f, g = acc[j] * xs, u = acc[2 + j] * xs;
+        const float h = g / (1.f + expf(-g)) * u;
+        const uint16_t hi = f2bf(h);
+        uint16_t* to = hidden + (size_t)(base + rank) * 2 * wide + at;
+        to[0] = hi;
+        // what the first part lost; nothing where it is not finite
+        to[wide] = (hi & 0x7F80u) == 0x7F80u ? 0 : f2bf(h - bf2f(hi));
+      }
+    } else {  // rows row + r and row + 8 + r
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int rank = first + 2 * c + (j & 1);
+        if (rank < n.count) p.y[(size_t)(n.first + rank) * p.m.H + row + (j >> 1) * 8 + r] = acc[j] * s.weight[n.first + rank];
+      }
+    }
+  }
 
-  // A fence waits for the stores before it: what units wrote is made known several units at a time.  h goes to copies.
+  // A fence waits for the stores before it: what units wrote is made known several units at a time.  
   __device__ __forceinline__ void tell_hidden() {
     if (!hidden_done) return;
-    asm volatile("fence.proxy.async.global;" ::: "memory");
     __syncwarp();
     if (lane == 0) {
       __threadfence();
@@ -844,26 +844,31 @@ struct Worker {
   }
 
   __device__ __forceinline__ void run() {
-    prepare_next();
-    fill();
-    for (worked = 0; ok && worked != pushed; ++worked) {
-      __syncwarp();
-      const Unit n = unit_of(queue[worked % kQueue]);
-      if (n.kind && !hidden_ready) {  // every unit of the first kind is in the hands of a warp that waits for nothing
-        tell_hidden();
-        for (uint32_t i = 0; ok; ++i) {
-          const unsigned done = (unsigned)ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1));
-          if (__all_sync(~0u, done >= (unsigned)units_a)) break;
-          if (i == kSpinLimit) {
-            raise_error(p.c.err, kErrTimeout);
-            ok = false;
-          }
-          __nanosleep(32);
-        }
+    if (half == 0) {
+      prepare_next();
+      fill();
+    }
+    for (worked = 0;; ++worked) {
+      if (half == 0 && worked == pushed && lane == 0) queue[worked % kQueue] = -1;
+      ok = team_sync(team, ok);
+      const int u = queue[worked % kQueue];
+      if (!ok || u < 0) break;
+      const Unit n = unit_of(u);
+      if (n.kind && !hidden_ready) {  // every unit of the first kind is in the hands of a team that waits for nothing
         hidden_ready = true;
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-        load_late();
-        if (!ok) break;
+        tell_hidden();
+        if (half == 0) {
+          for (uint32_t i = 0; ok; ++i) {
+            const unsigned done = (unsigned)ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1));
+            if (__all_sync(~0u, done >= (unsigned)halves_a)) break;
+            if (i == kSpinLimit) {
+              raise_error(p.c.err, kErrTimeout);
+              ok = false;
+            }
+            __nanosleep(32);
+          }
+          load_late();
+        }
       }
       if (n.kind == 0) {
         if (n.count <= 8) work<0, true>(n);
@@ -872,55 +877,74 @@ struct Worker {
         if (n.count <= 8) work<1, true>(n);
         else work<1, false>(n);
       }
+      if (!ok) break;
       if (owed == kOwed) tell_rows();
-      prepare_next();
-      fill();
+      if (half == 0) {
+        prepare_next();
+        fill();
+      }
     }
     tell_hidden();
     tell_rows();
-    if (!ok && !hidden_ready) load_late();  // a stage that lacks its values would never be full
+    if (half) return;
+    if (!hidden_ready) load_late();  // a stage that lacks its values would never be full
     // copies in flight land before the CTA ends, after a wait that ran out too
     for (; ahead; --ahead) {
       warp_wait(bars + 8 * now, pass);
-      if (++now == kEntries) now = 0, pass ^= 1;
+      if (++now == stages) now = 0, pass ^= 1;
     }
   }
 };
 
-struct Rings {  // behind the warps' stages
+struct Rings {  // behind the teams' stages
   Lists lists;
-  uint64_t bars[kWarps][kEntries];
-  int queues[kWarps][kQueue];
+  uint64_t bars[kTeams][kStages];
+  int queues[kTeams][kQueue];
 };
-constexpr size_t kSmem = 1024 + (size_t)kWarps * kRing + sizeof(Rings);
+constexpr size_t kSmem = 1024 + (size_t)kTeams * kRing + sizeof(Rings);
 static_assert(kSmem <= 232448, "");
-static_assert(kRing / kStageBytes < kEntries && kRing / kStageBytes < kQueue, "");
+static_assert(kStages + 2 <= kQueue, "");
 
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  Rings& rings = *reinterpret_cast<Rings*>(smem + kWarps * kRing);
+  Rings& rings = *reinterpret_cast<Rings*>(smem + kTeams * kRing);
   Lists& s = rings.lists;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x < kWarps * kEntries) mbar_init(smem_u32(&rings.bars[0][0] + threadIdx.x), 1);
+  if (threadIdx.x < kTeams * kStages) mbar_init(smem_u32(&rings.bars[0][0] + threadIdx.x), 33);  // the weights; every lane's copies
   if (threadIdx.x == 0) {
     prefetch_tensormap(&p.gate_up);
     prefetch_tensormap(&p.down);
   }
   fence_mbar_init();
   await_grid();
-  asm volatile("fence.proxy.async.global;" ::: "memory");  // tokens are read by copies
-  Worker<kE4M3> w = {p, s, lane, smem_u32(smem + warp * kRing), smem_u32(rings.bars[warp]), rings.queues[warp], s.scales[warp]};
-  w.take();
+  const int team = warp >> 1;
+  Worker<kE4M3> w = {p,
+                     s,
+                     lane,
+                     team,
+                     warp & 1,
+                     smem_u32(smem + team * kRing),
+                     smem_u32(rings.bars[team]),
+                     rings.queues[team],
+                     s.scales[team]};
+  if (w.half == 0) w.take();
   make_lists(p, s);
-  w.hidden_units = p.m.I / 8;
-  w.out_units = p.m.H / 16;
-  w.units_a = s.active * w.hidden_units + p.m.Is / 8;
+  w.hidden_units = (p.m.I + 15) / 16;
+  w.out_units = (p.m.H + 31) / 32;
+  w.shared_units = (p.m.Is + 15) / 16;
+  w.halves_a = s.active * (p.m.I / 8) + p.m.Is / 8;
+  w.units_a = s.active * w.hidden_units + w.shared_units;
   w.units = w.units_a + (s.active + (p.m.Is ? 1 : 0)) * w.out_units;
-  w.pushed = w.left = w.x = w.y = w.z = w.load_size = w.load_tokens = w.next = w.tail = w.used = w.entry = 0;
-  w.head = w.ahead = w.worked = w.now = w.pass = w.hidden_done = w.owed = w.owed_row = 0;
-  w.load_src = nullptr;
+  w.stages = kStages;
+  while (kRing / w.stages < kStageBytes + s.most * 2 * w.kRowBytes) --w.stages;  // h of the tokens of an expert beside its weights
+  w.stage_bytes = kRing / w.stages;
+  w.pushed = w.left = w.x = w.z = w.next = w.pieces = w.slot = w.ahead = w.worked = w.now = w.pass = w.stopped = 0;
+  w.hidden_done = w.owed = w.owed_row = 0;
+  w.load = Unit{};
+  w.first_to = 0;
+  w.values = nullptr;
   w.map = nullptr;
   w.next_upper = w.next_lower = 0.f;
   w.more = w.ok = true;
@@ -936,8 +960,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
 template <bool kE4M3>
 cudaError_t encode(CUtensorMap* map, const void* base, int k, int rows, int matrices, bool halves) {
   if (!base || !rows || !k) return cudaSuccess;
-  return kE4M3 ? encode_u8_3d_sw128(map, base, k, rows, matrices, 128, halves ? 8 : 16, halves ? 2 : 1)
-               : encode_bf16_3d_sw128(map, base, k, rows, matrices, 64, halves ? 8 : 16, halves ? 2 : 1);
+  return kE4M3 ? encode_u8_3d_sw128(map, base, k, rows, matrices, 128, halves ? 16 : 32, halves ? 2 : 1)
+               : encode_bf16_3d_sw128(map, base, k, rows, matrices, 64, halves ? 16 : 32, halves ? 2 : 1);
 }
 
 template <bool kE4M3>
