@@ -25,7 +25,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kTeams = 8, kWarps = 2 * kTeams, kThreads = kWarps * 32;  // two warps share a ring
+constexpr int kTeams = 8, kWarps = 2 * kTeams, kThreads = kWarps * 32;  // a team: a warp that loads, one that multiplies
 constexpr int kMaxTokens = 64, kMaxTopK = 16, kMaxExperts = 1024;
 constexpr int kMaxSlots = kMaxTokens * (kMaxTopK + 1);  // (token, expert) pairs
 constexpr int kStageBytes = 4096;  // of weights: 32 rows of 128 bytes
@@ -209,19 +209,16 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
 // ---------------------------------------------------------------- the choice
 
 // What every CTA works out for itself: the tokens' experts and the experts' tokens.
+struct Choice {  // on the way to the lists
+  unsigned long long mask[kMaxExperts];  // tokens of an expert
+  float weight[kMaxTokens][kMaxTopK];
+  uint32_t sums[kWarps];
+  uint16_t index[kMaxExperts];           // the active expert's number
+  int16_t id[kMaxTokens][kMaxTopK];      // negative: none
+};
 struct Lists {
-  union {
-    struct {                                         // until the lists are there
-      unsigned long long mask[kMaxExperts];          // tokens of an expert
-      float chosen_weight[kMaxTokens][kMaxTopK];
-      uint16_t index[kMaxExperts];                   // the active expert's number
-      int16_t chosen[kMaxTokens][kMaxTopK];          // negative: none
-    };
-    float scales[kTeams][kQueue * 2 * kScales];      // then: of the units on their way
-  };
   float weight[kMaxSlots];
   float x_scale[kMaxTokens];
-  uint32_t sums[kWarps];
   int active;                       // experts that have tokens
   int most;                         // tokens of one, among those of up to 8
   uint16_t expert[kMaxExperts];     // of an active expert
@@ -233,7 +230,7 @@ constexpr uint16_t kNone = 0xFFFF;
 
 // One warp: token t's top_k experts and their weights.  A lane holds the keys of every 32nd expert.
 template <int kOwn>
-__device__ __forceinline__ void choose(const MoeParams& p, Lists& s, int t, int lane) {
+__device__ __forceinline__ void choose(const MoeParams& p, Choice& s, int t, int lane) {
   const MoeCall& c = p.c;
   const int E = p.m.E;
   const float* l = p.logits + (size_t)t * (E + 1);
@@ -288,8 +285,8 @@ __device__ __forceinline__ void choose(const MoeParams& p, Lists& s, int t, int 
   }
   w *= c.scale;
   if (chosen) {
-    s.chosen[t][lane] = (int16_t)id;
-    s.chosen_weight[t][lane] = w;
+    s.id[t][lane] = (int16_t)id;
+    s.weight[t][lane] = w;
     if (blockIdx.x == 0) {
       if (c.ids_out) c.ids_out[t * c.top_k + lane] = id;
       if (c.weights_out) c.weights_out[t * c.top_k + lane] = w;
@@ -298,11 +295,11 @@ __device__ __forceinline__ void choose(const MoeParams& p, Lists& s, int t, int 
 }
 
 // The whole CTA.
-__device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
+__device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, Lists& s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.c.T, k = p.c.top_k, E = p.m.E;
   constexpr int kPass = kThreads / kMaxTopK;  // tokens at a time, a thread for each of their choices
   const int j = tid % kMaxTopK, t0 = tid / kMaxTopK;
-  for (int e = tid; e < E; e += kThreads) s.mask[e] = 0;
+  for (int e = tid; e < E; e += kThreads) choice.mask[e] = 0;
   if (tid == 0) s.most = p.m.Is && T <= 8 ? T : 0;
   if (tid < T) s.x_scale[tid] = ld_f32(p.x_scale + tid);
   if (p.c.ids_in) {
@@ -313,27 +310,27 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
         if (blockIdx.x == 0) raise_error(p.c.err, kErrDeviceArgument);
         id = -1;
       }
-      s.chosen[t][j] = (int16_t)max(id, -1);
-      s.chosen_weight[t][j] = ld_f32(p.c.weights_in + t * k + j);
+      choice.id[t][j] = (int16_t)max(id, -1);
+      choice.weight[t][j] = ld_f32(p.c.weights_in + t * k + j);
     }
   } else {
     for (int t = warp; t < T; t += kWarps) {
-      if (E <= 64) choose<2>(p, s, t, lane);
-      else if (E <= 128) choose<4>(p, s, t, lane);
-      else if (E <= 320) choose<10>(p, s, t, lane);
-      else choose<32>(p, s, t, lane);
+      if (E <= 64) choose<2>(p, choice, t, lane);
+      else if (E <= 128) choose<4>(p, choice, t, lane);
+      else if (E <= 320) choose<10>(p, choice, t, lane);
+      else choose<32>(p, choice, t, lane);
     }
   }
   __syncthreads();
   for (int t = t0; t < T && j < k; t += kPass)
-    if (s.chosen[t][j] >= 0) atomicOr(&s.mask[s.chosen[t][j]], 1ull << t);
+    if (choice.id[t][j] >= 0) atomicOr(&choice.mask[choice.id[t][j]], 1ull << t);
   __syncthreads();
   // experts that have tokens, in order: each thread has some neighbours; experts above, slots below in a word
   constexpr int kOwn = (kMaxExperts + kThreads - 1) / kThreads;
   uint32_t own = 0, most = 0;
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
-    const int e = tid * kOwn + i, n = e < E ? __popcll(s.mask[e]) : 0;
+    const int e = tid * kOwn + i, n = e < E ? __popcll(choice.mask[e]) : 0;
     own += n ? 0x10000u + n : 0;
     if (n <= 8) most = max(most, (uint32_t)n);
   }
@@ -344,7 +341,7 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
   }
   most = __reduce_max_sync(~0u, most);
   if (lane == 31) {
-    s.sums[warp] = before;
+    choice.sums[warp] = before;
     if (most) atomicMax(&s.most, (int)most);
   }
   __syncthreads();
@@ -352,16 +349,16 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
   before -= own;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s.sums[w];
-    all += s.sums[w];
+    if (w < warp) before += choice.sums[w];
+    all += choice.sums[w];
   }
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
-    const int e = tid * kOwn + i, n = e < E ? __popcll(s.mask[e]) : 0;
+    const int e = tid * kOwn + i, n = e < E ? __popcll(choice.mask[e]) : 0;
     if (n) {
       s.expert[before >> 16] = (uint16_t)e;
       s.first[before >> 16] = (uint16_t)(before & 0xFFFF);
-      s.index[e] = (uint16_t)(before >> 16);
+      choice.index[e] = (uint16_t)(before >> 16);
       before += 0x10000u + n;
     }
   }
@@ -373,17 +370,17 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Lists& s) {
   }
   __syncthreads();
   for (int t = t0; t < T && j < k; t += kPass) {
-    const int e = s.chosen[t][j];
+    const int e = choice.id[t][j];
     bool again = e < 0;
     float w = 0.f;
     for (int q = 0; q < k; ++q)
-      if (s.chosen[t][q] == e) {
-        w += s.chosen_weight[t][q];
+      if (choice.id[t][q] == e) {
+        w += choice.weight[t][q];
         again |= q < j;
       }
     int slot = kNone;
     if (!again) {
-      slot = s.first[s.index[e]] + __popcll(s.mask[e] & ((1ull << t) - 1));
+      slot = s.first[choice.index[e]] + __popcll(choice.mask[e] & ((1ull << t) - 1));
       s.token[slot] = (uint8_t)t;
       s.weight[slot] = w;
     }
@@ -440,16 +437,24 @@ __device__ __forceinline__ int place_of_8(int i) {
   return kE4M3 ? (i & 4) | (i & 1) << 1 | (i >> 1 & 1) : i;
 }
 
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    uint32_t done;
-    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-                 : "=r"(done)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    if (__all_sync(~0u, done)) return true;
+__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(done)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return __all_sync(~0u, done);
+}
+__device__ __forceinline__ void warp_wait(uint32_t bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitLimit && !warp_poll(bar, parity); ++i) {
   }
-  return false;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// by one lane of the warp
+__device__ __forceinline__ void first_arrive(uint32_t bar) {
+  asm volatile("{\n.reg .pred e;\nelect.sync _|e, 0xFFFFFFFF;\n@e mbarrier.arrive.shared::cta.b64 _, [%0];\n}" ::"r"(bar) : "memory");
 }
 // A stage's load of weights, by one lane of the warp.
 __device__ __forceinline__ void warp_load(uint32_t dst, const void* map, int x, int y, int z, uint32_t bar) {
@@ -469,69 +474,70 @@ __device__ __forceinline__ void copy_16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copies_done_to(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-// both warps of a team have come here, and whether both are `ok`
-__device__ __forceinline__ bool team_sync(int team, bool ok) {
-  uint32_t both;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.ne.b32 p, %2, 0;\nbarrier.cta.red.and.pred q, %1, 64, p;\nselp.u32 %0, 1, 0, q;\n}"
-      : "=r"(both)
-      : "r"(team + 1), "r"((int)ok)
-      : "memory");
-  return both;
+__device__ __forceinline__ void copy_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // A unit of work.
 struct Unit {
-  int kind;            // 0: 16 rows of gate and up, 1: 32 rows of down
-  int a;               // the active expert, `active` for the shared one
+  int kind;          // 0: 16 rows of gate and up, 1: 32 rows of down
+  int a;             // the active expert, `active` for the shared one
   bool shared;
-  int row, k;          // first row; length of a row
-  int first, count;    // the expert's slots
+  int row, k;        // first row; length of a row
+  int first, count;  // the expert's slots
 };
 
-// A warp of a team of two.  A stage of their ring has 4 KB of weights and behind them, for an expert of up to 8 tokens, the
-// tokens' values for the same k (loads through the cache take several thousand cycles while the copies fill the memory's
-// queues).  Each warp has the products of half of a stage's rows; the first one loads.
+// Of a team: a warp that loads and one that multiplies.  A stage of their ring has 4 KB of weights and behind them, for an
+// expert of up to 8 tokens, the tokens' values for the same k (loads through the cache take several thousand cycles while
+// the copies fill the memory's queues).
+struct Team {
+  float scales[kQueue][2][kScales];  // of the units on their way
+  uint64_t full[kStages], empty[kStages];
+  int queue[kQueue];  // units on their way; negative: no more
+  int finished;       // units of the first kind
+  int failed;         // a wait ran out
+};
+struct Rings {  // behind the teams' stages
+  union {
+    Choice choice;
+    Team team[kTeams];
+  };
+  Lists lists;
+};
+
 template <bool kE4M3>
-struct Worker {
+struct Warp {
   static constexpr int kStageK = kE4M3 ? 128 : 64;  // of a stage
   static constexpr int kRowBytes = 2 * kStageK;     // of a token in a stage
   const MoeParams& p;
-  Lists& s;
-  const int lane, team, half;
-  const uint32_t ring, bars;  // the team's stages and barriers
-  int* queue;                 // units on their way
-  float* scales;              // theirs: [kQueue][2][kScales]
-  int halves_a;               // halves of units of the first kind that have rows
-  int units_a, units;         // of the first kind, of both
-  int stages;                 // of the ring
+  const Lists& s;
+  Team& team;
+  const int lane;
+  const uint32_t ring;
+  int units_a, units;                           // of the first kind, of both
+  int hidden_units, out_units, shared_units;    // units of an expert of either kind; of the shared one's first kind
+  int stages;                                   // of the ring
   uint32_t stage_bytes;
-  int hidden_units, out_units, shared_units;  // units of an expert of either kind; of the shared one's first kind
-  // loading: the unit that is being loaded, and the one after it
-  unsigned ticket;
-  int pushed, left, x, z, next, pieces;  // 16-byte pieces of values of a stage
-  uint32_t first_to;       // where this lane's first one goes in a stage
-  const uint16_t* values;  // and where from; the unit's values
-  const void* map;
-  Unit load;
-  float next_upper, next_lower;
-  bool more, next_ready;
-  int slot;                   // the next stage to load
-  // working
-  int ahead, worked, now, pass;  // stages loaded, units done, the next stage and its phase
-  int stopped;         // after a wait that ran out: stages done of the unit in hand
-  int hidden_done;     // units of the first kind done and not yet told
-  int owed, owed_row;  // units of the second kind not yet told; lane i: the row of unit i
-  bool hidden_ready, ok;
 
+  __device__ __forceinline__ Warp(const MoeParams& params, const Lists& lists, Team& t, uint32_t at)
+      : p(params), s(lists), team(t), lane(threadIdx.x & 31), ring(at) {
+    hidden_units = (p.m.I + 15) / 16;
+    out_units = (p.m.H + 31) / 32;
+    shared_units = (p.m.Is + 15) / 16;
+    units_a = s.active * hidden_units + shared_units;
+    units = units_a + (s.active + (p.m.Is ? 1 : 0)) * out_units;
+    stages = kStages;
+    while (kRing / stages < kStageBytes + s.most * 2 * kRowBytes) --stages;  // h of an expert's tokens beside its weights
+    stage_bytes = kRing / stages;
+  }
   __device__ __forceinline__ Unit unit_of(int u) const {  // the shared expert's are first: they take longest
     Unit n;
     n.kind = u >= units_a;
-    const int each = n.kind ? out_units : hidden_units, ahead_of = p.m.Is ? (n.kind ? out_units : shared_units) : 0;
-    const int v = (n.kind ? u - units_a : u) - ahead_of;
+    const int each = n.kind ? out_units : hidden_units, before = p.m.Is ? (n.kind ? out_units : shared_units) : 0;
+    const int v = (n.kind ? u - units_a : u) - before;
     n.shared = v < 0;
     n.a = n.shared ? s.active : (unsigned)v / (unsigned)each;
-    n.row = (n.shared ? v + ahead_of : v - n.a * each) * (n.kind ? 32 : 16);
+    n.row = (n.shared ? v + before : v - n.a * each) * (n.kind ? 32 : 16);
     n.k = !n.kind ? p.m.H : n.shared ? p.m.Is : p.m.I;
     n.first = s.first[n.a];
     n.count = s.first[n.a + 1] - n.first;
@@ -542,7 +548,7 @@ struct Worker {
     const size_t row = n.kind == 0 ? s.token[n.first + rank] : 2 * (size_t)(n.shared ? rank : n.first + rank);
     return (n.kind == 0 ? p.x : n.shared ? p.shared_hidden : p.hidden) + row * pad256(n.k);
   }
-  // the scales of a unit's rows by blocks of k: its upper and lower 8
+  // the scales of a unit's rows by blocks of k: of gate and of up, or of down
   __device__ __forceinline__ void scales_of(const Unit& n, const float*& upper, const float*& lower) const {
     const int kb = (n.k + kBlock - 1) / kBlock;
     if (n.kind) {
@@ -556,103 +562,192 @@ struct Worker {
       lower = upper + (size_t)rb * kb;
     }
   }
-  __device__ __forceinline__ void take() {  // the next unit's number, known later
-    if (lane == 0) ticket = atomicAdd(p.counters, 1u);
-  }
-  // the unit after the one that is being loaded: its scales are asked for
-  __device__ __forceinline__ void prepare_next() {
-    if (next_ready || !more) return;
-    next = (int)__shfl_sync(~0u, ticket, 0);
-    if ((unsigned)next >= (unsigned)units) {
-      more = false;
-      return;
-    }
-    take();
-    next_ready = true;
-    if (kE4M3) {
-      const Unit n = unit_of(next);
-      const float *upper, *lower;
-      scales_of(n, upper, lower);
-      const bool in = lane < (n.k + kBlock - 1) / kBlock;
-      next_upper = in ? ld_f32(upper + lane) : 0.f;
-      next_lower = in ? ld_f32(lower + lane) : 0.f;
-    }
+};
+
+// The warp that loads.
+template <bool kE4M3>
+struct Loader : Warp<kE4M3> {
+  using W = Warp<kE4M3>;
+  using W::kRowBytes;
+  using W::kStageK;
+  using W::lane;
+  using W::p;
+  using W::s;
+  using W::team;
+  static constexpr int kPieces = kRowBytes / 16;  // of 16 bytes of a token's values
+  Unit load;
+  int pieces;              // of 16 bytes, of a stage's values
+  uint32_t first_to;       // where this lane's first one goes in a stage
+  const uint16_t* values;  // and where from
+  int slot = 0, pass = 0;  // the next stage to load
+  bool ok = true, hidden_ready = false;
+
+  __device__ __forceinline__ Loader(const MoeParams& params, const Lists& lists, Team& t, uint32_t at)
+      : W(params, lists, t, at) {}
+
+  // Pieces 4 apart are swapped for odd tokens: a quarter warp reads 4 pieces of two tokens.
+  __device__ __forceinline__ static uint32_t place_of(int kind, int row, int piece) {
+    return kStageBytes + row * kRowBytes + ((piece ^ (kind ? row & 2 : (row & 1) << 1) << 1) << 4);
   }
   // the unit whose values are loaded
   __device__ __forceinline__ void aim(const Unit& n) {
     load = n;
-    constexpr int kPieces = kRowBytes / 16;
-    const int i = lane / kPieces, piece = lane % kPieces, width = pad256(n.k);
+    const int row = lane / kPieces, piece = lane % kPieces;
     pieces = n.count > 8 ? 0 : n.count * (n.kind + 1) * kPieces;
-    first_to = kStageBytes + i * kRowBytes + ((piece ^ (n.kind ? i & 2 : (i & 1) << 1) << 1) << 4);
-    if (lane < pieces) values = (n.kind ? values_of(n, 0) + (size_t)i * width : values_of(n, i)) + piece * 8;
+    first_to = place_of(n.kind, row, piece);
+    values = nullptr;
+    if (lane < pieces)
+      values = (n.kind ? this->values_of(n, 0) + (size_t)row * pad256(n.k) : this->values_of(n, row)) + piece * 8;
   }
-  // goes on to the prepared unit
-  __device__ __forceinline__ void begin_next() {
-    const Unit n = unit_of(next);
-    const int q = pushed % kQueue;
-    if (lane == 0) queue[q] = next;
-    if (kE4M3) {
-      scales[q * 2 * kScales + lane] = next_upper;
-      scales[q * 2 * kScales + kScales + lane] = next_lower;
-    }
-    ++pushed;
-    const int e = n.shared ? 0 : s.expert[n.a];
-    x = 0;
-    z = n.kind ? e : 2 * e;
-    left = (n.k + kStageK - 1) / kStageK;
-    aim(n);
-    map = n.kind ? (n.shared ? &p.shared_down : &p.down) : (n.shared ? &p.shared_gate_up : &p.gate_up);
-    next_ready = false;
-  }
-  // The tokens' values of a stage: rows of 16-byte pieces, pieces 4 apart swapped for odd tokens (a quarter warp reads 4 pieces
-  // of two tokens); h in two parts.
+  // The tokens' values of a stage: rows of 16-byte pieces, h in two parts.
   __device__ __forceinline__ void load_values(uint32_t at, int k, uint32_t bar) {
     if (lane < pieces) copy_16(at + first_to, values + k);
     if (pieces > 32) {
-      constexpr int kPieces = kRowBytes / 16;
       const int piece = lane % kPieces, width = pad256(load.k);
 #pragma unroll 1
       for (int q = lane + 32; q < pieces; q += 32) {
-        const int i = q / kPieces, swap = load.kind ? i & 2 : (i & 1) << 1;
-        const uint16_t* from = load.kind ? values + (size_t)(i - lane / kPieces) * width : values_of(load, i) + piece * 8;
-        copy_16(at + kStageBytes + i * kRowBytes + ((piece ^ swap << 1) << 4), from + k);
+        const int row = q / kPieces;
+        const uint16_t* from = load.kind ? values + (size_t)(row - lane / kPieces) * width : this->values_of(load, row) + piece * 8;
+        copy_16(at + place_of(load.kind, row, piece), from + k);
       }
     }
-    copies_done_to(bar);
+    copies_done_to(bar);  // a unit's scales too
   }
-  // loads stages while there is room and something to load
-  __device__ __forceinline__ void fill() {
-    while (ahead < stages) {
-      if (left == 0) {
-        if (!next_ready) return;
-        begin_next();
-        prepare_next();
-      }
-      const uint32_t bar = bars + 8 * slot, at = ring + slot * stage_bytes;
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // values that lay there came by plain copies
-      warp_load(at, map, x, load.row, z, bar);
-      if (load.kind == 0 || hidden_ready) load_values(at, x, bar);
-      if (++slot == stages) slot = 0;
-      ++ahead;
-      x += kStageK;
-      --left;
+  __device__ __forceinline__ void fail() {
+    if (ok && lane == 0) {
+      raise_error(p.c.err, kErrTimeout);
+      *(volatile int*)&team.failed = 1;
     }
+    ok = false;
   }
-  // The stages that were loaded before h was there get its values.
-  __device__ __forceinline__ void load_late() {
+  // Every unit of the first kind is in the hands of a team that waits for nothing: h will be there.  Then `late` stages from
+  // `at` on, of units from `unit` on, get its values.
+  __device__ __forceinline__ void await_hidden(int mine, int late, int at, int unit) {
+    for (uint32_t i = 0;; ++i) {
+      int done = 0;
+      asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(done) : "r"(smem_u32(&team.finished)) : "memory");
+      if (__all_sync(~0u, done >= mine)) break;
+      if (i == kSpinLimit || *(volatile int*)&team.failed) return fail();
+      __nanosleep(32);
+    }
+    if (lane == 0 && mine) {
+      __threadfence();
+      atomicAdd(p.counters + 1, (unsigned)mine);
+    }
+    if (late == 0) return;
+    for (uint32_t i = 0;; ++i) {
+      const unsigned done = (unsigned)ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1));
+      if (__all_sync(~0u, done >= (unsigned)this->units_a)) break;
+      if (i == kSpinLimit) return fail();
+      __nanosleep(32);
+    }
     const Unit loading = load;
-    int e = now, w = worked, st = stopped;
-    for (int i = 0; i < ahead; ++i) {
+    int st = 0;
+    for (int i = 0; i < late; ++i) {
       if (i == 0 || st == (load.k + kStageK - 1) / kStageK) {
-        if (i) st = 0, ++w;
-        aim(unit_of(queue[w % kQueue]));
+        aim(this->unit_of(team.queue[unit++ % kQueue]));
+        st = 0;
       }
-      if (load.kind) load_values(ring + e * stage_bytes, st * kStageK, bars + 8 * e);
-      if (++e == stages) e = 0;
-      ++st;
+      load_values(this->ring + at * this->stage_bytes, st++ * kStageK, smem_u32(team.full + at));
+      if (++at == this->stages) at = 0;
     }
     aim(loading);
+    hidden_ready = true;
+  }
+  // waits until the next stage may be loaded
+  __device__ __forceinline__ void await_place() {
+    const uint32_t bar = smem_u32(team.empty + slot);
+    for (uint32_t i = 0; !warp_poll(bar, pass ^ 1); ++i)
+      if (i == kWaitLimit || *(volatile int*)&team.failed) return fail();
+  }
+
+  __device__ __forceinline__ void run(unsigned ticket) {
+    int mine = 0, late = 0, late_at = 0, late_unit = 0, pushed = 0, loaded = 0;
+    int next = (int)__shfl_sync(~0u, ticket, 0);
+    while (ok && (unsigned)next < (unsigned)this->units) {
+      const int q = pushed % kQueue;
+      const Unit n = this->unit_of(next);
+      if (lane == 0) {
+        team.queue[q] = next;
+        ticket = atomicAdd(p.counters, 1u);  // the next unit's number, known later
+      }
+      if (kE4M3) {
+        const float *upper, *lower;
+        this->scales_of(n, upper, lower);
+        if (lane < (n.k + kBlock - 1) / kBlock) {
+          copy_4(smem_u32(&team.scales[q][0][lane]), upper + lane);
+          if (!n.kind) copy_4(smem_u32(&team.scales[q][1][lane]), lower + lane);
+        }
+      }
+      aim(n);
+      const void* map = n.kind ? (n.shared ? &p.shared_down : &p.down) : (n.shared ? &p.shared_gate_up : &p.gate_up);
+      const int z = n.shared ? 0 : s.expert[n.a] * (n.kind ? 1 : 2), steps = (n.k + kStageK - 1) / kStageK;
+      if (n.kind == 0) ++mine;
+      __syncwarp();
+#pragma unroll 1
+      for (int st = 0; st < steps; ++st) {
+        if (n.kind && !hidden_ready) {
+          if (late == this->stages) await_hidden(mine, late, late_at, late_unit);
+          else if (late++ == 0) late_at = slot, late_unit = pushed;
+        }
+        await_place();
+        if (!ok) break;
+        const uint32_t bar = smem_u32(team.full + slot), at = this->ring + slot * this->stage_bytes;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // values that lay there came by plain copies
+        warp_load(at, map, st * kStageK, n.row, z, bar);
+        if (n.kind == 0 || hidden_ready) load_values(at, st * kStageK, bar);
+        if (++slot == this->stages) slot = 0, pass ^= 1;
+        ++loaded;
+      }
+      ++pushed;
+      next = (int)__shfl_sync(~0u, ticket, 0);
+    }
+    if (ok && !hidden_ready) await_hidden(mine, late, late_at, late_unit);
+    if (ok) await_place();
+    if (ok) {  // no more
+      if (lane == 0) team.queue[pushed % kQueue] = -1;
+      __syncwarp();
+      arrive(smem_u32(team.full + slot));
+      if (lane == 0) arrive(smem_u32(team.full + slot));
+      return;
+    }
+    // a wait ran out: copies in flight land before the CTA ends
+    for (int i = 0; i < late && !hidden_ready; ++i) copies_done_to(smem_u32(team.full + (late_at + i) % this->stages));
+    for (int i = 0; i < loaded && i < this->stages; ++i) {
+      if (slot-- == 0) slot = this->stages - 1, pass ^= 1;
+      warp_wait(smem_u32(team.full + slot), pass);
+    }
+  }
+};
+
+// The warp that multiplies.
+template <bool kE4M3>
+struct Multiplier : Warp<kE4M3> {
+  using W = Warp<kE4M3>;
+  using W::kRowBytes;
+  using W::kStageK;
+  using W::lane;
+  using W::p;
+  using W::s;
+  using W::team;
+  int worked = 0, now = 0, pass = 0;  // units; the next stage
+  int owed = 0, owed_row = 0;         // units of the second kind not yet told; lane i: the row of unit i
+  bool ok = true, hidden_ready = false;
+
+  __device__ __forceinline__ Multiplier(const MoeParams& params, const Lists& lists, Team& t, uint32_t at)
+      : W(params, lists, t, at) {}
+
+  __device__ __forceinline__ void await_stage() {
+    const uint32_t bar = smem_u32(team.full + now);
+    for (uint32_t i = 0; !warp_poll(bar, pass); ++i)
+      if (i == kWaitLimit || *(volatile int*)&team.failed) {
+        if (lane == 0) {
+          raise_error(p.c.err, kErrTimeout);
+          *(volatile int*)&team.failed = 1;
+        }
+        ok = false;
+        return;
+      }
   }
 
   // One unit; kFew: of at most 8 tokens, whose values are in the ring, else of up to 64.
@@ -660,81 +755,79 @@ struct Worker {
   __device__ __forceinline__ void work(const Unit& n) {
     const int r = lane >> 2, c = lane & 3, width = pad256(n.k), steps = (n.k + kStageK - 1) / kStageK;
     constexpr int kTiles = kFew ? 1 : 8;
-    constexpr int kLoads = kE4M3 ? 4 : 2;       // of a lane from a token for a piece, 32 values apart
+    constexpr int kLoads = kE4M3 ? 4 : 2;       // of a lane from a token for a stage, 32 values apart
     constexpr int kParts = kKind == 0 ? 1 : 2;  // h is held in two
     constexpr int kSteps = kE4M3 ? 4 : 2;       // products of a chunk
     constexpr int kChains = kFew ? 2 : 1;       // sums that do not wait for one another
     const int tiles = kFew ? 1 : (n.count + 7) / 8;
-    float acc[kTiles][4];
+    float acc[kTiles][2][4];                    // the two groups of 16 rows
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-    const float* at_hand = scales + worked % kQueue * 2 * kScales;
+      for (int j = 0; j < 8; ++j) acc[i][j >> 2][j & 3] = 0.f;
+    const float(*at_hand)[kScales] = team.scales[worked % kQueue];
     const float *upper = nullptr, *lower = nullptr;
-    if (kE4M3 && n.k > kScales * kBlock) scales_of(n, upper, lower);
-    const uint32_t rows = half * (kKind == 0 ? 1024 : 2048) + r * 128, apart = kKind == 0 ? 2048 : 1024;
-    const uint32_t place0 = rows + ((2 * c ^ r) << 4), place1 = rows + (((2 * c + 1) ^ r) << 4);
+    if (kE4M3 && n.k > kScales * kBlock) this->scales_of(n, upper, lower);
+    // rows r and r + 8 of a group: in gate and up, or in down
+    const uint32_t apart = kKind == 0 ? 2048 : 1024, group = kKind == 0 ? 1024 : 2048;
+    const uint32_t place0 = r * 128 + ((2 * c ^ r) << 4), place1 = r * 128 + (((2 * c + 1) ^ r) << 4);
     // columns behind the last token repeat it, and are not stored
     const int rank = min(r, n.count - 1);
     const uint32_t values0 = kStageBytes + rank * kParts * kRowBytes + c * 16 + (rank & 1) * 64;
 #pragma unroll 1
     for (int st = 0; st < steps; ++st) {
-      if (!warp_wait(bars + 8 * now, pass)) {
-        raise_error(p.c.err, kErrTimeout);
-        ok = false;
-      }
-      const uint32_t at = ring + now * stage_bytes;
-      // rows r and r + 8, chunks 2 c and 2 c + 1, swizzled
-      uint4 w[2][2], b[kParts][kLoads];
+      await_stage();
+      if (!ok) return;
+      const uint32_t at = this->ring + now * this->stage_bytes;
+      // chunks 2 c and 2 c + 1 of the rows, swizzled
+      uint4 w[2][2][2], b[kParts][kLoads];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        w[0][h] = lds128(at + h * apart + place0);
-        w[1][h] = lds128(at + h * apart + place1);
-      }
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          w[g][0][h] = lds128(at + g * group + h * apart + place0);
+          w[g][1][h] = lds128(at + g * group + h * apart + place1);
+        }
       if (kFew)
 #pragma unroll
         for (int h = 0; h < kParts; ++h)
 #pragma unroll
           for (int q = 0; q < kLoads; ++q) b[h][q] = lds128((at + values0 + h * kRowBytes) ^ q * 64);
-      ok = team_sync(team, ok);
-      if (!ok) {
-        stopped = st;
-        return;
-      }
-      if (++now == stages) now = 0, pass ^= 1;
-      --ahead;
-      if (half == 0) fill();
       float fu = 1.f, fl = 1.f;
       if (kE4M3) {
         const bool here = st < kScales;
-        fu = here ? at_hand[st] : ld_f32(upper + st);
-        fl = kKind == 1 ? fu : here ? at_hand[kScales + st] : ld_f32(lower + st);
+        fu = here ? at_hand[0][st] : ld_f32(upper + st);
+        fl = kKind == 1 ? fu : here ? at_hand[1][st] : ld_f32(lower + st);
       }
-      uint2 a[2][kSteps][2];
+      __syncwarp();
+      first_arrive(smem_u32(team.empty + now));
+      if (++now == this->stages) now = 0, pass ^= 1;
+      uint2 a[2][2][kSteps][2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t u[4] = {w[j][h].x, w[j][h].y, w[j][h].z, w[j][h].w};
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int q = 0; q < kSteps; ++q) {
-            if constexpr (!kE4M3) a[j][q][h] = make_uint2(u[2 * q], u[2 * q + 1]);
-            else if constexpr (kKind == 0) a[j][q][h] = e4m3x4_to_half4(u[q]);
-            else a[j][q][h] = e4m3x4_to_bf16x4(u[q]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t u[4] = {w[g][j][h].x, w[g][j][h].y, w[g][j][h].z, w[g][j][h].w};
+#pragma unroll
+            for (int q = 0; q < kSteps; ++q) {
+              if constexpr (!kE4M3) a[g][j][q][h] = make_uint2(u[2 * q], u[2 * q + 1]);
+              else if constexpr (kKind == 0) a[g][j][q][h] = e4m3x4_to_half4(u[q]);
+              else a[g][j][q][h] = e4m3x4_to_bf16x4(u[q]);
+            }
           }
-        }
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
         if (!kFew && i >= tiles) break;
         if (!kFew) {
-          const uint16_t* src = values_of(n, min(8 * i + r, n.count - 1)) + c * 8 + st * kStageK;
+          const uint16_t* src = this->values_of(n, min(8 * i + r, n.count - 1)) + c * 8 + st * kStageK;
 #pragma unroll
           for (int h = 0; h < kParts; ++h)
 #pragma unroll
             for (int q = 0; q < kLoads; ++q) b[h][q] = ld_here(src + h * width + q * 32);
         }
-        float part[kChains][4];
+        float part[2][kChains][4];
         int nth = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -743,29 +836,41 @@ struct Worker {
 #pragma unroll
             for (int q = 0; q < kSteps; ++q, ++nth) {
               const uint4& v = b[h][j * (kLoads / 2) + q / 2];
-              if (nth < kChains) mma_16816<kE4M3 && kKind == 0, true>(part[nth % kChains], a[j][q][0], a[j][q][1], q & 1 ? v.z : v.x, q & 1 ? v.w : v.y);
-              else mma_16816<kE4M3 && kKind == 0, false>(part[nth % kChains], a[j][q][0], a[j][q][1], q & 1 ? v.z : v.x, q & 1 ? v.w : v.y);
+              const uint32_t b0 = q & 1 ? v.z : v.x, b1 = q & 1 ? v.w : v.y;
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                float(&d)[4] = part[g][nth % kChains];
+                if (nth < kChains) mma_16816<kE4M3 && kKind == 0, true>(d, a[g][j][q][0], a[g][j][q][1], b0, b1);
+                else mma_16816<kE4M3 && kKind == 0, false>(d, a[g][j][q][0], a[g][j][q][1], b0, b1);
+              }
             }
         // a block of k is summed by itself, then scaled
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float d = part[0][j];
-          if (kChains > 1) d += part[kChains - 1][j];
-          acc[i][j] = fmaf(d, j < 2 ? fu : fl, acc[i][j]);
-        }
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float d = part[g][0][j];
+            if (kChains > 1) d += part[g][kChains - 1][j];
+            acc[i][g][j] = fmaf(d, j < 2 ? fu : fl, acc[i][g][j]);
+          }
       }
     }
-    const int row = n.row + half * (kKind == 0 ? 8 : 16);
-    if (row >= (kKind == 1 ? p.m.H : n.shared ? p.m.Is : p.m.I)) return;  // the last unit's half
+    const int rows = kKind == 1 ? p.m.H : n.shared ? p.m.Is : p.m.I;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) {
       if (!kFew && i >= tiles) break;
-      finish<kKind>(n, row, 8 * i, acc[i]);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int row = n.row + g * (kKind == 0 ? 8 : 16);
+        if (row < rows) finish<kKind>(n, row, 8 * i, acc[i][g]);
+      }
     }
-    if (kKind == 0) {
-      ++hidden_done;
+    __syncwarp();
+    if (kKind == 0) {  // the other warp makes it known
+      if (lane == 0)
+        asm volatile("red.release.cta.shared.add.u32 [%0], 1;" ::"r"(smem_u32(&team.finished)) : "memory");
     } else {
-      if (lane == owed) owed_row = row;
+      if (lane == owed) owed_row = n.row;
       ++owed;
     }
   }
@@ -798,16 +903,7 @@ struct Worker {
     }
   }
 
-  // A fence waits for the stores before it: what units wrote is made known several units at a time.  
-  __device__ __forceinline__ void tell_hidden() {
-    if (!hidden_done) return;
-    __syncwarp();
-    if (lane == 0) {
-      __threadfence();
-      atomicAdd(p.counters + 1, (unsigned)hidden_done);
-    }
-    hidden_done = 0;
-  }
+  // A fence waits for the stores before it: what units wrote is made known several units at a time.
   static constexpr int kOwed = 4;
   __device__ __forceinline__ void tell_rows() {
     if (owed == 0) return;
@@ -815,7 +911,7 @@ struct Worker {
     unsigned before = 0;
     if (lane < owed) {
       __threadfence();
-      before = atomicAdd(p.counters + 2 + owed_row / 16, 1u);
+      before = atomicAdd(p.counters + 2 + owed_row / 32, 1u);
       __threadfence();
     }
     const unsigned last = __ballot_sync(~0u, lane < owed && before + 1 == (unsigned)(s.active + (p.m.Is ? 1 : 0)));
@@ -824,10 +920,11 @@ struct Worker {
     owed = 0;
   }
 
-  // 16 columns of the output, from the experts' rows in the order of the choice: the last of their units does it
+  // 32 columns of the output, from the experts' rows in the order of the choice: the last of their units does it
   __device__ __forceinline__ void join(int row) {
-    const int col = row + (lane & 3) * 4;
-    for (int t = lane >> 2; t < p.c.T; t += 8) {
+    const int col = row + (lane & 7) * 4;
+    if (col >= p.m.H) return;
+    for (int t = lane >> 3; t < p.c.T; t += 4) {
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int j = 0; j <= p.c.top_k; ++j) {
@@ -844,31 +941,16 @@ struct Worker {
   }
 
   __device__ __forceinline__ void run() {
-    if (half == 0) {
-      prepare_next();
-      fill();
-    }
-    for (worked = 0;; ++worked) {
-      if (half == 0 && worked == pushed && lane == 0) queue[worked % kQueue] = -1;
-      ok = team_sync(team, ok);
-      const int u = queue[worked % kQueue];
-      if (!ok || u < 0) break;
-      const Unit n = unit_of(u);
-      if (n.kind && !hidden_ready) {  // every unit of the first kind is in the hands of a team that waits for nothing
-        hidden_ready = true;
-        tell_hidden();
-        if (half == 0) {
-          for (uint32_t i = 0; ok; ++i) {
-            const unsigned done = (unsigned)ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1));
-            if (__all_sync(~0u, done >= (unsigned)halves_a)) break;
-            if (i == kSpinLimit) {
-              raise_error(p.c.err, kErrTimeout);
-              ok = false;
-            }
-            __nanosleep(32);
-          }
-          load_late();
+    for (;; ++worked) {
+      await_stage();
+      if (!ok) return;
+      const int u = team.queue[worked % kQueue];
+      if (u < 0) break;
+      const Unit n = this->unit_of(u);
+      if (n.kind && !hidden_ready) {  // the other warp has seen all of h; now this one
+        for (uint32_t i = 0; ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1)) < this->units_a && i < kSpinLimit; ++i) {
         }
+        hidden_ready = true;
       }
       if (n.kind == 0) {
         if (n.count <= 8) work<0, true>(n);
@@ -877,33 +959,12 @@ struct Worker {
         if (n.count <= 8) work<1, true>(n);
         else work<1, false>(n);
       }
-      if (!ok) break;
+      if (!ok) return;
       if (owed == kOwed) tell_rows();
-      if (half == 0) {
-        prepare_next();
-        fill();
-      }
     }
-    tell_hidden();
     tell_rows();
-    if (half) return;
-    if (!hidden_ready) load_late();  // a stage that lacks its values would never be full
-    // copies in flight land before the CTA ends, after a wait that ran out too
-    for (; ahead; --ahead) {
-      warp_wait(bars + 8 * now, pass);
-      if (++now == stages) now = 0, pass ^= 1;
-    }
   }
 };
-
-struct Rings {  // behind the teams' stages
-  Lists lists;
-  uint64_t bars[kTeams][kStages];
-  int queues[kTeams][kQueue];
-};
-constexpr size_t kSmem = 1024 + (size_t)kTeams * kRing + sizeof(Rings);
-static_assert(kSmem <= 232448, "");
-static_assert(kStages + 2 <= kQueue, "");
 
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ MoeParams p) {
@@ -911,51 +972,44 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
   uint8_t* smem = align1024(smem_raw);
   Rings& rings = *reinterpret_cast<Rings*>(smem + kTeams * kRing);
   Lists& s = rings.lists;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x < kTeams * kStages) mbar_init(smem_u32(&rings.bars[0][0] + threadIdx.x), 33);  // the weights; every lane's copies
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp & (kTeams - 1);
   if (threadIdx.x == 0) {
     prefetch_tensormap(&p.gate_up);
     prefetch_tensormap(&p.down);
   }
-  fence_mbar_init();
   await_grid();
-  const int team = warp >> 1;
-  Worker<kE4M3> w = {p,
-                     s,
-                     lane,
-                     team,
-                     warp & 1,
-                     smem_u32(smem + team * kRing),
-                     smem_u32(rings.bars[team]),
-                     rings.queues[team],
-                     s.scales[team]};
-  if (w.half == 0) w.take();
-  make_lists(p, s);
-  w.hidden_units = (p.m.I + 15) / 16;
-  w.out_units = (p.m.H + 31) / 32;
-  w.shared_units = (p.m.Is + 15) / 16;
-  w.halves_a = s.active * (p.m.I / 8) + p.m.Is / 8;
-  w.units_a = s.active * w.hidden_units + w.shared_units;
-  w.units = w.units_a + (s.active + (p.m.Is ? 1 : 0)) * w.out_units;
-  w.stages = kStages;
-  while (kRing / w.stages < kStageBytes + s.most * 2 * w.kRowBytes) --w.stages;  // h of the tokens of an expert beside its weights
-  w.stage_bytes = kRing / w.stages;
-  w.pushed = w.left = w.x = w.z = w.next = w.pieces = w.slot = w.ahead = w.worked = w.now = w.pass = w.stopped = 0;
-  w.hidden_done = w.owed = w.owed_row = 0;
-  w.load = Unit{};
-  w.first_to = 0;
-  w.values = nullptr;
-  w.map = nullptr;
-  w.next_upper = w.next_lower = 0.f;
-  w.more = w.ok = true;
-  w.next_ready = w.hidden_ready = false;
-  if (w.units == 0) {  // no token has an expert
+  unsigned ticket = 0;
+  if (warp < kTeams && lane == 0) ticket = atomicAdd(p.counters, 1u);
+  make_lists(p, rings.choice, s);
+  if (s.active == 0 && p.m.Is == 0) {  // no token has an expert
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.c.T * p.m.H / 8; i += gridDim.x * kThreads)
       reinterpret_cast<uint4*>(p.c.out)[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  w.run();
+  Team& team = rings.team[mine];  // where the choice was
+  if (warp < kTeams && lane < kStages) {
+    mbar_init(smem_u32(team.full + lane), 33);  // the weights; every lane's copies
+    mbar_init(smem_u32(team.empty + lane), 1);
+    if (lane == 0) team.finished = team.failed = 0;
+  }
+  fence_mbar_init();
+  __syncthreads();
+  const uint32_t ring = smem_u32(smem + mine * kRing);
+  // 512 threads are launched with 128 registers each
+  if (warp < kTeams) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    Loader<kE4M3> loader(p, s, team, ring);
+    loader.run(ticket);
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    Multiplier<kE4M3> worker(p, s, team, ring);
+    worker.run();
+  }
 }
+
+constexpr size_t kSmem = 1024 + (size_t)kTeams * kRing + sizeof(Rings);
+static_assert(kSmem <= 232448, "");
+static_assert(kStages + 2 <= kQueue, "");
 
 template <bool kE4M3>
 cudaError_t encode(CUtensorMap* map, const void* base, int k, int rows, int matrices, bool halves) {
