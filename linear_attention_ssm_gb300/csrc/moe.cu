@@ -38,15 +38,17 @@ constexpr uint32_t kSpinLimit = 1u << 22;  // polls of the counter of finished u
 constexpr int kBlock = 128;
 
 struct Layout {  // of the workspace
-  size_t counters, logits, x, x_scale, hidden, shared_hidden, y, bytes;
+  size_t counters, logits, ids, weights, x, x_scale, hidden, shared_hidden, y, bytes;
 };
 __host__ __device__ inline int pad256(int n) { return (n + 255) & ~255; }
 Layout layout(const Moe& m, int T, int k) {
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   Layout l;
   l.counters = 0;
-  l.logits = l.counters + up((2 + m.H / 16) * 4);
-  l.x = l.logits + up((size_t)T * (m.E + 1) * 4);
+  l.logits = l.counters + up((2 + (m.H + 31) / 32) * 4);
+  l.ids = l.logits + up((size_t)T * (m.E + 1) * 4);
+  l.weights = l.ids + up((size_t)T * k * 4);
+  l.x = l.weights + up((size_t)T * k * 4);
   l.x_scale = l.x + up((size_t)T * pad256(m.H) * 2);
   l.hidden = l.x_scale + up((size_t)T * 4);
   l.shared_hidden = l.hidden + up((size_t)T * k * pad256(m.I) * 4);
@@ -59,7 +61,10 @@ struct MoeParams {
   CUtensorMap gate_up, down, shared_gate_up, shared_down;  // boxes of 128 bytes x 16 rows x 2 halves, or x 32 rows x 1
   Moe m;
   MoeCall c;
-  unsigned* counters;  // next unit; first units done; for each 16 rows of the output, down units done
+  unsigned* counters;  // next unit; first units done; for each 32 rows of the output, down units done
+  bool chosen;         // a kernel of its own chooses
+  int32_t* ids;        // [T][top_k] and their weights, where a kernel of its own chooses
+  float* weights;
   float* logits;       // [T][E + 1], the shared gate's behind the experts'
   uint16_t* x;         // [T][pad256(H)] tokens in the products' order, bf16 or binary16
   float* x_scale;      // [T] what a binary16 token is multiplied with
@@ -109,15 +114,16 @@ __device__ __forceinline__ uint32_t order_key(float f) {
 
 constexpr int kPrepareWarps = 8, kPrepareThreads = kPrepareWarps * 32;
 
-// A CTA for each token's layout, then a warp for the dot products of one expert's row of the router (the shared gate's behind
-// the last) with up to 8 tokens.
+// A CTA for each token's layout, then one for the dot products of 4 rows of the router (the shared gate's behind the last)
+// with 8 tokens, whose warps split H.
+constexpr int kRows = 4;
 template <bool kE4M3>
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ MoeParams p) {
-  __shared__ float tops[kPrepareWarps];
+  __shared__ float tops[kPrepareWarps], parts[kPrepareWarps][32];
   await_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = p.m.H;
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < 2 + H / 16; i += kPrepareThreads) p.counters[i] = 0;
+    for (int i = threadIdx.x; i < 2 + (H + 31) / 32; i += kPrepareThreads) p.counters[i] = 0;
   if (blockIdx.x < p.c.T) {
     const int t = blockIdx.x;
     const uint16_t* x = p.c.x + t * p.c.x_stride;
@@ -169,40 +175,47 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     return;
   }
   // rows of the router, unless the routing is given, then the shared gate
-  const int groups = (p.c.T + 7) / 8, item = (blockIdx.x - p.c.T) * kPrepareWarps + warp;
-  const int e = (p.c.ids_in ? p.m.E : 0) + item / groups, t0 = item % groups * 8;
-  const uint16_t* w = e < p.m.E ? p.m.router + (size_t)e * H : p.m.shared_gate;
-  if (e > p.m.E || !w) return;
+  const int groups = (p.c.T + 7) / 8, item = blockIdx.x - p.c.T, t0 = item % groups * 8;
+  const int e0 = (p.c.ids_in ? p.m.E : 0) + item / groups * kRows, rows = min(kRows, p.m.E + (p.m.shared_gate ? 1 : 0) - e0);
   const int count = min(8, p.c.T - t0);
-  float sum[8] = {};
-  constexpr int kAhead = 4;  // pieces of a row in flight
-  for (int k0 = lane * 8; k0 < H; k0 += 256 * kAhead) {
-    uint4 a[kAhead];
+  float sum[32] = {};  // of row j and token i at 8 j + i
+  for (int k = threadIdx.x * 8; k < H; k += kPrepareThreads * 8) {
+    uint4 a[kRows], b[8];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) a[j] = k0 + 256 * j < H ? ld_once(w + k0 + 256 * j) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < kRows; ++j)
+      a[j] = j < rows ? ld_once((e0 + j < p.m.E ? p.m.router + (size_t)(e0 + j) * H : p.m.shared_gate) + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = i < count ? ld_here(p.c.x + (t0 + i) * p.c.x_stride + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i >= count) break;
-      uint4 b[kAhead];
+      const uint32_t bw[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j)
-        b[j] = k0 + 256 * j < H ? ld_here(p.c.x + (t0 + i) * p.c.x_stride + k0 + 256 * j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const uint32_t aw[4] = {a[j].x, a[j].y, a[j].z, a[j].w}, bw[4] = {b[j].x, b[j].y, b[j].z, b[j].w};
+      for (int j = 0; j < kRows; ++j) {
+        const uint32_t aw[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          sum[i] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), sum[i]);
-          sum[i] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), sum[i]);
+          sum[8 * j + i] = fmaf(__uint_as_float(aw[q] << 16), __uint_as_float(bw[q] << 16), sum[8 * j + i]);
+          sum[8 * j + i] = fmaf(__uint_as_float(aw[q] & 0xFFFF0000u), __uint_as_float(bw[q] & 0xFFFF0000u), sum[8 * j + i]);
         }
       }
     }
   }
+  // lane l gets sum l of the warp: halves of what is left are exchanged
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i >= count) break;
-    const float s = warp_sum(sum[i]);
-    if (lane == 0) p.logits[(size_t)(t0 + i) * (p.m.E + 1) + e] = s;
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float mine = lane & o ? sum[i + o] : sum[i], other = lane & o ? sum[i] : sum[i + o];
+      sum[i] = mine + __shfl_xor_sync(~0u, other, o);
+    }
+  parts[warp][lane] = sum[0];
+  __syncthreads();
+  if (warp == 0 && lane / 8 < rows && lane % 8 < count) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPrepareWarps; ++w) s += parts[w][lane];
+    p.logits[(size_t)(t0 + lane % 8) * (p.m.E + 1) + e0 + lane / 8] = s;
   }
 }
 
@@ -228,9 +241,9 @@ struct Lists {
 };
 constexpr uint16_t kNone = 0xFFFF;
 
-// One warp: token t's top_k experts and their weights.  A lane holds the keys of every 32nd expert.
+// One warp: token t's top_k experts and their weights, of choice j in lane j.  A lane holds the keys of every 32nd expert.
 template <int kOwn>
-__device__ __forceinline__ void choose(const MoeParams& p, Choice& s, int t, int lane) {
+__device__ __forceinline__ void choose(const MoeParams& p, int t, int lane, int& id, float& w) {
   const MoeCall& c = p.c;
   const int E = p.m.E;
   const float* l = p.logits + (size_t)t * (E + 1);
@@ -255,7 +268,7 @@ __device__ __forceinline__ void choose(const MoeParams& p, Choice& s, int t, int
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) key[i] = lane + 32 * i < E ? order_key(a[i]) : 0;
   }
-  int id = 0;  // lane j: choice j
+  id = 0;
   for (int j = 0; j < c.top_k; ++j) {
     uint32_t best = 0;
     int at = kMaxExperts;
@@ -272,7 +285,6 @@ __device__ __forceinline__ void choose(const MoeParams& p, Choice& s, int t, int
   }
   const bool chosen = lane < c.top_k;
   const float mine = chosen ? ld_f32(l + id) : 0.f;
-  float w;
   if (c.renormalise) {
     // in logarithms, relative to the largest: no score underflows before its sum is formed
     const float v = !c.sigmoid ? mine : fminf(mine, 0.f) - log1pf(expf(-fabsf(mine)));
@@ -284,13 +296,30 @@ __device__ __forceinline__ void choose(const MoeParams& p, Choice& s, int t, int
     w = score(mine);
   }
   w *= c.scale;
-  if (chosen) {
-    s.id[t][lane] = (int16_t)id;
-    s.weight[t][lane] = w;
-    if (blockIdx.x == 0) {
-      if (c.ids_out) c.ids_out[t * c.top_k + lane] = id;
-      if (c.weights_out) c.weights_out[t * c.top_k + lane] = w;
-    }
+  if (chosen && (p.chosen || blockIdx.x == 0)) {
+    if (c.ids_out) c.ids_out[t * c.top_k + lane] = id;
+    if (c.weights_out) c.weights_out[t * c.top_k + lane] = w;
+  }
+}
+__device__ __forceinline__ void choose_any(const MoeParams& p, int t, int lane, int& id, float& w) {
+  if (p.m.E <= 64) choose<2>(p, t, lane, id, w);
+  else if (p.m.E <= 128) choose<4>(p, t, lane, id, w);
+  else if (p.m.E <= 320) choose<10>(p, t, lane, id, w);
+  else choose<32>(p, t, lane, id, w);
+}
+// A warp for each token.  Up to 16 tokens every CTA of the next kernel chooses for itself.
+constexpr int kChooseWarps = 4;
+static_assert(kWarps == 16, "");
+__global__ void __launch_bounds__(kChooseWarps * 32) choose_kernel(const __grid_constant__ MoeParams p) {
+  await_grid();
+  const int t = blockIdx.x * kChooseWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= p.c.T) return;
+  int id;
+  float w;
+  choose_any(p, t, lane, id, w);
+  if (lane < p.c.top_k) {
+    p.ids[t * p.c.top_k + lane] = id;
+    p.weights[t * p.c.top_k + lane] = w;
   }
 }
 
@@ -302,23 +331,26 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, L
   for (int e = tid; e < E; e += kThreads) choice.mask[e] = 0;
   if (tid == 0) s.most = p.m.Is && T <= 8 ? T : 0;
   if (tid < T) s.x_scale[tid] = ld_f32(p.x_scale + tid);
-  if (p.c.ids_in) {
+  if (p.c.ids_in || p.chosen) {
+    const int32_t* ids = p.c.ids_in ? p.c.ids_in : p.ids;
+    const float* weights = p.c.ids_in ? p.c.weights_in : p.weights;
     for (int t = t0; t < T && j < k; t += kPass) {
       int id;
-      asm volatile("ld.global.b32 %0, [%1];" : "=r"(id) : "l"(p.c.ids_in + t * k + j));
+      asm volatile("ld.global.b32 %0, [%1];" : "=r"(id) : "l"(ids + t * k + j));
       if (id >= E) {
         if (blockIdx.x == 0) raise_error(p.c.err, kErrDeviceArgument);
         id = -1;
       }
       choice.id[t][j] = (int16_t)max(id, -1);
-      choice.weight[t][j] = ld_f32(p.c.weights_in + t * k + j);
+      choice.weight[t][j] = ld_f32(weights + t * k + j);
     }
-  } else {
-    for (int t = warp; t < T; t += kWarps) {
-      if (E <= 64) choose<2>(p, choice, t, lane);
-      else if (E <= 128) choose<4>(p, choice, t, lane);
-      else if (E <= 320) choose<10>(p, choice, t, lane);
-      else choose<32>(p, choice, t, lane);
+  } else if (warp < T) {
+    int id;
+    float w;
+    choose_any(p, warp, lane, id, w);
+    if (lane < k) {
+      choice.id[warp][lane] = (int16_t)id;
+      choice.weight[warp][lane] = w;
     }
   }
   __syncthreads();
@@ -480,11 +512,11 @@ __device__ __forceinline__ void copy_4(uint32_t dst, const void* src) {
 
 // A unit of work.
 struct Unit {
-  int kind;          // 0: 16 rows of gate and up, 1: 32 rows of down
+  int kind;          // 0: 16 rows of gate and up, 1: 32 rows of down, 2: 32 columns of the output for 8 tokens
   int a;             // the active expert, `active` for the shared one
   bool shared;
   int row, k;        // first row; length of a row
-  int first, count;  // the expert's slots
+  int first, count;  // the expert's slots; the first token
 };
 
 // Of a team: a warp that loads and one that multiplies.  A stage of their ring has 4 KB of weights and behind them, for an
@@ -514,7 +546,7 @@ struct Warp {
   Team& team;
   const int lane;
   const uint32_t ring;
-  int units_a, units;                           // of the first kind, of both
+  int units_a, units_b, units;                  // of the first kind, of the first two, of all
   int hidden_units, out_units, shared_units;    // units of an expert of either kind; of the shared one's first kind
   int stages;                                   // of the ring
   uint32_t stage_bytes;
@@ -525,13 +557,21 @@ struct Warp {
     out_units = (p.m.H + 31) / 32;
     shared_units = (p.m.Is + 15) / 16;
     units_a = s.active * hidden_units + shared_units;
-    units = units_a + (s.active + (p.m.Is ? 1 : 0)) * out_units;
+    units_b = units_a + (s.active + (p.m.Is ? 1 : 0)) * out_units;
+    units = units_b + (p.c.T + 7) / 8 * out_units;
     stages = kStages;
     while (kRing / stages < kStageBytes + s.most * 2 * kRowBytes) --stages;  // h of an expert's tokens beside its weights
     stage_bytes = kRing / stages;
   }
   __device__ __forceinline__ Unit unit_of(int u) const {  // the shared expert's are first: they take longest
     Unit n;
+    if (u >= units_b) {
+      n.kind = 2;
+      n.first = (unsigned)(u - units_b) / (unsigned)out_units;
+      n.row = (u - units_b - n.first * out_units) * 32;
+      n.first *= 8;
+      return n;
+    }
     n.kind = u >= units_a;
     const int each = n.kind ? out_units : hidden_units, before = p.m.Is ? (n.kind ? out_units : shared_units) : 0;
     const int v = (n.kind ? u - units_a : u) - before;
@@ -580,6 +620,7 @@ struct Loader : Warp<kE4M3> {
   uint32_t first_to;       // where this lane's first one goes in a stage
   const uint16_t* values;  // and where from
   int slot = 0, pass = 0;  // the next stage to load
+  int loaded = 0;
   bool ok = true, hidden_ready = false;
 
   __device__ __forceinline__ Loader(const MoeParams& params, const Lists& lists, Team& t, uint32_t at)
@@ -634,7 +675,10 @@ struct Loader : Warp<kE4M3> {
       __threadfence();
       atomicAdd(p.counters + 1, (unsigned)mine);
     }
-    if (late == 0) return;
+    if (late == 0) {
+      hidden_ready = true;
+      return;
+    }
     for (uint32_t i = 0;; ++i) {
       const unsigned done = (unsigned)ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1));
       if (__all_sync(~0u, done >= (unsigned)this->units_a)) break;
@@ -661,8 +705,20 @@ struct Loader : Warp<kE4M3> {
       if (i == kWaitLimit || *(volatile int*)&team.failed) return fail();
   }
 
+  // a stage without anything: the queue has news
+  __device__ __forceinline__ void pass_on() {
+    if (ok) await_place();
+    if (!ok) return;
+    __syncwarp();
+    const uint32_t bar = smem_u32(team.full + slot);
+    arrive(bar);
+    if (lane == 0) arrive(bar);
+    if (++slot == this->stages) slot = 0, pass ^= 1;
+    ++loaded;
+  }
+
   __device__ __forceinline__ void run(unsigned ticket) {
-    int mine = 0, late = 0, late_at = 0, late_unit = 0, pushed = 0, loaded = 0;
+    int mine = 0, late = 0, late_at = 0, late_unit = 0, pushed = 0;
     int next = (int)__shfl_sync(~0u, ticket, 0);
     while (ok && (unsigned)next < (unsigned)this->units) {
       const int q = pushed % kQueue;
@@ -670,6 +726,13 @@ struct Loader : Warp<kE4M3> {
       if (lane == 0) {
         team.queue[q] = next;
         ticket = atomicAdd(p.counters, 1u);  // the next unit's number, known later
+      }
+      if (n.kind == 2) {  // nothing to load
+        if (!hidden_ready) await_hidden(mine, late, late_at, late_unit);
+        pass_on();
+        ++pushed;
+        next = (int)__shfl_sync(~0u, ticket, 0);
+        continue;
       }
       if (kE4M3) {
         const float *upper, *lower;
@@ -703,14 +766,9 @@ struct Loader : Warp<kE4M3> {
       next = (int)__shfl_sync(~0u, ticket, 0);
     }
     if (ok && !hidden_ready) await_hidden(mine, late, late_at, late_unit);
-    if (ok) await_place();
-    if (ok) {  // no more
-      if (lane == 0) team.queue[pushed % kQueue] = -1;
-      __syncwarp();
-      arrive(smem_u32(team.full + slot));
-      if (lane == 0) arrive(smem_u32(team.full + slot));
-      return;
-    }
+    if (lane == 0) team.queue[pushed % kQueue] = -1;
+    pass_on();
+    if (ok) return;
     // a wait ran out: copies in flight land before the CTA ends
     for (int i = 0; i < late && !hidden_ready; ++i) copies_done_to(smem_u32(team.full + (late_at + i) % this->stages));
     for (int i = 0; i < loaded && i < this->stages; ++i) {
@@ -740,14 +798,14 @@ struct Multiplier : Warp<kE4M3> {
   __device__ __forceinline__ void await_stage() {
     const uint32_t bar = smem_u32(team.full + now);
     for (uint32_t i = 0; !warp_poll(bar, pass); ++i)
-      if (i == kWaitLimit || *(volatile int*)&team.failed) {
-        if (lane == 0) {
-          raise_error(p.c.err, kErrTimeout);
-          *(volatile int*)&team.failed = 1;
-        }
-        ok = false;
-        return;
-      }
+      if (i == kWaitLimit || *(volatile int*)&team.failed) return fail();
+  }
+  __device__ __forceinline__ void fail() {
+    if (lane == 0) {
+      raise_error(p.c.err, kErrTimeout);
+      *(volatile int*)&team.failed = 1;
+    }
+    ok = false;
   }
 
   // One unit; kFew: of at most 8 tokens, whose values are in the ring, else of up to 64.
@@ -906,27 +964,29 @@ struct Multiplier : Warp<kE4M3> {
   // A fence waits for the stores before it: what units wrote is made known several units at a time.
   static constexpr int kOwed = 4;
   __device__ __forceinline__ void tell_rows() {
-    if (owed == 0) return;
     __syncwarp();
-    unsigned before = 0;
     if (lane < owed) {
       __threadfence();
-      before = atomicAdd(p.counters + 2 + owed_row / 32, 1u);
-      __threadfence();
+      atomicAdd(p.counters + 2 + owed_row / 32, 1u);
     }
-    const unsigned last = __ballot_sync(~0u, lane < owed && before + 1 == (unsigned)(s.active + (p.m.Is ? 1 : 0)));
-    for (int i = 0; i < kOwed; ++i)
-      if (last >> i & 1) join(__shfl_sync(~0u, owed_row, i));
     owed = 0;
   }
 
-  // 32 columns of the output, from the experts' rows in the order of the choice: the last of their units does it
-  __device__ __forceinline__ void join(int row) {
-    const int col = row + (lane & 7) * 4;
+  // 32 columns of the output for 8 tokens, from the experts' rows in the order of the choice
+  __device__ __forceinline__ void join(const Unit& n) {
+    const int* done = reinterpret_cast<const int*>(p.counters + 2 + n.row / 32);
+    for (uint32_t i = 0; !__all_sync(~0u, ld_acquire_gpu(done) >= s.active + (p.m.Is ? 1 : 0)); ++i) {
+      if (i == kSpinLimit) return fail();
+      __nanosleep(32);
+    }
+    const int col = n.row + (lane & 7) * 4;
     if (col >= p.m.H) return;
-    for (int t = lane >> 3; t < p.c.T; t += 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = n.first + i * 4 + (lane >> 3);
+      if (t >= p.c.T) break;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 6
       for (int j = 0; j <= p.c.top_k; ++j) {
         const int slot = s.slot_of[t][j == p.c.top_k ? kMaxTopK : j];
         if (slot == kNone) continue;
@@ -947,6 +1007,15 @@ struct Multiplier : Warp<kE4M3> {
       const int u = team.queue[worked % kQueue];
       if (u < 0) break;
       const Unit n = this->unit_of(u);
+      if (n.kind == 2) {
+        __syncwarp();
+        first_arrive(smem_u32(team.empty + now));
+        if (++now == this->stages) now = 0, pass ^= 1;
+        tell_rows();
+        join(n);
+        if (!ok) return;
+        continue;
+      }
       if (n.kind && !hidden_ready) {  // the other warp has seen all of h; now this one
         for (uint32_t i = 0; ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1)) < this->units_a && i < kSpinLimit; ++i) {
         }
@@ -1036,8 +1105,11 @@ cudaError_t launch(const LaunchEnv& env, MoeParams& p) {
   if (e == cudaSuccess) e = encode<kE4M3>(&p.shared_gate_up, m.Is ? m.shared_gate_up : nullptr, m.H, m.Is, 2, true);
   if (e == cudaSuccess) e = encode<kE4M3>(&p.shared_down, m.Is ? m.shared_down : nullptr, m.Is, m.H, 1, false);
   if (e != cudaSuccess) return e;
-  const int dots = ((p.c.ids_in ? 0 : m.E) + (m.shared_gate ? 1 : 0)) * ((p.c.T + 7) / 8);
-  e = launch_early(prepare_kernel<kE4M3>, dim3(p.c.T + (dots + kPrepareWarps - 1) / kPrepareWarps), kPrepareThreads, 0, env.stream, p);
+  const int rows = (p.c.ids_in ? 0 : m.E) + (m.shared_gate ? 1 : 0), dots = (rows + kRows - 1) / kRows * ((p.c.T + 7) / 8);
+  e = launch_early(prepare_kernel<kE4M3>, dim3(p.c.T + dots), kPrepareThreads, 0, env.stream, p);
+  p.chosen = !p.c.ids_in && p.c.T > kWarps;
+  if (e == cudaSuccess && p.chosen)
+    e = launch_early(choose_kernel, dim3((p.c.T + kChooseWarps - 1) / kChooseWarps), kChooseWarps * 32, 0, env.stream, p);
   if (e != cudaSuccess) return e;
   return launch_early(experts_kernel<kE4M3>, dim3(sms), kThreads, kSmem, env.stream, p);
 }
@@ -1056,6 +1128,8 @@ cudaError_t launch_moe(const LaunchEnv& env, const Moe& m, MoeCall c, void* work
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.counters = reinterpret_cast<unsigned*>(ws + l.counters);
   p.logits = reinterpret_cast<float*>(ws + l.logits);
+  p.ids = reinterpret_cast<int32_t*>(ws + l.ids);
+  p.weights = reinterpret_cast<float*>(ws + l.weights);
   p.x = reinterpret_cast<uint16_t*>(ws + l.x);
   p.x_scale = reinterpret_cast<float*>(ws + l.x_scale);
   p.hidden = reinterpret_cast<uint16_t*>(ws + l.hidden);
