@@ -110,6 +110,9 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return (b >> 31 ? ~b : b | 0x80000000u) + 1;
 }
 
+// The next kernel of the stream may take its places on the SMs: it waits for this one's end all the same.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // ---------------------------------------------------------------- tokens and logits
 
 constexpr int kPrepareWarps = 8, kPrepareThreads = kPrepareWarps * 32;
@@ -120,6 +123,7 @@ constexpr int kRows = 4;
 template <bool kE4M3>
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ MoeParams p) {
   __shared__ float tops[kPrepareWarps], parts[kPrepareWarps][32];
+  let_next_start();
   await_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = p.m.H;
   if (blockIdx.x == 0)
@@ -311,6 +315,7 @@ __device__ __forceinline__ void choose_any(const MoeParams& p, int t, int lane, 
 constexpr int kChooseWarps = 4;
 static_assert(kWarps == 16, "");
 __global__ void __launch_bounds__(kChooseWarps * 32) choose_kernel(const __grid_constant__ MoeParams p) {
+  let_next_start();
   await_grid();
   const int t = blockIdx.x * kChooseWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (t >= p.c.T) return;
