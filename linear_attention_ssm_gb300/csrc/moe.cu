@@ -1,22 +1,32 @@
-// moe.cu -- a mixture-of-experts layer for a few tokens, in two kernels.
+// moe.cu -- a mixture-of-experts layer for a few tokens.
 //
 //   l = x Wr^T,  score = softmax(l) or sigmoid(l),  chosen = the top_k of score + bias
 //   h_e = silu(x G_e^T) * (x U_e^T),  out = sum_e weight_e h_e D_e^T + sigmoid(x . g) shared(x)
 //
-// The first kernel forms the logits and lays the tokens out for the second one, which streams the chosen experts' weights
-// once: HBM bounds it.  Every warp of it takes units of work from one list by an atomic counter -- first 8 rows of a gate
-// matrix with the 8 rows of the up projection beside them, over all of H (h for those 8 places and every token of the
-// expert), then 16 rows of a down projection over all of I -- and copies their weights by TMA into a ring of its own, which
-// runs ahead over the ends of units and from the first kind to the second: the wait for all of h falls into that time.
-// A unit is waited for only when it is a down one, and then every unit of the first kind has been taken by a warp that runs
-// and waits for nothing, so the kernel ends however few of its CTAs run at a time.
+// The first kernel forms the logits and lays the tokens out; with more than 16 tokens a second one chooses (16 warps of every
+// CTA of the last one do it otherwise: 64 tokens of 288 experts took 28 us there, 14 us with a kernel of their own).  The last
+// kernel streams the chosen experts' weights once, and HBM bounds it: 64 tokens of 288 experts of 4096 x 1536 and a shared
+// one, 3 GB of e4m3 weights, 645 us, 5.3 TB/s between the choice and the join; one token of 64 experts of 2048 x 1024, 50 MB,
+// 36 us, of which the logits take 3, the choice 5, and the two kinds of units 16 and 10 steps of a microsecond each that wait
+// for one another.
 //
-// Products are m16n8k16 of mma.sync: weights fill the 16 rows, an expert's tokens the 8 columns.  Both operands of a lane may
-// come from any places of k as long as they are the same ones; a lane reads 16-byte chunks of its rows, and the tokens lie in
-// memory in that order.  e4m3 weights become binary16 beside the tokens (exact; a token is divided by a power of two that
-// brings its largest value to 2^14 .. 2^15: values down to 2^-32 of the largest are exact, and what others lose is below
-// 2^-40 of it) and bf16 beside h, which has no bound known beforehand: it is held as a bf16 and the bf16 of what that lost,
-// 16 bits together, in two products.
+// Work is taken in units from one list by an atomic counter: 16 rows of a gate matrix with the 16 rows of the up projection
+// beside them, over all of H (h for those places and every token of the expert), then 32 rows of a down projection over all
+// of I, then 32 columns of the output for 8 tokens, whose sum over the experts is formed in the order of the choice.  A team
+// of two warps has a ring of stages in shared memory: one warp takes units and copies their weights by TMA and their tokens'
+// values by plain asynchronous copies, the other multiplies.  The ring runs ahead over the ends of units and from one kind
+// to the next, and the wait for all of h falls into that time.  (Eight warps that both loaded and multiplied took 1027 us
+// for the first of the sizes above, two warps that shared the products and of which one loaded 943: a copy's instructions
+// take about 1000 cycles a stage, as the products do.)  A unit is waited for only by units of the next kind, and by then
+// every unit of its kind has been taken by a team that runs and waits for nothing: the kernel ends however few of its CTAs
+// run at a time.
+//
+// Products are m16n8k16 of mma.sync: weights fill the 16 rows, an expert's tokens the 8 columns, so that a weight is an operand
+// as it lies in memory.  Both operands of a lane may come from any places of k as long as they are the same ones; a lane reads
+// 16-byte chunks of its rows, and the tokens lie in memory in that order.  e4m3 weights become binary16 beside the tokens
+// (exact; a token is divided by a power of two that brings its largest value to 2^14 .. 2^15: values down to 2^-32 of the
+// largest are exact, and what others lose is below 2^-40 of it) and bf16 beside h, which has no bound known beforehand: it is
+// held as a bf16 and the bf16 of what that lost, 16 bits together, in two products.
 #include <string.h>
 
 #include "attn_common.cuh"
@@ -311,9 +321,8 @@ __device__ __forceinline__ void choose_any(const MoeParams& p, int t, int lane, 
   else if (p.m.E <= 320) choose<10>(p, t, lane, id, w);
   else choose<32>(p, t, lane, id, w);
 }
-// A warp for each token.  Up to 16 tokens every CTA of the next kernel chooses for itself.
+// A warp for each token, where the next kernel's CTAs do not choose for themselves: they have a warp for each of 16 tokens.
 constexpr int kChooseWarps = 4;
-static_assert(kWarps == 16, "");
 __global__ void __launch_bounds__(kChooseWarps * 32) choose_kernel(const __grid_constant__ MoeParams p) {
   let_next_start();
   await_grid();
@@ -813,7 +822,8 @@ struct Multiplier : Warp<kE4M3> {
     ok = false;
   }
 
-  // One unit; kFew: of at most 8 tokens, whose values are in the ring, else of up to 64.
+  // One unit; kFew: of at most 8 tokens, whose values are in the ring, else of up to 64, whose values come through the cache
+  // (as stages of their own in the ring they took as long for 64 tokens of 8 experts, and a sixth longer for 64 of 64).
   template <int kKind, bool kFew>
   __device__ __forceinline__ void work(const Unit& n) {
     const int r = lane >> 2, c = lane & 3, width = pad256(n.k), steps = (n.k + kStageK - 1) / kStageK;
@@ -1069,7 +1079,8 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
   fence_mbar_init();
   __syncthreads();
   const uint32_t ring = smem_u32(smem + mine * kRing);
-  // 512 threads are launched with 128 registers each
+  // 512 threads are launched with 128 registers each; 56 in the warps that load leave 200 for the products of 64 tokens (with
+  // 72 and 184 an expert of 64 tokens takes 177 us instead of 150, and the cases with few tokens 2 to 4 % less)
   if (warp < kTeams) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     Loader<kE4M3> loader(p, s, team, ring);
@@ -1112,7 +1123,7 @@ cudaError_t launch(const LaunchEnv& env, MoeParams& p) {
   if (e != cudaSuccess) return e;
   const int rows = (p.c.ids_in ? 0 : m.E) + (m.shared_gate ? 1 : 0), dots = (rows + kRows - 1) / kRows * ((p.c.T + 7) / 8);
   e = launch_early(prepare_kernel<kE4M3>, dim3(p.c.T + dots), kPrepareThreads, 0, env.stream, p);
-  p.chosen = !p.c.ids_in && p.c.T > kWarps;
+  p.chosen = !p.c.ids_in && p.c.T > kWarps;  // more tokens than a CTA has warps
   if (e == cudaSuccess && p.chosen)
     e = launch_early(choose_kernel, dim3((p.c.T + kChooseWarps - 1) / kChooseWarps), kChooseWarps * 32, 0, env.stream, p);
   if (e != cudaSuccess) return e;
