@@ -3,8 +3,8 @@
 //   out[t, n] = sum_b sx[t, b] sw[n / 128, b] sum_{k in block b} x[t, k] w[n, k]
 //
 // The inner sum is four tcgen05 instructions on one 128-byte-wide stage of each operand; its result lies in tensor memory
-// and is taken into the running fp32 sums of the registers with the block's scales, while the next block's products run
-// into the other half of the accumulators.
+// and is taken into the running fp32 sums of the registers with the block's scales, while the next blocks' products run
+// into other places there.  Up to 16 tokens are too few for that: weights pass through the registers once.
 #include <string.h>
 
 #include "attn_common.cuh"
@@ -20,20 +20,13 @@ constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before givin
 // under a predicate of elect.sync in one piece of assembly.  Measured for a warp: a poll that finds its phase complete takes
 // 58 cycles this way, 255 in a branch of one lane; four products and two arrivals 270, 340 in a branch of the elected lane
 // and 560 in one of `lane == 0`, whose operands have to be gathered from that lane.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool cluster) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     uint32_t done;
-    if (cluster)
-      asm volatile(
-          "{\n.reg .pred p;\nmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-          : "=r"(done)
-          : "r"(bar), "r"(parity)
-          : "memory");
-    else
-      asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-                   : "=r"(done)
-                   : "r"(bar), "r"(parity)
-                   : "memory");
+    asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
     if (__all_sync(~0u, done)) return true;
   }
   return false;
@@ -146,8 +139,9 @@ constexpr int kFewWarps = 8;
 
 // One CTA: 16 rows of w and up to 8 kTiles tokens; its warps share the blocks of k.  A lane takes 16 codes of its two rows
 // and of its token at a time and widens them to binary16, which holds them exactly; which of a quad's lanes has which k does
-// not matter as long as both operands agree.  HBM bounds the kernel: 16 KB of weights in flight for each CTA, several CTAs an
-// SM, no barrier before the sums meet.
+// not matter as long as both operands agree.  HBM bounds the kernel: 32 KB of weights in flight for each CTA, three (two)
+// CTAs an SM, no barrier before the sums meet.  One token x 16384 x 2048 takes 9.3 us, 3.6 TB/s: the start of the kernel and
+// two and a half waves of CTAs that live for one trip to memory each.
 template <int kTiles>
 __global__ void __launch_bounds__(kFewWarps * 32, kTiles == 1 ? 3 : 2) few_kernel(const __grid_constant__ MatmulParams p) {
   __shared__ float parts[kFewWarps][kTiles][4][32];
@@ -310,7 +304,14 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& m
 }
 
 // kSplit: the CTAs of a cluster share a tile, each a part of its blocks; the parts are added up through the cluster's shared
-// memory, each CTA its share of the tokens, beginning with its own part (all at once from one CTA they would queue there).  Otherwise a CTA takes tile after tile.
+// memory, each CTA its share of the tokens, beginning with its own part (all at once from one CTA they would queue there).
+// Otherwise a CTA takes tile after tile.
+//
+// What bounds the large tiles is the tensor cores' time for a block, 518 cycles, and the sums' beside it, 128 columns a
+// thread of loads from tensor memory and packed multiply-adds (3.3 cycles a warp's instruction): 8192 tokens x 16384 x 4096
+// 460 to 500 us with the clocks that a second of it leaves, 2.2 to 2.4 PFLOP/s; 2048 x 4096 x 6144 51 us, 2.0 PFLOP/s.  Two
+// CTAs that shared a tile's loads by multicast, or one product over two SMs, were no faster.  The small ones are bound by
+// what a block waits for: 64 x 2048 x 6144 9.3 us, 777 x 5003 x 2041 (140 large tiles of 16 blocks) 19 us.
 template <int kN, bool kSplit>
 __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __grid_constant__ MatmulParams p) {
   using C = Tiles<kN>;
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
 
   bool ok = true;
   auto await = [&](uint32_t bar, uint32_t parity) {
-    if (ok && !warp_wait(bar, parity, false)) {
+    if (ok && !warp_wait(bar, parity)) {
       raise_error(p.err, kErrTimeout);
       ok = false;
     }
@@ -358,40 +359,40 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
   // large tiles: 384 threads are launched with 168 registers each; 56 in the first four warps leave 224 for the sums'
   if (warp < C::kFirst) {
     if constexpr (C::kLarge) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  if (warp == 0) {
-    int i = 0, pass = 0;  // stage, passes over the ring
-    for (int id = first; id < tiles && ok; id += step) {
-      int m, n;
-      tile_of(id, p.tiles_m, p.tiles_n, m, n);
-      for (int b = begin; b < end; ++b) {
-        if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
-        const uint32_t at = smem_u32(smem) + i * stage_bytes;
-        warp_load_stage(full + 8 * i, stage_bytes, at, &p.tmap_x, m * C::kTileM, at + x_bytes, &p.tmap_w, n * C::kTileN,
-                        b * kBlockK);
-        if (++i == stages) i = 0, ++pass;
+    if (warp == 0) {
+      int i = 0, pass = 0;  // stage, passes over the ring
+      for (int id = first; id < tiles && ok; id += step) {
+        int m, n;
+        tile_of(id, p.tiles_m, p.tiles_n, m, n);
+        for (int b = begin; b < end; ++b) {
+          if (pass && !await(empty + 8 * i, (pass - 1) & 1)) break;
+          const uint32_t at = smem_u32(smem) + i * stage_bytes;
+          warp_load_stage(full + 8 * i, stage_bytes, at, &p.tmap_x, m * C::kTileM, at + x_bytes, &p.tmap_w, n * C::kTileN,
+                          b * kBlockK);
+          if (++i == stages) i = 0, ++pass;
+        }
       }
-    }
-    // copies in flight land before the CTA ends, after a wait that ran out too
-    for (int c = 0; c < stages; ++c) {
-      const int passes = pass + (c < i);  // loads into stage c
-      if (passes) mbar_wait(full + 8 * c, (passes - 1) & 1, kWaitLimit);
-    }
-  } else if (warp == 1) {
-    // A full stage has its loads and the word of the sums that they have read what lay in its place of tensor memory: one wait
-    // for each block.  The tensor cores hold about two instructions ahead, and a wait takes 150 cycles beside them: with
-    // two the products of a block took 711 cycles instead of 552.
-    int i = 0, pass = 0, j = 0;
-    for (int id = first; id < tiles && ok; id += step)
-      for (int b = begin; b < end; ++b, ++j) {
-        if (!await(full + 8 * i, pass & 1)) break;
-        tc_fence_after();
-        const uint32_t at = smem_u32(smem) + i * stage_bytes;
-        warp_mma_e4m3(tmem + j % C::kBufs * kN, sw128_desc(at), sw128_desc(at + x_bytes),
-                      idesc_e4m3_f32(C::kTileM, kN), empty + 8 * i, done + 8 * (j % C::kBufs / C::kGroup),
-                      C::kGroup == 1 || j % C::kGroup == C::kGroup - 1 || b + 1 == end);
-        if (++i == stages) i = 0, ++pass;
+      // copies in flight land before the CTA ends, after a wait that ran out too
+      for (int c = 0; c < stages; ++c) {
+        const int passes = pass + (c < i);  // loads into stage c
+        if (passes) mbar_wait(full + 8 * c, (passes - 1) & 1, kWaitLimit);
       }
-  }
+    } else if (warp == 1) {
+      // A full stage has its loads and the word of the sums that they have read what lay in its place of tensor memory: one wait
+      // for each block.  The tensor cores hold about two instructions ahead, and a wait takes 150 cycles beside them: with
+      // two the products of a block took 711 cycles instead of 552.
+      int i = 0, pass = 0, j = 0;
+      for (int id = first; id < tiles && ok; id += step)
+        for (int b = begin; b < end; ++b, ++j) {
+          if (!await(full + 8 * i, pass & 1)) break;
+          tc_fence_after();
+          const uint32_t at = smem_u32(smem) + i * stage_bytes;
+          warp_mma_e4m3(tmem + j % C::kBufs * kN, sw128_desc(at), sw128_desc(at + x_bytes),
+                        idesc_e4m3_f32(C::kTileM, kN), empty + 8 * i, done + 8 * (j % C::kBufs / C::kGroup),
+                        C::kGroup == 1 || j % C::kGroup == C::kGroup - 1 || b + 1 == end);
+          if (++i == stages) i = 0, ++pass;
+        }
+    }
   } else {
     if constexpr (C::kLarge) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int quarter = warp & 3, own = warp - C::kFirst, side = own >> 2;  // side: of the columns
@@ -503,8 +504,8 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
         asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
         if (t < p.tokens)
 #pragma unroll
-        for (int i = 0; i < C::kCols / 4; ++i)
-          reinterpret_cast<float4*>(part)[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
+          for (int i = 0; i < C::kCols / 4; ++i)
+            reinterpret_cast<float4*>(part)[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
         break;
       }
       if (!ok) break;
@@ -643,7 +644,8 @@ cudaError_t encode_tiles(MatmulParams& p, const Fp8Matmul& m) {
   p.tiles_m = (int)((m.tokens + 127L) / 128);
   p.tiles_n = (int)((m.n + (long)kN - 1) / kN);
   // Rows of x that are not there are not asked for: filling them with zeroes takes the time of loads (17 tokens x
-  // 16384 x 2048 in tiles of 64 rows: 17.8 us with them, 12.5 without).  What the stage holds in their place reaches rows of the result that are not written.
+  // 16384 x 2048 in tiles of 64 rows: 17.8 us with them, 12.5 without).  What the stage holds in their place reaches rows of
+  // the result that are not written.
   p.rows_x = m.tokens < 128 ? (m.tokens + 7) / 8 * 8 : 128;
   const int fit = Tiles<kN>::kRing / ((p.rows_x + kN) * kBlockK);
   p.stages = fit < Tiles<kN>::kMaxStages ? fit : Tiles<kN>::kMaxStages;

@@ -1,0 +1,41 @@
+"""The kernels of the 8-bit product and of the expert layer are launched before the kernel ahead of them ends, so what that
+one writes is written in their lifetime: none of their loads may be of the non-coherent kind, nor one that the compiler may
+move past the wait, and none may come before it."""
+from __future__ import annotations
+
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "linear_attention_ssm_gb300", "csrc")
+FILES = ["fp8_quantize.cu", "fp8_matmul.cu", "moe.cu"]
+
+
+def code(name):
+    """The file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+@pytest.mark.parametrize("name", FILES)
+def test_loads_are_coherent_and_stay_behind_the_wait(name):
+    text = code(name)
+    assert not re.findall(r"__ldg\b|\bld\.global\.nc\b|__ldc[agsv]\b|__ldlu\b|__restrict__", text)
+    for asm in re.findall(r'asm\b(?! volatile)\s*\([^;]*', text):  # an asm that may be moved reads no memory
+        assert not re.search(r'"[^"]*\bld\.', asm), asm
+
+
+def test_every_kernel_waits_first():
+    kernels = {}
+    for name in FILES:
+        text = code(name)
+        for m in re.finditer(r"__global__ void[^;{]*?(\w+)\(const (?:__grid_constant__ )?\w+ p[^)]*\) \{", text):
+            body = text[m.end():]
+            wait = body.index("await_grid();")
+            kernels[m.group(1)] = re.search(
+                r"\bp\.(x|w|x_scale|w_scale|out|codes|scales|err|c\.\w+|m\.\w+\[|counters|logits|ids|weights|hidden|y)\b[\[ +]*[\[+]",
+                body[:wait])
+    assert {"quantize_rows_kernel", "quantize_blocks_kernel", "few_kernel", "tile_kernel", "prepare_kernel", "choose_kernel",
+            "experts_kernel"} <= set(kernels)
+    assert not any(kernels.values()), kernels

@@ -108,6 +108,18 @@ def test_product(T, N, K, dtype):
     assert torch.equal(got, g.gdn_fp8_matmul(x, xs, w, ws, out_dtype=dtype)), "two calls, the same bits"
 
 
+# either side of where tiles of 64 rows share their k among 4, 2 or 1 CTAs, and of where tiles of 256 rows begin, on a
+# device with 152 SMs; many tiles for each CTA; odd everything
+BORDERS = [(128, 38 * 64, 640), (100, 39 * 64, 640), (128, 76 * 64, 300), (120, 76 * 64 + 1, 300), (128, 152 * 64, 129),
+           (256, 76 * 64, 200), (129, 76 * 64 + 1, 200), (200, 5003, 129), (1500, 1603, 257), (2500, 4099, 1023)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,N,K", BORDERS)
+def test_product_where_tiles_change(T, N, K, dtype):
+    test_product(T, N, K, dtype)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("pad", [1, 3, 8, 250])
 @pytest.mark.parametrize("T,N,K", [(5, 129, 256), (130, 384, 200), (513, 250, 128)])
