@@ -108,10 +108,11 @@ def test_product(T, N, K, dtype):
     assert torch.equal(got, g.gdn_fp8_matmul(x, xs, w, ws, out_dtype=dtype)), "two calls, the same bits"
 
 
-# either side of where tiles of 64 rows share their k among 4, 2 or 1 CTAs, and of where tiles of 256 rows begin, on a
-# device with 152 SMs; many tiles for each CTA; odd everything
+# either side of where tiles of 64 rows share their k among 4, 2 or 1 CTAs, and of where tiles of 256 rows begin and share
+# theirs, on a device with 152 SMs; many tiles for each CTA; odd everything
 BORDERS = [(128, 38 * 64, 640), (100, 39 * 64, 640), (128, 76 * 64, 300), (120, 76 * 64 + 1, 300), (128, 152 * 64, 129),
-           (256, 76 * 64, 200), (129, 76 * 64 + 1, 200), (200, 5003, 129), (1500, 1603, 257), (2500, 4099, 1023)]
+           (256, 76 * 64, 200), (129, 76 * 64 + 1, 200), (200, 5003, 129), (1500, 1603, 257), (2500, 4099, 1023),
+           (70, 9793, 4097), (300, 4096, 4096), (128, 19456, 4000), (128, 19457, 4224)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
