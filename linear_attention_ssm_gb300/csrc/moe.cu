@@ -6,20 +6,20 @@
 // The first kernel forms the logits and lays the tokens out; with more than 16 tokens a second one chooses (16 warps of every
 // CTA of the last one do it otherwise: 64 tokens of 288 experts took 28 us there, 14 us with a kernel of their own).  The last
 // kernel streams the chosen experts' weights once, and HBM bounds it: 64 tokens of 288 experts of 4096 x 1536 and a shared
-// one, 3 GB of e4m3 weights, 645 us, 5.3 TB/s between the choice and the join; one token of 64 experts of 2048 x 1024, 50 MB,
-// 36 us, of which the logits take 3, the choice 5, and the two kinds of units 16 and 10 steps of a microsecond each that wait
-// for one another.
+// one, 3 GB of e4m3 weights, 575 us, 5.3 TB/s with everything; one token of 64 experts of 2048 x 1024, 50 MB, 33 us, of
+// which the logits take 3, the choice 5, and then 16 and 8 steps of about half a microsecond each wait for one another.
 //
 // Work is taken in units from one list by an atomic counter: 16 rows of a gate matrix with the 16 rows of the up projection
-// beside them, over all of H (h for those places and every token of the expert), then 32 rows of a down projection over all
-// of I, then 32 columns of the output for 8 tokens, whose sum over the experts is formed in the order of the choice.  A team
-// of two warps has a ring of stages in shared memory: one warp takes units and copies their weights by TMA and their tokens'
-// values by plain asynchronous copies, the other multiplies.  The ring runs ahead over the ends of units and from one kind
-// to the next, and the wait for all of h falls into that time.  (Eight warps that both loaded and multiplied took 1027 us
-// for the first of the sizes above, two warps that shared the products and of which one loaded 943: a copy's instructions
-// take about 1000 cycles a stage, as the products do.)  A unit is waited for only by units of the next kind, and by then
-// every unit of its kind has been taken by a team that runs and waits for nothing: the kernel ends however few of its CTAs
-// run at a time.
+// beside them, over all of H (h for those places and up to 8 of the expert's tokens), then 32 rows of a down projection over
+// all of I (for up to 4 tokens, whose h are in two parts), then 32 columns of the output for 8 tokens, whose sum over the
+// experts is formed in the order of the choice.  An expert of more tokens has units for each group of them, one after another
+// in the list: the first finds the weights in HBM, the others in L2.  A team of two warps has a ring of stages in shared
+// memory: one warp takes units and copies their weights by TMA and their tokens' values by plain asynchronous copies, the
+// other multiplies.  The ring runs ahead over the ends of units and from one kind to the next, and the wait for all of h falls
+// into that time.  (Eight warps that both loaded and multiplied took 1027 us for the first of the sizes above, two warps that
+// shared the products and of which one loaded 943; ten teams with rings of three stages take 560, and 36 for one token.)  A
+// unit is waited for only by units of the next kind, and by then every unit of its kind has been taken by a team that runs and
+// waits for nothing: the kernel ends however few of its CTAs run at a time.
 //
 // Products are m16n8k16 of mma.sync: weights fill the 16 rows, an expert's tokens the 8 columns, so that a weight is an operand
 // as it lies in memory.  Both operands of a lane may come from any places of k as long as they are the same ones; a lane reads
@@ -39,10 +39,9 @@ constexpr int kTeams = 8, kWarps = 2 * kTeams, kThreads = kWarps * 32;  // a tea
 constexpr int kMaxTokens = 64, kMaxTopK = 16, kMaxExperts = 1024;
 constexpr int kMaxSlots = kMaxTokens * (kMaxTopK + 1);  // (token, expert) pairs
 constexpr int kStageBytes = 4096;  // of weights: 32 rows of 128 bytes
-constexpr int kRing = 24576;       // of a team: 4 stages with 2 KB of values, or 3 with 4 KB
+constexpr int kValueRows = 8;       // beside them: columns of a product
 constexpr int kStages = 4;
-constexpr int kQueue = 8;          // units on their way: more than stages fit, and the one in hand
-constexpr int kScales = 32;        // of a unit's scales of either kind, as many blocks as are kept at hand
+constexpr int kQueue = 8;           // units on their way: more than stages, and the one in hand
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before giving up
 constexpr uint32_t kSpinLimit = 1u << 22;  // polls of the counter of finished units
 constexpr int kBlock = 128;
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
 struct Choice {  // on the way to the lists
   unsigned long long mask[kMaxExperts];  // tokens of an expert
   float weight[kMaxTokens][kMaxTopK];
-  uint32_t sums[kWarps];
+  unsigned long long sums[kWarps];
   uint16_t index[kMaxExperts];           // the active expert's number
   int16_t id[kMaxTokens][kMaxTopK];      // negative: none
 };
@@ -247,12 +246,16 @@ struct Lists {
   float weight[kMaxSlots];
   float x_scale[kMaxTokens];
   int active;                       // experts that have tokens
-  int most;                         // tokens of one, among those of up to 8
   uint16_t expert[kMaxExperts];     // of an active expert
   uint16_t first[kMaxExperts + 2];  // its first slot
+  // groups of an expert's tokens, the columns of a unit of either kind: those before it, and the expert of a group
+  uint16_t groups[2][kMaxExperts + 1];
+  uint16_t owner[2][kMaxExperts + kMaxTokens * kMaxTopK / 4];
   uint16_t slot_of[kMaxTokens][kMaxTopK + 1];  // kNone: none; the shared expert's last
   uint8_t token[kMaxSlots];
 };
+// tokens of a group: 8 columns hold so many tokens, or their h in two parts
+__host__ __device__ constexpr int group_of(int kind) { return kind ? 4 : 8; }
 constexpr uint16_t kNone = 0xFFFF;
 
 // One warp: token t's top_k experts and their weights, of choice j in lane j.  A lane holds the keys of every 32nd expert.
@@ -343,7 +346,6 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, L
   constexpr int kPass = kThreads / kMaxTopK;  // tokens at a time, a thread for each of their choices
   const int j = tid % kMaxTopK, t0 = tid / kMaxTopK;
   for (int e = tid; e < E; e += kThreads) choice.mask[e] = 0;
-  if (tid == 0) s.most = p.m.Is && T <= 8 ? T : 0;
   if (tid < T) s.x_scale[tid] = ld_f32(p.x_scale + tid);
   if (p.c.ids_in || p.chosen) {
     const int32_t* ids = p.c.ids_in ? p.c.ids_in : p.ids;
@@ -371,27 +373,27 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, L
   for (int t = t0; t < T && j < k; t += kPass)
     if (choice.id[t][j] >= 0) atomicOr(&choice.mask[choice.id[t][j]], 1ull << t);
   __syncthreads();
-  // experts that have tokens, in order: each thread has some neighbours; experts above, slots below in a word
+  // Experts that have tokens, in order: each thread has some neighbours.  Of those before it, 16 bits each: experts, slots,
+  // groups of the two kinds.
   constexpr int kOwn = (kMaxExperts + kThreads - 1) / kThreads;
-  uint32_t own = 0, most = 0;
+  typedef unsigned long long u64;
+  auto adds = [](int n) {
+    return n ? 1ull | (u64)n << 16 | (u64)((n + group_of(0) - 1) / group_of(0)) << 32 | (u64)((n + group_of(1) - 1) / group_of(1)) << 48 : 0ull;
+  };
+  u64 own = 0;
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
-    const int e = tid * kOwn + i, n = e < E ? __popcll(choice.mask[e]) : 0;
-    own += n ? 0x10000u + n : 0;
-    if (n <= 8) most = max(most, (uint32_t)n);
+    const int e = tid * kOwn + i;
+    own += adds(e < E ? __popcll(choice.mask[e]) : 0);
   }
-  uint32_t before = own;
+  u64 before = own;
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(~0u, before, o);
+    const u64 x = __shfl_up_sync(~0u, before, o);
     if (lane >= o) before += x;
   }
-  most = __reduce_max_sync(~0u, most);
-  if (lane == 31) {
-    choice.sums[warp] = before;
-    if (most) atomicMax(&s.most, (int)most);
-  }
+  if (lane == 31) choice.sums[warp] = before;
   __syncthreads();
-  uint32_t all = 0;
+  u64 all = 0;
   before -= own;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -402,17 +404,26 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, L
   for (int i = 0; i < kOwn; ++i) {
     const int e = tid * kOwn + i, n = e < E ? __popcll(choice.mask[e]) : 0;
     if (n) {
-      s.expert[before >> 16] = (uint16_t)e;
-      s.first[before >> 16] = (uint16_t)(before & 0xFFFF);
-      choice.index[e] = (uint16_t)(before >> 16);
-      before += 0x10000u + n;
+      const int a = before & 0xFFFF;
+      s.expert[a] = (uint16_t)e;
+      s.first[a] = (uint16_t)(before >> 16);
+      choice.index[e] = (uint16_t)a;
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        const int g = before >> (32 + 16 * kind) & 0xFFFF;
+        s.groups[kind][a] = (uint16_t)g;
+        for (int q = 0; q * group_of(kind) < n; ++q) s.owner[kind][g + q] = (uint16_t)a;
+      }
+      before += adds(n);
     }
   }
-  const int active = all >> 16, slots = all & 0xFFFF;
+  const int active = all & 0xFFFF, slots = all >> 16 & 0xFFFF;
   if (tid == 0) {
     s.active = active;
     s.first[active] = (uint16_t)slots;  // the shared expert's slots are behind the others'
     s.first[active + 1] = (uint16_t)(slots + T);
+    s.groups[0][active] = (uint16_t)(all >> 32);
+    s.groups[1][active] = (uint16_t)(all >> 48);
   }
   __syncthreads();
   for (int t = t0; t < T && j < k; t += kPass) {
@@ -530,54 +541,53 @@ struct Unit {
   int a;             // the active expert, `active` for the shared one
   bool shared;
   int row, k;        // first row; length of a row
-  int first, count;  // the expert's slots; the first token
+  int first, count;  // slots of a group of the expert's tokens; the first token
 };
 
-// Of a team: a warp that loads and one that multiplies.  A stage of their ring has 4 KB of weights and behind them, for an
-// expert of up to 8 tokens, the tokens' values for the same k (loads through the cache take several thousand cycles while
-// the copies fill the memory's queues).
-struct Team {
-  float scales[kQueue][2][kScales];  // of the units on their way
-  uint64_t full[kStages], empty[kStages];
-  int queue[kQueue];  // units on their way; negative: no more
-  int finished;       // units of the first kind
-  int failed;         // a wait ran out
+// Of a team: a warp that loads and one that multiplies.  A stage of their ring has 4 KB of weights and behind them the tokens'
+// values for the same k (loads through the cache take several thousand cycles while the copies fill the memory's queues):
+// a row for each token, or two for the two parts of its h.
+template <bool kE4M3>
+struct Stage {
+  static constexpr int kK = kE4M3 ? 128 : 64;  // values of a row
+  static constexpr int kRowBytes = 2 * kK;     // of values
+  static constexpr int kBytes = (kStageBytes + kValueRows * kRowBytes + 1023) / 1024 * 1024;
 };
-struct Rings {  // behind the teams' stages
-  union {
-    Choice choice;
-    Team team[kTeams];
-  };
-  Lists lists;
+struct Team {
+  uint64_t full[kStages], empty[kStages];
+  float scales[kStages][2];  // of a stage's rows: of gate and up, or of down
+  int queue[kQueue];         // units on their way; negative: no more
+  int finished;              // units of the first kind
+  int failed;                // a wait ran out
 };
 
 template <bool kE4M3>
 struct Warp {
-  static constexpr int kStageK = kE4M3 ? 128 : 64;  // of a stage
-  static constexpr int kRowBytes = 2 * kStageK;     // of a token in a stage
+  using S = Stage<kE4M3>;
   const MoeParams& p;
   const Lists& s;
   Team& team;
   const int lane;
   const uint32_t ring;
-  int units_a, units_b, units;                  // of the first kind, of the first two, of all
-  int hidden_units, out_units, shared_units;    // units of an expert of either kind; of the shared one's first kind
-  int stages;                                   // of the ring
-  uint32_t stage_bytes;
+  int units_a, units_b, units;                // of the first kind, of the first two, of all
+  int hidden_units, out_units, shared_units;  // units of a group of either kind; of the shared expert's first kind
 
   __device__ __forceinline__ Warp(const MoeParams& params, const Lists& lists, Team& t, uint32_t at)
       : p(params), s(lists), team(t), lane(threadIdx.x & 31), ring(at) {
     hidden_units = (p.m.I + 15) / 16;
     out_units = (p.m.H + 31) / 32;
     shared_units = (p.m.Is + 15) / 16;
-    units_a = s.active * hidden_units + shared_units;
-    units_b = units_a + (s.active + (p.m.Is ? 1 : 0)) * out_units;
+    units_a = s.groups[0][s.active] * hidden_units + shared_groups(0) * shared_units;
+    units_b = units_a + rows_of_y() * out_units;
     units = units_b + (p.c.T + 7) / 8 * out_units;
-    stages = kStages;
-    while (kRing / stages < kStageBytes + s.most * 2 * kRowBytes) --stages;  // h of an expert's tokens beside its weights
-    stage_bytes = kRing / stages;
   }
-  __device__ __forceinline__ Unit unit_of(int u) const {  // the shared expert's are first: they take longest
+  __device__ __forceinline__ int shared_groups(int kind) const {
+    return p.m.Is ? (p.c.T + group_of(kind) - 1) / group_of(kind) : 0;
+  }
+  __device__ __forceinline__ int rows_of_y() const { return s.groups[1][s.active] + shared_groups(1); }  // units of 32 columns
+  // Units of the groups of an expert that have the same rows follow one another: the second one finds the weights in L2.
+  // The shared expert's are first.
+  __device__ __forceinline__ Unit unit_of(int u) const {
     Unit n;
     if (u >= units_b) {
       n.kind = 2;
@@ -587,34 +597,25 @@ struct Warp {
       return n;
     }
     n.kind = u >= units_a;
-    const int each = n.kind ? out_units : hidden_units, before = p.m.Is ? (n.kind ? out_units : shared_units) : 0;
-    const int v = (n.kind ? u - units_a : u) - before;
-    n.shared = v < 0;
-    n.a = n.shared ? s.active : (unsigned)v / (unsigned)each;
-    n.row = (n.shared ? v + before : v - n.a * each) * (n.kind ? 32 : 16);
-    n.k = !n.kind ? p.m.H : n.shared ? p.m.Is : p.m.I;
-    n.first = s.first[n.a];
-    n.count = s.first[n.a + 1] - n.first;
-    return n;
-  }
-  // where token `rank` of the unit has its values
-  __device__ __forceinline__ const uint16_t* values_of(const Unit& n, int rank) const {
-    const size_t row = n.kind == 0 ? s.token[n.first + rank] : 2 * (size_t)(n.shared ? rank : n.first + rank);
-    return (n.kind == 0 ? p.x : n.shared ? p.shared_hidden : p.hidden) + row * pad256(n.k);
-  }
-  // the scales of a unit's rows by blocks of k: of gate and of up, or of down
-  __device__ __forceinline__ void scales_of(const Unit& n, const float*& upper, const float*& lower) const {
-    const int kb = (n.k + kBlock - 1) / kBlock;
-    if (n.kind) {
-      const int rb = (p.m.H + kBlock - 1) / kBlock;
-      const float* base = n.shared ? p.m.shared_down_scale : p.m.down_scale + (size_t)s.expert[n.a] * rb * kb;
-      upper = lower = base + (size_t)(n.row / kBlock) * kb;
+    int v = n.kind ? u - units_a : u, groups = shared_groups(n.kind);
+    const int before = groups * (n.kind ? out_units : shared_units);
+    n.shared = v < before;
+    if (n.shared) {
+      n.a = s.active;
     } else {
-      const int rb = ((n.shared ? p.m.Is : p.m.I) + kBlock - 1) / kBlock;
-      const float* base = n.shared ? p.m.shared_gate_up_scale : p.m.gate_up_scale + (size_t)s.expert[n.a] * 2 * rb * kb;
-      upper = base + (size_t)(n.row / kBlock) * kb;
-      lower = upper + (size_t)rb * kb;
+      const int each = n.kind ? out_units : hidden_units;
+      v -= before;
+      n.a = s.owner[n.kind][(unsigned)v / (unsigned)each];
+      const int g = s.groups[n.kind][n.a];
+      groups = s.groups[n.kind][n.a + 1] - g;
+      v -= g * each;
     }
+    const int row = groups == 1 ? v : (unsigned)v / (unsigned)groups;
+    n.row = row * (n.kind ? 32 : 16);
+    n.k = !n.kind ? p.m.H : n.shared ? p.m.Is : p.m.I;
+    n.first = s.first[n.a] + (v - row * groups) * group_of(n.kind);
+    n.count = min(group_of(n.kind), s.first[n.a + 1] - n.first);
+    return n;
   }
 };
 
@@ -622,51 +623,50 @@ struct Warp {
 template <bool kE4M3>
 struct Loader : Warp<kE4M3> {
   using W = Warp<kE4M3>;
-  using W::kRowBytes;
-  using W::kStageK;
+  using S = Stage<kE4M3>;
   using W::lane;
   using W::p;
   using W::s;
   using W::team;
-  static constexpr int kPieces = kRowBytes / 16;  // of 16 bytes of a token's values
-  Unit load;
-  int pieces;              // of 16 bytes, of a stage's values
-  uint32_t first_to;       // where this lane's first one goes in a stage
-  const uint16_t* values;  // and where from
-  int slot = 0, pass = 0;  // the next stage to load
-  int loaded = 0;
+  static constexpr int kPieces = S::kRowBytes / 16;             // of 16 bytes of a row of values
+  static constexpr int kStep = 32 / kPieces, kIts = kValueRows / kStep;  // rows at a time
+  static_assert(kStep % 2 == 0, "");
+  // of the unit that is loaded
+  int rows, steps, kind;
+  const uint16_t* base;
+  uint32_t from[kIts];  // this lane's piece of its rows of values
+  uint32_t to;          // where the first one goes in a stage
+  // the next stage to load
+  int slot = 0, pass = 0, loaded = 0;
   bool ok = true, hidden_ready = false;
 
   __device__ __forceinline__ Loader(const MoeParams& params, const Lists& lists, Team& t, uint32_t at)
-      : W(params, lists, t, at) {}
-
-  // Pieces 4 apart are swapped for odd tokens: a quarter warp reads 4 pieces of two tokens.
-  __device__ __forceinline__ static uint32_t place_of(int kind, int row, int piece) {
-    return kStageBytes + row * kRowBytes + ((piece ^ (kind ? row & 2 : (row & 1) << 1) << 1) << 4);
-  }
-  // the unit whose values are loaded
-  __device__ __forceinline__ void aim(const Unit& n) {
-    load = n;
+      : W(params, lists, t, at) {
+    // pieces 4 apart are swapped in odd rows: a quarter warp reads 4 pieces of two rows
     const int row = lane / kPieces, piece = lane % kPieces;
-    pieces = n.count > 8 ? 0 : n.count * (n.kind + 1) * kPieces;
-    first_to = place_of(n.kind, row, piece);
-    values = nullptr;
-    if (lane < pieces)
-      values = (n.kind ? this->values_of(n, 0) + (size_t)row * pad256(n.k) : this->values_of(n, row)) + piece * 8;
+    to = kStageBytes + row * S::kRowBytes + ((piece ^ (row & 1) << 2) << 4);
   }
-  // The tokens' values of a stage: rows of 16-byte pieces, h in two parts.
-  __device__ __forceinline__ void load_values(uint32_t at, int k, uint32_t bar) {
-    if (lane < pieces) copy_16(at + first_to, values + k);
-    if (pieces > 32) {
-      const int piece = lane % kPieces, width = pad256(load.k);
-#pragma unroll 1
-      for (int q = lane + 32; q < pieces; q += 32) {
-        const int row = q / kPieces;
-        const uint16_t* from = load.kind ? values + (size_t)(row - lane / kPieces) * width : this->values_of(load, row) + piece * 8;
-        copy_16(at + place_of(load.kind, row, piece), from + k);
-      }
+  __device__ __forceinline__ void aim(const Unit& n) {
+    kind = n.kind;
+    rows = n.count * (kind + 1);
+    steps = (n.k + S::kK - 1) / S::kK;
+    base = !kind ? p.x : n.shared ? p.shared_hidden : p.hidden;
+    const int first = 2 * (n.first - (n.shared ? s.first[n.a] : 0));
+#pragma unroll
+    for (int i = 0; i < kIts; ++i) {
+      const int row = min(lane / kPieces + i * kStep, rows - 1);
+      from[i] = (kind ? first + row : s.token[n.first + row]) * pad256(n.k) + lane % kPieces * 8;
     }
-    copies_done_to(bar);  // a unit's scales too
+  }
+  __device__ __forceinline__ void load_values(uint32_t at, int k, uint32_t bar) {
+    const int mine = rows - lane / kPieces;
+    if (mine > 0) copy_16(at + to, base + from[0] + k);
+    if (rows > kStep) {
+#pragma unroll
+      for (int i = 1; i < kIts; ++i)
+        if (mine > i * kStep) copy_16(at + to + i * kStep * S::kRowBytes, base + from[i] + k);
+    }
+    copies_done_to(bar);  // the scales too
   }
   __device__ __forceinline__ void fail() {
     if (ok && lane == 0) {
@@ -699,17 +699,15 @@ struct Loader : Warp<kE4M3> {
       if (i == kSpinLimit) return fail();
       __nanosleep(32);
     }
-    const Unit loading = load;
     int st = 0;
     for (int i = 0; i < late; ++i) {
-      if (i == 0 || st == (load.k + kStageK - 1) / kStageK) {
+      if (i == 0 || st == steps) {
         aim(this->unit_of(team.queue[unit++ % kQueue]));
         st = 0;
       }
-      load_values(this->ring + at * this->stage_bytes, st++ * kStageK, smem_u32(team.full + at));
-      if (++at == this->stages) at = 0;
+      load_values(this->ring + at * S::kBytes, st++ * S::kK, smem_u32(team.full + at));
+      if (++at == kStages) at = 0;
     }
-    aim(loading);
     hidden_ready = true;
   }
   // waits until the next stage may be loaded
@@ -718,7 +716,10 @@ struct Loader : Warp<kE4M3> {
     for (uint32_t i = 0; !warp_poll(bar, pass ^ 1); ++i)
       if (i == kWaitLimit || *(volatile int*)&team.failed) return fail();
   }
-
+  __device__ __forceinline__ void next_stage() {
+    if (++slot == kStages) slot = 0, pass ^= 1;
+    ++loaded;
+  }
   // a stage without anything: the queue has news
   __device__ __forceinline__ void pass_on() {
     if (ok) await_place();
@@ -727,18 +728,16 @@ struct Loader : Warp<kE4M3> {
     const uint32_t bar = smem_u32(team.full + slot);
     arrive(bar);
     if (lane == 0) arrive(bar);
-    if (++slot == this->stages) slot = 0, pass ^= 1;
-    ++loaded;
+    next_stage();
   }
 
   __device__ __forceinline__ void run(unsigned ticket) {
     int mine = 0, late = 0, late_at = 0, late_unit = 0, pushed = 0;
     int next = (int)__shfl_sync(~0u, ticket, 0);
     while (ok && (unsigned)next < (unsigned)this->units) {
-      const int q = pushed % kQueue;
       const Unit n = this->unit_of(next);
       if (lane == 0) {
-        team.queue[q] = next;
+        team.queue[pushed % kQueue] = next;
         ticket = atomicAdd(p.counters, 1u);  // the next unit's number, known later
       }
       if (n.kind == 2) {  // nothing to load
@@ -748,33 +747,41 @@ struct Loader : Warp<kE4M3> {
         next = (int)__shfl_sync(~0u, ticket, 0);
         continue;
       }
+      aim(n);
+      const float* scale = nullptr;  // lane 0: of gate, or of down; lane 1: of up, or of down
       if (kE4M3) {
-        const float *upper, *lower;
-        this->scales_of(n, upper, lower);
-        if (lane < (n.k + kBlock - 1) / kBlock) {
-          copy_4(smem_u32(&team.scales[q][0][lane]), upper + lane);
-          if (!n.kind) copy_4(smem_u32(&team.scales[q][1][lane]), lower + lane);
+        const int kb = (n.k + kBlock - 1) / kBlock, e = n.shared ? 0 : s.expert[n.a];
+        if (n.kind) {
+          const int rb = (p.m.H + kBlock - 1) / kBlock;
+          scale = (n.shared ? p.m.shared_down_scale : p.m.down_scale) + ((size_t)e * rb + n.row / kBlock) * kb;
+        } else {
+          const int rb = ((n.shared ? p.m.Is : p.m.I) + kBlock - 1) / kBlock;
+          scale = (n.shared ? p.m.shared_gate_up_scale : p.m.gate_up_scale) +
+                  (((size_t)e * 2 + (lane & 1)) * rb + n.row / kBlock) * kb;
         }
       }
-      aim(n);
       const void* map = n.kind ? (n.shared ? &p.shared_down : &p.down) : (n.shared ? &p.shared_gate_up : &p.gate_up);
-      const int z = n.shared ? 0 : s.expert[n.a] * (n.kind ? 1 : 2), steps = (n.k + kStageK - 1) / kStageK;
+      const int z = n.shared ? 0 : s.expert[n.a] * (n.kind ? 1 : 2);
       if (n.kind == 0) ++mine;
       __syncwarp();
 #pragma unroll 1
       for (int st = 0; st < steps; ++st) {
-        if (n.kind && !hidden_ready) {
-          if (late == this->stages) await_hidden(mine, late, late_at, late_unit);
-          else if (late++ == 0) late_at = slot, late_unit = pushed;
+        if (kind && !hidden_ready) {
+          if (late == kStages) {
+            await_hidden(mine, late, late_at, late_unit);
+            aim(n);
+          } else if (late++ == 0) {
+            late_at = slot;
+            late_unit = pushed;
+          }
         }
         await_place();
         if (!ok) break;
-        const uint32_t bar = smem_u32(team.full + slot), at = this->ring + slot * this->stage_bytes;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // values that lay there came by plain copies
-        warp_load(at, map, st * kStageK, n.row, z, bar);
-        if (n.kind == 0 || hidden_ready) load_values(at, st * kStageK, bar);
-        if (++slot == this->stages) slot = 0, pass ^= 1;
-        ++loaded;
+        const uint32_t bar = smem_u32(team.full + slot), at = this->ring + slot * S::kBytes;
+        warp_load(at, map, st * S::kK, n.row, z, bar);
+        if (kE4M3 && lane < 2) copy_4(smem_u32(&team.scales[slot][lane]), scale + st);
+        if (!kind || hidden_ready) load_values(at, st * S::kK, bar);
+        next_stage();
       }
       ++pushed;
       next = (int)__shfl_sync(~0u, ticket, 0);
@@ -784,9 +791,9 @@ struct Loader : Warp<kE4M3> {
     pass_on();
     if (ok) return;
     // a wait ran out: copies in flight land before the CTA ends
-    for (int i = 0; i < late && !hidden_ready; ++i) copies_done_to(smem_u32(team.full + (late_at + i) % this->stages));
-    for (int i = 0; i < loaded && i < this->stages; ++i) {
-      if (slot-- == 0) slot = this->stages - 1, pass ^= 1;
+    for (int i = 0; i < late && !hidden_ready; ++i) copies_done_to(smem_u32(team.full + (late_at + i) % kStages));
+    for (int i = 0; i < loaded && i < kStages; ++i) {
+      if (slot-- == 0) slot = kStages - 1, pass ^= 1;
       warp_wait(smem_u32(team.full + slot), pass);
     }
   }
@@ -796,15 +803,14 @@ struct Loader : Warp<kE4M3> {
 template <bool kE4M3>
 struct Multiplier : Warp<kE4M3> {
   using W = Warp<kE4M3>;
-  using W::kRowBytes;
-  using W::kStageK;
+  using S = Stage<kE4M3>;
   using W::lane;
   using W::p;
   using W::s;
   using W::team;
   int worked = 0, now = 0, pass = 0;  // units; the next stage
   int owed = 0, owed_row = 0;         // units of the second kind not yet told; lane i: the row of unit i
-  bool ok = true, hidden_ready = false;
+  bool ok = true;
 
   __device__ __forceinline__ Multiplier(const MoeParams& params, const Lists& lists, Team& t, uint32_t at)
       : W(params, lists, t, at) {}
@@ -822,121 +828,69 @@ struct Multiplier : Warp<kE4M3> {
     ok = false;
   }
 
-  // One unit; kFew: of at most 8 tokens, whose values are in the ring, else of up to 64, whose values come through the cache
-  // (as stages of their own in the ring they took as long for 64 tokens of 8 experts, and a sixth longer for 64 of 64).
-  template <int kKind, bool kFew>
+  // One unit.  The loop is short on purpose: every warp is at another place of the code, and waits for its instructions more
+  // than for anything else.  64 tokens of 288 experts take 575 us so, 637 with both chunks in one pass of the loop, 1150 with
+  // two stages in one, the next one's loads before the products; 595 with halves of chunks.
+  template <int kKind>
   __device__ __forceinline__ void work(const Unit& n) {
-    const int r = lane >> 2, c = lane & 3, width = pad256(n.k), steps = (n.k + kStageK - 1) / kStageK;
-    constexpr int kTiles = kFew ? 1 : 8;
-    constexpr int kLoads = kE4M3 ? 4 : 2;       // of a lane from a token for a stage, 32 values apart
-    constexpr int kParts = kKind == 0 ? 1 : 2;  // h is held in two
-    constexpr int kSteps = kE4M3 ? 4 : 2;       // products of a chunk
-    constexpr int kChains = kFew ? 2 : 1;       // sums that do not wait for one another
-    const int tiles = kFew ? 1 : (n.count + 7) / 8;
-    float acc[kTiles][2][4];                    // the two groups of 16 rows
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j >> 2][j & 3] = 0.f;
-    const float(*at_hand)[kScales] = team.scales[worked % kQueue];
-    const float *upper = nullptr, *lower = nullptr;
-    if (kE4M3 && n.k > kScales * kBlock) this->scales_of(n, upper, lower);
-    // rows r and r + 8 of a group: in gate and up, or in down
-    const uint32_t apart = kKind == 0 ? 2048 : 1024, group = kKind == 0 ? 1024 : 2048;
-    const uint32_t place0 = r * 128 + ((2 * c ^ r) << 4), place1 = r * 128 + (((2 * c + 1) ^ r) << 4);
-    // columns behind the last token repeat it, and are not stored
-    const int rank = min(r, n.count - 1);
-    const uint32_t values0 = kStageBytes + rank * kParts * kRowBytes + c * 16 + (rank & 1) * 64;
+    const int r = lane >> 2, c = lane & 3, steps = (n.k + S::kK - 1) / S::kK;
+    constexpr int kLoads = kE4M3 ? 2 : 1;  // of a lane from a row of values for a chunk, 32 values apart
+    constexpr int kSteps = kE4M3 ? 4 : 2;  // products of a chunk
+    // rows r and r + 8 of a group of 16: in gate and up, or in down
+    constexpr uint32_t apart = kKind == 0 ? 2048 : 1024, group = kKind == 0 ? 1024 : 2048;
+    // columns behind the last row of values repeat it, and are not stored
+    const int row = min(r, n.count * (kKind + 1) - 1);
+    const uint32_t weights = r * 128 + ((2 * c ^ r) << 4);
+    const uint32_t values = kStageBytes + row * S::kRowBytes + c * 16 + (row & 1) * 64;
+    float acc[2][4] = {};
 #pragma unroll 1
     for (int st = 0; st < steps; ++st) {
       await_stage();
-      if (!ok) return;
-      const uint32_t at = this->ring + now * this->stage_bytes;
-      // chunks 2 c and 2 c + 1 of the rows, swizzled
-      uint4 w[2][2][2], b[kParts][kLoads];
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          w[g][0][h] = lds128(at + g * group + h * apart + place0);
-          w[g][1][h] = lds128(at + g * group + h * apart + place1);
-        }
-      if (kFew)
-#pragma unroll
-        for (int h = 0; h < kParts; ++h)
-#pragma unroll
-          for (int q = 0; q < kLoads; ++q) b[h][q] = lds128((at + values0 + h * kRowBytes) ^ q * 64);
-      float fu = 1.f, fl = 1.f;
-      if (kE4M3) {
-        const bool here = st < kScales;
-        fu = here ? at_hand[0][st] : ld_f32(upper + st);
-        fl = kKind == 1 ? fu : here ? at_hand[1][st] : ld_f32(lower + st);
-      }
-      __syncwarp();
-      first_arrive(smem_u32(team.empty + now));
-      if (++now == this->stages) now = 0, pass ^= 1;
-      uint2 a[2][2][kSteps][2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t u[4] = {w[g][j][h].x, w[g][j][h].y, w[g][j][h].z, w[g][j][h].w};
-#pragma unroll
-            for (int q = 0; q < kSteps; ++q) {
-              if constexpr (!kE4M3) a[g][j][q][h] = make_uint2(u[2 * q], u[2 * q + 1]);
-              else if constexpr (kKind == 0) a[g][j][q][h] = e4m3x4_to_half4(u[q]);
-              else a[g][j][q][h] = e4m3x4_to_bf16x4(u[q]);
-            }
-          }
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        if (!kFew && i >= tiles) break;
-        if (!kFew) {
-          const uint16_t* src = this->values_of(n, min(8 * i + r, n.count - 1)) + c * 8 + st * kStageK;
-#pragma unroll
-          for (int h = 0; h < kParts; ++h)
-#pragma unroll
-            for (int q = 0; q < kLoads; ++q) b[h][q] = ld_here(src + h * width + q * 32);
-        }
-        float part[2][kChains][4];
-        int nth = 0;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int h = 0; h < kParts; ++h)
-#pragma unroll
-            for (int q = 0; q < kSteps; ++q, ++nth) {
-              const uint4& v = b[h][j * (kLoads / 2) + q / 2];
-              const uint32_t b0 = q & 1 ? v.z : v.x, b1 = q & 1 ? v.w : v.y;
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                float(&d)[4] = part[g][nth % kChains];
-                if (nth < kChains) mma_16816<kE4M3 && kKind == 0, true>(d, a[g][j][q][0], a[g][j][q][1], b0, b1);
-                else mma_16816<kE4M3 && kKind == 0, false>(d, a[g][j][q][0], a[g][j][q][1], b0, b1);
-              }
-            }
-        // a block of k is summed by itself, then scaled
+      if (!ok) break;
+      const uint32_t at = this->ring + now * S::kBytes;
+      float part[2][4] = {};
+#pragma unroll 1
+      for (uint32_t j = 0; j < 2; ++j) {  // chunks 2 c and 2 c + 1 of the rows, swizzled
+        uint4 w[2][2], b[kLoads];
 #pragma unroll
         for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float d = part[g][0][j];
-            if (kChains > 1) d += part[g][kChains - 1][j];
-            acc[i][g][j] = fmaf(d, j < 2 ? fu : fl, acc[i][g][j]);
+          for (int h = 0; h < 2; ++h) w[g][h] = lds128(at + g * group + h * apart + (weights ^ j << 4));
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) b[q] = lds128((at + values) ^ (j * kLoads + q) << 6);
+#pragma unroll
+        for (int q = 0; q < kSteps; ++q) {
+          const uint4& v = b[q / 2];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint2 a[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t u[4] = {w[g][h].x, w[g][h].y, w[g][h].z, w[g][h].w};
+              if constexpr (!kE4M3) a[h] = make_uint2(u[2 * q], u[2 * q + 1]);
+              else if constexpr (kKind == 0) a[h] = e4m3x4_to_half4(u[q]);
+              else a[h] = e4m3x4_to_bf16x4(u[q]);
+            }
+            mma_16816<kE4M3 && kKind == 0, false>(part[g], a[0], a[1], q & 1 ? v.z : v.x, q & 1 ? v.w : v.y);
           }
+        }
       }
+      // a block of k is summed by itself, then scaled
+      const float upper = kE4M3 ? team.scales[now][0] : 1.f, lower = kE4M3 ? team.scales[now][1] : 1.f;
+      __syncwarp();
+      first_arrive(smem_u32(team.empty + now));
+      if (++now == kStages) now = 0, pass ^= 1;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[g][i] = fmaf(part[g][i], i < 2 ? upper : lower, acc[g][i]);
     }
+    if (!ok) return;
     const int rows = kKind == 1 ? p.m.H : n.shared ? p.m.Is : p.m.I;
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      if (!kFew && i >= tiles) break;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int row = n.row + g * (kKind == 0 ? 8 : 16);
-        if (row < rows) finish<kKind>(n, row, 8 * i, acc[i][g]);
-      }
+    for (int g = 0; g < 2; ++g) {
+      const int row = n.row + g * (kKind == 0 ? 8 : 16);
+      if (row < rows) finish<kKind>(n, row, acc[g]);
     }
     __syncwarp();
     if (kKind == 0) {  // the other warp makes it known
@@ -947,32 +901,31 @@ struct Multiplier : Warp<kE4M3> {
       ++owed;
     }
   }
-  // what comes of a unit's sums for tokens `first` to `first` + 7
+  // what comes of a group of 16 rows' sums
   template <int kKind>
-  __device__ __forceinline__ void finish(const Unit& n, int row, int first, const float (&acc)[4]) {
+  __device__ __forceinline__ void finish(const Unit& n, int row, const float (&acc)[4]) {
     const int r = lane >> 2, c = lane & 3;
-    if constexpr (kKind == 0) {  // silu(gate) * up for places row + r, tokens 2 c and the next
+    if constexpr (kKind == 0) {  // silu(gate) * up for place row + r, tokens 2 c and the next
       uint16_t* hidden = n.shared ? p.shared_hidden : p.hidden;
-      const int base = n.shared ? 0 : n.first, wide = pad256(n.shared ? p.m.Is : p.m.I);
+      const int first = n.first - (n.shared ? s.first[n.a] : 0), wide = pad256(n.shared ? p.m.Is : p.m.I);
       const int at = place<kE4M3>(row) + place_of_8<kE4M3>(r);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int rank = first + 2 * c + j;
+        const int rank = 2 * c + j;
         if (rank >= n.count) continue;
         const float xs = kE4M3 ? s.x_scale[s.token[n.first + rank]] : 1.f, g = acc[j] * xs, u = acc[2 + j] * xs;
         const float h = g / (1.f + expf(-g)) * u;
         const uint16_t hi = f2bf(h);
-        uint16_t* to = hidden + (size_t)(base + rank) * 2 * wide + at;
+        uint16_t* to = hidden + (size_t)(first + rank) * 2 * wide + at;
         to[0] = hi;
         // what the first part lost; nothing where it is not finite
         to[wide] = (hi & 0x7F80u) == 0x7F80u ? 0 : f2bf(h - bf2f(hi));
       }
-    } else {  // rows row + r and row + 8 + r
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int rank = first + 2 * c + (j & 1);
-        if (rank < n.count) p.y[(size_t)(n.first + rank) * p.m.H + row + (j >> 1) * 8 + r] = acc[j] * s.weight[n.first + rank];
-      }
+    } else if (c < n.count) {  // rows row + r and row + 8 + r: the products with the two parts of token c's h
+      float* y = p.y + (size_t)(n.first + c) * p.m.H + row + r;
+      const float w = s.weight[n.first + c];
+      y[0] = (acc[0] + acc[1]) * w;
+      y[8] = (acc[2] + acc[3]) * w;
     }
   }
 
@@ -990,7 +943,7 @@ struct Multiplier : Warp<kE4M3> {
   // 32 columns of the output for 8 tokens, from the experts' rows in the order of the choice
   __device__ __forceinline__ void join(const Unit& n) {
     const int* done = reinterpret_cast<const int*>(p.counters + 2 + n.row / 32);
-    for (uint32_t i = 0; !__all_sync(~0u, ld_acquire_gpu(done) >= s.active + (p.m.Is ? 1 : 0)); ++i) {
+    for (uint32_t i = 0; !__all_sync(~0u, ld_acquire_gpu(done) >= this->rows_of_y()); ++i) {
       if (i == kSpinLimit) return fail();
       __nanosleep(32);
     }
@@ -1025,23 +978,13 @@ struct Multiplier : Warp<kE4M3> {
       if (n.kind == 2) {
         __syncwarp();
         first_arrive(smem_u32(team.empty + now));
-        if (++now == this->stages) now = 0, pass ^= 1;
+        if (++now == kStages) now = 0, pass ^= 1;
         tell_rows();
         join(n);
-        if (!ok) return;
-        continue;
-      }
-      if (n.kind && !hidden_ready) {  // the other warp has seen all of h; now this one
-        for (uint32_t i = 0; ld_acquire_gpu(reinterpret_cast<const int*>(p.counters + 1)) < this->units_a && i < kSpinLimit; ++i) {
-        }
-        hidden_ready = true;
-      }
-      if (n.kind == 0) {
-        if (n.count <= 8) work<0, true>(n);
-        else work<0, false>(n);
+      } else if (n.kind == 0) {
+        work<0>(n);
       } else {
-        if (n.count <= 8) work<1, true>(n);
-        else work<1, false>(n);
+        work<1>(n);
       }
       if (!ok) return;
       if (owed == kOwed) tell_rows();
@@ -1050,13 +993,24 @@ struct Multiplier : Warp<kE4M3> {
   }
 };
 
+struct Shared {  // behind the teams' stages
+  Lists lists;
+  Team team[kTeams];
+};
+template <bool kE4M3>
+constexpr size_t smem_of() {
+  return 1024 + (size_t)kTeams * Stage<kE4M3>::kBytes * kStages + sizeof(Shared);
+}
+static_assert(smem_of<true>() <= 232448 && smem_of<false>() <= 232448, "");
+static_assert(sizeof(Choice) <= kTeams * kStages * Stage<false>::kBytes && kStages + 2 <= kQueue, "");
+
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
-  Rings& rings = *reinterpret_cast<Rings*>(smem + kTeams * kRing);
-  Lists& s = rings.lists;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp & (kTeams - 1);
+  Shared& shared = *reinterpret_cast<Shared*>(smem + kTeams * Stage<kE4M3>::kBytes * kStages);
+  Lists& s = shared.lists;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp % kTeams;
   if (threadIdx.x == 0) {
     prefetch_tensormap(&p.gate_up);
     prefetch_tensormap(&p.down);
@@ -1064,37 +1018,30 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
   await_grid();
   unsigned ticket = 0;
   if (warp < kTeams && lane == 0) ticket = atomicAdd(p.counters, 1u);
-  make_lists(p, rings.choice, s);
+  make_lists(p, *reinterpret_cast<Choice*>(smem), s);  // on the way to the lists: where the stages will be
   if (s.active == 0 && p.m.Is == 0) {  // no token has an expert
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.c.T * p.m.H / 8; i += gridDim.x * kThreads)
       reinterpret_cast<uint4*>(p.c.out)[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  Team& team = rings.team[mine];  // where the choice was
+  Team& team = shared.team[mine];
   if (warp < kTeams && lane < kStages) {
     mbar_init(smem_u32(team.full + lane), 33);  // the weights; every lane's copies
     mbar_init(smem_u32(team.empty + lane), 1);
     if (lane == 0) team.finished = team.failed = 0;
   }
   fence_mbar_init();
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // copies come where the choice was
   __syncthreads();
-  const uint32_t ring = smem_u32(smem + mine * kRing);
-  // 512 threads are launched with 128 registers each; 56 in the warps that load leave 200 for the products of 64 tokens (with
-  // 72 and 184 an expert of 64 tokens takes 177 us instead of 150, and the cases with few tokens 2 to 4 % less)
+  const uint32_t ring = smem_u32(smem + mine * Stage<kE4M3>::kBytes * kStages);
   if (warp < kTeams) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     Loader<kE4M3> loader(p, s, team, ring);
     loader.run(ticket);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     Multiplier<kE4M3> worker(p, s, team, ring);
     worker.run();
   }
 }
-
-constexpr size_t kSmem = 1024 + (size_t)kTeams * kRing + sizeof(Rings);
-static_assert(kSmem <= 232448, "");
-static_assert(kStages + 2 <= kQueue, "");
 
 template <bool kE4M3>
 cudaError_t encode(CUtensorMap* map, const void* base, int k, int rows, int matrices, bool halves) {
@@ -1111,7 +1058,7 @@ cudaError_t launch(const LaunchEnv& env, MoeParams& p) {
   if (e == cudaSuccess) e = device_sm_count(&sms);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !done[dev]) {
-    e = cudaFuncSetAttribute(experts_kernel<kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(experts_kernel<kE4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of<kE4M3>());
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = 1;
   }
@@ -1127,7 +1074,7 @@ cudaError_t launch(const LaunchEnv& env, MoeParams& p) {
   if (e == cudaSuccess && p.chosen)
     e = launch_early(choose_kernel, dim3((p.c.T + kChooseWarps - 1) / kChooseWarps), kChooseWarps * 32, 0, env.stream, p);
   if (e != cudaSuccess) return e;
-  return launch_early(experts_kernel<kE4M3>, dim3(sms), kThreads, kSmem, env.stream, p);
+  return launch_early(experts_kernel<kE4M3>, dim3(sms), kThreads, smem_of<kE4M3>(), env.stream, p);
 }
 
 }  // namespace
