@@ -6,7 +6,7 @@
 // The first kernel forms the logits and lays the tokens out; with more than 16 tokens a second one chooses (16 warps of every
 // CTA of the last one do it otherwise: 64 tokens of 288 experts took 28 us there, 14 us with a kernel of their own).  The last
 // kernel streams the chosen experts' weights once, and HBM bounds it: 64 tokens of 288 experts of 4096 x 1536 and a shared
-// one, 3 GB of e4m3 weights, 575 us, 5.3 TB/s with everything; one token of 64 experts of 2048 x 1024, 50 MB, 33 us, of
+// one, 3 GB of e4m3 weights, 575 us, 5.3 TB/s with everything; one token of 64 experts of 2048 x 1024, 50 MB, 31 us, of
 // which the logits take 3, the choice 5, and then 16 and 8 steps of about half a microsecond each wait for one another.
 //
 // Work is taken in units from one list by an atomic counter: 16 rows of a gate matrix with the 16 rows of the up projection
@@ -17,7 +17,7 @@
 // memory: one warp takes units and copies their weights by TMA and their tokens' values by plain asynchronous copies, the
 // other multiplies.  The ring runs ahead over the ends of units and from one kind to the next, and the wait for all of h falls
 // into that time.  (Eight warps that both loaded and multiplied took 1027 us for the first of the sizes above, two warps that
-// shared the products and of which one loaded 943; ten teams with rings of three stages take 560, and 36 for one token.)  A
+// shared the products and of which one loaded 943; ten teams with rings of three stages take 560, and 36 instead of 33 for one token.)  A
 // unit is waited for only by units of the next kind, and by then every unit of its kind has been taken by a team that runs and
 // waits for nothing: the kernel ends however few of its CTAs run at a time.
 //
@@ -340,10 +340,11 @@ __global__ void __launch_bounds__(kChooseWarps * 32) choose_kernel(const __grid_
   }
 }
 
-// The whole CTA.
-__device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, Lists& s) {
+constexpr int kPass = kThreads / kMaxTopK;  // tokens at a time, a thread for each of their choices
+
+// The whole CTA: every token's choice.
+__device__ __forceinline__ void make_choice(const MoeParams& p, Choice& choice, Lists& s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.c.T, k = p.c.top_k, E = p.m.E;
-  constexpr int kPass = kThreads / kMaxTopK;  // tokens at a time, a thread for each of their choices
   const int j = tid % kMaxTopK, t0 = tid / kMaxTopK;
   for (int e = tid; e < E; e += kThreads) choice.mask[e] = 0;
   if (tid < T) s.x_scale[tid] = ld_f32(p.x_scale + tid);
@@ -370,6 +371,11 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, L
     }
   }
   __syncthreads();
+}
+// The whole CTA: what the units of work need to know.
+__device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, Lists& s) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, T = p.c.T, k = p.c.top_k, E = p.m.E;
+  const int j = tid % kMaxTopK, t0 = tid / kMaxTopK;
   for (int t = t0; t < T && j < k; t += kPass)
     if (choice.id[t][j] >= 0) atomicOr(&choice.mask[choice.id[t][j]], 1ull << t);
   __syncthreads();
@@ -1017,8 +1023,17 @@ __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_const
   }
   await_grid();
   unsigned ticket = 0;
-  if (warp < kTeams && lane == 0) ticket = atomicAdd(p.counters, 1u);
-  make_lists(p, *reinterpret_cast<Choice*>(smem), s);  // on the way to the lists: where the stages will be
+  // Where there are fewer units than teams they are spread over the SMs: a CTA's first team takes one first, the last four when
+  // the lists are there.
+  auto take = [&](int first, int last) {
+    if (warp >= first && warp < last && lane == 0) ticket = atomicAdd(p.counters, 1u);
+  };
+  Choice& choice = *reinterpret_cast<Choice*>(smem);  // where the stages will be
+  take(0, 1);
+  make_choice(p, choice, s);
+  take(1, 4);
+  make_lists(p, choice, s);
+  take(4, kTeams);
   if (s.active == 0 && p.m.Is == 0) {  // no token has an expert
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.c.T * p.m.H / 8; i += gridDim.x * kThreads)
       reinterpret_cast<uint4*>(p.c.out)[i] = make_uint4(0, 0, 0, 0);
