@@ -17,16 +17,16 @@
 // memory: one warp takes units and copies their weights by TMA and their tokens' values by plain asynchronous copies, the
 // other multiplies.  The ring runs ahead over the ends of units and from one kind to the next, and the wait for all of h falls
 // into that time.  (Eight warps that both loaded and multiplied took 1027 us for the first of the sizes above, two warps that
-// shared the products and of which one loaded 943; ten teams with rings of three stages take 560, and 36 instead of 33 for one token.)  A
-// unit is waited for only by units of the next kind, and by then every unit of its kind has been taken by a team that runs and
-// waits for nothing: the kernel ends however few of its CTAs run at a time.
+// shared the products and of which one loaded 943; ten teams with rings of three stages take 560, and 36 instead of 33 for
+// one token.)  A unit is waited for only by units of the next kind, and by then every unit of its kind has been taken by a
+// team that runs and waits for nothing: the kernel ends however few of its CTAs run at a time.
 //
 // Products are m16n8k16 of mma.sync: weights fill the 16 rows, an expert's tokens the 8 columns, so that a weight is an operand
 // as it lies in memory.  Both operands of a lane may come from any places of k as long as they are the same ones; a lane reads
 // 16-byte chunks of its rows, and the tokens lie in memory in that order.  e4m3 weights become binary16 beside the tokens
 // (exact; a token is divided by a power of two that brings its largest value to 2^14 .. 2^15: values down to 2^-32 of the
 // largest are exact, and what others lose is below 2^-40 of it) and bf16 beside h, which has no bound known beforehand: it is
-// held as a bf16 and the bf16 of what that lost, 16 bits together, in two products.
+// held as a bf16 and the bf16 of what that lost, 16 bits together, in two columns.
 #include <string.h>
 
 #include "attn_common.cuh"
