@@ -1092,12 +1092,19 @@ def gdn_fp8_quantize(x, block_rows=1, codes=None, scales=None, stream=None):
         raise ValueError(f"block_rows must be 1 or {FP8_BLOCK}, got {block_rows}")
     (rows, cols), dev = x.shape, x.device
     if codes is None:
-        codes = _empty((rows, -(-cols // 16) * 16), torch.float8_e4m3fn, dev, stream)[:, :cols]
-    cp, cs = _codes(codes, "codes", dev, (rows, cols))
+        cs = -(-cols // 16) * 16
+        codes = _empty((rows, cs), torch.float8_e4m3fn, dev, stream)
+        cp = codes.data_ptr()
+        if cs != cols:
+            codes = codes[:, :cols]
+    else:
+        cp, cs = _codes(codes, "codes", dev, (rows, cols))
     shape = (-(-rows // block_rows), _blocks(cols))
     if scales is None:
         scales = _empty(shape, torch.float32, dev, stream)
-    sp = _flat(scales, torch.float32, "scales", shape, dev)
+        sp = scales.data_ptr()
+    else:
+        sp = _flat(scales, torch.float32, "scales", shape, dev)
     _call(_L().gdn_fp8_quantize, dev, stream, xp, xs if rows > 1 else cols, rows, cols, block_rows, cp, cs, sp)
     return codes, scales
 
@@ -1112,14 +1119,17 @@ def gdn_fp8_matmul(x, x_scale, w, w_scale, out=None, out_dtype=torch.bfloat16, s
     (T, K), N = x.shape, w.shape[0]
     if w.shape[1] != K:
         raise ValueError(f"x and w must have the same number of columns, got {K} and {w.shape[1]}")
+    if out is not None:
+        op, os_ = _matrix(out, "out", dev, (T, N))
+        out_dtype = out.dtype
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise TypeError(f"out must be {torch.bfloat16} or {torch.float32}, got {out_dtype}")
     if out is None:
         out = _empty((T, N), out_dtype, dev, stream)
-    op, os_ = _matrix(out, "out", dev, (T, N))
-    if out.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"out must be {torch.bfloat16} or {torch.float32}, got {out.dtype}")
+        op, os_ = out.data_ptr(), N
     _call(_L().gdn_fp8_matmul, dev, stream, xp, xs, _flat(x_scale, torch.float32, "x_scale", (T, _blocks(K)), dev), wp, ws,
           _flat(w_scale, torch.float32, "w_scale", (_blocks(N), _blocks(K)), dev), T, N, K,
-          out.dtype is torch.float32, op, os_ if T > 1 else N)
+          out_dtype is torch.float32, op, os_ if T > 1 else N)
     return out
 
 
