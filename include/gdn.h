@@ -720,8 +720,9 @@ typedef struct {
 #define GDN_MOE_MAX_TOP_K 16
 
 #define GDN_WEIGHT_BF16 0
-#define GDN_WEIGHT_E4M3 1 /* with a scale for each block of 128 x 128 of every [I, H] or [H, I] matrix; no code is NaN */
+#define GDN_WEIGHT_E4M3 1 /* with a scale for each block of 128 x 128 of every [I, H] or [H, I] matrix */
 
+/* The experts' matrices and scales are finite: what a NaN or an infinity among them gives is not defined. */
 typedef struct {
   int32_t type;                      /* of the experts' matrices, GDN_WEIGHT_* */
   const gdn_bf16* router;            /* [E, H] */

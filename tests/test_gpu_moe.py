@@ -43,7 +43,9 @@ CASES = [  # T, E, top_k, H, I, Is
     (33, 60, 4, 256, 176, 704), (64, 288, 8, 256, 64, 64), (64, 8, 8, 512, 256, 0), (64, 5, 2, 4096, 32, 0), (3, 1024, 16, 64, 32, 0),
     # more blocks of k than scales are kept at hand; shared experts of every number of tokens; units of one stage by the thousand
     (2, 3, 2, 4240, 48, 0), (20, 3, 2, 144, 4368, 0), (4, 6, 3, 4112, 4112, 0), (6, 20, 3, 400, 80, 272), (17, 5, 2, 96, 112, 1040),
-    (64, 1000, 16, 128, 16, 16), (64, 40, 3, 2048, 96, 0)]
+    (64, 1000, 16, 128, 16, 16), (64, 40, 3, 2048, 96, 0),
+    # the widest
+    (3, 3, 2, 16384, 2064, 0), (2, 2, 2, 1040, 16384, 16)]
 
 
 @pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "bf16"])
