@@ -267,6 +267,11 @@ __device__ __forceinline__ void choose(const MoeParams& p, int t, int lane, int&
   float a[kOwn], top = -INFINITY, sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) a[i] = lane + 32 * i < E ? ld_f32(l + lane + 32 * i) : -INFINITY;
+  float bias[kOwn];  // on its way beside the logits
+  if (p.m.router_bias) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) bias[i] = lane + 32 * i < E ? ld_f32(p.m.router_bias + lane + 32 * i) : 0.f;
+  }
   if (!c.sigmoid && (p.m.router_bias || !c.renormalise)) {
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) top = fmaxf(top, a[i]);
@@ -280,7 +285,7 @@ __device__ __forceinline__ void choose(const MoeParams& p, int t, int lane, int&
   if (p.m.router_bias) {
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
-      key[i] = lane + 32 * i < E ? order_key(score(a[i]) + ld_f32(p.m.router_bias + lane + 32 * i)) : 0;
+      key[i] = lane + 32 * i < E ? order_key(score(a[i]) + bias[i]) : 0;
   } else {
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) key[i] = lane + 32 * i < E ? order_key(a[i]) : 0;
@@ -301,7 +306,12 @@ __device__ __forceinline__ void choose(const MoeParams& p, int t, int lane, int&
       if (e == lane + 32 * i) key[i] = 0;
   }
   const bool chosen = lane < c.top_k;
-  const float mine = chosen ? ld_f32(l + id) : 0.f;
+  float mine = 0.f;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const float v = __shfl_sync(~0u, a[i], id & 31);
+    if (chosen && id >> 5 == i) mine = v;
+  }
   if (c.renormalise) {
     // in logarithms, relative to the largest: no score underflows before its sum is formed
     const float v = !c.sigmoid ? mine : fminf(mine, 0.f) - log1pf(expf(-fabsf(mine)));
@@ -436,11 +446,13 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, L
     const int e = choice.id[t][j];
     bool again = e < 0;
     float w = 0.f;
-    for (int q = 0; q < k; ++q)
-      if (choice.id[t][q] == e) {
-        w += choice.weight[t][q];
-        again |= q < j;
-      }
+#pragma unroll 4
+    for (int q = 0; q < k; ++q) {
+      const bool same = choice.id[t][q] == e;
+      const float v = choice.weight[t][q];
+      if (same) w += v;
+      again |= same && q < j;
+    }
     int slot = kNone;
     if (!again) {
       slot = s.first[choice.index[e]] + __popcll(choice.mask[e] & ((1ull << t) - 1));
