@@ -107,6 +107,12 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ float2 lds_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
@@ -573,7 +579,7 @@ struct Stage {
 };
 struct Team {
   uint64_t full[kStages], empty[kStages];
-  float scales[kStages][2];  // of a stage's rows: of gate and up, or of down
+  alignas(8) float scales[kStages][2];  // of a stage's rows: of gate and up, or of down
   int queue[kQueue];         // units on their way; negative: no more
   int finished;              // units of the first kind
   int failed;                // a wait ran out
@@ -586,12 +592,12 @@ struct Warp {
   const Lists& s;
   Team& team;
   const int lane;
-  const uint32_t ring;
+  const uint32_t ring, full, empty;           // in shared memory
   int units_a, units_b, units;                // of the first kind, of the first two, of all
   int hidden_units, out_units, shared_units;  // units of a group of either kind; of the shared expert's first kind
 
   __device__ __forceinline__ Warp(const MoeParams& params, const Lists& lists, Team& t, uint32_t at)
-      : p(params), s(lists), team(t), lane(threadIdx.x & 31), ring(at) {
+      : p(params), s(lists), team(t), lane(threadIdx.x & 31), ring(at), full(smem_u32(t.full)), empty(smem_u32(t.empty)) {
     hidden_units = (p.m.I + 15) / 16;
     out_units = (p.m.H + 31) / 32;
     shared_units = (p.m.Is + 15) / 16;
@@ -723,14 +729,14 @@ struct Loader : Warp<kE4M3> {
         aim(this->unit_of(team.queue[unit++ % kQueue]));
         st = 0;
       }
-      load_values(this->ring + at * S::kBytes, st++ * S::kK, smem_u32(team.full + at));
+      load_values(this->ring + at * S::kBytes, st++ * S::kK, this->full + 8 * at);
       if (++at == kStages) at = 0;
     }
     hidden_ready = true;
   }
   // waits until the next stage may be loaded
   __device__ __forceinline__ void await_place() {
-    const uint32_t bar = smem_u32(team.empty + slot);
+    const uint32_t bar = this->empty + 8 * slot;
     for (uint32_t i = 0; !warp_poll(bar, pass ^ 1); ++i)
       if (i == kWaitLimit || *(volatile int*)&team.failed) return fail();
   }
@@ -743,7 +749,7 @@ struct Loader : Warp<kE4M3> {
     if (ok) await_place();
     if (!ok) return;
     __syncwarp();
-    const uint32_t bar = smem_u32(team.full + slot);
+    const uint32_t bar = this->full + 8 * slot;
     arrive(bar);
     if (lane == 0) arrive(bar);
     next_stage();
@@ -780,6 +786,7 @@ struct Loader : Warp<kE4M3> {
       }
       const void* map = n.kind ? (n.shared ? &p.shared_down : &p.down) : (n.shared ? &p.shared_gate_up : &p.gate_up);
       const int z = n.shared ? 0 : s.expert[n.a] * (n.kind ? 1 : 2);
+      const uint32_t scales = smem_u32(team.scales) + 4 * (lane & 1);
       if (n.kind == 0) ++mine;
       __syncwarp();
 #pragma unroll 1
@@ -795,9 +802,9 @@ struct Loader : Warp<kE4M3> {
         }
         await_place();
         if (!ok) break;
-        const uint32_t bar = smem_u32(team.full + slot), at = this->ring + slot * S::kBytes;
+        const uint32_t bar = this->full + 8 * slot, at = this->ring + slot * S::kBytes;
         warp_load(at, map, st * S::kK, n.row, z, bar);
-        if (kE4M3 && lane < 2) copy_4(smem_u32(&team.scales[slot][lane]), scale + st);
+        if (kE4M3 && lane < 2) copy_4(scales + 8 * slot, scale + st);
         if (!kind || hidden_ready) load_values(at, st * S::kK, bar);
         next_stage();
       }
@@ -809,10 +816,10 @@ struct Loader : Warp<kE4M3> {
     pass_on();
     if (ok) return;
     // a wait ran out: copies in flight land before the CTA ends
-    for (int i = 0; i < late && !hidden_ready; ++i) copies_done_to(smem_u32(team.full + (late_at + i) % kStages));
+    for (int i = 0; i < late && !hidden_ready; ++i) copies_done_to(this->full + (late_at + i) % kStages * 8);
     for (int i = 0; i < loaded && i < kStages; ++i) {
       if (slot-- == 0) slot = kStages - 1, pass ^= 1;
-      warp_wait(smem_u32(team.full + slot), pass);
+      warp_wait(this->full + 8 * slot, pass);
     }
   }
 };
@@ -834,7 +841,7 @@ struct Multiplier : Warp<kE4M3> {
       : W(params, lists, t, at) {}
 
   __device__ __forceinline__ void await_stage() {
-    const uint32_t bar = smem_u32(team.full + now);
+    const uint32_t bar = this->full + 8 * now;
     for (uint32_t i = 0; !warp_poll(bar, pass); ++i)
       if (i == kWaitLimit || *(volatile int*)&team.failed) return fail();
   }
@@ -860,6 +867,7 @@ struct Multiplier : Warp<kE4M3> {
     const int row = min(r, n.count * (kKind + 1) - 1);
     const uint32_t weights = r * 128 + ((2 * c ^ r) << 4);
     const uint32_t values = kStageBytes + row * S::kRowBytes + c * 16 + (row & 1) * 64;
+    const uint32_t scales = smem_u32(team.scales);
     float acc[2][4] = {};
 #pragma unroll 1
     for (int st = 0; st < steps; ++st) {
@@ -894,14 +902,14 @@ struct Multiplier : Warp<kE4M3> {
         }
       }
       // a block of k is summed by itself, then scaled
-      const float upper = kE4M3 ? team.scales[now][0] : 1.f, lower = kE4M3 ? team.scales[now][1] : 1.f;
+      const float2 scale = kE4M3 ? lds_f32x2(scales + 8 * now) : make_float2(1.f, 1.f);
       __syncwarp();
-      first_arrive(smem_u32(team.empty + now));
+      first_arrive(this->empty + 8 * now);
       if (++now == kStages) now = 0, pass ^= 1;
 #pragma unroll
       for (int g = 0; g < 2; ++g)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[g][i] = fmaf(part[g][i], i < 2 ? upper : lower, acc[g][i]);
+        for (int i = 0; i < 4; ++i) acc[g][i] = fmaf(part[g][i], i < 2 ? scale.x : scale.y, acc[g][i]);
     }
     if (!ok) return;
     const int rows = kKind == 1 ? p.m.H : n.shared ? p.m.Is : p.m.I;
@@ -995,7 +1003,7 @@ struct Multiplier : Warp<kE4M3> {
       const Unit n = this->unit_of(u);
       if (n.kind == 2) {
         __syncwarp();
-        first_arrive(smem_u32(team.empty + now));
+        first_arrive(this->empty + 8 * now);
         if (++now == kStages) now = 0, pass ^= 1;
         tell_rows();
         join(n);
