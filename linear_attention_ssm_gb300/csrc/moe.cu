@@ -6,7 +6,7 @@
 // The first kernel forms the logits and lays the tokens out; with more than 16 tokens a second one chooses (16 warps of every
 // CTA of the last one do it otherwise: 64 tokens of 288 experts took 28 us there, 14 us with a kernel of their own).  The last
 // kernel streams the chosen experts' weights once, and HBM bounds it: 64 tokens of 288 experts of 4096 x 1536 and a shared
-// one, 3 GB of e4m3 weights, 575 us, 5.3 TB/s with everything; one token of 64 experts of 2048 x 1024, 50 MB, 31 us, of
+// one, 3 GB of e4m3 weights, 556 us, 5.5 TB/s with everything; one token of 64 experts of 2048 x 1024, 50 MB, 30 us, of
 // which the logits take 3, the choice 5, and then 16 and 8 steps of about half a microsecond each wait for one another.
 //
 // Work is taken in units from one list by an atomic counter: 16 rows of a gate matrix with the 16 rows of the up projection
@@ -17,7 +17,7 @@
 // memory: one warp takes units and copies their weights by TMA and their tokens' values by plain asynchronous copies, the
 // other multiplies.  The ring runs ahead over the ends of units and from one kind to the next, and the wait for all of h falls
 // into that time.  (Eight warps that both loaded and multiplied took 1027 us for the first of the sizes above, two warps that
-// shared the products and of which one loaded 943; ten teams with rings of three stages take 560, and 36 instead of 33 for
+// shared the products and of which one loaded 943; ten teams with rings of three stages take 551, and 32 instead of 30 for
 // one token.)  A unit is waited for only by units of the next kind, and by then every unit of its kind has been taken by a
 // team that runs and waits for nothing: the kernel ends however few of its CTAs run at a time.
 //
@@ -853,9 +853,8 @@ struct Multiplier : Warp<kE4M3> {
     ok = false;
   }
 
-  // One unit.  The loop is short on purpose: every warp is at another place of the code, and waits for its instructions more
-  // than for anything else.  64 tokens of 288 experts take 575 us so, 637 with both chunks in one pass of the loop, 1150 with
-  // two stages in one, the next one's loads before the products; 595 with halves of chunks.
+  // One unit.  64 tokens of 288 experts take 556 us so; 575 with a pass of the loop for each chunk, 595 for each half of one;
+  // an earlier release of the stage makes no difference.
   template <int kKind>
   __device__ __forceinline__ void work(const Unit& n) {
     const int r = lane >> 2, c = lane & 3, steps = (n.k + S::kK - 1) / S::kK;
@@ -875,7 +874,7 @@ struct Multiplier : Warp<kE4M3> {
       if (!ok) break;
       const uint32_t at = this->ring + now * S::kBytes;
       float part[2][4] = {};
-#pragma unroll 1
+#pragma unroll
       for (uint32_t j = 0; j < 2; ++j) {  // chunks 2 c and 2 c + 1 of the rows, swizzled
         uint4 w[2][2], b[kLoads];
 #pragma unroll
