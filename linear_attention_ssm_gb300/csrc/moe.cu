@@ -4,7 +4,7 @@
 //   h_e = silu(x G_e^T) * (x U_e^T),  out = sum_e weight_e h_e D_e^T + sigmoid(x . g) shared(x)
 //
 // The first kernel forms the logits and lays the tokens out; with more than 16 tokens a second one chooses (16 warps of every
-// CTA of the last one do it otherwise: 64 tokens of 288 experts took 28 us there, 14 us with a kernel of their own).  The last
+// CTA of the last one do it otherwise: 64 tokens of 288 experts took 28 us there, 12 us with a kernel of their own).  The last
 // kernel streams the chosen experts' weights once, and HBM bounds it: 64 tokens of 288 experts of 4096 x 1536 and a shared
 // one, 3 GB of e4m3 weights, 556 us, 5.5 TB/s with everything; one token of 64 experts of 2048 x 1024, 50 MB, 30 us, of
 // which the logits take 3, the choice 5, and then 16 and 8 steps of about half a microsecond each wait for one another.
