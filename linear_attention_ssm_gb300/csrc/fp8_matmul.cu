@@ -538,6 +538,9 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
       } else {  // rows of any alignment: 32 x 16 values at a time through shared memory, half a row a store
         // a small tile's CTA has no other one: the ring is free
         if constexpr (!C::kLarge) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
+        const int half = lane >> 4, col = lane & 15, size = p.out_f32 ? 4 : 2;
+        const long rows = p.tokens - t0 - half, row_bytes = 2 * p.out_stride * size;  // every second row is this lane's
+        uint8_t* to = static_cast<uint8_t*>(p.out) + ((t0 + half) * p.out_stride + n0 + col) * size;
 #pragma unroll
         for (int c = 0; c < C::kCols / 16; ++c) {
           __syncwarp();
@@ -547,10 +550,18 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
             mine[lane * C::kPitch + 2 * i + 1] = acc[c * 8 + i].y;
           }
           __syncwarp();
-          const int col = lane & 15;
-          if (n0 + c * 16 + col < p.n)
-            for (int r = lane >> 4; r < 32 && t0 + r < p.tokens; r += 2)
-              store_out(p, t0 + r, n0 + c * 16 + col, mine[r * C::kPitch + col]);
+          float v[16];  // all of a lane's at once: one after another they take 8 us more (777 x 5003 x 2041)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = mine[(2 * i + half) * C::kPitch + col];
+          if (n0 + c * 16 + col < p.n) {
+            uint8_t* at = to + c * 16 * size;
+#pragma unroll
+            for (int i = 0; i < 16; ++i, at += row_bytes) {
+              if (2 * i >= rows) continue;
+              if (p.out_f32) *reinterpret_cast<float*>(at) = v[i];
+              else *reinterpret_cast<uint16_t*>(at) = f2bf(v[i]);
+            }
+          }
         }
       }
     }
