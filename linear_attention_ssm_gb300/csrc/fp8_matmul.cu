@@ -311,7 +311,7 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& m
 // thread of loads from tensor memory and packed multiply-adds (3.3 cycles a warp's instruction): 8192 tokens x 16384 x 4096
 // 460 to 500 us with the clocks that a second of it leaves, 2.2 to 2.4 PFLOP/s; 2048 x 4096 x 6144 51 us, 2.0 PFLOP/s.  Two
 // CTAs that shared a tile's loads by multicast, or one product over two SMs, were no faster.  The small ones are bound by
-// what a block waits for: 64 x 2048 x 6144 9.3 us, 777 x 5003 x 2041 (140 large tiles of 16 blocks) 19 us.
+// what a block waits for: 64 x 2048 x 6144 9.3 us, 777 x 5003 x 2041 (140 large tiles of 16 blocks) 15.5 us.
 template <int kN, bool kSplit>
 __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __grid_constant__ MatmulParams p) {
   using C = Tiles<kN>;
@@ -535,31 +535,55 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
             }
           }
         }
-      } else {  // rows of any alignment: 32 x 16 values at a time through shared memory, half a row a store
-        // a small tile's CTA has no other one: the ring is free
+      } else {
+        // Rows of any alignment, 32 x 16 words at a time through shared memory: half a row of fp32 values or a row of 32 bf16
+        // ones a store, sixteen stores of a lane at once: 777 x 5003 x 2041 15.5 us (bf16 15.1), 19.8 with one store after another.
+        // A small tile's CTA has no other one: the ring is free.
         if constexpr (!C::kLarge) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
-        const int half = lane >> 4, col = lane & 15, size = p.out_f32 ? 4 : 2;
-        const long rows = p.tokens - t0 - half, row_bytes = 2 * p.out_stride * size;  // every second row is this lane's
-        uint8_t* to = static_cast<uint8_t*>(p.out) + ((t0 + half) * p.out_stride + n0 + col) * size;
+        if (p.out_f32) {
+          const int half = lane >> 4, col = lane & 15;
+          const long rows = p.tokens - t0 - half;
+          float* to = static_cast<float*>(p.out) + (t0 + half) * p.out_stride + n0 + col;
 #pragma unroll
-        for (int c = 0; c < C::kCols / 16; ++c) {
-          __syncwarp();
+          for (int c = 0; c < C::kCols / 16; ++c) {
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            mine[lane * C::kPitch + 2 * i] = acc[c * 8 + i].x;
-            mine[lane * C::kPitch + 2 * i + 1] = acc[c * 8 + i].y;
+            for (int i = 0; i < 8; ++i) {
+              mine[lane * C::kPitch + 2 * i] = acc[c * 8 + i].x;
+              mine[lane * C::kPitch + 2 * i + 1] = acc[c * 8 + i].y;
+            }
+            __syncwarp();
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = mine[(2 * i + half) * C::kPitch + col];
+            if (n0 + c * 16 + col < p.n) {
+              float* at = to + c * 16;
+#pragma unroll
+              for (int i = 0; i < 16; ++i, at += 2 * p.out_stride)
+                if (2 * i < rows) *at = v[i];
+            }
           }
-          __syncwarp();
-          float v[16];  // all of a lane's at once: one after another they take 8 us more (777 x 5003 x 2041)
+        } else {
+          uint32_t* words = reinterpret_cast<uint32_t*>(mine);
+          const uint16_t* values = reinterpret_cast<const uint16_t*>(mine) + lane;
+          const long rows = p.tokens - t0;
+          uint16_t* to = static_cast<uint16_t*>(p.out) + t0 * p.out_stride + n0 + lane;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = mine[(2 * i + half) * C::kPitch + col];
-          if (n0 + c * 16 + col < p.n) {
-            uint8_t* at = to + c * 16 * size;
+          for (int c = 0; c < C::kCols / 32; ++c) {
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 16; ++i, at += row_bytes) {
-              if (2 * i >= rows) continue;
-              if (p.out_f32) *reinterpret_cast<float*>(at) = v[i];
-              else *reinterpret_cast<uint16_t*>(at) = f2bf(v[i]);
+            for (int i = 0; i < 16; ++i) words[lane * C::kPitch + i] = pack_bf2(acc[c * 16 + i].x, acc[c * 16 + i].y);
+            __syncwarp();
+            uint16_t* at = to + c * 32;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint16_t v[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = values[(16 * h + i) * 2 * C::kPitch];
+              if (n0 + c * 32 + lane < p.n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (16 * h + i < rows) at[(16 * h + i) * p.out_stride] = v[i];
             }
           }
         }
