@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   float* stage_out = reinterpret_cast<float*>(smem + C::kRing);
-  float* scales = C::kLarge ? stage_out + C::kWarps * 32 * C::kPitch : stage_out;  // [2][kAhead][kWarps][32], then [2][kWarps][kAhead]
+  // [2][kAhead][kWarps][32] of tokens, then [2][kWarps][kAhead] of weights
+  float* scales = C::kLarge ? stage_out + C::kWarps * 32 * C::kPitch : stage_out;
   uint64_t* bars = reinterpret_cast<uint64_t*>(scales + C::kScales);
   __shared__ uint32_t tmem_slot;
   const uint32_t full = smem_u32(bars), empty = full + 8 * C::kMaxStages, done = empty + 8 * C::kMaxStages;
