@@ -25,8 +25,11 @@
 // as it lies in memory.  Both operands of a lane may come from any places of k as long as they are the same ones; a lane reads
 // 16-byte chunks of its rows, and the tokens lie in memory in that order.  e4m3 weights become binary16 beside the tokens
 // (exact; a token is divided by a power of two that brings its largest value to 2^14 .. 2^15: values down to 2^-32 of the
-// largest are exact, and what others lose is below 2^-40 of it) and bf16 beside h, which has no bound known beforehand: it is
-// held as a bf16 and the bf16 of what that lost, 16 bits together, in two columns.
+// largest are exact, and what others lose is below 2^-40 of it).  h is held in fp32 and split by the warp that multiplies: beside
+// e4m3 weights into two binary16 parts in two columns, relative to the largest h of its token and expert, which the units of the
+// first kind gather and which is there when all of h is: off by at most 2^-23 of itself or 2^-39 of the largest; beside bf16
+// weights into three bf16 parts, all 24 bits, in two columns and, by a second product, the third part in the second one.  (With
+// two bf16 parts beside either, 16 bits, 64 tokens of 288 experts took 557 us, now 537, and 17 of 32 in bf16 102.6, now 104.8.)
 #include <string.h>
 
 #include "attn_common.cuh"
@@ -47,7 +50,7 @@ constexpr uint32_t kSpinLimit = 1u << 22;  // polls of the counter of finished u
 constexpr int kBlock = 128;
 
 struct Layout {  // of the workspace
-  size_t counters, logits, ids, weights, x, x_scale, hidden, shared_hidden, y, bytes;
+  size_t counters, logits, ids, weights, x, x_scale, tops, hidden, shared_hidden, y, bytes;
 };
 __host__ __device__ inline int pad256(int n) { return (n + 255) & ~255; }
 Layout layout(const Moe& m, int T, int k) {
@@ -59,7 +62,8 @@ Layout layout(const Moe& m, int T, int k) {
   l.weights = l.ids + up((size_t)T * k * 4);
   l.x = l.weights + up((size_t)T * k * 4);
   l.x_scale = l.x + up((size_t)T * pad256(m.H) * 2);
-  l.hidden = l.x_scale + up((size_t)T * 4);
+  l.tops = l.x_scale + up((size_t)T * 4);
+  l.hidden = l.tops + up((size_t)T * (k + 1) * 16);
   l.shared_hidden = l.hidden + up((size_t)T * k * pad256(m.I) * 4);
   l.y = l.shared_hidden + up((size_t)T * pad256(m.Is) * 4);
   l.bytes = l.y + up((size_t)T * (k + (m.Is ? 1 : 0)) * m.H * 4);
@@ -77,8 +81,9 @@ struct MoeParams {
   float* logits;       // [T][E + 1], the shared gate's behind the experts'
   uint16_t* x;         // [T][pad256(H)] tokens in the products' order, bf16 or binary16
   float* x_scale;      // [T] what a binary16 token is multiplied with
-  uint16_t* hidden;    // [T * top_k][2][pad256(I)] in the products' order: bf16, then the rest
-  uint16_t* shared_hidden;
+  uint4* tops;         // [T * top_k], then [T] for the shared expert: x is the largest finite |h| of a slot, as bits
+  float* hidden;       // [T * top_k][pad256(I)] in the products' order
+  float* shared_hidden;
   float* y;            // [slots][H] weighted rows of the experts
 };
 
@@ -88,6 +93,15 @@ template <bool kE4M3>
 __host__ __device__ __forceinline__ int place(int k) {
   const int g = (k >> 3) & 15;
   return (k & ~127) + 8 * (kE4M3 ? (g & 3) * 4 + (g >> 2) : (((g >> 3) * 2 + (g & 1)) * 4 + ((g >> 1) & 3)));
+}
+
+// The same for a single k of h, four values of which are 16 bytes: a lane's 16 bytes of weights go with 16 or 8 values, and its
+// four values of a product lie beside the other three lanes' of the quad.
+template <bool kE4M3>
+__host__ __device__ __forceinline__ int hidden_place(int k) {
+  constexpr int kChunk = kE4M3 ? 16 : 8, kRow = 8 * kChunk;  // values beside a chunk; a row of weights
+  const int in = k & (kRow - 1), chunk = in / kChunk;
+  return k - in + (((chunk & 1) * (kChunk / 4) + (in % kChunk) / 4) * 4 + (chunk >> 1)) * 4 + (k & 3);
 }
 
 // Loads of what other kernels or CTAs wrote, or read often: where they are written, through L1.
@@ -143,6 +157,8 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = p.m.H;
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < 2 + (H + 31) / 32; i += kPrepareThreads) p.counters[i] = 0;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < p.c.T * (p.c.top_k + 1); i += kPrepareThreads) p.tops[i] = make_uint4(0, 0, 0, 0);
   if (blockIdx.x < p.c.T) {
     const int t = blockIdx.x;
     const uint16_t* x = p.c.x + t * p.c.x_stride;
@@ -185,12 +201,12 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const int wide = pad256(p.m.I), shared_wide = pad256(p.m.Is);
     for (int k = H + threadIdx.x * 8; k < pad256(H); k += kPrepareThreads * 8) *reinterpret_cast<uint4*>(to + place<kE4M3>(k)) = zero;
-    for (int s = 0; s < 2 * p.c.top_k; ++s)
-      for (int k = p.m.I + threadIdx.x * 8; k < wide; k += kPrepareThreads * 8)
-        *reinterpret_cast<uint4*>(p.hidden + ((size_t)t * 2 * p.c.top_k + s) * wide + place<kE4M3>(k)) = zero;
-    for (int s = 0; s < 2; ++s)
-      for (int k = p.m.Is + threadIdx.x * 8; k < shared_wide; k += kPrepareThreads * 8)
-        *reinterpret_cast<uint4*>(p.shared_hidden + ((size_t)t * 2 + s) * shared_wide + place<kE4M3>(k)) = zero;
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < p.c.top_k; ++s)
+      for (int k = p.m.I + threadIdx.x * 4; k < wide; k += kPrepareThreads * 4)
+        *reinterpret_cast<float4*>(p.hidden + ((size_t)t * p.c.top_k + s) * wide + hidden_place<kE4M3>(k)) = none;
+    for (int k = p.m.Is + threadIdx.x * 4; k < shared_wide; k += kPrepareThreads * 4)
+      *reinterpret_cast<float4*>(p.shared_hidden + (size_t)t * shared_wide + hidden_place<kE4M3>(k)) = none;
     return;
   }
   // rows of the router, unless the routing is given, then the shared gate
@@ -480,42 +496,38 @@ __device__ __forceinline__ void make_lists(const MoeParams& p, Choice& choice, L
 
 // ---------------------------------------------------------------- the experts
 
-// D = A B, or D += A B: m16n8k16 with binary16 or bf16 operands and fp32 sums.  Lane l has rows l / 4 and l / 4 + 8 of A at
-// the k of its place l % 4, column l / 4 of B at the same k, and columns 2 (l % 4), + 1 of D's two rows.
-template <bool kHalf, bool kFirst>
+// D += A B: m16n8k16 with binary16 or bf16 operands and fp32 sums.  Lane l has rows l / 4 and l / 4 + 8 of A at the k of its
+// place l % 4, column l / 4 of B at the same k, and columns 2 (l % 4), + 1 of D's two rows.
+template <bool kHalf>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint2& upper, const uint2& lower, uint32_t b0, uint32_t b1) {
-  const float z = 0.f;
-  if constexpr (kHalf && kFirst)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(upper.x), "r"(lower.x), "r"(upper.y), "r"(lower.y), "r"(b0), "r"(b1), "f"(z));
-  else if constexpr (kHalf)
+  if constexpr (kHalf)
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(upper.x), "r"(lower.x), "r"(upper.y), "r"(lower.y), "r"(b0), "r"(b1));
-  else if constexpr (kFirst)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(upper.x), "r"(lower.x), "r"(upper.y), "r"(lower.y), "r"(b0), "r"(b1), "f"(z));
   else
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(upper.x), "r"(lower.x), "r"(upper.y), "r"(lower.y), "r"(b0), "r"(b1));
 }
-// Four finite e4m3 codes -> pairs of bf16, codes 0 and 2, then 1 and 3: the code's exponent and significand at their places
-// of a bf16 stand for its value times 2^-120, subnormals too, and the product with 2^120 is exact.
-__device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t v) {
-  auto scaled = [](uint32_t r) {
-    const __nv_bfloat162 up = __nv_bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&r), up);
-    return *reinterpret_cast<const uint32_t*>(&y);
-  };
-  return make_uint2(scaled((v * 16 & 0x07F007F0u) | (v * 256 & 0x80008000u)), scaled((v >> 4 & 0x07F007F0u) | (v & 0x80008000u)));
+// The operand that a column of h needs beside a product's weights, from four values: the first part of them in even columns,
+// the second in odd ones.  Binary16, after the product with a power of two:
+__device__ __forceinline__ uint2 half_parts(const float4& h, float by, uint32_t odd) {  // odd: all ones, or 0
+  const uint32_t a = pack_half2(h.x * by, h.y * by) & odd, b = pack_half2(h.z * by, h.w * by) & odd;
+  const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&a)), v = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  return make_uint2(pack_half2(fmaf(h.x, by, -u.x), fmaf(h.y, by, -u.y)), pack_half2(fmaf(h.z, by, -v.x), fmaf(h.w, by, -v.y)));
 }
-// where the products' order of h has the i-th of 8 places
-template <bool kE4M3>
-__device__ __forceinline__ int place_of_8(int i) {
-  return kE4M3 ? (i & 4) | (i & 1) << 1 | (i >> 1 & 1) : i;
+// bf16, each part eight bits of the significand, cut off so that the three are exact; `third` is of odd columns, too.
+__device__ __forceinline__ uint2 bf16_parts(const float4& h, uint32_t odd, uint2& third) {
+  const float f[4] = {h.x, h.y, h.z, h.w};
+  uint32_t part[4], rest[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = f[i] - __uint_as_float(__float_as_uint(f[i]) & odd & 0xFFFF0000u);  // h, or its last 16 bits
+    part[i] = __float_as_uint(a);
+    rest[i] = __float_as_uint(a - __uint_as_float(part[i] & (0xFFFF0000u | ~odd)));  // 0, or its last eight
+  }
+  third = make_uint2(__byte_perm(rest[0], rest[1], 0x7632), __byte_perm(rest[2], rest[3], 0x7632));
+  return make_uint2(__byte_perm(part[0], part[1], 0x7632), __byte_perm(part[2], part[3], 0x7632));
 }
 
 __device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity) {
@@ -570,7 +582,7 @@ struct Unit {
 
 // Of a team: a warp that loads and one that multiplies.  A stage of their ring has 4 KB of weights and behind them the tokens'
 // values for the same k (loads through the cache take several thousand cycles while the copies fill the memory's queues):
-// a row for each token, or two for the two parts of its h.
+// a row for each token, or two for its h.
 template <bool kE4M3>
 struct Stage {
   static constexpr int kK = kE4M3 ? 128 : 64;  // values of a row
@@ -579,6 +591,7 @@ struct Stage {
 };
 struct Team {
   uint64_t full[kStages], empty[kStages];
+  alignas(16) uint4 tops[kStages][4];   // of a unit's first stage: its slots' largest h
   alignas(8) float scales[kStages][2];  // of a stage's rows: of gate and up, or of down
   int queue[kQueue];         // units on their way; negative: no more
   int finished;              // units of the first kind
@@ -658,6 +671,7 @@ struct Loader : Warp<kE4M3> {
   // of the unit that is loaded
   int rows, steps, kind;
   const uint16_t* base;
+  const uint4* tops;    // of its slots
   uint32_t from[kIts];  // this lane's piece of its rows of values
   uint32_t to;          // where the first one goes in a stage
   // the next stage to load
@@ -674,16 +688,20 @@ struct Loader : Warp<kE4M3> {
     kind = n.kind;
     rows = n.count * (kind + 1);
     steps = (n.k + S::kK - 1) / S::kK;
-    base = !kind ? p.x : n.shared ? p.shared_hidden : p.hidden;
-    const int first = 2 * (n.first - (n.shared ? s.first[n.a] : 0));
+    base = !kind ? p.x : reinterpret_cast<const uint16_t*>(n.shared ? p.shared_hidden : p.hidden);
+    const int first = n.first - (n.shared ? s.first[n.a] : 0);
+    tops = p.tops + (n.shared ? p.c.T * p.c.top_k : 0) + first;
 #pragma unroll
     for (int i = 0; i < kIts; ++i) {
       const int row = min(lane / kPieces + i * kStep, rows - 1);
-      from[i] = (kind ? first + row : s.token[n.first + row]) * pad256(n.k) + lane % kPieces * 8;
+      from[i] = (kind ? (first + row / 2) * 2 : (int)s.token[n.first + row]) * pad256(n.k) + (kind ? (row & 1) * S::kK : 0) +
+                lane % kPieces * 8;
     }
   }
   __device__ __forceinline__ void load_values(uint32_t at, int k, uint32_t bar) {
     const int mine = rows - lane / kPieces;
+    if (kE4M3 && kind && k == 0 && lane < rows / 2) copy_16(smem_u32(team.tops) + 64 * ((bar - this->full) / 8) + 16 * lane, tops + lane);
+    k <<= kind;  // h is twice as long
     if (mine > 0) copy_16(at + to, base + from[0] + k);
     if (rows > kStep) {
 #pragma unroll
@@ -858,14 +876,16 @@ struct Multiplier : Warp<kE4M3> {
   template <int kKind>
   __device__ __forceinline__ void work(const Unit& n) {
     const int r = lane >> 2, c = lane & 3, steps = (n.k + S::kK - 1) / S::kK;
-    constexpr int kLoads = kE4M3 ? 2 : 1;  // of a lane from a row of values for a chunk, 32 values apart
     constexpr int kSteps = kE4M3 ? 4 : 2;  // products of a chunk
+    constexpr int kLoads = kKind == 0 ? kSteps / 2 : kSteps;  // of a lane from its column's values for a chunk, 64 bytes apart
     // rows r and r + 8 of a group of 16: in gate and up, or in down
     constexpr uint32_t apart = kKind == 0 ? 2048 : 1024, group = kKind == 0 ? 1024 : 2048;
     // columns behind the last row of values repeat it, and are not stored
     const int row = min(r, n.count * (kKind + 1) - 1);
     const uint32_t weights = r * 128 + ((2 * c ^ r) << 4);
-    const uint32_t values = kStageBytes + row * S::kRowBytes + c * 16 + (row & 1) * 64;
+    const uint32_t values = kStageBytes + (kKind == 0 ? row * S::kRowBytes + c * 16 + (row & 1) * 64 : (row & ~1) * S::kRowBytes + c * 16);
+    const uint32_t odd = r & 1 ? ~0u : 0u;  // the column of the second part
+    float by = 1.f, back = 1.f;             // h is multiplied with, and the sums of token c
     const uint32_t scales = smem_u32(team.scales);
     float acc[2][4] = {};
 #pragma unroll 1
@@ -873,6 +893,14 @@ struct Multiplier : Warp<kE4M3> {
       await_stage();
       if (!ok) break;
       const uint32_t at = this->ring + now * S::kBytes;
+      if (kE4M3 && kKind == 1 && st == 0) {
+        auto up = [&](int i) {  // the exponent of a power of two that takes the largest h to 2^14 .. 2^15
+          const uint4 top = lds128(smem_u32(team.tops) + 64 * now + 16 * i);
+          return max(top.x >> 23, 15u) - 14;
+        };
+        by = __uint_as_float((254 - up(row >> 1)) << 23);
+        back = __uint_as_float(up(min(c, n.count - 1)) << 23);
+      }
       float part[2][4] = {};
 #pragma unroll
       for (uint32_t j = 0; j < 2; ++j) {  // chunks 2 c and 2 c + 1 of the rows, swizzled
@@ -882,21 +910,28 @@ struct Multiplier : Warp<kE4M3> {
 #pragma unroll
           for (int h = 0; h < 2; ++h) w[g][h] = lds128(at + g * group + h * apart + (weights ^ j << 4));
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) b[q] = lds128((at + values) ^ (j * kLoads + q) << 6);
+        for (int q = 0; q < kLoads; ++q)
+          b[q] = lds128(kKind == 0 ? (at + values) ^ (j * kLoads + q) << 6 : ((at + values) ^ q << 6 ^ j << 6) + j * S::kRowBytes);
 #pragma unroll
         for (int q = 0; q < kSteps; ++q) {
-          const uint4& v = b[q / 2];
+          uint2 v, third;
+          if constexpr (kKind == 0) {
+            v = q & 1 ? make_uint2(b[q / 2].z, b[q / 2].w) : make_uint2(b[q / 2].x, b[q / 2].y);
+          } else {
+            const float4 h = make_float4(__uint_as_float(b[q].x), __uint_as_float(b[q].y), __uint_as_float(b[q].z), __uint_as_float(b[q].w));
+            v = kE4M3 ? half_parts(h, by, odd) : bf16_parts(h, odd, third);
+          }
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             uint2 a[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t u[4] = {w[g][h].x, w[g][h].y, w[g][h].z, w[g][h].w};
-              if constexpr (!kE4M3) a[h] = make_uint2(u[2 * q], u[2 * q + 1]);
-              else if constexpr (kKind == 0) a[h] = e4m3x4_to_half4(u[q]);
-              else a[h] = e4m3x4_to_bf16x4(u[q]);
+              if constexpr (kE4M3) a[h] = e4m3x4_to_half4(u[q]);
+              else a[h] = make_uint2(u[2 * q], u[2 * q + 1]);
             }
-            mma_16816<kE4M3 && kKind == 0, false>(part[g], a[0], a[1], q & 1 ? v.z : v.x, q & 1 ? v.w : v.y);
+            mma_16816<kE4M3>(part[g], a[0], a[1], v.x, v.y);
+            if constexpr (!kE4M3 && kKind == 1) mma_16816<false>(part[g], a[0], a[1], third.x, third.y);
           }
         }
       }
@@ -912,10 +947,21 @@ struct Multiplier : Warp<kE4M3> {
     }
     if (!ok) return;
     const int rows = kKind == 1 ? p.m.H : n.shared ? p.m.Is : p.m.I;
+    uint32_t top[2] = {0, 0};  // of tokens 2 c and the next
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       const int row = n.row + g * (kKind == 0 ? 8 : 16);
-      if (row < rows) finish<kKind>(n, row, acc[g]);
+      if (row < rows) finish<kKind>(n, row, acc[g], back, top);
+    }
+    if constexpr (kE4M3 && kKind == 0) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) top[j] = max(top[j], __shfl_xor_sync(~0u, top[j], o));
+      uint4* tops = p.tops + (n.shared ? p.c.T * p.c.top_k - s.first[n.a] : 0) + n.first + 2 * c;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (r == 0 && 2 * c + j < n.count) atomicMax(&tops[j].x, top[j]);
     }
     __syncwarp();
     if (kKind == 0) {  // the other warp makes it known
@@ -928,29 +974,27 @@ struct Multiplier : Warp<kE4M3> {
   }
   // what comes of a group of 16 rows' sums
   template <int kKind>
-  __device__ __forceinline__ void finish(const Unit& n, int row, const float (&acc)[4]) {
+  __device__ __forceinline__ void finish(const Unit& n, int row, const float (&acc)[4], float back, uint32_t (&top)[2]) {
     const int r = lane >> 2, c = lane & 3;
     if constexpr (kKind == 0) {  // silu(gate) * up for place row + r, tokens 2 c and the next
-      uint16_t* hidden = n.shared ? p.shared_hidden : p.hidden;
+      float* hidden = n.shared ? p.shared_hidden : p.hidden;
       const int first = n.first - (n.shared ? s.first[n.a] : 0), wide = pad256(n.shared ? p.m.Is : p.m.I);
-      const int at = place<kE4M3>(row) + place_of_8<kE4M3>(r);
+      const int at = hidden_place<kE4M3>(row + r);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int rank = 2 * c + j;
         if (rank >= n.count) continue;
         const float xs = kE4M3 ? s.x_scale[s.token[n.first + rank]] : 1.f, g = acc[j] * xs, u = acc[2 + j] * xs;
         const float h = g / (1.f + expf(-g)) * u;
-        const uint16_t hi = f2bf(h);
-        uint16_t* to = hidden + (size_t)(first + rank) * 2 * wide + at;
-        to[0] = hi;
-        // what the first part lost; nothing where it is not finite
-        to[wide] = (hi & 0x7F80u) == 0x7F80u ? 0 : f2bf(h - bf2f(hi));
+        hidden[(size_t)(first + rank) * wide + at] = h;
+        const uint32_t size = __float_as_uint(h) & 0x7FFFFFFFu;
+        if (size < 0x7F800000u) top[j] = max(top[j], size);
       }
     } else if (c < n.count) {  // rows row + r and row + 8 + r: the products with the two parts of token c's h
       float* y = p.y + (size_t)(n.first + c) * p.m.H + row + r;
       const float w = s.weight[n.first + c];
-      y[0] = (acc[0] + acc[1]) * w;
-      y[8] = (acc[2] + acc[3]) * w;
+      y[0] = (acc[0] + acc[1]) * back * w;
+      y[8] = (acc[2] + acc[3]) * back * w;
     }
   }
 
@@ -1129,8 +1173,9 @@ cudaError_t launch_moe(const LaunchEnv& env, const Moe& m, MoeCall c, void* work
   p.weights = reinterpret_cast<float*>(ws + l.weights);
   p.x = reinterpret_cast<uint16_t*>(ws + l.x);
   p.x_scale = reinterpret_cast<float*>(ws + l.x_scale);
-  p.hidden = reinterpret_cast<uint16_t*>(ws + l.hidden);
-  p.shared_hidden = reinterpret_cast<uint16_t*>(ws + l.shared_hidden);
+  p.tops = reinterpret_cast<uint4*>(ws + l.tops);
+  p.hidden = reinterpret_cast<float*>(ws + l.hidden);
+  p.shared_hidden = reinterpret_cast<float*>(ws + l.shared_hidden);
   p.y = reinterpret_cast<float*>(ws + l.y);
   return m.gate_up_scale ? launch<true>(env, p) : launch<false>(env, p);
 }

@@ -1,0 +1,59 @@
+"""What an expert layer keeps of its values: h = silu(gate) * up between the two products."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from tests.fp8_reference import DEV, HALF_BF16, TINY, ULP, assert_within
+from tests.gpu_common import lib
+
+pytestmark = pytest.mark.gpu
+
+
+def weights_of(matrix, e4m3):
+    """(matrix, scales of one) in a type that holds its values."""
+    m = matrix.to(torch.float8_e4m3fn if e4m3 else torch.bfloat16)
+    assert torch.equal(m.float(), matrix)
+    return m, torch.ones(*matrix.shape[:-2], 1, 1, device=DEV) if e4m3 else None
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "bf16"])
+@pytest.mark.parametrize("T", [1, 3, 64])
+def test_h_keeps_what_32_bits_hold(T, e4m3, shared):
+    """An h of 23 bits, exact in fp32, less two others that come near it: what is left is its last bits.
+
+    Gate values are 64 at least, whose silu is the value itself in fp32, and every gate, up and h is exact there.  The first
+    h may be held in two parts of 11 bits (off by 2^-22 of it), and three values are added up in parts: 3 additions in all,
+    one more for the sum over experts, each off by at most 2^-23 of the sum of magnitudes."""
+    g = lib()
+    H, I = 32, 16
+    gen = torch.Generator(device=DEV).manual_seed(21)
+    x = torch.zeros(T, H, dtype=torch.float64, device=DEV)
+    a, b, c = (1 + torch.rand(3, T, generator=gen, device=DEV)).bfloat16().double()
+    h = (64 * a + c / 2) * b
+    near = (h / 64).bfloat16().double()
+    rest = ((h - 64 * near) / 64).bfloat16().double()
+    for j, v in enumerate((64 * a, b, torch.full_like(a, 64), near, rest, 64 * c)):
+        x[:, j] = v
+    gate_up = torch.zeros(2, I, H, device=DEV)
+    gate_up[0, 0, 0], gate_up[0, 0, 5], gate_up[0, 1:3, 2] = 1, 2.0 ** -7, 1
+    gate_up[1, 0, 1], gate_up[1, 1, 3], gate_up[1, 2, 4] = 1, 1, 1
+    down = torch.zeros(H, I, device=DEV)
+    down[:, 0], down[:, 1:3] = 1, -1
+    (gu, gus), (dn, dns) = weights_of(gate_up, e4m3), weights_of(down, e4m3)
+    none = torch.zeros_like(gu)[None], torch.zeros_like(dn)[None]  # an expert that gives nothing
+    one = (lambda s: None if s is None else s[None])
+    if shared:
+        ex = g.Experts(*none, one(gus), one(dns), shared_gate_up=gu, shared_down=dn, shared_gate_up_scale=gus,
+                       shared_down_scale=dns)
+    else:
+        ex = g.Experts(gu[None], dn[None], one(gus), one(dns))
+    ids, w = torch.zeros(T, 1, dtype=torch.int32, device=DEV), torch.ones(T, 1, device=DEV)
+    out = g.gdn_moe_step_routed(x.bfloat16(), ex, ids, w)
+    g.gdn_check_device_errors()
+    assert torch.equal(x.bfloat16().double(), x) and torch.equal(h.float().double(), h)
+    want = h - 64 * near - 64 * rest
+    size = h + 64 * near + 64 * rest.abs()
+    tol = size * (2.0 ** -22 + 4 * ULP) + TINY
+    assert_within(out, want[:, None].expand(T, H), (tol + HALF_BF16 * (want.abs() + tol))[:, None].expand(T, H), "h")
