@@ -56,6 +56,11 @@ GDN_API gdn_status gdn_debug_mma_probe_ex(const gdn_bf16* A, const gdn_bf16* B, 
  * Other bits: GDN_ERR_INVALID_ARGUMENT. */
 GDN_API gdn_status gdn_debug_set_dropped_copy(unsigned which);
 
+/* While on (nonzero), one warp of every tile of gdn_fp8_matmul (17 tokens and more) takes its first wait as run out, and the
+ * other waits end after 4096 polls: the kernel sets the timeout bit and returns with nothing in flight, whichever of the
+ * other warps' waits succeeded.  The rows of the affected call are unspecified.  Set on the current device. */
+GDN_API gdn_status gdn_debug_set_matmul_give_up(int on);
+
 #ifdef __cplusplus
 }
 #endif

@@ -132,6 +132,7 @@ def _configure(lib, debug: bool):
             "gdn_debug_mma_probe": ([P, P, ctypes.c_int, P, P, P], ctypes.c_int),
             "gdn_debug_mma_probe_ex": ([P, P, ctypes.c_int, ctypes.c_int, P, P, P], ctypes.c_int),
             "gdn_debug_set_dropped_copy": ([ctypes.c_uint], ctypes.c_int),
+            "gdn_debug_set_matmul_give_up": ([ctypes.c_int], ctypes.c_int),
         })
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -653,6 +654,11 @@ def gdn_debug_set_dropped_copy(which: int):
     """libgdn_test.so only: bit 0 drops the binary16 decode step's state copy, bit 1 the chunk
     state kernel's first vector-block copy, so that the bounded wait on it runs out (0: off)."""
     _check_test(load_test_library().gdn_debug_set_dropped_copy(int(which)))
+
+
+def gdn_debug_set_matmul_give_up(on: bool):
+    """libgdn_test.so only: while on, one warp of every tile of the 8-bit product gives up its first wait."""
+    _check_test(load_test_library().gdn_debug_set_matmul_give_up(int(on)))
 
 
 def gdn_debug_mma_probe(A, B, stream=None):

@@ -15,13 +15,17 @@ namespace {
 
 constexpr int kBlockK = 128;  // codes of a stage's row, one scale block
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls of one mbarrier before giving up
+#ifdef GDN_TEST_HOOKS
+constexpr uint32_t kTestWaitLimit = 1u << 12;
+__device__ unsigned g_test_give_up;  // 1: the first warp of a tile's sums takes its first wait as run out
+#endif
 
 // A whole warp works on barriers, copies and products without a branch: every lane polls, and what one lane issues stands
 // under a predicate of elect.sync in one piece of assembly.  Measured for a warp: a poll that finds its phase complete takes
 // 58 cycles this way, 255 in a branch of one lane; four products and two arrivals 270, 340 in a branch of the elected lane
 // and 560 in one of `lane == 0`, whose operands have to be gathered from that lane.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint32_t limit) {
+  for (uint32_t i = 0; i < limit; ++i) {
     uint32_t done;
     asm volatile("{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
                  : "=r"(done)
@@ -349,8 +353,15 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
   await_grid();
 
   bool ok = true;
+#ifdef GDN_TEST_HOOKS
+  const uint32_t limit = !g_test_give_up ? kWaitLimit : warp == C::kFirst ? 0 : kTestWaitLimit;
+#else
+  constexpr uint32_t limit = kWaitLimit;
+#endif
+  // A warp whose wait ran out goes on to the barriers behind the sums: the others of its CTA and cluster may have
+  // passed the same wait.
   auto await = [&](uint32_t bar, uint32_t parity) {
-    if (ok && !warp_wait(bar, parity)) {
+    if (ok && !warp_wait(bar, parity, limit)) {
       raise_error(p.err, kErrTimeout);
       ok = false;
     }
@@ -376,7 +387,7 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
       // copies in flight land before the CTA ends, after a wait that ran out too
       for (int c = 0; c < stages; ++c) {
         const int passes = pass + (c < i);  // loads into stage c
-        if (passes) mbar_wait(full + 8 * c, (passes - 1) & 1, kWaitLimit);
+        if (passes) mbar_wait(full + 8 * c, (passes - 1) & 1, limit);
       }
     } else if (warp == 1) {
       // A full stage has its loads and the word of the sums that they have read what lay in its place of tensor memory: one wait
@@ -393,6 +404,8 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
                         C::kGroup == 1 || j % C::kGroup == C::kGroup - 1 || b + 1 == end);
           if (++i == stages) i = 0, ++pass;
         }
+      // products in flight end before the CTA does, after a wait that ran out too
+      if (i || pass) warp_wait(empty + 8 * (i ? i - 1 : stages - 1), (i ? pass : pass - 1) & 1, limit);
     }
   } else {
     if constexpr (C::kLarge) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
@@ -509,6 +522,9 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
             reinterpret_cast<float4*>(part)[i] = make_float4(acc[2 * i].x, acc[2 * i].y, acc[2 * i + 1].x, acc[2 * i + 1].y);
         break;
       }
+      // a small tile's CTA has no other one: its ring takes rows of any alignment on their way out
+      if constexpr (!C::kLarge)
+        if (!p.whole_out) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
       if (!ok) break;
       if (p.whole_out) {  // whole sectors of a row from its thread
         if (t < p.tokens) {
@@ -539,8 +555,6 @@ __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __gr
       } else {
         // Rows of any alignment, 32 x 16 words at a time through shared memory: half a row of fp32 values or a row of 32 bf16
         // ones a store, sixteen stores of a lane at once: 777 x 5003 x 2041 15.5 us (bf16 15.1), 19.8 with one store after another.
-        // A small tile's CTA has no other one: the ring is free.
-        if constexpr (!C::kLarge) asm volatile("bar.sync 1, %0;" ::"n"(C::kWarps * 32) : "memory");
         if (p.out_f32) {
           const int half = lane >> 4, col = lane & 15;
           const long rows = p.tokens - t0 - half;
@@ -720,6 +734,10 @@ cudaError_t launch_many(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul& 
 }
 
 }  // namespace
+
+#ifdef GDN_TEST_HOOKS
+cudaError_t test_set_give_up_matmul(unsigned on) { return cudaMemcpyToSymbol(g_test_give_up, &on, sizeof on); }
+#endif
 
 cudaError_t launch_fp8_matmul(const LaunchEnv& env, const Fp8Matmul& m) {
   MatmulParams p;

@@ -1245,6 +1245,12 @@ gdn_status gdn_debug_set_dropped_copy(unsigned which) {
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "setting the dropped-copy hook: %s", cudaGetErrorString(e));
   return ok();
 }
+
+gdn_status gdn_debug_set_matmul_give_up(int on) {
+  const cudaError_t e = gdn::test_set_give_up_matmul(on != 0);
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "setting the hook: %s", cudaGetErrorString(e));
+  return ok();
+}
 #endif
 
 }  // extern "C"

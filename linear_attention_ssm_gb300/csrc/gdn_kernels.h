@@ -124,6 +124,8 @@ cudaError_t launch_chunk_prefill_split(const LaunchEnv& env, const uint16_t* qkv
 // a timeout -- nothing is in flight when the CTA leaves.  Set for the current device.
 cudaError_t test_set_dropped_copy_decode(unsigned on);  // the binary16 decode step's state-slice copy
 cudaError_t test_set_dropped_copy_chunk(unsigned on);   // the chunk state kernel's first vector-block copy
+// Test library only: while set (1), the first warp of the sums of an 8-bit product's tile takes its first wait as run out.
+cudaError_t test_set_give_up_matmul(unsigned on);
 #endif
 
 // Softmax attention over a paged key/value cache (attn_cache.cu, attn.cu).

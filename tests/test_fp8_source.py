@@ -39,3 +39,12 @@ def test_every_kernel_waits_first():
     assert {"quantize_rows_kernel", "quantize_blocks_kernel", "few_kernel", "tile_kernel", "prepare_kernel", "choose_kernel",
             "experts_kernel"} <= set(kernels)
     assert not any(kernels.values()), kernels
+
+
+def test_a_wait_that_ran_out_passes_every_barrier_of_the_tile():
+    """The warps of the sums count their polls apart, so one may give up where the others do not: none may leave between
+    its sums and the last barrier that the others wait at."""
+    text = code("fp8_matmul.cu")
+    body = text[text.index("tile_kernel("):text.index("cudaError_t launch_tiles")]
+    sums, last = body.index("++group;\n      asm volatile(\"cp.async.wait_group 0"), body.rindex("bar.sync")
+    assert sums < last and not re.search(r"!ok|\breturn\b", body[sums:last])
