@@ -84,8 +84,10 @@ __device__ __forceinline__ float scale_of(uint32_t top) {  // of the larger half
 
 // x / s as IEEE division rounds it, for 2^-90 <= s <= 2^120 and quotients that matter to a code (2^-11 and more): with r the
 // rounded 1 / s, q = x r is within two units of the quotient, and one more step with what is left of x gives the rounded
-// quotient (P. Markstein, Computation of elementary functions on the IBM RISC System/6000 processor, 1990).  What is left is
-// taken as q s - x, so that a -0 stays one: x - q s is +0 there, and the sum with q = -0 +0.
+// quotient (after P. Markstein, Computation of elementary functions on the IBM RISC System/6000 processor, 1990, where r is
+// close enough for what is left to be exact; here it is rounded for 35 pairs of significands).  x and the largest value are
+// bf16, so that there are 128 x 128 pairs of significands, and a CPU test goes through them all.  What is left is taken as
+// q s - x, so that a -0 stays one: x - q s is +0 there, and the sum with q = -0 +0.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = __fmul_rn(x, r);
   return __fmaf_rn(-__fmaf_rn(q, s, -x), r, q);
