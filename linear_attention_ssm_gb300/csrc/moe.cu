@@ -24,8 +24,8 @@
 // Products are m16n8k16 of mma.sync: weights fill the 16 rows, an expert's tokens the 8 columns, so that a weight is an operand
 // as it lies in memory.  Both operands of a lane may come from any places of k as long as they are the same ones; a lane reads
 // 16-byte chunks of its rows, and the tokens lie in memory in that order.  e4m3 weights become binary16 beside the tokens
-// (exact; a token is divided by a power of two that brings its largest value to 2^14 .. 2^15: values down to 2^-32 of the
-// largest are exact, and what others lose is below 2^-40 of it).  h is held in fp32 and split by the warp that multiplies: beside
+// (exact; a token is divided by a power of two that brings its largest value to 2^15 .. 65280, the largest bf16 below 2^16:
+// values down to 2^-32 of it, 2^-17 at least, are exact, and smaller ones lose at most half of 2^-24, 2^-40 of it).  h is held in fp32 and split by the warp that multiplies: beside
 // e4m3 weights into two binary16 parts in two columns, relative to the largest h of its token and expert, which the units of the
 // first kind gather and which is there when all of h is: off by at most 2^-23 of itself or 2^-39 of the largest; beside bf16
 // weights into three bf16 parts, all 24 bits, in two columns and, by a second product, the third part in the second one.  (With
@@ -181,9 +181,9 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
       __syncthreads();
       for (int w = 0; w < kPrepareWarps; ++w) top = fmaxf(top, tops[w]);
       // the largest value's exponent, raised to where the power of two has a reciprocal
-      const int e = max((int)(__float_as_uint(top) >> 23), 15);
-      scale = __uint_as_float((uint32_t)(e - 14) << 23);
-      const float inverse = __uint_as_float((uint32_t)(254 - (e - 14)) << 23);
+      const int e = max((int)(__float_as_uint(top) >> 23), 16);
+      scale = __uint_as_float((uint32_t)(e - 15) << 23);
+      const float inverse = __uint_as_float((uint32_t)(254 - (e - 15)) << 23);
       for (int k = threadIdx.x * 8; k < H; k += kPrepareThreads * 8) {
         const uint4 v = ld_once(x + k);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};

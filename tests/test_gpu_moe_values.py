@@ -57,3 +57,36 @@ def test_h_keeps_what_32_bits_hold(T, e4m3, shared):
     size = h + 64 * near + 64 * rest.abs()
     tol = size * (2.0 ** -22 + 4 * ULP) + TINY
     assert_within(out, want[:, None].expand(T, H), (tol + HALF_BF16 * (want.abs() + tol))[:, None].expand(T, H), "h")
+
+
+@pytest.mark.parametrize("largest", [64.0, 65.0, 127.5, -64.0])
+def test_small_values_beside_a_large_one(largest):
+    """e4m3 weights that single out one small value of a token: exact down to 2^-32 of the token's largest value, off by at
+    most 2^-40 of it below.  The gate is the largest value's magnitude, whose silu is the value itself in fp32, and the
+    token's one h is a power of two times 16 bits; with 64 as the largest value the row's 8 bits are the small value's own."""
+    g = lib()
+    H, I, T = 32, 16, 64
+    j = torch.arange(T, device=DEV)
+    small = (1 + (37 * j % 128) / 128.0) * 2.0 ** -(8 + j * 0.5).floor() * 32
+    small[40] = abs(largest) * 2.0 ** -32 * (1 + 2.0 ** -7)
+    x = torch.zeros(T, H, device=DEV)
+    x[:, 0], x[:, 1] = largest, small
+    x = x.bfloat16()
+    gate_up = torch.zeros(2, I, H, device=DEV)
+    gate_up[0, 0, 0], gate_up[1, 0, 1] = (1 if largest > 0 else -1), 1
+    down = torch.zeros(H, I, device=DEV)
+    down[:, 0] = 1
+    (gu, gus), (dn, dns) = weights_of(gate_up, True), weights_of(down, True)
+    ex = g.Experts(gu[None], dn[None], gus[None], dns[None])
+    ids, w = torch.zeros(T, 1, dtype=torch.int32, device=DEV), torch.ones(T, 1, device=DEV)
+    out = g.gdn_moe_step_routed(x, ex, ids, w)
+    g.gdn_check_device_errors()
+    top, v = x[:, 0].double().abs(), x[:, 1].double()
+    want = top * v
+    exact = v >= top * 2.0 ** -32
+    assert bool(exact[40]) and 5 < int(exact.sum()) < T - 5
+    room = top * torch.where(exact, 0.0, top * 2.0 ** -40)
+    room = room + want.abs() * (2.0 ** -23 + 4 * ULP)  # h in two parts, sums as above
+    if abs(largest) == 64:
+        assert torch.equal(out[exact], want[exact].bfloat16()[:, None].expand(-1, H))
+    assert_within(out, want[:, None].expand(T, H), (room + HALF_BF16 * (want.abs() + room))[:, None].expand(T, H), "small values")
