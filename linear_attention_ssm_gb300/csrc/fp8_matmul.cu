@@ -751,7 +751,7 @@ cudaError_t launch_fp8_matmul(const LaunchEnv& env, const Fp8Matmul& m) {
   p.w_scale = m.w_scale;
   p.tokens = m.tokens;
   p.n = m.n;
-  p.blocks = (m.k + kBlockK - 1) / kBlockK;
+  p.blocks = (m.k - 1) / kBlockK + 1;
   p.out = m.out;
   p.out_stride = m.out_stride;
   p.out_f32 = m.out_f32;

@@ -48,3 +48,13 @@ def test_a_wait_that_ran_out_passes_every_barrier_of_the_tile():
     body = text[text.index("tile_kernel("):text.index("cudaError_t launch_tiles")]
     sums, last = body.index("++group;\n      asm volatile(\"cp.async.wait_group 0"), body.rindex("bar.sync")
     assert sums < last and not re.search(r"!ok|\breturn\b", body[sums:last])
+
+
+def test_blocks_of_the_longest_rows():
+    """k is at most 2^31 - 1: the number of its blocks is formed without a sum that leaves 31 bits."""
+    text = code("fp8_matmul.cu")
+    for k in (1, 127, 128, 129, 2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 1):
+        expr = re.search(r"p\.blocks = ([^;]*);", text).group(1).replace("m.k", str(k)).replace("kBlockK", "128")
+        steps = re.findall(r"\(([^()]*)\)", expr)
+        assert all(abs(eval(s)) < 2 ** 31 for s in steps), expr
+        assert eval(expr.replace("/", "//")) == -(-k // 128)

@@ -279,3 +279,25 @@ def test_refusals():
     with pytest.raises(g.GdnError) as e:  # rows of 100 bytes
         g.gdn_fp8_matmul(x.contiguous(), xs, w, ws)
     assert e.value.name == "GDN_ERR_MISALIGNED"
+
+
+@pytest.mark.parametrize("T", [1, 17])
+def test_product_of_the_longest_rows(T):
+    """k = 2^31 - 1: nearly all codes are 0, the others stand at the ends and in the middle."""
+    g = lib()
+    K, N = 2 ** 31 - 1, 2
+    at = torch.tensor([0, 1, 127, 128, 2 ** 30 + 5, K - 129, K - 128, K - 17, K - 16, K - 15, K - 2, K - 1], device=DEV)
+    gen = gen_of(19)
+
+    def matrix(rows):
+        c = torch.zeros(rows, K + 1, dtype=torch.uint8, device=DEV)
+        few = torch.randn(rows, at.numel(), generator=gen, device=DEV).to(E4M3)
+        c[:, at] = few.view(torch.uint8)
+        c[:, K] = 0x7E  # behind the end: not read
+        return c.view(E4M3)[:, :K], few.double()
+    (x, xf), (w, wf) = matrix(T), matrix(N)
+    out = g.gdn_fp8_matmul(x, torch.ones(T, blocks(K), device=DEV), w, torch.ones(1, blocks(K), device=DEV),
+                           out_dtype=torch.float32)
+    g.gdn_check_device_errors()
+    # zeros add nothing: a product is in at most as many sums as there are products, and the joins
+    assert_within(out, xf @ wf.T, (at.numel() + 16) * 2.0 ** -23 * (xf.abs() @ wf.abs().T), "long rows")
