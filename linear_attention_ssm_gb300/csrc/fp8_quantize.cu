@@ -116,7 +116,7 @@ __device__ __forceinline__ void store16(const QuantizeParams& p, uint8_t* row, i
                 two_codes(__fdiv_rn(__uint_as_float(b << 16), s), __fdiv_rn(__uint_as_float(b & 0xFFFF0000u), s)) << 16;
     }
   }
-  if (c + 16 <= p.cols) {
+  if (c <= p.cols - 16) {
     *reinterpret_cast<uint4*>(row + c) = make_uint4(code[0], code[1], code[2], code[3]);
   } else {
 #pragma unroll

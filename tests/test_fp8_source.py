@@ -58,3 +58,15 @@ def test_blocks_of_the_longest_rows():
         steps = re.findall(r"\(([^()]*)\)", expr)
         assert all(abs(eval(s)) < 2 ** 31 for s in steps), expr
         assert eval(expr.replace("/", "//")) == -(-k // 128)
+
+
+def test_columns_of_the_longest_rows():
+    """Columns are numbered in 31 bits, up to 2^31 - 2: whether sixteen values from one on are all there is asked without a
+    sum beyond that (their codes would go behind the row's end)."""
+    text = code("fp8_quantize.cu")
+    asked = re.search(r"if \(([^()]*)\) \{\s*\*reinterpret_cast<uint4\*>\(row \+ c\)", text).group(1)
+    sides = asked.split("<=")
+    for cols in (1, 15, 16, 17, 300, 2 ** 31 - 17, 2 ** 31 - 16, 2 ** 31 - 1):
+        for c in range(0, cols, 16) if cols < 1000 else range(cols // 128 * 128, cols, 16):
+            left, right = (eval(s.replace("p.cols", str(cols)), {"c": c}) for s in sides)
+            assert abs(left) < 2 ** 31 and abs(right) < 2 ** 31 and (left <= right) == (c + 16 <= cols)
