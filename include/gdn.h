@@ -700,7 +700,8 @@ GDN_API gdn_status gdn_fp8_quantize(const gdn_bf16* x, int64_t x_row_stride, int
  *   w_scale  [ceil(n / 128), ceil(k / 128)] fp32
  *   out      tokens rows of n bf16 or fp32 values, out_row_stride elements apart (>= n, any); overlaps no input.  What
  *            lies between n and the stride is left as it was
- * k codes that are NaN (or scales that are not finite) make the rows and columns they belong to NaN, and no others.
+ * A code or a scale that is NaN makes the rows and columns it belongs to NaN, and a scale that is infinite makes them
+ * infinite or NaN; no others change.
  * tokens == 0 or n == 0 is a no-op that returns GDN_OK; k >= 1.
  */
 GDN_API gdn_status gdn_fp8_matmul(const uint8_t* x, int64_t x_row_stride, const float* x_scale, const uint8_t* w,

@@ -301,3 +301,29 @@ def test_product_of_the_longest_rows(T):
     g.gdn_check_device_errors()
     # zeros add nothing: a product is in at most as many sums as there are products, and the joins
     assert_within(out, xf @ wf.T, (at.numel() + 16) * 2.0 ** -23 * (xf.abs() @ wf.abs().T), "long rows")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,N,K", [(5, 200, 300), (16, 200, 300), (60, 400, 300), (200, 400, 300), (1100, 600, 300)])
+def test_nan_gives_nan_and_infinite_scales_what_is_not_finite(T, N, K, dtype):
+    g = lib()
+    gen = gen_of(20)
+    x, xs = codes_of(gen, T, K, 1)
+    w, ws = codes_of(gen, N, K, 128)
+    clean = g.gdn_fp8_matmul(x, xs, w, ws, out_dtype=dtype)
+    x[0, 7], w[3, 299], xs[1, 2], ws[1, 0] = math.nan, math.nan, math.nan, math.nan
+    xs[2, 0] = math.inf
+    nan, room = (torch.zeros(T, N, dtype=torch.bool, device=DEV) for _ in range(2))
+    nan[:2], nan[:, 3], nan[:, 128:256] = True, True, True
+    room[2] = True
+    room &= ~nan
+    got = g.gdn_fp8_matmul(x, xs, w, ws, out_dtype=dtype)
+    assert bool(got[nan].isnan().all()) and not bool(got[room].isfinite().any())
+    assert bool(got[room].isinf().any()) and torch.equal(got[~nan & ~room], clean[~nan & ~room])
+    ws = ws.clone()
+    ws[0, 1] = -math.inf
+    got = g.gdn_fp8_matmul(x, xs, w, ws, out_dtype=dtype)
+    room[:, :128] = True
+    room &= ~nan
+    assert bool(got[nan].isnan().all()) and not bool(got[room].isfinite().any())
+    assert torch.equal(got[~nan & ~room], clean[~nan & ~room])
