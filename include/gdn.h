@@ -723,7 +723,8 @@ typedef struct {
 #define GDN_WEIGHT_BF16 0
 #define GDN_WEIGHT_E4M3 1 /* with a scale for each block of 128 x 128 of every [I, H] or [H, I] matrix */
 
-/* The experts' matrices and scales are finite: what a NaN or an infinity among them gives is not defined. */
+/* A NaN or an infinity among an expert's matrices or scales makes the rows of the tokens that pass the expert not finite, in
+ * the columns whose sums it enters, and changes no other row. */
 typedef struct {
   int32_t type;                      /* of the experts' matrices, GDN_WEIGHT_* */
   const gdn_bf16* router;            /* [E, H] */

@@ -1,10 +1,12 @@
 """What an expert layer keeps of its values: h = silu(gate) * up between the two products."""
 from __future__ import annotations
 
+import math
+
 import pytest
 import torch
 
-from tests.fp8_reference import DEV, HALF_BF16, TINY, ULP, assert_within
+from tests.fp8_reference import DEV, HALF_BF16, TINY, ULP, assert_within, experts
 from tests.gpu_common import lib
 
 pytestmark = pytest.mark.gpu
@@ -90,3 +92,36 @@ def test_small_values_beside_a_large_one(largest):
     if abs(largest) == 64:
         assert torch.equal(out[exact], want[exact].bfloat16()[:, None].expand(-1, H))
     assert_within(out, want[:, None].expand(T, H), (room + HALF_BF16 * (want.abs() + room))[:, None].expand(T, H), "small values")
+
+
+@pytest.mark.parametrize("shared", [0, 32])
+@pytest.mark.parametrize("e4m3", [True, False], ids=["e4m3", "bf16"])
+def test_weights_that_are_not_finite_reach_the_tokens_that_pass_them(e4m3, shared):
+    """One NaN (or infinity) among an expert's weights or scales: the rows of its tokens are not finite where the definition's
+    are not, every other row is as it was."""
+    g = lib()
+    gen = torch.Generator(device=DEV).manual_seed(22)
+    T, E, H, I = 40, 6, 272, 144
+    clean = experts(g, gen, E, H, I, shared, e4m3)
+    x = (torch.randn(T, H, generator=gen, device=DEV)).bfloat16()
+    ids = torch.randint(0, E, (T, 2), generator=gen, device=DEV).int()
+    ids[:, 1] = (ids[:, 0] + 1 + ids[:, 1] % (E - 1)) % E
+    w = torch.rand(T, 2, generator=gen, device=DEV) + 0.1
+    want = g.gdn_moe_step_routed(x, clean, ids, w)
+    parts = ["gate_up", "down"] + (["gate_up_scale", "down_scale"] if e4m3 else [])
+    for name in parts:
+        for value in [math.nan] + ([] if e4m3 and "scale" not in name else [math.inf]):
+            t = getattr(clean, name)
+            kept = t.clone()
+            row = t.view(E, -1).shape[1] // 2 + 3
+            t.view(E, -1)[2, row if "scale" not in name else 1] = value
+            out = g.gdn_moe_step_routed(x, clean, ids, w)
+            g.gdn_check_device_errors()
+            hit = (ids == 2).any(1)
+            assert bool(hit.any()) and torch.equal(out[~hit], want[~hit]), name
+            bad = ~out[hit].isfinite()
+            assert bool(bad.any(1).all()), (name, value)
+            if name.startswith("gate_up"):  # an h that is not finite reaches every column
+                assert bool(bad.all()), (name, value)
+            t.copy_(kept)
+    assert torch.equal(g.gdn_moe_step_routed(x, clean, ids, w), want)
