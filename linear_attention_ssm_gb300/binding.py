@@ -1006,6 +1006,16 @@ def gdn_attn_workspace_size(num_q_heads: int, num_kv_heads: int, head_dim: int) 
     return int(_L().gdn_attn_workspace_size(_attn_geo(num_q_heads, num_kv_heads, head_dim)))
 
 
+def _check_workspace(t, device):
+    """The call writes numel() elements from the tensor's address on: they have to be its own."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"workspace is on {t.device}, the call is on {device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out, workspace, stream):
     lib = _L()
     c, hkv, D, dev = _cache_arg(cache)
@@ -1027,8 +1037,8 @@ def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out
             workspace = _take_workspace(key, need, dev, stream)
         else:
             workspace = _empty(need, torch.uint8, dev, stream)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, the call is on {dev}")
+    else:
+        _check_workspace(workspace, dev)
     tail = (softmax_scale, *zp, op, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     if cu is None:
         _call(lib.gdn_attn_decode_step, dev, stream, geo, qp, c, table, pages, lens, T, *tail)
@@ -1216,8 +1226,8 @@ def _moe(fn, x, experts, top_k, head, tail, out, workspace, stream):
     if workspace is None:
         need = _L().gdn_moe_workspace_size(experts._geo, T, top_k)
         workspace = _empty(max(need, 1), torch.uint8, dev, stream)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, the call is on {dev}")
+    else:
+        _check_workspace(workspace, dev)
     _call(fn, dev, stream, experts._geo, experts._weights, *head, xp, xs if T > 1 else H, T, *tail, op,
           workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out
