@@ -225,6 +225,19 @@ def _dev(t, dtype, name, shape=None):
     return t
 
 
+def _workspace_bytes(t, device) -> int:
+    """Size of a workspace; None: 0.  The calls write that many bytes from its address on, so they have to be its own."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"workspace is on {t.device}, the call is on {device}")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
 def gdn_version() -> str:
     return _L().gdn_version().decode()
 
@@ -295,7 +308,7 @@ def gdn_chunk_prefill(qkv, g, beta, cu_seqlens, q_scale, l2_eps=1e-6, state_in=N
     need = lib.gdn_chunk_prefill_workspace_size(_geo(geometry), N, T)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=qkv.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, qkv.device)
     _check(lib.gdn_chunk_prefill(_geo(geometry), _p(qkv), _p(g), _p(beta), _p(cu_seqlens), N, T,
                                  float(q_scale), float(l2_eps), _p(state_in), _p(state_out), _p(z),
                                  _p(norm_w), float(rms_eps), _p(out), _p(workspace), wbytes,
@@ -458,7 +471,7 @@ def gdn_kda_chunk_prefill(qkv, g, beta, cu_seqlens, q_scale, g_min=float("-inf")
     need = lib.gdn_kda_chunk_prefill_workspace_size(_geo(geometry), N, T)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=qkv.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, qkv.device)
     _check(lib.gdn_kda_chunk_prefill(_geo(geometry), _p(qkv), _p(g), float(g_min), _p(beta), _p(cu_seqlens), N, T,
                                      float(q_scale), float(l2_eps), _p(state_in), _p(state_out), _p(z), _p(norm_w),
                                      float(rms_eps), _p(out), _p(workspace), wbytes, _stream(stream)))
@@ -522,7 +535,7 @@ def gdn_chunk_prefill_fused_gates(qkv, a, b, A_log, dt_bias, cu_seqlens, q_scale
     need = lib.gdn_chunk_prefill_workspace_size(_geo(geometry), N, T)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=qkv.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, qkv.device)
     _check(lib.gdn_chunk_prefill_fused_gates(_geo(geometry), _p(qkv), _p(a), _p(b), _p(A_log), _p(dt_bias),
                                              _p(cu_seqlens), N, T, float(q_scale), float(l2_eps), _p(state_in),
                                              _p(state_out), _p(z), _p(norm_w), float(rms_eps), _p(out),
@@ -717,7 +730,7 @@ def gdn_prefill(x, conv_w, cu_seqlens, g, beta, z, norm_w, q_scale, l2_eps=1e-6,
     need = lib.gdn_chunk_prefill_workspace_size(_geo(geometry), N, T)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, x.device)
     _check(lib.gdn_prefill(_geo(geometry), _p(x), _p(conv_w), _p(cu_seqlens), N, T, _p(conv_state_in),
                            _p(conv_state_out), _p(qkv_buf), _p(g), _p(beta), float(q_scale), float(l2_eps),
                            _p(state_in), _p(state_out), _p(z), _p(norm_w), float(rms_eps), _p(out), _p(workspace),
@@ -763,7 +776,7 @@ def gdn_kda_prefill(x, conv_w, cu_seqlens, g, beta, z, norm_w, q_scale, g_min=fl
     need = lib.gdn_kda_chunk_prefill_workspace_size(_geo(geometry), N, T)
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    wbytes = _workspace_bytes(workspace, x.device)
     _check(lib.gdn_kda_prefill(_geo(geometry), _p(x), _p(conv_w), _p(cu_seqlens), N, T, _p(conv_state_in),
                                _p(conv_state_out), _p(qkv_buf), _p(g), float(g_min), _p(beta), float(q_scale),
                                float(l2_eps), _p(state_in), _p(state_out), _p(z), _p(norm_w), float(rms_eps),
@@ -1006,16 +1019,6 @@ def gdn_attn_workspace_size(num_q_heads: int, num_kv_heads: int, head_dim: int) 
     return int(_L().gdn_attn_workspace_size(_attn_geo(num_q_heads, num_kv_heads, head_dim)))
 
 
-def _check_workspace(t, device):
-    """The call writes numel() elements from the tensor's address on: they have to be its own."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("workspace must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"workspace is on {t.device}, the call is on {device}")
-    if not t.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-
-
 def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out, workspace, stream):
     lib = _L()
     c, hkv, D, dev = _cache_arg(cache)
@@ -1037,9 +1040,10 @@ def _attention(q, cache, block_table, kv_lens, cu_seqlens, softmax_scale, z, out
             workspace = _take_workspace(key, need, dev, stream)
         else:
             workspace = _empty(need, torch.uint8, dev, stream)
+        size = workspace.numel()
     else:
-        _check_workspace(workspace, dev)
-    tail = (softmax_scale, *zp, op, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        size = _workspace_bytes(workspace, dev)
+    tail = (softmax_scale, *zp, op, workspace.data_ptr(), size)
     if cu is None:
         _call(lib.gdn_attn_decode_step, dev, stream, geo, qp, c, table, pages, lens, T, *tail)
     else:
@@ -1226,10 +1230,11 @@ def _moe(fn, x, experts, top_k, head, tail, out, workspace, stream):
     if workspace is None:
         need = _L().gdn_moe_workspace_size(experts._geo, T, top_k)
         workspace = _empty(max(need, 1), torch.uint8, dev, stream)
+        size = workspace.numel()
     else:
-        _check_workspace(workspace, dev)
+        size = _workspace_bytes(workspace, dev)
     _call(fn, dev, stream, experts._geo, experts._weights, *head, xp, xs if T > 1 else H, T, *tail, op,
-          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+          workspace.data_ptr(), size)
     return out
 
 

@@ -53,3 +53,42 @@ def test_a_workspace_is_contiguous_memory(calls, name):
     with pytest.raises(TypeError):
         call(b"256")
     assert not given
+
+
+class _Library:
+    """Every workspace is of 64 bytes, every call succeeds."""
+    def __init__(self, given):
+        self.given = given
+
+    def __getattr__(self, name):
+        if name.endswith("workspace_size"):
+            return lambda *a: 64
+        return lambda *a: self.given.append(a[-3:-1])
+
+
+@pytest.mark.parametrize("name", ["gdn_chunk_prefill", "gdn_kda_chunk_prefill", "gdn_chunk_prefill_fused_gates", "gdn_prefill",
+                                  "gdn_kda_prefill"])
+def test_the_prefills_workspaces_too(monkeypatch, name):
+    given = []
+    monkeypatch.setattr(binding, "_L", lambda: _Library(given))
+    monkeypatch.setattr(binding, "_dev", lambda t, *a, **kw: t)
+    monkeypatch.setattr(binding, "_stream", lambda stream: None)
+    monkeypatch.setattr(binding, "_check", lambda status: None)
+    monkeypatch.setattr(binding, "_p", lambda t: None if t is None else t.data_ptr())
+    x, cu = torch.zeros(2, 16, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    args = {"gdn_chunk_prefill": (x, None, None, cu, 0.1), "gdn_kda_chunk_prefill": (x, None, None, cu, 0.1),
+            "gdn_chunk_prefill_fused_gates": (x, None, None, None, None, cu, 0.1),
+            "gdn_prefill": (x, None, cu, None, None, None, None, 0.1), "gdn_kda_prefill": (x, None, cu, None, None, None, None, 0.1)}
+
+    def call(workspace):
+        getattr(binding, name)(*args[name], workspace=workspace)
+    room = torch.empty(256, dtype=torch.uint8)
+    for t in (room, room.view(torch.float32)):
+        call(t)
+        assert given.pop() == (t.data_ptr(), 256)
+    call(None)
+    assert given.pop()[1] == 64
+    for t in (room[::2], room[:64].expand(4, 64), torch.empty(256, dtype=torch.uint8, device="meta")):
+        with pytest.raises(ValueError):
+            call(t)
+    assert not given
