@@ -621,6 +621,8 @@ struct Warp {
   __device__ __forceinline__ int shared_groups(int kind) const {
     return p.m.Is ? (p.c.T + group_of(kind) - 1) / group_of(kind) : 0;
   }
+  // the whole warp: the other one, or this, gave up
+  __device__ __forceinline__ bool failed() const { return __any_sync(~0u, *(volatile int*)&team.failed); }
   __device__ __forceinline__ int rows_of_y() const { return s.groups[1][s.active] + shared_groups(1); }  // units of 32 columns
   // Units of the groups of an expert that have the same rows follow one another: the second one finds the weights in L2.
   // The shared expert's are first.
@@ -724,7 +726,7 @@ struct Loader : Warp<kE4M3> {
       int done = 0;
       asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(done) : "r"(smem_u32(&team.finished)) : "memory");
       if (__all_sync(~0u, done >= mine)) break;
-      if (i == kSpinLimit || *(volatile int*)&team.failed) return fail();
+      if (i == kSpinLimit || this->failed()) return fail();
       __nanosleep(32);
     }
     if (lane == 0 && mine) {
@@ -756,7 +758,7 @@ struct Loader : Warp<kE4M3> {
   __device__ __forceinline__ void await_place() {
     const uint32_t bar = this->empty + 8 * slot;
     for (uint32_t i = 0; !warp_poll(bar, pass ^ 1); ++i)
-      if (i == kWaitLimit || *(volatile int*)&team.failed) return fail();
+      if (i == kWaitLimit || this->failed()) return fail();
   }
   __device__ __forceinline__ void next_stage() {
     if (++slot == kStages) slot = 0, pass ^= 1;
@@ -861,7 +863,7 @@ struct Multiplier : Warp<kE4M3> {
   __device__ __forceinline__ void await_stage() {
     const uint32_t bar = this->full + 8 * now;
     for (uint32_t i = 0; !warp_poll(bar, pass); ++i)
-      if (i == kWaitLimit || *(volatile int*)&team.failed) return fail();
+      if (i == kWaitLimit || this->failed()) return fail();
   }
   __device__ __forceinline__ void fail() {
     if (lane == 0) {

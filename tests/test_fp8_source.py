@@ -70,3 +70,10 @@ def test_columns_of_the_longest_rows():
         for c in range(0, cols, 16) if cols < 1000 else range(cols // 128 * 128, cols, 16):
             left, right = (eval(s.replace("p.cols", str(cols)), {"c": c}) for s in sides)
             assert abs(left) < 2 ** 31 and abs(right) < 2 ** 31 and (left <= right) == (c + 16 <= cols)
+
+
+def test_a_warp_leaves_a_wait_as_a_whole():
+    """What another warp writes while this one reads it is one answer for all lanes: the votes of the next wait name them all."""
+    text = code("moe.cu")
+    reads = [m.start() for m in re.finditer(r"\*\(volatile int\*\)&team\.failed(?! = 1)", text)]
+    assert reads and all(re.search(r"__any_sync\(~0u, $", text[:at]) for at in reads)
