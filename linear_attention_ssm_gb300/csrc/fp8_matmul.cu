@@ -143,11 +143,12 @@ constexpr int kFewWarps = 8;
 
 // One CTA: 16 rows of w and up to 8 kTiles tokens; its warps share the blocks of k.  A lane takes 16 codes of its two rows
 // and of its token at a time and widens them to binary16, which holds them exactly; which of a quad's lanes has which k does
-// not matter as long as both operands agree.  HBM bounds the kernel: 32 KB of weights in flight for each CTA, three (two)
-// CTAs an SM, no barrier before the sums meet.  One token x 16384 x 2048 takes 9.3 us, 3.6 TB/s: the start of the kernel and
-// two and a half waves of CTAs that live for one trip to memory each.
+// not matter as long as both operands agree.  What bounds the kernel is its way to memory: 32 KB of weights in flight for each
+// CTA, two CTAs an SM, no barrier before the sums meet.  (Three of them have 80 registers a thread and spill: one token x
+// 16384 x 2048 9.3 us, 8.8 with two; x 2048 x 6144 5.5 and 5.2; x 8192 x 8192 16.1 and 13.9.)  One token x 16384 x 2048 at 3.8 TB/s
+// is the start of the kernel and more than three waves of CTAs that live for one trip to memory each.
 template <int kTiles>
-__global__ void __launch_bounds__(kFewWarps * 32, kTiles == 1 ? 3 : 2) few_kernel(const __grid_constant__ MatmulParams p) {
+__global__ void __launch_bounds__(kFewWarps * 32, 2) few_kernel(const __grid_constant__ MatmulParams p) {
   __shared__ float parts[kFewWarps][kTiles][4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const long n0 = (long)blockIdx.x * 16;
