@@ -761,8 +761,9 @@ GDN_API size_t gdn_moe_workspace_size(const gdn_moe_geometry* geo, int32_t token
  *   f_e(x) = down_e (silu(gate_e x) * up_e x);
  *   out = sum over the chosen weight_e f_e(x) + sigmoid(x . shared_gate) f_shared(x).
  * Logits, sums and an expert's h = silu(gate) * up are fp32, and out is rounded once to bf16.  Beside GDN_WEIGHT_E4M3 an h
- * enters the down projection off by at most 2^-23 of itself or 2^-39 of the largest one of its token and expert, and a token's values pass through binary16, relative to its largest finite one: those of at least
- * 2^-32 of it are exact, and smaller ones change by at most 2^-40 of it.
+ * enters the down projection off by at most 2^-23 of itself or 2^-39 of the largest one of its token and expert, and a
+ * token's values pass through binary16, relative to its largest finite one: those of at least 2^-32 of it are exact, and
+ * smaller ones change by at most 2^-40 of it.
  * The order of the sums depends on the call's arguments alone: two calls give the same bits.
  *   x        tokens rows of H bf16, x_row_stride elements apart (a multiple of 8)
  *   ids      [tokens, top_k] int32, receives the chosen experts, largest first, or NULL

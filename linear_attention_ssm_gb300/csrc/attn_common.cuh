@@ -357,7 +357,8 @@ constexpr size_t kPartBytes = 131072;
 // happen during this kernel's lifetime, so it reads nothing that another kernel may have written (lengths, pages, cu_seqlens,
 // scales, gates, norms) through the non-coherent path (ld.global.nc, __ldg), which is for memory that stays as it
 // is for a kernel's whole life, and which a compiler may move past the wait; plain loads and volatile asm stay behind it.
-// No kernel here signals its dependents before it ends.
+// No kernel signals its dependents before it ends but the two small ones ahead of an expert layer's last one: a kernel that
+// follows such a one waits for its end all the same, and with it for everything before.
 template <typename... A>
 cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchAttribute early;

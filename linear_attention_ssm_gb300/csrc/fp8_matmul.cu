@@ -312,11 +312,13 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int& m
 // memory, each CTA its share of the tokens, beginning with its own part (all at once from one CTA they would queue there).
 // Otherwise a CTA takes tile after tile.
 //
-// What bounds the large tiles is the tensor cores' time for a block, 518 cycles, and the sums' beside it, 128 columns a
-// thread of loads from tensor memory and packed multiply-adds (3.3 cycles a warp's instruction): 8192 tokens x 16384 x 4096
-// 460 to 500 us with the clocks that a second of it leaves, 2.2 to 2.4 PFLOP/s; 2048 x 4096 x 6144 51 us, 2.0 PFLOP/s.  Two
-// CTAs that shared a tile's loads by multicast, or one product over two SMs, were no faster.  The small ones are bound by
-// what a block waits for: 64 x 2048 x 6144 9.3 us, 777 x 5003 x 2041 (140 large tiles of 16 blocks) 15.5 us.
+// What bounds the large tiles is the sums' loop, about 1000 cycles a block, beside which the tensor cores are busy for 518: the
+// wait for a load from tensor memory waits for all of a warp's, so that one load of 32 columns is under way (100 to 200
+// cycles) beside 16 packed multiply-adds (3.3 cycles a warp's instruction), and two warps a scheduler do not cover the rest.
+// 2048 x 4096 x 6144 takes 50 us, 2.0 PFLOP/s, at 2.04 GHz (two waves of 48 blocks); 8192 x 16384 x 4096 (27 tiles of 32 blocks
+// a CTA) 451 us at first, 2.4 PFLOP/s, and 486 once the power limit has brought the clock to 1.91 GHz.  Two CTAs that shared
+// a tile's loads by multicast, or one product over two SMs, were no faster.  The small ones are bound by what a block waits
+// for: 64 x 2048 x 6144 9.1 us, 777 x 5003 x 2041 (140 large tiles of 16 blocks) 15.0 us.
 template <int kN, bool kSplit>
 __global__ void __launch_bounds__(Tiles<kN>::kThreads, 1) tile_kernel(const __grid_constant__ MatmulParams p) {
   using C = Tiles<kN>;
@@ -713,7 +715,7 @@ cudaError_t launch_many(const LaunchEnv& env, MatmulParams& p, const Fp8Matmul& 
   // Tiles of 64 rows of w, a CTA each, while every one has an SM; a block costs them 0.27 us, the large ones' 0.5 us for four
   // times the products.  256 tokens x 4096 x 4096 (128 small tiles): 11.5 us, large 18.9; x 10240 (320): 33 : 19.9; 64 x
   // 16384 x 2048 (256): 14.7 : 11.8.  Few tiles share their k: 64 x 2048 x 6144 (32 tiles) 23 us with one CTA a tile,
-  // 13.7 with two, 9.8 with four, 11 with eight; 128 x 4096 x 4096 (64 tiles) 16.8, 11.2, 13.4 (256 CTAs).
+  // 13.7 with two, 9.8 with four (9.1 by now), 11 with eight; 128 x 4096 x 4096 (64 tiles) 16.8, 11.2, 13.4 (256 CTAs).
   const long small = ((m.tokens + 127L) / 128) * ((m.n + 63L) / 64);
   if (small <= sms) {
     e = encode_tiles<64>(p, m);

@@ -5,9 +5,10 @@
 //
 // The first kernel forms the logits and lays the tokens out; with more than 16 tokens a second one chooses (16 warps of every
 // CTA of the last one do it otherwise: 64 tokens of 288 experts took 28 us there, 12 us with a kernel of their own).  The last
-// kernel streams the chosen experts' weights once, and HBM bounds it: 64 tokens of 288 experts of 4096 x 1536 and a shared
-// one, 3 GB of e4m3 weights, 556 us, 5.5 TB/s with everything; one token of 64 experts of 2048 x 1024, 50 MB, 30 us, of
-// which the logits take 3, the choice 5, and then 16 and 8 steps of about half a microsecond each wait for one another.
+// kernel streams the chosen experts' weights once.  HBM bounds it where they are many: 64 tokens of 288 experts of 4096 x 1536
+// and a shared one, 3.1 GB of e4m3 weights, 538 us, 5.7 TB/s with everything.  Latency does where they are few: one token of
+// 64 experts of 2048 x 1024, 50 MB, 30 us, of which the logits take 3, the choice 5, and then 16 and 8 steps of about half a
+// microsecond each wait for one another.
 //
 // Work is taken in units from one list by an atomic counter: 16 rows of a gate matrix with the 16 rows of the up projection
 // beside them, over all of H (h for those places and up to 8 of the expert's tokens), then 32 rows of a down projection over
@@ -17,19 +18,21 @@
 // memory: one warp takes units and copies their weights by TMA and their tokens' values by plain asynchronous copies, the
 // other multiplies.  The ring runs ahead over the ends of units and from one kind to the next, and the wait for all of h falls
 // into that time.  (Eight warps that both loaded and multiplied took 1027 us for the first of the sizes above, two warps that
-// shared the products and of which one loaded 943; ten teams with rings of three stages take 551, and 32 instead of 30 for
-// one token.)  A unit is waited for only by units of the next kind, and by then every unit of its kind has been taken by a
-// team that runs and waits for nothing: the kernel ends however few of its CTAs run at a time.
+// shared the products and of which one loaded 943; ten teams with rings of three stages 551 where these took 556, and 32
+// instead of 30 for one token.)  A unit is waited for only by units of the next kind, and by then every unit of its kind has
+// been taken by a team that runs and waits for nothing: the kernel ends however few of its CTAs run at a time.
 //
 // Products are m16n8k16 of mma.sync: weights fill the 16 rows, an expert's tokens the 8 columns, so that a weight is an operand
 // as it lies in memory.  Both operands of a lane may come from any places of k as long as they are the same ones; a lane reads
 // 16-byte chunks of its rows, and the tokens lie in memory in that order.  e4m3 weights become binary16 beside the tokens
 // (exact; a token is divided by a power of two that brings its largest value to 2^15 .. 65280, the largest bf16 below 2^16:
-// values down to 2^-32 of it, 2^-17 at least, are exact, and smaller ones lose at most half of 2^-24, 2^-40 of it).  h is held in fp32 and split by the warp that multiplies: beside
-// e4m3 weights into two binary16 parts in two columns, relative to the largest h of its token and expert, which the units of the
-// first kind gather and which is there when all of h is: off by at most 2^-23 of itself or 2^-39 of the largest; beside bf16
-// weights into three bf16 parts, all 24 bits, in two columns and, by a second product, the third part in the second one.  (With
-// two bf16 parts beside either, 16 bits, 64 tokens of 288 experts took 557 us, now 537, and 17 of 32 in bf16 102.6, now 104.8.)
+// values down to 2^-32 of it, 2^-17 at least, are exact, and smaller ones lose at most half of 2^-24, 2^-40 of it).
+//
+// h is held in fp32 and split by the warp that multiplies: beside e4m3 weights into two binary16 parts in two columns, relative
+// to the largest h of its token and expert, which the units of the first kind gather and which is there when all of h is: off
+// by at most 2^-23 of itself or 2^-39 of the largest; beside bf16 weights into three bf16 parts, all 24 bits, in two columns
+// and, by a second product, the third part in the second one.  (With two bf16 parts beside either, 16 bits, 64 tokens of 288
+// experts took 557 us, now 537, and 17 of 32 in bf16 102.6, now 104.8.)
 #include <string.h>
 
 #include "attn_common.cuh"
@@ -350,6 +353,9 @@ __device__ __forceinline__ void choose(const MoeParams& p, int t, int lane, int&
     if (c.weights_out) c.weights_out[t * c.top_k + lane] = w;
   }
 }
+// Keys a lane, by the number of experts: 8 tokens of 64 experts 24.5 us with 2 and 25.8 with 10, of 128 25.6 with 4 and 26.6 with
+// 10; 16 of 288 30.1 with 10 and 37.7 with 32 (64, whose choice has a kernel: 42.7 and 44.9).  256 experts take no less with 8
+// than with 10: 30.1 (64 tokens: 40.9 and 41.2).
 __device__ __forceinline__ void choose_any(const MoeParams& p, int t, int lane, int& id, float& w) {
   if (p.m.E <= 64) choose<2>(p, t, lane, id, w);
   else if (p.m.E <= 128) choose<4>(p, t, lane, id, w);
@@ -513,7 +519,8 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint2& upper, con
 // the second in odd ones.  Binary16, after the product with a power of two:
 __device__ __forceinline__ uint2 half_parts(const float4& h, float by, uint32_t odd) {  // odd: all ones, or 0
   const uint32_t a = pack_half2(h.x * by, h.y * by) & odd, b = pack_half2(h.z * by, h.w * by) & odd;
-  const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&a)), v = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&b));
   return make_uint2(pack_half2(fmaf(h.x, by, -u.x), fmaf(h.y, by, -u.y)), pack_half2(fmaf(h.z, by, -v.x), fmaf(h.w, by, -v.y)));
 }
 // bf16, each part eight bits of the significand, cut off so that the three are exact; `third` is of odd columns, too.
@@ -702,7 +709,8 @@ struct Loader : Warp<kE4M3> {
   }
   __device__ __forceinline__ void load_values(uint32_t at, int k, uint32_t bar) {
     const int mine = rows - lane / kPieces;
-    if (kE4M3 && kind && k == 0 && lane < rows / 2) copy_16(smem_u32(team.tops) + 64 * ((bar - this->full) / 8) + 16 * lane, tops + lane);
+    if (kE4M3 && kind && k == 0 && lane < rows / 2)
+      copy_16(smem_u32(team.tops) + 64 * ((bar - this->full) / 8) + 16 * lane, tops + lane);
     k <<= kind;  // h is twice as long
     if (mine > 0) copy_16(at + to, base + from[0] + k);
     if (rows > kStep) {
@@ -873,8 +881,8 @@ struct Multiplier : Warp<kE4M3> {
     ok = false;
   }
 
-  // One unit.  64 tokens of 288 experts take 556 us so; 575 with a pass of the loop for each chunk, 595 for each half of one;
-  // an earlier release of the stage makes no difference.
+  // One unit.  With h in two bf16 parts 64 tokens of 288 experts took 556 us so; 575 with a pass of the loop for each chunk,
+  // 595 for each half of one; an earlier release of the stage made no difference.
   template <int kKind>
   __device__ __forceinline__ void work(const Unit& n) {
     const int r = lane >> 2, c = lane & 3, steps = (n.k + S::kK - 1) / S::kK;
@@ -885,7 +893,7 @@ struct Multiplier : Warp<kE4M3> {
     // columns behind the last row of values repeat it, and are not stored
     const int row = min(r, n.count * (kKind + 1) - 1);
     const uint32_t weights = r * 128 + ((2 * c ^ r) << 4);
-    const uint32_t values = kStageBytes + (kKind == 0 ? row * S::kRowBytes + c * 16 + (row & 1) * 64 : (row & ~1) * S::kRowBytes + c * 16);
+    const uint32_t values = kStageBytes + c * 16 + (kKind == 0 ? row * S::kRowBytes + (row & 1) * 64 : (row & ~1) * S::kRowBytes);
     const uint32_t odd = r & 1 ? ~0u : 0u;  // the column of the second part
     float by = 1.f, back = 1.f;             // h is multiplied with, and the sums of token c
     const uint32_t scales = smem_u32(team.scales);
@@ -913,14 +921,16 @@ struct Multiplier : Warp<kE4M3> {
           for (int h = 0; h < 2; ++h) w[g][h] = lds128(at + g * group + h * apart + (weights ^ j << 4));
 #pragma unroll
         for (int q = 0; q < kLoads; ++q)
-          b[q] = lds128(kKind == 0 ? (at + values) ^ (j * kLoads + q) << 6 : ((at + values) ^ q << 6 ^ j << 6) + j * S::kRowBytes);
+          b[q] = lds128(kKind == 0 ? (at + values) ^ (j * kLoads + q) << 6
+                                   : ((at + values) ^ q << 6 ^ j << 6) + j * S::kRowBytes);
 #pragma unroll
         for (int q = 0; q < kSteps; ++q) {
           uint2 v, third;
           if constexpr (kKind == 0) {
             v = q & 1 ? make_uint2(b[q / 2].z, b[q / 2].w) : make_uint2(b[q / 2].x, b[q / 2].y);
           } else {
-            const float4 h = make_float4(__uint_as_float(b[q].x), __uint_as_float(b[q].y), __uint_as_float(b[q].z), __uint_as_float(b[q].w));
+            const float4 h = make_float4(__uint_as_float(b[q].x), __uint_as_float(b[q].y), __uint_as_float(b[q].z),
+                                         __uint_as_float(b[q].w));
             v = kE4M3 ? half_parts(h, by, odd) : bf16_parts(h, odd, third);
           }
 #pragma unroll
@@ -1075,6 +1085,7 @@ constexpr size_t smem_of() {
 static_assert(smem_of<true>() <= 232448 && smem_of<false>() <= 232448, "");
 static_assert(sizeof(Choice) <= kTeams * kStages * Stage<false>::kBytes && kStages + 2 <= kQueue, "");
 
+// 512 threads have 128 registers each, and 16 (bf16) or 20 bytes of a thread's are spilled.
 template <bool kE4M3>
 __global__ void __launch_bounds__(kThreads, 1) experts_kernel(const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
